@@ -48,8 +48,9 @@ extern "C" {
 #endif
 
 /* TC_I8 / TC_I32: operands and accumulator of tc_gemm_i8_dequant; TC_I8
- * also the weight type of tc_gemm_q8_weight. */
-typedef enum { TC_F16 = 1, TC_BF16 = 2, TC_F32 = 3, TC_I8 = 4, TC_I32 = 5 } tc_dtype_t;
+ * also the weight type of tc_gemm_q8_weight; TC_I4 the weight type of
+ * tc_gemm_q4_weight. */
+typedef enum { TC_F16 = 1, TC_BF16 = 2, TC_F32 = 3, TC_I8 = 4, TC_I32 = 5, TC_I4 = 6 } tc_dtype_t;
 
 typedef enum {
     TC_OK = 0,
@@ -60,7 +61,7 @@ typedef enum {
     TC_ERR_SCALAR = 5,             /* alpha or beta not finite */
     TC_ERR_OVERLAP = 6,            /* C's byte range overlaps A's or B's */
     TC_ERR_OVERFLOW = 7,           /* an element or byte count overflows int64 */
-    TC_ERR_ALIGN_UNSUPPORTED = 8,  /* only from tc_gemm_splitk_noalloc: operands TMA cannot read in place */
+    TC_ERR_ALIGN_UNSUPPORTED = 8,  /* tc_gemm_splitk_noalloc: operands TMA cannot read in place; tc_q4_weight: a base off 16 bytes */
     TC_ERR_CUDA = 9,               /* a CUDA runtime error (launch, copy, no device) */
     TC_ERR_DEVICE_TIMEOUT = 10,    /* a kernel's bounded wait expired; it stopped early */
     TC_ERR_STRIDE = 11,            /* batched: negative stride */
@@ -233,7 +234,8 @@ tc_status_t tc_gemm_i8_dequant_async(tc_ctx *ctx, const tc_gemm_desc *d, const f
  * scales in its epilogue.  Any alignment and leading dimension; the same
  * validation, error and determinism rules as tc_gemm.  The Q4_0 / Q4_K
  * block formats and the Q8_0 block layout are not printed on the pages and
- * have no entry point. */
+ * have no entry point; 4-bit weights have this library's own format,
+ * tc_q4_weight below. */
 tc_status_t tc_gemm_q8_weight(tc_ctx *ctx, const tc_gemm_desc *d, const float *scale, const void *X,
                               const void *W, void *C);
 tc_status_t tc_gemm_q8_weight_async(tc_ctx *ctx, const tc_gemm_desc *d, const float *scale, const void *X,
@@ -241,6 +243,112 @@ tc_status_t tc_gemm_q8_weight_async(tc_ctx *ctx, const tc_gemm_desc *d, const fl
 /* Host-only: the validation tc_gemm_q8_weight runs first (no device needed). */
 tc_status_t tc_gemm_q8_weight_validate(const tc_gemm_desc *d, const float *scale, const void *X, const void *W,
                                        const void *C);
+
+/* ---- 4-bit weights with group scales (this library's format: the pages name
+ * Q4 formats without printing a layout).  A weight W[N,K] -- N outputs, K
+ * inputs, as a linear layer stores it -- is
+ *   codes   N rows of nibbles, ldw elements (ldw / 2 bytes) apart.  Eight
+ *           consecutive elements e0..e7 of a row fill one little-endian
+ *           32-bit word, from its lowest nibble: e0 e2 e4 e6 e1 e3 e5 e7.
+ *           Elements at k >= K are ignored.
+ *   scales  [ceil(K / group), ld_scale] of scale_dtype: row i holds, for each
+ *           n, the scale of W[n, i * group .. i * group + group - 1]
+ *   zeros   uint8, laid out as the scales, the zero points (the low four
+ *           bits are used); NULL means 8 everywhere
+ * and stands for W[n,k] = (code - zero) * scale.  group is 32, 64 or 128
+ * (the last group of a row may be shorter), scale_dtype TC_F16 or TC_BF16.
+ * ldw is a multiple of 32 and at least K (0 = K rounded up), ld_scale a
+ * multiple of 16 and at least N (0 = N rounded up); codes, scales and zeros
+ * are DEVICE pointers to 16-byte aligned memory owned by the caller
+ * (TC_ERR_ALIGN_UNSUPPORTED otherwise).  A stack of experts is one tall
+ * weight, its experts' rows below each other. */
+typedef struct {
+    int32_t N, K;
+    int32_t group;
+    tc_dtype_t scale_dtype;
+    int32_t ldw, ld_scale;
+    void *codes;
+    void *scales;
+    void *zeros;
+} tc_q4_weight;
+
+/* Quantise W, stored [N,K] with leading dimension ld (0 = K) in w_dtype
+ * (TC_F16, TC_BF16 or TC_F32), into q's codes, scales and (when given)
+ * zeros.  Per group, in fp32, rounding to nearest even:
+ *   zeros NULL:  s = (max|w| / 7) rounded to scale_dtype, zero = 8
+ *   zeros given: lo = min(w, 0), hi = max(w, 0), s = ((hi - lo) / 15) rounded,
+ *                zero = clamp(round(-lo / s), 0, 15)
+ *   code = clamp(round(w / s) + zero, 0, 15)
+ * A group whose scale is 0 (all zeros, or too small for scale_dtype) gets
+ * code = zero = 8.  A group that holds a NaN or an infinity, or is too large
+ * for scale_dtype, gets a scale that is not finite, so its values read back
+ * as NaN or infinity.  Codes from K to K rounded up to 32 stand for 0. */
+tc_status_t tc_quantize_q4(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W, const tc_q4_weight *q);
+tc_status_t tc_quantize_q4_async(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W,
+                                 const tc_q4_weight *q, tc_stream *s);
+/* V = the values q stands for, [N,K] with leading dimension ld (0 = K) in
+ * v_dtype (TC_F16, TC_BF16 or TC_F32): the fp32 product, rounded once. */
+tc_status_t tc_dequantize_q4(tc_ctx *ctx, const tc_q4_weight *q, tc_dtype_t v_dtype, int32_t ld, void *V);
+tc_status_t tc_dequantize_q4_async(tc_ctx *ctx, const tc_q4_weight *q, tc_dtype_t v_dtype, int32_t ld, void *V,
+                                   tc_stream *s);
+/* Host-only: the checks of a 4-bit weight (and of a matrix W[N,K] of
+ * dtype with leading dimension ld beside it) that both calls run first. */
+tc_status_t tc_q4_validate(const tc_q4_weight *q, tc_dtype_t dtype, int32_t ld, const void *W);
+
+/* 4-bit-weight product: C = alpha * X @ W^T + beta * C with W the weight q
+ * stands for.  The descriptor has a_dtype = X's type (TC_F16 or TC_BF16),
+ * b_dtype = TC_I4, accum_dtype = TC_F32, c_dtype = a_dtype or TC_F32
+ * (TC_ERR_DTYPE otherwise), transpose_a = false and transpose_b = true
+ * (TC_ERR_LAYOUT otherwise), N and K equal to q's (TC_ERR_DIM otherwise) and
+ * ldb = 0 or q's ldw (TC_ERR_LD otherwise).  X and C may have any alignment
+ * and leading dimension; C overlaps none of the inputs.  The products of X
+ * with the whole numbers code - zero are exact and summed in fp32 within a
+ * group, the groups' sums times their scales are summed in fp32: no weight
+ * is rounded to 16 bits on the way.  Deterministic run to run. */
+tc_status_t tc_gemm_q4_weight(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C);
+tc_status_t tc_gemm_q4_weight_async(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X,
+                                    void *C, tc_stream *s);
+/* Host-only: the validation tc_gemm_q4_weight runs first. */
+tc_status_t tc_gemm_q4_weight_validate(const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, const void *C);
+
+/* A mixture-of-experts layer for a few tokens over 4-bit weights:
+ *   l[t, e]  = sum_h X[t, h] * R[e, h]                       (fp32)
+ *   the top_k experts e_j of token t by l, ties to the lowest index (a NaN
+ *   counts as the largest), weights p_j = softmax(l)[e_j], with renormalize
+ *   divided by their sum
+ *   h_j[i]   = silu(W1[e_j, i] . x) * (W1[e_j, inter + i] . x)
+ *   Y[t, :]  = sum_j p_j * W2[e_j] h_j
+ * X [tokens, hidden] and Y [tokens, hidden] row-major (ldx, ldy; 0 =
+ * contiguous), x_dtype TC_F16 or TC_BF16, y_dtype x_dtype or TC_F32; the
+ * router R [experts, hidden] (ld_router), router_dtype x_dtype or TC_F32;
+ * gate_up the 4-bit weight of experts * 2 * inter rows and hidden columns
+ * (per expert inter gate rows, then inter up rows), down that of experts *
+ * hidden rows and inter columns.  ids (int32 [tokens, top_k]) and weights
+ * (float [tokens, top_k]) receive the chosen experts and their p_j, in
+ * descending order of l; either may be NULL.  silu(x) = x / (1 + exp(-x)).
+ * h is kept to 16 bits of significand and more (never rounded to 16-bit
+ * floats), sums are fp32, Y is rounded once.  1 <= tokens <=
+ * TC_MOE_MAX_TOKENS, 1 <= top_k <= min(experts, TC_MOE_MAX_TOPK), experts <=
+ * TC_MOE_MAX_EXPERTS (TC_ERR_DIM otherwise, and when the weights' N and K do
+ * not fit); Y, ids and weights overlap no input and one another
+ * (TC_ERR_OVERLAP).  Deterministic run to run. */
+#define TC_MOE_MAX_TOKENS 32
+#define TC_MOE_MAX_EXPERTS 512
+#define TC_MOE_MAX_TOPK 16
+typedef struct {
+    int32_t tokens, hidden, inter, experts, top_k;
+    tc_dtype_t x_dtype, router_dtype, y_dtype;
+    bool renormalize;
+    int32_t ldx, ld_router, ldy;
+} tc_moe_desc;
+tc_status_t tc_moe_q4(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void *router,
+                      const tc_q4_weight *gate_up, const tc_q4_weight *down, void *Y, int32_t *ids, float *weights);
+tc_status_t tc_moe_q4_async(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void *router,
+                            const tc_q4_weight *gate_up, const tc_q4_weight *down, void *Y, int32_t *ids,
+                            float *weights, tc_stream *s);
+/* Host-only: the validation tc_moe_q4 runs first. */
+tc_status_t tc_moe_q4_validate(const tc_moe_desc *d, const void *X, const void *router, const tc_q4_weight *gate_up,
+                               const tc_q4_weight *down, const void *Y, const int32_t *ids, const float *weights);
 
 /* Same GEMM with HOST operands: copies A and B (and C when beta != 0) to the
  * device, runs, copies C back and waits.  Device buffers are cached in the

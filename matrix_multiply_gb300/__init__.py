@@ -29,7 +29,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libtcgemm.so")
 
 # ------------------------------------------------------------------ enums
 
-TC_F16, TC_BF16, TC_F32, TC_I8, TC_I32 = 1, 2, 3, 4, 5
+TC_F16, TC_BF16, TC_F32, TC_I8, TC_I32, TC_I4 = 1, 2, 3, 4, 5, 6
 STATUS = {
     0: "TC_OK", 1: "TC_ERR_NULL", 2: "TC_ERR_DIM", 3: "TC_ERR_LD", 4: "TC_ERR_DTYPE",
     5: "TC_ERR_SCALAR", 6: "TC_ERR_OVERLAP", 7: "TC_ERR_OVERFLOW", 8: "TC_ERR_ALIGN_UNSUPPORTED",
@@ -67,6 +67,24 @@ class tc_gemm_batched_desc(ctypes.Structure):
                 ("stride_c", ctypes.c_int64)]
 
 
+class tc_q4_weight(ctypes.Structure):
+    """A 4-bit weight with group scales (see include/tcgemm.h)."""
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int), ("ldw", ctypes.c_int32), ("ld_scale", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
+
+
+TC_MOE_MAX_TOKENS, TC_MOE_MAX_EXPERTS, TC_MOE_MAX_TOPK = 32, 512, 16
+
+
+class tc_moe_desc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("inter", ctypes.c_int32),
+                ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int), ("router_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
+                ("renormalize", ctypes.c_bool),
+                ("ldx", ctypes.c_int32), ("ld_router", ctypes.c_int32), ("ldy", ctypes.c_int32)]
+
+
 class TcError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -85,6 +103,9 @@ def _load():
     D = ctypes.POINTER(tc_gemm_desc)
     BD = ctypes.POINTER(tc_gemm_batched_desc)
     E = ctypes.POINTER(tc_epilogue)
+    Q = ctypes.POINTER(tc_q4_weight)
+    MD = ctypes.POINTER(tc_moe_desc)
+    i32 = ctypes.c_int32
     sig = {
         "tc_ctx_create": (st, [ctypes.POINTER(vp), ctypes.c_int]),
         "tc_ctx_destroy": (None, [vp]),
@@ -109,6 +130,17 @@ def _load():
         "tc_gemm_q8_weight_async": (st, [vp, D, vp, vp, vp, vp, vp]),
         "tc_gemm_q8_weight_validate": (st, [D, vp, vp, vp, vp]),
         "tc_gemm_f32_relaxed_async": (st, [vp, D, E, vp, vp, vp, vp]),
+        "tc_quantize_q4": (st, [vp, ctypes.c_int, i32, vp, Q]),
+        "tc_quantize_q4_async": (st, [vp, ctypes.c_int, i32, vp, Q, vp]),
+        "tc_dequantize_q4": (st, [vp, Q, ctypes.c_int, i32, vp]),
+        "tc_dequantize_q4_async": (st, [vp, Q, ctypes.c_int, i32, vp, vp]),
+        "tc_q4_validate": (st, [Q, ctypes.c_int, i32, vp]),
+        "tc_gemm_q4_weight": (st, [vp, D, Q, vp, vp]),
+        "tc_gemm_q4_weight_async": (st, [vp, D, Q, vp, vp, vp]),
+        "tc_gemm_q4_weight_validate": (st, [D, Q, vp, vp]),
+        "tc_moe_q4": (st, [vp, MD, vp, vp, Q, Q, vp, vp, vp]),
+        "tc_moe_q4_async": (st, [vp, MD, vp, vp, Q, Q, vp, vp, vp, vp]),
+        "tc_moe_q4_validate": (st, [MD, vp, vp, Q, Q, vp, vp, vp]),
         "tc_gemm_host": (st, [vp, D, vp, vp, vp]),
         "tc_gemm_splitk_noalloc": (st, [D, vp, vp, vp, ctypes.c_int, vp]),
         "tc_gemm_validate": (st, [D, vp, vp, vp]),
@@ -135,6 +167,9 @@ EXPORTED = (
     "tc_status_string", "tc_gemm_epilogue", "tc_gemm_epilogue_async", "tc_gemm_epilogue_validate",
     "tc_gemm_f32_relaxed", "tc_gemm_f32_relaxed_async", "tc_gemm_i8_dequant", "tc_gemm_i8_dequant_async",
     "tc_gemm_q8_weight", "tc_gemm_q8_weight_async", "tc_gemm_q8_weight_validate",
+    "tc_quantize_q4", "tc_quantize_q4_async", "tc_dequantize_q4", "tc_dequantize_q4_async", "tc_q4_validate",
+    "tc_gemm_q4_weight", "tc_gemm_q4_weight_async", "tc_gemm_q4_weight_validate",
+    "tc_moe_q4", "tc_moe_q4_async", "tc_moe_q4_validate",
 )
 
 
@@ -150,7 +185,7 @@ def _check(status: int, what: str):
 
 # ------------------------------------------------------------------ helpers
 
-_DT_NAMES = {"f16": TC_F16, "bf16": TC_BF16, "f32": TC_F32, "i8": TC_I8}
+_DT_NAMES = {"f16": TC_F16, "bf16": TC_BF16, "f32": TC_F32, "i8": TC_I8, "i4": TC_I4}
 
 
 def _torch_dtype_code(t) -> int:
@@ -170,7 +205,8 @@ def _addr(x) -> int:
 def make_desc(M, N, K, a_dtype, c_dtype=None, *, transpose_a=False, transpose_b=False,
               alpha=1.0, beta=0.0, lda=0, ldb=0, ldc=0, b_dtype=None) -> tc_gemm_desc:
     """A descriptor; B has A's type unless ``b_dtype`` is given (the
-    int8-weight product: a_dtype "f16"/"bf16", b_dtype "i8")."""
+    int8-weight and 4-bit-weight products: a_dtype "f16"/"bf16", b_dtype
+    "i8" or "i4")."""
     a = _DT_NAMES.get(a_dtype, a_dtype)
     b = _DT_NAMES.get(b_dtype, b_dtype) if b_dtype is not None else a
     c = _DT_NAMES.get(c_dtype, c_dtype) if c_dtype is not None else a
@@ -270,6 +306,54 @@ class Stream:
             pass
 
 
+class Q4Weight:
+    """A 4-bit weight W[N, K] with group scales in caller-owned CUDA tensors:
+    codes uint8 [N, >= K/2], scales f16/bf16 [ceil(K/group), >= N], zeros
+    uint8 laid out as the scales or None (include/tcgemm.h states the
+    format).  Strides and capacities are checked here; ``desc`` is the C
+    structure.  The tensors stay referenced as long as this object.
+    ``Q4Weight.empty`` allocates the tensors for tc_quantize_q4 to fill."""
+
+    def __init__(self, N: int, K: int, group: int, codes, scales, zeros=None):
+        import torch
+        groups = -(-K // group) if group > 0 else 0
+        for name, t, rows, need in (("codes", codes, N, -(-K // 32) * 16), ("scales", scales, groups, N),
+                                    ("zeros", zeros, groups, N)):
+            if t is None and name == "zeros":
+                continue
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.dim() != 2 or t.stride(1) != 1:
+                raise ValueError(f"{name} must be 2-D with unit column stride")
+            if t.shape[0] < rows or t.shape[1] < need:
+                raise ValueError(f"{name} is {tuple(t.shape)}, the weight needs at least ({rows}, {need})")
+        for name, t in (("codes", codes), ("zeros", zeros)):
+            if t is not None and t.dtype != torch.uint8:
+                raise ValueError(f"{name} must be uint8")
+        if scales.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("scales must be float16 or bfloat16")
+        if zeros is not None and groups > 1 and zeros.stride(0) != scales.stride(0):
+            raise ValueError("zeros must be laid out as the scales")
+        self.N, self.K, self.group = N, K, group
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        # (a single row's stride is torch's choice: 0 lets the library take the minimum)
+        self.desc = tc_q4_weight(N, K, group, _torch_dtype_code(scales), codes.stride(0) * 2 if N > 1 else 0,
+                                 scales.stride(0) if groups > 1 else 0, codes.data_ptr(), scales.data_ptr(),
+                                 zeros.data_ptr() if zeros is not None else None)
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, N: int, K: int, group: int = 128, *, scale_dtype=None, zeros: bool = False, device="cuda"):
+        """Uninitialised tensors of an [N, K] weight, for tc_quantize_q4."""
+        import torch
+        if N < 1 or K < 1 or group < 1:
+            raise ValueError("N, K and group must be at least 1")
+        groups, ns = -(-K // group), -(-N // 16) * 16
+        return cls(N, K, group, torch.empty(N, -(-K // 32) * 16, dtype=torch.uint8, device=device),
+                   torch.empty(groups, ns, dtype=scale_dtype or torch.float16, device=device),
+                   torch.empty(groups, ns, dtype=torch.uint8, device=device) if zeros else None)
+
+
 # ------------------------------------------------------------------ C names
 
 def tc_gemm(ctx: Context, d: tc_gemm_desc, A, B, C):
@@ -328,7 +412,8 @@ class PreparedGemm:
     """One asynchronous product with its arguments checked and marshalled
     once: tc_gemm_async; with ``bias``/``activation`` tc_gemm_epilogue_async;
     with ``relaxed`` tc_gemm_f32_relaxed_async; with ``col_scale``
-    tc_gemm_i8_dequant_async; with ``q8_scale`` tc_gemm_q8_weight_async.
+    tc_gemm_i8_dequant_async; with ``q8_scale`` tc_gemm_q8_weight_async;
+    with a Q4Weight for B tc_gemm_q4_weight_async.
     enqueue() is then one C call -- the library still plans the product and
     launches its kernels every time -- for a caller that issues the same
     product on the same buffers many times (the Python checks otherwise
@@ -337,11 +422,19 @@ class PreparedGemm:
 
     def __init__(self, ctx: Context, d: tc_gemm_desc, A, B, C, stream: Stream, *, bias=None, activation=None,
                  relaxed: bool = False, col_scale=None, q8_scale=None):
-        _check_capacity(d, A, B, C)
         vp = ctypes.c_void_p
+        self._e = None
+        if isinstance(B, Q4Weight):
+            if relaxed or any(x is not None for x in (bias, activation, col_scale, q8_scale)):
+                raise ValueError("a 4-bit weight takes no epilogue, scales or relaxed mode")
+            _check_q4_capacity(d, A, C)
+            self._fn, self._name = _lib.tc_gemm_q4_weight_async, "tc_gemm_q4_weight_async"
+            self._args = (vp(ctx.ptr), ctypes.byref(d), B.ref, vp(_addr(A)), vp(_addr(C)), vp(stream.ptr))
+            self._keep = (ctx, d, A, B, C, stream)
+            return
+        _check_capacity(d, A, B, C)
         head = (vp(ctx.ptr), ctypes.byref(d))
         abc = (vp(_addr(A)), vp(_addr(B)), vp(_addr(C)), vp(stream.ptr))
-        self._e = None
         if q8_scale is not None:
             _require(q8_scale, d.N, "scale")
             self._fn, self._name = _lib.tc_gemm_q8_weight_async, "tc_gemm_q8_weight_async"
@@ -458,6 +551,131 @@ def tc_gemm_q8_weight_async(ctx: Context, d: tc_gemm_desc, X, W, C, scale, strea
 def tc_gemm_q8_weight_validate(d: tc_gemm_desc, scale=4 << 40, X=1 << 20, W=2 << 40, C=3 << 40) -> int:
     """Host-only validation status of an int8-weight product."""
     return int(_lib.tc_gemm_q8_weight_validate(ctypes.byref(d), _addr(scale), _addr(X), _addr(W), _addr(C)))
+
+
+def _matrix_2d(t, N: int, K: int, what: str) -> tuple[int, int]:
+    """(dtype code, leading dimension) of a CUDA tensor holding [N, K]."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 2 or tuple(t.shape) != (N, K) or (K > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be [{N}, {K}] with unit column stride")
+    return _torch_dtype_code(t), t.stride(0) if N > 1 else 0
+
+
+def tc_quantize_q4(ctx: Context, W, q: Q4Weight):
+    """W [N, K] (f16/bf16/f32 CUDA tensor) into q's codes, scales and zeros,
+    synchronously."""
+    dt, ld = _matrix_2d(W, q.N, q.K, "W")
+    _check(_lib.tc_quantize_q4(ctx.ptr, dt, ld, _addr(W), q.ref), "tc_quantize_q4")
+
+
+def tc_quantize_q4_async(ctx: Context, W, q: Q4Weight, stream: Stream):
+    dt, ld = _matrix_2d(W, q.N, q.K, "W")
+    _check(_lib.tc_quantize_q4_async(ctx.ptr, dt, ld, _addr(W), q.ref, stream.ptr), "tc_quantize_q4_async")
+
+
+def tc_dequantize_q4(ctx: Context, q: Q4Weight, V):
+    """V [N, K] (f16/bf16/f32 CUDA tensor) = the values q stands for,
+    synchronously."""
+    dt, ld = _matrix_2d(V, q.N, q.K, "V")
+    _check(_lib.tc_dequantize_q4(ctx.ptr, q.ref, dt, ld, _addr(V)), "tc_dequantize_q4")
+
+
+def tc_dequantize_q4_async(ctx: Context, q: Q4Weight, V, stream: Stream):
+    dt, ld = _matrix_2d(V, q.N, q.K, "V")
+    _check(_lib.tc_dequantize_q4_async(ctx.ptr, q.ref, dt, ld, _addr(V), stream.ptr), "tc_dequantize_q4_async")
+
+
+def tc_q4_validate(q: tc_q4_weight, dtype: int = TC_F16, ld: int = 0, W=1 << 20) -> int:
+    """Host-only validation status of a 4-bit weight and a matrix beside it."""
+    return int(_lib.tc_q4_validate(ctypes.byref(q) if q is not None else None, dtype, ld, _addr(W)))
+
+
+def _check_q4_capacity(d: tc_gemm_desc, X, C):
+    if min(d.M, d.N, d.K) < 1:
+        return   # the library reports the precise error
+    _require(X, _extent(d.M, d.K, d.lda or d.K), "X")
+    _require(C, _extent(d.M, d.N, d.ldc or d.N), "C")
+
+
+def tc_gemm_q4_weight(ctx: Context, d: tc_gemm_desc, X, q: Q4Weight, C):
+    """C = alpha * X @ W^T + beta * C, X [M,K] f16/bf16, W the 4-bit weight q
+    (d: b_dtype "i4", transpose_b), synchronously."""
+    _check_q4_capacity(d, X, C)
+    _check(_lib.tc_gemm_q4_weight(ctx.ptr, ctypes.byref(d), q.ref, _addr(X), _addr(C)), "tc_gemm_q4_weight")
+
+
+def tc_gemm_q4_weight_async(ctx: Context, d: tc_gemm_desc, X, q: Q4Weight, C, stream: Stream):
+    _check_q4_capacity(d, X, C)
+    _check(_lib.tc_gemm_q4_weight_async(ctx.ptr, ctypes.byref(d), q.ref, _addr(X), _addr(C), stream.ptr),
+           "tc_gemm_q4_weight_async")
+
+
+def tc_gemm_q4_weight_validate(d: tc_gemm_desc, q: tc_q4_weight, X=1 << 20, C=3 << 40) -> int:
+    """Host-only validation status of a 4-bit-weight product."""
+    return int(_lib.tc_gemm_q4_weight_validate(ctypes.byref(d), ctypes.byref(q), _addr(X), _addr(C)))
+
+
+def make_moe_desc(tokens, hidden, inter, experts, top_k, x_dtype, y_dtype=None, *, router_dtype="f32",
+                  renormalize=True, ldx=0, ld_router=0, ldy=0) -> tc_moe_desc:
+    x = _DT_NAMES.get(x_dtype, x_dtype)
+    y = _DT_NAMES.get(y_dtype, y_dtype) if y_dtype is not None else x
+    return tc_moe_desc(tokens, hidden, inter, experts, top_k, x, _DT_NAMES.get(router_dtype, router_dtype), y,
+                       bool(renormalize), ldx, ld_router, ldy)
+
+
+class PreparedMoe:
+    """A mixture-of-experts layer (tc_moe_q4) with its arguments checked and
+    marshalled once, as PreparedGemm does for a product: X [tokens, hidden],
+    router [experts, hidden], gate_up and down Q4Weights, Y [tokens, hidden],
+    and optionally ids (int32) and weights (float32), both [tokens, top_k]
+    and contiguous.  enqueue() is one C call; run() the synchronous form."""
+
+    def __init__(self, ctx: Context, d: tc_moe_desc, X, router, gate_up: Q4Weight, down: Q4Weight, Y,
+                 stream: Stream | None = None, *, ids=None, weights=None):
+        import torch
+        vp = ctypes.c_void_p
+        if min(d.tokens, d.hidden, d.experts, d.top_k) >= 1:
+            for name, t, rows, ld, code in (("X", X, d.tokens, d.ldx, d.x_dtype),
+                                            ("router", router, d.experts, d.ld_router, d.router_dtype),
+                                            ("Y", Y, d.tokens, d.ldy, d.y_dtype)):
+                _require(t, _extent(rows, d.hidden, ld or d.hidden), name)
+                if not isinstance(t, int) and _torch_dtype_code(t) != code:
+                    raise ValueError(f"{name} must have the descriptor's dtype")
+            for name, t, dt in (("ids", ids, torch.int32), ("weights", weights, torch.float32)):
+                _require(t, d.tokens * d.top_k, name)
+                if t is not None and not isinstance(t, int) and (t.dtype != dt or not t.is_contiguous()):
+                    raise ValueError(f"{name} must be contiguous {dt}")
+        self._args = (vp(ctx.ptr), ctypes.byref(d), vp(_addr(X)), vp(_addr(router)), gate_up.ref, down.ref,
+                      vp(_addr(Y)), vp(_addr(ids) or None), vp(_addr(weights) or None))
+        self._async = self._args + (vp(stream.ptr),) if stream is not None else None
+        self._keep = (ctx, d, X, router, gate_up, down, Y, stream, ids, weights)
+
+    def enqueue(self):
+        if self._async is None:
+            raise ValueError("enqueue() needs the stream the layer was prepared with")
+        _check(_lib.tc_moe_q4_async(*self._async), "tc_moe_q4_async")
+
+    def run(self):
+        _check(_lib.tc_moe_q4(*self._args), "tc_moe_q4")
+
+
+def tc_moe_q4(ctx: Context, d: tc_moe_desc, X, router, gate_up: Q4Weight, down: Q4Weight, Y, ids=None, weights=None):
+    """A mixture-of-experts layer over 4-bit weights (include/tcgemm.h),
+    synchronously."""
+    PreparedMoe(ctx, d, X, router, gate_up, down, Y, ids=ids, weights=weights).run()
+
+
+def tc_moe_q4_async(ctx: Context, d: tc_moe_desc, X, router, gate_up: Q4Weight, down: Q4Weight, Y, stream: Stream,
+                    ids=None, weights=None):
+    PreparedMoe(ctx, d, X, router, gate_up, down, Y, stream, ids=ids, weights=weights).enqueue()
+
+
+def tc_moe_q4_validate(d: tc_moe_desc, gate_up: tc_q4_weight, down: tc_q4_weight, X=1 << 20, router=1 << 30,
+                       Y=3 << 40, ids=None, weights=None) -> int:
+    """Host-only validation status of a mixture-of-experts layer."""
+    return int(_lib.tc_moe_q4_validate(ctypes.byref(d), _addr(X), _addr(router), ctypes.byref(gate_up),
+                                       ctypes.byref(down), _addr(Y), _addr(ids) or None, _addr(weights) or None))
 
 
 def tc_gemm_host(ctx: Context, d: tc_gemm_desc, A_host, B_host, C_host):

@@ -1372,6 +1372,244 @@ tc_status_t run_q8w(tc_ctx *ctx, const tc_gemm_desc *d, const float *scale, cons
     return st;
 }
 
+// ------------------------------------------------------------ 4-bit weights
+// The checks of a tc_q4_weight (after which q's fields are in v), in the
+// order of validate(): pointers, sizes, types, leading dimensions,
+// overflow, alignment.
+struct Q4Norm {
+    Q4View v;
+    int64_t codes_bytes, scales_bytes, zeros_bytes;
+};
+
+tc_status_t check_q4(const tc_q4_weight *q, Q4Norm *out)
+{
+    if (!q || !q->codes || !q->scales) return TC_ERR_NULL;
+    if (q->N < 1 || q->K < 1 || (q->group != 32 && q->group != 64 && q->group != 128)) return TC_ERR_DIM;
+    if (q->scale_dtype != TC_F16 && q->scale_dtype != TC_BF16) return TC_ERR_DTYPE;
+    Q4Norm n{};
+    n.v.N = q->N;
+    n.v.K = q->K;
+    n.v.ldw = q->ldw ? q->ldw : cdiv(q->K, 32) * 32;
+    n.v.lds = q->ld_scale ? q->ld_scale : cdiv(q->N, 16) * 16;
+    if (n.v.ldw < q->K || n.v.ldw % 32 || n.v.lds < q->N || n.v.lds % 16) return TC_ERR_LD;
+    int64_t nibbles;
+    // (N - 1) ldw + K rounded up to whole 32-element pieces: what TMA may read
+    if (!extent(q->N, cdiv(q->K, 32) * 32, n.v.ldw, 1, 0, 1, &nibbles) ||
+        !extent(cdiv(q->K, q->group), q->N, n.v.lds, 1, 0, 2, &n.scales_bytes))
+        return TC_ERR_OVERFLOW;
+    n.codes_bytes = nibbles / 2;
+    n.zeros_bytes = q->zeros ? n.scales_bytes / 2 : 0;
+    if (!aligned16(q->codes) || !aligned16(q->scales) || (q->zeros && !aligned16(q->zeros)))
+        return TC_ERR_ALIGN_UNSUPPORTED;
+    n.v.codes = static_cast<const uint8_t *>(q->codes);
+    n.v.scales = q->scales;
+    n.v.zeros = static_cast<const uint8_t *>(q->zeros);
+    n.v.group = q->group;
+    n.v.scale_bf16 = q->scale_dtype == TC_BF16;
+    *out = n;
+    return TC_OK;
+}
+
+// p's bytes apart from every part of q
+bool overlaps_q4(const Q4Norm &n, const void *p, int64_t bytes)
+{
+    return ranges_overlap(p, bytes, n.v.codes, n.codes_bytes) || ranges_overlap(p, bytes, n.v.scales, n.scales_bytes) ||
+           (n.v.zeros && ranges_overlap(p, bytes, n.v.zeros, n.zeros_bytes));
+}
+
+// A matrix [N,K] beside q: quantising reads it, dequantising writes it.
+tc_status_t check_q4_matrix(const tc_q4_weight *q, tc_dtype_t dtype, int32_t ld, const void *W, Q4Norm *n,
+                            int64_t *ldn)
+{
+    if (!W) return TC_ERR_NULL;
+    tc_status_t st = check_q4(q, n);
+    if (st != TC_OK) return st;
+    if (dtype != TC_F16 && dtype != TC_BF16 && dtype != TC_F32) return TC_ERR_DTYPE;
+    *ldn = ld ? ld : q->K;
+    if (*ldn < q->K) return TC_ERR_LD;
+    int64_t bytes;
+    if (!extent(q->N, q->K, *ldn, 1, 0, (int64_t)elem_size(dtype), &bytes)) return TC_ERR_OVERFLOW;
+    if (overlaps_q4(*n, W, bytes)) return TC_ERR_OVERLAP;
+    // the parts of q must not share memory either
+    if (ranges_overlap(n->v.codes, n->codes_bytes, n->v.scales, n->scales_bytes) ||
+        (n->v.zeros && (ranges_overlap(n->v.zeros, n->zeros_bytes, n->v.codes, n->codes_bytes) ||
+                        ranges_overlap(n->v.zeros, n->zeros_bytes, n->v.scales, n->scales_bytes))))
+        return TC_ERR_OVERLAP;
+    return TC_OK;
+}
+
+tc_status_t run_quantize(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W, const tc_q4_weight *q,
+                         tc_stream *s)
+{
+    if (!ctx || !s) return TC_ERR_NULL;
+    Q4Norm n;
+    Q4QuantArgs a{};
+    int64_t ldn;
+    const tc_status_t st = check_q4_matrix(q, w_dtype, ld, W, &n, &ldn);
+    if (st != TC_OK) return st;
+    a.W = W;
+    a.ld = ldn;
+    a.w_dtype = w_dtype;
+    a.q = n.v;
+    std::lock_guard<std::mutex> lk(ctx->mu);
+    if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    if (launch_q4_quantize(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += 1;
+    ctx->last = "q4_quantize";
+    return TC_OK;
+}
+
+tc_status_t run_dequantize(tc_ctx *ctx, const tc_q4_weight *q, tc_dtype_t v_dtype, int32_t ld, void *V, tc_stream *s)
+{
+    if (!ctx || !s) return TC_ERR_NULL;
+    Q4Norm n;
+    Q4DequantArgs a{};
+    int64_t ldn;
+    const tc_status_t st = check_q4_matrix(q, v_dtype, ld, V, &n, &ldn);
+    if (st != TC_OK) return st;
+    a.q = n.v;
+    a.V = V;
+    a.ld = ldn;
+    a.v_dtype = v_dtype;
+    std::lock_guard<std::mutex> lk(ctx->mu);
+    if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    if (launch_q4_dequantize(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += 1;
+    ctx->last = "q4_dequantize";
+    return TC_OK;
+}
+
+tc_status_t validate_q4w(const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, const void *C, Q4GemmArgs *out)
+{
+    if (!d || !q || !X || !C) return TC_ERR_NULL;
+    if (d->M < 1 || d->N < 1 || d->K < 1) return TC_ERR_DIM;
+    Q4Norm n;
+    const tc_status_t st = check_q4(q, &n);
+    if (st != TC_OK) return st;
+    if (d->N != q->N || d->K != q->K) return TC_ERR_DIM;
+    if ((d->a_dtype != TC_F16 && d->a_dtype != TC_BF16) || d->b_dtype != TC_I4 || d->accum_dtype != TC_F32 ||
+        (d->c_dtype != d->a_dtype && d->c_dtype != TC_F32))
+        return TC_ERR_DTYPE;
+    if (d->transpose_a || !d->transpose_b) return TC_ERR_LAYOUT;
+    Q4GemmArgs a{};
+    a.q = n.v;
+    a.X = X;
+    a.C = const_cast<void *>(C);
+    a.M = d->M;
+    a.x_bf16 = d->a_dtype == TC_BF16;
+    a.c_dtype = d->c_dtype;
+    a.ldx = d->lda ? d->lda : d->K;
+    a.ldc = d->ldc ? d->ldc : d->N;
+    a.alpha = d->alpha;
+    a.beta = d->beta;
+    if (a.ldx < d->K || a.ldc < d->N || (d->ldb && d->ldb != n.v.ldw)) return TC_ERR_LD;
+    int64_t xb, cb;
+    if (!extent(d->M, d->K, a.ldx, 1, 0, 2, &xb) ||
+        !extent(d->M, d->N, a.ldc, 1, 0, (int64_t)elem_size(d->c_dtype), &cb))
+        return TC_ERR_OVERFLOW;
+    if (!std::isfinite(d->alpha) || !std::isfinite(d->beta)) return TC_ERR_SCALAR;
+    if (ranges_overlap(C, cb, X, xb) || overlaps_q4(n, C, cb)) return TC_ERR_OVERLAP;
+    *out = a;
+    return TC_OK;
+}
+
+tc_status_t run_q4w(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C, tc_stream *s)
+{
+    if (!ctx || !s) return TC_ERR_NULL;
+    Q4GemmArgs a;
+    const tc_status_t st = validate_q4w(d, q, X, C, &a);
+    if (st != TC_OK) return st;
+    std::lock_guard<std::mutex> lk(ctx->mu);
+    if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    if (launch_q4_gemm(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += 1;
+    ctx->last = "q4w_ffma";
+    return TC_OK;
+}
+
+// The layer's checks; fills everything of `out` but the scratch pointers.
+tc_status_t validate_moe(const tc_moe_desc *d, const void *X, const void *R, const tc_q4_weight *w1,
+                         const tc_q4_weight *w2, const void *Y, const int32_t *ids, const float *weights, MoeArgs *out)
+{
+    if (!d || !X || !R || !w1 || !w2 || !Y) return TC_ERR_NULL;
+    if (d->tokens < 1 || d->tokens > TC_MOE_MAX_TOKENS || d->hidden < 1 || d->inter < 1 || d->experts < 1 ||
+        d->experts > TC_MOE_MAX_EXPERTS || d->top_k < 1 || d->top_k > TC_MOE_MAX_TOPK || d->top_k > d->experts)
+        return TC_ERR_DIM;
+    Q4Norm n1, n2;
+    tc_status_t st;
+    if ((st = check_q4(w1, &n1)) != TC_OK || (st = check_q4(w2, &n2)) != TC_OK) return st;
+    if (n1.v.N != 2LL * d->experts * d->inter || n1.v.K != d->hidden || n2.v.N != (int64_t)d->experts * d->hidden ||
+        n2.v.K != d->inter)
+        return TC_ERR_DIM;
+    if ((d->x_dtype != TC_F16 && d->x_dtype != TC_BF16) ||
+        (d->router_dtype != d->x_dtype && d->router_dtype != TC_F32) ||
+        (d->y_dtype != d->x_dtype && d->y_dtype != TC_F32))
+        return TC_ERR_DTYPE;
+    MoeArgs a{};
+    a.T = d->tokens;
+    a.H = d->hidden;
+    a.I = d->inter;
+    a.E = d->experts;
+    a.k = d->top_k;
+    a.x_bf16 = d->x_dtype == TC_BF16;
+    a.r_dtype = d->router_dtype;
+    a.y_dtype = d->y_dtype;
+    a.renorm = d->renormalize;
+    a.X = X;
+    a.R = R;
+    a.Y = const_cast<void *>(Y);
+    a.ldx = d->ldx ? d->ldx : d->hidden;
+    a.ldr = d->ld_router ? d->ld_router : d->hidden;
+    a.ldy = d->ldy ? d->ldy : d->hidden;
+    if (a.ldx < d->hidden || a.ldr < d->hidden || a.ldy < d->hidden) return TC_ERR_LD;
+    a.w1 = n1.v;
+    a.w2 = n2.v;
+    int64_t xb, rb, yb;
+    if (!extent(d->tokens, d->hidden, a.ldx, 1, 0, 2, &xb) ||
+        !extent(d->experts, d->hidden, a.ldr, 1, 0, (int64_t)elem_size(d->router_dtype), &rb) ||
+        !extent(d->tokens, d->hidden, a.ldy, 1, 0, (int64_t)elem_size(d->y_dtype), &yb))
+        return TC_ERR_OVERFLOW;
+    const int64_t kb = 4LL * d->tokens * d->top_k;
+    const struct { const void *p; int64_t bytes; } outs[3] = {{Y, yb}, {ids, ids ? kb : 0}, {weights, weights ? kb : 0}};
+    for (int i = 0; i < 3; ++i) {
+        if (!outs[i].bytes) continue;
+        if (ranges_overlap(outs[i].p, outs[i].bytes, X, xb) || ranges_overlap(outs[i].p, outs[i].bytes, R, rb) ||
+            overlaps_q4(n1, outs[i].p, outs[i].bytes) || overlaps_q4(n2, outs[i].p, outs[i].bytes))
+            return TC_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].bytes && ranges_overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+                return TC_ERR_OVERLAP;
+    }
+    a.ids = const_cast<int *>(ids);
+    a.p = const_cast<float *>(weights);
+    *out = a;
+    return TC_OK;
+}
+
+tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void *R, const tc_q4_weight *w1,
+                    const tc_q4_weight *w2, void *Y, int32_t *ids, float *weights, tc_stream *s)
+{
+    if (!ctx || !s) return TC_ERR_NULL;
+    MoeArgs a;
+    tc_status_t st = validate_moe(d, X, R, w1, w2, Y, ids, weights, &a);
+    if (st != TC_OK) return st;
+    // scratch: logits, the choice where the caller does not take it, and h
+    const size_t lb = round_up((size_t)a.T * a.E * 4, 256), kb = round_up((size_t)a.T * a.k * 4, 256);
+    const size_t hb = round_up((size_t)a.T * a.k * (size_t)a.I * 4, 256);
+    std::lock_guard<std::mutex> lk(ctx->mu);
+    if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    if ((st = ensure_ws(s, lb + 2 * kb + hb)) != TC_OK) return st;
+    uint8_t *ws = static_cast<uint8_t *>(s->ws);
+    a.logits = reinterpret_cast<float *>(ws);
+    if (!a.ids) a.ids = reinterpret_cast<int *>(ws + lb);
+    if (!a.p) a.p = reinterpret_cast<float *>(ws + lb + kb);
+    a.h = reinterpret_cast<float *>(ws + lb + 2 * kb);
+    if (launch_moe(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += moe_launches();
+    ctx->last = "moe_q4";
+    return TC_OK;
+}
+
 tc_status_t stream_init(tc_ctx *ctx, tc_stream *s)
 {
     s->ctx = ctx;
@@ -1605,6 +1843,80 @@ tc_status_t tc_gemm_q8_weight_validate(const tc_gemm_desc *d, const float *scale
     if (!scale) return TC_ERR_NULL;
     if (ranges_overlap(scale, (int64_t)d->N * 4, C, n.c_bytes)) return TC_ERR_OVERLAP;
     return TC_OK;
+}
+
+tc_status_t tc_quantize_q4_async(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W, const tc_q4_weight *q,
+                                 tc_stream *s)
+{
+    return run_quantize(ctx, w_dtype, ld, W, q, s);
+}
+
+tc_status_t tc_quantize_q4(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W, const tc_q4_weight *q)
+{
+    if (!ctx) return TC_ERR_NULL;
+    const tc_status_t st = run_quantize(ctx, w_dtype, ld, W, q, ctx->def);
+    return st == TC_OK ? tc_stream_sync(ctx->def) : st;
+}
+
+tc_status_t tc_dequantize_q4_async(tc_ctx *ctx, const tc_q4_weight *q, tc_dtype_t v_dtype, int32_t ld, void *V,
+                                   tc_stream *s)
+{
+    return run_dequantize(ctx, q, v_dtype, ld, V, s);
+}
+
+tc_status_t tc_dequantize_q4(tc_ctx *ctx, const tc_q4_weight *q, tc_dtype_t v_dtype, int32_t ld, void *V)
+{
+    if (!ctx) return TC_ERR_NULL;
+    const tc_status_t st = run_dequantize(ctx, q, v_dtype, ld, V, ctx->def);
+    return st == TC_OK ? tc_stream_sync(ctx->def) : st;
+}
+
+tc_status_t tc_q4_validate(const tc_q4_weight *q, tc_dtype_t dtype, int32_t ld, const void *W)
+{
+    Q4Norm n;
+    int64_t ldn;
+    return check_q4_matrix(q, dtype, ld, W, &n, &ldn);
+}
+
+tc_status_t tc_gemm_q4_weight_async(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C,
+                                    tc_stream *s)
+{
+    return run_q4w(ctx, d, q, X, C, s);
+}
+
+tc_status_t tc_gemm_q4_weight(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C)
+{
+    if (!ctx) return TC_ERR_NULL;
+    const tc_status_t st = run_q4w(ctx, d, q, X, C, ctx->def);
+    return st == TC_OK ? tc_stream_sync(ctx->def) : st;
+}
+
+tc_status_t tc_gemm_q4_weight_validate(const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, const void *C)
+{
+    Q4GemmArgs a;
+    return validate_q4w(d, q, X, C, &a);
+}
+
+tc_status_t tc_moe_q4_async(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void *router,
+                            const tc_q4_weight *gate_up, const tc_q4_weight *down, void *Y, int32_t *ids,
+                            float *weights, tc_stream *s)
+{
+    return run_moe(ctx, d, X, router, gate_up, down, Y, ids, weights, s);
+}
+
+tc_status_t tc_moe_q4(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void *router,
+                      const tc_q4_weight *gate_up, const tc_q4_weight *down, void *Y, int32_t *ids, float *weights)
+{
+    if (!ctx) return TC_ERR_NULL;
+    const tc_status_t st = run_moe(ctx, d, X, router, gate_up, down, Y, ids, weights, ctx->def);
+    return st == TC_OK ? tc_stream_sync(ctx->def) : st;
+}
+
+tc_status_t tc_moe_q4_validate(const tc_moe_desc *d, const void *X, const void *router, const tc_q4_weight *gate_up,
+                               const tc_q4_weight *down, const void *Y, const int32_t *ids, const float *weights)
+{
+    MoeArgs a;
+    return validate_moe(d, X, router, gate_up, down, Y, ids, weights, &a);
 }
 
 tc_status_t tc_gemm_batched_async(tc_ctx *ctx, const tc_gemm_batched_desc *bd, const void *A, const void *B,

@@ -325,4 +325,58 @@ struct PackBatch {
 };
 cudaError_t launch_pack(PackBatch &pb, cudaStream_t st);
 
+// ------------------------------------------------------------- 4-bit weights
+// A tc_q4_weight after validation (the public header states the format):
+// row n's codes at codes + n * ldw / 2 bytes, the scale of (n, k) at
+// scales[(k / group) * lds + n], the zero point beside it (8 when null).
+struct Q4View {
+    const uint8_t *codes;
+    const void *scales;
+    const uint8_t *zeros;
+    long long N, K, ldw, lds;
+    int group, scale_bf16;
+};
+
+struct Q4QuantArgs {
+    const void *W;
+    long long ld;
+    int w_dtype;
+    Q4View q;              // codes, scales and zeros are written
+};
+cudaError_t launch_q4_quantize(const Q4QuantArgs &a, cudaStream_t st);
+struct Q4DequantArgs {
+    Q4View q;
+    void *V;
+    long long ld;
+    int v_dtype;
+};
+cudaError_t launch_q4_dequantize(const Q4DequantArgs &a, cudaStream_t st);
+
+// C[M, N] = alpha * X[M, K] W^T + beta * C
+struct Q4GemmArgs {
+    Q4View q;
+    const void *X;
+    void *C;
+    int M, x_bf16, c_dtype;
+    long long ldx, ldc;
+    float alpha, beta;
+};
+cudaError_t launch_q4_gemm(const Q4GemmArgs &a, cudaStream_t st);
+
+// The mixture-of-experts layer (the public header states the formulas).
+struct MoeArgs {
+    int T, H, I, E, k;
+    int x_bf16, r_dtype, y_dtype, renorm;
+    const void *X, *R;
+    void *Y;
+    long long ldx, ldr, ldy;
+    Q4View w1, w2;
+    float *logits;         // [T, E]
+    int *ids;              // [T, k], the caller's or scratch
+    float *p;              // [T, k], the caller's or scratch
+    float *h;              // [T k, I]
+};
+cudaError_t launch_moe(const MoeArgs &a, cudaStream_t st);
+int moe_launches();        // kernels one launch_moe starts
+
 }  // namespace tc

@@ -1,0 +1,156 @@
+// 4-bit weights with group scales: quantising, giving the values back, and
+// the product with activations.
+#include "q4.cuh"
+
+namespace tc {
+namespace {
+
+constexpr int Q4_THREADS = 256;
+
+// ------------------------------------------------------------------ quantise
+
+// Rounding to nearest even throughout; the quotient is the IEEE one, so that
+// the code of a 16-bit weight is that of the exact quotient.
+__device__ __forceinline__ uint32_t q4_code(float w, float s, float z)
+{
+    if (s == 0.0f) return 8u;
+    const float c = rintf(__fdiv_rn(w, s)) + z;
+    return (uint32_t)fminf(fmaxf(c, 0.0f), 15.0f);
+}
+
+__global__ void __launch_bounds__(Q4_THREADS) q4_quantize_kernel(const Q4QuantArgs a)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const Q4View &q = a.q;
+    const long long ngroups = (q.K + q.group - 1) / q.group;
+    const long long i = (long long)blockIdx.x * Q4_THREADS + threadIdx.x;
+    if (i >= ngroups * q.N) return;
+    const long long n = i / ngroups, gi = i - n * ngroups;
+    const long long k0 = gi * q.group, k1 = min(q.K, k0 + q.group);
+    const long long kpad = min((q.K + 31) / 32 * 32, k0 + q.group);
+    float lo = 0.0f, hi = 0.0f;
+    bool finite = true;
+    for (long long k = k0; k < k1; ++k) {
+        const float w = load_c(a.W, n * a.ld + k, a.w_dtype);
+        lo = fminf(lo, w);
+        hi = fmaxf(hi, w);
+        finite = finite && isfinite(w);
+    }
+    float s = q.zeros ? __fdiv_rn(hi - lo, 15.0f) : __fdiv_rn(fmaxf(hi, -lo), 7.0f);
+    if (!finite) s = __int_as_float(0x7fc00000);
+    uint16_t bits;
+    if (q.scale_bf16) {
+        bits = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+        s = __bfloat162float(__ushort_as_bfloat16(bits));
+    } else {
+        bits = __half_as_ushort(__float2half_rn(s));
+        s = __half2float(__ushort_as_half(bits));
+    }
+    float z = 8.0f;
+    if (q.zeros && s != 0.0f) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
+    const_cast<uint16_t *>(static_cast<const uint16_t *>(q.scales))[gi * q.lds + n] = bits;
+    if (q.zeros) const_cast<uint8_t *>(q.zeros)[gi * q.lds + n] = (uint8_t)z;
+    uint32_t *row = reinterpret_cast<uint32_t *>(const_cast<uint8_t *>(q.codes) + n * (q.ldw >> 1));
+    for (long long k = k0; k < kpad; k += 8) {
+        uint32_t w = 0;
+        for (int j = 0; j < 8; ++j) {
+            const float v = k + j < k1 ? load_c(a.W, n * a.ld + k + j, a.w_dtype) : 0.0f;
+            w |= q4_code(v, s, z) << (4 * q4_nibble(j));
+        }
+        row[k / 8] = w;
+    }
+}
+
+// ---------------------------------------------------------------- dequantise
+
+__global__ void __launch_bounds__(Q4_THREADS) q4_dequantize_kernel(const Q4DequantArgs a)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const Q4View &q = a.q;
+    const long long words = (q.K + 7) / 8;
+    const long long i = (long long)blockIdx.x * Q4_THREADS + threadIdx.x;
+    if (i >= words * q.N) return;
+    const long long n = i / words, wi = i - n * words, k = wi * 8;
+    const uint32_t w = q4_word(q, n, wi);
+    const float s = q4_scale(q, k / q.group, n);
+    const int z = q4_zero(q, k / q.group, n);
+    for (int j = 0; j < 8; ++j)
+        if (k + j < q.K)
+            store_c1(a.V, n * a.ld + k + j, (float)((int)((w >> (4 * q4_nibble(j))) & 15u) - z) * s, a.v_dtype);
+}
+
+// ------------------------------------------------------------------- product
+
+// A warp takes one row of W against up to 8 rows of X, its lanes striding
+// over the row's words: the whole numbers code - zero times x summed within
+// the word, then times the scale.
+__global__ void __launch_bounds__(Q4_THREADS) q4_gemm_kernel(const Q4GemmArgs a)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const Q4View &q = a.q;
+    const int lane = threadIdx.x & 31;
+    const long long n = (long long)blockIdx.x * (Q4_THREADS / 32) + (threadIdx.x >> 5);
+    const int m0 = blockIdx.y * 8;
+    if (n >= q.N) return;
+    float acc[8] = {};
+    const long long words = (q.K + 7) / 8;
+    for (long long wi = lane; wi < words; wi += 32) {
+        const uint32_t w = q4_word(q, n, wi);
+        const long long k = wi * 8;
+        const float s = q4_scale(q, k / q.group, n);
+        const int z = q4_zero(q, k / q.group, n);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            float sum = 0.0f;
+            if (m0 + m < a.M) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (k + j < q.K)
+                        sum = fmaf((float)((int)((w >> (4 * q4_nibble(j))) & 15u) - z),
+                                   load_16(a.X, (m0 + m) * a.ldx + k + j, a.x_bf16), sum);
+            }
+            acc[m] = fmaf(s, sum, acc[m]);
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
+    if (lane == 0) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+            if (m0 + m >= a.M) break;
+            const long long off = (m0 + m) * a.ldc + n;
+            const float v = a.alpha * acc[m];
+            store_c1(a.C, off, a.beta != 0.0f ? fmaf(a.beta, load_c(a.C, off, a.c_dtype), v) : v, a.c_dtype);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_q4_quantize(const Q4QuantArgs &a, cudaStream_t st)
+{
+    const long long n = (a.q.K + a.q.group - 1) / a.q.group * a.q.N, blocks = (n + Q4_THREADS - 1) / Q4_THREADS;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch_dependent(q4_quantize_kernel, dim3((unsigned)blocks), dim3(Q4_THREADS), 0, st, 1u, a);
+}
+
+cudaError_t launch_q4_dequantize(const Q4DequantArgs &a, cudaStream_t st)
+{
+    const long long n = (a.q.K + 7) / 8 * a.q.N, blocks = (n + Q4_THREADS - 1) / Q4_THREADS;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch_dependent(q4_dequantize_kernel, dim3((unsigned)blocks), dim3(Q4_THREADS), 0, st, 1u, a);
+}
+
+cudaError_t launch_q4_gemm(const Q4GemmArgs &a, cudaStream_t st)
+{
+    const long long bx = (a.q.N + Q4_THREADS / 32 - 1) / (Q4_THREADS / 32), by = (a.M + 7LL) / 8;
+    if (bx > 0x7fffffffLL || by > 65535) return cudaErrorInvalidValue;
+    return launch_dependent(q4_gemm_kernel, dim3((unsigned)bx, (unsigned)by), dim3(Q4_THREADS), 0, st, 1u, a);
+}
+
+}  // namespace tc
