@@ -52,6 +52,7 @@ struct tc_ctx {
     std::mutex host_mu;                            // one tc_gemm_host at a time (it owns dbuf, host_ev)
     int max_pairs[3] = {-1, -1, -1};               // resident CTA pairs (BN 128, 192, 256), queried once
     int csplit_clusters[2][17];                    // resident cluster splits (BN 64, 128; S), -1 = not queried
+    int q4_clusters[9] = {-1, -1, -1, -1, -1, -1, -1, -1, -1};   // resident clusters of the 4-bit streaming kernel
     std::mutex mu;
     tc_ctx()
     {
@@ -1513,6 +1514,46 @@ tc_status_t validate_q4w(const tc_gemm_desc *d, const tc_q4_weight *q, const voi
     return TC_OK;
 }
 
+// A 2-D tensor map of one part of a 4-bit weight.
+bool encode_q4(tc_ctx *ctx, CUtensorMap *m, CUtensorMapDataType t, const void *base, int64_t inner, int64_t outer,
+               int64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle)
+{
+    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    cuuint64_t strides[1] = {(cuuint64_t)pitch_bytes};
+    cuuint32_t box[2] = {box_inner, box_outer}, estr[2] = {1, 1};
+    return ctx->encode(m, t, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The streaming kernel's grid and tensor maps.  One cluster of ksplit CTAs
+// per range of W's rows, ksplit the fewest that leave a warp one slab of K.
+bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f, Q4GemvPlan *p)
+{
+    const int64_t slabs = cdiv(a.q.K, 256);
+    p->ksplit = f.gemv_ks > 0 ? std::min(f.gemv_ks, 8) : (int)std::min<int64_t>(8, cdiv(slabs, 16));
+    p->ksplit = (int)std::min<int64_t>(p->ksplit, slabs);
+    int &fit = ctx->q4_clusters[p->ksplit];
+    if (fit < 0) fit = q4_gemv_max_clusters(p->ksplit);
+    if (fit < 1) return false;
+    const int most = f.gemv_grid > 0 ? f.gemv_grid : fit;
+    p->rows = (int)cdiv(a.q.N, std::min<int64_t>(a.q.N, most));
+    p->clusters = (int)cdiv(a.q.N, p->rows);
+    p->nblk = (int)cdiv(p->rows, 16);
+    p->block_rows = (int)cdiv(p->rows, p->nblk);
+    p->status = s->status_dev;
+    p->timeout_ns = 4000000000ull;
+    const int64_t groups = cdiv(a.q.K, a.q.group);
+    const uint32_t gp = 256 / a.q.group;
+    if (!encode_q4(ctx, &p->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.codes, cdiv(a.q.K, 8) * 4, a.q.N, a.q.ldw / 2, 64,
+                   (uint32_t)p->block_rows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_q4(ctx, &p->scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.q.scales, a.q.N, groups, a.q.lds * 2, Q4_SCALE_BOX,
+                   gp, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return false;
+    p->zeros = p->scales;
+    return !a.q.zeros || encode_q4(ctx, &p->zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.zeros, a.q.N, groups, a.q.lds,
+                                   Q4_ZERO_BOX, gp, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
 tc_status_t run_q4w(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C, tc_stream *s)
 {
     if (!ctx || !s) return TC_ERR_NULL;
@@ -1521,6 +1562,18 @@ tc_status_t run_q4w(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, c
     if (st != TC_OK) return st;
     std::lock_guard<std::mutex> lk(ctx->mu);
     if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    const Force f = read_force();
+    if (a.M <= Q4_GEMV_MAX_ROWS && f.gemv != 0) {
+        Q4GemvPlan p;
+        if (!plan_q4_gemv(ctx, s, a, f, &p)) return TC_ERR_CUDA;
+        if (launch_q4_gemv(a, p, s->st) != cudaSuccess) return TC_ERR_CUDA;
+        ctx->launches += 1;
+        char buf[64];
+        std::snprintf(buf, sizeof buf, "q4w_gemv_x%d_g%d_c%dx%d_b%dx%d", a.M, a.q.group, p.clusters, p.ksplit, p.nblk,
+                      p.block_rows);
+        ctx->last = buf;
+        return TC_OK;
+    }
     if (launch_q4_gemm(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
     ctx->launches += 1;
     ctx->last = "q4w_ffma";

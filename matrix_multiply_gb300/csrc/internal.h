@@ -363,6 +363,24 @@ struct Q4GemmArgs {
 };
 cudaError_t launch_q4_gemm(const Q4GemmArgs &a, cudaStream_t st);
 
+// The same with at most Q4_GEMV_MAX_ROWS rows of X, streaming W (q4_gemv.cu).
+// The grid is `clusters` clusters of ksplit CTAs; cluster c owns the rows
+// [c * rows, (c + 1) * rows) of W, in nblk blocks of block_rows <= 16 rows,
+// and its CTA of rank r the slabs [r n / ksplit, (r + 1) n / ksplit) of the
+// n = ceil(K / 256) slabs of 256 k.
+constexpr int Q4_GEMV_MAX_ROWS = 16;
+struct Q4GemvPlan {
+    int clusters, ksplit, rows, nblk, block_rows;
+    CUtensorMap codes, scales, zeros;
+    unsigned *status;
+    unsigned long long timeout_ns;
+};
+// boxes of the three maps: {64 bytes, block_rows}, {24 scales, 256 / group}, {32 zeros, 256 / group}
+constexpr int Q4_SCALE_BOX = 24, Q4_ZERO_BOX = 32;
+cudaError_t launch_q4_gemv(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st);
+// clusters of ksplit CTAs of that kernel resident at once (0: none)
+int q4_gemv_max_clusters(int ksplit);
+
 // The mixture-of-experts layer (the public header states the formulas).
 struct MoeArgs {
     int T, H, I, E, k;

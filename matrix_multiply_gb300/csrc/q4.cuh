@@ -31,4 +31,191 @@ __device__ __forceinline__ float load_16(const void *p, long long off, int bf16)
     return bf16 ? __bfloat162float(__ushort_as_bfloat16(b)) : __half2float(__ushort_as_half(b));
 }
 
+
+// ------------------------------------------------- streaming kernels' pieces
+// A piece of a 4-bit weight as the streaming kernels hold it in shared
+// memory: 16 rows x Q4_SLAB k as two halves of 16 rows x 64 bytes (128 k),
+// each copied by TMA with the 64-byte swizzle (16-byte unit u of row r sits
+// at u ^ ((r / 2) % 4)), so that a warp reading one 32-bit word per lane --
+// word t of 16-byte unit j of row g, lane = 4 g + t -- touches all 32 banks.
+constexpr int Q4_SLAB = 256;
+constexpr int Q4_HALF_BYTES = 1024;
+
+// D(16x8, f32) = A(16x16) * B(16x8) + C, A row-major, B column-major
+template <bool BF16>
+__device__ __forceinline__ void q4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                       const float (&c)[4])
+{
+    if constexpr (BF16) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+    } else {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+    }
+}
+
+// What turns a row's codes into whole numbers code - zero: the zero point in
+// the biased form that q4_widen subtracts.
+struct Q4Zero {
+    uint32_t a, b;
+};
+template <bool BF16>
+__device__ __forceinline__ Q4Zero q4_zero_form(uint32_t z)
+{
+    const uint32_t zz = z * 0x00010001u;
+    if constexpr (BF16) return Q4Zero{0x43004300u | zz, 0u};             // 128 + z
+    return Q4Zero{0x64006400u | zz, 0xD400D400u | (zz << 4)};            // 1024 + z and -(64 + z)
+}
+
+// The word's eight codes minus the zero point as four pairs of exact 16-bit
+// floats (elements 0 1 | 2 3 | 4 5 | 6 7).  A masked nibble put under the
+// exponent of 2^10 (f16) is 1024 + code, or 1024 + 16 code for the nibble
+// above it, which one multiply-add brings back; bf16 has 7 fraction bits, so
+// there every nibble is shifted to the bottom under 2^7.
+template <bool BF16>
+__device__ __forceinline__ void q4_widen(uint32_t w, const Q4Zero &z, uint32_t (&p)[4])
+{
+    if constexpr (BF16) {
+        const __nv_bfloat162 zz = *reinterpret_cast<const __nv_bfloat162 *>(&z.a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v;
+            asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)));
+            const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), zz);
+            p[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    } else {
+        const __half2 za = *reinterpret_cast<const __half2 *>(&z.a), zb = *reinterpret_cast<const __half2 *>(&z.b);
+        const __half2 sixteenth = __half2half2(__ushort_as_half((unsigned short)0x2C00u));
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            uint32_t u, v;
+            const uint32_t x = w >> (4 * i);
+            asm("lop3.b32 %0, %1, 0x000f000f, 0x64006400, 0xEA;" : "=r"(u) : "r"(x));
+            asm("lop3.b32 %0, %1, 0x00f000f0, 0x64006400, 0xEA;" : "=r"(v) : "r"(x));
+            const __half2 h0 = __hsub2(*reinterpret_cast<const __half2 *>(&u), za);
+            const __half2 h1 = __hfma2(*reinterpret_cast<const __half2 *>(&v), sixteenth, zb);
+            p[i] = *reinterpret_cast<const uint32_t *>(&h0);
+            p[i + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float q4_scale_bits(uint32_t b, int bf16)
+{
+    return bf16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+}
+
+// Where a lane (g, t) finds its share of a slab: the codes of rows g and
+// g + 8 (512 bytes on), and the two rows' scales and zero points of the
+// slab's first group (`ss`, `zs` bytes between groups; z0 == 0: none).
+struct Q4Slab {
+    uint32_t codes, s0, s1, ss, z0, z1, zs;
+};
+
+// acc[nt] (rows g, g + 8 x X rows 8 nt + 2 t, + 1) += the slab's product with
+// xf: step j's register q holds X row 8 nt + g, k = 32 j + 8 t + 2 q and + 1.
+// Each group's products are summed from zero by the tensor core -- whole
+// numbers times 16-bit floats, exact, added in fp32 -- and join the
+// accumulator times the row's scale.  Every lane of the warp calls it.
+template <bool BF16, int NT, int G>
+__device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, const uint32_t (&xf)[NT][8][4], int g,
+                                        int scale_bf16)
+{
+    constexpr int STEPS = G / 32;                  // 32-k steps per group
+    const uint32_t sw = (uint32_t)(g >> 1) & 3u;
+#pragma unroll
+    for (int gr = 0; gr < Q4_SLAB / G; ++gr) {
+        Q4Zero z0 = q4_zero_form<BF16>(8u), z1 = z0;
+        if (b.z0) {
+            z0 = q4_zero_form<BF16>(lds_u8(b.z0 + gr * b.zs) & 15u);
+            z1 = q4_zero_form<BF16>(lds_u8(b.z1 + gr * b.zs) & 15u);
+        }
+        const float s0 = q4_scale_bits(lds_u16(b.s0 + gr * b.ss), scale_bf16);
+        const float s1 = q4_scale_bits(lds_u16(b.s1 + gr * b.ss), scale_bf16);
+        float part[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < STEPS; ++st) {
+            const int j = gr * STEPS + st;
+            const uint32_t at = b.codes + (j >> 2) * Q4_HALF_BYTES + (((uint32_t)(j & 3) ^ sw) << 4);
+            uint32_t p0[4], p1[4];
+            q4_widen<BF16>(lds32(at), z0, p0);
+            q4_widen<BF16>(lds32(at + 512), z1, p1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t lo[4] = {p0[0], p1[0], p0[1], p1[1]}, hi[4] = {p0[2], p1[2], p0[3], p1[3]};
+                q4_mma<BF16>(part[nt], lo, xf[nt][j][0], xf[nt][j][1], part[nt]);
+                q4_mma<BF16>(part[nt], hi, xf[nt][j][2], xf[nt][j][3], part[nt]);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            acc[nt][0] = fmaf(s0, part[nt][0], acc[nt][0]);
+            acc[nt][1] = fmaf(s0, part[nt][1], acc[nt][1]);
+            acc[nt][2] = fmaf(s1, part[nt][2], acc[nt][2]);
+            acc[nt][3] = fmaf(s1, part[nt][3], acc[nt][3]);
+        }
+    }
+}
+
+// A bounded wait: false once `timeout_ns` has passed without the phase.  The
+// kernel then reports through `status`, goes on without the data (its
+// outputs are undefined) and ends.
+static __device__ __noinline__ bool q4_wait_slow(uint32_t bar, uint32_t parity, unsigned *status, unsigned long long timeout_ns)
+{
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 15u) == 0 && globaltimer_ns() - t0 > timeout_ns) {
+            *(volatile unsigned *)status = 0x200u;
+            __threadfence_system();
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, unsigned *status, unsigned long long timeout_ns)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    return q4_wait_slow(bar, parity, status, timeout_ns);
+}
+
+// 16 bytes (8 elements) of X from element k of a row, zeros past K; `vec`:
+// rows are 16-byte aligned
+__device__ __forceinline__ uint4 q4_load_x(const uint16_t *row, long long k, long long K, bool vec)
+{
+    if (vec && k + 8 <= K) return __ldg(reinterpret_cast<const uint4 *>(row + k));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (k + j < K) w[j >> 1] |= (uint32_t)row[k + j] << (16 * (j & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 }  // namespace tc
