@@ -1544,8 +1544,8 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
     p->timeout_ns = 4000000000ull;
     const int64_t groups = cdiv(a.q.K, a.q.group);
     const uint32_t gp = 256 / a.q.group;
-    if (!encode_q4(ctx, &p->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.codes, cdiv(a.q.K, 8) * 4, a.q.N, a.q.ldw / 2, 64,
-                   (uint32_t)p->block_rows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+    if (!encode_q4(ctx, &p->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.codes, cdiv(a.q.K, 8) * 4, a.q.N, a.q.ldw / 2, 128,
+                   (uint32_t)p->block_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_q4(ctx, &p->scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.q.scales, a.q.N, groups, a.q.lds * 2, Q4_SCALE_BOX,
                    gp, CU_TENSOR_MAP_SWIZZLE_NONE))
         return false;

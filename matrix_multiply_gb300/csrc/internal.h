@@ -375,7 +375,8 @@ struct Q4GemvPlan {
     unsigned *status;
     unsigned long long timeout_ns;
 };
-// boxes of the three maps: {64 bytes, block_rows}, {24 scales, 256 / group}, {32 zeros, 256 / group}
+// boxes of the three maps: {128 bytes, block_rows} with the 128-byte swizzle,
+// {24 scales, 256 / group}, {32 zeros, 256 / group}
 constexpr int Q4_SCALE_BOX = 24, Q4_ZERO_BOX = 32;
 cudaError_t launch_q4_gemv(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st);
 // clusters of ksplit CTAs of that kernel resident at once (0: none)

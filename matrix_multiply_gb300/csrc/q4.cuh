@@ -34,12 +34,15 @@ __device__ __forceinline__ float load_16(const void *p, long long off, int bf16)
 
 // ------------------------------------------------- streaming kernels' pieces
 // A piece of a 4-bit weight as the streaming kernels hold it in shared
-// memory: 16 rows x Q4_SLAB k as two halves of 16 rows x 64 bytes (128 k),
-// each copied by TMA with the 64-byte swizzle (16-byte unit u of row r sits
-// at u ^ ((r / 2) % 4)), so that a warp reading one 32-bit word per lane --
-// word t of 16-byte unit j of row g, lane = 4 g + t -- touches all 32 banks.
+// memory: 16 rows x Q4_SLAB k, 128 bytes a row, copied by TMA with the
+// 128-byte swizzle (16-byte unit u of row r sits at u ^ (r % 8)), so that a
+// warp reading one 32-bit word per lane -- word t of unit u of row g, lane =
+// 4 g + t -- touches all 32 banks.  Beside the codes lie, per group, the
+// scales of 24 rows and the zero points of 32, from the last row at or
+// before the piece's first that is a multiple of 8 (16): TMA copies start at
+// multiples of 16 bytes.
 constexpr int Q4_SLAB = 256;
-constexpr int Q4_HALF_BYTES = 1024;
+constexpr int Q4_SCALE_PITCH = 2 * Q4_SCALE_BOX, Q4_ZERO_PITCH = Q4_ZERO_BOX;
 
 // D(16x8, f32) = A(16x16) * B(16x8) + C, A row-major, B column-major
 template <bool BF16>
@@ -126,48 +129,48 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a)
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
-__device__ __forceinline__ float q4_scale_bits(uint32_t b, int bf16)
+template <bool BF16>
+__device__ __forceinline__ float q4_scale_bits(uint32_t b)
 {
-    return bf16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+    return BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
 }
 
-// Where a lane (g, t) finds its share of a slab: the codes of rows g and
-// g + 8 (512 bytes on), and the two rows' scales and zero points of the
-// slab's first group (`ss`, `zs` bytes between groups; z0 == 0: none).
+// Where a lane (g, t) finds its share of a slab: its word of unit 0 of row
+// g (unit u: the address ^ 16 u; row g + 8: 1024 bytes on), and the two
+// rows' scales and zero points of the slab's first group (z0 == 0: none).
 struct Q4Slab {
-    uint32_t codes, s0, s1, ss, z0, z1, zs;
+    uint32_t codes, s0, s1, z0, z1;
 };
+__device__ __forceinline__ uint32_t q4_first_word(int g, int t) { return g * 128 + g * 16 + t * 4; }
 
 // acc[nt] (rows g, g + 8 x X rows 8 nt + 2 t, + 1) += the slab's product with
 // xf: step j's register q holds X row 8 nt + g, k = 32 j + 8 t + 2 q and + 1.
 // Each group's products are summed from zero by the tensor core -- whole
 // numbers times 16-bit floats, exact, added in fp32 -- and join the
 // accumulator times the row's scale.  Every lane of the warp calls it.
-template <bool BF16, int NT, int G>
-__device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, const uint32_t (&xf)[NT][8][4], int g,
-                                        int scale_bf16)
+template <bool BF16, bool SBF16, int NT, int G>
+__device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, const uint32_t (&xf)[NT][8][4])
 {
     constexpr int STEPS = G / 32;                  // 32-k steps per group
-    const uint32_t sw = (uint32_t)(g >> 1) & 3u;
 #pragma unroll
     for (int gr = 0; gr < Q4_SLAB / G; ++gr) {
         Q4Zero z0 = q4_zero_form<BF16>(8u), z1 = z0;
         if (b.z0) {
-            z0 = q4_zero_form<BF16>(lds_u8(b.z0 + gr * b.zs) & 15u);
-            z1 = q4_zero_form<BF16>(lds_u8(b.z1 + gr * b.zs) & 15u);
+            z0 = q4_zero_form<BF16>(lds_u8(b.z0 + gr * Q4_ZERO_PITCH) & 15u);
+            z1 = q4_zero_form<BF16>(lds_u8(b.z1 + gr * Q4_ZERO_PITCH) & 15u);
         }
-        const float s0 = q4_scale_bits(lds_u16(b.s0 + gr * b.ss), scale_bf16);
-        const float s1 = q4_scale_bits(lds_u16(b.s1 + gr * b.ss), scale_bf16);
+        const float s0 = q4_scale_bits<SBF16>(lds_u16(b.s0 + gr * Q4_SCALE_PITCH));
+        const float s1 = q4_scale_bits<SBF16>(lds_u16(b.s1 + gr * Q4_SCALE_PITCH));
         float part[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.0f;
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
             const int j = gr * STEPS + st;
-            const uint32_t at = b.codes + (j >> 2) * Q4_HALF_BYTES + (((uint32_t)(j & 3) ^ sw) << 4);
+            const uint32_t at = b.codes ^ (uint32_t)(j << 4);
             uint32_t p0[4], p1[4];
             q4_widen<BF16>(lds32(at), z0, p0);
-            q4_widen<BF16>(lds32(at + 512), z1, p1);
+            q4_widen<BF16>(lds32(at + 1024), z1, p1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const uint32_t lo[4] = {p0[0], p1[0], p0[1], p1[1]}, hi[4] = {p0[2], p1[2], p0[3], p1[3]};
@@ -188,7 +191,8 @@ __device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, co
 // A bounded wait: false once `timeout_ns` has passed without the phase.  The
 // kernel then reports through `status`, goes on without the data (its
 // outputs are undefined) and ends.
-static __device__ __noinline__ bool q4_wait_slow(uint32_t bar, uint32_t parity, unsigned *status, unsigned long long timeout_ns)
+static __device__ __noinline__ bool q4_wait_slow(uint32_t bar, uint32_t parity, unsigned *status,
+                                                 unsigned long long timeout_ns)
 {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t n = 1;; ++n) {

@@ -8,8 +8,8 @@
 //     slabs, several groups of warps take different blocks.
 //   * Each warp streams its slabs through a ring of its own in shared
 //     memory, filled by TMA (codes, scales, zero points of a block's slab),
-//     several pieces ahead; nothing is shared with other warps until their
-//     sums of a block are added in warp order.
+//     several pieces ahead; nothing is shared with other warps until, every
+//     few blocks, the warps' sums of those blocks are added in a fixed order.
 //   * K above 4096 is split over a cluster of CTAs, whose sums are added in
 //     rank order through distributed shared memory.
 //   * The multiply-adds run on mma.sync m16n8k16 with W as the 16-row
@@ -24,26 +24,30 @@ namespace {
 
 constexpr int GV_WARPS = 16;
 constexpr int GV_STAGES = 3;
-constexpr int GV_STAGE_BYTES = 3072;       // codes 2048, scales <= 384, zero points <= 256 (512-byte aligned stages)
-constexpr int GV_SCALE_AT = 2048, GV_ZERO_AT = 2560;
-constexpr int GV_TILE_LD = 20;             // floats between X rows of a 16-row partial tile: conflict-free both ways
-constexpr int GV_SUM_BLOCKS = 16;          // blocks whose sums a cluster member holds between two exchanges
+constexpr int GV_SCALE_AT = 2048, GV_ZERO_AT = GV_SCALE_AT + 8 * Q4_SCALE_PITCH;
+constexpr int GV_STAGE_BYTES = 3072;       // codes, scales, zero points; a multiple of the swizzle's 1024
+static_assert(GV_ZERO_AT % 128 == 0 && GV_ZERO_AT + 8 * Q4_ZERO_PITCH <= GV_STAGE_BYTES, "stage layout");
 constexpr int GV_RING = GV_WARPS * GV_STAGES * GV_STAGE_BYTES;
+constexpr int GV_TILE_LD = 20;             // floats between X rows of a 16-row partial tile: conflict-free both ways
 
+// blocks whose partial tiles are held before they are added up
+template <int NT>
+__host__ __device__ constexpr int gv_hold() { return NT == 1 ? 6 : 3; }
 template <int NT>
 __host__ __device__ constexpr int gv_tile() { return NT * 8 * GV_TILE_LD; }       // floats
 template <int NT>
 __host__ __device__ constexpr int gv_smem()
 {
-    return 512 + GV_RING + (2 * GV_WARPS + GV_SUM_BLOCKS) * gv_tile<NT>() * 4 + GV_WARPS * GV_STAGES * 8;
+    return 1024 + GV_RING + (GV_WARPS + 1) * gv_hold<NT>() * gv_tile<NT>() * 4 + GV_WARPS * GV_STAGES * 8;
 }
+static_assert(gv_smem<1>() <= SMEM_LIMIT && gv_smem<2>() <= SMEM_LIMIT, "one CTA per SM");
 
 __device__ __forceinline__ void bar_sync(int id, int threads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-template <bool BF16, int NT, int G>
+template <bool BF16, bool SBF16, int NT, int G>
 __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     q4_gemv_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
                    const __grid_constant__ CUtensorMap tmZ, int ksplit, int rows, int nblk, int block_rows,
@@ -51,173 +55,224 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
 {
     constexpr int GP = Q4_SLAB / G;                // groups per slab
     constexpr int TILE = gv_tile<NT>();
-    constexpr int COLS = NT * 8;
+    constexpr int HOLD = gv_hold<NT>();
+    constexpr int S = GV_STAGES;
     extern __shared__ uint8_t raw[];
-    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 511) & ~static_cast<uintptr_t>(511));
-    float *red = reinterpret_cast<float *>(ring + GV_RING);            // [2][GV_WARPS][TILE]
-    float *sums = red + 2 * GV_WARPS * TILE;                           // [GV_SUM_BLOCKS][TILE]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sums + GV_SUM_BLOCKS * TILE);
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    float *tiles = reinterpret_cast<float *>(ring + GV_RING);          // [HOLD][GV_WARPS][TILE]
+    float *sums = tiles + GV_WARPS * HOLD * TILE;                      // [HOLD][TILE], for the cluster
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sums + HOLD * TILE);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int cluster = blockIdx.x / ksplit, rank = blockIdx.x - cluster * ksplit;
-    const int nslab = (int)((a.q.K + Q4_SLAB - 1) / Q4_SLAB);
-    const int s_lo = (int)((long long)rank * nslab / ksplit), s_hi = (int)((long long)(rank + 1) * nslab / ksplit);
+    const int K = (int)a.q.K;
+    const int nslab = (K - 1) / Q4_SLAB + 1;
+    int cluster = blockIdx.x, rank = 0, s_lo = 0, s_hi = nslab;
+    if (ksplit > 1) {
+        cluster = blockIdx.x / (unsigned)ksplit;
+        rank = blockIdx.x - cluster * ksplit;
+        s_lo = (unsigned)(rank * nslab) / (unsigned)ksplit;
+        s_hi = (unsigned)((rank + 1) * nslab) / (unsigned)ksplit;
+    }
     const int mine = s_hi - s_lo;                                      // slabs of this CTA (at least 1)
-    const int wk_n = min(mine, GV_WARPS), wr_n = GV_WARPS / wk_n;      // warps along K, groups along the blocks
-    const int wr = warp / wk_n, wk = warp - wr * wk_n;
+    int wk_n = GV_WARPS, wr_n = 1, wr = 0, wk = warp;                  // warps along K, groups along the blocks
+    if (mine < GV_WARPS) {
+        wk_n = mine;
+        wr_n = ksplit > 1 ? 1u : (unsigned)GV_WARPS / (unsigned)mine;
+        wr = (unsigned)warp / (unsigned)mine;
+        wk = warp - wr * mine;
+    }
     const bool active = wr < wr_n;
-    const int per = active ? (mine - wk + wk_n - 1) / wk_n : 0;        // slabs of this warp in every block
-    const long long r_lo = (long long)cluster * rows, r_hi = min(a.q.N, r_lo + rows);
-    const int nb = active ? (nblk - wr + wr_n - 1) / wr_n : 0;         // blocks of this warp's group: wr, wr + wr_n, ..
-    const int items = nb * per;
+    // slabs of this warp in every block: one, unless K is above 4096 * 8
+    const int per = !active ? 0 : mine <= GV_WARPS ? 1 : (mine - wk + GV_WARPS - 1) / GV_WARPS;
+    const long long r_lo = (long long)cluster * rows;
+    const int nrows = (int)min((long long)rows, a.q.N - r_lo);
 
-    const uint32_t my_ring = smem_u32(ring) + warp * (GV_STAGES * GV_STAGE_BYTES);
-    const uint32_t my_bar = smem_u32(bars + warp * GV_STAGES);
+    const uint32_t my_ring = smem_u32(ring) + warp * (S * GV_STAGE_BYTES);
+    const uint32_t my_bar = smem_u32(bars + warp * S);
+    const bool zeros = a.q.zeros != nullptr;
     if (lane == 0) {
-        for (int i = 0; i < GV_STAGES; ++i) mbar_init(my_bar + 8 * i, 1);
-        fence_barrier_init();
         prefetch_tmap(&tmC);
         prefetch_tmap(&tmS);
+        if (zeros) prefetch_tmap(&tmZ);
+        for (int i = 0; i < S; ++i) mbar_init(my_bar + 8 * i, 1);
+        fence_barrier_init();
     }
     __syncwarp();
     griddep_launch_dependents();
     griddep_wait();
 
-    const bool zeros = a.q.zeros != nullptr;
-    const uint32_t bytes = 2 * block_rows * 64 + GP * (Q4_SCALE_BOX * 2 + (zeros ? Q4_ZERO_BOX : 0));
-    int i_blk = wr, i_s = 0, i_stage = 0;                              // the next item to fetch
+    // lane 0 fetches the warp's pieces in order
+    const uint32_t bytes = block_rows * 128 + GP * (Q4_SCALE_PITCH + (zeros ? Q4_ZERO_PITCH : 0));
+    int f_row = wr * block_rows, f_s = 0, f_stage = 0, fetched = 0;
     auto fetch = [&]() {
-        const int row = (int)(r_lo + (long long)i_blk * block_rows);
-        const int slab = s_lo + wk + i_s * wk_n;
-        const uint32_t st = my_ring + i_stage * GV_STAGE_BYTES, bar = my_bar + 8 * i_stage;
+        if (f_row >= nrows || per == 0) return;
+        const int row = (int)(r_lo + f_row), slab = s_lo + wk + f_s * GV_WARPS;
+        const uint32_t st = my_ring + f_stage * GV_STAGE_BYTES, bar = my_bar + 8 * f_stage;
         mbar_arrive_expect_tx(bar, bytes);
         tma_load_2d(st, &tmC, bar, slab * (Q4_SLAB / 2), row);
-        tma_load_2d(st + Q4_HALF_BYTES, &tmC, bar, slab * (Q4_SLAB / 2) + 64, row);
         tma_load_2d(st + GV_SCALE_AT, &tmS, bar, row & ~7, slab * GP);
         if (zeros) tma_load_2d(st + GV_ZERO_AT, &tmZ, bar, row & ~15, slab * GP);
-        if (++i_stage == GV_STAGES) i_stage = 0;
-        if (++i_s == per) i_s = 0, i_blk += wr_n;
+        ++fetched;
+        if (++f_stage == S) f_stage = 0;
+        if (++f_s == per) f_s = 0, f_row += wr_n * block_rows;
     };
-    int fetched = min(items, GV_STAGES);                               // lane 0's count
     if (lane == 0)
-        for (int i = 0; i < fetched; ++i) fetch();
+        for (int i = 0; i < S; ++i) fetch();
     __syncwarp();
 
     // this warp's share of X: of one slab, for the whole kernel; with several
-    // slabs a warp (K above 4096 * 8) it is read again for each piece
+    // slabs a warp it is read again for each piece
     const uint16_t *X = static_cast<const uint16_t *>(a.X);
     const bool x_vec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (a.ldx & 7) == 0;
     uint32_t xf[NT][8][4];
     auto load_xf = [&](int slab) {
+        const bool whole = x_vec && slab < K / Q4_SLAB;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            const uint16_t *row = X + (nt * 8 + g) * a.ldx;
+            const long long k = (long long)slab * Q4_SLAB + t * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (nt * 8 + g < a.M)
-                    v = q4_load_x(X + (nt * 8 + g) * a.ldx, (long long)slab * Q4_SLAB + j * 32 + t * 8, a.q.K, x_vec);
-                xf[nt][j][0] = v.x, xf[nt][j][1] = v.y, xf[nt][j][2] = v.z, xf[nt][j][3] = v.w;
+            for (int j = 0; j < 8; ++j) xf[nt][j][0] = xf[nt][j][1] = xf[nt][j][2] = xf[nt][j][3] = 0u;
+            if (nt * 8 + g < a.M) {
+                if (whole) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + k) + 4 * j);
+                        xf[nt][j][0] = v.x, xf[nt][j][1] = v.y, xf[nt][j][2] = v.z, xf[nt][j][3] = v.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint4 v = q4_load_x(row, k + 32 * j, K, x_vec);
+                        xf[nt][j][0] = v.x, xf[nt][j][1] = v.y, xf[nt][j][2] = v.z, xf[nt][j][3] = v.w;
+                    }
+                }
             }
-    };
-    if (per > 0) load_xf(s_lo + wk);
-
-    auto write_out = [&](int blk, int e, float v) {
-        const int col = e >> 4, r = e & 15;
-        const long long n = r_lo + (long long)blk * block_rows + r;
-        if (r < block_rows && n < r_hi && col < a.M) {
-            const long long off = col * a.ldc + n;
-            v *= a.alpha;
-            store_c1(a.C, off, a.beta != 0.0f ? fmaf(a.beta, load_c(a.C, off, a.c_dtype), v) : v, a.c_dtype);
         }
     };
+    if (per > 0) load_xf(s_lo + wk);
+    const uint32_t word = q4_first_word(g, t);
 
-    int stage = 0, parity = 0, buf = 0;
+    // outputs of X row `col`, W rows r and r + 1 of a block
+    auto write_out = [&](int blk, int col, int r, float v0, float v1) {
+        const int left = min(block_rows, nrows - blk * block_rows) - r;
+        if (left <= 0 || col >= a.M) return;
+        const long long off = col * a.ldc + r_lo + blk * block_rows + r;
+        v0 *= a.alpha, v1 *= a.alpha;
+        if (a.beta != 0.0f) {
+            v0 = fmaf(a.beta, load_c(a.C, off, a.c_dtype), v0);
+            if (left > 1) v1 = fmaf(a.beta, load_c(a.C, off + 1, a.c_dtype), v1);
+        }
+        store_c1(a.C, off, v0, a.c_dtype);
+        if (left > 1) store_c1(a.C, off + 1, v1, a.c_dtype);
+    };
+
+    int stage = 0, parity = 0;
     bool ok = true;
-    // phases of GV_SUM_BLOCKS blocks when a cluster exchanges its sums, else one
-    const int phase_blocks = ksplit > 1 ? GV_SUM_BLOCKS : nblk;
-    int blk = wr;
-    for (int first = 0; first < nblk; first += phase_blocks) {
-        const int last = min(nblk, first + phase_blocks);
-        for (; active && blk < last; blk += wr_n) {
+    // phases of HOLD blocks per group of warps
+    for (int first = ksplit > 1 ? 0 : wr; first < nblk; first += HOLD * wr_n) {
+        if (!active) {
+            if (ksplit == 1) break;
+        }
+        int held = 0;
+        for (int blk = first; active && blk < nblk && held < HOLD; blk += wr_n, ++held) {
             float acc[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-            const int row = (int)(r_lo + (long long)blk * block_rows);
+            const int row = (int)(r_lo & 15) + blk * block_rows;       // (only its low bits are used)
             for (int s = 0; s < per; ++s) {
-                if (per > 1) load_xf(s_lo + wk + s * wk_n);
+                if (blk * block_rows >= nrows) break;                  // rows past N: nothing was fetched
+                if (per > 1) load_xf(s_lo + wk + s * GV_WARPS);
                 ok = ok && q4_wait(my_bar + 8 * stage, parity, status, timeout_ns);
                 __syncwarp();
                 const uint32_t st = my_ring + stage * GV_STAGE_BYTES;
                 Q4Slab b;
-                b.codes = st + g * 64 + t * 4;
+                b.codes = st + word;
                 b.s0 = st + GV_SCALE_AT + ((row & 7) + g) * 2;
                 b.s1 = b.s0 + 16;
-                b.ss = Q4_SCALE_BOX * 2;
                 b.z0 = zeros ? st + GV_ZERO_AT + (row & 15) + g : 0u;
                 b.z1 = b.z0 + 8;
-                b.zs = Q4_ZERO_BOX;
-                q4_slab<BF16, NT, G>(acc, b, xf, g, a.q.scale_bf16);
-                __syncwarp();
-                if (fetched < items && lane == 0 && ok) fetch(), ++fetched;
-                if (++stage == GV_STAGES) stage = 0, parity ^= 1;
+                q4_slab<BF16, SBF16, NT, G>(acc, b, xf);
+                __syncwarp();                                          // every lane has read the piece
+                if (lane == 0 && ok) fetch();
+                if (++stage == S) stage = 0, parity ^= 1;
             }
-            // the group's warps add their tiles in warp order; two buffers, so
-            // that one barrier a block is enough
-            float *tile = red + (buf * GV_WARPS + warp) * TILE;
+            float *tile = tiles + (held * GV_WARPS + warp) * TILE + 2 * t * GV_TILE_LD + g;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    tile[(nt * 8 + 2 * t + (e & 1)) * GV_TILE_LD + g + 8 * (e >> 1)] = acc[nt][e];
+                    tile[(nt * 8 + (e & 1)) * GV_TILE_LD + 8 * (e >> 1)] = acc[nt][e];
+        }
+        __syncwarp();
+        if (active) {
             bar_sync(wr, wk_n * 32);
-            const float *tiles = red + (buf * GV_WARPS + wr * wk_n) * TILE;
-            for (int e = wk * 32 + lane; e < COLS * 16; e += wk_n * 32) {
-                const int at = (e >> 4) * GV_TILE_LD + (e & 15);
-                float v = tiles[at];
-                for (int w = 1; w < wk_n; ++w) v += tiles[w * TILE + at];
+            // a pair of threads per four rows of one X row: each adds every
+            // other warp's tile, in warp order, then the two join
+            const int half = lane & 1;
+            for (int e = (wk * 32 + lane) >> 1; e < HOLD * NT * 32; e += wk_n * 16) {
+                const int h = e / (NT * 32), c = (e >> 2) % (NT * 8), r = (e & 3) * 4;
+                const int o = c * GV_TILE_LD + r;
+                const bool in = h < held && c < a.M;
+                const float *p = tiles + (h * GV_WARPS + warp - wk) * TILE + o;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int w = 0; w < GV_WARPS; w += 2)
+                    if (in && w + half < wk_n) {
+                        const float4 x = *reinterpret_cast<const float4 *>(p + (w + half) * TILE);
+                        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+                    }
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, 1);
+                v.y += __shfl_xor_sync(0xffffffffu, v.y, 1);
+                v.z += __shfl_xor_sync(0xffffffffu, v.z, 1);
+                v.w += __shfl_xor_sync(0xffffffffu, v.w, 1);
+                if (!in) continue;
                 if (ksplit == 1)
-                    write_out(blk, e, v);
-                else
-                    sums[(blk - first) * TILE + at] = v;
+                    write_out(first + h * wr_n, c, r + 2 * half, half ? v.z : v.x, half ? v.w : v.y);
+                else if (!half)
+                    *reinterpret_cast<float4 *>(sums + h * TILE + o) = v;
             }
-            buf ^= 1;
         }
         if (ksplit > 1) {
             __syncwarp();
             cluster_sync();
             const uint32_t base = smem_u32(sums);
-            for (int i = threadIdx.x; i < (last - first) * COLS * 16; i += GV_WARPS * 32) {
-                const int b = i / (COLS * 16), e = i - b * (COLS * 16);
-                if (b % ksplit != rank) continue;
-                const uint32_t at = base + (uint32_t)(b * TILE + (e >> 4) * GV_TILE_LD + (e & 15)) * 4u;
-                float part[8];
+            const int count = min(HOLD, nblk - first);
+            // the phase's outputs, pairs of rows, dealt out to the ranks' threads
+            for (int i = rank * (GV_WARPS * 32) + threadIdx.x; i < count * NT * 64; i += ksplit * GV_WARPS * 32) {
+                const int h = i / (NT * 64), c = (i >> 3) % (NT * 8), r = (i & 7) * 2;
+                if (c >= a.M) continue;
+                const uint32_t o = base + (uint32_t)(h * TILE + c * GV_TILE_LD + r) * 4u;
+                float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                    if (q < ksplit) part[q] = ld_shared_cluster_f32(mapa_shared(at, (uint32_t)q));
-                float v = part[0];
-#pragma unroll
-                for (int q = 1; q < 8; ++q)
-                    if (q < ksplit) v += part[q];
-                write_out(first + b, e, v);
+                    if (q < ksplit) {
+                        const uint32_t peer = mapa_shared(o, (uint32_t)q);
+                        v0 += ld_shared_cluster_f32(peer);
+                        v1 += ld_shared_cluster_f32(peer + 4);
+                    }
+                write_out(first + h, c, r, v0, v1);
             }
             __syncwarp();
             cluster_sync();      // the sums are read before they are overwritten, or their CTA ends
+        } else if (first + HOLD * wr_n < nblk) {
+            bar_sync(wr, wk_n * 32);      // the tiles are read before the next phase's are written
         }
     }
     // after an expired wait: copies still in flight land (within a limit)
     // before shared memory is released
     if (!ok && lane == 0)
-        for (int i = 0; i < GV_STAGES; ++i) {
-            const int n = (fetched + GV_STAGES - 1 - i) / GV_STAGES;   // copies into this stage
+        for (int i = 0; i < S; ++i) {
+            const int n = (fetched + S - 1 - i) / S;                   // copies into this stage
             const uint64_t t0 = globaltimer_ns();
             while (n > 0 && !mbar_try_wait(my_bar + 8 * i, (uint32_t)(n - 1) & 1u) && globaltimer_ns() - t0 < 200000000ull) {}
         }
 }
 
-template <bool BF16, int NT, int G>
+template <bool BF16, bool SBF16, int NT, int G>
 cudaError_t launch_one(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st)
 {
-    constexpr auto kern = q4_gemv_kernel<BF16, NT, G>;
+    constexpr auto kern = q4_gemv_kernel<BF16, SBF16, NT, G>;
     constexpr int smem = gv_smem<NT>();
     static std::atomic<bool> configured[64] = {};
     int dev = 0;
@@ -233,6 +288,16 @@ cudaError_t launch_one(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st
                             p.status, p.timeout_ns);
 }
 
+template <bool BF16, bool SBF16, int NT>
+cudaError_t launch_group(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st)
+{
+    switch (a.q.group) {
+    case 32: return launch_one<BF16, SBF16, NT, 32>(a, p, st);
+    case 64: return launch_one<BF16, SBF16, NT, 64>(a, p, st);
+    default: return launch_one<BF16, SBF16, NT, 128>(a, p, st);
+    }
+}
+
 }  // namespace
 
 int q4_gemv_max_clusters(int ksplit)
@@ -243,7 +308,7 @@ int q4_gemv_max_clusters(int ksplit)
         cudaGetDevice(&dev);
         return cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? sms : 0;
     }
-    constexpr auto kern = q4_gemv_kernel<true, 2, 128>;
+    constexpr auto kern = q4_gemv_kernel<true, true, 2, 128>;
     constexpr int smem = gv_smem<2>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
@@ -267,21 +332,12 @@ cudaError_t launch_q4_gemv(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_
     if (a.M < 1 || a.M > Q4_GEMV_MAX_ROWS || p.ksplit < 1 || p.ksplit > 8 || p.clusters < 1 || p.block_rows < 1 ||
         p.block_rows > 16)
         return cudaErrorInvalidValue;
-    const int g = a.q.group == 32 ? 0 : a.q.group == 64 ? 1 : 2;
-    switch ((a.x_bf16 ? 6 : 0) + (a.M > 8 ? 3 : 0) + g) {
-    case 0: return launch_one<false, 1, 32>(a, p, st);
-    case 1: return launch_one<false, 1, 64>(a, p, st);
-    case 2: return launch_one<false, 1, 128>(a, p, st);
-    case 3: return launch_one<false, 2, 32>(a, p, st);
-    case 4: return launch_one<false, 2, 64>(a, p, st);
-    case 5: return launch_one<false, 2, 128>(a, p, st);
-    case 6: return launch_one<true, 1, 32>(a, p, st);
-    case 7: return launch_one<true, 1, 64>(a, p, st);
-    case 8: return launch_one<true, 1, 128>(a, p, st);
-    case 9: return launch_one<true, 2, 32>(a, p, st);
-    case 10: return launch_one<true, 2, 64>(a, p, st);
-    default: return launch_one<true, 2, 128>(a, p, st);
-    }
+    const bool wide = a.M > 8;
+    if (a.x_bf16)
+        return a.q.scale_bf16 ? (wide ? launch_group<true, true, 2>(a, p, st) : launch_group<true, true, 1>(a, p, st))
+                              : (wide ? launch_group<true, false, 2>(a, p, st) : launch_group<true, false, 1>(a, p, st));
+    return a.q.scale_bf16 ? (wide ? launch_group<false, true, 2>(a, p, st) : launch_group<false, true, 1>(a, p, st))
+                          : (wide ? launch_group<false, false, 2>(a, p, st) : launch_group<false, false, 1>(a, p, st));
 }
 
 }  // namespace tc
