@@ -50,13 +50,13 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], const uint32_t (&a)[4], ui
                                        const float (&c)[4])
 {
     if constexpr (BF16) {
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%10, %11, %12, %13};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
     } else {
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%10, %11, %12, %13};"
             : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -111,35 +111,21 @@ __device__ __forceinline__ void q4_widen(uint32_t w, const Q4Zero &z, uint32_t (
     }
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
-{
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t a)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
 template <bool BF16>
 __device__ __forceinline__ float q4_scale_bits(uint32_t b)
 {
     return BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
 }
 
-// Where a lane (g, t) finds its share of a slab: its word of unit 0 of row
-// g (unit u: the address ^ 16 u; row g + 8: 1024 bytes on), and the two
-// rows' scales and zero points of the slab's first group (z0 == 0: none).
+// Where a lane (g, t) finds its share of a slab in shared memory: its word
+// of unit 0 of row g (unit u: the offset ^ 16 u; row g + 8: 1024 bytes on),
+// and the two rows' scales and zero points of the slab's first group
+// (z0 null: none).
 struct Q4Slab {
-    uint32_t codes, s0, s1, z0, z1;
+    const uint8_t *base;       // a multiple of 1024 in shared memory
+    uint32_t codes;
+    const uint16_t *s0, *s1;
+    const uint8_t *z0, *z1;
 };
 __device__ __forceinline__ uint32_t q4_first_word(int g, int t) { return g * 128 + g * 16 + t * 4; }
 
@@ -156,21 +142,21 @@ __device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, co
     for (int gr = 0; gr < Q4_SLAB / G; ++gr) {
         Q4Zero z0 = q4_zero_form<BF16>(8u), z1 = z0;
         if (b.z0) {
-            z0 = q4_zero_form<BF16>(lds_u8(b.z0 + gr * Q4_ZERO_PITCH) & 15u);
-            z1 = q4_zero_form<BF16>(lds_u8(b.z1 + gr * Q4_ZERO_PITCH) & 15u);
+            z0 = q4_zero_form<BF16>((uint32_t)b.z0[gr * Q4_ZERO_PITCH] & 15u);
+            z1 = q4_zero_form<BF16>((uint32_t)b.z1[gr * Q4_ZERO_PITCH] & 15u);
         }
-        const float s0 = q4_scale_bits<SBF16>(lds_u16(b.s0 + gr * Q4_SCALE_PITCH));
-        const float s1 = q4_scale_bits<SBF16>(lds_u16(b.s1 + gr * Q4_SCALE_PITCH));
+        const float s0 = q4_scale_bits<SBF16>(b.s0[gr * (Q4_SCALE_PITCH / 2)]);
+        const float s1 = q4_scale_bits<SBF16>(b.s1[gr * (Q4_SCALE_PITCH / 2)]);
         float part[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.0f;
 #pragma unroll
         for (int st = 0; st < STEPS; ++st) {
             const int j = gr * STEPS + st;
-            const uint32_t at = b.codes ^ (uint32_t)(j << 4);
+            const uint32_t *at = reinterpret_cast<const uint32_t *>(b.base + (b.codes ^ (uint32_t)(j << 4)));
             uint32_t p0[4], p1[4];
-            q4_widen<BF16>(lds32(at), z0, p0);
-            q4_widen<BF16>(lds32(at + 1024), z1, p1);
+            q4_widen<BF16>(at[0], z0, p0);
+            q4_widen<BF16>(at[256], z1, p1);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const uint32_t lo[4] = {p0[0], p1[0], p0[1], p1[1]}, hi[4] = {p0[2], p1[2], p0[3], p1[3]};

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     constexpr int HOLD = gv_hold<NT>();
     constexpr int S = GV_STAGES;
     extern __shared__ uint8_t raw[];
-    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     float *tiles = reinterpret_cast<float *>(ring + GV_RING);          // [HOLD][GV_WARPS][TILE]
     float *sums = tiles + GV_WARPS * HOLD * TILE;                      // [HOLD][TILE], for the cluster
     uint64_t *bars = reinterpret_cast<uint64_t *>(sums + HOLD * TILE);
@@ -185,12 +185,13 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
                 if (per > 1) load_xf(s_lo + wk + s * GV_WARPS);
                 ok = ok && q4_wait(my_bar + 8 * stage, parity, status, timeout_ns);
                 __syncwarp();
-                const uint32_t st = my_ring + stage * GV_STAGE_BYTES;
+                const uint8_t *st = ring + (warp * S + stage) * GV_STAGE_BYTES;
                 Q4Slab b;
-                b.codes = st + word;
-                b.s0 = st + GV_SCALE_AT + ((row & 7) + g) * 2;
-                b.s1 = b.s0 + 16;
-                b.z0 = zeros ? st + GV_ZERO_AT + (row & 15) + g : 0u;
+                b.base = st;
+                b.codes = word;
+                b.s0 = reinterpret_cast<const uint16_t *>(st + GV_SCALE_AT) + (row & 7) + g;
+                b.s1 = b.s0 + 8;
+                b.z0 = zeros ? st + GV_ZERO_AT + (row & 15) + g : nullptr;
                 b.z1 = b.z0 + 8;
                 q4_slab<BF16, SBF16, NT, G>(acc, b, xf);
                 __syncwarp();                                          // every lane has read the piece
