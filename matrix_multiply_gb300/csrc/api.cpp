@@ -1554,6 +1554,73 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
                                    Q4_ZERO_BOX, gp, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// The tensor-core kernel's tile width and K split: the least estimated time,
+// in cycles -- a 64-k block of a 128 x bn tile takes 2 bn on the tensor core
+// and about 150 to convert; a tile has a fixed part besides.
+void plan_q4_mma(int num_sms, const Q4GemmArgs &a, const Force &f, Q4MmaPlan *p)
+{
+    const int64_t kbs = cdiv(a.q.K, 64), tn = cdiv(a.q.N, Q4_MMA_ROWS);
+    double best = 0.0;
+    p->bn = 0;
+    for (int bn : {128, 96, 64, 32}) {
+        if (f.bn > 0 && f.bn != bn) continue;
+        const int64_t tm = cdiv(a.M, bn), tiles = tn * tm;
+        int split = f.split > 0 ? std::min(f.split, 8) : (int)std::min<int64_t>(8, num_sms / tiles);
+        split = std::max(1, (int)std::min<int64_t>(split, cdiv(kbs, 4)));
+        if (f.split == 0 && split > 1) split = (int)std::max<int64_t>(1, std::min<int64_t>(split, kbs / 8));
+        const double waves = split > 1 ? 1.0 : (double)cdiv(tiles, num_sms);
+        const double t = waves * ((double)cdiv(kbs, split) * std::max(2.0 * bn, 150.0) + 2500.0 + 10.0 * bn) +
+                         (split > 1 ? 3000.0 : 0.0);
+        if (p->bn == 0 || t < best) {
+            best = t;
+            p->bn = bn;
+            p->split = split;
+            p->tiles_n = (int)tn;
+            p->tiles_m = (int)tm;
+            p->grid = split > 1 ? (int)(tiles * split) : (int)std::min<int64_t>(tiles, num_sms);
+        }
+    }
+    if (p->bn == 0) {          // a forced width this kernel does not have
+        Force g = f;
+        g.bn = 0;
+        plan_q4_mma(num_sms, a, g, p);
+    }
+}
+
+tc_status_t enqueue_q4_mma(tc_ctx *ctx, tc_stream *s, Q4GemmArgs a, const Force &f)
+{
+    Q4MmaPlan p{};
+    plan_q4_mma(ctx->num_sms, a, f, &p);
+    if ((int64_t)p.tiles_n * p.tiles_m * p.split > INT32_MAX / 2) return TC_ERR_OVERFLOW;
+    int launches = 1;
+    if (!aligned16(a.X) || a.ldx % 8 != 0) {
+        // rows TMA cannot address: a copy with padded rows in the stream's buffer
+        const int64_t ld = cdiv(a.q.K, 64) * 64;
+        const tc_status_t st = ensure_rx(s, (size_t)(a.M * ld * 2));
+        if (st != TC_OK) return st;
+        PackBatch pb;
+        pb.count = 1;
+        pb.seg[0] = PackArgs{static_cast<const uint16_t *>(a.X), static_cast<uint16_t *>(s->rx), a.M, a.q.K, a.ldx, ld, 0, 0, 1};
+        if (launch_pack(pb, s->st) != cudaSuccess) return TC_ERR_CUDA;
+        ++launches;
+        a.X = s->rx;
+        a.ldx = ld;
+    }
+    if (!encode_q4(ctx, &p.codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.codes, cdiv(a.q.K, 8) * 4, a.q.N, a.q.ldw / 2, 128,
+                   Q4_MMA_ROWS, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_q4(ctx, &p.x, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.X, a.q.K, a.M, a.ldx * 2, 64, (uint32_t)p.bn,
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+        return TC_ERR_CUDA;
+    p.status = s->status_dev;
+    p.timeout_ns = 4000000000ull + (unsigned long long)cdiv(a.q.K, 64) * 20000ull;
+    if (launch_q4_mma(a, p, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += launches;
+    char buf[64];
+    std::snprintf(buf, sizeof buf, "q4w_tcgen05_128x%d_g%d%s_s%d", p.bn, a.q.group, launches > 1 ? "_pack" : "", p.split);
+    ctx->last = buf;
+    return TC_OK;
+}
+
 tc_status_t run_q4w(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C, tc_stream *s)
 {
     if (!ctx || !s) return TC_ERR_NULL;
@@ -1574,10 +1641,7 @@ tc_status_t run_q4w(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, c
         ctx->last = buf;
         return TC_OK;
     }
-    if (launch_q4_gemm(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
-    ctx->launches += 1;
-    ctx->last = "q4w_ffma";
-    return TC_OK;
+    return enqueue_q4_mma(ctx, s, a, f);
 }
 
 // The layer's checks; fills everything of `out` but the scratch pointers.

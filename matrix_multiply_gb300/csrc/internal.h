@@ -361,9 +361,8 @@ struct Q4GemmArgs {
     long long ldx, ldc;
     float alpha, beta;
 };
-cudaError_t launch_q4_gemm(const Q4GemmArgs &a, cudaStream_t st);
 
-// The same with at most Q4_GEMV_MAX_ROWS rows of X, streaming W (q4_gemv.cu).
+// For at most Q4_GEMV_MAX_ROWS rows of X, streaming W (q4_gemv.cu).
 // The grid is `clusters` clusters of ksplit CTAs; cluster c owns the rows
 // [c * rows, (c + 1) * rows) of W, in nblk blocks of block_rows <= 16 rows,
 // and its CTA of rank r the slabs [r n / ksplit, (r + 1) n / ksplit) of the
@@ -381,6 +380,19 @@ constexpr int Q4_SCALE_BOX = 24, Q4_ZERO_BOX = 32;
 cudaError_t launch_q4_gemv(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st);
 // clusters of ksplit CTAs of that kernel resident at once (0: none)
 int q4_gemv_max_clusters(int ksplit);
+
+// The same for more rows of X, on the tcgen05 tensor cores (q4_mma.cu): tiles
+// of 128 rows of W by bn rows of X, bn in {32, 64, 96, 128}; with split > 1
+// the K slices of a tile form a cluster whose sums are added on chip (one
+// unit per CTA).  X is readable by TMA (16-byte base and row pitch).
+constexpr int Q4_MMA_ROWS = 128;
+struct Q4MmaPlan {
+    int bn, split, tiles_n, tiles_m, grid;
+    CUtensorMap codes, x;      // boxes {128 bytes, 128 rows} and {64 elements, bn rows}, 128-byte swizzle
+    unsigned *status;
+    unsigned long long timeout_ns;
+};
+cudaError_t launch_q4_mma(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st);
 
 // The mixture-of-experts layer (the public header states the formulas).
 struct MoeArgs {

@@ -1,5 +1,4 @@
-// 4-bit weights with group scales: quantising, giving the values back, and
-// the product with activations.
+// 4-bit weights with group scales: quantising and giving the values back.
 #include "q4.cuh"
 
 namespace tc {
@@ -81,55 +80,6 @@ __global__ void __launch_bounds__(Q4_THREADS) q4_dequantize_kernel(const Q4Dequa
             store_c1(a.V, n * a.ld + k + j, (float)((int)((w >> (4 * q4_nibble(j))) & 15u) - z) * s, a.v_dtype);
 }
 
-// ------------------------------------------------------------------- product
-
-// A warp takes one row of W against up to 8 rows of X, its lanes striding
-// over the row's words: the whole numbers code - zero times x summed within
-// the word, then times the scale.
-__global__ void __launch_bounds__(Q4_THREADS) q4_gemm_kernel(const Q4GemmArgs a)
-{
-    griddep_launch_dependents();
-    griddep_wait();
-    const Q4View &q = a.q;
-    const int lane = threadIdx.x & 31;
-    const long long n = (long long)blockIdx.x * (Q4_THREADS / 32) + (threadIdx.x >> 5);
-    const int m0 = blockIdx.y * 8;
-    if (n >= q.N) return;
-    float acc[8] = {};
-    const long long words = (q.K + 7) / 8;
-    for (long long wi = lane; wi < words; wi += 32) {
-        const uint32_t w = q4_word(q, n, wi);
-        const long long k = wi * 8;
-        const float s = q4_scale(q, k / q.group, n);
-        const int z = q4_zero(q, k / q.group, n);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            float sum = 0.0f;
-            if (m0 + m < a.M) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (k + j < q.K)
-                        sum = fmaf((float)((int)((w >> (4 * q4_nibble(j))) & 15u) - z),
-                                   load_16(a.X, (m0 + m) * a.ldx + k + j, a.x_bf16), sum);
-            }
-            acc[m] = fmaf(s, sum, acc[m]);
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(0xffffffffu, acc[m], o);
-    if (lane == 0) {
-#pragma unroll
-        for (int m = 0; m < 8; ++m) {
-            if (m0 + m >= a.M) break;
-            const long long off = (m0 + m) * a.ldc + n;
-            const float v = a.alpha * acc[m];
-            store_c1(a.C, off, a.beta != 0.0f ? fmaf(a.beta, load_c(a.C, off, a.c_dtype), v) : v, a.c_dtype);
-        }
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_q4_quantize(const Q4QuantArgs &a, cudaStream_t st)
@@ -144,13 +94,6 @@ cudaError_t launch_q4_dequantize(const Q4DequantArgs &a, cudaStream_t st)
     const long long n = (a.q.K + 7) / 8 * a.q.N, blocks = (n + Q4_THREADS - 1) / Q4_THREADS;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     return launch_dependent(q4_dequantize_kernel, dim3((unsigned)blocks), dim3(Q4_THREADS), 0, st, 1u, a);
-}
-
-cudaError_t launch_q4_gemm(const Q4GemmArgs &a, cudaStream_t st)
-{
-    const long long bx = (a.q.N + Q4_THREADS / 32 - 1) / (Q4_THREADS / 32), by = (a.M + 7LL) / 8;
-    if (bx > 0x7fffffffLL || by > 65535) return cudaErrorInvalidValue;
-    return launch_dependent(q4_gemm_kernel, dim3((unsigned)bx, (unsigned)by), dim3(Q4_THREADS), 0, st, 1u, a);
 }
 
 }  // namespace tc

@@ -174,26 +174,39 @@ __device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, co
     }
 }
 
-// A bounded wait: false once `timeout_ns` has passed without the phase.  The
-// kernel then reports through `status`, goes on without the data (its
-// outputs are undefined) and ends.
-static __device__ __noinline__ bool q4_wait_slow(uint32_t bar, uint32_t parity, unsigned *status,
-                                                 unsigned long long timeout_ns)
+// Bounded waits.  A wait that runs out reports through `status` and raises
+// the CTA's abort flag (where it has one), which ends the other waits of the
+// CTA; the kernel then finishes without the data, its outputs undefined.
+struct Q4Watch {
+    volatile uint32_t *abort_flag;      // or null
+    unsigned *status;
+    unsigned long long timeout_ns;
+};
+static __device__ __noinline__ bool q4_wait_slow(uint32_t bar, uint32_t parity, const Q4Watch &w)
 {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t n = 1;; ++n) {
         if (mbar_try_wait(bar, parity)) return true;
-        if ((n & 15u) == 0 && globaltimer_ns() - t0 > timeout_ns) {
-            *(volatile unsigned *)status = 0x200u;
+        if ((n & 15u) != 0) continue;
+        if (w.abort_flag && *w.abort_flag) return false;
+        if (globaltimer_ns() - t0 > w.timeout_ns) {
+            if (w.abort_flag) *w.abort_flag = 1u;
+            *(volatile unsigned *)w.status = 0x200u;
             __threadfence_system();
             return false;
         }
     }
 }
-__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, unsigned *status, unsigned long long timeout_ns)
+__device__ __forceinline__ bool q4_wait(uint32_t bar, uint32_t parity, const Q4Watch &w)
 {
     if (mbar_try_wait(bar, parity)) return true;
-    return q4_wait_slow(bar, parity, status, timeout_ns);
+    return q4_wait_slow(bar, parity, w);
+}
+// after an expired wait: up to 0.2 s for a copy or an MMA already under way
+static __device__ __noinline__ void q4_drain(uint32_t bar, uint32_t parity)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < 200000000ull) {}
 }
 
 // 16 bytes (8 elements) of X from element k of a row, zeros past K; `vec`:

@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
         if (left > 1) store_c1(a.C, off + 1, v1, a.c_dtype);
     };
 
+    const Q4Watch watch{nullptr, status, timeout_ns};
     int stage = 0, parity = 0;
     bool ok = true;
     // phases of HOLD blocks per group of warps
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
             for (int s = 0; s < per; ++s) {
                 if (blk * block_rows >= nrows) break;                  // rows past N: nothing was fetched
                 if (per > 1) load_xf(s_lo + wk + s * GV_WARPS);
-                ok = ok && q4_wait(my_bar + 8 * stage, parity, status, timeout_ns);
+                ok = ok && q4_wait(my_bar + 8 * stage, parity, watch);
                 __syncwarp();
                 const uint8_t *st = ring + (warp * S + stage) * GV_STAGE_BYTES;
                 Q4Slab b;
@@ -265,8 +266,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     if (!ok && lane == 0)
         for (int i = 0; i < S; ++i) {
             const int n = (fetched + S - 1 - i) / S;                   // copies into this stage
-            const uint64_t t0 = globaltimer_ns();
-            while (n > 0 && !mbar_try_wait(my_bar + 8 * i, (uint32_t)(n - 1) & 1u) && globaltimer_ns() - t0 < 200000000ull) {}
+            if (n > 0) q4_drain(my_bar + 8 * i, (uint32_t)(n - 1) & 1u);
         }
 }
 

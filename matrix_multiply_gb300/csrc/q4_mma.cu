@@ -1,0 +1,413 @@
+// The product of many rows of X with a 4-bit weight on the tcgen05 tensor
+// cores: C = alpha X W^T + beta C, W the 128-row operand, X's rows its
+// columns.
+//
+// W stays 4 bits up to the SM: converter warps (thread = row of W) read the
+// codes that TMA brought to shared memory, turn them into the whole numbers
+// code - zero, exact in X's 16-bit type, and write them to TMEM, from where
+// the tensor core takes its 128-row operand; X's tiles come through shared
+// memory by TMA.  Each group of k is summed from zero in one of two TMEM
+// accumulators; promoting warps (thread = row of W, so a group's scale is
+// one number per thread) read it and add it times the scale to fp32 sums in
+// registers.  No weight is rounded, and the scales cost one packed
+// multiply-add per two sums and group.  Roles, one CTA of 14 warps per SM
+// (14: the register file holds 128 registers for each thread of 16 warps, 96
+// for more):
+//   converters   one or, for narrow tiles, two per 32 rows (on alternate 64-k
+//                blocks: a narrow block's MMAs take less time than converting)
+//   promoters    one or, for wide tiles, two per 32 rows (half the columns
+//                each: their sums fill the registers); they write C
+//   one warp for the TMA copies, one that issues the MMAs
+// Few tiles: the K slices of a tile form a cluster and add their sums in
+// rank order through distributed shared memory.  Deterministic.
+#include "q4.cuh"
+
+#include <atomic>
+
+namespace tc {
+namespace {
+
+__host__ __device__ constexpr int qm_conv(int bn) { return bn > 64 ? 4 : 8; }
+__host__ __device__ constexpr int qm_prom(int bn) { return bn > 64 ? 8 : 4; }
+constexpr int QM_THREADS = (4 + 8 + 2) * 32;
+constexpr int QM_XS = 8, QM_CS = 4;             // ring stages: X (64 k), codes (256 k)
+constexpr int QM_AS = 4;                        // TMEM stages of the converted operand (64 k, 32 columns)
+constexpr int QM_CODE_BYTES = Q4_MMA_ROWS * 128;
+constexpr int QM_PART_LD = Q4_MMA_ROWS + 4;     // floats between columns of a slice's partial tile
+
+// (never below half an SM's: a CTA holds all of TMEM, and one that waits for
+// its cluster while another, on the same SM, waits for that TMEM could wait
+// for ever)
+__host__ __device__ constexpr int qm_smem(int bn)
+{
+    const int need = 1024 + QM_XS * bn * 128 + QM_CS * QM_CODE_BYTES + 512;
+    return need > 120 * 1024 ? need : 120 * 1024;
+}
+static_assert(qm_smem(128) <= SMEM_LIMIT, "one CTA per SM");
+static_assert(32 * QM_PART_LD * 4 <= QM_XS * 32 * 128 && 128 * QM_PART_LD * 4 <= QM_XS * 128 * 128,
+              "a partial tile fits in the idle X ring");
+
+// D[tmem] (+)= A[tmem] B[smem]
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// two fp32 multiply-adds
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+    return d;
+}
+
+struct QmUnit {
+    int n0, m0, kb0, kb1;
+};
+__device__ __forceinline__ QmUnit qm_unit(int u, int split, int tiles_m, int bn, int num_kb)
+{
+    const int tile = split > 1 ? u / split : u, s = u - tile * split;
+    QmUnit w;
+    w.n0 = (tile / tiles_m) * Q4_MMA_ROWS;
+    w.m0 = (tile % tiles_m) * bn;
+    // slices of whole 256-k blocks: no group is cut
+    const int nb = (num_kb + 3) / 4;
+    w.kb0 = split > 1 ? (int)((long long)s * nb / split) * 4 : 0;
+    w.kb1 = split > 1 ? min(num_kb, (int)((long long)(s + 1) * nb / split) * 4) : num_kb;
+    return w;
+}
+
+template <bool BF16, int BN, int G>
+__global__ void __launch_bounds__(QM_THREADS, 1)
+    q4_mma_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
+                  int split, int tiles_m, int units, unsigned *status, unsigned long long timeout_ns)
+{
+    constexpr int X_BYTES = BN * 128;
+    constexpr int QM_CONV = qm_conv(BN), QM_PROM = qm_prom(BN);
+    constexpr int HB = BN / (QM_PROM / 4);         // columns of one promoting warp
+    constexpr uint32_t TMEM_COLS = 512;
+    constexpr uint32_t A_COL = 2 * BN;             // the converted operand's stages follow the accumulators
+    static_assert(2 * BN + QM_AS * 32 <= 512 && BN % 32 == 0, "TMEM columns");
+    constexpr uint32_t IDESC = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((uint32_t)(BN >> 3) << 17) |
+                               ((uint32_t)(Q4_MMA_ROWS >> 4) << 24);
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint8_t *codes = smem + QM_XS * X_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(codes + QM_CS * QM_CODE_BYTES);
+    const uint32_t xfull = smem_u32(bars), xempty = xfull + 8 * QM_XS, cfull = xempty + 8 * QM_XS,
+                   cempty = cfull + 8 * QM_CS, afull = cempty + 8 * QM_CS, aempty = afull + 8 * QM_AS,
+                   dfull = aempty + 8 * QM_AS, dempty = dfull + 16, drain = dempty + 16;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 2 * QM_XS + 2 * QM_CS + 2 * QM_AS + 5);
+    volatile uint32_t *abort_flag = slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < QM_XS; ++i) mbar_init(xfull + 8 * i, 1), mbar_init(xempty + 8 * i, 1);
+        for (int i = 0; i < QM_CS; ++i) mbar_init(cfull + 8 * i, 1), mbar_init(cempty + 8 * i, QM_CONV);
+        for (int i = 0; i < QM_AS; ++i) mbar_init(afull + 8 * i, 4), mbar_init(aempty + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, QM_PROM);
+        mbar_init(drain, 1);
+        *abort_flag = 0u;
+        fence_barrier_init();
+        prefetch_tmap(&tmC);
+        prefetch_tmap(&tmX);
+        griddep_launch_dependents();
+    }
+    __syncwarp();
+    if (warp == 0) tmem_alloc(smem_u32(slot), TMEM_COLS);
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *slot;
+    griddep_wait();
+
+    const Q4Watch watch{abort_flag, status, timeout_ns};
+    const int num_kb = (int)((a.q.K + 63) / 64);
+    const int step = split > 1 ? units : (int)gridDim.x;       // a cluster's CTAs take one unit each
+    bool ok = true;
+
+    if (warp == QM_CONV + QM_PROM) {
+        // ------------------------------------------------------ TMA copies
+        if (lane == 0) {
+            int xi = 0, ci = 0;                                 // copies issued
+            for (int u = blockIdx.x; ok && u < units; u += step) {
+                const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    if ((kb & 3) == 0) {
+                        const int st = ci % QM_CS;
+                        if (!(ok = q4_wait(cempty + 8 * st, ((ci / QM_CS) & 1) ^ 1, watch))) break;
+                        mbar_arrive_expect_tx(cfull + 8 * st, QM_CODE_BYTES);
+                        tma_load_2d(smem_u32(codes) + st * QM_CODE_BYTES, &tmC, cfull + 8 * st, kb * 32, w.n0);
+                        ++ci;
+                    }
+                    const int st = xi % QM_XS;
+                    if (!(ok = q4_wait(xempty + 8 * st, ((xi / QM_XS) & 1) ^ 1, watch))) break;
+                    mbar_arrive_expect_tx(xfull + 8 * st, X_BYTES);
+                    tma_load_2d(smem_u32(smem) + st * X_BYTES, &tmX, xfull + 8 * st, kb * 64, w.m0);
+                    ++xi;
+                }
+            }
+            if (!ok) {       // let the copies already issued land before shared memory is released
+                for (int i = max(0, xi - QM_XS); i < xi; ++i) q4_drain(xfull + 8 * (i % QM_XS), (i / QM_XS) & 1);
+                for (int i = max(0, ci - QM_CS); i < ci; ++i) q4_drain(cfull + 8 * (i % QM_CS), (i / QM_CS) & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == QM_CONV + QM_PROM + 1) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int it = 0, gi = 0;                                 // 64-k blocks and groups so far
+            const uint64_t bd0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+            for (int u = blockIdx.x; ok && u < units; u += step) {
+                const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+                for (int kb = w.kb0; ok && kb < w.kb1; ++kb, ++it) {
+                    const int xs = it % QM_XS, as = it % QM_AS;
+                    if (!(ok = q4_wait(xfull + 8 * xs, (it / QM_XS) & 1, watch))) break;
+                    if (!(ok = q4_wait(afull + 8 * as, (it / QM_AS) & 1, watch))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const bool first = ((kb * 4 + k) % (G / 16)) == 0;
+                        if (first) {
+                            if (!(ok = q4_wait(dempty + 8 * (gi & 1), ((gi >> 1) & 1) ^ 1, watch))) break;
+                            tc_fence_after();
+                        }
+                        mma_f16_ts(tmem + (gi & 1) * BN, tmem + A_COL + as * 32 + k * 8,
+                                   bd0 + (uint64_t)(xs * (X_BYTES >> 4) + k * 2), IDESC, first ? 0u : 1u);
+                        if ((kb * 4 + k + 1) % (G / 16) == 0 || (k == 3 && kb + 1 == w.kb1)) {
+                            mma_commit(dfull + 8 * (gi & 1));
+                            ++gi;
+                        }
+                    }
+                    mma_commit(xempty + 8 * xs);
+                    mma_commit(aempty + 8 * as);
+                }
+            }
+            if (!ok) {
+                mma_commit(drain);
+                q4_drain(drain, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp < QM_CONV) {
+        // ------------------------------------------------------ converters
+        const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+        constexpr int GP = Q4_SLAB / G;
+        const long long ngroups = (a.q.K + G - 1) / G;
+        int it = 0, ci = 0;
+        for (int u = blockIdx.x; ok && u < units; u += step) {
+            const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+            const bool in = a.q.zeros && w.n0 + row < a.q.N;
+            const uint8_t *zp = in ? a.q.zeros + w.n0 + row : a.q.zeros;
+            // a row's zero points of a 256-k block, loaded one block ahead
+            uint32_t z[GP], zn[GP];
+            auto load_z = [&](int kb) {
+#pragma unroll
+                for (int i = 0; i < GP; ++i) {
+                    const long long gr = (long long)kb * 64 / G + i;
+                    zn[i] = (in && gr < ngroups) ? zp[gr * a.q.lds] & 15u : 8u;
+                }
+            };
+            load_z(w.kb0);
+            for (int kb = w.kb0; ok && kb < w.kb1; kb += 4, ++ci) {
+#pragma unroll
+                for (int i = 0; i < GP; ++i) z[i] = zn[i];
+                if (kb + 4 < w.kb1) load_z(kb + 4);
+                const int cs = ci % QM_CS;
+                ok = __all_sync(0xffffffffu, q4_wait(cfull + 8 * cs, (ci / QM_CS) & 1, watch));
+                if (!ok) break;
+                const uint8_t *src = codes + cs * QM_CODE_BYTES + row * 128;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (kb + i >= w.kb1 || !ok) break;
+                    const int at = it++;
+                    if (QM_CONV == 8 && (at & 1) != half) continue;
+                    const int as = at % QM_AS;
+                    uint32_t words[8];
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (((2 * i + v) ^ (row & 7)) << 4));
+                        words[4 * v] = x.x, words[4 * v + 1] = x.y, words[4 * v + 2] = x.z, words[4 * v + 3] = x.w;
+                    }
+                    uint32_t out[32];
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        const Q4Zero zf = q4_zero_form<BF16>(z[(i * 64 + v * 8) / G]);
+                        uint32_t p[4];
+                        q4_widen<BF16>(words[v], zf, p);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) out[4 * v + j] = p[j];
+                    }
+                    ok = __all_sync(0xffffffffu, q4_wait(aempty + 8 * as, ((at / QM_AS) & 1) ^ 1, watch));
+                    if (!ok) break;
+                    tc_fence_after();
+                    tmem_st_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + A_COL + as * 32, out);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(afull + 8 * as);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(cempty + 8 * cs);
+            }
+        }
+    } else {
+        // ------------------------------------------------------ promoting warps
+        const int pw = warp - QM_CONV, quarter = pw & 3, half = pw >> 2, row = quarter * 32 + lane;
+        const long long ngroups = (a.q.K + G - 1) / G;
+        const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * HB;
+        int gi = 0;
+        for (int u = blockIdx.x; ok && u < units; u += step) {
+            const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+            const long long n = w.n0 + row;
+            uint64_t acc[HB / 2];
+#pragma unroll
+            for (int i = 0; i < HB / 2; ++i) acc[i] = 0ull;
+            const int g0 = (int)((long long)w.kb0 * 64 / G);
+            const int gn = G == 32 ? 2 * (w.kb1 - w.kb0) : (w.kb1 - w.kb0 + G / 64 - 1) / (G / 64);
+            auto scale = [&](int i) { return (n < a.q.N && g0 + i < ngroups && i < gn) ? q4_scale(a.q, g0 + i, n) : 0.0f; };
+            float s0 = scale(0), s1 = scale(1), s2 = scale(2);
+            for (int i = 0; i < gn; ++i, ++gi) {
+                const float s = s0;
+                s0 = s1, s1 = s2, s2 = scale(i + 3);       // loaded three groups ahead
+                ok = __all_sync(0xffffffffu, q4_wait(dfull + 8 * (gi & 1), (gi >> 1) & 1, watch));
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ss = pack64(__float_as_uint(s), __float_as_uint(s));
+#pragma unroll
+                for (int c = 0; c < HB; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld_x16(taddr + (gi & 1) * BN + c, r);
+                    tmem_ld_wait();
+                    if (c + 16 == HB) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(dempty + 8 * (gi & 1));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        acc[c / 2 + j] = fma2(ss, pack64(r[2 * j], r[2 * j + 1]), acc[c / 2 + j]);
+                }
+            }
+            if (!ok) break;
+            if (split > 1) {
+                // all of the unit's MMAs have completed: the X ring is idle
+                float *part = reinterpret_cast<float *>(smem);
+#pragma unroll
+                for (int c = 0; c < HB; ++c)
+                    part[(half * HB + c) * QM_PART_LD + row] =
+                        __uint_as_float(c & 1 ? (uint32_t)(acc[c / 2] >> 32) : (uint32_t)acc[c / 2]);
+            } else if (n < a.q.N) {
+                const int cols = min(HB, a.M - w.m0 - half * HB);
+                const long long off = (long long)(w.m0 + half * HB) * a.ldc + n;
+#pragma unroll
+                for (int c = 0; c < HB; ++c)
+                    if (c < cols) {
+                        float v = a.alpha * __uint_as_float(c & 1 ? (uint32_t)(acc[c / 2] >> 32) : (uint32_t)acc[c / 2]);
+                        if (a.beta != 0.0f) v = fmaf(a.beta, load_c(a.C, off + c * a.ldc, a.c_dtype), v);
+                        store_c1(a.C, off + c * a.ldc, v, a.c_dtype);
+                    }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) {
+        cluster_sync();              // every slice's partial tile is in its CTA's shared memory
+        const QmUnit w = qm_unit(blockIdx.x, split, tiles_m, BN, num_kb);
+        const int rank = (int)cluster_ctarank();
+        const int c0 = rank * BN / split, c1 = (rank + 1) * BN / split;
+        const uint32_t base = smem_u32(smem);
+        for (int i = c0 * Q4_MMA_ROWS + threadIdx.x; i < c1 * Q4_MMA_ROWS; i += QM_THREADS) {
+            const int c = i / Q4_MMA_ROWS, r = i % Q4_MMA_ROWS;
+            const long long n = w.n0 + r;
+            if (n >= a.q.N || w.m0 + c >= a.M || *abort_flag) continue;
+            const uint32_t o = base + (uint32_t)(c * QM_PART_LD + r) * 4u;
+            float p[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < split) p[q] = ld_shared_cluster_f32(mapa_shared(o, (uint32_t)q));
+            float v = p[0];
+#pragma unroll
+            for (int q = 1; q < 8; ++q)
+                if (q < split) v += p[q];
+            v *= a.alpha;
+            const long long off = (long long)(w.m0 + c) * a.ldc + n;
+            if (a.beta != 0.0f) v = fmaf(a.beta, load_c(a.C, off, a.c_dtype), v);
+            store_c1(a.C, off, v, a.c_dtype);
+        }
+        __syncwarp();
+        cluster_sync();              // no CTA releases its shared memory while a peer may read it
+    }
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+}
+
+template <bool BF16, int BN, int G>
+cudaError_t launch_one(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st)
+{
+    constexpr auto kern = q4_mma_kernel<BF16, BN, G>;
+    constexpr int smem = qm_smem(BN);
+    static std::atomic<bool> configured[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        configured[dev].store(true, std::memory_order_release);
+    }
+    return launch_dependent(kern, dim3((unsigned)p.grid), dim3(QM_THREADS), smem, st, (unsigned)p.split, a, p.codes, p.x,
+                            p.split, p.tiles_m, p.tiles_n * p.tiles_m * p.split, p.status, p.timeout_ns);
+}
+
+template <bool BF16, int BN>
+cudaError_t launch_group(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st)
+{
+    switch (a.q.group) {
+    case 32: return launch_one<BF16, BN, 32>(a, p, st);
+    case 64: return launch_one<BF16, BN, 64>(a, p, st);
+    default: return launch_one<BF16, BN, 128>(a, p, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_q4_mma(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st)
+{
+    if (p.split < 1 || p.split > 8 || p.grid < 1 || p.grid % p.split != 0 ||
+        (p.split > 1 && p.grid != p.tiles_n * p.tiles_m * p.split))
+        return cudaErrorInvalidValue;
+    switch (p.bn) {
+    case 32: return a.x_bf16 ? launch_group<true, 32>(a, p, st) : launch_group<false, 32>(a, p, st);
+    case 64: return a.x_bf16 ? launch_group<true, 64>(a, p, st) : launch_group<false, 64>(a, p, st);
+    case 96: return a.x_bf16 ? launch_group<true, 96>(a, p, st) : launch_group<false, 96>(a, p, st);
+    case 128: return a.x_bf16 ? launch_group<true, 128>(a, p, st) : launch_group<false, 128>(a, p, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace tc
