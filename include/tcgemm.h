@@ -323,7 +323,8 @@ tc_status_t tc_gemm_q4_weight_validate(const tc_gemm_desc *d, const tc_q4_weight
  * router R [experts, hidden] (ld_router), router_dtype x_dtype or TC_F32;
  * gate_up the 4-bit weight of experts * 2 * inter rows and hidden columns
  * (per expert inter gate rows, then inter up rows), down that of experts *
- * hidden rows and inter columns.  ids (int32 [tokens, top_k]) and weights
+ * hidden rows and inter columns, both with the same group (TC_ERR_DIM
+ * otherwise) and scale_dtype (TC_ERR_DTYPE).  ids (int32 [tokens, top_k]) and weights
  * (float [tokens, top_k]) receive the chosen experts and their p_j, in
  * descending order of l; either may be NULL.  silu(x) = x / (1 + exp(-x)).
  * h is kept to 16 bits of significand and more (never rounded to 16-bit

@@ -34,6 +34,8 @@ struct tc_stream {
     size_t ws_cap = 0;
     void *rx = nullptr;              // relaxed fp32: the bf16 split operands
     size_t rx_cap = 0;
+    unsigned *sync = nullptr;        // the grid barrier's words of kernels that cross one
+    bool sync_clear = false;         // they are as such a kernel expects and leaves them
     unsigned *status_host = nullptr; // mapped, pinned: kernels report timeouts here
     unsigned *status_dev = nullptr;
 };
@@ -611,6 +613,7 @@ tc_status_t read_status(tc_stream *s)
     volatile unsigned *st = s->status_host;
     if (st && *st != 0u) {
         *st = 0u;
+        s->sync_clear = false;
         return TC_ERR_DEVICE_TIMEOUT;
     }
     return TC_OK;
@@ -1656,8 +1659,9 @@ tc_status_t validate_moe(const tc_moe_desc *d, const void *X, const void *R, con
     tc_status_t st;
     if ((st = check_q4(w1, &n1)) != TC_OK || (st = check_q4(w2, &n2)) != TC_OK) return st;
     if (n1.v.N != 2LL * d->experts * d->inter || n1.v.K != d->hidden || n2.v.N != (int64_t)d->experts * d->hidden ||
-        n2.v.K != d->inter)
+        n2.v.K != d->inter || n1.v.group != n2.v.group)
         return TC_ERR_DIM;
+    if (n1.v.scale_bf16 != n2.v.scale_bf16) return TC_ERR_DTYPE;
     if ((d->x_dtype != TC_F16 && d->x_dtype != TC_BF16) ||
         (d->router_dtype != d->x_dtype && d->router_dtype != TC_F32) ||
         (d->y_dtype != d->x_dtype && d->y_dtype != TC_F32))
@@ -1710,20 +1714,46 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     MoeArgs a;
     tc_status_t st = validate_moe(d, X, R, w1, w2, Y, ids, weights, &a);
     if (st != TC_OK) return st;
-    // scratch: logits, the choice where the caller does not take it, and h
-    const size_t lb = round_up((size_t)a.T * a.E * 4, 256), kb = round_up((size_t)a.T * a.k * 4, 256);
-    const size_t hb = round_up((size_t)a.T * a.k * (size_t)a.I * 4, 256);
+    // scratch: logits and the two parts of h
+    a.ldh = cdiv(a.I, 8) * 8;
+    const size_t lb = round_up((size_t)a.T * a.E * 4, 256);
+    const size_t hb = (size_t)a.T * a.k * (size_t)a.ldh * 2 * 2;
+    MoeMaps m;
+    const uint32_t gp = 256 / a.w1.group;
+    const struct { const Q4View &w; CUtensorMap &c, &s, &z; } maps[2] = {{a.w1, m.c1, m.s1, m.z1}, {a.w2, m.c2, m.s2, m.z2}};
     std::lock_guard<std::mutex> lk(ctx->mu);
     if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
-    if ((st = ensure_ws(s, lb + 2 * kb + hb)) != TC_OK) return st;
-    uint8_t *ws = static_cast<uint8_t *>(s->ws);
-    a.logits = reinterpret_cast<float *>(ws);
-    if (!a.ids) a.ids = reinterpret_cast<int *>(ws + lb);
-    if (!a.p) a.p = reinterpret_cast<float *>(ws + lb + kb);
-    a.h = reinterpret_cast<float *>(ws + lb + 2 * kb);
-    if (launch_moe(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
-    ctx->launches += moe_launches();
-    ctx->last = "moe_q4";
+    for (const auto &q : maps) {
+        const int64_t groups = cdiv(q.w.K, q.w.group);
+        if (!encode_q4(ctx, &q.c, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w.codes, cdiv(q.w.K, 8) * 4, q.w.N, q.w.ldw / 2, 128, 8,
+                       CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_q4(ctx, &q.s, CU_TENSOR_MAP_DATA_TYPE_UINT16, q.w.scales, q.w.N, groups, q.w.lds * 2, MOE_SCALE_BOX, gp,
+                       CU_TENSOR_MAP_SWIZZLE_NONE))
+            return TC_ERR_CUDA;
+        q.z = q.s;
+        if (q.w.zeros && !encode_q4(ctx, &q.z, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w.zeros, q.w.N, groups, q.w.lds, Q4_ZERO_BOX,
+                                    gp, CU_TENSOR_MAP_SWIZZLE_NONE))
+            return TC_ERR_CUDA;
+    }
+    if ((st = ensure_ws(s, lb + hb)) != TC_OK) return st;
+    if (!s->sync && cudaMallocAsync(reinterpret_cast<void **>(&s->sync), 256, s->st) != cudaSuccess) {
+        s->sync = nullptr;
+        return TC_ERR_CUDA;
+    }
+    if (!s->sync_clear) {
+        if (cudaMemsetAsync(s->sync, 0, 256, s->st) != cudaSuccess) return TC_ERR_CUDA;
+        s->sync_clear = true;
+    }
+    a.logits = static_cast<float *>(s->ws);
+    a.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(s->ws) + lb);
+    a.sync = s->sync;
+    a.status = s->status_dev;
+    a.timeout_ns = 4000000000ull;
+    if (launch_moe(a, m, ctx->num_sms, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += 1;
+    char buf[64];
+    std::snprintf(buf, sizeof buf, "moe_q4_t%d_e%d_k%d_g%d", a.T, a.E, a.k, a.w1.group);
+    ctx->last = buf;
     return TC_OK;
 }
 
@@ -1745,6 +1775,7 @@ void stream_free(tc_stream *s)
     if (s->st) cudaStreamSynchronize(s->st);
     if (s->ws) cudaFree(s->ws);
     if (s->rx) cudaFree(s->rx);
+    if (s->sync) cudaFree(s->sync);
     if (s->status_host) cudaFreeHost(s->status_host);
     if (s->owned && s->st) cudaStreamDestroy(s->st);
     delete s;

@@ -394,20 +394,30 @@ struct Q4MmaPlan {
 };
 cudaError_t launch_q4_mma(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st);
 
-// The mixture-of-experts layer (the public header states the formulas).
+// The mixture-of-experts layer (the public header states the formulas): one
+// cooperative launch of `grid` CTAs (moe.cu).
 struct MoeArgs {
     int T, H, I, E, k;
     int x_bf16, r_dtype, y_dtype, renorm;
     const void *X, *R;
     void *Y;
     long long ldx, ldr, ldy;
-    Q4View w1, w2;
-    float *logits;         // [T, E]
-    int *ids;              // [T, k], the caller's or scratch
-    float *p;              // [T, k], the caller's or scratch
-    float *h;              // [T k, I]
+    Q4View w1, w2;         // the same group and scale type
+    int *ids;              // [T, k] or null
+    float *p;              // [T, k] or null
+    float *logits;         // scratch [T, E]
+    uint16_t *h;           // scratch, bf16: the leading parts [T k, ldh], then the remainders
+    long long ldh;         // I rounded up to 8
+    unsigned *sync;        // two words, 0 before the first launch that uses them; launches leave the first 0
+    unsigned *status;
+    unsigned long long timeout_ns;
 };
-cudaError_t launch_moe(const MoeArgs &a, cudaStream_t st);
-int moe_launches();        // kernels one launch_moe starts
+// boxes: codes {128 bytes, 8 rows} with the 128-byte swizzle, scales
+// {16, 256 / group}, zero points {32, 256 / group}
+constexpr int MOE_SCALE_BOX = 16;
+struct MoeMaps {
+    CUtensorMap c1, s1, z1, c2, s2, z2;
+};
+cudaError_t launch_moe(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_t st);
 
 }  // namespace tc

@@ -133,9 +133,11 @@ __device__ __forceinline__ uint32_t q4_first_word(int g, int t) { return g * 128
 // xf: step j's register q holds X row 8 nt + g, k = 32 j + 8 t + 2 q and + 1.
 // Each group's products are summed from zero by the tensor core -- whole
 // numbers times 16-bit floats, exact, added in fp32 -- and join the
-// accumulator times the row's scale.  Every lane of the warp calls it.
-template <bool BF16, bool SBF16, int NT, int G>
-__device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, const uint32_t (&xf)[NT][8][4])
+// accumulator times the row's scale.  JOIN: the NT operands are the parts of
+// one (x = part 0 + part 1), their sums join acc[0].  SP: elements between
+// two groups' scales.  Every lane of the warp calls it.
+template <bool BF16, bool SBF16, int NT, int G, int SP, bool JOIN = false>
+__device__ __forceinline__ void q4_slab(float (&acc)[JOIN ? 1 : NT][4], const Q4Slab &b, const uint32_t (&xf)[NT][8][4])
 {
     constexpr int STEPS = G / 32;                  // 32-k steps per group
 #pragma unroll
@@ -145,8 +147,8 @@ __device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, co
             z0 = q4_zero_form<BF16>((uint32_t)b.z0[gr * Q4_ZERO_PITCH] & 15u);
             z1 = q4_zero_form<BF16>((uint32_t)b.z1[gr * Q4_ZERO_PITCH] & 15u);
         }
-        const float s0 = q4_scale_bits<SBF16>(b.s0[gr * (Q4_SCALE_PITCH / 2)]);
-        const float s1 = q4_scale_bits<SBF16>(b.s1[gr * (Q4_SCALE_PITCH / 2)]);
+        const float s0 = q4_scale_bits<SBF16>(b.s0[gr * SP]);
+        const float s1 = q4_scale_bits<SBF16>(b.s1[gr * SP]);
         float part[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) part[nt][0] = part[nt][1] = part[nt][2] = part[nt][3] = 0.0f;
@@ -164,14 +166,29 @@ __device__ __forceinline__ void q4_slab(float (&acc)[NT][4], const Q4Slab &b, co
                 q4_mma<BF16>(part[nt], hi, xf[nt][j][2], xf[nt][j][3], part[nt]);
             }
         }
+        if constexpr (JOIN) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 1; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part[0][e] += part[nt][e];
+        }
+#pragma unroll
+        for (int nt = 0; nt < (JOIN ? 1 : NT); ++nt) {
             acc[nt][0] = fmaf(s0, part[nt][0], acc[nt][0]);
             acc[nt][1] = fmaf(s0, part[nt][1], acc[nt][1]);
             acc[nt][2] = fmaf(s1, part[nt][2], acc[nt][2]);
             acc[nt][3] = fmaf(s1, part[nt][3], acc[nt][3]);
         }
     }
+}
+
+// The warps of one group (of `n` warps, several groups to a CTA) meet.
+// Barrier 0 is __syncthreads'; a group of one warp needs none, so at most 8
+// others are in use.
+__device__ __forceinline__ void q4_group_sync(int group, int n)
+{
+    __syncwarp();
+    if (n > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(n * 32) : "memory");
 }
 
 // Bounded waits.  A wait that runs out reports through `status` and raises

@@ -42,11 +42,6 @@ __host__ __device__ constexpr int gv_smem()
 }
 static_assert(gv_smem<1>() <= SMEM_LIMIT && gv_smem<2>() <= SMEM_LIMIT, "one CTA per SM");
 
-__device__ __forceinline__ void bar_sync(int id, int threads)
-{
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 template <bool BF16, bool SBF16, int NT, int G>
 __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     q4_gemv_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
@@ -194,7 +189,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
                 b.s1 = b.s0 + 8;
                 b.z0 = zeros ? st + GV_ZERO_AT + (row & 15) + g : nullptr;
                 b.z1 = b.z0 + 8;
-                q4_slab<BF16, SBF16, NT, G>(acc, b, xf);
+                q4_slab<BF16, SBF16, NT, G, Q4_SCALE_BOX>(acc, b, xf);
                 __syncwarp();                                          // every lane has read the piece
                 if (lane == 0 && ok) fetch();
                 if (++stage == S) stage = 0, parity ^= 1;
@@ -208,7 +203,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
         }
         __syncwarp();
         if (active) {
-            bar_sync(wr, wk_n * 32);
+            q4_group_sync(wr, wk_n);
             // a pair of threads per four rows of one X row: each adds every
             // other warp's tile, in warp order, then the two join
             const int half = lane & 1;
@@ -258,7 +253,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
             __syncwarp();
             cluster_sync();      // the sums are read before they are overwritten, or their CTA ends
         } else if (first + HOLD * wr_n < nblk) {
-            bar_sync(wr, wk_n * 32);      // the tiles are read before the next phase's are written
+            q4_group_sync(wr, wk_n);      // the tiles are read before the next phase's are written
         }
     }
     // after an expired wait: copies still in flight land (within a limit)

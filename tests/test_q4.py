@@ -82,6 +82,7 @@ def moe(T=2, H=96, I=40, E=6, k=2, x="bf16", y=None, w1=None, w2=None, validate=
     ({"E": 40, "k": 17}, tg.TC_ERR_DIM),
     ({"w1": weight(N=481, K=96)}, tg.TC_ERR_DIM), ({"w1": weight(N=480, K=97)}, tg.TC_ERR_DIM),
     ({"w2": weight(N=577, K=40)}, tg.TC_ERR_DIM), ({"w2": weight(N=576, K=41)}, tg.TC_ERR_DIM),
+    ({"w1": weight(N=480, K=96, group=64)}, tg.TC_ERR_DIM), ({"w2": weight(N=576, K=40, scale=tg.TC_BF16)}, tg.TC_ERR_DTYPE),
     ({"w1": weight(N=480, K=96, group=16)}, tg.TC_ERR_DIM), ({"w2": weight(N=576, K=40, ldw=48)}, tg.TC_ERR_LD),
     ({"x": "f32"}, tg.TC_ERR_DTYPE), ({"y": "f16"}, tg.TC_ERR_DTYPE), ({"router_dtype": "f16"}, tg.TC_ERR_DTYPE),
     ({"ldx": 95}, tg.TC_ERR_LD), ({"ld_router": 95}, tg.TC_ERR_LD), ({"ldy": -1}, tg.TC_ERR_LD),
