@@ -1662,6 +1662,8 @@ tc_status_t validate_moe(const tc_moe_desc *d, const void *X, const void *R, con
         n2.v.K != d->inter || n1.v.group != n2.v.group)
         return TC_ERR_DIM;
     if (n1.v.scale_bf16 != n2.v.scale_bf16) return TC_ERR_DTYPE;
+    // the kernel counts (entry, 8 rows of inter) units in 32 bits
+    if ((int64_t)d->tokens * d->top_k * cdiv(d->inter, 8) > INT32_MAX) return TC_ERR_OVERFLOW;
     if ((d->x_dtype != TC_F16 && d->x_dtype != TC_BF16) ||
         (d->router_dtype != d->x_dtype && d->router_dtype != TC_F32) ||
         (d->y_dtype != d->x_dtype && d->y_dtype != TC_F32))

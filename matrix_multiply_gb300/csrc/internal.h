@@ -408,7 +408,7 @@ struct MoeArgs {
     float *logits;         // scratch [T, E]
     uint16_t *h;           // scratch, bf16: the leading parts [T k, ldh], then the remainders
     long long ldh;         // I rounded up to 8
-    unsigned *sync;        // two words, 0 before the first launch that uses them; launches leave the first 0
+    unsigned *sync;        // the grid barrier's word, 0 before the first launch of this grid size that uses it
     unsigned *status;
     unsigned long long timeout_ns;
 };

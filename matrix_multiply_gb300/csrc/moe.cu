@@ -58,166 +58,170 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// All CTAs of the grid (a cooperative launch: all are resident).  sync[0]
-// counts arrivals, the last of which resets it and moves sync[1] on.  The wait
-// is bounded: past the limit the kernel reports and goes on, its outputs
+// All CTAs of the grid (a cooperative launch: all are resident).  One word
+// counts arrivals: what the CTAs add makes 2^31 together, so its top bit
+// flips when the last has arrived, and it needs no reset.  The wait is
+// bounded: past the limit the kernel reports and goes on, its outputs
 // undefined.
-__device__ __forceinline__ void grid_arrive(unsigned *sync, unsigned &gen)
+__device__ __forceinline__ unsigned grid_arrive(unsigned *sync)
 {
+    unsigned old = 0;
     __syncthreads();
     if (threadIdx.x == 0) {
-        gen = *(volatile unsigned *)(sync + 1);
-        __threadfence();
-        if (atomicAdd(sync, 1u) == gridDim.x - 1) {
-            *(volatile unsigned *)sync = 0u;
-            __threadfence();
-            atomicAdd(sync + 1, 1u);
-        }
+        const unsigned add = blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(sync), "r"(add) : "memory");
     }
+    return old;
 }
-__device__ __forceinline__ void grid_wait(unsigned *sync, unsigned gen, unsigned *status, unsigned long long timeout_ns)
+__device__ __forceinline__ void grid_wait(unsigned *sync, unsigned old, unsigned *status, unsigned long long timeout_ns)
 {
     if (threadIdx.x == 0) {
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t n = 1;; ++n) {
             unsigned v;
-            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(sync + 1) : "memory");
-            if (v != gen) break;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(sync) : "memory");
+            if ((v ^ old) & 0x80000000u) break;
             if ((n & 63u) == 0 && globaltimer_ns() - t0 > timeout_ns) {
                 *(volatile unsigned *)status = 0x201u;
                 __threadfence_system();
                 break;
             }
         }
-        __threadfence();
     }
     __syncthreads();
 }
 
-// A float as an unsigned number of the same order, a NaN above all, -0 as 0
+// A float as an unsigned number of the same order, a NaN above all, -0 as 0;
+// and back
 __device__ __forceinline__ uint32_t order_key(float v)
 {
     if (isnan(v)) return 0xffffffffu;
     const uint32_t b = __float_as_uint(v + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-
-// Eight elements of a row from element h, zeros past H
-__device__ __forceinline__ void load8(const void *row, int dtype, int h, int H, bool vec, float (&v)[8])
+__device__ __forceinline__ float key_value(uint32_t k)
 {
-    if (vec && h + 8 <= H) {
-        if (dtype == TC_F32) {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + h);
-            const float4 x = __ldg(q), y = __ldg(q + 1);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-        } else {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + h));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint16_t b = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-                v[i] = dtype == TC_BF16 ? __bfloat162float(__ushort_as_bfloat16(b)) : __half2float(__ushort_as_half(b));
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = h + i < H ? load_c(row, h + i, dtype) : 0.0f;
+    return k == 0xffffffffu ? __uint_as_float(0x7fc00000u) : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
-// Stage 0: the logits of experts blockIdx.x, + gridDim.x, ...
-__device__ void moe_router(const MoeArgs &a, MoeLists &L)
+// the low or high half of a register as fp32
+template <bool BF16>
+__device__ __forceinline__ float half_word(uint32_t w, int high)
+{
+    if constexpr (BF16) return __uint_as_float(high ? w & 0xffff0000u : w << 16);
+    return __half2float(__ushort_as_half((unsigned short)(high ? w >> 16 : w)));
+}
+
+// Stage 0: the logits of (expert, up to TW tokens) tasks blockIdx.x, +
+// gridDim.x, ...; a thread takes eight elements of the rows at a time, all of
+// a step's loads issued before their use.
+template <bool BF16, int TW>
+__device__ __forceinline__ void moe_router(const MoeArgs &a, MoeLists &L)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int xt = a.x_bf16 ? TC_BF16 : TC_F16, rs = a.r_dtype == TC_F32 ? 4 : 2;
+    const bool rf32 = a.r_dtype == TC_F32;
     const bool x_vec = (reinterpret_cast<uintptr_t>(a.X) & 15u) == 0 && a.ldx % 8 == 0;
-    const bool r_vec = (reinterpret_cast<uintptr_t>(a.R) & 15u) == 0 && a.ldr * rs % 16 == 0;
-    for (int e = blockIdx.x; e < a.E; e += gridDim.x) {
-        const uint8_t *r = static_cast<const uint8_t *>(a.R) + (long long)e * a.ldr * rs;
-        for (int t0 = 0; t0 < a.T; t0 += 8) {
-            float acc[8] = {};
-            for (int h = threadIdx.x * 8; h < a.H; h += MO_THREADS * 8) {
-                float rv[8], xv[8];
-                load8(r, a.r_dtype, h, a.H, r_vec, rv);
+    const bool r_vec = (reinterpret_cast<uintptr_t>(a.R) & 15u) == 0 && a.ldr % (rf32 ? 4 : 8) == 0;
+    const int chunks = (a.T + TW - 1) / TW;
+    for (int task = blockIdx.x; task < a.E * chunks; task += gridDim.x) {
+        const int e = task / chunks, t0 = (task - e * chunks) * TW;
+        float acc[TW] = {};
+        for (int h = threadIdx.x * 8; h < a.H; h += MO_THREADS * 8) {
+            uint4 x[TW];
+            float r[8];
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    if (t0 + t >= a.T) break;
-                    load8(static_cast<const uint16_t *>(a.X) + (t0 + t) * a.ldx, xt, h, a.H, x_vec, xv);
+            for (int t = 0; t < TW; ++t)
+                x[t] = q4_load_x(static_cast<const uint16_t *>(a.X) + min(t0 + t, a.T - 1) * a.ldx, h, a.H, x_vec);
+            if (rf32) {
+                const float *row = static_cast<const float *>(a.R) + e * a.ldr + h;
+                if (r_vec && h + 8 <= a.H) {
+                    const float4 u = __ldg(reinterpret_cast<const float4 *>(row)), v = __ldg(reinterpret_cast<const float4 *>(row) + 1);
+                    r[0] = u.x, r[1] = u.y, r[2] = u.z, r[3] = u.w, r[4] = v.x, r[5] = v.y, r[6] = v.z, r[7] = v.w;
+                } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[t] = fmaf(rv[i], xv[i], acc[t]);
+                    for (int i = 0; i < 8; ++i) r[i] = h + i < a.H ? row[i] : 0.0f;
                 }
+            } else {
+                const uint4 v = q4_load_x(static_cast<const uint16_t *>(a.R) + e * a.ldr, h, a.H, r_vec);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = half_word<BF16>(w[i >> 1], i & 1);
             }
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                if (t0 + t >= a.T) break;
-                acc[t] = warp_sum(acc[t]);
-                if (lane == 0) L.red[warp][t] = acc[t];
-            }
-            __syncthreads();
-            if (threadIdx.x < 8 && t0 + (int)threadIdx.x < a.T) {
-                float v = 0.0f;
+            for (int t = 0; t < TW; ++t) {
+                const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
 #pragma unroll
-                for (int w = 0; w < MO_WARPS; ++w) v += L.red[w][threadIdx.x];
-                a.logits[(t0 + threadIdx.x) * a.E + e] = v;
+                for (int i = 0; i < 8; ++i) acc[t] = fmaf(r[i], half_word<BF16>(w[i >> 1], i & 1), acc[t]);
             }
-            __syncthreads();
         }
+        // the warp's sums: halving the tokens a lane holds, then the lanes
+        int tok = 0;
+#pragma unroll
+        for (int n = TW / 2, o = 16; n >= 1; n >>= 1, o >>= 1) {
+            const bool up = lane & o;
+            if (up) tok += n;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float keep = up ? acc[i + n] : acc[i], send = up ? acc[i] : acc[i + n];
+                acc[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        }
+#pragma unroll
+        for (int o = 16 / TW; o > 0; o >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], o);
+        if ((lane & (32 / TW - 1)) == 0) L.red[warp][tok] = acc[0];
+        __syncthreads();
+        if (threadIdx.x < TW && t0 + (int)threadIdx.x < a.T) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < MO_WARPS; ++w) v += L.red[w][threadIdx.x];
+            a.logits[(t0 + threadIdx.x) * a.E + e] = v;
+        }
+        __syncthreads();
     }
 }
 
 // The chosen experts of every token, a warp per token: top_k rounds of a
-// maximum over the logits' keys, the lowest index among equals.
-__device__ void moe_choose(const MoeArgs &a, MoeLists &L)
+// maximum over the logits' keys (NQ per lane), the lowest index among equals.
+template <int NQ>
+__device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeLists &L)
 {
-    constexpr int PER = TC_MOE_MAX_EXPERTS / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int t = warp; t < a.T; t += MO_WARPS) {
-        uint32_t key[PER];
-        float l[PER];
+        uint32_t key[NQ];
+        float l[NQ];
 #pragma unroll
-        for (int q = 0; q < PER; ++q) {
-            key[q] = 0u;
-            l[q] = 0.0f;
-            if (q * 32 >= a.E) continue;
-            if (q * 32 + lane < a.E) {
-                l[q] = __ldcg(a.logits + t * a.E + q * 32 + lane);
-                key[q] = order_key(l[q]);
-            }
-        }
-        float top = 0.0f, chosen = 0.0f, mine = 0.0f, all = 0.0f;
+        for (int q = 0; q < NQ; ++q) l[q] = q * 32 + lane < a.E ? __ldcg(a.logits + t * a.E + q * 32 + lane) : 0.0f;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) key[q] = q * 32 + lane < a.E ? order_key(l[q]) : 0u;
+        uint32_t top = 0u, mine = 0u;
         for (int j = 0; j < a.k; ++j) {
-            uint32_t best = 0u;
-            int at = 0x7fffffff;
+            uint32_t best = key[0];
+            int at = lane;
 #pragma unroll
-            for (int q = 0; q < PER; ++q) {
-                if (q * 32 >= a.E) continue;
+            for (int q = 1; q < NQ; ++q)
                 if (key[q] > best) best = key[q], at = q * 32 + lane;      // the lane's lowest index of its largest
-            }
             const uint32_t m = __reduce_max_sync(0xffffffffu, best);
             const int e = __reduce_min_sync(0xffffffffu, best == m ? at : 0x7fffffff);
-            const float v = m == 0xffffffffu ? __uint_as_float(0x7fc00000u)
-                                             : __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
-            if (j == 0) {
-                top = v;
 #pragma unroll
-                for (int q = 0; q < PER; ++q) {
-                    if (q * 32 >= a.E) continue;
-                    if (q * 32 + lane < a.E) all += expf(l[q] - top);
-                }
-                all = warp_sum(all);
-            }
-#pragma unroll
-            for (int q = 0; q < PER; ++q)
+            for (int q = 0; q < NQ; ++q)
                 if (q * 32 + lane == e) key[q] = 0u;
-            const float x = expf(v - top);
-            chosen += x;
+            if (j == 0) top = m;
             if (lane == j) {
-                mine = x;
+                mine = m;
                 L.id[t * a.k + j] = (uint16_t)e;
                 atomicOr(&L.mask[e], 1u << t);
             }
         }
-        if (lane < a.k) L.p[t * a.k + lane] = mine / (a.renorm ? chosen : all);
+        const float ftop = key_value(top), x = lane < a.k ? expf(key_value(mine) - ftop) : 0.0f;
+        float sum = 0.0f;
+        if (a.renorm) {
+            sum = x;
+        } else {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) sum += q * 32 + lane < a.E ? expf(l[q] - ftop) : 0.0f;
+        }
+        sum = warp_sum(sum);
+        if (lane < a.k) L.p[t * a.k + lane] = x / sum;
     }
 }
 
@@ -286,53 +290,82 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         for (int i = 0; i < S; ++i) mbar_init(my_bar + 8 * i, 1);
         fence_barrier_init();
     }
+    __syncwarp();
     for (int e = threadIdx.x; e < a.E; e += MO_THREADS) L.mask[e] = 0u;
 
-    unsigned gen = 0;
-    moe_router(a, L);
-    grid_arrive(a.sync, gen);
-    grid_wait(a.sync, gen, a.status, a.timeout_ns);
-    moe_choose(a, L);
+    if (a.T <= 2)
+        moe_router<BF16, 2>(a, L);
+    else
+        moe_router<BF16, 8>(a, L);
+    unsigned old = grid_arrive(a.sync);
+
+    // what does not depend on the choice, while the others arrive
+    const int G1 = (int)gridDim.x, nb = (a.I + 7) >> 3;            // units per entry
+    const int ns1 = (a.H + Q4_SLAB - 1) / Q4_SLAB, ns2 = (a.I + Q4_SLAB - 1) / Q4_SLAB;
+    int wk_n = MO_WARPS, wr_n = 1, wr = 0, wk = warp;              // stage 1: warps along hidden, groups along the units
+    if (ns1 < MO_WARPS) {
+        wk_n = ns1;
+        wr_n = (unsigned)MO_WARPS / (unsigned)ns1;
+        wr = (unsigned)warp / (unsigned)ns1;
+        wk = warp - wr * ns1;
+    }
+    const bool active = wr < wr_n;
+    const int per = !active ? 0 : ns1 <= MO_WARPS ? 1 : (ns1 - wk + MO_WARPS - 1) / MO_WARPS;
+    // stage 2: this CTA's rows of hidden, in whole 8s
+    const int rows8 = (int)(((unsigned)(a.H + 7) / 8u + (unsigned)G1 - 1u) / (unsigned)G1);
+    const int r_lo = (int)min((long long)a.H, (long long)blockIdx.x * rows8 * 8);
+    const int r_hi = (int)min((long long)a.H, (long long)r_lo + rows8 * 8);
+    // A piece is up to six copies -- codes, scales, zero points of two 8-row
+    // parts -- issued by lanes 0-5 at once.
+    const int c_what = lane >> 1, c_part = lane & 1;
+    const uint32_t c_dst = c_what == 0 ? c_part * 1024 : c_what == 1 ? MO_SCALE_AT + c_part * 256 : MO_ZERO_AT + c_part * 256;
+    const int c_mask = c_what == 1 ? ~7 : ~15;
+    const CUtensorMap *map1 = c_what == 0 ? &maps.c1 : c_what == 1 ? &maps.s1 : &maps.z1;
+    const CUtensorMap *map2 = c_what == 0 ? &maps.c2 : c_what == 1 ? &maps.s2 : &maps.z2;
+    const bool c_do1 = c_what < (zeros1 ? 3 : 2), c_do2 = c_what < (zeros2 ? 3 : 2);
+
+    grid_wait(a.sync, old, a.status, a.timeout_ns);
+    if (a.E <= 32)
+        moe_choose<1>(a, L);
+    else if (a.E <= 64)
+        moe_choose<2>(a, L);
+    else if (a.E <= 128)
+        moe_choose<4>(a, L);
+    else if (a.E <= 256)
+        moe_choose<8>(a, L);
+    else
+        moe_choose<16>(a, L);
     __syncthreads();
     moe_list(a, L);
     const int entries = L.entries;
 
-    // stage 1: this CTA's units and this warp's share of them
-    const int nb = (a.I + 7) / 8;
-    const long long units = (long long)entries * nb;
-    const long long u0 = blockIdx.x * units / gridDim.x, u1 = (blockIdx.x + 1LL) * units / gridDim.x;
-    const int ns1 = (a.H + Q4_SLAB - 1) / Q4_SLAB, ns2 = (a.I + Q4_SLAB - 1) / Q4_SLAB;
-    const int wk_n = min(ns1, MO_WARPS), wr_n = MO_WARPS / wk_n;
-    const int wr = warp / wk_n, wk = warp - wr * wk_n;
-    const bool active = wr < wr_n;
-    const int per = active ? (ns1 - wk + wk_n - 1) / wk_n : 0;
-    // stage 2: this CTA's rows of hidden, in whole 8s
-    const int rows8 = ((a.H + 7) / 8 + (int)gridDim.x - 1) / (int)gridDim.x;
-    const int r_lo = min((long long)a.H, (long long)blockIdx.x * rows8 * 8), r_hi = min((long long)a.H, (long long)r_lo + rows8 * 8);
-    const int slabs2 = entries * ns2;                   // (entry, slab) pieces, dealt out to the warps
+    // stage 1: an equal share of the units for every CTA
+    const unsigned units = (unsigned)entries * (unsigned)nb, share = units / (unsigned)G1, extra = units - share * G1;
+    const unsigned u0 = blockIdx.x * share + min(blockIdx.x, extra), u1 = u0 + share + (blockIdx.x < extra ? 1u : 0u);
+    const int slabs2 = entries * ns2;                   // stage 2's (entry, slab) pieces, dealt out to the warps
+    const unsigned u_first = active ? u0 + wr : u1;
+    const int ent_first = (int)(u_first / (unsigned)nb), b_first = (int)(u_first - (unsigned)ent_first * nb);
 
-    // lane 0 fetches the warp's pieces: stage 1's, then stage 2's
-    long long f_u = active ? u0 + wr : u1;
-    int f_s = 0, f_ent = (int)(f_u / nb), f_b = (int)(f_u - (long long)f_ent * nb);
-    int f_panel = r_lo, f_i = warp, f_row = r_lo, f_stage = 0, fetched = 0;
-    auto piece = [&](const CUtensorMap *c, const CUtensorMap *s, const CUtensorMap *z, int ra, int rb, int slab) {
-        const uint32_t st = my_ring + f_stage * MO_STAGE_BYTES, bar = my_bar + 8 * f_stage;
-        mbar_arrive_expect_tx(bar, 2 * (1024 + GP * (MOE_SCALE_BOX * 2 + (z ? Q4_ZERO_BOX : 0))));
-        tma_load_2d(st, c, bar, slab * (Q4_SLAB / 2), ra);
-        tma_load_2d(st + 1024, c, bar, slab * (Q4_SLAB / 2), rb);
-        tma_load_2d(st + MO_SCALE_AT, s, bar, ra & ~7, slab * GP);
-        tma_load_2d(st + MO_SCALE_AT + 256, s, bar, rb & ~7, slab * GP);
-        if (z) {
-            tma_load_2d(st + MO_ZERO_AT, z, bar, ra & ~15, slab * GP);
-            tma_load_2d(st + MO_ZERO_AT + 256, z, bar, rb & ~15, slab * GP);
-        }
+    // fetching the warp's pieces: stage 1's, then stage 2's
+    unsigned f_u = u_first;
+    int f_s = 0, f_ent = ent_first, f_b = b_first, f_panel = r_lo, f_i = warp, f_row = r_lo, f_stage = 0, fetched = 0;
+    auto piece = [&](const CUtensorMap *map, bool on, uint32_t bytes, int ra, int rb, int slab) {
+        const uint32_t bar = my_bar + 8 * f_stage;
+        const int row = c_part ? rb : ra;
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        if (on)
+            tma_load_2d(my_ring + f_stage * MO_STAGE_BYTES + c_dst, map, bar, c_what == 0 ? slab * (Q4_SLAB / 2) : row & c_mask,
+                        c_what == 0 ? row : slab * GP);
+        __syncwarp();
         ++fetched;
         if (++f_stage == S) f_stage = 0;
     };
-    auto fetch = [&]() {
+    constexpr uint32_t CS_BYTES = 2 * (1024 + GP * MOE_SCALE_BOX * 2), Z_BYTES = 2 * GP * Q4_ZERO_BOX;
+    auto fetch = [&]() {                                // the whole warp
         if (f_u < u1) {
             const int ra = L.ent_e[f_ent] * 2 * a.I + f_b * 8;
-            piece(&maps.c1, &maps.s1, zeros1 ? &maps.z1 : nullptr, ra, ra + a.I, wk + f_s * wk_n);
+            piece(map1, c_do1, CS_BYTES + (zeros1 ? Z_BYTES : 0u), ra, ra + a.I, wk + f_s * MO_WARPS);
             if (++f_s == per) {
                 f_s = 0;
                 f_u += wr_n;
@@ -340,8 +373,8 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                 while (f_b >= nb) f_b -= nb, ++f_ent;
             }
         } else if (f_panel < r_hi && f_i < slabs2) {
-            const int ent = f_i / ns2, ra = L.ent_e[ent] * a.H + f_row;
-            piece(&maps.c2, &maps.s2, zeros2 ? &maps.z2 : nullptr, ra, ra + 8, f_i - ent * ns2);
+            const int ent = ns2 == 1 ? f_i : (int)((unsigned)f_i / (unsigned)ns2), ra = L.ent_e[ent] * a.H + f_row;
+            piece(map2, c_do2, CS_BYTES + (zeros2 ? Z_BYTES : 0u), ra, ra + 8, f_i - ent * ns2);
             f_row += 16;
             if (f_row >= min(r_hi, f_panel + MO_PANEL)) {
                 f_row = f_panel;
@@ -354,9 +387,8 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
             }
         }
     };
-    if (lane == 0)
-        for (int i = 0; i < S; ++i) fetch();
-    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < S; ++i) fetch();
 
     const Q4Watch watch{nullptr, a.status, a.timeout_ns};
     const uint32_t word = q4_first_word(g, t);
@@ -377,8 +409,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     };
     auto release = [&]() {
         __syncwarp();
-        if (lane == 0 && ok) fetch();
-        __syncwarp();
+        if (__all_sync(0xffffffffu, ok)) fetch();
         if (++stage == S) stage = 0, parity ^= 1;
     };
 
@@ -388,24 +419,33 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         const bool x_vec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (a.ldx & 7) == 0;
         uint32_t xf[1][8][4];
         int have_ent = -1, have_slab = -1;
-        int ent = active ? (int)((u0 + wr) / nb) : 0, b8 = active ? (int)((u0 + wr) - (long long)ent * nb) : 0;
-        for (long long first = u0 + wr; active && first < u1; first += MO_HOLD * wr_n) {
+        int ent = ent_first, b8 = b_first;
+        for (unsigned first = u_first; first < u1; first += MO_HOLD * wr_n) {
             int held = 0;
-            for (long long u = first; u < u1 && held < MO_HOLD; u += wr_n, ++held) {
+            for (unsigned u = first; u < u1 && held < MO_HOLD; u += wr_n, ++held) {
                 float acc[1][4] = {};
                 const int ra = L.ent_e[ent] * 2 * a.I + b8 * 8;
                 for (int s = 0; s < per; ++s) {
-                    const int slab = wk + s * wk_n;
+                    const int slab = wk + s * MO_WARPS;
                     if (ent != have_ent || slab != have_slab) {
                         have_ent = ent, have_slab = slab;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) xf[0][j][0] = xf[0][j][1] = xf[0][j][2] = xf[0][j][3] = 0u;
                         if (g < L.ent_n[ent]) {
                             const uint16_t *row = X + (L.pair[L.ent_at[ent] + g] / a.k) * a.ldx;
+                            const int k = slab * Q4_SLAB + 8 * t;
+                            if (x_vec && slab < a.H / Q4_SLAB) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint4 v = q4_load_x(row, slab * Q4_SLAB + 32 * j + 8 * t, a.H, x_vec);
-                                xf[0][j][0] = v.x, xf[0][j][1] = v.y, xf[0][j][2] = v.z, xf[0][j][3] = v.w;
+                                for (int j = 0; j < 8; ++j) {
+                                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + k) + 4 * j);
+                                    xf[0][j][0] = v.x, xf[0][j][1] = v.y, xf[0][j][2] = v.z, xf[0][j][3] = v.w;
+                                }
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    const uint4 v = q4_load_x(row, k + 32 * j, a.H, x_vec);
+                                    xf[0][j][0] = v.x, xf[0][j][1] = v.y, xf[0][j][2] = v.z, xf[0][j][3] = v.w;
+                                }
                             }
                         }
                     }
@@ -426,8 +466,8 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
             const int half = lane & 1;
             for (int e = (wk * 32 + lane) >> 1; e < MO_HOLD * 16; e += wk_n * 16) {
                 const int hu = e >> 4, c = (e >> 1) & 7, r = (e & 1) * 4;
-                const long long u = first + (long long)hu * wr_n;
-                const int ue = hu < held ? (int)(u / nb) : 0;
+                const unsigned u = first + (unsigned)(hu * wr_n);
+                const int ue = hu < held ? (int)(u / (unsigned)nb) : 0;
                 const bool in = hu < held && c < L.ent_n[ue];
                 const float *p = space + (hu * MO_WARPS + warp - wk) * MO_TILE + c * MO_TILE_LD + r;
                 float v[8] = {};
@@ -442,7 +482,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1);
                 if (!in) continue;
-                const int i0 = (int)(u - (long long)ue * nb) * 8 + r + 2 * half;
+                const int i0 = (int)(u - (unsigned)ue * nb) * 8 + r + 2 * half;
                 uint16_t *h = a.h + L.pair[L.ent_at[ue] + c] * a.ldh + i0;
                 uint16_t hi[2], lo[2];
 #pragma unroll
@@ -463,17 +503,17 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
             q4_group_sync(wr, wk_n);          // the tiles are read before the next ones are written
         }
     }
-    grid_arrive(a.sync, gen);
+    old = grid_arrive(a.sync);
     // this warp's sums start at zero while the others arrive
     float *sums = space + warp * a.T * MO_PANEL;
     for (int i = lane; i < a.T * MO_PANEL; i += 32) sums[i] = 0.0f;
-    grid_wait(a.sync, gen, a.status, a.timeout_ns);
+    grid_wait(a.sync, old, a.status, a.timeout_ns);
 
     // ------------------------------------------------ stage 2: down
     for (int panel = r_lo; panel < r_hi; panel += MO_PANEL) {
         const int p_hi = min(r_hi, panel + MO_PANEL);
         for (int i = warp; i < slabs2; i += MO_WARPS) {
-            const int ent = i / ns2, slab = i - ent * ns2, n = L.ent_n[ent], at = L.ent_at[ent];
+            const int ent = (int)((unsigned)i / (unsigned)ns2), slab = i - ent * ns2, n = L.ent_n[ent], at = L.ent_at[ent];
             uint32_t xf[2][8][4];
             {
                 const uint16_t *row = a.h + (long long)(g < n ? L.pair[at + g] : 0) * a.ldh;
