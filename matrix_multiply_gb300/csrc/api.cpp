@@ -1517,15 +1517,18 @@ tc_status_t validate_q4w(const tc_gemm_desc *d, const tc_q4_weight *q, const voi
     return TC_OK;
 }
 
-// A 2-D tensor map of one part of a 4-bit weight.
+// A tensor map of one part of a 4-bit weight: 2-D, or with `deep` > 0 3-D,
+// `deep` such matrices deep_pitch bytes apart.
 bool encode_q4(tc_ctx *ctx, CUtensorMap *m, CUtensorMapDataType t, const void *base, int64_t inner, int64_t outer,
-               int64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle)
+               int64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle, int64_t deep = 0,
+               int64_t deep_pitch = 0, uint32_t box_deep = 0)
 {
-    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
-    cuuint64_t strides[1] = {(cuuint64_t)pitch_bytes};
-    cuuint32_t box[2] = {box_inner, box_outer}, estr[2] = {1, 1};
-    return ctx->encode(m, t, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)deep};
+    cuuint64_t strides[2] = {(cuuint64_t)pitch_bytes, (cuuint64_t)deep_pitch};
+    cuuint32_t box[3] = {box_inner, box_outer, box_deep}, estr[3] = {1, 1, 1};
+    return ctx->encode(m, t, deep > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The streaming kernel's grid and tensor maps.  One cluster of ksplit CTAs
@@ -1722,21 +1725,25 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     const size_t hb = (size_t)a.T * a.k * (size_t)a.ldh * 2 * 2;
     MoeMaps m;
     const uint32_t gp = 256 / a.w1.group;
-    const struct { const Q4View &w; CUtensorMap &c, &s, &z; } maps[2] = {{a.w1, m.c1, m.s1, m.z1}, {a.w2, m.c2, m.s2, m.z2}};
     std::lock_guard<std::mutex> lk(ctx->mu);
     if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
-    for (const auto &q : maps) {
-        const int64_t groups = cdiv(q.w.K, q.w.group);
-        if (!encode_q4(ctx, &q.c, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w.codes, cdiv(q.w.K, 8) * 4, q.w.N, q.w.ldw / 2, 128, 8,
-                       CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !encode_q4(ctx, &q.s, CU_TENSOR_MAP_DATA_TYPE_UINT16, q.w.scales, q.w.N, groups, q.w.lds * 2, MOE_SCALE_BOX, gp,
-                       CU_TENSOR_MAP_SWIZZLE_NONE))
-            return TC_ERR_CUDA;
-        q.z = q.s;
-        if (q.w.zeros && !encode_q4(ctx, &q.z, CU_TENSOR_MAP_DATA_TYPE_UINT8, q.w.zeros, q.w.N, groups, q.w.lds, Q4_ZERO_BOX,
-                                    gp, CU_TENSOR_MAP_SWIZZLE_NONE))
-            return TC_ERR_CUDA;
-    }
+    const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, u16 = CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, plain = CU_TENSOR_MAP_SWIZZLE_NONE;
+    const int64_t g1 = cdiv(a.H, a.w1.group), g2 = cdiv(a.I, a.w2.group), p1 = a.w1.ldw / 2, halves = 2LL * a.E;
+    m.s1_3d = a.I % 8 == 0;
+    m.z1_3d = a.I % 16 == 0;
+    bool enc = encode_q4(ctx, &m.c1, u8, a.w1.codes, cdiv(a.H, 8) * 4, a.I, p1, 128, 8, sw, halves, a.I * p1, 2) &&
+               encode_q4(ctx, &m.c2, u8, a.w2.codes, cdiv(a.I, 8) * 4, a.w2.N, a.w2.ldw / 2, 128, 16, sw) &&
+               encode_q4(ctx, &m.s2, u16, a.w2.scales, a.w2.N, g2, a.w2.lds * 2, Q4_SCALE_BOX, gp, plain);
+    enc = enc && (m.s1_3d ? encode_q4(ctx, &m.s1, u16, a.w1.scales, a.I, g1, a.w1.lds * 2, MOE_SCALE_BOX, gp, plain, halves,
+                                      a.I * 2LL, 2)
+                          : encode_q4(ctx, &m.s1, u16, a.w1.scales, a.w1.N, g1, a.w1.lds * 2, MOE_SCALE_BOX, gp, plain));
+    m.z1 = m.z2 = m.s2;
+    if (a.w1.zeros)
+        enc = enc && (m.z1_3d ? encode_q4(ctx, &m.z1, u8, a.w1.zeros, a.I, g1, a.w1.lds, Q4_ZERO_BOX, gp, plain, halves, a.I, 2)
+                              : encode_q4(ctx, &m.z1, u8, a.w1.zeros, a.w1.N, g1, a.w1.lds, Q4_ZERO_BOX, gp, plain));
+    if (a.w2.zeros) enc = enc && encode_q4(ctx, &m.z2, u8, a.w2.zeros, a.w2.N, g2, a.w2.lds, Q4_ZERO_BOX, gp, plain);
+    if (!enc) return TC_ERR_CUDA;
     if ((st = ensure_ws(s, lb + hb)) != TC_OK) return st;
     if (!s->sync && cudaMallocAsync(reinterpret_cast<void **>(&s->sync), 256, s->st) != cudaSuccess) {
         s->sync = nullptr;

@@ -412,11 +412,16 @@ struct MoeArgs {
     unsigned *status;
     unsigned long long timeout_ns;
 };
-// boxes: codes {128 bytes, 8 rows} with the 128-byte swizzle, scales
-// {16, 256 / group}, zero points {32, 256 / group}
+// gate_up is seen as [2 experts][inter rows][..]: one copy brings 8 rows of
+// gate and the same 8 of up.  Boxes: codes {128 bytes, 8 rows, 2} with the
+// 128-byte swizzle, scales {16, 256 / group, 2} where rows of inter are 16-byte
+// multiples (s1_3d; else {16, 256 / group}, two copies), zero points {32, ..}
+// likewise.  down: codes {128 bytes, 16 rows}, scales {24, 256 / group}, zero
+// points {32, 256 / group}.
 constexpr int MOE_SCALE_BOX = 16;
 struct MoeMaps {
     CUtensorMap c1, s1, z1, c2, s2, z2;
+    int s1_3d, z1_3d;
 };
 cudaError_t launch_moe(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_t st);
 

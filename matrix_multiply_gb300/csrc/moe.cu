@@ -25,7 +25,7 @@ namespace {
 
 constexpr int MO_WARPS = 16, MO_THREADS = MO_WARPS * 32;
 constexpr int MO_STAGES = 3;
-constexpr int MO_SCALE_AT = 2048, MO_ZERO_AT = 2560;     // codes 2 x 8 rows; scales, zero points 2 x 256 bytes
+constexpr int MO_SCALE_AT = 2048, MO_ZERO_AT = 2560;     // codes of 16 rows, scales, zero points
 constexpr int MO_STAGE_BYTES = 3072;
 constexpr int MO_RING = MO_WARPS * MO_STAGES * MO_STAGE_BYTES;
 constexpr int MO_TILE_LD = 20, MO_TILE = 8 * MO_TILE_LD; // floats: a unit's partial tile, 8 tokens x 16 rows
@@ -315,14 +315,8 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     const int rows8 = (int)(((unsigned)(a.H + 7) / 8u + (unsigned)G1 - 1u) / (unsigned)G1);
     const int r_lo = (int)min((long long)a.H, (long long)blockIdx.x * rows8 * 8);
     const int r_hi = (int)min((long long)a.H, (long long)r_lo + rows8 * 8);
-    // A piece is up to six copies -- codes, scales, zero points of two 8-row
-    // parts -- issued by lanes 0-5 at once.
-    const int c_what = lane >> 1, c_part = lane & 1;
-    const uint32_t c_dst = c_what == 0 ? c_part * 1024 : c_what == 1 ? MO_SCALE_AT + c_part * 256 : MO_ZERO_AT + c_part * 256;
-    const int c_mask = c_what == 1 ? ~7 : ~15;
-    const CUtensorMap *map1 = c_what == 0 ? &maps.c1 : c_what == 1 ? &maps.s1 : &maps.z1;
-    const CUtensorMap *map2 = c_what == 0 ? &maps.c2 : c_what == 1 ? &maps.s2 : &maps.z2;
-    const bool c_do1 = c_what < (zeros1 ? 3 : 2), c_do2 = c_what < (zeros2 ? 3 : 2);
+    // bytes between the two 8-row parts' scales and zero points in stage 1
+    const int s_part = maps.s1_3d ? GP * MOE_SCALE_BOX * 2 : 256, z_part = maps.z1_3d ? GP * Q4_ZERO_BOX : 256;
 
     grid_wait(a.sync, old, a.status, a.timeout_ns);
     if (a.E <= 32)
@@ -349,23 +343,31 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     // fetching the warp's pieces: stage 1's, then stage 2's
     unsigned f_u = u_first;
     int f_s = 0, f_ent = ent_first, f_b = b_first, f_panel = r_lo, f_i = warp, f_row = r_lo, f_stage = 0, fetched = 0;
-    auto piece = [&](const CUtensorMap *map, bool on, uint32_t bytes, int ra, int rb, int slab) {
-        const uint32_t bar = my_bar + 8 * f_stage;
-        const int row = c_part ? rb : ra;
-        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-        __syncwarp();
-        if (on)
-            tma_load_2d(my_ring + f_stage * MO_STAGE_BYTES + c_dst, map, bar, c_what == 0 ? slab * (Q4_SLAB / 2) : row & c_mask,
-                        c_what == 0 ? row : slab * GP);
-        __syncwarp();
-        ++fetched;
-        if (++f_stage == S) f_stage = 0;
-    };
-    constexpr uint32_t CS_BYTES = 2 * (1024 + GP * MOE_SCALE_BOX * 2), Z_BYTES = 2 * GP * Q4_ZERO_BOX;
-    auto fetch = [&]() {                                // the whole warp
+    constexpr uint32_t CS1 = 2048 + 2 * GP * MOE_SCALE_BOX * 2, Z1 = 2 * GP * Q4_ZERO_BOX;
+    constexpr uint32_t CS2 = 2048 + GP * Q4_SCALE_BOX * 2, Z2 = GP * Q4_ZERO_BOX;
+    auto fetch = [&]() {                                // the whole warp; lane 0 issues the copies
+        const uint32_t st = my_ring + f_stage * MO_STAGE_BYTES, bar = my_bar + 8 * f_stage;
         if (f_u < u1) {
-            const int ra = L.ent_e[f_ent] * 2 * a.I + f_b * 8;
-            piece(map1, c_do1, CS_BYTES + (zeros1 ? Z_BYTES : 0u), ra, ra + a.I, wk + f_s * MO_WARPS);
+            const int half = L.ent_e[f_ent] * 2, slab = wk + f_s * MO_WARPS, x = f_b * 8;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, CS1 + (zeros1 ? Z1 : 0u));
+                tma_load_3d(st, &maps.c1, bar, slab * (Q4_SLAB / 2), x, half);
+                const int ra = half * a.I + x, rb = ra + a.I;
+                if (maps.s1_3d) {
+                    tma_load_3d(st + MO_SCALE_AT, &maps.s1, bar, x, slab * GP, half);
+                } else {
+                    tma_load_2d(st + MO_SCALE_AT, &maps.s1, bar, ra & ~7, slab * GP);
+                    tma_load_2d(st + MO_SCALE_AT + 256, &maps.s1, bar, rb & ~7, slab * GP);
+                }
+                if (zeros1) {
+                    if (maps.z1_3d) {
+                        tma_load_3d(st + MO_ZERO_AT, &maps.z1, bar, x & ~15, slab * GP, half);
+                    } else {
+                        tma_load_2d(st + MO_ZERO_AT, &maps.z1, bar, ra & ~15, slab * GP);
+                        tma_load_2d(st + MO_ZERO_AT + 256, &maps.z1, bar, rb & ~15, slab * GP);
+                    }
+                }
+            }
             if (++f_s == per) {
                 f_s = 0;
                 f_u += wr_n;
@@ -373,8 +375,14 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                 while (f_b >= nb) f_b -= nb, ++f_ent;
             }
         } else if (f_panel < r_hi && f_i < slabs2) {
-            const int ent = ns2 == 1 ? f_i : (int)((unsigned)f_i / (unsigned)ns2), ra = L.ent_e[ent] * a.H + f_row;
-            piece(map2, c_do2, CS_BYTES + (zeros2 ? Z_BYTES : 0u), ra, ra + 8, f_i - ent * ns2);
+            const int ent = ns2 == 1 ? f_i : (int)((unsigned)f_i / (unsigned)ns2), slab = f_i - ent * ns2;
+            const int row = L.ent_e[ent] * a.H + f_row;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, CS2 + (zeros2 ? Z2 : 0u));
+                tma_load_2d(st, &maps.c2, bar, slab * (Q4_SLAB / 2), row);
+                tma_load_2d(st + MO_SCALE_AT, &maps.s2, bar, row & ~7, slab * GP);
+                if (zeros2) tma_load_2d(st + MO_ZERO_AT, &maps.z2, bar, row & ~15, slab * GP);
+            }
             f_row += 16;
             if (f_row >= min(r_hi, f_panel + MO_PANEL)) {
                 f_row = f_panel;
@@ -385,7 +393,11 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                     f_row = f_panel;
                 }
             }
+        } else {
+            return;
         }
+        ++fetched;
+        if (++f_stage == S) f_stage = 0;
     };
 #pragma unroll 1
     for (int i = 0; i < S; ++i) fetch();
@@ -394,18 +406,10 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     const uint32_t word = q4_first_word(g, t);
     int stage = 0, parity = 0;
     bool ok = true;
-    auto arrive = [&](int ra, int rb, bool zeros) {      // the next piece, when it is there
+    auto arrive = [&]() {                                // the next piece, when it is there
         ok = ok && q4_wait(my_bar + 8 * stage, parity, watch);
         __syncwarp();
-        const uint8_t *st = ring + (warp * S + stage) * MO_STAGE_BYTES;
-        Q4Slab b;
-        b.base = st;
-        b.codes = word;
-        b.s0 = reinterpret_cast<const uint16_t *>(st + MO_SCALE_AT) + (ra & 7) + g;
-        b.s1 = reinterpret_cast<const uint16_t *>(st + MO_SCALE_AT + 256) + (rb & 7) + g;
-        b.z0 = zeros ? st + MO_ZERO_AT + (ra & 15) + g : nullptr;
-        b.z1 = st + MO_ZERO_AT + 256 + (rb & 15) + g;
-        return b;
+        return ring + (warp * S + stage) * MO_STAGE_BYTES;
     };
     auto release = [&]() {
         __syncwarp();
@@ -424,7 +428,10 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
             int held = 0;
             for (unsigned u = first; u < u1 && held < MO_HOLD; u += wr_n, ++held) {
                 float acc[1][4] = {};
-                const int ra = L.ent_e[ent] * 2 * a.I + b8 * 8;
+                const int ra = L.ent_e[ent] * 2 * a.I + b8 * 8, rb = ra + a.I;
+                // where the parts' first rows lie in their copies
+                const int sa = maps.s1_3d ? 0 : ra & 7, sb = maps.s1_3d ? 0 : rb & 7;
+                const int za = maps.z1_3d ? b8 * 8 & 15 : ra & 15, zb = maps.z1_3d ? b8 * 8 & 15 : rb & 15;
                 for (int s = 0; s < per; ++s) {
                     const int slab = wk + s * MO_WARPS;
                     if (ent != have_ent || slab != have_slab) {
@@ -449,7 +456,14 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                             }
                         }
                     }
-                    const Q4Slab b = arrive(ra, ra + a.I, zeros1);
+                    const uint8_t *st = arrive();
+                    Q4Slab b;
+                    b.base = st;
+                    b.codes = word;
+                    b.s0 = reinterpret_cast<const uint16_t *>(st + MO_SCALE_AT) + sa + g;
+                    b.s1 = reinterpret_cast<const uint16_t *>(st + MO_SCALE_AT + s_part) + sb + g;
+                    b.z0 = zeros1 ? st + MO_ZERO_AT + za + g : nullptr;
+                    b.z1 = st + MO_ZERO_AT + z_part + zb + g;
                     q4_slab<BF16, SBF16, 1, G, MOE_SCALE_BOX>(acc, b, xf);
                     release();
                 }
@@ -540,8 +554,15 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
             for (int row = panel; row < p_hi; row += 16) {
                 float acc[1][4] = {};
                 const int ra = L.ent_e[ent] * a.H + row;
-                const Q4Slab b = arrive(ra, ra + 8, zeros2);
-                q4_slab<true, SBF16, 2, G, MOE_SCALE_BOX, true>(acc, b, xf);
+                const uint8_t *st = arrive();
+                Q4Slab b;
+                b.base = st;
+                b.codes = word;
+                b.s0 = reinterpret_cast<const uint16_t *>(st + MO_SCALE_AT) + (ra & 7) + g;
+                b.s1 = b.s0 + 8;
+                b.z0 = zeros2 ? st + MO_ZERO_AT + (ra & 15) + g : nullptr;
+                b.z1 = b.z0 + 8;
+                q4_slab<true, SBF16, 2, G, Q4_SCALE_BOX, true>(acc, b, xf);
                 release();
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
