@@ -30,8 +30,7 @@ namespace {
 __host__ __device__ constexpr int qm_conv(int bn) { return bn > 64 ? 4 : 8; }
 __host__ __device__ constexpr int qm_prom(int bn) { return bn > 64 ? 8 : 4; }
 constexpr int QM_THREADS = (4 + 8 + 2) * 32;
-constexpr int QM_XS = 8, QM_CS = 4;             // ring stages: X (64 k), codes (256 k)
-constexpr int QM_AS = 4;                        // TMEM stages of the converted operand (64 k, 32 columns)
+constexpr int QM_XS = 8, QM_CS = 4;             // ring stages: X and the converted operand (64 k), codes (256 k)
 constexpr int QM_CODE_BYTES = Q4_MMA_ROWS * 128;
 constexpr int QM_PART_LD = Q4_MMA_ROWS + 4;     // floats between columns of a slice's partial tile
 
@@ -108,24 +107,23 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     constexpr int HB = BN / (QM_PROM / 4);         // columns of one promoting warp
     constexpr uint32_t TMEM_COLS = 512;
     constexpr uint32_t A_COL = 2 * BN;             // the converted operand's stages follow the accumulators
-    static_assert(2 * BN + QM_AS * 32 <= 512 && BN % 32 == 0, "TMEM columns");
+    static_assert(2 * BN + QM_XS * 32 <= 512 && BN % 32 == 0, "TMEM columns");
     constexpr uint32_t IDESC = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((uint32_t)(BN >> 3) << 17) |
                                ((uint32_t)(Q4_MMA_ROWS >> 4) << 24);
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint8_t *codes = smem + QM_XS * X_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(codes + QM_CS * QM_CODE_BYTES);
-    const uint32_t xfull = smem_u32(bars), xempty = xfull + 8 * QM_XS, cfull = xempty + 8 * QM_XS,
-                   cempty = cfull + 8 * QM_CS, afull = cempty + 8 * QM_CS, aempty = afull + 8 * QM_AS,
-                   dfull = aempty + 8 * QM_AS, dempty = dfull + 16, drain = dempty + 16;
-    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 2 * QM_XS + 2 * QM_CS + 2 * QM_AS + 5);
+    // full: X's copy and the four converting warps of a 64-k block; empty: its MMAs
+    const uint32_t full = smem_u32(bars), empty = full + 8 * QM_XS, cfull = empty + 8 * QM_XS, cempty = cfull + 8 * QM_CS,
+                   dfull = cempty + 8 * QM_CS, dempty = dfull + 16, drain = dempty + 16;
+    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 2 * QM_XS + 2 * QM_CS + 5);
     volatile uint32_t *abort_flag = slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < QM_XS; ++i) mbar_init(xfull + 8 * i, 1), mbar_init(xempty + 8 * i, 1);
+        for (int i = 0; i < QM_XS; ++i) mbar_init(full + 8 * i, 5), mbar_init(empty + 8 * i, 1);
         for (int i = 0; i < QM_CS; ++i) mbar_init(cfull + 8 * i, 1), mbar_init(cempty + 8 * i, QM_CONV);
-        for (int i = 0; i < QM_AS; ++i) mbar_init(afull + 8 * i, 4), mbar_init(aempty + 8 * i, 1);
         for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, QM_PROM);
         mbar_init(drain, 1);
         *abort_flag = 0u;
@@ -163,14 +161,17 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                         ++ci;
                     }
                     const int st = xi % QM_XS;
-                    if (!(ok = q4_wait(xempty + 8 * st, ((xi / QM_XS) & 1) ^ 1, watch))) break;
-                    mbar_arrive_expect_tx(xfull + 8 * st, X_BYTES);
-                    tma_load_2d(smem_u32(smem) + st * X_BYTES, &tmX, xfull + 8 * st, kb * 64, w.m0);
+                    if (!(ok = q4_wait(empty + 8 * st, ((xi / QM_XS) & 1) ^ 1, watch))) break;
+                    mbar_arrive_expect_tx(full + 8 * st, X_BYTES);
+                    tma_load_2d(smem_u32(smem) + st * X_BYTES, &tmX, full + 8 * st, kb * 64, w.m0);
                     ++xi;
                 }
             }
-            if (!ok) {       // let the copies already issued land before shared memory is released
-                for (int i = max(0, xi - QM_XS); i < xi; ++i) q4_drain(xfull + 8 * (i % QM_XS), (i / QM_XS) & 1);
+            // after an expired wait: the copies already issued land before shared
+            // memory is released.  X's barriers may still lack the converters, so
+            // the wait is for its limit.
+            if (!ok) {
+                for (int i = max(0, xi - QM_XS); i < xi; ++i) q4_drain(full + 8 * (i % QM_XS), (i / QM_XS) & 1);
                 for (int i = max(0, ci - QM_CS); i < ci; ++i) q4_drain(cfull + 8 * (i % QM_CS), (i / QM_CS) & 1);
             }
         }
@@ -178,31 +179,40 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     } else if (warp == QM_CONV + QM_PROM + 1) {
         // ------------------------------------------------------ MMA issuer
         if (lane == 0) {
-            int it = 0, gi = 0;                                 // 64-k blocks and groups so far
+            // The thread's own latency per block paces the tensor core: each
+            // barrier is looked at once ahead of time, so that a wait that is
+            // already over costs nothing.
+            uint32_t st = 0, ph = 0, db = 0, dph = 1;           // ring stage, accumulator, and their phases
+            bool ready = false, dready = true;
             const uint64_t bd0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
             for (int u = blockIdx.x; ok && u < units; u += step) {
                 const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
-                for (int kb = w.kb0; ok && kb < w.kb1; ++kb, ++it) {
-                    const int xs = it % QM_XS, as = it % QM_AS;
-                    if (!(ok = q4_wait(xfull + 8 * xs, (it / QM_XS) & 1, watch))) break;
-                    if (!(ok = q4_wait(afull + 8 * as, (it / QM_AS) & 1, watch))) break;
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!ready && !(ok = q4_wait(full + 8 * st, ph, watch))) break;
                     tc_fence_after();
+                    const uint32_t nst = (st + 1) % QM_XS, nph = st + 1 == QM_XS ? ph ^ 1u : ph;
+                    ready = mbar_test_wait(full + 8 * nst, nph);
+                    const uint64_t bd = bd0 + (uint64_t)(st * (X_BYTES >> 4));
+                    const uint32_t at = tmem + A_COL + st * 32;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const bool first = ((kb * 4 + k) % (G / 16)) == 0;
+                        const bool first = G == 128 ? k == 0 && (kb & 1) == 0 : (k * 16) % G == 0;
                         if (first) {
-                            if (!(ok = q4_wait(dempty + 8 * (gi & 1), ((gi >> 1) & 1) ^ 1, watch))) break;
+                            if (!dready && !(ok = q4_wait(dempty + 8 * db, dph, watch))) break;
                             tc_fence_after();
                         }
-                        mma_f16_ts(tmem + (gi & 1) * BN, tmem + A_COL + as * 32 + k * 8,
-                                   bd0 + (uint64_t)(xs * (X_BYTES >> 4) + k * 2), IDESC, first ? 0u : 1u);
-                        if ((kb * 4 + k + 1) % (G / 16) == 0 || (k == 3 && kb + 1 == w.kb1)) {
-                            mma_commit(dfull + 8 * (gi & 1));
-                            ++gi;
+                        mma_f16_ts(tmem + db * BN, at + k * 8, bd + k * 2, IDESC, first ? 0u : 1u);
+                        if (G == 128 ? k == 3 && ((kb & 1) == 1 || kb + 1 == w.kb1) : (k * 16 + 16) % G == 0) {
+                            mma_commit(dfull + 8 * db);
+                            db ^= 1u;
+                            if (db == 0) dph ^= 1u;
+                            dready = mbar_test_wait(dempty + 8 * db, dph);
                         }
                     }
-                    mma_commit(xempty + 8 * xs);
-                    mma_commit(aempty + 8 * as);
+                    if (!ok) break;
+                    mma_commit(empty + 8 * st);
+                    st = nst;
+                    ph = nph;
                 }
             }
             if (!ok) {
@@ -221,13 +231,15 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
             const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
             const bool in = a.q.zeros && w.n0 + row < a.q.N;
             const uint8_t *zp = in ? a.q.zeros + w.n0 + row : a.q.zeros;
-            // a row's zero points of a 256-k block, loaded one block ahead
-            uint32_t z[GP], zn[GP];
+            // a row's zero points of a 256-k block, loaded one block ahead (and
+            // used only then: a use next to its load would wait for it)
+            uint8_t z[GP], zn[GP];
             auto load_z = [&](int kb) {
 #pragma unroll
                 for (int i = 0; i < GP; ++i) {
                     const long long gr = (long long)kb * 64 / G + i;
-                    zn[i] = (in && gr < ngroups) ? zp[gr * a.q.lds] & 15u : 8u;
+                    zn[i] = 8;
+                    if (in && gr < ngroups) zn[i] = zp[gr * a.q.lds];
                 }
             };
             load_z(w.kb0);
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                     if (kb + i >= w.kb1 || !ok) break;
                     const int at = it++;
                     if (QM_CONV == 8 && (at & 1) != half) continue;
-                    const int as = at % QM_AS;
+                    const int as = at % QM_XS;
                     uint32_t words[8];
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
@@ -254,20 +266,20 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                     uint32_t out[32];
 #pragma unroll
                     for (int v = 0; v < 8; ++v) {
-                        const Q4Zero zf = q4_zero_form<BF16>(z[(i * 64 + v * 8) / G]);
+                        const Q4Zero zf = q4_zero_form<BF16>((uint32_t)z[(i * 64 + v * 8) / G] & 15u);
                         uint32_t p[4];
                         q4_widen<BF16>(words[v], zf, p);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) out[4 * v + j] = p[j];
                     }
-                    ok = __all_sync(0xffffffffu, q4_wait(aempty + 8 * as, ((at / QM_AS) & 1) ^ 1, watch));
+                    ok = __all_sync(0xffffffffu, q4_wait(empty + 8 * as, ((at / QM_XS) & 1) ^ 1, watch));
                     if (!ok) break;
                     tc_fence_after();
                     tmem_st_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + A_COL + as * 32, out);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(afull + 8 * as);
+                    if (lane == 0) mbar_arrive(full + 8 * as);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(cempty + 8 * cs);
@@ -287,28 +299,41 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
             for (int i = 0; i < HB / 2; ++i) acc[i] = 0ull;
             const int g0 = (int)((long long)w.kb0 * 64 / G);
             const int gn = G == 32 ? 2 * (w.kb1 - w.kb0) : (w.kb1 - w.kb0 + G / 64 - 1) / (G / 64);
-            auto scale = [&](int i) { return (n < a.q.N && g0 + i < ngroups && i < gn) ? q4_scale(a.q, g0 + i, n) : 0.0f; };
-            float s0 = scale(0), s1 = scale(1), s2 = scale(2);
+            // scales as they are stored, loaded AHEAD groups before their use
+            constexpr int AHEAD = 4;
+            const uint16_t *sp = static_cast<const uint16_t *>(a.q.scales) + g0 * a.q.lds + (n < a.q.N ? n : 0);
+            const int sn = n < a.q.N ? (int)min((long long)gn, ngroups - g0) : 0;
+            uint16_t sq[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                sq[i] = 0;
+                if (i < sn) sq[i] = sp[i * a.q.lds];
+            }
             for (int i = 0; i < gn; ++i, ++gi) {
-                const float s = s0;
-                s0 = s1, s1 = s2, s2 = scale(i + 3);       // loaded three groups ahead
+                const float s = a.q.scale_bf16 ? q4_scale_bits<true>(sq[0]) : q4_scale_bits<false>(sq[0]);
+#pragma unroll
+                for (int j = 0; j + 1 < AHEAD; ++j) sq[j] = sq[j + 1];
+                sq[AHEAD - 1] = 0;
+                if (i + AHEAD < sn) sq[AHEAD - 1] = sp[(i + AHEAD) * a.q.lds];
                 ok = __all_sync(0xffffffffu, q4_wait(dfull + 8 * (gi & 1), (gi >> 1) & 1, watch));
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ss = pack64(__float_as_uint(s), __float_as_uint(s));
+                uint32_t r[2][16];
+                tmem_ld_x16(taddr + (gi & 1) * BN, r[0]);
 #pragma unroll
                 for (int c = 0; c < HB; c += 16) {
-                    uint32_t r[16];
-                    tmem_ld_x16(taddr + (gi & 1) * BN + c, r);
                     tmem_ld_wait();
-                    if (c + 16 == HB) {
+                    if (c + 16 < HB) {
+                        tmem_ld_x16(taddr + (gi & 1) * BN + c + 16, r[(c / 16 + 1) & 1]);
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(dempty + 8 * (gi & 1));
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        acc[c / 2 + j] = fma2(ss, pack64(r[2 * j], r[2 * j + 1]), acc[c / 2 + j]);
+                        acc[c / 2 + j] = fma2(ss, pack64(r[(c / 16) & 1][2 * j], r[(c / 16) & 1][2 * j + 1]), acc[c / 2 + j]);
                 }
             }
             if (!ok) break;
