@@ -46,15 +46,36 @@ static_assert(qm_smem(128) <= SMEM_LIMIT, "one CTA per SM");
 static_assert(32 * QM_PART_LD * 4 <= QM_XS * 32 * 128 && 128 * QM_PART_LD * 4 <= QM_XS * 128 * 128,
               "a partial tile fits in the idle X ring");
 
-// D[tmem] (+)= A[tmem] B[smem]
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+// D[tmem] (+)= A[tmem] B[smem], issued by the lane whose `leader` is set.
+// The whole warp runs the issuing loop, so that its addresses and
+// descriptors stay in uniform registers; one lane's loop, a divergent region,
+// moved every operand there for each MMA and took longer than the MMAs.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                                           uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
+}
+__device__ __forceinline__ void mma_commit_by(uint32_t bar, uint32_t leader)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+// 1 in one lane of the (converged) warp
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
 
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
@@ -79,6 +100,24 @@ __device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi)
     uint64_t d;
     asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
     return d;
+}
+
+// alpha * sum + beta * C_old of one row of W: C[off + c ldc], c < cols; the
+// lanes of a warp hold neighbouring rows
+template <int DT, int HB>
+__device__ __forceinline__ void store_columns(const Q4GemmArgs &a, long long off, int cols, const uint64_t (&acc)[HB / 2])
+{
+    const bool whole = cols >= HB && a.beta == 0.0f;
+#pragma unroll
+    for (int c = 0; c < HB; ++c) {
+        float v = a.alpha * __uint_as_float(c & 1 ? (uint32_t)(acc[c / 2] >> 32) : (uint32_t)acc[c / 2]);
+        if (!whole) {
+            if (c >= cols) break;
+            if (a.beta != 0.0f) v = fmaf(a.beta, load_c(a.C, off, DT), v);
+        }
+        store_c1(a.C, off, v, DT);
+        off += a.ldc;
+    }
 }
 
 struct QmUnit {
@@ -178,101 +217,109 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
         __syncwarp();
     } else if (warp == QM_CONV + QM_PROM + 1) {
         // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            // The thread's own latency per block paces the tensor core: each
-            // barrier is looked at once ahead of time, so that a wait that is
-            // already over costs nothing.
-            uint32_t st = 0, ph = 0, db = 0, dph = 1;           // ring stage, accumulator, and their phases
-            bool ready = false, dready = true;
-            const uint64_t bd0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
-            for (int u = blockIdx.x; ok && u < units; u += step) {
-                const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
-                for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!ready && !(ok = q4_wait(full + 8 * st, ph, watch))) break;
+        // The warp's own latency per block paces the tensor core: each barrier
+        // is looked at once ahead of time, so that a wait that is already over
+        // costs nothing.
+        const uint32_t leader = elect_one();
+        uint32_t st = 0, ph = 0, db = 0, dph = 1;               // ring stage, accumulator, and their phases
+        bool ready = false, dready = true;
+        const uint64_t bd0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+        auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, q4_wait(bar, parity, watch)); };
+        for (int u = blockIdx.x; ok && u < units; u += step) {
+            const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+#pragma unroll 1
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (!ready && !(ok = wait(full + 8 * st, ph))) break;
+                const uint32_t nst = (st + 1) % QM_XS, nph = st + 1 == QM_XS ? ph ^ 1u : ph;
+                const uint64_t bd = bd0 + (uint64_t)(st * (X_BYTES >> 4));
+                const uint32_t at = tmem + A_COL + st * 32;
+                // a group's first step and last step in this block
+                const bool head = G < 128 || (kb & 1) == 0, tail = G < 128 || (kb & 1) == 1 || kb + 1 == w.kb1;
+                if (head && !dready && !(ok = wait(dempty + 8 * db, dph))) break;
+                tc_fence_after();
+                mma_f16_ts(tmem + db * BN, at, bd, IDESC, head ? 0u : 1u, leader);
+                mma_f16_ts(tmem + db * BN, at + 8, bd + 2, IDESC, 1u, leader);
+                if constexpr (G == 32) {
+                    mma_commit_by(dfull + 8 * db, leader);
+                    db ^= 1u;
+                    dph ^= db ^ 1u;
+                    if (!(ok = wait(dempty + 8 * db, dph))) break;
                     tc_fence_after();
-                    const uint32_t nst = (st + 1) % QM_XS, nph = st + 1 == QM_XS ? ph ^ 1u : ph;
-                    ready = mbar_test_wait(full + 8 * nst, nph);
-                    const uint64_t bd = bd0 + (uint64_t)(st * (X_BYTES >> 4));
-                    const uint32_t at = tmem + A_COL + st * 32;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const bool first = G == 128 ? k == 0 && (kb & 1) == 0 : (k * 16) % G == 0;
-                        if (first) {
-                            if (!dready && !(ok = q4_wait(dempty + 8 * db, dph, watch))) break;
-                            tc_fence_after();
-                        }
-                        mma_f16_ts(tmem + db * BN, at + k * 8, bd + k * 2, IDESC, first ? 0u : 1u);
-                        if (G == 128 ? k == 3 && ((kb & 1) == 1 || kb + 1 == w.kb1) : (k * 16 + 16) % G == 0) {
-                            mma_commit(dfull + 8 * db);
-                            db ^= 1u;
-                            if (db == 0) dph ^= 1u;
-                            dready = mbar_test_wait(dempty + 8 * db, dph);
-                        }
-                    }
-                    if (!ok) break;
-                    mma_commit(empty + 8 * st);
-                    st = nst;
-                    ph = nph;
                 }
+                mma_f16_ts(tmem + db * BN, at + 16, bd + 4, IDESC, G == 32 ? 0u : 1u, leader);
+                mma_f16_ts(tmem + db * BN, at + 24, bd + 6, IDESC, 1u, leader);
+                mma_commit_by(empty + 8 * st, leader);
+                if (tail) {
+                    mma_commit_by(dfull + 8 * db, leader);
+                    db ^= 1u;
+                    dph ^= db ^ 1u;
+                }
+                ready = __all_sync(0xffffffffu, mbar_test_wait(full + 8 * nst, nph));
+                if (tail) dready = __all_sync(0xffffffffu, mbar_test_wait(dempty + 8 * db, dph));
+                st = nst;
+                ph = nph;
             }
-            if (!ok) {
-                mma_commit(drain);
-                q4_drain(drain, 0);
-            }
+        }
+        if (!ok) {
+            mma_commit_by(drain, leader);
+            if (leader) q4_drain(drain, 0);
         }
         __syncwarp();
     } else if (warp < QM_CONV) {
         // ------------------------------------------------------ converters
         const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-        constexpr int GP = Q4_SLAB / G;
+        constexpr int ZN = G == 32 ? 2 : 1;                      // zero points of a row in a 64-k block
         const long long ngroups = (a.q.K + G - 1) / G;
         int it = 0, ci = 0;
         for (int u = blockIdx.x; ok && u < units; u += step) {
             const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
             const bool in = a.q.zeros && w.n0 + row < a.q.N;
             const uint8_t *zp = in ? a.q.zeros + w.n0 + row : a.q.zeros;
-            // a row's zero points of a 256-k block, loaded one block ahead (and
-            // used only then: a use next to its load would wait for it)
-            uint8_t z[GP], zn[GP];
-            auto load_z = [&](int kb) {
+            // loaded three blocks ahead, and used only then: a use next to its
+            // load would wait for it
+            uint8_t z[3][ZN];
+            auto load_z = [&](uint8_t (&d)[ZN], int kb) {
 #pragma unroll
-                for (int i = 0; i < GP; ++i) {
+                for (int i = 0; i < ZN; ++i) {
                     const long long gr = (long long)kb * 64 / G + i;
-                    zn[i] = 8;
-                    if (in && gr < ngroups) zn[i] = zp[gr * a.q.lds];
+                    d[i] = 8;
+                    if (in && gr < ngroups) d[i] = zp[gr * a.q.lds];
                 }
             };
-            load_z(w.kb0);
-            for (int kb = w.kb0; ok && kb < w.kb1; kb += 4, ++ci) {
 #pragma unroll
-                for (int i = 0; i < GP; ++i) z[i] = zn[i];
-                if (kb + 4 < w.kb1) load_z(kb + 4);
+            for (int i = 0; i < 3; ++i) load_z(z[i], w.kb0 + i);
+#pragma unroll 1
+            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int cs = ci % QM_CS;
-                ok = __all_sync(0xffffffffu, q4_wait(cfull + 8 * cs, (ci / QM_CS) & 1, watch));
-                if (!ok) break;
-                const uint8_t *src = codes + cs * QM_CODE_BYTES + row * 128;
+                if ((kb & 3) == 0) {
+                    ok = __all_sync(0xffffffffu, q4_wait(cfull + 8 * cs, (ci / QM_CS) & 1, watch));
+                    if (!ok) break;
+                }
+                uint32_t zz[ZN];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (kb + i >= w.kb1 || !ok) break;
-                    const int at = it++;
-                    if (QM_CONV == 8 && (at & 1) != half) continue;
-                    const int as = at % QM_XS;
-                    uint32_t words[8];
+                for (int i = 0; i < ZN; ++i) zz[i] = z[0][i] & 15u, z[0][i] = z[1][i], z[1][i] = z[2][i];
+                load_z(z[2], kb + 3);
+                if (QM_CONV == 4 || (it & 1) == half) {
+                    const uint8_t *src = codes + cs * QM_CODE_BYTES + row * 128;
+                    const int as = it % QM_XS;
+                    uint32_t words[8], out[32];
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (((2 * i + v) ^ (row & 7)) << 4));
+                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (((2 * (kb & 3) + v) ^ (row & 7)) << 4));
                         words[4 * v] = x.x, words[4 * v + 1] = x.y, words[4 * v + 2] = x.z, words[4 * v + 3] = x.w;
                     }
-                    uint32_t out[32];
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                        const Q4Zero zf = q4_zero_form<BF16>((uint32_t)z[(i * 64 + v * 8) / G] & 15u);
-                        uint32_t p[4];
-                        q4_widen<BF16>(words[v], zf, p);
+                    for (int i = 0; i < ZN; ++i) {
+                        const Q4Zero zf = q4_zero_form<BF16>(zz[i]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) out[4 * v + j] = p[j];
+                        for (int v = i * 8 / ZN; v < (i + 1) * 8 / ZN; ++v) {
+                            uint32_t p[4];
+                            q4_widen<BF16>(words[v], zf, p);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) out[4 * v + j] = p[j];
+                        }
                     }
-                    ok = __all_sync(0xffffffffu, q4_wait(empty + 8 * as, ((at / QM_XS) & 1) ^ 1, watch));
+                    ok = __all_sync(0xffffffffu, q4_wait(empty + 8 * as, ((it / QM_XS) & 1) ^ 1, watch));
                     if (!ok) break;
                     tc_fence_after();
                     tmem_st_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + A_COL + as * 32, out);
@@ -281,8 +328,11 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(full + 8 * as);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(cempty + 8 * cs);
+                if ((kb & 3) == 3 || kb + 1 == w.kb1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(cempty + 8 * cs);
+                    ++ci;
+                }
             }
         }
     } else {
@@ -347,13 +397,10 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
             } else if (n < a.q.N) {
                 const int cols = min(HB, a.M - w.m0 - half * HB);
                 const long long off = (long long)(w.m0 + half * HB) * a.ldc + n;
-#pragma unroll
-                for (int c = 0; c < HB; ++c)
-                    if (c < cols) {
-                        float v = a.alpha * __uint_as_float(c & 1 ? (uint32_t)(acc[c / 2] >> 32) : (uint32_t)acc[c / 2]);
-                        if (a.beta != 0.0f) v = fmaf(a.beta, load_c(a.C, off + c * a.ldc, a.c_dtype), v);
-                        store_c1(a.C, off + c * a.ldc, v, a.c_dtype);
-                    }
+                if (a.c_dtype == TC_F32)
+                    store_columns<TC_F32, HB>(a, off, cols, acc);
+                else
+                    store_columns<BF16 ? TC_BF16 : TC_F16, HB>(a, off, cols, acc);
             }
         }
     }
