@@ -1565,7 +1565,7 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
 // and about 150 to convert; a tile has a fixed part besides.
 void plan_q4_mma(int num_sms, const Q4GemmArgs &a, const Force &f, Q4MmaPlan *p)
 {
-    const int64_t kbs = cdiv(a.q.K, 64), tn = cdiv(a.q.N, Q4_MMA_ROWS);
+    const int64_t kbs = 2 * cdiv(a.q.K, 128), tn = cdiv(a.q.N, Q4_MMA_ROWS);
     double best = 0.0;
     p->bn = 0;
     for (int bn : {128, 96, 64, 32}) {

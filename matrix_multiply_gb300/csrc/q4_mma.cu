@@ -30,7 +30,8 @@ namespace {
 __host__ __device__ constexpr int qm_conv(int bn) { return bn > 64 ? 4 : 8; }
 __host__ __device__ constexpr int qm_prom(int bn) { return bn > 64 ? 8 : 4; }
 constexpr int QM_THREADS = (4 + 8 + 2) * 32;
-constexpr int QM_XS = 8, QM_CS = 4;             // ring stages: X and the converted operand (64 k), codes (256 k)
+constexpr int QM_BK = 128;                      // k of a block: the unit of every hand-over
+constexpr int QM_XS = 4, QM_CS = 4;             // ring stages: X and the converted operand (a block), codes (two)
 constexpr int QM_CODE_BYTES = Q4_MMA_ROWS * 128;
 constexpr int QM_PART_LD = Q4_MMA_ROWS + 4;     // floats between columns of a slice's partial tile
 
@@ -39,11 +40,11 @@ constexpr int QM_PART_LD = Q4_MMA_ROWS + 4;     // floats between columns of a s
 // for ever)
 __host__ __device__ constexpr int qm_smem(int bn)
 {
-    const int need = 1024 + QM_XS * bn * 128 + QM_CS * QM_CODE_BYTES + 512;
+    const int need = 1024 + QM_XS * bn * 256 + QM_CS * QM_CODE_BYTES + 512;
     return need > 120 * 1024 ? need : 120 * 1024;
 }
 static_assert(qm_smem(128) <= SMEM_LIMIT, "one CTA per SM");
-static_assert(32 * QM_PART_LD * 4 <= QM_XS * 32 * 128 && 128 * QM_PART_LD * 4 <= QM_XS * 128 * 128,
+static_assert(32 * QM_PART_LD * 4 <= QM_XS * 32 * 256 && 128 * QM_PART_LD * 4 <= QM_XS * 128 * 256,
               "a partial tile fits in the idle X ring");
 
 // D[tmem] (+)= A[tmem] B[smem], issued by the lane whose `leader` is set.
@@ -129,10 +130,10 @@ __device__ __forceinline__ QmUnit qm_unit(int u, int split, int tiles_m, int bn,
     QmUnit w;
     w.n0 = (tile / tiles_m) * Q4_MMA_ROWS;
     w.m0 = (tile % tiles_m) * bn;
-    // slices of whole 256-k blocks: no group is cut
-    const int nb = (num_kb + 3) / 4;
-    w.kb0 = split > 1 ? (int)((long long)s * nb / split) * 4 : 0;
-    w.kb1 = split > 1 ? min(num_kb, (int)((long long)(s + 1) * nb / split) * 4) : num_kb;
+    // slices of whole pairs of blocks, as the codes are copied
+    const int nb = (num_kb + 1) / 2;
+    w.kb0 = split > 1 ? (int)((long long)s * nb / split) * 2 : 0;
+    w.kb1 = split > 1 ? min(num_kb, (int)((long long)(s + 1) * nb / split) * 2) : num_kb;
     return w;
 }
 
@@ -141,19 +142,20 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     q4_mma_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
                   int split, int tiles_m, int units, unsigned *status, unsigned long long timeout_ns)
 {
-    constexpr int X_BYTES = BN * 128;
+    constexpr int X_BYTES = BN * 256;              // a block of X: two halves of BN rows x 128 bytes
+    constexpr int NG = QM_BK / G;                  // groups per block
     constexpr int QM_CONV = qm_conv(BN), QM_PROM = qm_prom(BN);
     constexpr int HB = BN / (QM_PROM / 4);         // columns of one promoting warp
     constexpr uint32_t TMEM_COLS = 512;
     constexpr uint32_t A_COL = 2 * BN;             // the converted operand's stages follow the accumulators
-    static_assert(2 * BN + QM_XS * 32 <= 512 && BN % 32 == 0, "TMEM columns");
+    static_assert(2 * BN + QM_XS * 64 <= 512 && BN % 32 == 0, "TMEM columns");
     constexpr uint32_t IDESC = (1u << 4) | ((BF16 ? 1u : 0u) << 7) | ((BF16 ? 1u : 0u) << 10) | ((uint32_t)(BN >> 3) << 17) |
                                ((uint32_t)(Q4_MMA_ROWS >> 4) << 24);
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint8_t *codes = smem + QM_XS * X_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(codes + QM_CS * QM_CODE_BYTES);
-    // full: X's copy and the four converting warps of a 64-k block; empty: its MMAs
+    // full: X's copies and the four converting warps of a block; empty: its MMAs
     const uint32_t full = smem_u32(bars), empty = full + 8 * QM_XS, cfull = empty + 8 * QM_XS, cempty = cfull + 8 * QM_CS,
                    dfull = cempty + 8 * QM_CS, dempty = dfull + 16, drain = dempty + 16;
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 2 * QM_XS + 2 * QM_CS + 5);
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     griddep_wait();
 
     const Q4Watch watch{abort_flag, status, timeout_ns};
-    const int num_kb = (int)((a.q.K + 63) / 64);
+    const int num_kb = (int)((a.q.K + QM_BK - 1) / QM_BK);
     const int step = split > 1 ? units : (int)gridDim.x;       // a cluster's CTAs take one unit each
     bool ok = true;
 
@@ -192,17 +194,18 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
             for (int u = blockIdx.x; ok && u < units; u += step) {
                 const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    if ((kb & 3) == 0) {
+                    if ((kb & 1) == 0) {
                         const int st = ci % QM_CS;
                         if (!(ok = q4_wait(cempty + 8 * st, ((ci / QM_CS) & 1) ^ 1, watch))) break;
                         mbar_arrive_expect_tx(cfull + 8 * st, QM_CODE_BYTES);
-                        tma_load_2d(smem_u32(codes) + st * QM_CODE_BYTES, &tmC, cfull + 8 * st, kb * 32, w.n0);
+                        tma_load_2d(smem_u32(codes) + st * QM_CODE_BYTES, &tmC, cfull + 8 * st, kb * (QM_BK / 2), w.n0);
                         ++ci;
                     }
                     const int st = xi % QM_XS;
                     if (!(ok = q4_wait(empty + 8 * st, ((xi / QM_XS) & 1) ^ 1, watch))) break;
                     mbar_arrive_expect_tx(full + 8 * st, X_BYTES);
-                    tma_load_2d(smem_u32(smem) + st * X_BYTES, &tmX, full + 8 * st, kb * 64, w.m0);
+                    tma_load_2d(smem_u32(smem) + st * X_BYTES, &tmX, full + 8 * st, kb * QM_BK, w.m0);
+                    tma_load_2d(smem_u32(smem) + st * X_BYTES + X_BYTES / 2, &tmX, full + 8 * st, kb * QM_BK + 64, w.m0);
                     ++xi;
                 }
             }
@@ -232,30 +235,23 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                 if (!ready && !(ok = wait(full + 8 * st, ph))) break;
                 const uint32_t nst = (st + 1) % QM_XS, nph = st + 1 == QM_XS ? ph ^ 1u : ph;
                 const uint64_t bd = bd0 + (uint64_t)(st * (X_BYTES >> 4));
-                const uint32_t at = tmem + A_COL + st * 32;
-                // a group's first step and last step in this block
-                const bool head = G < 128 || (kb & 1) == 0, tail = G < 128 || (kb & 1) == 1 || kb + 1 == w.kb1;
-                if (head && !dready && !(ok = wait(dempty + 8 * db, dph))) break;
-                tc_fence_after();
-                mma_f16_ts(tmem + db * BN, at, bd, IDESC, head ? 0u : 1u, leader);
-                mma_f16_ts(tmem + db * BN, at + 8, bd + 2, IDESC, 1u, leader);
-                if constexpr (G == 32) {
-                    mma_commit_by(dfull + 8 * db, leader);
-                    db ^= 1u;
-                    dph ^= db ^ 1u;
-                    if (!(ok = wait(dempty + 8 * db, dph))) break;
+                const uint32_t at = tmem + A_COL + st * 64;
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    if (!dready && !(ok = wait(dempty + 8 * db, dph))) break;
                     tc_fence_after();
-                }
-                mma_f16_ts(tmem + db * BN, at + 16, bd + 4, IDESC, G == 32 ? 0u : 1u, leader);
-                mma_f16_ts(tmem + db * BN, at + 24, bd + 6, IDESC, 1u, leader);
-                mma_commit_by(empty + 8 * st, leader);
-                if (tail) {
+#pragma unroll
+                    for (int k = i * (G / 16); k < (i + 1) * (G / 16); ++k)
+                        mma_f16_ts(tmem + db * BN, at + k * 8, bd + (uint64_t)((k >> 2) * (X_BYTES >> 5) + (k & 3) * 2), IDESC,
+                                   k > i * (G / 16) ? 1u : 0u, leader);
+                    if (i == NG - 1) mma_commit_by(empty + 8 * st, leader);
                     mma_commit_by(dfull + 8 * db, leader);
                     db ^= 1u;
                     dph ^= db ^ 1u;
+                    dready = __all_sync(0xffffffffu, mbar_test_wait(dempty + 8 * db, dph));
                 }
+                if (!ok) break;
                 ready = __all_sync(0xffffffffu, mbar_test_wait(full + 8 * nst, nph));
-                if (tail) dready = __all_sync(0xffffffffu, mbar_test_wait(dempty + 8 * db, dph));
                 st = nst;
                 ph = nph;
             }
@@ -268,73 +264,85 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     } else if (warp < QM_CONV) {
         // ------------------------------------------------------ converters
         const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-        constexpr int ZN = G == 32 ? 2 : 1;                      // zero points of a row in a 64-k block
         const long long ngroups = (a.q.K + G - 1) / G;
         int it = 0, ci = 0;
+        uint32_t pending = 0;                                    // the barrier of the block whose stores are under way
+        auto hand_over = [&]() {
+            if (!pending) return;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pending);
+            pending = 0;
+        };
         for (int u = blockIdx.x; ok && u < units; u += step) {
             const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
             const bool in = a.q.zeros && w.n0 + row < a.q.N;
             const uint8_t *zp = in ? a.q.zeros + w.n0 + row : a.q.zeros;
-            // loaded three blocks ahead, and used only then: a use next to its
-            // load would wait for it
-            uint8_t z[3][ZN];
-            auto load_z = [&](uint8_t (&d)[ZN], int kb) {
+            // a row's zero points of a block, loaded two blocks ahead, and used
+            // only then: a use next to its load would wait for it
+            uint8_t z[2][NG];
+            auto load_z = [&](uint8_t (&d)[NG], int kb) {
 #pragma unroll
-                for (int i = 0; i < ZN; ++i) {
-                    const long long gr = (long long)kb * 64 / G + i;
+                for (int i = 0; i < NG; ++i) {
+                    const long long gr = (long long)kb * NG + i;
                     d[i] = 8;
                     if (in && gr < ngroups) d[i] = zp[gr * a.q.lds];
                 }
             };
-#pragma unroll
-            for (int i = 0; i < 3; ++i) load_z(z[i], w.kb0 + i);
+            load_z(z[0], w.kb0);
+            load_z(z[1], w.kb0 + 1);
 #pragma unroll 1
             for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                 const int cs = ci % QM_CS;
-                if ((kb & 3) == 0) {
+                if ((kb & 1) == 0) {
                     ok = __all_sync(0xffffffffu, q4_wait(cfull + 8 * cs, (ci / QM_CS) & 1, watch));
                     if (!ok) break;
                 }
-                uint32_t zz[ZN];
+                uint32_t zz[NG];
 #pragma unroll
-                for (int i = 0; i < ZN; ++i) zz[i] = z[0][i] & 15u, z[0][i] = z[1][i], z[1][i] = z[2][i];
-                load_z(z[2], kb + 3);
+                for (int i = 0; i < NG; ++i) zz[i] = z[0][i] & 15u, z[0][i] = z[1][i];
+                load_z(z[1], kb + 2);
                 if (QM_CONV == 4 || (it & 1) == half) {
                     const uint8_t *src = codes + cs * QM_CODE_BYTES + row * 128;
                     const int as = it % QM_XS;
-                    uint32_t words[8], out[32];
 #pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(src + (((2 * (kb & 3) + v) ^ (row & 7)) << 4));
-                        words[4 * v] = x.x, words[4 * v + 1] = x.y, words[4 * v + 2] = x.z, words[4 * v + 3] = x.w;
-                    }
+                    for (int h = 0; h < 2; ++h) {                // two halves of 64 k
+                        uint32_t words[8], out[32];
 #pragma unroll
-                    for (int i = 0; i < ZN; ++i) {
-                        const Q4Zero zf = q4_zero_form<BF16>(zz[i]);
+                        for (int v = 0; v < 2; ++v) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(
+                                src + (((4 * (kb & 1) + 2 * h + v) ^ (row & 7)) << 4));
+                            words[4 * v] = x.x, words[4 * v + 1] = x.y, words[4 * v + 2] = x.z, words[4 * v + 3] = x.w;
+                        }
 #pragma unroll
-                        for (int v = i * 8 / ZN; v < (i + 1) * 8 / ZN; ++v) {
+                        for (int v = 0; v < 8; ++v) {
                             uint32_t p[4];
-                            q4_widen<BF16>(words[v], zf, p);
+                            q4_widen<BF16>(words[v], q4_zero_form<BF16>(zz[(h * 64 + v * 8) / G]), p);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) out[4 * v + j] = p[j];
                         }
+                        if (h == 0) {
+                            // the block before is handed over now: its stores have
+                            // had this block's first half to complete
+                            hand_over();
+                            ok = __all_sync(0xffffffffu, q4_wait(empty + 8 * as, ((it / QM_XS) & 1) ^ 1, watch));
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        tmem_st_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + A_COL + as * 64 + h * 32, out);
                     }
-                    ok = __all_sync(0xffffffffu, q4_wait(empty + 8 * as, ((it / QM_XS) & 1) ^ 1, watch));
                     if (!ok) break;
-                    tc_fence_after();
-                    tmem_st_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + A_COL + as * 32, out);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full + 8 * as);
+                    pending = full + 8 * as;
                 }
-                if ((kb & 3) == 3 || kb + 1 == w.kb1) {
+                if ((kb & 1) == 1 || kb + 1 == w.kb1) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(cempty + 8 * cs);
                     ++ci;
                 }
             }
         }
+        hand_over();
     } else {
         // ------------------------------------------------------ promoting warps
         const int pw = warp - QM_CONV, quarter = pw & 3, half = pw >> 2, row = quarter * 32 + lane;
@@ -347,8 +355,7 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
             uint64_t acc[HB / 2];
 #pragma unroll
             for (int i = 0; i < HB / 2; ++i) acc[i] = 0ull;
-            const int g0 = (int)((long long)w.kb0 * 64 / G);
-            const int gn = G == 32 ? 2 * (w.kb1 - w.kb0) : (w.kb1 - w.kb0 + G / 64 - 1) / (G / 64);
+            const int g0 = w.kb0 * NG, gn = (w.kb1 - w.kb0) * NG;
             // scales as they are stored, loaded AHEAD groups before their use
             constexpr int AHEAD = 4;
             const uint16_t *sp = static_cast<const uint16_t *>(a.q.scales) + g0 * a.q.lds + (n < a.q.N ? n : 0);
@@ -369,21 +376,28 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ss = pack64(__float_as_uint(s), __float_as_uint(s));
-                uint32_t r[2][16];
-                tmem_ld_x16(taddr + (gi & 1) * BN, r[0]);
+                // 32 columns to a load: a wait is for all loads before it
 #pragma unroll
-                for (int c = 0; c < HB; c += 16) {
-                    tmem_ld_wait();
-                    if (c + 16 < HB) {
-                        tmem_ld_x16(taddr + (gi & 1) * BN + c + 16, r[(c / 16 + 1) & 1]);
+                for (int c = 0; c < HB; c += 32) {
+                    constexpr int W = 32;
+                    uint32_t r[W];
+                    if (c + 32 <= HB) {
+                        tmem_ld_32x32b_x32(taddr + (gi & 1) * BN + c, r);
                     } else {
+                        uint32_t q[16];
+                        tmem_ld_x16(taddr + (gi & 1) * BN + c, q);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) r[j] = q[j];
+                    }
+                    tmem_ld_wait();
+                    if (c + 32 >= HB) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(dempty + 8 * (gi & 1));
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        acc[c / 2 + j] = fma2(ss, pack64(r[(c / 16) & 1][2 * j], r[(c / 16) & 1][2 * j + 1]), acc[c / 2 + j]);
+                    for (int j = 0; j < (c + 32 <= HB ? 16 : 8); ++j)
+                        acc[c / 2 + j] = fma2(ss, pack64(r[2 * j], r[2 * j + 1]), acc[c / 2 + j]);
                 }
             }
             if (!ok) break;
