@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
         const int pw = warp - QM_CONV, quarter = pw & 3, half = pw >> 2, row = quarter * 32 + lane;
         const long long ngroups = (a.q.K + G - 1) / G;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * HB;
-        int gi = 0;
+        uint32_t db = 0, dph = 0;                                // accumulator and its phase
         for (int u = blockIdx.x; ok && u < units; u += step) {
             const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
             const long long n = w.n0 + row;
@@ -356,48 +356,50 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < HB / 2; ++i) acc[i] = 0ull;
             const int g0 = w.kb0 * NG, gn = (w.kb1 - w.kb0) * NG;
-            // scales as they are stored, loaded AHEAD groups before their use
-            constexpr int AHEAD = 4;
+            // scales as they are stored, loaded two groups before their use into
+            // registers that nothing touches in between (a move would wait)
             const uint16_t *sp = static_cast<const uint16_t *>(a.q.scales) + g0 * a.q.lds + (n < a.q.N ? n : 0);
             const int sn = n < a.q.N ? (int)min((long long)gn, ngroups - g0) : 0;
-            uint16_t sq[AHEAD];
+            uint16_t sq[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < AHEAD; ++i) {
-                sq[i] = 0;
+            for (int i = 0; i < 2; ++i)
                 if (i < sn) sq[i] = sp[i * a.q.lds];
-            }
-            for (int i = 0; i < gn; ++i, ++gi) {
-                const float s = a.q.scale_bf16 ? q4_scale_bits<true>(sq[0]) : q4_scale_bits<false>(sq[0]);
+#pragma unroll 1
+            for (int i = 0; i < gn && ok; i += 2) {
 #pragma unroll
-                for (int j = 0; j + 1 < AHEAD; ++j) sq[j] = sq[j + 1];
-                sq[AHEAD - 1] = 0;
-                if (i + AHEAD < sn) sq[AHEAD - 1] = sp[(i + AHEAD) * a.q.lds];
-                ok = __all_sync(0xffffffffu, q4_wait(dfull + 8 * (gi & 1), (gi >> 1) & 1, watch));
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t ss = pack64(__float_as_uint(s), __float_as_uint(s));
-                // 32 columns to a load: a wait is for all loads before it
+                for (int j = 0; j < 2; ++j) {
+                    if (i + j >= gn) break;
+                    ok = __all_sync(0xffffffffu, q4_wait(dfull + 8 * db, dph, watch));
+                    if (!ok) break;
+                    const float s = a.q.scale_bf16 ? q4_scale_bits<true>(sq[j]) : q4_scale_bits<false>(sq[j]);
+                    sq[j] = 0;
+                    if (i + j + 2 < sn) sq[j] = sp[(i + j + 2) * a.q.lds];
+                    tc_fence_after();
+                    const uint64_t ss = pack64(__float_as_uint(s), __float_as_uint(s));
+                    // 32 columns to a load: a wait is for all loads before it
 #pragma unroll
-                for (int c = 0; c < HB; c += 32) {
-                    constexpr int W = 32;
-                    uint32_t r[W];
-                    if (c + 32 <= HB) {
-                        tmem_ld_32x32b_x32(taddr + (gi & 1) * BN + c, r);
-                    } else {
-                        uint32_t q[16];
-                        tmem_ld_x16(taddr + (gi & 1) * BN + c, q);
+                    for (int c = 0; c < HB; c += 32) {
+                        uint32_t r[32];
+                        if (c + 32 <= HB) {
+                            tmem_ld_32x32b_x32(taddr + db * BN + c, r);
+                        } else {
+                            uint32_t q[16];
+                            tmem_ld_x16(taddr + db * BN + c, q);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) r[j] = q[j];
+                            for (int k = 0; k < 16; ++k) r[k] = q[k];
+                        }
+                        tmem_ld_wait();
+                        if (c + 32 >= HB) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(dempty + 8 * db);
+                        }
+#pragma unroll
+                        for (int k = 0; k < (c + 32 <= HB ? 16 : 8); ++k)
+                            acc[c / 2 + k] = fma2(ss, pack64(r[2 * k], r[2 * k + 1]), acc[c / 2 + k]);
                     }
-                    tmem_ld_wait();
-                    if (c + 32 >= HB) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(dempty + 8 * (gi & 1));
-                    }
-#pragma unroll
-                    for (int j = 0; j < (c + 32 <= HB ? 16 : 8); ++j)
-                        acc[c / 2 + j] = fma2(ss, pack64(r[2 * j], r[2 * j + 1]), acc[c / 2 + j]);
+                    db ^= 1u;
+                    dph ^= db ^ 1u;
                 }
             }
             if (!ok) break;
