@@ -14,60 +14,197 @@ namespace {
 
 constexpr int QZ_ROWS = 16, QZ_THREADS = QZ_ROWS * 32;
 constexpr int QZ_STEPS = 4, QZ_COLS = QZ_STEPS * 256;      // k of a CTA
-constexpr int QZ_GROUPS = QZ_COLS / 32;                    // groups of a CTA, at most
 
-// Eight values of a row from k, zeros past K; `vec`: 16-byte aligned rows
+// What a lane holds of a step of its warp's row -- 256 k, lane l the eight
+// from 8 l -- as stored: four words of 16-bit pairs, or eight of fp32.
 template <int DT>
-__device__ __forceinline__ void load_w8(const void *row, long long k, long long K, bool vec, float (&v)[8])
+constexpr int QZ_RAW = DT == TC_F32 ? 8 : 4;
+
+// Rows off 16 bytes (or the last piece of one) are read element by element,
+// neighbouring lanes neighbouring elements, zeros past K, and change places
+// through shared memory (`buf`, 8 x 33 words of the warp's own: element 8 l +
+// j at 33 j + l).
+template <int DT>
+__device__ __forceinline__ void load_step(const void *row, long long k0, long long K, bool vec, uint32_t *buf,
+                                          uint32_t (&raw)[QZ_RAW<DT>])
 {
-    if (vec && k + 8 <= K) {
-        if constexpr (DT == TC_F32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + k);
-            const float4 x = __ldcs(p), y = __ldcs(p + 1);
-            v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-        } else {
-            const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + k));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const int lane = threadIdx.x & 31;
+    if (vec && k0 + 256 <= K) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) + k0 * (DT == TC_F32 ? 4 : 2));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (DT == TC_BF16) {
-                    v[2 * i] = __uint_as_float(w[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-                } else {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-                    v[2 * i] = f.x;
-                    v[2 * i + 1] = f.y;
-                }
-            }
+        for (int i = 0; i < QZ_RAW<DT> / 4; ++i) {
+            const uint4 x = __ldcs(p + lane * (QZ_RAW<DT> / 4) + i);
+            raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
         }
         return;
     }
+    uint32_t x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? load_c(row, k + i, DT) : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+        const long long k = k0 + i * 32 + lane;
+        x[i] = 0u;
+        if (k < K) x[i] = DT == TC_F32 ? static_cast<const uint32_t *>(row)[k] : (uint32_t)static_cast<const uint16_t *>(row)[k];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = i * 32 + lane;
+        buf[33 * (e & 7) + (e >> 3)] = x[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t b = buf[33 * i + lane];
+        if constexpr (DT == TC_F32)
+            raw[i] = b;
+        else
+            raw[i >> 1] = i & 1 ? raw[i >> 1] | b << 16 : b;
+    }
 }
 
-// round(w / s) to nearest even, as the IEEE quotient rounds.  For 16-bit w
-// and s the quotient is a tie or at least 2^-17 of its size away from one, so
-// w (1 / s), good to 2^-22, rounds to the same whole number unless it is a
-// tie -- which the exact remainder w - r s shows -- and no division is needed.
-template <bool DIVIDE>
-__device__ __forceinline__ float q4_round(float w, float s, float inv, float half)
+template <int DT>
+__device__ __forceinline__ void to_floats(const uint32_t (&raw)[QZ_RAW<DT>], float (&v)[8])
 {
-    if constexpr (DIVIDE) return rintf(__fdiv_rn(w, s));
-    float r = rintf(w * inv);
-    const float e = fmaf(-r, s, w);
-    if (fabsf(e) == half) {
-        const float other = r + copysignf(1.0f, e);        // the tie's other side
-        r = fmodf(r, 2.0f) != 0.0f ? other : r;
+#pragma unroll
+    for (int i = 0; i < QZ_RAW<DT>; ++i) {
+        if constexpr (DT == TC_F32) {
+            v[i] = __uint_as_float(raw[i]);
+        } else if constexpr (DT == TC_BF16) {
+            v[2 * i] = __uint_as_float(raw[i] << 16);
+            v[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&raw[i]));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
     }
+}
+
+// max(-w, 0) and max(w, 0) over a group, or, both, max |w|; a NaN wins.  The
+// group is 1 << LOG2 neighbouring lanes.  16-bit weights are compared as
+// pairs, and both extremes travel in one register.
+struct QzExtremes {
+    float neg, pos;
+};
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-
-template <int DT, bool ZEROS>
-__global__ void __launch_bounds__(QZ_THREADS) q4_quantize_kernel(const Q4QuantArgs a, int lanes_log2)
+template <int DT>
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b)
 {
-    __shared__ uint16_t sc[QZ_GROUPS][QZ_ROWS];
-    __shared__ uint8_t zp[QZ_GROUPS][QZ_ROWS];
+    uint32_t r;
+    if constexpr (DT == TC_BF16)
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <int DT, bool ZEROS, int LOG2>
+__device__ __forceinline__ void extremes(const uint32_t (&raw)[QZ_RAW<DT>], uint32_t (&out)[DT == TC_F32 && ZEROS ? 2 : 1])
+{
+    if constexpr (DT == TC_F32) {
+        float neg = 0.0f, pos = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float v = __uint_as_float(raw[i]);
+            pos = max_nan(pos, ZEROS ? v : fabsf(v));
+            if constexpr (ZEROS) neg = max_nan(neg, -v);
+        }
+#pragma unroll
+        for (int o = 1; o < 1 << LOG2; o <<= 1) {
+            pos = max_nan(pos, __shfl_xor_sync(0xffffffffu, pos, o));
+            if constexpr (ZEROS) neg = max_nan(neg, __shfl_xor_sync(0xffffffffu, neg, o));
+        }
+        out[0] = __float_as_uint(pos);
+        if constexpr (ZEROS) out[1] = __float_as_uint(neg);
+    } else {
+        constexpr uint32_t SIGN = 0x80008000u;
+        uint32_t m = 0u;
+        if constexpr (ZEROS) {
+            uint32_t pos = 0u, neg = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                pos = max2_nan<DT>(pos, raw[i]);
+                neg = max2_nan<DT>(neg, raw[i] ^ SIGN);
+            }
+            // low half: -w, high half: w
+            m = max2_nan<DT>(__byte_perm(neg, pos, 0x5410u), __byte_perm(neg, pos, 0x7632u));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max2_nan<DT>(m, raw[i] & ~SIGN);
+            m = max2_nan<DT>(m, __byte_perm(m, 0u, 0x1032u));
+        }
+#pragma unroll
+        for (int o = 1; o < 1 << LOG2; o <<= 1) m = max2_nan<DT>(m, __shfl_xor_sync(0xffffffffu, m, o));
+        out[0] = m;
+    }
+}
+template <int DT, bool ZEROS>
+__device__ __forceinline__ QzExtremes to_extremes(const uint32_t (&x)[DT == TC_F32 && ZEROS ? 2 : 1])
+{
+    if constexpr (DT == TC_F32) {
+        return QzExtremes{__uint_as_float(x[ZEROS ? 1 : 0]), __uint_as_float(x[0])};
+    } else if constexpr (DT == TC_BF16) {
+        return QzExtremes{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u)};
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x[0]));
+        return QzExtremes{f.x, f.y};
+    }
+}
+
+// Whole numbers are rounded by adding 1.5 2^23: the sum's low bits are the
+// number, to nearest even.
+constexpr float QZ_MAGIC = 12582912.0f;
+
+// The codes round(w / s) + z, clamped to 0 .. 15, of the eight values, as a
+// word.  DIVIDE: by the IEEE quotient.  Otherwise -- 16-bit weights, whose
+// quotient by a 16-bit scale is a tie or at least 2^-17 of its size away from
+// one -- w (1 / s), good to 2^-22, rounds to the same number unless it is a
+// tie, which the exact remainder w - r s = s / 2 shows; then the quotient is
+// taken after all.
+template <bool DIVIDE>
+__device__ __forceinline__ uint32_t q4_word_of(const float (&v)[8], float s, float inv, int z)
+{
+    float m[8];
+    bool tie = isinf(inv);                                 // (a bf16 scale below 2^-128)
+    const float half = 0.5f * s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (DIVIDE) {
+            m[i] = fminf(fmaxf(__fdiv_rn(v[i], s), -16.0f), 16.0f) + QZ_MAGIC;
+        } else {
+            m[i] = fmaf(v[i], inv, QZ_MAGIC);
+            const float e = fmaf(-(m[i] - QZ_MAGIC), s, v[i]);
+            tie = tie || fabsf(e) == half;
+        }
+    }
+    if (!DIVIDE && tie) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = rintf(__fdiv_rn(v[i], s)) + QZ_MAGIC;
+    }
+    // pairs of elements in halves of a register: + z, then clamped, two at a time
+    const uint32_t zz = (uint32_t)z * 0x00010001u;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t p = __byte_perm(__float_as_uint(m[2 * i]), __float_as_uint(m[2 * i + 1]), 0x5410u);
+        w |= __viaddmin_s16x2_relu(p, zz, 0x000f000fu) << (4 * i);
+    }
+    return w;
+}
+
+template <int DT, bool ZEROS, int LOG2>
+__global__ void __launch_bounds__(QZ_THREADS, 2) q4_quantize_kernel(const Q4QuantArgs a)
+{
+    constexpr int PER = 32 >> LOG2;                            // groups of a warp's step
+    constexpr int GROUPS = QZ_STEPS * PER;                     // and of its row
+    static_assert(GROUPS <= 32, "a lane for each group");
+    __shared__ uint16_t sc[GROUPS][QZ_ROWS];
+    __shared__ uint8_t zp[GROUPS][QZ_ROWS];
+    __shared__ uint32_t bufs[QZ_ROWS][8 * 33];
     griddep_launch_dependents();
     griddep_wait();
     const Q4View &q = a.q;
@@ -76,69 +213,68 @@ __global__ void __launch_bounds__(QZ_THREADS) q4_quantize_kernel(const Q4QuantAr
     const long long k0 = (long long)blockIdx.y * QZ_COLS;
     const int es = DT == TC_F32 ? 4 : 2;
     const bool vec = (reinterpret_cast<uintptr_t>(a.W) & 15u) == 0 && (a.ld * es) % 16 == 0;
-    const long long kpad = (q.K + 31) / 32 * 32;
     if (n < q.N) {
         const uint8_t *src = static_cast<const uint8_t *>(a.W) + n * a.ld * es;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(const_cast<uint8_t *>(q.codes) + n * (q.ldw >> 1));
-        float v[QZ_STEPS][8];
-#pragma unroll
-        for (int i = 0; i < QZ_STEPS; ++i) load_w8<DT>(src, k0 + i * 256 + lane * 8, q.K, vec, v[i]);
+        const int steps = (int)min((long long)QZ_STEPS, (q.K - k0 + 255) / 256);
+        uint32_t raw[QZ_STEPS][QZ_RAW<DT>];
 #pragma unroll
         for (int i = 0; i < QZ_STEPS; ++i) {
-            const long long k = k0 + i * 256 + lane * 8;
-            if (k0 + i * 256 >= q.K) break;                // (the whole warp)
-            // the group's extremes; a value that is not finite makes `bad` one
-            float lo = 0.0f, hi = 0.0f, bad = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if constexpr (ZEROS) {
-                    lo = fminf(lo, v[i][j]);
-                    hi = fmaxf(hi, v[i][j]);
-                } else {
-                    hi = fmaxf(hi, fabsf(v[i][j]));
-                }
-                bad = fmaf(v[i][j], 0.0f, bad);            // 0, or NaN from an infinity or a NaN on
-            }
-            for (int o = 1; o < (1 << lanes_log2); o <<= 1) {
-                if constexpr (ZEROS) lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-                hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-                bad += __shfl_xor_sync(0xffffffffu, bad, o);
-            }
-            float s = ZEROS ? __fdiv_rn(hi - lo, 15.0f) : __fdiv_rn(hi, 7.0f);
-            s = bad == 0.0f ? s : __int_as_float(0x7fc00000);
-            uint16_t bits;
-            if (q.scale_bf16) {
-                bits = __bfloat16_as_ushort(__float2bfloat16_rn(s));
-                s = __bfloat162float(__ushort_as_bfloat16(bits));
-            } else {
-                bits = __half_as_ushort(__float2half_rn(s));
-                s = __half2float(__ushort_as_half(bits));
-            }
-            const float inv = DT == TC_F32 ? 0.0f : __fdiv_rn(1.0f, s), half = 0.5f * s;
-            float z = 8.0f;
-            if (ZEROS && s != 0.0f) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, s)), 0.0f), 15.0f);
-            uint32_t w = 0x88888888u;                      // a scale of 0: code = zero = 8
-            if (s != 0.0f) {
-                w = 0u;
+            for (int j = 0; j < QZ_RAW<DT>; ++j) raw[i][j] = 0u;
+            if (i < steps) load_step<DT>(src, k0 + i * 256, q.K, vec, bufs[row], raw[i]);
+        }
+        // lane i PER + j takes group j of step i: its scale, computed once, and
+        // handed back to the group's lanes
+        uint32_t ext[DT == TC_F32 && ZEROS ? 2 : 1] = {};
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float c = q4_round<DT == TC_F32>(v[i][j], s, inv, half) + z;
-                    w |= (uint32_t)fminf(fmaxf(c, 0.0f), 15.0f) << (4 * q4_nibble(j));
-                }
+        for (int i = 0; i < QZ_STEPS; ++i) {
+            uint32_t x[DT == TC_F32 && ZEROS ? 2 : 1];
+            extremes<DT, ZEROS, LOG2>(raw[i], x);
+#pragma unroll
+            for (int j = 0; j < (DT == TC_F32 && ZEROS ? 2 : 1); ++j) {
+                const uint32_t y = __shfl_sync(0xffffffffu, x[j], (lane & (PER - 1)) << LOG2);
+                if (lane / PER == i) ext[j] = y;
             }
-            if (k < kpad) dst[k / 8] = w;
-            if ((lane & ((1 << lanes_log2) - 1)) == 0) {
-                const int gl = (i * 32 + lane) >> lanes_log2;
-                sc[gl][row] = bits;
-                if constexpr (ZEROS) zp[gl][row] = (uint8_t)z;
-            }
+        }
+        const QzExtremes e = to_extremes<DT, ZEROS>(ext);
+        float s = ZEROS ? __fdiv_rn(e.pos + e.neg, 15.0f) : __fdiv_rn(e.pos, 7.0f);
+        if (!(e.pos < INFINITY && e.neg < INFINITY)) s = __int_as_float(0x7fc00000);
+        uint16_t bits;
+        if (q.scale_bf16) {
+            bits = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+            s = __bfloat162float(__ushort_as_bfloat16(bits));
+        } else {
+            bits = __half_as_ushort(__float2half_rn(s));
+            s = __half2float(__ushort_as_half(bits));
+        }
+        // a scale of 0 is used as infinity: every quotient is then 0, the code
+        // the zero point 8
+        const float div = s != 0.0f ? s : __int_as_float(0x7f800000);
+        const float inv = DT == TC_F32 ? 0.0f : __fdiv_rn(1.0f, div);
+        int z = 8;
+        if (ZEROS && s != 0.0f) z = (int)fminf(fmaxf(rintf(__fdiv_rn(e.neg, s)), 0.0f), 15.0f);
+        if (lane < GROUPS) {
+            sc[lane][row] = bits;
+            if constexpr (ZEROS) zp[lane][row] = (uint8_t)z;
+        }
+        uint32_t *dst = reinterpret_cast<uint32_t *>(const_cast<uint8_t *>(q.codes) + n * (q.ldw >> 1)) + k0 / 8 + lane;
+        const int words = (int)min((long long)QZ_COLS / 8, ((q.K + 31) / 32 * 32 - k0) / 8) - lane;
+#pragma unroll
+        for (int i = 0; i < QZ_STEPS; ++i) {
+            if (i >= steps) break;                             // (the whole warp)
+            const int from = i * PER + (lane >> LOG2);
+            float v[8];
+            to_floats<DT>(raw[i], v);
+            const uint32_t w = q4_word_of<DT == TC_F32>(v, __shfl_sync(0xffffffffu, div, from), __shfl_sync(0xffffffffu, inv, from),
+                                                        ZEROS ? __shfl_sync(0xffffffffu, z, from) : 8);
+            if (32 * i < words) dst[32 * i] = w;
         }
     }
     __syncthreads();
     uint16_t *scales = const_cast<uint16_t *>(static_cast<const uint16_t *>(q.scales));
     uint8_t *zeros = const_cast<uint8_t *>(q.zeros);
-    const long long g0 = k0 >> (3 + lanes_log2), ngroups = (q.K + q.group - 1) / q.group;
-    for (int i = threadIdx.x; i < (QZ_COLS >> (3 + lanes_log2)) * QZ_ROWS; i += QZ_THREADS) {
+    const long long g0 = k0 >> (3 + LOG2), ngroups = (q.K + q.group - 1) / q.group;
+    for (int i = threadIdx.x; i < GROUPS * QZ_ROWS; i += QZ_THREADS) {
         const int gl = i / QZ_ROWS, r = i % QZ_ROWS;
         if (g0 + gl >= ngroups || n0 + r >= q.N) continue;
         scales[(g0 + gl) * q.lds + n0 + r] = sc[gl][r];
@@ -149,10 +285,12 @@ __global__ void __launch_bounds__(QZ_THREADS) q4_quantize_kernel(const Q4QuantAr
 // ---------------------------------------------------------------- dequantise
 
 // The same shape: a word of codes per lane and step; the 16 rows of a CTA
-// share the lines of the scales.
+// share the lines of the scales.  The whole numbers code - zero come as
+// exact f16 pairs (q4_widen), times the scale in fp32.
 template <int DT>
 __global__ void __launch_bounds__(QZ_THREADS) q4_dequantize_kernel(const Q4DequantArgs a, int group_log2)
 {
+    __shared__ float bufs[QZ_ROWS][8 * 33];
     griddep_launch_dependents();
     griddep_wait();
     const Q4View &q = a.q;
@@ -163,28 +301,36 @@ __global__ void __launch_bounds__(QZ_THREADS) q4_dequantize_kernel(const Q4Dequa
     const int es = DT == TC_F32 ? 4 : 2;
     const bool vec = (reinterpret_cast<uintptr_t>(a.V) & 15u) == 0 && (a.ld * es) % 16 == 0;
     const uint32_t *src = reinterpret_cast<const uint32_t *>(q.codes + n * (q.ldw >> 1));
+    const uint16_t *scales = static_cast<const uint16_t *>(q.scales) + n;
     uint32_t w[QZ_STEPS];
-    float s[QZ_STEPS];
-    int z[QZ_STEPS];
+    uint16_t s[QZ_STEPS];
+    uint8_t z[QZ_STEPS];
 #pragma unroll
     for (int i = 0; i < QZ_STEPS; ++i) {
         const long long k = k0 + i * 256 + lane * 8;
-        w[i] = 0u, s[i] = 0.0f, z[i] = 8;
+        w[i] = 0u, s[i] = 0, z[i] = 8;
         if (k < q.K) {
             w[i] = __ldcs(src + k / 8);
-            s[i] = q4_scale(q, k >> group_log2, n);
-            z[i] = q4_zero(q, k >> group_log2, n);
+            s[i] = scales[(k >> group_log2) * q.lds];
+            if (q.zeros) z[i] = q.zeros[(k >> group_log2) * q.lds + n];
         }
     }
 #pragma unroll
     for (int i = 0; i < QZ_STEPS; ++i) {
-        const long long k = k0 + i * 256 + lane * 8;
-        if (k >= q.K) continue;
+        const long long ks = k0 + i * 256, k = ks + lane * 8;
+        if (ks >= q.K) break;                                  // (the whole warp)
+        uint32_t p[4];
+        q4_widen<false>(w[i], q4_zero_form<false>(z[i] & 15u), p);
+        const float f = q.scale_bf16 ? q4_scale_bits<true>(s[i]) : q4_scale_bits<false>(s[i]);
         float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (float)((int)((w[i] >> (4 * q4_nibble(j))) & 15u) - z[i]) * s[i];
+        for (int j = 0; j < 4; ++j) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&p[j]));
+            v[2 * j] = x.x * f;
+            v[2 * j + 1] = x.y * f;
+        }
         const long long off = n * a.ld + k;
-        if (vec && k + 8 <= q.K) {
+        if (vec && ks + 256 <= q.K) {
             if constexpr (DT == TC_F32) {
                 float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.V) + off);
                 __stcs(d, make_float4(v[0], v[1], v[2], v[3]));
@@ -195,9 +341,17 @@ __global__ void __launch_bounds__(QZ_THREADS) q4_dequantize_kernel(const Q4Dequa
                                   pack2(v[6], v[7], DT)));
             }
         } else {
+            // neighbouring lanes store neighbouring elements (see load_step)
+            float *buf = bufs[threadIdx.x >> 5];
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (k + j < q.K) store_c1(a.V, off + j, v[j], DT);
+            for (int j = 0; j < 8; ++j) buf[33 * j + lane] = v[j];
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int e = j * 32 + lane;
+                if (ks + e < q.K) store_c1(a.V, n * a.ld + ks + e, buf[33 * (e & 7) + (e >> 3)], DT);
+            }
         }
     }
 }
@@ -218,12 +372,20 @@ int log2_of(int x)
     return n;
 }
 
+template <int DT, bool ZEROS>
+cudaError_t quantize_group(const Q4QuantArgs &a, dim3 grid, cudaStream_t st)
+{
+    switch (a.q.group) {
+    case 32: return launch_dependent(q4_quantize_kernel<DT, ZEROS, 2>, grid, dim3(QZ_THREADS), 0, st, 1u, a);
+    case 64: return launch_dependent(q4_quantize_kernel<DT, ZEROS, 3>, grid, dim3(QZ_THREADS), 0, st, 1u, a);
+    default: return launch_dependent(q4_quantize_kernel<DT, ZEROS, 4>, grid, dim3(QZ_THREADS), 0, st, 1u, a);
+    }
+}
+
 template <int DT>
 cudaError_t quantize(const Q4QuantArgs &a, dim3 grid, cudaStream_t st)
 {
-    const int lanes = log2_of(a.q.group) - 3;
-    return a.q.zeros ? launch_dependent(q4_quantize_kernel<DT, true>, grid, dim3(QZ_THREADS), 0, st, 1u, a, lanes)
-                     : launch_dependent(q4_quantize_kernel<DT, false>, grid, dim3(QZ_THREADS), 0, st, 1u, a, lanes);
+    return a.q.zeros ? quantize_group<DT, true>(a, grid, st) : quantize_group<DT, false>(a, grid, st);
 }
 
 }  // namespace
