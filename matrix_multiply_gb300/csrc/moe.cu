@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     MoeLists &L = *reinterpret_cast<MoeLists *>(ring + MO_RING + MO_SUMS);
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + MO_RING + MO_SUMS + (sizeof(MoeLists) + 7) / 8 * 8);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t my_ring = smem_u32(ring) + warp * (S * MO_STAGE_BYTES);
     const uint32_t my_bar = smem_u32(bars + warp * S);
     const bool zeros1 = a.w1.zeros != nullptr, zeros2 = a.w2.zeros != nullptr;
@@ -345,27 +345,26 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     int f_s = 0, f_ent = ent_first, f_b = b_first, f_panel = r_lo, f_i = warp, f_row = r_lo, f_stage = 0, fetched = 0;
     constexpr uint32_t CS1 = 2048 + 2 * GP * MOE_SCALE_BOX * 2, Z1 = 2 * GP * Q4_ZERO_BOX;
     constexpr uint32_t CS2 = 2048 + GP * Q4_SCALE_BOX * 2, Z2 = GP * Q4_ZERO_BOX;
-    auto fetch = [&]() {                                // the whole warp; lane 0 issues the copies
+    const uint32_t leader = elect_one();
+    auto fetch = [&]() {                                // the whole warp
         const uint32_t st = my_ring + f_stage * MO_STAGE_BYTES, bar = my_bar + 8 * f_stage;
         if (f_u < u1) {
             const int half = L.ent_e[f_ent] * 2, slab = wk + f_s * MO_WARPS, x = f_b * 8;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, CS1 + (zeros1 ? Z1 : 0u));
-                tma_load_3d(st, &maps.c1, bar, slab * (Q4_SLAB / 2), x, half);
-                const int ra = half * a.I + x, rb = ra + a.I;
-                if (maps.s1_3d) {
-                    tma_load_3d(st + MO_SCALE_AT, &maps.s1, bar, x, slab * GP, half);
+            arrive_expect_by(bar, CS1 + (zeros1 ? Z1 : 0u), leader);
+            tma_load_3d_by(st, &maps.c1, bar, slab * (Q4_SLAB / 2), x, half, leader);
+            const int ra = half * a.I + x, rb = ra + a.I;
+            if (maps.s1_3d) {
+                tma_load_3d_by(st + MO_SCALE_AT, &maps.s1, bar, x, slab * GP, half, leader);
+            } else {
+                tma_load_2d_by(st + MO_SCALE_AT, &maps.s1, bar, ra & ~7, slab * GP, leader);
+                tma_load_2d_by(st + MO_SCALE_AT + 256, &maps.s1, bar, rb & ~7, slab * GP, leader);
+            }
+            if (zeros1) {
+                if (maps.z1_3d) {
+                    tma_load_3d_by(st + MO_ZERO_AT, &maps.z1, bar, x & ~15, slab * GP, half, leader);
                 } else {
-                    tma_load_2d(st + MO_SCALE_AT, &maps.s1, bar, ra & ~7, slab * GP);
-                    tma_load_2d(st + MO_SCALE_AT + 256, &maps.s1, bar, rb & ~7, slab * GP);
-                }
-                if (zeros1) {
-                    if (maps.z1_3d) {
-                        tma_load_3d(st + MO_ZERO_AT, &maps.z1, bar, x & ~15, slab * GP, half);
-                    } else {
-                        tma_load_2d(st + MO_ZERO_AT, &maps.z1, bar, ra & ~15, slab * GP);
-                        tma_load_2d(st + MO_ZERO_AT + 256, &maps.z1, bar, rb & ~15, slab * GP);
-                    }
+                    tma_load_2d_by(st + MO_ZERO_AT, &maps.z1, bar, ra & ~15, slab * GP, leader);
+                    tma_load_2d_by(st + MO_ZERO_AT + 256, &maps.z1, bar, rb & ~15, slab * GP, leader);
                 }
             }
             if (++f_s == per) {
@@ -377,12 +376,10 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         } else if (f_panel < r_hi && f_i < slabs2) {
             const int ent = ns2 == 1 ? f_i : (int)((unsigned)f_i / (unsigned)ns2), slab = f_i - ent * ns2;
             const int row = L.ent_e[ent] * a.H + f_row;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, CS2 + (zeros2 ? Z2 : 0u));
-                tma_load_2d(st, &maps.c2, bar, slab * (Q4_SLAB / 2), row);
-                tma_load_2d(st + MO_SCALE_AT, &maps.s2, bar, row & ~7, slab * GP);
-                if (zeros2) tma_load_2d(st + MO_ZERO_AT, &maps.z2, bar, row & ~15, slab * GP);
-            }
+            arrive_expect_by(bar, CS2 + (zeros2 ? Z2 : 0u), leader);
+            tma_load_2d_by(st, &maps.c2, bar, slab * (Q4_SLAB / 2), row, leader);
+            tma_load_2d_by(st + MO_SCALE_AT, &maps.s2, bar, row & ~7, slab * GP, leader);
+            if (zeros2) tma_load_2d_by(st + MO_ZERO_AT, &maps.z2, bar, row & ~15, slab * GP, leader);
             f_row += 16;
             if (f_row >= min(r_hi, f_panel + MO_PANEL)) {
                 f_row = f_panel;

@@ -182,6 +182,46 @@ __device__ __forceinline__ void q4_slab(float (&acc)[JOIN ? 1 : NT][4], const Q4
     }
 }
 
+// Work of one lane inside a loop that the whole warp runs: the lane whose
+// `leader` is set (elect_one) arms a barrier and issues a copy.  As a
+// divergent branch the same would take every address and coordinate out of
+// uniform registers and back for each copy.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ void arrive_expect_by(uint32_t bar, uint32_t bytes, uint32_t leader)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_by(uint32_t dst, const void *tmap, uint32_t bar, int32_t c0, int32_t c1,
+                                               uint32_t leader)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+        "\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_by(uint32_t dst, const void *tmap, uint32_t bar, int32_t c0, int32_t c1, int32_t c2,
+                                               uint32_t leader)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        "\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(leader)
+        : "memory");
+}
+
 // The warps of one group (of `n` warps, several groups to a CTA) meet.
 // Barrier 0 is __syncthreads'; a group of one warp needs none, so at most 8
 // others are in use.

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     float *sums = tiles + GV_WARPS * HOLD * TILE;                      // [HOLD][TILE], for the cluster
     uint64_t *bars = reinterpret_cast<uint64_t *>(sums + HOLD * TILE);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int K = (int)a.q.K;
     const int nslab = (K - 1) / Q4_SLAB + 1;
     int cluster = blockIdx.x, rank = 0, s_lo = 0, s_hi = nslab;
@@ -96,24 +96,25 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     griddep_launch_dependents();
     griddep_wait();
 
-    // lane 0 fetches the warp's pieces in order
+    // the warp's pieces, fetched in order
+    const uint32_t leader = elect_one();
     const uint32_t bytes = block_rows * 128 + GP * (Q4_SCALE_PITCH + (zeros ? Q4_ZERO_PITCH : 0));
-    int f_row = wr * block_rows, f_s = 0, f_stage = 0, fetched = 0;
-    auto fetch = [&]() {
+    int f_row = wr * block_rows, f_s = 0, fetched = 0;
+    uint32_t f_at = 0;                             // the stage's offset in the ring
+    auto fetch = [&]() {                           // the whole warp
         if (f_row >= nrows || per == 0) return;
-        const int row = (int)(r_lo + f_row), slab = s_lo + wk + f_s * GV_WARPS;
-        const uint32_t st = my_ring + f_stage * GV_STAGE_BYTES, bar = my_bar + 8 * f_stage;
-        mbar_arrive_expect_tx(bar, bytes);
-        tma_load_2d(st, &tmC, bar, slab * (Q4_SLAB / 2), row);
-        tma_load_2d(st + GV_SCALE_AT, &tmS, bar, row & ~7, slab * GP);
-        if (zeros) tma_load_2d(st + GV_ZERO_AT, &tmZ, bar, row & ~15, slab * GP);
+        const int row = (int)r_lo + f_row, slab = s_lo + wk + f_s * GV_WARPS;
+        const uint32_t st = my_ring + f_at, bar = my_bar + f_at / (GV_STAGE_BYTES / 8);
+        arrive_expect_by(bar, bytes, leader);
+        tma_load_2d_by(st, &tmC, bar, slab * (Q4_SLAB / 2), row, leader);
+        tma_load_2d_by(st + GV_SCALE_AT, &tmS, bar, row & ~7, slab * GP, leader);
+        if (zeros) tma_load_2d_by(st + GV_ZERO_AT, &tmZ, bar, row & ~15, slab * GP, leader);
         ++fetched;
-        if (++f_stage == S) f_stage = 0;
+        f_at = f_at == (S - 1) * GV_STAGE_BYTES ? 0u : f_at + GV_STAGE_BYTES;
         if (++f_s == per) f_s = 0, f_row += wr_n * block_rows;
     };
-    if (lane == 0)
-        for (int i = 0; i < S; ++i) fetch();
-    __syncwarp();
+#pragma unroll 1
+    for (int i = 0; i < S; ++i) fetch();
 
     // this warp's share of X: of one slab, for the whole kernel; with several
     // slabs a warp it is read again for each piece
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
                 b.z1 = b.z0 + 8;
                 q4_slab<BF16, SBF16, NT, G, Q4_SCALE_BOX>(acc, b, xf);
                 __syncwarp();                                          // every lane has read the piece
-                if (lane == 0 && ok) fetch();
+                if (__all_sync(0xffffffffu, ok)) fetch();
                 if (++stage == S) stage = 0, parity ^= 1;
             }
             float *tile = tiles + (held * GV_WARPS + warp) * TILE + 2 * t * GV_TILE_LD + g;

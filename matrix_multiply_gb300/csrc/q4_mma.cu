@@ -71,14 +71,6 @@ __device__ __forceinline__ void mma_commit_by(uint32_t bar, uint32_t leader)
         "r"(leader)
         : "memory");
 }
-// 1 in one lane of the (converged) warp
-__device__ __forceinline__ uint32_t elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
-
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
 {
     asm volatile(
