@@ -44,7 +44,7 @@ struct MoeLists {
     float p[MO_PAIRS];                       //   and its weight
     uint16_t ent_e[MO_PAIRS], ent_at[MO_PAIRS];   // entries: expert, first place in `pair`
     uint8_t ent_n[MO_PAIRS];                      //   and number of tokens (1 .. 8)
-    uint32_t scan[MO_WARPS];
+    uint8_t tok[MO_PAIRS];                        // the token of pair[i]
     int entries;
     float red[MO_WARPS][8];
 };
@@ -180,7 +180,7 @@ __device__ __forceinline__ void moe_router(const MoeArgs &a, MoeLists &L)
     }
 }
 
-// The chosen experts of every token, a warp per token: top_k rounds of a
+// The chosen experts of every token: a warp per token, top_k rounds of a
 // maximum over the logits' keys (NQ per lane), the lowest index among equals.
 template <int NQ>
 __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeLists &L)
@@ -194,6 +194,7 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeLists &L)
 #pragma unroll
         for (int q = 0; q < NQ; ++q) key[q] = q * 32 + lane < a.E ? order_key(l[q]) : 0u;
         uint32_t top = 0u, mine = 0u;
+#pragma unroll 1
         for (int j = 0; j < a.k; ++j) {
             uint32_t best = key[0];
             int at = lane;
@@ -201,10 +202,10 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeLists &L)
             for (int q = 1; q < NQ; ++q)
                 if (key[q] > best) best = key[q], at = q * 32 + lane;      // the lane's lowest index of its largest
             const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-            const int e = __reduce_min_sync(0xffffffffu, best == m ? at : 0x7fffffff);
+            const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? (uint32_t)at : 0xffffffffu);
 #pragma unroll
             for (int q = 0; q < NQ; ++q)
-                if (q * 32 + lane == e) key[q] = 0u;
+                if (q * 32 + lane == (int)e) key[q] = 0u;
             if (j == 0) top = m;
             if (lane == j) {
                 mine = m;
@@ -213,10 +214,9 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeLists &L)
             }
         }
         const float ftop = key_value(top), x = lane < a.k ? expf(key_value(mine) - ftop) : 0.0f;
-        float sum = 0.0f;
-        if (a.renorm) {
-            sum = x;
-        } else {
+        float sum = x;
+        if (!a.renorm) {
+            sum = 0.0f;
 #pragma unroll
             for (int q = 0; q < NQ; ++q) sum += q * 32 + lane < a.E ? expf(l[q] - ftop) : 0.0f;
         }
@@ -226,46 +226,37 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeLists &L)
 }
 
 // The entries: for each expert with tokens, in index order, its tokens in
-// order, 8 to an entry.
-__device__ void moe_list(const MoeArgs &a, MoeLists &L)
+// order, 8 to an entry.  One warp: its lanes scan 32 experts at a time.
+__device__ __forceinline__ void moe_list(const MoeArgs &a, MoeLists &L)
 {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int n = tid < a.E ? __popc(L.mask[tid]) : 0, chunks = (n + 7) >> 3;
-    uint32_t v = (uint32_t)n << 16 | (uint32_t)chunks, s = v;
+    const int lane = threadIdx.x & 31;
+    uint32_t base = 0;                                  // places in `pair` << 16 | entries so far
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane, n = e < a.E ? __popc(L.mask[e]) : 0, chunks = (n + 7) >> 3;
+        const uint32_t v = (uint32_t)n << 16 | (uint32_t)chunks;
+        uint32_t s = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += x;
-    }
-    if (lane == 31) L.scan[warp] = s;
-    __syncthreads();
-    uint32_t base = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < MO_WARPS; ++w) {
-        if (w < warp) base += L.scan[w];
-        total += L.scan[w];
-    }
-    s += base - v;                                      // before this expert
-    if (tid < a.E) {
-        L.off[tid] = (uint16_t)(s >> 16);
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += x;
+        }
+        const uint32_t at = base + s - v;
+        base += __shfl_sync(0xffffffffu, s, 31);
+        if (n > 0) L.off[e] = (uint16_t)(at >> 16);
         for (int c = 0; c < chunks; ++c) {
-            const int i = (int)(s & 0xffffu) + c;
-            L.ent_e[i] = (uint16_t)tid;
-            L.ent_at[i] = (uint16_t)((s >> 16) + 8 * c);
+            const int i = (int)(at & 0xffffu) + c;
+            L.ent_e[i] = (uint16_t)e;
+            L.ent_at[i] = (uint16_t)((at >> 16) + 8 * c);
             L.ent_n[i] = (uint8_t)min(8, n - 8 * c);
         }
     }
-    if (tid == 0) L.entries = (int)(total & 0xffffu);
-    __syncthreads();
-    if (tid < a.T * a.k) {
-        const int t = tid / a.k, e = L.id[tid];
-        L.pair[L.off[e] + __popc(L.mask[e] & ((1u << t) - 1u))] = (uint16_t)tid;
-        if (blockIdx.x == 0) {
-            if (a.ids) a.ids[tid] = e;
-            if (a.p) a.p[tid] = L.p[tid];
-        }
+    if (lane == 0) L.entries = (int)(base & 0xffffu);
+    __syncwarp();
+    for (int i = lane; i < a.T * a.k; i += 32) {
+        const int t = (int)((unsigned)i / (unsigned)a.k), e = L.id[i];
+        L.pair[L.off[e] + __popc(L.mask[e] & ((1u << t) - 1u))] = (uint16_t)i;
+        L.tok[L.off[e] + __popc(L.mask[e] & ((1u << t) - 1u))] = (uint8_t)t;
     }
-    __syncthreads();
 }
 
 template <bool BF16, bool SBF16, int G>
@@ -330,8 +321,13 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     else
         moe_choose<16>(a, L);
     __syncthreads();
-    moe_list(a, L);
+    if (warp == 0) moe_list(a, L);
+    __syncthreads();
     const int entries = L.entries;
+    if (blockIdx.x == gridDim.x - 1 && threadIdx.x < a.T * a.k) {
+        if (a.ids) a.ids[threadIdx.x] = L.id[threadIdx.x];
+        if (a.p) a.p[threadIdx.x] = L.p[threadIdx.x];
+    }
 
     // stage 1: an equal share of the units for every CTA
     const unsigned units = (unsigned)entries * (unsigned)nb, share = units / (unsigned)G1, extra = units - share * G1;
@@ -436,21 +432,8 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
 #pragma unroll
                         for (int j = 0; j < 8; ++j) xf[0][j][0] = xf[0][j][1] = xf[0][j][2] = xf[0][j][3] = 0u;
                         if (g < L.ent_n[ent]) {
-                            const uint16_t *row = X + (L.pair[L.ent_at[ent] + g] / a.k) * a.ldx;
-                            const int k = slab * Q4_SLAB + 8 * t;
-                            if (x_vec && slab < a.H / Q4_SLAB) {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + k) + 4 * j);
-                                    xf[0][j][0] = v.x, xf[0][j][1] = v.y, xf[0][j][2] = v.z, xf[0][j][3] = v.w;
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const uint4 v = q4_load_x(row, k + 32 * j, a.H, x_vec);
-                                    xf[0][j][0] = v.x, xf[0][j][1] = v.y, xf[0][j][2] = v.z, xf[0][j][3] = v.w;
-                                }
-                            }
+                            const uint16_t *row = X + L.tok[L.ent_at[ent] + g] * a.ldx;
+                            q4_load_slab(xf[0], row, (long long)slab * Q4_SLAB + 8 * t, a.H, x_vec && slab < a.H / Q4_SLAB);
                         }
                     }
                     const uint8_t *st = arrive();
@@ -544,9 +527,8 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
             float pw[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int pr = 2 * t + c < n ? L.pair[at + 2 * t + c] : 0;
-                tok[c] = 2 * t + c < n ? pr / a.k : -1;
-                pw[c] = L.p[pr];
+                tok[c] = 2 * t + c < n ? L.tok[at + 2 * t + c] : -1;
+                pw[c] = 2 * t + c < n ? L.p[L.pair[at + 2 * t + c]] : 0.0f;
             }
             for (int row = panel; row < p_hi; row += 16) {
                 float acc[1][4] = {};

@@ -278,4 +278,35 @@ __device__ __forceinline__ uint4 q4_load_x(const uint16_t *row, long long k, lon
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A lane's share of a slab of an X row as q4_slab takes it (from element k:
+// eight of every 32), zeros past K.  `whole`: 16-byte aligned rows, the slab
+// inside K.  Otherwise single elements, 32 loads under way at a time.
+__device__ __forceinline__ void q4_load_slab(uint32_t (&xf)[8][4], const uint16_t *row, long long k, long long K, bool whole)
+{
+    if (whole) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + k) + 4 * j);
+            xf[j][0] = v.x, xf[j][1] = v.y, xf[j][2] = v.z, xf[j][3] = v.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int b = 0; b < 8; b += 4) {
+        uint16_t h[4][8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const long long at = k + 32 * (b + j) + i;
+                h[j][i] = 0;
+                if (at < K) h[j][i] = __ldg(row + at);
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xf[b + j][i] = (uint32_t)h[j][2 * i] | (uint32_t)h[j][2 * i + 1] << 16;
+    }
+}
+
 }  // namespace tc

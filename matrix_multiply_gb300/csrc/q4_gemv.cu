@@ -125,25 +125,10 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
         const bool whole = x_vec && slab < K / Q4_SLAB;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const uint16_t *row = X + (nt * 8 + g) * a.ldx;
-            const long long k = (long long)slab * Q4_SLAB + t * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) xf[nt][j][0] = xf[nt][j][1] = xf[nt][j][2] = xf[nt][j][3] = 0u;
-            if (nt * 8 + g < a.M) {
-                if (whole) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + k) + 4 * j);
-                        xf[nt][j][0] = v.x, xf[nt][j][1] = v.y, xf[nt][j][2] = v.z, xf[nt][j][3] = v.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint4 v = q4_load_x(row, k + 32 * j, K, x_vec);
-                        xf[nt][j][0] = v.x, xf[nt][j][1] = v.y, xf[nt][j][2] = v.z, xf[nt][j][3] = v.w;
-                    }
-                }
-            }
+            if (nt * 8 + g < a.M)
+                q4_load_slab(xf[nt], X + (nt * 8 + g) * a.ldx, (long long)slab * Q4_SLAB + t * 8, K, whole);
         }
     };
     if (per > 0) load_xf(s_lo + wk);
