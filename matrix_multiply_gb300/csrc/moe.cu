@@ -193,7 +193,7 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeLists &L)
         for (int q = 0; q < NQ; ++q) l[q] = q * 32 + lane < a.E ? __ldcg(a.logits + t * a.E + q * 32 + lane) : 0.0f;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) key[q] = q * 32 + lane < a.E ? order_key(l[q]) : 0u;
-        uint32_t top = 0u, mine = 0u;
+        uint32_t top = 0u, mine = 0u, id = 0u;
 #pragma unroll 1
         for (int j = 0; j < a.k; ++j) {
             uint32_t best = key[0];
@@ -207,11 +207,11 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &a, MoeLists &L)
             for (int q = 0; q < NQ; ++q)
                 if (q * 32 + lane == (int)e) key[q] = 0u;
             if (j == 0) top = m;
-            if (lane == j) {
-                mine = m;
-                L.id[t * a.k + j] = (uint16_t)e;
-                atomicOr(&L.mask[e], 1u << t);
-            }
+            if (lane == j) mine = m, id = e;
+        }
+        if (lane < a.k) {
+            L.id[t * a.k + lane] = (uint16_t)id;
+            atomicOr(&L.mask[id], 1u << t);
         }
         const float ftop = key_value(top), x = lane < a.k ? expf(key_value(mine) - ftop) : 0.0f;
         float sum = x;
