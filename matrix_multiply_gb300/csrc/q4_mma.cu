@@ -256,8 +256,11 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     } else if (warp < QM_CONV) {
         // ------------------------------------------------------ converters
         const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-        const long long ngroups = (a.q.K + G - 1) / G;
-        int it = 0, ci = 0;
+        constexpr int BLOCKS = QM_CONV == 4 ? 2 : 1;             // blocks of a pair that a warp converts
+        const int ngroups = (int)((a.q.K + G - 1) / G);
+        const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + A_COL;
+        const uint8_t *src = codes + row * 128;
+        int it = 0, ci = 0;                                      // blocks and pairs before this one
         uint32_t pending = 0;                                    // the barrier of the block whose stores are under way
         auto hand_over = [&]() {
             if (!pending) return;
@@ -269,48 +272,50 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
         };
         for (int u = blockIdx.x; ok && u < units; u += step) {
             const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
-            const bool in = a.q.zeros && w.n0 + row < a.q.N;
-            const uint8_t *zp = in ? a.q.zeros + w.n0 + row : a.q.zeros;
-            // a row's zero points of a block, loaded two blocks ahead, and used
-            // only then: a use next to its load would wait for it
-            uint8_t z[2][NG];
-            auto load_z = [&](uint8_t (&d)[NG], int kb) {
+            const uint8_t *zp = a.q.zeros ? a.q.zeros + min((long long)w.n0 + row, a.q.N - 1) : nullptr;
+            // a row's zero points of a pair of blocks, loaded a pair ahead: a use
+            // next to its load would wait for it
+            uint8_t zn[BLOCKS][NG];
+            auto load_z = [&](int kb) {
 #pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    const long long gr = (long long)kb * NG + i;
-                    d[i] = 8;
-                    if (in && gr < ngroups) d[i] = zp[gr * a.q.lds];
-                }
+                for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) {
+                        const int gr = (kb + (BLOCKS == 1 ? half : b)) * NG + i;
+                        zn[b][i] = 8;
+                        if (zp && gr < ngroups) zn[b][i] = zp[gr * a.q.lds];
+                    }
             };
-            load_z(z[0], w.kb0);
-            load_z(z[1], w.kb0 + 1);
+            load_z(w.kb0);
 #pragma unroll 1
-            for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+            for (int kb = w.kb0; kb < w.kb1; kb += 2, it += 2, ++ci) {
                 const int cs = ci % QM_CS;
-                if ((kb & 1) == 0) {
-                    ok = __all_sync(0xffffffffu, q4_wait(cfull + 8 * cs, (ci / QM_CS) & 1, watch));
-                    if (!ok) break;
-                }
-                uint32_t zz[NG];
+                uint32_t zz[BLOCKS][NG];
 #pragma unroll
-                for (int i = 0; i < NG; ++i) zz[i] = z[0][i] & 15u, z[0][i] = z[1][i];
-                load_z(z[1], kb + 2);
-                if (QM_CONV == 4 || (it & 1) == half) {
-                    const uint8_t *src = codes + cs * QM_CODE_BYTES + row * 128;
-                    const int as = it % QM_XS;
+                for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) zz[b][i] = zn[b][i] & 15u;
+                if (zp) load_z(kb + 2);
+                ok = __all_sync(0xffffffffu, q4_wait(cfull + 8 * cs, (ci / QM_CS) & 1, watch));
+                if (!ok) break;
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) {
+                    const int bb = BLOCKS == 1 ? half : b;
+                    if (kb + bb >= w.kb1) break;
+                    const int as = (it + bb) % QM_XS;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {                // two halves of 64 k
                         uint32_t words[8], out[32];
 #pragma unroll
                         for (int v = 0; v < 2; ++v) {
                             const uint4 x = *reinterpret_cast<const uint4 *>(
-                                src + (((4 * (kb & 1) + 2 * h + v) ^ (row & 7)) << 4));
+                                src + cs * QM_CODE_BYTES + (((4 * bb + 2 * h + v) ^ (row & 7)) << 4));
                             words[4 * v] = x.x, words[4 * v + 1] = x.y, words[4 * v + 2] = x.z, words[4 * v + 3] = x.w;
                         }
 #pragma unroll
                         for (int v = 0; v < 8; ++v) {
                             uint32_t p[4];
-                            q4_widen<BF16>(words[v], q4_zero_form<BF16>(zz[(h * 64 + v * 8) / G]), p);
+                            q4_widen<BF16>(words[v], q4_zero_form<BF16>(zz[b][(h * 64 + v * 8) / G]), p);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) out[4 * v + j] = p[j];
                         }
@@ -318,21 +323,20 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                             // the block before is handed over now: its stores have
                             // had this block's first half to complete
                             hand_over();
-                            ok = __all_sync(0xffffffffu, q4_wait(empty + 8 * as, ((it / QM_XS) & 1) ^ 1, watch));
+                            ok = __all_sync(0xffffffffu, q4_wait(empty + 8 * as, (((it + bb) / QM_XS) & 1) ^ 1, watch));
                             if (!ok) break;
                             tc_fence_after();
                         }
-                        tmem_st_32x32b_x32(tmem + ((uint32_t)(quarter * 32) << 16) + A_COL + as * 64 + h * 32, out);
+                        tmem_st_32x32b_x32(to + as * 64 + h * 32, out);
                     }
                     if (!ok) break;
                     pending = full + 8 * as;
                 }
-                if ((kb & 1) == 1 || kb + 1 == w.kb1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(cempty + 8 * cs);
-                    ++ci;
-                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(cempty + 8 * cs);
             }
+            it -= (w.kb1 - w.kb0) & 1;
         }
         hand_over();
     } else {
