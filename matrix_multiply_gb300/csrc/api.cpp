@@ -1766,6 +1766,18 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     return TC_OK;
 }
 
+// A C entry lets no C++ exception out (the name of the last kernel is a
+// std::string, the context's lock may throw).
+template <typename F>
+tc_status_t guarded(F f) noexcept
+{
+    try {
+        return f();
+    } catch (...) {
+        return TC_ERR_CUDA;
+    }
+}
+
 tc_status_t stream_init(tc_ctx *ctx, tc_stream *s)
 {
     s->ctx = ctx;
@@ -2005,26 +2017,26 @@ tc_status_t tc_gemm_q8_weight_validate(const tc_gemm_desc *d, const float *scale
 tc_status_t tc_quantize_q4_async(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W, const tc_q4_weight *q,
                                  tc_stream *s)
 {
-    return run_quantize(ctx, w_dtype, ld, W, q, s);
+    return guarded([&] { return run_quantize(ctx, w_dtype, ld, W, q, s); });
 }
 
 tc_status_t tc_quantize_q4(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W, const tc_q4_weight *q)
 {
     if (!ctx) return TC_ERR_NULL;
-    const tc_status_t st = run_quantize(ctx, w_dtype, ld, W, q, ctx->def);
+    const tc_status_t st = guarded([&] { return run_quantize(ctx, w_dtype, ld, W, q, ctx->def); });
     return st == TC_OK ? tc_stream_sync(ctx->def) : st;
 }
 
 tc_status_t tc_dequantize_q4_async(tc_ctx *ctx, const tc_q4_weight *q, tc_dtype_t v_dtype, int32_t ld, void *V,
                                    tc_stream *s)
 {
-    return run_dequantize(ctx, q, v_dtype, ld, V, s);
+    return guarded([&] { return run_dequantize(ctx, q, v_dtype, ld, V, s); });
 }
 
 tc_status_t tc_dequantize_q4(tc_ctx *ctx, const tc_q4_weight *q, tc_dtype_t v_dtype, int32_t ld, void *V)
 {
     if (!ctx) return TC_ERR_NULL;
-    const tc_status_t st = run_dequantize(ctx, q, v_dtype, ld, V, ctx->def);
+    const tc_status_t st = guarded([&] { return run_dequantize(ctx, q, v_dtype, ld, V, ctx->def); });
     return st == TC_OK ? tc_stream_sync(ctx->def) : st;
 }
 
@@ -2038,13 +2050,13 @@ tc_status_t tc_q4_validate(const tc_q4_weight *q, tc_dtype_t dtype, int32_t ld, 
 tc_status_t tc_gemm_q4_weight_async(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C,
                                     tc_stream *s)
 {
-    return run_q4w(ctx, d, q, X, C, s);
+    return guarded([&] { return run_q4w(ctx, d, q, X, C, s); });
 }
 
 tc_status_t tc_gemm_q4_weight(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C)
 {
     if (!ctx) return TC_ERR_NULL;
-    const tc_status_t st = run_q4w(ctx, d, q, X, C, ctx->def);
+    const tc_status_t st = guarded([&] { return run_q4w(ctx, d, q, X, C, ctx->def); });
     return st == TC_OK ? tc_stream_sync(ctx->def) : st;
 }
 
@@ -2058,14 +2070,14 @@ tc_status_t tc_moe_q4_async(tc_ctx *ctx, const tc_moe_desc *d, const void *X, co
                             const tc_q4_weight *gate_up, const tc_q4_weight *down, void *Y, int32_t *ids,
                             float *weights, tc_stream *s)
 {
-    return run_moe(ctx, d, X, router, gate_up, down, Y, ids, weights, s);
+    return guarded([&] { return run_moe(ctx, d, X, router, gate_up, down, Y, ids, weights, s); });
 }
 
 tc_status_t tc_moe_q4(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void *router,
                       const tc_q4_weight *gate_up, const tc_q4_weight *down, void *Y, int32_t *ids, float *weights)
 {
     if (!ctx) return TC_ERR_NULL;
-    const tc_status_t st = run_moe(ctx, d, X, router, gate_up, down, Y, ids, weights, ctx->def);
+    const tc_status_t st = guarded([&] { return run_moe(ctx, d, X, router, gate_up, down, Y, ids, weights, ctx->def); });
     return st == TC_OK ? tc_stream_sync(ctx->def) : st;
 }
 

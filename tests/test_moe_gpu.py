@@ -72,6 +72,16 @@ def test_layer(ctx, shape, x, y, r, group, zeros, renorm):
     check(*out, X, R, w1, w2, I, k, y, renorm, f"{shape} {x}->{y} {ctx.last_kernel}")
 
 
+@pytest.mark.parametrize("shape", [(2, 6000, 40, 3, 2), (9, 9100, 24, 3, 1), (3, 72, 5000, 3, 2), (20, 5200, 70, 12, 3)])
+def test_long_axes(ctx, shape):
+    """hidden beyond one slab per warp and one panel of rows, inter beyond one
+    slab, more than 8 tokens to an expert."""
+    T, H, I, E, k = shape
+    X, R, w1, w2 = problem(T, H, I, E, k, group=64)
+    out = layer(ctx, X.cuda(), R.cuda(), w1, w2, I, E, k)
+    check(*out, X, R, w1, w2, I, k, "f32", True, f"{shape}")
+
+
 def test_ties_go_to_the_lowest_index(ctx):
     T, H, I, E, k = 3, 64, 32, 70, 5
     X, R, w1, w2 = problem(T, H, I, E, k)

@@ -156,6 +156,20 @@ def test_whole_numbers_bit_for_bit(ctx, M, x):
         assert torch.equal(out.cpu().double(), X.double() @ w.values.t()), (M, N, K, ctx.last_kernel)
 
 
+@pytest.mark.parametrize("shape", [(3, 100, 40000), (16, 33, 33000), (4, 20000, 5000), (9, 9001, 9000), (3, 130001, 256),
+                                   (2, 70000, 700), (16, 40000, 1030), (17, 100, 40000), (33, 3001, 9000), (1, 5, 100000)])
+def test_long_axes(ctx, shape):
+    """K beyond one slab per warp and one cluster, more blocks of rows than are
+    held at once, K slices on the tensor cores."""
+    M, N, K = shape
+    w = Weight(N, K, 64, True, "f16", seed=N, kind="pow2")
+    X = torch.randint(-2, 3, (M, K), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16)
+    out = run(ctx, X.cuda(), w, "f32")
+    want = X.double() @ w.values.t()
+    assert float(want.abs().max()) * 4 < 2 ** 24           # exact: quarter steps below 2^22
+    assert torch.equal(out.cpu().double(), want), ctx.last_kernel
+
+
 @pytest.mark.parametrize("M", [1, 6, 16, 40, 200])
 def test_strides_and_alignment(ctx, M):
     """Padded rows of every tensor, X and C off any alignment."""
