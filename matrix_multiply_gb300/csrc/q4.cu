@@ -178,7 +178,7 @@ __device__ __forceinline__ uint32_t q4_word_of(const float (&v)[8], float s, flo
         } else {
             m[i] = fmaf(v[i], inv, QZ_MAGIC);
             const float e = fmaf(-(m[i] - QZ_MAGIC), s, v[i]);
-            tie = tie || fabsf(e) == half;
+            tie |= fabsf(e) == half;
         }
     }
     if (!DIVIDE && tie) {
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(QZ_THREADS, 2) q4_quantize_kernel(const Q4Quan
 // share the lines of the scales.  The whole numbers code - zero come as
 // exact f16 pairs (q4_widen), times the scale in fp32.
 template <int DT>
-__global__ void __launch_bounds__(QZ_THREADS) q4_dequantize_kernel(const Q4DequantArgs a, int group_log2)
+__global__ void __launch_bounds__(QZ_THREADS, 4) q4_dequantize_kernel(const Q4DequantArgs a, int group_log2)
 {
     __shared__ float bufs[QZ_ROWS][8 * 33];
     griddep_launch_dependents();
