@@ -1531,12 +1531,17 @@ bool encode_q4(tc_ctx *ctx, CUtensorMap *m, CUtensorMapDataType t, const void *b
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The streaming kernel's grid and tensor maps.  One cluster of ksplit CTAs
-// per range of W's rows, ksplit the fewest that leave a warp one slab of K.
+// The streaming kernel's grid and tensor maps.  One CTA per range of W's
+// rows, or, when K has more slabs than a CTA has warps and the ranges would
+// be shorter than a block of 16 rows, a cluster of ksplit CTAs.  Measured on
+// GB300, microseconds unsplit and split: 4 x 4096 x 11008 (27 rows a range)
+// 10.1 and 11.4; 1 x 1024 x 8192 (7 rows) 4.8 and 4.3; 1 x 512 x 11008 (4
+// rows) 5.6 and 4.2.
 bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f, Q4GemvPlan *p)
 {
     const int64_t slabs = cdiv(a.q.K, 256);
-    p->ksplit = f.gemv_ks > 0 ? std::min(f.gemv_ks, 8) : (int)std::min<int64_t>(8, cdiv(slabs, 16));
+    const bool split = slabs > 16 && a.q.N < 16LL * ctx->num_sms;
+    p->ksplit = f.gemv_ks > 0 ? std::min(f.gemv_ks, 8) : split ? (int)std::min<int64_t>(8, cdiv(slabs, 16)) : 1;
     p->ksplit = (int)std::min<int64_t>(p->ksplit, slabs);
     int &fit = ctx->q4_clusters[p->ksplit];
     if (fit < 0) fit = q4_gemv_max_clusters(p->ksplit);
@@ -1546,6 +1551,7 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
     p->clusters = (int)cdiv(a.q.N, p->rows);
     p->nblk = (int)cdiv(p->rows, 16);
     p->block_rows = (int)cdiv(p->rows, p->nblk);
+    p->nblk = (int)cdiv(p->rows, p->block_rows);
     p->status = s->status_dev;
     p->timeout_ns = 4000000000ull;
     const int64_t groups = cdiv(a.q.K, a.q.group);

@@ -99,11 +99,14 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     // the warp's pieces, fetched in order
     const uint32_t leader = elect_one();
     const uint32_t bytes = block_rows * 128 + GP * (Q4_SCALE_PITCH + (zeros ? Q4_ZERO_PITCH : 0));
-    int f_row = wr * block_rows, f_s = 0, fetched = 0;
+    // blocks with rows in them
+    const int have = nrows == rows ? nblk : (int)((unsigned)(nrows - 1) / (unsigned)block_rows) + 1;
+    int f_first = wr, f_h = 0, f_s = 0, fetched = 0;
     uint32_t f_at = 0;                             // the stage's offset in the ring
+    // the order of the pieces: HOLD blocks at a time, of these slab by slab
     auto fetch = [&]() {                           // the whole warp
-        if (f_row >= nrows || per == 0) return;
-        const int row = (int)r_lo + f_row, slab = s_lo + wk + f_s * GV_WARPS;
+        if (f_first >= have || per == 0) return;
+        const int row = (int)r_lo + (f_first + f_h * wr_n) * block_rows, slab = s_lo + wk + f_s * GV_WARPS;
         const uint32_t st = my_ring + f_at, bar = my_bar + f_at / (GV_STAGE_BYTES / 8);
         arrive_expect_by(bar, bytes, leader);
         tma_load_2d_by(st, &tmC, bar, slab * (Q4_SLAB / 2), row, leader);
@@ -111,13 +114,16 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
         if (zeros) tma_load_2d_by(st + GV_ZERO_AT, &tmZ, bar, row & ~15, slab * GP, leader);
         ++fetched;
         f_at = f_at == (S - 1) * GV_STAGE_BYTES ? 0u : f_at + GV_STAGE_BYTES;
-        if (++f_s == per) f_s = 0, f_row += wr_n * block_rows;
+        if (++f_h == HOLD || f_first + f_h * wr_n >= have) {
+            f_h = 0;
+            if (++f_s == per) f_s = 0, f_first += HOLD * wr_n;
+        }
     };
 #pragma unroll 1
     for (int i = 0; i < S; ++i) fetch();
 
-    // this warp's share of X: of one slab, for the whole kernel; with several
-    // slabs a warp it is read again for each piece
+    // this warp's share of X: of one slab, for the whole kernel, or of the
+    // slab at hand
     const uint16_t *X = static_cast<const uint16_t *>(a.X);
     const bool x_vec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (a.ldx & 7) == 0;
     uint32_t xf[NT][8][4];
@@ -157,14 +163,14 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
             if (ksplit == 1) break;
         }
         int held = 0;
-        for (int blk = first; active && blk < nblk && held < HOLD; blk += wr_n, ++held) {
-            float acc[NT][4];
+        if (active) held = wr_n == 1 ? min(HOLD, have - first) : min(HOLD, (have - first + wr_n - 1) / wr_n);
+        for (int s = 0; s < per; ++s) {
+            if (per > 1) load_xf(s_lo + wk + s * GV_WARPS);
+            for (int h = 0; h < held; ++h) {
+                const int row = (int)(r_lo & 15) + (first + h * wr_n) * block_rows;      // (only its low bits are used)
+                float acc[NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-            const int row = (int)(r_lo & 15) + blk * block_rows;       // (only its low bits are used)
-            for (int s = 0; s < per; ++s) {
-                if (blk * block_rows >= nrows) break;                  // rows past N: nothing was fetched
-                if (per > 1) load_xf(s_lo + wk + s * GV_WARPS);
+                for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
                 ok = ok && q4_wait(my_bar + 8 * stage, parity, watch);
                 __syncwarp();
                 const uint8_t *st = ring + (warp * S + stage) * GV_STAGE_BYTES;
@@ -179,13 +185,17 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
                 __syncwarp();                                          // every lane has read the piece
                 if (__all_sync(0xffffffffu, ok)) fetch();
                 if (++stage == S) stage = 0, parity ^= 1;
+                // the block's partial tile, a slab at a time
+                float *tile = tiles + (h * GV_WARPS + warp) * TILE + 2 * t * GV_TILE_LD + g;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float *p = tile + (nt * 8 + (e & 1)) * GV_TILE_LD + 8 * (e >> 1);
+                        if (s > 0) acc[nt][e] += *p;
+                        *p = acc[nt][e];
+                    }
             }
-            float *tile = tiles + (held * GV_WARPS + warp) * TILE + 2 * t * GV_TILE_LD + g;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    tile[(nt * 8 + (e & 1)) * GV_TILE_LD + 8 * (e >> 1)] = acc[nt][e];
         }
         __syncwarp();
         if (active) {
