@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                         for (int j = 0; j < 8; ++j) xf[0][j][0] = xf[0][j][1] = xf[0][j][2] = xf[0][j][3] = 0u;
                         if (g < L.ent_n[ent]) {
                             const uint16_t *row = X + L.tok[L.ent_at[ent] + g] * a.ldx;
-                            q4_load_slab(xf[0], row, (long long)slab * Q4_SLAB + 8 * t, a.H, x_vec && slab < a.H / Q4_SLAB);
+                            q4_load_slab<false>(xf[0], row, (long long)slab * Q4_SLAB + 8 * t, a.H, x_vec && slab < a.H / Q4_SLAB);
                         }
                     }
                     const uint8_t *st = arrive();

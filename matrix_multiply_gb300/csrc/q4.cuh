@@ -280,7 +280,10 @@ __device__ __forceinline__ uint4 q4_load_x(const uint16_t *row, long long k, lon
 
 // A lane's share of a slab of an X row as q4_slab takes it (from element k:
 // eight of every 32), zeros past K.  `whole`: 16-byte aligned rows, the slab
-// inside K.  Otherwise single elements, 32 loads under way at a time.
+// inside K.  Otherwise pairs of elements (rows on 4 bytes) or single ones,
+// half of them under way at a time.
+// PAIRS false leaves the pairs out, where the load is part of a kernel's main loop.
+template <bool PAIRS = true>
 __device__ __forceinline__ void q4_load_slab(uint32_t (&xf)[8][4], const uint16_t *row, long long k, long long K, bool whole)
 {
     if (whole) {
@@ -289,23 +292,37 @@ __device__ __forceinline__ void q4_load_slab(uint32_t (&xf)[8][4], const uint16_
             const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + k) + 4 * j);
             xf[j][0] = v.x, xf[j][1] = v.y, xf[j][2] = v.z, xf[j][3] = v.w;
         }
-        return;
-    }
+    } else if (PAIRS && (reinterpret_cast<uintptr_t>(row) & 3u) == 0) {
+        const int left = (int)min(1024LL, K - k);              // elements from the lane's first on (k is even)
 #pragma unroll
-    for (int b = 0; b < 8; b += 4) {
-        uint16_t h[4][8];
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const long long at = k + 32 * (b + j) + i;
-                h[j][i] = 0;
-                if (at < K) h[j][i] = __ldg(row + at);
+            for (int i = 0; i < 4; ++i) {
+                const int at = 32 * j + 2 * i;
+                xf[j][i] = 0u;
+                if (at + 1 < left)
+                    xf[j][i] = __ldg(reinterpret_cast<const uint32_t *>(row + k + at));
+                else if (at < left)
+                    xf[j][i] = __ldg(row + k + at);
             }
+    } else {
+        const int left = (int)min(1024LL, K - k);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int b = 0; b < 8; b += 4) {
+            uint16_t h[4][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) xf[b + j][i] = (uint32_t)h[j][2 * i] | (uint32_t)h[j][2 * i + 1] << 16;
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = 32 * (b + j) + i;
+                    h[j][i] = 0;
+                    if (at < left) h[j][i] = __ldg(row + k + at);
+                }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xf[b + j][i] = (uint32_t)h[j][2 * i] | (uint32_t)h[j][2 * i + 1] << 16;
+        }
     }
 }
 
