@@ -13,7 +13,10 @@ namespace tc {
 namespace {
 
 constexpr int QZ_ROWS = 16, QZ_THREADS = QZ_ROWS * 32;
-constexpr int QZ_STEPS = 4, QZ_COLS = QZ_STEPS * 256;      // k of a CTA
+constexpr int QZ_STEPS = 4, QZ_COLS = QZ_STEPS * 256;      // k of a CTA (dequantising)
+// k steps of a warp when quantising: as many as its registers hold
+template <int DT>
+constexpr int QZ_N = DT == TC_F32 ? 4 : 8;
 
 // What a lane holds of a step of its warp's row -- 256 k, lane l the eight
 // from 8 l -- as stored: four words of 16-bit pairs, or eight of fp32.
@@ -199,9 +202,10 @@ __device__ __forceinline__ uint32_t q4_word_of(const float (&v)[8], float s, flo
 template <int DT, bool ZEROS, int LOG2>
 __global__ void __launch_bounds__(QZ_THREADS, 2) q4_quantize_kernel(const Q4QuantArgs a)
 {
+    constexpr int STEPS = QZ_N<DT>, COLS = STEPS * 256;
     constexpr int PER = 32 >> LOG2;                            // groups of a warp's step
-    constexpr int GROUPS = QZ_STEPS * PER;                     // and of its row
-    static_assert(GROUPS <= 32, "a lane for each group");
+    constexpr int GROUPS = STEPS * PER;                     // and of its row
+    constexpr int TURNS = (GROUPS + 31) / 32;                  // of a lane for each group
     __shared__ uint16_t sc[GROUPS][QZ_ROWS];
     __shared__ uint8_t zp[GROUPS][QZ_ROWS];
     __shared__ uint32_t bufs[QZ_ROWS][8 * 33];
@@ -210,63 +214,68 @@ __global__ void __launch_bounds__(QZ_THREADS, 2) q4_quantize_kernel(const Q4Quan
     const Q4View &q = a.q;
     const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
     const long long n0 = (long long)blockIdx.x * QZ_ROWS, n = n0 + row;
-    const long long k0 = (long long)blockIdx.y * QZ_COLS;
+    const long long k0 = (long long)blockIdx.y * COLS;
     const int es = DT == TC_F32 ? 4 : 2;
     const bool vec = (reinterpret_cast<uintptr_t>(a.W) & 15u) == 0 && (a.ld * es) % 16 == 0;
     if (n < q.N) {
         const uint8_t *src = static_cast<const uint8_t *>(a.W) + n * a.ld * es;
-        const int steps = (int)min((long long)QZ_STEPS, (q.K - k0 + 255) / 256);
-        uint32_t raw[QZ_STEPS][QZ_RAW<DT>];
+        const int steps = (int)min((long long)STEPS, (q.K - k0 + 255) / 256);
+        uint32_t raw[STEPS][QZ_RAW<DT>];
 #pragma unroll
-        for (int i = 0; i < QZ_STEPS; ++i) {
+        for (int i = 0; i < STEPS; ++i) {
 #pragma unroll
             for (int j = 0; j < QZ_RAW<DT>; ++j) raw[i][j] = 0u;
             if (i < steps) load_step<DT>(src, k0 + i * 256, q.K, vec, bufs[row], raw[i]);
         }
-        // lane i PER + j takes group j of step i: its scale, computed once, and
-        // handed back to the group's lanes
-        uint32_t ext[DT == TC_F32 && ZEROS ? 2 : 1] = {};
+        // lane l takes the groups l, l + 32, ... of the row: their scales,
+        // computed once, and handed back to the groups' lanes
+        uint32_t ext[TURNS][DT == TC_F32 && ZEROS ? 2 : 1] = {};
 #pragma unroll
-        for (int i = 0; i < QZ_STEPS; ++i) {
+        for (int i = 0; i < STEPS; ++i) {
             uint32_t x[DT == TC_F32 && ZEROS ? 2 : 1];
             extremes<DT, ZEROS, LOG2>(raw[i], x);
 #pragma unroll
             for (int j = 0; j < (DT == TC_F32 && ZEROS ? 2 : 1); ++j) {
                 const uint32_t y = __shfl_sync(0xffffffffu, x[j], (lane & (PER - 1)) << LOG2);
-                if (lane / PER == i) ext[j] = y;
+                if (lane / PER == i % (32 / PER)) ext[i * PER / 32][j] = y;
             }
         }
-        const QzExtremes e = to_extremes<DT, ZEROS>(ext);
-        float s = ZEROS ? __fdiv_rn(e.pos + e.neg, 15.0f) : __fdiv_rn(e.pos, 7.0f);
-        if (!(e.pos < INFINITY && e.neg < INFINITY)) s = __int_as_float(0x7fc00000);
-        uint16_t bits;
-        if (q.scale_bf16) {
-            bits = __bfloat16_as_ushort(__float2bfloat16_rn(s));
-            s = __bfloat162float(__ushort_as_bfloat16(bits));
-        } else {
-            bits = __half_as_ushort(__float2half_rn(s));
-            s = __half2float(__ushort_as_half(bits));
-        }
-        // a scale of 0 is used as infinity: every quotient is then 0, the code
-        // the zero point 8
-        const float div = s != 0.0f ? s : __int_as_float(0x7f800000);
-        const float inv = DT == TC_F32 ? 0.0f : __fdiv_rn(1.0f, div);
-        int z = 8;
-        if (ZEROS && s != 0.0f) z = (int)fminf(fmaxf(rintf(__fdiv_rn(e.neg, s)), 0.0f), 15.0f);
-        if (lane < GROUPS) {
-            sc[lane][row] = bits;
-            if constexpr (ZEROS) zp[lane][row] = (uint8_t)z;
+        float div[TURNS], inv[TURNS];
+        int z[TURNS];
+#pragma unroll
+        for (int t = 0; t < TURNS; ++t) {
+            const QzExtremes e = to_extremes<DT, ZEROS>(ext[t]);
+            float s = ZEROS ? __fdiv_rn(e.pos + e.neg, 15.0f) : __fdiv_rn(e.pos, 7.0f);
+            if (!(e.pos < INFINITY && e.neg < INFINITY)) s = __int_as_float(0x7fc00000);
+            uint16_t bits;
+            if (q.scale_bf16) {
+                bits = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+                s = __bfloat162float(__ushort_as_bfloat16(bits));
+            } else {
+                bits = __half_as_ushort(__float2half_rn(s));
+                s = __half2float(__ushort_as_half(bits));
+            }
+            // a scale of 0 is used as infinity: every quotient is then 0, the
+            // code the zero point 8
+            div[t] = s != 0.0f ? s : __int_as_float(0x7f800000);
+            inv[t] = DT == TC_F32 ? 0.0f : __fdiv_rn(1.0f, div[t]);
+            z[t] = 8;
+            if (ZEROS && s != 0.0f) z[t] = (int)fminf(fmaxf(rintf(__fdiv_rn(e.neg, s)), 0.0f), 15.0f);
+            if (t * 32 + lane < GROUPS) {
+                sc[t * 32 + lane][row] = bits;
+                if constexpr (ZEROS) zp[t * 32 + lane][row] = (uint8_t)z[t];
+            }
         }
         uint32_t *dst = reinterpret_cast<uint32_t *>(const_cast<uint8_t *>(q.codes) + n * (q.ldw >> 1)) + k0 / 8 + lane;
-        const int words = (int)min((long long)QZ_COLS / 8, ((q.K + 31) / 32 * 32 - k0) / 8) - lane;
+        const int words = (int)min((long long)COLS / 8, ((q.K + 31) / 32 * 32 - k0) / 8) - lane;
 #pragma unroll
-        for (int i = 0; i < QZ_STEPS; ++i) {
+        for (int i = 0; i < STEPS; ++i) {
             if (i >= steps) break;                             // (the whole warp)
-            const int from = i * PER + (lane >> LOG2);
+            const int turn = i * PER / 32, from = (i * PER + (lane >> LOG2)) % 32;
             float v[8];
             to_floats<DT>(raw[i], v);
-            const uint32_t w = q4_word_of<DT == TC_F32>(v, __shfl_sync(0xffffffffu, div, from), __shfl_sync(0xffffffffu, inv, from),
-                                                        ZEROS ? __shfl_sync(0xffffffffu, z, from) : 8);
+            const uint32_t w = q4_word_of<DT == TC_F32>(v, __shfl_sync(0xffffffffu, div[turn], from), __shfl_sync(0xffffffffu, inv[turn], from),
+                                                        ZEROS ? __shfl_sync(0xffffffffu, z[turn], from) : 8);
             if (32 * i < words) dst[32 * i] = w;
         }
     }
@@ -356,11 +365,11 @@ __global__ void __launch_bounds__(QZ_THREADS, 4) q4_dequantize_kernel(const Q4De
     }
 }
 
-// CTAs of 16 rows x 1024 k; grid.y is limited to 65535 (K below 2^26: beyond,
+// CTAs of 16 rows x `cols` k; grid.y is limited to 65535 (K below 2^26: beyond,
 // a row alone would be 33 MB of codes)
-bool qz_grid(const Q4View &q, dim3 *grid)
+bool qz_grid(const Q4View &q, int cols, dim3 *grid)
 {
-    const long long bx = (q.N + QZ_ROWS - 1) / QZ_ROWS, by = (q.K + QZ_COLS - 1) / QZ_COLS;
+    const long long bx = (q.N + QZ_ROWS - 1) / QZ_ROWS, by = (q.K + cols - 1) / cols;
     *grid = dim3((unsigned)bx, (unsigned)by);
     return bx <= 0x7fffffffLL && by <= 65535;
 }
@@ -393,7 +402,7 @@ cudaError_t quantize(const Q4QuantArgs &a, dim3 grid, cudaStream_t st)
 cudaError_t launch_q4_quantize(const Q4QuantArgs &a, cudaStream_t st)
 {
     dim3 grid;
-    if (!qz_grid(a.q, &grid)) return cudaErrorInvalidValue;
+    if (!qz_grid(a.q, a.w_dtype == TC_F32 ? QZ_N<TC_F32> * 256 : QZ_N<TC_BF16> * 256, &grid)) return cudaErrorInvalidValue;
     switch (a.w_dtype) {
     case TC_F16: return quantize<TC_F16>(a, grid, st);
     case TC_BF16: return quantize<TC_BF16>(a, grid, st);
@@ -404,7 +413,7 @@ cudaError_t launch_q4_quantize(const Q4QuantArgs &a, cudaStream_t st)
 cudaError_t launch_q4_dequantize(const Q4DequantArgs &a, cudaStream_t st)
 {
     dim3 grid;
-    if (!qz_grid(a.q, &grid)) return cudaErrorInvalidValue;
+    if (!qz_grid(a.q, QZ_COLS, &grid)) return cudaErrorInvalidValue;
     const int g = log2_of(a.q.group);
     switch (a.v_dtype) {
     case TC_F16: return launch_dependent(q4_dequantize_kernel<TC_F16>, grid, dim3(QZ_THREADS), 0, st, 1u, a, g);
