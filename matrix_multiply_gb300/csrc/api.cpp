@@ -1566,31 +1566,68 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
                                    Q4_ZERO_BOX, gp, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// The tensor-core kernel's tile width and K split: the least estimated time,
-// in cycles -- a 64-k block of a 128 x bn tile takes 2 bn on the tensor core
-// and about 150 to convert; a tile has a fixed part besides.
+// The stream's words that kernels leave at 0: those of the grid barriers,
+// then the counts of the cut tiles of the 4-bit product.
+constexpr size_t SYNC_WORDS = 64;
+tc_status_t ensure_sync(tc_ctx *ctx, tc_stream *s)
+{
+    const size_t bytes = (SYNC_WORDS + (size_t)2 * ctx->num_sms * Q4_MMA_COUNTS) * sizeof(unsigned);
+    if (!s->sync && cudaMallocAsync(reinterpret_cast<void **>(&s->sync), bytes, s->st) != cudaSuccess) {
+        s->sync = nullptr;
+        return TC_ERR_CUDA;
+    }
+    if (!s->sync_clear) {
+        if (cudaMemsetAsync(s->sync, 0, bytes, s->st) != cudaSuccess) return TC_ERR_CUDA;
+        s->sync_clear = true;
+    }
+    return TC_OK;
+}
+
+// The tensor-core kernel's tile width and how its tiles are shared out: the
+// least estimated time, in us beyond a launch's own, from times measured over
+// 17 to 4096 rows of three weights (4096 x 4096 to 11008 x 4096, groups of
+// 128; smaller groups slow all of them alike).  256 k of a tile take 0.8 to
+// 1.07 by its width -- converting the 128 rows of W is the greater part -- and
+// a tile takes 1 besides.  Shared out
+//   whole          in turn: 4096 x 11008 x 4096 330, cut 359
+//   in a cluster   K slices of each tile, where the tiles leave SMs idle: the
+//                  sums on chip take 2 to 7 (100 x 4096 x 4096: 13.3, whole 22)
+//   cut            the last tiles in equal ranges, where the last wave of whole
+//                  ones is short: the sums in memory take 9, and this kernel is
+//                  7% slower per k (200 x 11008 x 4096: 31.3, whole 37.6;
+//                  384 rows: 42.4, whole 40.5)
 void plan_q4_mma(int num_sms, const Q4GemmArgs &a, const Force &f, Q4MmaPlan *p)
 {
-    const int64_t kbs = 2 * cdiv(a.q.K, 128), tn = cdiv(a.q.N, Q4_MMA_ROWS);
+    const int64_t pairs = cdiv(a.q.K, 256), tn = cdiv(a.q.N, Q4_MMA_ROWS);
     double best = 0.0;
     p->bn = 0;
     for (int bn : {128, 96, 64, 32}) {
         if (f.bn > 0 && f.bn != bn) continue;
         const int64_t tm = cdiv(a.M, bn), tiles = tn * tm;
-        int split = f.split > 0 ? std::min(f.split, 8) : (int)std::min<int64_t>(8, num_sms / tiles);
-        split = std::max(1, (int)std::min<int64_t>(split, cdiv(kbs, 4)));
-        if (f.split == 0 && split > 1) split = (int)std::max<int64_t>(1, std::min<int64_t>(split, kbs / 8));
-        const double waves = split > 1 ? 1.0 : (double)cdiv(tiles, num_sms);
-        const double t = waves * ((double)cdiv(kbs, split) * std::max(2.0 * bn, 150.0) + 2500.0 + 10.0 * bn) +
-                         (split > 1 ? 3000.0 : 0.0);
-        if (p->bn == 0 || t < best) {
+        const double pair = bn == 128 ? 1.07 : bn == 96 ? 1.02 : bn == 64 ? 0.92 : 0.8;
+        auto take = [&](double t, int split, int64_t whole, int64_t grid) {
+            if (p->bn != 0 && t >= best) return;
             best = t;
             p->bn = bn;
             p->split = split;
+            p->whole = (int)whole;
             p->tiles_n = (int)tn;
             p->tiles_m = (int)tm;
-            p->grid = split > 1 ? (int)(tiles * split) : (int)std::min<int64_t>(tiles, num_sms);
+            p->grid = (int)grid;
+        };
+        // the tiles beyond whole waves, with one wave's more, in equal ranges
+        const int64_t whole = std::max<int64_t>(tiles / num_sms - 1, 0) * num_sms, cut = (tiles - whole) * pairs;
+        const bool can_cut = bn == 128 && tiles % num_sms != 0 && cut >= num_sms && cut * num_sms <= UINT32_MAX;
+        if (can_cut && f.tail != 0 && f.split == 0) {
+            take((double)cdiv(tiles * pairs, num_sms) * 1.07 * pair + (double)tiles / num_sms + 9.0, 1, whole, num_sms);
+            if (f.tail == 1) continue;
         }
+        int split = f.split > 0 ? std::min(f.split, 8) : (int)std::min<int64_t>(8, num_sms / tiles);
+        split = (int)std::min<int64_t>(split, f.split > 0 ? pairs : pairs / 2);
+        if (split > 1)
+            take((double)cdiv(pairs, split) * pair + 1.0 + bn * (0.03 + 0.05 / split), split, tiles, tiles * split);
+        else
+            take((double)cdiv(tiles, num_sms) * ((double)pairs * pair + 1.0), 1, tiles, std::min<int64_t>(tiles, num_sms));
     }
     if (p->bn == 0) {          // a forced width this kernel does not have
         Force g = f;
@@ -1623,12 +1660,21 @@ tc_status_t enqueue_q4_mma(tc_ctx *ctx, tc_stream *s, Q4GemmArgs a, const Force 
         !encode_q4(ctx, &p.x, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.X, a.q.K, a.M, a.ldx * 2, 64, (uint32_t)p.bn,
                    CU_TENSOR_MAP_SWIZZLE_128B))
         return TC_ERR_CUDA;
+    p.partial = nullptr;
+    p.counts = nullptr;
+    if (p.whole < p.tiles_n * p.tiles_m) {
+        tc_status_t st = ensure_ws(s, (size_t)p.grid * 2 * p.bn * Q4_MMA_ROWS * 4);
+        if (st != TC_OK || (st = ensure_sync(ctx, s)) != TC_OK) return st;
+        p.partial = static_cast<float *>(s->ws);
+        p.counts = s->sync + SYNC_WORDS;
+    }
     p.status = s->status_dev;
     p.timeout_ns = 4000000000ull + (unsigned long long)cdiv(a.q.K, 64) * 20000ull;
     if (launch_q4_mma(a, p, s->st) != cudaSuccess) return TC_ERR_CUDA;
     ctx->launches += launches;
     char buf[64];
-    std::snprintf(buf, sizeof buf, "q4w_tcgen05_128x%d_g%d%s_s%d", p.bn, a.q.group, launches > 1 ? "_pack" : "", p.split);
+    std::snprintf(buf, sizeof buf, "q4w_tcgen05_128x%d_g%d%s_s%d%s", p.bn, a.q.group, launches > 1 ? "_pack" : "", p.split,
+                  p.partial ? "_cut" : "");
     ctx->last = buf;
     return TC_OK;
 }
@@ -1751,14 +1797,7 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     if (a.w2.zeros) enc = enc && encode_q4(ctx, &m.z2, u8, a.w2.zeros, a.w2.N, g2, a.w2.lds, Q4_ZERO_BOX, gp, plain);
     if (!enc) return TC_ERR_CUDA;
     if ((st = ensure_ws(s, lb + hb)) != TC_OK) return st;
-    if (!s->sync && cudaMallocAsync(reinterpret_cast<void **>(&s->sync), 256, s->st) != cudaSuccess) {
-        s->sync = nullptr;
-        return TC_ERR_CUDA;
-    }
-    if (!s->sync_clear) {
-        if (cudaMemsetAsync(s->sync, 0, 256, s->st) != cudaSuccess) return TC_ERR_CUDA;
-        s->sync_clear = true;
-    }
+    if ((st = ensure_sync(ctx, s)) != TC_OK) return st;
     a.logits = static_cast<float *>(s->ws);
     a.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(s->ws) + lb);
     a.sync = s->sync;

@@ -384,10 +384,15 @@ int q4_gemv_max_clusters(int ksplit);
 // The same for more rows of X, on the tcgen05 tensor cores (q4_mma.cu): tiles
 // of 128 rows of W by bn rows of X, bn in {32, 64, 96, 128}; with split > 1
 // the K slices of a tile form a cluster whose sums are added on chip (one
-// unit per CTA).  X is readable by TMA (16-byte base and row pitch).
+// unit per CTA); with bn 128 the last tiles can be cut instead.  X is readable
+// by TMA (16-byte base and row pitch).
 constexpr int Q4_MMA_ROWS = 128;
+constexpr int Q4_MMA_COUNTS = 8;      // promoting warps of a tile
 struct Q4MmaPlan {
     int bn, split, tiles_n, tiles_m, grid;
+    int whole;                 // tiles taken whole; the rest is cut into one equal range per CTA (split 1)
+    float *partial;            // 2 grid tiles of fp32, where whole < tiles
+    unsigned *counts;          // Q4_MMA_COUNTS per tile that is cut, 0 before and after a launch
     CUtensorMap codes, x;      // boxes {128 bytes, 128 rows} and {64 elements, bn rows}, 128-byte swizzle
     unsigned *status;
     unsigned long long timeout_ns;

@@ -13,13 +13,25 @@
 // multiply-add per two sums and group.  Roles, one CTA of 14 warps per SM
 // (14: the register file holds 128 registers for each thread of 16 warps, 96
 // for more):
-//   converters   one or, for narrow tiles, two per 32 rows (on alternate 64-k
-//                blocks: a narrow block's MMAs take less time than converting)
+//   converters   one or, for narrow tiles, two per 32 rows (each one block of
+//                a pair: a narrow block's MMAs take less time than converting)
 //   promoters    one or, for wide tiles, two per 32 rows (half the columns
 //                each: their sums fill the registers); they write C
 //   one warp for the TMA copies, one that issues the MMAs
 // Few tiles: the K slices of a tile form a cluster and add their sums in
-// rank order through distributed shared memory.  Deterministic.
+// rank order through distributed shared memory.  A short last wave: its tiles
+// are cut into equal ranges of K (CUT), whose sums meet in memory; whichever
+// warp comes last adds them in a fixed order.  Deterministic, all of it.
+//
+// What bounds it: the warps that convert.  256 k of a 128 x 128 tile take
+// 1.07 us, twice the tensor core's time for it; of the ~600
+// instructions per 128 k and scheduler two thirds widen codes, one warp's
+// chain of them with the stores to TMEM.  Wider tiles do not fit: the operand's
+// stages and two accumulators fill TMEM, the sums the registers.
+// Measured: 4096 x 11008 x 4096 (M x N x K, bf16, groups of 128 with zero
+// points) 329 us, 1.12 PFLOP/s, 60% of a bf16 product's measured rate;
+// 200 x 11008 x 4096 33 us; 17 x 4096 x 4096 9.3 us.  The plan's figures stand
+// beside its cost model.
 #include "q4.cuh"
 
 #include <atomic>
@@ -81,11 +93,30 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16])
         : "r"(taddr));
 }
 
-// two fp32 multiply-adds
+__device__ __forceinline__ unsigned ld_acquire(const unsigned *p)
+{
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned atom_add_acq_rel(unsigned *p, unsigned v)
+{
+    unsigned old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
+// two fp32 multiply-adds, two additions
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
 {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi)
@@ -114,12 +145,13 @@ __device__ __forceinline__ void store_columns(const Q4GemmArgs &a, long long off
 }
 
 struct QmUnit {
-    int n0, m0, kb0, kb1;
+    int n0, m0, kb0, kb1, tile;
 };
 __device__ __forceinline__ QmUnit qm_unit(int u, int split, int tiles_m, int bn, int num_kb)
 {
     const int tile = split > 1 ? u / split : u, s = u - tile * split;
     QmUnit w;
+    w.tile = tile;
     w.n0 = (tile / tiles_m) * Q4_MMA_ROWS;
     w.m0 = (tile % tiles_m) * bn;
     // slices of whole pairs of blocks, as the codes are copied
@@ -129,10 +161,50 @@ __device__ __forceinline__ QmUnit qm_unit(int u, int split, int tiles_m, int bn,
     return w;
 }
 
-template <bool BF16, int BN, int G>
+// Tiles from `whole` on are laid end to end, in pairs of blocks, and cut into
+// one equal range per CTA (CUT): the pieces of this CTA's range come first,
+// then the whole tiles, in turn.
+struct QmCut {
+    int whole, pairs, first, pieces;               // tiles taken whole; pairs of a tile; the range's tiles
+    unsigned total, lo, hi;                        // pairs of all cut tiles; this CTA's range of them
+
+    __device__ __forceinline__ unsigned bound(unsigned cta) const { return cta * total / gridDim.x; }
+    // the CTA that a pair belongs to
+    __device__ __forceinline__ unsigned owner(unsigned pair) const { return ((pair + 1) * gridDim.x - 1) / total; }
+    __device__ __forceinline__ void init(int whole_, int tiles, int num_kb)
+    {
+        whole = whole_;
+        pairs = (num_kb + 1) / 2;
+        total = (unsigned)((tiles - whole) * pairs);
+        lo = bound(blockIdx.x);
+        hi = bound(blockIdx.x + 1);
+        first = (int)(lo / (unsigned)pairs);
+        pieces = (int)((hi - 1) / (unsigned)pairs) - first + 1;
+        first += whole;
+    }
+    // the CTA's i-th piece
+    __device__ __forceinline__ bool get(int i, int tiles_m, int bn, int num_kb, QmUnit &w) const
+    {
+        int tile = first + i, p0 = 0, p1 = pairs;
+        if (i < pieces) {
+            const unsigned t0 = (unsigned)((tile - whole) * pairs);
+            p0 = (int)(max(lo, t0) - t0);
+            p1 = (int)(min(hi, t0 + pairs) - t0);
+        } else {
+            tile = blockIdx.x + (i - pieces) * gridDim.x;
+            if (tile >= whole) return false;
+        }
+        const int tn = (unsigned)tile / (unsigned)tiles_m;
+        w = QmUnit{tn * Q4_MMA_ROWS, (tile - tn * tiles_m) * bn, 2 * p0, min(num_kb, 2 * p1), tile};
+        return true;
+    }
+};
+
+template <bool BF16, int BN, int G, bool CUT>
 __global__ void __launch_bounds__(QM_THREADS, 1)
     q4_mma_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
-                  int split, int tiles_m, int units, unsigned *status, unsigned long long timeout_ns)
+                  int split, int tiles_m, int units, int whole, float *partial, unsigned *counts, unsigned *status,
+                  unsigned long long timeout_ns)
 {
     constexpr int X_BYTES = BN * 256;              // a block of X: two halves of BN rows x 128 bytes
     constexpr int NG = QM_BK / G;                  // groups per block
@@ -153,12 +225,16 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 2 * QM_XS + 2 * QM_CS + 5);
     volatile uint32_t *abort_flag = slot + 1;
 
+    __shared__ QmCut cut;
+    const int num_kb = (int)((a.q.K + QM_BK - 1) / QM_BK);
+
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < QM_XS; ++i) mbar_init(full + 8 * i, 5), mbar_init(empty + 8 * i, 1);
         for (int i = 0; i < QM_CS; ++i) mbar_init(cfull + 8 * i, 1), mbar_init(cempty + 8 * i, QM_CONV);
         for (int i = 0; i < 2; ++i) mbar_init(dfull + 8 * i, 1), mbar_init(dempty + 8 * i, QM_PROM);
         mbar_init(drain, 1);
+        if (CUT) cut.init(whole, units, num_kb);
         *abort_flag = 0u;
         fence_barrier_init();
         prefetch_tmap(&tmC);
@@ -169,22 +245,30 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     if (warp == 0) tmem_alloc(smem_u32(slot), TMEM_COLS);
     tc_fence_before();
     __syncthreads();
-    if (split > 1) cluster_sync();
+    if (!CUT && split > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *slot;
     griddep_wait();
 
     const Q4Watch watch{abort_flag, status, timeout_ns};
-    const int num_kb = (int)((a.q.K + QM_BK - 1) / QM_BK);
     const int step = split > 1 ? units : (int)gridDim.x;       // a cluster's CTAs take one unit each
     bool ok = true;
+    // the CTA's pieces, one after the other
+    QmUnit w;
+    int u = CUT ? 0 : blockIdx.x;
+    auto next = [&]() {
+        if (CUT) return cut.get(u++, tiles_m, BN, num_kb, w);
+        if (u >= units) return false;
+        w = qm_unit(u, split, tiles_m, BN, num_kb);
+        u += step;
+        return true;
+    };
 
     if (warp == QM_CONV + QM_PROM) {
         // ------------------------------------------------------ TMA copies
         if (lane == 0) {
             int xi = 0, ci = 0;                                 // copies issued
-            for (int u = blockIdx.x; ok && u < units; u += step) {
-                const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+            while (ok && next()) {
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     if ((kb & 1) == 0) {
                         const int st = ci % QM_CS;
@@ -220,8 +304,7 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
         bool ready = false, dready = true;
         const uint64_t bd0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
         auto wait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, q4_wait(bar, parity, watch)); };
-        for (int u = blockIdx.x; ok && u < units; u += step) {
-            const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+        while (ok && next()) {
 #pragma unroll 1
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
                 if (!ready && !(ok = wait(full + 8 * st, ph))) break;
@@ -270,8 +353,7 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
             if (lane == 0) mbar_arrive(pending);
             pending = 0;
         };
-        for (int u = blockIdx.x; ok && u < units; u += step) {
-            const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+        while (ok && next()) {
             const uint8_t *zp = a.q.zeros ? a.q.zeros + min((long long)w.n0 + row, a.q.N - 1) : nullptr;
             // a row's zero points of a pair of blocks, loaded a pair ahead: a use
             // next to its load would wait for it
@@ -345,8 +427,7 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
         const long long ngroups = (a.q.K + G - 1) / G;
         const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + half * HB;
         uint32_t db = 0, dph = 0;                                // accumulator and its phase
-        for (int u = blockIdx.x; ok && u < units; u += step) {
-            const QmUnit w = qm_unit(u, split, tiles_m, BN, num_kb);
+        while (ok && next()) {
             const long long n = w.n0 + row;
             uint64_t acc[HB / 2];
 #pragma unroll
@@ -399,14 +480,68 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                 }
             }
             if (!ok) break;
-            if (split > 1) {
+            if (!CUT && split > 1) {
                 // all of the unit's MMAs have completed: the X ring is idle
                 float *part = reinterpret_cast<float *>(smem);
 #pragma unroll
                 for (int c = 0; c < HB; ++c)
                     part[(half * HB + c) * QM_PART_LD + row] =
                         __uint_as_float(c & 1 ? (uint32_t)(acc[c / 2] >> 32) : (uint32_t)acc[c / 2]);
-            } else if (n < a.q.N) {
+                continue;
+            }
+            bool last = true;
+            if (CUT && w.kb1 - w.kb0 != num_kb) {
+                // A piece of the tile: the sums go to this CTA's place for its
+                // first or its last piece, and whichever warp finds all the
+                // others written adds them up; no warp waits for another.  Of two
+                // pieces the later warp adds the earlier's to its own; more are
+                // added in order of k.
+                const unsigned t0 = (unsigned)((w.tile - whole) * cut.pairs);
+                const unsigned c0 = cut.owner(t0), c1 = cut.owner(t0 + cut.pairs - 1);
+                unsigned *count = counts + (w.tile - whole) * QM_PROM + pw;
+                // this warp's part of a place: four columns at a time, a lane's next to each other
+                const auto place = [&](unsigned cta, bool second) {
+                    return reinterpret_cast<float4 *>(partial) + (size_t)(2 * cta + second) * (BN * Q4_MMA_ROWS / 4) +
+                           pw * (HB * 8) + lane;
+                };
+                unsigned before = 0;
+                if (c1 == c0 + 1) {
+                    if (lane == 0) before = ld_acquire(count);
+                    before = __shfl_sync(0xffffffffu, before, 0);
+                }
+                if (before == 0) {
+                    float4 *mine = place(blockIdx.x, w.tile != cut.first);
+#pragma unroll
+                    for (int c = 0; c < HB / 4; ++c)
+                        __stcg(mine + 32 * c, make_float4(__uint_as_float((uint32_t)acc[2 * c]),
+                                                          __uint_as_float((uint32_t)(acc[2 * c] >> 32)),
+                                                          __uint_as_float((uint32_t)acc[2 * c + 1]),
+                                                          __uint_as_float((uint32_t)(acc[2 * c + 1] >> 32))));
+                    __syncwarp();
+                    if (lane == 0) before = atom_add_acq_rel(count, 1u);
+                    before = __shfl_sync(0xffffffffu, before, 0);
+                }
+                last = before == c1 - c0;
+                if (last) {
+                    if (lane == 0) *count = 0u;                // as the next launch expects it
+                    if (c1 > c0 + 1)
+#pragma unroll
+                        for (int c = 0; c < HB / 2; ++c) acc[c] = 0ull;
+#pragma unroll 1
+                    for (unsigned q = c0; q <= c1; ++q) {
+                        if (c1 == c0 + 1 && q == blockIdx.x) continue;
+                        // the first owner's piece may be its last one; the others' are their first
+                        const float4 *p = place(q, cut.bound(q) < t0);
+#pragma unroll
+                        for (int c = 0; c < HB / 4; ++c) {
+                            const float4 v = __ldcg(p + 32 * c);
+                            acc[2 * c] = add2(acc[2 * c], pack64(__float_as_uint(v.x), __float_as_uint(v.y)));
+                            acc[2 * c + 1] = add2(acc[2 * c + 1], pack64(__float_as_uint(v.z), __float_as_uint(v.w)));
+                        }
+                    }
+                }
+            }
+            if (last && n < a.q.N) {
                 const int cols = min(HB, a.M - w.m0 - half * HB);
                 const long long off = (long long)(w.m0 + half * HB) * a.ldc + n;
                 if (a.c_dtype == TC_F32)
@@ -419,9 +554,9 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (split > 1) {
+    if (!CUT && split > 1) {
         cluster_sync();              // every slice's partial tile is in its CTA's shared memory
-        const QmUnit w = qm_unit(blockIdx.x, split, tiles_m, BN, num_kb);
+        w = qm_unit(blockIdx.x, split, tiles_m, BN, num_kb);
         const int rank = (int)cluster_ctarank();
         const int c0 = rank * BN / split, c1 = (rank + 1) * BN / split;
         const uint32_t base = smem_u32(smem);
@@ -450,10 +585,10 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
     if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-template <bool BF16, int BN, int G>
+template <bool BF16, int BN, int G, bool CUT = false>
 cudaError_t launch_one(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st)
 {
-    constexpr auto kern = q4_mma_kernel<BF16, BN, G>;
+    constexpr auto kern = q4_mma_kernel<BF16, BN, G, CUT>;
     constexpr int smem = qm_smem(BN);
     static std::atomic<bool> configured[64] = {};
     int dev = 0;
@@ -465,12 +600,19 @@ cudaError_t launch_one(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st)
         configured[dev].store(true, std::memory_order_release);
     }
     return launch_dependent(kern, dim3((unsigned)p.grid), dim3(QM_THREADS), smem, st, (unsigned)p.split, a, p.codes, p.x,
-                            p.split, p.tiles_m, p.tiles_n * p.tiles_m * p.split, p.status, p.timeout_ns);
+                            p.split, p.tiles_m, p.tiles_n * p.tiles_m * p.split, p.whole, p.partial, p.counts, p.status,
+                            p.timeout_ns);
 }
 
 template <bool BF16, int BN>
 cudaError_t launch_group(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st)
 {
+    if constexpr (BN == 128)
+        if (p.whole < p.tiles_n * p.tiles_m) switch (a.q.group) {
+            case 32: return launch_one<BF16, BN, 32, true>(a, p, st);
+            case 64: return launch_one<BF16, BN, 64, true>(a, p, st);
+            default: return launch_one<BF16, BN, 128, true>(a, p, st);
+            }
     switch (a.q.group) {
     case 32: return launch_one<BF16, BN, 32>(a, p, st);
     case 64: return launch_one<BF16, BN, 64>(a, p, st);
@@ -484,6 +626,9 @@ cudaError_t launch_q4_mma(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t 
 {
     if (p.split < 1 || p.split > 8 || p.grid < 1 || p.grid % p.split != 0 ||
         (p.split > 1 && p.grid != p.tiles_n * p.tiles_m * p.split))
+        return cudaErrorInvalidValue;
+    const long long cut = (long long)(p.tiles_n * p.tiles_m - p.whole) * ((a.q.K + 255) / 256);
+    if (cut > 0 && (p.bn != 128 || p.split > 1 || cut < p.grid || cut * p.grid > 0xffffffffll || !p.partial || !p.counts))
         return cudaErrorInvalidValue;
     switch (p.bn) {
     case 32: return a.x_bf16 ? launch_group<true, 32>(a, p, st) : launch_group<false, 32>(a, p, st);

@@ -211,6 +211,26 @@ def test_not_finite(ctx, M):
     assert ((out.double() - want).abs() <= unit(K) * T)[clean].all()
 
 
+@pytest.mark.parametrize("M,N,K", [(150, 1300, 9000), (66, 5000, 2900), (290, 6000, 700), (1200, 5000, 400), (130, 130, 40000)])
+def test_cut_tiles(ctx, monkeypatch, M, N, K):
+    """Tiles cut along K where a range of work ends: exact sums, so any cut
+    gives the same bits; then sums that round, the same in every run."""
+    monkeypatch.setenv("TC_FORCE_VARIANT", "bn=128 tail=1")
+    w = Weight(N, K, 64, True, "f16", seed=N, kind="pow2")
+    X = torch.randint(-2, 3, (M, K), generator=torch.Generator().manual_seed(M)).to(torch.bfloat16)
+    out = run(ctx, X.cuda(), w, "f32")
+    assert ctx.last_kernel.endswith("_cut")
+    want = X.double() @ w.values.t()
+    assert float(want.abs().max()) * 4 < 2 ** 24
+    assert torch.equal(out.cpu().double(), want), ctx.last_kernel
+    old = torch.rand(M, N, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    X = torch.randn(M, K, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    q, Xc = w.cuda(tg), X.cuda()
+    outs = [run(ctx, Xc, w, "bf16", 0.75, -0.5, C=old.cuda(), q=q) for _ in range(3)]
+    assert torch.equal(outs[1], outs[0]) and torch.equal(outs[2], outs[0])
+    check(outs[0], X, w, "bf16", 0.75, -0.5, old, ctx.last_kernel)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (4, 4096, 11008), (16, 11008, 4096), (200, 4096, 4096)])
 def test_deterministic_and_async(ctx, M, N, K):
     w = Weight(N, K, 128, True, seed=71)
