@@ -1771,10 +1771,11 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     MoeArgs a;
     tc_status_t st = validate_moe(d, X, R, w1, w2, Y, ids, weights, &a);
     if (st != TC_OK) return st;
-    // scratch: logits and the two parts of h
+    // scratch: logits and the parts of h
     a.ldh = cdiv(a.I, 8) * 8;
+    a.parts = a.y_dtype == TC_F32 ? 3 : 2;
     const size_t lb = round_up((size_t)a.T * a.E * 4, 256);
-    const size_t hb = (size_t)a.T * a.k * (size_t)a.ldh * 2 * 2;
+    const size_t hb = (size_t)a.T * a.k * (size_t)a.ldh * 2 * a.parts;
     MoeMaps m;
     const uint32_t gp = 256 / a.w1.group;
     std::lock_guard<std::mutex> lk(ctx->mu);

@@ -404,6 +404,7 @@ cudaError_t launch_q4_mma(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t 
 struct MoeArgs {
     int T, H, I, E, k;
     int x_bf16, r_dtype, y_dtype, renorm;
+    int parts;             // bf16 parts of h: 2 or 3
     const void *X, *R;
     void *Y;
     long long ldx, ldr, ldy;
@@ -411,7 +412,7 @@ struct MoeArgs {
     int *ids;              // [T, k] or null
     float *p;              // [T, k] or null
     float *logits;         // scratch [T, E]
-    uint16_t *h;           // scratch, bf16: the leading parts [T k, ldh], then the remainders
+    uint16_t *h;           // scratch, bf16: h's leading parts, each [T k, ldh]
     long long ldh;         // I rounded up to 8
     unsigned *sync;        // the grid barrier's word, 0 before the first launch of this grid size that uses it
     unsigned *status;

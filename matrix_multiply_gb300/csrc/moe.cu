@@ -13,9 +13,10 @@
 //      with the tokens' weights in shared memory, per warp in a fixed order
 // The codes go through a TMA ring per warp; its copies run ahead across the
 // second barrier, since which weights stage 2 reads does not depend on h.  h
-// is kept as two bf16 parts, h = hi + lo (16 bits of significand, any
-// exponent), multiplied one after the other.  Deterministic: lists in index
-// order, sums in fixed orders.
+// is kept as a sum of bf16 parts, multiplied one after the other: two of them
+// (16 bits of significand, any exponent) where y has 16 bits, 11 of them
+// significant at most; three (all 24 bits) where y is fp32.  Deterministic:
+// lists in index order, sums in fixed orders.
 #include "q4.cuh"
 
 #include <atomic>
@@ -259,7 +260,7 @@ __device__ __forceinline__ void moe_list(const MoeArgs &a, MoeLists &L)
     }
 }
 
-template <bool BF16, bool SBF16, int G>
+template <bool BF16, bool SBF16, int G, int PARTS>
 __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, const __grid_constant__ MoeMaps maps)
 {
     constexpr int GP = Q4_SLAB / G, S = MO_STAGES;
@@ -478,21 +479,23 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                 if (!in) continue;
                 const int i0 = (int)(u - (unsigned)ue * nb) * 8 + r + 2 * half;
                 uint16_t *h = a.h + L.pair[L.ent_at[ue] + c] * a.ldh + i0;
-                uint16_t hi[2], lo[2];
+                uint32_t part[PARTS] = {};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float gt = half ? v[2 + i] : v[i], up = half ? v[6 + i] : v[4 + i];
-                    const float x = gt / (1.0f + expf(-gt)) * up;
-                    const __nv_bfloat16 b = __float2bfloat16_rn(x);
-                    const float rest = x - __bfloat162float(b);
-                    hi[i] = __bfloat16_as_ushort(b);
-                    // (an infinity or a NaN stands in the first part alone)
-                    lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(isfinite(rest) ? rest : 0.0f));
-                    if (i0 + i >= a.I) hi[i] = lo[i] = 0;
+                    float x = i0 + i < a.I ? gt / (1.0f + expf(-gt)) * up : 0.0f;
+#pragma unroll
+                    for (int q = 0; q < PARTS; ++q) {
+                        const __nv_bfloat16 b = __float2bfloat16_rn(x);
+                        part[q] |= (uint32_t)__bfloat16_as_ushort(b) << (16 * i);
+                        x -= __bfloat162float(b);
+                        if (!isfinite(x)) x = 0.0f;            // an infinity or a NaN stands in the first part alone
+                    }
                 }
                 // (ldh is I rounded up to 8, so both elements are in the row)
-                *reinterpret_cast<uint32_t *>(h) = hi[0] | (uint32_t)hi[1] << 16;
-                *reinterpret_cast<uint32_t *>(h + (long long)a.T * a.k * a.ldh) = lo[0] | (uint32_t)lo[1] << 16;
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q)
+                    *reinterpret_cast<uint32_t *>(h + (long long)q * a.T * a.k * a.ldh) = part[q];
             }
             q4_group_sync(wr, wk_n);          // the tiles are read before the next ones are written
         }
@@ -508,11 +511,11 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         const int p_hi = min(r_hi, panel + MO_PANEL);
         for (int i = warp; i < slabs2; i += MO_WARPS) {
             const int ent = (int)((unsigned)i / (unsigned)ns2), slab = i - ent * ns2, n = L.ent_n[ent], at = L.ent_at[ent];
-            uint32_t xf[2][8][4];
+            uint32_t xf[PARTS][8][4];
             {
                 const uint16_t *row = a.h + (long long)(g < n ? L.pair[at + g] : 0) * a.ldh;
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+                for (int q = 0; q < PARTS; ++q)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int k = slab * Q4_SLAB + 32 * j + 8 * t;
@@ -541,7 +544,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                 b.s1 = b.s0 + 8;
                 b.z0 = zeros2 ? st + MO_ZERO_AT + (ra & 15) + g : nullptr;
                 b.z1 = b.z0 + 8;
-                q4_slab<true, SBF16, 2, G, Q4_SCALE_BOX, true>(acc, b, xf);
+                q4_slab<true, SBF16, PARTS, G, Q4_SCALE_BOX, true>(acc, b, xf);
                 release();
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
@@ -575,10 +578,10 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         }
 }
 
-template <bool BF16, bool SBF16, int G>
+template <bool BF16, bool SBF16, int G, int PARTS>
 cudaError_t launch_one(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_t st)
 {
-    constexpr auto kern = moe_kernel<BF16, SBF16, G>;
+    constexpr auto kern = moe_kernel<BF16, SBF16, G, PARTS>;
     static std::atomic<bool> configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -601,13 +604,20 @@ cudaError_t launch_one(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_
     return cudaLaunchKernelEx(&cfg, kern, a, m);
 }
 
+template <bool BF16, bool SBF16, int G>
+cudaError_t launch_parts(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_t st)
+{
+    return a.parts == 3 ? launch_one<BF16, SBF16, G, 3>(a, m, grid, st)
+                                     : launch_one<BF16, SBF16, G, 2>(a, m, grid, st);
+}
+
 template <bool BF16, bool SBF16>
 cudaError_t launch_group(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_t st)
 {
     switch (a.w1.group) {
-    case 32: return launch_one<BF16, SBF16, 32>(a, m, grid, st);
-    case 64: return launch_one<BF16, SBF16, 64>(a, m, grid, st);
-    default: return launch_one<BF16, SBF16, 128>(a, m, grid, st);
+    case 32: return launch_parts<BF16, SBF16, 32>(a, m, grid, st);
+    case 64: return launch_parts<BF16, SBF16, 64>(a, m, grid, st);
+    default: return launch_parts<BF16, SBF16, 128>(a, m, grid, st);
     }
 }
 

@@ -82,6 +82,24 @@ def test_long_axes(ctx, shape):
     check(*out, X, R, w1, w2, I, k, "f32", True, f"{shape}")
 
 
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+def test_fp32_outputs_keep_24_bits(ctx, x):
+    """One expert, one column of inter, one element of x per token: nothing is
+    summed, so a factor's error is an output's.  Fewer than 16 roundings of
+    2^-24 (scales, the exponential's two units, the sigmoid, the products)."""
+    T, H = 32, 64
+    g = torch.Generator().manual_seed(5)
+    X = torch.zeros(T, H, dtype=DT[x])
+    X[torch.arange(T), torch.randperm(H, generator=g)[:T]] = (torch.rand(T, generator=g) * 3 + 1).to(DT[x])
+    w1, w2 = Weight(2, H, 32, False, "f16", 6), Weight(H, 1, 32, False, "f16", 7)
+    R = torch.ones(1, H)
+    Y, ids, p = layer(ctx, X.cuda(), R.cuda(), w1, w2, 1, 1, 1, "f32")
+    gate, up = (X.double() @ w1.values.t()).unbind(1)
+    want = (gate / (1 + torch.exp(-gate)) * up)[:, None] * w2.values[:, 0]
+    within(Y.cpu(), want, 2.0 ** -20 * want.abs())
+    assert bool((want != 0).any()) and p.cpu().tolist() == [[1.0]] * T
+
+
 def test_ties_go_to_the_lowest_index(ctx):
     T, H, I, E, k = 3, 64, 32, 70, 5
     X, R, w1, w2 = problem(T, H, I, E, k)
