@@ -304,7 +304,10 @@ tc_status_t tc_q4_validate(const tc_q4_weight *q, tc_dtype_t dtype, int32_t ld, 
  * and leading dimension; C overlaps none of the inputs.  The products of X
  * with the whole numbers code - zero are exact and summed in fp32 within a
  * group, the groups' sums times their scales are summed in fp32: no weight
- * is rounded to 16 bits on the way.  Deterministic run to run. */
+ * is rounded to 16 bits on the way.  Deterministic run to run.  Calls of more
+ * than 16 rows may take workspace from the stream, enlarged when a call needs
+ * more than any before it: make the largest call once before a stream
+ * capture. */
 tc_status_t tc_gemm_q4_weight(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C);
 tc_status_t tc_gemm_q4_weight_async(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X,
                                     void *C, tc_stream *s);
@@ -327,12 +330,13 @@ tc_status_t tc_gemm_q4_weight_validate(const tc_gemm_desc *d, const tc_q4_weight
  * otherwise) and scale_dtype (TC_ERR_DTYPE).  ids (int32 [tokens, top_k]) and weights
  * (float [tokens, top_k]) receive the chosen experts and their p_j, in
  * descending order of l; either may be NULL.  silu(x) = x / (1 + exp(-x)).
- * h is kept to 16 bits of significand and more (never rounded to 16-bit
- * floats), sums are fp32, Y is rounded once.  1 <= tokens <=
+ * h keeps 16 bits of its significand, all 24 where y_dtype is TC_F32, with
+ * fp32's exponents; sums are fp32, Y is rounded once.  1 <= tokens <=
  * TC_MOE_MAX_TOKENS, 1 <= top_k <= min(experts, TC_MOE_MAX_TOPK), experts <=
  * TC_MOE_MAX_EXPERTS (TC_ERR_DIM otherwise, and when the weights' N and K do
  * not fit); Y, ids and weights overlap no input and one another
- * (TC_ERR_OVERLAP).  Deterministic run to run. */
+ * (TC_ERR_OVERLAP).  Deterministic run to run.  Takes workspace from the
+ * stream: make one call before a stream capture. */
 #define TC_MOE_MAX_TOKENS 32
 #define TC_MOE_MAX_EXPERTS 512
 #define TC_MOE_MAX_TOPK 16

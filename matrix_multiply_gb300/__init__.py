@@ -15,6 +15,10 @@ view of too few elements is refused, nothing is launched).  ``GroupedGemm``
 and ``PreparedGemm`` run those checks once for a group or a single product
 that is issued many times; each ``enqueue()`` is then one C call.
 
+``Q4Weight`` holds a 4-bit weight with group scales: ``tc_quantize_q4`` fills
+one, ``tc_gemm_q4_weight`` (or ``PreparedGemm``) multiplies by it, and
+``tc_moe_q4`` (or ``PreparedMoe``) runs a mixture-of-experts layer over two.
+
 There is no fallback: if the library is missing, importing this package
 raises.  Build it with ``python -c "import __graft_entry__ as g; g.build()"``.
 """

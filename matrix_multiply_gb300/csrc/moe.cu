@@ -17,6 +17,15 @@
 // (16 bits of significand, any exponent) where y has 16 bits, 11 of them
 // significant at most; three (all 24 bits) where y is fp32.  Deterministic:
 // lists in index order, sums in fixed orders.
+//
+// Measured: 1 token, hidden 2048, inter 768, 8 of 64 experts, groups of 128:
+// 18.2 us for 19.7 MB, of which the launch takes 3.1, each stage's dependent
+// loads, barriers and first passes through its code the rest.  16 tokens,
+// hidden 4096, inter 1408, 8 of 64, groups of 64 with zero points: 182 us for
+// about 530 MB, 43% of a plain copy's rate, bound by issue and the fixed
+// latencies of the widening chain (570 instructions per 16 rows x 256 k;
+// schedulers issue in 61% of the cycles).  As separate launches the stages
+// would add two of them, with their drains, to every call.
 #include "q4.cuh"
 
 #include <atomic>

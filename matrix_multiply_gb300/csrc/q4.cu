@@ -1,12 +1,19 @@
 // 4-bit weights with group scales: quantising and giving the values back.
 //
-// Both are bound by HBM: quantising 16-bit weights reads 2 bytes and writes
-// half a byte (and the scales) per weight.  A CTA takes 16 rows x 1024 k, a
-// warp a row, a lane eight consecutive k at a time -- one word of codes, one
-// 16-byte load -- so codes and weights move in whole lines; a group is 4, 8
-// or 16 neighbouring lanes, its extremes a few shuffles.  Scales lie n-major
-// beside each other: the 16 rows' scales meet in shared memory and leave as
-// 32-byte pieces.
+// Quantising 16-bit weights reads 2 bytes and writes half a byte (and the
+// scales) per weight, and back.  A CTA takes 16 rows, a warp a row, a lane
+// eight consecutive k at a time -- one word of codes, one 16-byte load -- so
+// codes and weights move in whole lines; a group is 4, 8 or 16 neighbouring
+// lanes, its extremes a few shuffles, its scale worked out by one of them.
+// Scales lie n-major beside each other: the 16 rows' scales meet in shared
+// memory and leave as 32-byte pieces.
+//
+// What bounds it: reading back, HBM; quantising, issue -- 154 instructions for
+// a warp's 256 weights, most of them the exact ties of the rounding.
+// Measured, quantising and reading back together: 65536 x 4096 f16, groups of
+// 64 with zero points, 288 us for 1.37 GB, 70% of a plain copy's rate (162 and
+// 139 us, 4.1 and 4.9 TB/s, under the profiler); 4096 x 4096 bf16 24 us;
+// 1001 x 2999 fp32 with padded rows 15 us.
 #include "q4.cuh"
 
 namespace tc {
@@ -14,7 +21,8 @@ namespace {
 
 constexpr int QZ_ROWS = 16, QZ_THREADS = QZ_ROWS * 32;
 constexpr int QZ_STEPS = 4, QZ_COLS = QZ_STEPS * 256;      // k of a CTA (dequantising)
-// k steps of a warp when quantising: as many as its registers hold
+// k steps of a warp when quantising: as many as its registers hold (four for
+// 16-bit weights: 65536 x 4096 both ways 348 us for 288)
 template <int DT>
 constexpr int QZ_N = DT == TC_F32 ? 4 : 8;
 

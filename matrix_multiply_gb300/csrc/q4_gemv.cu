@@ -4,17 +4,33 @@
 //   * A persistent CTA per SM owns a range of W's rows, equal to one row
 //     between CTAs, cut into blocks of at most 16 rows.  Its 16 warps divide
 //     K: a warp takes the same 256 k (a slab) of every block, so its share of
-//     X stays in registers for the whole kernel.  When K has fewer than 9
-//     slabs, several groups of warps take different blocks.
+//     X stays in registers for the whole kernel.  When K has at most 8
+//     slabs, several groups of warps take different blocks; when it has more
+//     than 16, a warp has several slabs and reads its share of X once per six
+//     (three, for more than 8 rows of X) blocks.
 //   * Each warp streams its slabs through a ring of its own in shared
 //     memory, filled by TMA (codes, scales, zero points of a block's slab),
 //     several pieces ahead; nothing is shared with other warps until, every
 //     few blocks, the warps' sums of those blocks are added in a fixed order.
-//   * K above 4096 is split over a cluster of CTAs, whose sums are added in
-//     rank order through distributed shared memory.
+//   * When N leaves fewer than 16 rows to a CTA, K above 4096 is split over a
+//     cluster of CTAs, whose sums are added in rank order through distributed
+//     shared memory.
 //   * The multiply-adds run on mma.sync m16n8k16 with W as the 16-row
 //     operand (see q4_slab).
 // Fixed orders everywhere: the result is deterministic.
+//
+// Measured (M x N x K, X and C in 16 bits but where said), with the share of
+// a plain copy's rate that the bytes come to:
+//   1 x 4096 x 4096, groups of 128              4.5 us   28%
+//   4 x 4096 x 11008, of 64 with zero points    9.9 us   37%
+//   16 x 11008 x 4096, of 32, C in fp32        12.7 us   30%
+// An empty launch takes 3.1; after it the kernel is bound by the issue of the
+// widening and its bookkeeping (about 390 instructions per 16 rows x 256 k and
+// warp, 230 of them in q4_slab for groups of 128; schedulers issue in half of
+// the cycles, 16 warps being what the registers hold), not by HBM.  mma.sync
+// rather than tcgen05: with at most 16 columns the tensor cores are idle
+// either way, and W goes from the ring to the operand's registers without a
+// second pass through shared memory or TMEM.
 #include "q4.cuh"
 
 #include <atomic>
