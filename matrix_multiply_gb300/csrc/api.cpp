@@ -1536,7 +1536,10 @@ bool encode_q4(tc_ctx *ctx, CUtensorMap *m, CUtensorMapDataType t, const void *b
 // be shorter than a block of 16 rows, a cluster of ksplit CTAs.  Measured on
 // GB300, microseconds unsplit and split: 4 x 4096 x 11008 (27 rows a range)
 // 10.1 and 11.4; 1 x 1024 x 8192 (7 rows) 4.8 and 4.3; 1 x 512 x 11008 (4
-// rows) 5.6 and 4.2.
+// rows) 5.6 and 4.2.  Blocks of 32 rows where a range has them, all warps
+// divide K and X has one tile of columns; of 32 and of 16: 4 x 4096 x 11008
+// 8.9 and 9.9, 1 x 11008 x 4096 7.0 and 7.8, but 16 x 20000 x 4096, whose
+// sums fill what the ring leaves of shared memory, 22.8 and 20.9.
 bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f, Q4GemvPlan *p)
 {
     const int64_t slabs = cdiv(a.q.K, 256);
@@ -1549,21 +1552,28 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
     const int most = f.gemv_grid > 0 ? f.gemv_grid : fit;
     p->rows = (int)cdiv(a.q.N, std::min<int64_t>(a.q.N, most));
     p->clusters = (int)cdiv(a.q.N, p->rows);
-    p->nblk = (int)cdiv(p->rows, 16);
-    p->block_rows = (int)cdiv(p->rows, p->nblk);
+    p->tall = a.M <= 8 && p->ksplit == 1 && slabs > 8 && p->rows > 16 ? 2 : 1;
+    p->nblk = (int)cdiv(p->rows, 16 * p->tall);
+    p->block_rows = p->tall > 1 ? std::min(p->rows, 32) : (int)cdiv(p->rows, p->nblk);
     p->nblk = (int)cdiv(p->rows, p->block_rows);
+    p->tail_rows = p->tall > 1 ? p->rows - (p->nblk - 1) * p->block_rows : p->block_rows;
     p->status = s->status_dev;
     p->timeout_ns = 4000000000ull;
     const int64_t groups = cdiv(a.q.K, a.q.group);
     const uint32_t gp = 256 / a.q.group;
     if (!encode_q4(ctx, &p->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.codes, cdiv(a.q.K, 8) * 4, a.q.N, a.q.ldw / 2, 128,
                    (uint32_t)p->block_rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_q4(ctx, &p->scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.q.scales, a.q.N, groups, a.q.lds * 2, Q4_SCALE_BOX,
-                   gp, CU_TENSOR_MAP_SWIZZLE_NONE))
+        !encode_q4(ctx, &p->scales, CU_TENSOR_MAP_DATA_TYPE_UINT16, a.q.scales, a.q.N, groups, a.q.lds * 2,
+                   8 + 16 * p->tall, gp, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return false;
+    p->tail = p->codes;
+    if (p->tail_rows < p->block_rows &&
+        !encode_q4(ctx, &p->tail, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.codes, cdiv(a.q.K, 8) * 4, a.q.N, a.q.ldw / 2, 128,
+                   (uint32_t)p->tail_rows, CU_TENSOR_MAP_SWIZZLE_128B))
         return false;
     p->zeros = p->scales;
     return !a.q.zeros || encode_q4(ctx, &p->zeros, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.zeros, a.q.N, groups, a.q.lds,
-                                   Q4_ZERO_BOX, gp, CU_TENSOR_MAP_SWIZZLE_NONE);
+                                   16 + 16 * p->tall, gp, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 // The stream's words that kernels leave at 0: those of the grid barriers,

@@ -364,18 +364,19 @@ struct Q4GemmArgs {
 
 // For at most Q4_GEMV_MAX_ROWS rows of X, streaming W (q4_gemv.cu).
 // The grid is `clusters` clusters of ksplit CTAs; cluster c owns the rows
-// [c * rows, (c + 1) * rows) of W, in nblk blocks of block_rows <= 16 rows,
+// [c * rows, (c + 1) * rows) of W, in nblk blocks of block_rows <= 16 tall rows
+// (tall 1 or 2; the last of a tall 2 range has tail_rows),
 // and its CTA of rank r the slabs [r n / ksplit, (r + 1) n / ksplit) of the
 // n = ceil(K / 256) slabs of 256 k.
 constexpr int Q4_GEMV_MAX_ROWS = 16;
 struct Q4GemvPlan {
-    int clusters, ksplit, rows, nblk, block_rows;
-    CUtensorMap codes, scales, zeros;
+    int clusters, ksplit, rows, nblk, block_rows, tall, tail_rows;
+    CUtensorMap codes, tail, scales, zeros;
     unsigned *status;
     unsigned long long timeout_ns;
 };
-// boxes of the three maps: {128 bytes, block_rows} with the 128-byte swizzle,
-// {24 scales, 256 / group}, {32 zeros, 256 / group}
+// boxes of the maps: {128 bytes, block_rows (tail_rows)} with the 128-byte
+// swizzle, {8 + 16 tall scales, 256 / group}, {16 + 16 tall zeros, 256 / group}
 constexpr int Q4_SCALE_BOX = 24, Q4_ZERO_BOX = 32;
 cudaError_t launch_q4_gemv(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st);
 // clusters of ksplit CTAs of that kernel resident at once (0: none)

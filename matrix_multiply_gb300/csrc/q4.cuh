@@ -112,9 +112,9 @@ __device__ __forceinline__ uint32_t q4_first_word(int g, int t) { return g * 128
 // Each group's products are summed from zero by the tensor core -- whole
 // numbers times 16-bit floats, exact, added in fp32 -- and join the
 // accumulator times the row's scale.  JOIN: the NT operands are the parts of
-// one (x = part 0 + part 1), their sums join acc[0].  SP: elements between
-// two groups' scales.  Every lane of the warp calls it.
-template <bool BF16, bool SBF16, int NT, int G, int SP, bool JOIN = false>
+// one (x = part 0 + part 1), their sums join acc[0].  SP, ZP: elements between
+// two groups' scales and zero points.  Every lane of the warp calls it.
+template <bool BF16, bool SBF16, int NT, int G, int SP, bool JOIN = false, int ZP = Q4_ZERO_PITCH>
 __device__ __forceinline__ void q4_slab(float (&acc)[JOIN ? 1 : NT][4], const Q4Slab &b, const uint32_t (&xf)[NT][8][4])
 {
     constexpr int STEPS = G / 32;                  // 32-k steps per group
@@ -122,8 +122,8 @@ __device__ __forceinline__ void q4_slab(float (&acc)[JOIN ? 1 : NT][4], const Q4
     for (int gr = 0; gr < Q4_SLAB / G; ++gr) {
         Q4Zero z0 = q4_zero_form<BF16>(8u), z1 = z0;
         if (b.z0) {
-            z0 = q4_zero_form<BF16>((uint32_t)b.z0[gr * Q4_ZERO_PITCH] & 15u);
-            z1 = q4_zero_form<BF16>((uint32_t)b.z1[gr * Q4_ZERO_PITCH] & 15u);
+            z0 = q4_zero_form<BF16>((uint32_t)b.z0[gr * ZP] & 15u);
+            z1 = q4_zero_form<BF16>((uint32_t)b.z1[gr * ZP] & 15u);
         }
         const float s0 = q4_scale_bits<SBF16>(b.s0[gr * SP]);
         const float s1 = q4_scale_bits<SBF16>(b.s1[gr * SP]);

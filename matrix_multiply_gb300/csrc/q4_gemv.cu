@@ -2,12 +2,12 @@
 // beta C.  Every code is read once, so HBM bounds it; the kernel is built
 // around that stream.
 //   * A persistent CTA per SM owns a range of W's rows, equal to one row
-//     between CTAs, cut into blocks of at most 16 rows.  Its 16 warps divide
-//     K: a warp takes the same 256 k (a slab) of every block, so its share of
-//     X stays in registers for the whole kernel.  When K has at most 8
-//     slabs, several groups of warps take different blocks; when it has more
-//     than 16, a warp has several slabs and reads its share of X once per six
-//     (three, for more than 8 rows of X) blocks.
+//     between CTAs, cut into blocks of at most 16 rows, or 32 (MT 2).  Its 16
+//     warps divide K: a warp takes the same 256 k (a slab) of every block, so
+//     its share of X stays in registers for the whole kernel.  When K has at
+//     most 8 slabs, several groups of warps take different blocks; when it has
+//     more than 16, a warp has several slabs and reads its share of X once per
+//     six blocks of 16 rows (three, for more than 8 rows of X).
 //   * Each warp streams its slabs through a ring of its own in shared
 //     memory, filled by TMA (codes, scales, zero points of a block's slab),
 //     several pieces ahead; nothing is shared with other warps until, every
@@ -21,13 +21,14 @@
 //
 // Measured (M x N x K, X and C in 16 bits but where said), with the share of
 // a plain copy's rate that the bytes come to:
-//   1 x 4096 x 4096, groups of 128              4.5 us   28%
-//   4 x 4096 x 11008, of 64 with zero points    9.9 us   37%
+//   1 x 4096 x 4096, groups of 128              4.4 us   29%
+//   4 x 4096 x 11008, of 64 with zero points    8.9 us   41%
 //   16 x 11008 x 4096, of 32, C in fp32        12.7 us   30%
 // An empty launch takes 3.1; after it the kernel is bound by the issue of the
-// widening and its bookkeeping (about 390 instructions per 16 rows x 256 k and
-// warp, 230 of them in q4_slab for groups of 128; schedulers issue in half of
-// the cycles, 16 warps being what the registers hold), not by HBM.  mma.sync
+// widening and its bookkeeping (about 230 instructions per 16 rows x 256 k in
+// q4_slab for groups of 128, and 130 for each piece of the ring; schedulers
+// issue in half of the cycles, 16 warps being what the registers hold), not by
+// HBM.  mma.sync
 // rather than tcgen05: with at most 16 columns the tensor cores are idle
 // either way, and W goes from the ring to the operand's registers without a
 // second pass through shared memory or TMEM.
@@ -39,40 +40,51 @@ namespace tc {
 namespace {
 
 constexpr int GV_WARPS = 16;
-constexpr int GV_STAGES = 3;
-constexpr int GV_SCALE_AT = 2048, GV_ZERO_AT = GV_SCALE_AT + 8 * Q4_SCALE_PITCH;
-constexpr int GV_STAGE_BYTES = 3072;       // codes, scales, zero points; a multiple of the swizzle's 1024
-static_assert(GV_ZERO_AT % 128 == 0 && GV_ZERO_AT + 8 * Q4_ZERO_PITCH <= GV_STAGE_BYTES, "stage layout");
-constexpr int GV_RING = GV_WARPS * GV_STAGES * GV_STAGE_BYTES;
+// A stage of a warp's ring: codes, scales, zero points of a block of MT
+// operands of 16 rows
+template <int MT>
+struct GvStage {
+    static constexpr int STAGES = MT == 1 ? 3 : 2;
+    static constexpr int SCALE_BOX = 8 + 16 * MT, ZERO_BOX = 16 + 16 * MT;
+    static constexpr int SCALE_AT = 2048 * MT, ZERO_AT = SCALE_AT + 8 * 2 * SCALE_BOX;
+    static constexpr int BYTES = MT == 1 ? 3072 : 5120;        // a multiple of the swizzle's 1024
+    static_assert(ZERO_AT % 128 == 0 && ZERO_AT + 8 * ZERO_BOX <= BYTES && BYTES % 1024 == 0, "stage layout");
+};
+static_assert(GvStage<1>::SCALE_BOX == Q4_SCALE_BOX && GvStage<1>::ZERO_BOX == Q4_ZERO_BOX, "boxes");
+template <int MT>
+constexpr int GV_RING = GV_WARPS * GvStage<MT>::STAGES * GvStage<MT>::BYTES;
 constexpr int GV_TILE_LD = 20;             // floats between X rows of a 16-row partial tile: conflict-free both ways
 
 // blocks whose partial tiles are held before they are added up
-template <int NT>
-__host__ __device__ constexpr int gv_hold() { return NT == 1 ? 6 : 3; }
+template <int NT, int MT>
+__host__ __device__ constexpr int gv_hold() { return (NT == 1 ? 6 : 3) / MT; }
 template <int NT>
 __host__ __device__ constexpr int gv_tile() { return NT * 8 * GV_TILE_LD; }       // floats
-template <int NT>
+template <int NT, int MT>
 __host__ __device__ constexpr int gv_smem()
 {
-    return 1024 + GV_RING + (GV_WARPS + 1) * gv_hold<NT>() * gv_tile<NT>() * 4 + GV_WARPS * GV_STAGES * 8;
+    return 1024 + GV_RING<MT> + (GV_WARPS + 1) * gv_hold<NT, MT>() * MT * gv_tile<NT>() * 4 +
+           GV_WARPS * GvStage<MT>::STAGES * 8;
 }
-static_assert(gv_smem<1>() <= SMEM_LIMIT && gv_smem<2>() <= SMEM_LIMIT, "one CTA per SM");
+static_assert(gv_smem<1, 1>() <= SMEM_LIMIT && gv_smem<2, 1>() <= SMEM_LIMIT && gv_smem<1, 2>() <= SMEM_LIMIT,
+              "one CTA per SM");
 
-template <bool BF16, bool SBF16, int NT, int G>
+template <bool BF16, bool SBF16, int NT, int G, int MT>
 __global__ void __launch_bounds__(GV_WARPS * 32, 1)
-    q4_gemv_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmS,
-                   const __grid_constant__ CUtensorMap tmZ, int ksplit, int rows, int nblk, int block_rows,
-                   unsigned *status, unsigned long long timeout_ns)
+    q4_gemv_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmT,
+                   const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmZ, int ksplit, int rows,
+                   int nblk, int block_rows, int tail_rows, unsigned *status, unsigned long long timeout_ns)
 {
     constexpr int GP = Q4_SLAB / G;                // groups per slab
     constexpr int TILE = gv_tile<NT>();
-    constexpr int HOLD = gv_hold<NT>();
-    constexpr int S = GV_STAGES;
+    constexpr int HOLD = gv_hold<NT, MT>();
+    using Stage = GvStage<MT>;
+    constexpr int S = Stage::STAGES;
     extern __shared__ uint8_t raw[];
     uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    float *tiles = reinterpret_cast<float *>(ring + GV_RING);          // [HOLD][GV_WARPS][TILE]
-    float *sums = tiles + GV_WARPS * HOLD * TILE;                      // [HOLD][TILE], for the cluster
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sums + HOLD * TILE);
+    float *tiles = reinterpret_cast<float *>(ring + GV_RING<MT>);      // [HOLD * MT][GV_WARPS][TILE]
+    float *sums = tiles + GV_WARPS * HOLD * MT * TILE;                 // [HOLD * MT][TILE], for the cluster
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sums + HOLD * MT * TILE);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int K = (int)a.q.K;
@@ -98,7 +110,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     const long long r_lo = (long long)cluster * rows;
     const int nrows = (int)min((long long)rows, a.q.N - r_lo);
 
-    const uint32_t my_ring = smem_u32(ring) + warp * (S * GV_STAGE_BYTES);
+    const uint32_t my_ring = smem_u32(ring) + warp * (S * Stage::BYTES);
     const uint32_t my_bar = smem_u32(bars + warp * S);
     const bool zeros = a.q.zeros != nullptr;
     if (lane == 0) {
@@ -114,7 +126,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
 
     // the warp's pieces, fetched in order
     const uint32_t leader = elect_one();
-    const uint32_t bytes = block_rows * 128 + GP * (Q4_SCALE_PITCH + (zeros ? Q4_ZERO_PITCH : 0));
+    const uint32_t beside = GP * (2 * Stage::SCALE_BOX + (zeros ? Stage::ZERO_BOX : 0));
     // blocks with rows in them
     const int have = nrows == rows ? nblk : (int)((unsigned)(nrows - 1) / (unsigned)block_rows) + 1;
     int f_first = wr, f_h = 0, f_s = 0, fetched = 0;
@@ -122,14 +134,15 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     // the order of the pieces: HOLD blocks at a time, of these slab by slab
     auto fetch = [&]() {                           // the whole warp
         if (f_first >= have || per == 0) return;
-        const int row = (int)r_lo + (f_first + f_h * wr_n) * block_rows, slab = s_lo + wk + f_s * GV_WARPS;
-        const uint32_t st = my_ring + f_at, bar = my_bar + f_at / (GV_STAGE_BYTES / 8);
-        arrive_expect_by(bar, bytes, leader);
-        tma_load_2d_by(st, &tmC, bar, slab * (Q4_SLAB / 2), row, leader);
-        tma_load_2d_by(st + GV_SCALE_AT, &tmS, bar, row & ~7, slab * GP, leader);
-        if (zeros) tma_load_2d_by(st + GV_ZERO_AT, &tmZ, bar, row & ~15, slab * GP, leader);
+        const int blk = f_first + f_h * wr_n, row = (int)r_lo + blk * block_rows, slab = s_lo + wk + f_s * GV_WARPS;
+        const uint32_t st = my_ring + f_at, bar = my_bar + f_at / (Stage::BYTES / 8);
+        const bool tail = MT > 1 && blk == nblk - 1;
+        arrive_expect_by(bar, (tail ? tail_rows : block_rows) * 128 + beside, leader);
+        tma_load_2d_by(st, tail ? &tmT : &tmC, bar, slab * (Q4_SLAB / 2), row, leader);
+        tma_load_2d_by(st + Stage::SCALE_AT, &tmS, bar, row & ~7, slab * GP, leader);
+        if (zeros) tma_load_2d_by(st + Stage::ZERO_AT, &tmZ, bar, row & ~15, slab * GP, leader);
         ++fetched;
-        f_at = f_at == (S - 1) * GV_STAGE_BYTES ? 0u : f_at + GV_STAGE_BYTES;
+        f_at = f_at == (S - 1) * Stage::BYTES ? 0u : f_at + Stage::BYTES;
         if (++f_h == HOLD || f_first + f_h * wr_n >= have) {
             f_h = 0;
             if (++f_s == per) f_s = 0, f_first += HOLD * wr_n;
@@ -183,34 +196,45 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
         for (int s = 0; s < per; ++s) {
             if (per > 1) load_xf(s_lo + wk + s * GV_WARPS);
             for (int h = 0; h < held; ++h) {
-                const int row = (int)(r_lo & 15) + (first + h * wr_n) * block_rows;      // (only its low bits are used)
-                float acc[NT][4];
+                const int blk = first + h * wr_n, row = (int)(r_lo & 15) + blk * block_rows;   // (only its low bits are used)
+                const bool second = MT > 1 && nrows - blk * block_rows > 16;
+                float acc[MT][NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) acc[m][nt][0] = acc[m][nt][1] = acc[m][nt][2] = acc[m][nt][3] = 0.0f;
                 ok = ok && q4_wait(my_bar + 8 * stage, parity, watch);
                 __syncwarp();
-                const uint8_t *st = ring + (warp * S + stage) * GV_STAGE_BYTES;
-                Q4Slab b;
-                b.base = st;
-                b.codes = word;
-                b.s0 = reinterpret_cast<const uint16_t *>(st + GV_SCALE_AT) + (row & 7) + g;
-                b.s1 = b.s0 + 8;
-                b.z0 = zeros ? st + GV_ZERO_AT + (row & 15) + g : nullptr;
-                b.z1 = b.z0 + 8;
-                q4_slab<BF16, SBF16, NT, G, Q4_SCALE_BOX>(acc, b, xf);
+                const uint8_t *st = ring + (warp * S + stage) * Stage::BYTES;
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (m > 0 && !second) break;
+                    Q4Slab b;
+                    b.base = st + 2048 * m;
+                    b.codes = word;
+                    b.s0 = reinterpret_cast<const uint16_t *>(st + Stage::SCALE_AT) + (row & 7) + g + 16 * m;
+                    b.s1 = b.s0 + 8;
+                    b.z0 = zeros ? st + Stage::ZERO_AT + (row & 15) + g + 16 * m : nullptr;
+                    b.z1 = b.z0 + 8;
+                    q4_slab<BF16, SBF16, NT, G, Stage::SCALE_BOX, false, Stage::ZERO_BOX>(acc[m], b, xf);
+                }
                 __syncwarp();                                          // every lane has read the piece
                 if (__all_sync(0xffffffffu, ok)) fetch();
                 if (++stage == S) stage = 0, parity ^= 1;
-                // the block's partial tile, a slab at a time
-                float *tile = tiles + (h * GV_WARPS + warp) * TILE + 2 * t * GV_TILE_LD + g;
+                // the block's partial tiles, a slab at a time
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int m = 0; m < MT; ++m) {
+                    if (m > 0 && !second) break;
+                    float *tile = tiles + ((h * MT + m) * GV_WARPS + warp) * TILE + 2 * t * GV_TILE_LD + g;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float *p = tile + (nt * 8 + (e & 1)) * GV_TILE_LD + 8 * (e >> 1);
-                        if (s > 0) acc[nt][e] += *p;
-                        *p = acc[nt][e];
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float *p = tile + (nt * 8 + (e & 1)) * GV_TILE_LD + 8 * (e >> 1);
+                            if (s > 0) acc[m][nt][e] += *p;
+                            *p = acc[m][nt][e];
+                        }
+                }
             }
         }
         __syncwarp();
@@ -219,11 +243,11 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
             // a pair of threads per four rows of one X row: each adds every
             // other warp's tile, in warp order, then the two join
             const int half = lane & 1;
-            for (int e = (wk * 32 + lane) >> 1; e < HOLD * NT * 32; e += wk_n * 16) {
-                const int h = e / (NT * 32), c = (e >> 2) % (NT * 8), r = (e & 3) * 4;
-                const int o = c * GV_TILE_LD + r;
-                const bool in = h < held && c < a.M;
-                const float *p = tiles + (h * GV_WARPS + warp - wk) * TILE + o;
+            for (int e = (wk * 32 + lane) >> 1; e < HOLD * MT * NT * 32; e += wk_n * 16) {
+                const int hm = e / (NT * 32), h = hm / MT, c = (e >> 2) % (NT * 8), r = (e & 3) * 4;
+                const int o = c * GV_TILE_LD + r, blk = first + h * wr_n, r0 = hm % MT * 16;
+                const bool in = h < held && c < a.M && nrows - blk * block_rows > r0;
+                const float *p = tiles + (hm * GV_WARPS + warp - wk) * TILE + o;
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int w = 0; w < GV_WARPS; w += 2)
@@ -237,9 +261,9 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
                 v.w += __shfl_xor_sync(0xffffffffu, v.w, 1);
                 if (!in) continue;
                 if (ksplit == 1)
-                    write_out(first + h * wr_n, c, r + 2 * half, half ? v.z : v.x, half ? v.w : v.y);
+                    write_out(blk, c, r0 + r + 2 * half, half ? v.z : v.x, half ? v.w : v.y);
                 else if (!half)
-                    *reinterpret_cast<float4 *>(sums + h * TILE + o) = v;
+                    *reinterpret_cast<float4 *>(sums + hm * TILE + o) = v;
             }
         }
         if (ksplit > 1) {
@@ -248,10 +272,10 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
             const uint32_t base = smem_u32(sums);
             const int count = min(HOLD, nblk - first);
             // the phase's outputs, pairs of rows, dealt out to the ranks' threads
-            for (int i = rank * (GV_WARPS * 32) + threadIdx.x; i < count * NT * 64; i += ksplit * GV_WARPS * 32) {
-                const int h = i / (NT * 64), c = (i >> 3) % (NT * 8), r = (i & 7) * 2;
-                if (c >= a.M) continue;
-                const uint32_t o = base + (uint32_t)(h * TILE + c * GV_TILE_LD + r) * 4u;
+            for (int i = rank * (GV_WARPS * 32) + threadIdx.x; i < count * MT * NT * 64; i += ksplit * GV_WARPS * 32) {
+                const int hm = i / (NT * 64), h = hm / MT, c = (i >> 3) % (NT * 8), r = (i & 7) * 2, r0 = hm % MT * 16;
+                if (c >= a.M || nrows - (first + h) * block_rows <= r0) continue;
+                const uint32_t o = base + (uint32_t)(hm * TILE + c * GV_TILE_LD + r) * 4u;
                 float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
@@ -260,7 +284,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
                         v0 += ld_shared_cluster_f32(peer);
                         v1 += ld_shared_cluster_f32(peer + 4);
                     }
-                write_out(first + h, c, r, v0, v1);
+                write_out(first + h, c, r0 + r, v0, v1);
             }
             __syncwarp();
             cluster_sync();      // the sums are read before they are overwritten, or their CTA ends
@@ -277,11 +301,11 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
         }
 }
 
-template <bool BF16, bool SBF16, int NT, int G>
+template <bool BF16, bool SBF16, int NT, int G, int MT>
 cudaError_t launch_one(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st)
 {
-    constexpr auto kern = q4_gemv_kernel<BF16, SBF16, NT, G>;
-    constexpr int smem = gv_smem<NT>();
+    constexpr auto kern = q4_gemv_kernel<BF16, SBF16, NT, G, MT>;
+    constexpr int smem = gv_smem<NT, MT>();
     static std::atomic<bool> configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -292,17 +316,25 @@ cudaError_t launch_one(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st
         configured[dev].store(true, std::memory_order_release);
     }
     return launch_dependent(kern, dim3((unsigned)(p.clusters * p.ksplit)), dim3(GV_WARPS * 32), smem, st,
-                            (unsigned)p.ksplit, a, p.codes, p.scales, p.zeros, p.ksplit, p.rows, p.nblk, p.block_rows,
-                            p.status, p.timeout_ns);
+                            (unsigned)p.ksplit, a, p.codes, p.tail, p.scales, p.zeros, p.ksplit, p.rows, p.nblk,
+                            p.block_rows, p.tail_rows, p.status, p.timeout_ns);
+}
+
+template <bool BF16, bool SBF16, int NT, int G>
+cudaError_t launch_tall(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st)
+{
+    if constexpr (NT == 1)
+        if (p.tall == 2) return launch_one<BF16, SBF16, NT, G, 2>(a, p, st);
+    return launch_one<BF16, SBF16, NT, G, 1>(a, p, st);
 }
 
 template <bool BF16, bool SBF16, int NT>
 cudaError_t launch_group(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st)
 {
     switch (a.q.group) {
-    case 32: return launch_one<BF16, SBF16, NT, 32>(a, p, st);
-    case 64: return launch_one<BF16, SBF16, NT, 64>(a, p, st);
-    default: return launch_one<BF16, SBF16, NT, 128>(a, p, st);
+    case 32: return launch_tall<BF16, SBF16, NT, 32>(a, p, st);
+    case 64: return launch_tall<BF16, SBF16, NT, 64>(a, p, st);
+    default: return launch_tall<BF16, SBF16, NT, 128>(a, p, st);
     }
 }
 
@@ -310,14 +342,15 @@ cudaError_t launch_group(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t 
 
 int q4_gemv_max_clusters(int ksplit)
 {
-    // the largest instantiation's shared memory; the others need no more
+    // split ranges are short: blocks of 16 rows; the larger instantiation's
+    // shared memory
     if (ksplit == 1) {
         int dev = 0, sms = 0;
         cudaGetDevice(&dev);
         return cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? sms : 0;
     }
-    constexpr auto kern = q4_gemv_kernel<true, true, 2, 128>;
-    constexpr int smem = gv_smem<2>();
+    constexpr auto kern = q4_gemv_kernel<true, true, 2, 128, 1>;
+    constexpr int smem = gv_smem<2, 1>();
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ksplit);
@@ -337,8 +370,9 @@ int q4_gemv_max_clusters(int ksplit)
 
 cudaError_t launch_q4_gemv(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st)
 {
-    if (a.M < 1 || a.M > Q4_GEMV_MAX_ROWS || p.ksplit < 1 || p.ksplit > 8 || p.clusters < 1 || p.block_rows < 1 ||
-        p.block_rows > 16)
+    if (a.M < 1 || a.M > Q4_GEMV_MAX_ROWS || p.ksplit < 1 || p.ksplit > 8 || p.clusters < 1 || p.tall < 1 || p.tall > 2 ||
+        (p.tall > 1 && (p.ksplit > 1 || a.M > 8)) || p.block_rows < 1 || p.block_rows > 16 * p.tall || p.tail_rows < 1 ||
+        p.tail_rows > p.block_rows)
         return cudaErrorInvalidValue;
     const bool wide = a.M > 8;
     if (a.x_bf16)
