@@ -1795,9 +1795,24 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     const int64_t g1 = cdiv(a.H, a.w1.group), g2 = cdiv(a.I, a.w2.group), p1 = a.w1.ldw / 2, halves = 2LL * a.E;
     m.s1_3d = a.I % 8 == 0;
     m.z1_3d = a.I % 16 == 0;
+    // Tall pieces where a group of stage 1's warps has eight units or more,
+    // counted with the experts that tokens choosing at random would meet (16
+    // tokens, hidden 4096, inter 1408, 8 of 64 experts: 186 us without, 174
+    // with; for few units they leave warps idle, and h in three parts fills
+    // the registers without them).
+    const double met = a.E * (1.0 - std::pow(1.0 - (double)a.k / a.E, a.T));
+    const int64_t groups1 = std::max<int64_t>(1, 16 / cdiv(a.H, 256));
+    const bool many = met * cdiv(a.I, 8) >= 8.0 * (double)(ctx->num_sms * groups1);
+    const int force = read_force().tail;
+    a.tall = a.parts == 2 && m.s1_3d && (force < 0 ? many : force > 0);
+    const int rows2 = a.tall ? 32 : 16;
+    // stage 2: a CTA's rows of hidden in whole 8s, in equal panels
+    a.rows8 = (int)cdiv(cdiv(a.H, 8), ctx->num_sms);
+    const int most = a.tall && a.T > moe_panel_tokens(a.w1.group) ? 2 : 4;
+    a.panel = 8 * (int)cdiv(a.rows8, cdiv(a.rows8, most));
     bool enc = encode_q4(ctx, &m.c1, u8, a.w1.codes, cdiv(a.H, 8) * 4, a.I, p1, 128, 8, sw, halves, a.I * p1, 2) &&
-               encode_q4(ctx, &m.c2, u8, a.w2.codes, cdiv(a.I, 8) * 4, a.w2.N, a.w2.ldw / 2, 128, 16, sw) &&
-               encode_q4(ctx, &m.s2, u16, a.w2.scales, a.w2.N, g2, a.w2.lds * 2, Q4_SCALE_BOX, gp, plain);
+               encode_q4(ctx, &m.c2, u8, a.w2.codes, cdiv(a.I, 8) * 4, a.w2.N, a.w2.ldw / 2, 128, (uint32_t)std::min(a.panel, rows2), sw) &&
+               encode_q4(ctx, &m.s2, u16, a.w2.scales, a.w2.N, g2, a.w2.lds * 2, 8 + rows2, gp, plain);
     enc = enc && (m.s1_3d ? encode_q4(ctx, &m.s1, u16, a.w1.scales, a.I, g1, a.w1.lds * 2, MOE_SCALE_BOX, gp, plain, halves,
                                       a.I * 2LL, 2)
                           : encode_q4(ctx, &m.s1, u16, a.w1.scales, a.w1.N, g1, a.w1.lds * 2, MOE_SCALE_BOX, gp, plain));
@@ -1805,7 +1820,7 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     if (a.w1.zeros)
         enc = enc && (m.z1_3d ? encode_q4(ctx, &m.z1, u8, a.w1.zeros, a.I, g1, a.w1.lds, Q4_ZERO_BOX, gp, plain, halves, a.I, 2)
                               : encode_q4(ctx, &m.z1, u8, a.w1.zeros, a.w1.N, g1, a.w1.lds, Q4_ZERO_BOX, gp, plain));
-    if (a.w2.zeros) enc = enc && encode_q4(ctx, &m.z2, u8, a.w2.zeros, a.w2.N, g2, a.w2.lds, Q4_ZERO_BOX, gp, plain);
+    if (a.w2.zeros) enc = enc && encode_q4(ctx, &m.z2, u8, a.w2.zeros, a.w2.N, g2, a.w2.lds, 16 + rows2, gp, plain);
     if (!enc) return TC_ERR_CUDA;
     if ((st = ensure_ws(s, lb + hb)) != TC_OK) return st;
     if ((st = ensure_sync(ctx, s)) != TC_OK) return st;
@@ -1817,7 +1832,7 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     if (launch_moe(a, m, ctx->num_sms, s->st) != cudaSuccess) return TC_ERR_CUDA;
     ctx->launches += 1;
     char buf[64];
-    std::snprintf(buf, sizeof buf, "moe_q4_t%d_e%d_k%d_g%d", a.T, a.E, a.k, a.w1.group);
+    std::snprintf(buf, sizeof buf, "moe_q4_t%d_e%d_k%d_g%d%s", a.T, a.E, a.k, a.w1.group, a.tall ? "_tall" : "");
     ctx->last = buf;
     return TC_OK;
 }

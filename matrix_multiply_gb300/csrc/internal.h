@@ -406,6 +406,8 @@ struct MoeArgs {
     int T, H, I, E, k;
     int x_bf16, r_dtype, y_dtype, renorm;
     int parts;             // bf16 parts of h: 2 or 3
+    int tall;              // pieces of two units or 32 rows (parts 2; rows of inter 16-byte multiples)
+    int rows8, panel;      // stage 2: a CTA's rows of hidden / 8, and those of a panel (8 .. 32)
     const void *X, *R;
     void *Y;
     long long ldx, ldr, ldy;
@@ -423,9 +425,11 @@ struct MoeArgs {
 // gate and the same 8 of up.  Boxes: codes {128 bytes, 8 rows, 2} with the
 // 128-byte swizzle, scales {16, 256 / group, 2} where rows of inter are 16-byte
 // multiples (s1_3d; else {16, 256 / group}, two copies), zero points {32, ..}
-// likewise.  down: codes {128 bytes, 16 rows}, scales {24, 256 / group}, zero
-// points {32, 256 / group}.
+// likewise.  down, with r = 16 rows or, tall, 32: codes {128 bytes, the least
+// of r and panel}, scales {8 + r, 256 / group}, zero points {16 + r, 256 / group}.
 constexpr int MOE_SCALE_BOX = 16;
+// tokens up to which a tall panel of stage 2 can have 32 rows (else 16)
+constexpr int moe_panel_tokens(int group) { return group == 32 ? 24 : 32; }
 struct MoeMaps {
     CUtensorMap c1, s1, z1, c2, s2, z2;
     int s1_3d, z1_3d;

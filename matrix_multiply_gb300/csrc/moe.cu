@@ -19,12 +19,12 @@
 // lists in index order, sums in fixed orders.
 //
 // Measured: 1 token, hidden 2048, inter 768, 8 of 64 experts, groups of 128:
-// 18.2 us for 19.7 MB, of which the launch takes 3.1, each stage's dependent
+// 18.1 us for 19.7 MB, of which the launch takes 3.1, each stage's dependent
 // loads, barriers and first passes through its code the rest.  16 tokens,
-// hidden 4096, inter 1408, 8 of 64, groups of 64 with zero points: 182 us for
-// about 530 MB, 43% of a plain copy's rate, bound by issue and the fixed
-// latencies of the widening chain (570 instructions per 16 rows x 256 k;
-// schedulers issue in 61% of the cycles).  As separate launches the stages
+// hidden 4096, inter 1408, 8 of 64, groups of 64 with zero points: 174 us for
+// about 530 MB, 45% of a plain copy's rate, bound by issue and the fixed
+// latencies of the widening chain (about 480 instructions per 16 rows x 256 k;
+// schedulers issue in 61% of the cycles), with pieces of 16 rows 186.  As separate launches the stages
 // would add two of them, with their drains, to every call.
 #include "q4.cuh"
 
@@ -34,16 +34,29 @@ namespace tc {
 namespace {
 
 constexpr int MO_WARPS = 16, MO_THREADS = MO_WARPS * 32;
-constexpr int MO_STAGES = 3;
-constexpr int MO_SCALE_AT = 2048, MO_ZERO_AT = 2560;     // codes of 16 rows, scales, zero points
-constexpr int MO_STAGE_BYTES = 3072;
-constexpr int MO_RING = MO_WARPS * MO_STAGES * MO_STAGE_BYTES;
 constexpr int MO_TILE_LD = 20, MO_TILE = 8 * MO_TILE_LD; // floats: a unit's partial tile, 8 tokens x 16 rows
-constexpr int MO_HOLD = 6;                               // units whose partial tiles are held before they are added
-constexpr int MO_PANEL = 32;                             // rows of hidden per stage-2 panel
+constexpr int MO_PANEL = 32;                             // rows of hidden per stage-2 panel, at most
 constexpr int MO_PAIRS = TC_MOE_MAX_TOKENS * TC_MOE_MAX_TOPK;
-constexpr int MO_SUMS = MO_WARPS * TC_MOE_MAX_TOKENS * MO_PANEL * 4;
-static_assert(MO_HOLD * MO_WARPS * MO_TILE * 4 <= MO_SUMS, "stage 1's tiles share stage 2's space");
+// Shared memory: the rings (the codes of all warps, then their scales and
+// zero points) and the sums, stage 1's tiles or stage 2's panel.  A piece of
+// a ring is one unit of stage 1 or 16 rows of stage 2; TALL two units, 32 rows.
+template <int G, bool TALL>
+struct MoSpace {
+    static constexpr int GP = Q4_SLAB / G;
+    static constexpr int STAGES = TALL ? 2 : 3, ROWS = TALL ? 32 : 16, CODES = ROWS * 128;
+    static constexpr int SCALE2_BOX = 8 + ROWS, ZERO2_BOX = 16 + ROWS;
+    static constexpr int up128(int x) { return (x + 127) / 128 * 128; }
+    static constexpr int larger(int x, int y) { return x > y ? x : y; }
+    // stage 1: two parts of GP groups' scales (zero points), on 128 bytes where they are copied apart
+    static constexpr int S_PART = up128(GP * MOE_SCALE_BOX * 2), Z_PART = up128(GP * Q4_ZERO_BOX);
+    static constexpr int ZERO_AT = up128(larger(2 * S_PART, GP * SCALE2_BOX * 2));
+    static constexpr int SIDE = ZERO_AT + up128(larger(2 * Z_PART, GP * ZERO2_BOX));
+    static constexpr int RING = MO_WARPS * STAGES * (CODES + SIDE);
+    static constexpr int HOLD = TALL && G == 32 ? 4 : 6;     // units whose partial tiles are held before they are added
+    static constexpr int SUMS = MO_WARPS * (TALL ? moe_panel_tokens(G) : TC_MOE_MAX_TOKENS) * MO_PANEL * 4;
+    static_assert(HOLD * MO_WARPS * MO_TILE * 4 <= SUMS, "stage 1's tiles share stage 2's space");
+    static_assert(TC_MOE_MAX_TOKENS * 16 <= moe_panel_tokens(G) * MO_PANEL, "a panel of 16 rows fits for any tokens");
+};
 static_assert(MO_PAIRS <= MO_THREADS && TC_MOE_MAX_EXPERTS <= MO_THREADS && TC_MOE_MAX_TOKENS <= 32, "one thread each");
 
 struct MoeLists {
@@ -58,8 +71,12 @@ struct MoeLists {
     int entries;
     float red[MO_WARPS][8];
 };
-constexpr int MO_SMEM = 1024 + MO_RING + MO_SUMS + (int)sizeof(MoeLists) + MO_WARPS * MO_STAGES * 8 + 16;
-static_assert(MO_SMEM <= SMEM_LIMIT, "one CTA per SM");
+template <int G, bool TALL>
+constexpr int MO_SMEM = 1024 + MoSpace<G, TALL>::RING + MoSpace<G, TALL>::SUMS + (int)sizeof(MoeLists) +
+                        MO_WARPS * MoSpace<G, TALL>::STAGES * 8 + 16;
+static_assert(MO_SMEM<32, true> <= SMEM_LIMIT && MO_SMEM<64, true> <= SMEM_LIMIT && MO_SMEM<128, true> <= SMEM_LIMIT &&
+                  MO_SMEM<32, false> <= SMEM_LIMIT,
+              "one CTA per SM");
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -269,18 +286,20 @@ __device__ __forceinline__ void moe_list(const MoeArgs &a, MoeLists &L)
     }
 }
 
-template <bool BF16, bool SBF16, int G, int PARTS>
+template <bool BF16, bool SBF16, int G, int PARTS, bool TALL>
 __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, const __grid_constant__ MoeMaps maps)
 {
-    constexpr int GP = Q4_SLAB / G, S = MO_STAGES;
+    using Space = MoSpace<G, TALL>;
+    constexpr int GP = Space::GP, S = Space::STAGES, HOLD = Space::HOLD, W = TALL ? 2 : 1;
     extern __shared__ uint8_t raw[];
     uint8_t *ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    float *space = reinterpret_cast<float *>(ring + MO_RING);       // stage 1: tiles; stage 2: sums
-    MoeLists &L = *reinterpret_cast<MoeLists *>(ring + MO_RING + MO_SUMS);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + MO_RING + MO_SUMS + (sizeof(MoeLists) + 7) / 8 * 8);
+    uint8_t *side = ring + MO_WARPS * S * Space::CODES;
+    float *space = reinterpret_cast<float *>(ring + Space::RING);   // stage 1: tiles; stage 2: sums
+    MoeLists &L = *reinterpret_cast<MoeLists *>(ring + Space::RING + Space::SUMS);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + Space::RING + Space::SUMS + (sizeof(MoeLists) + 7) / 8 * 8);
 
     const int warp = uniform_warp(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t my_ring = smem_u32(ring) + warp * (S * MO_STAGE_BYTES);
+    const uint32_t my_ring = smem_u32(ring) + warp * (S * Space::CODES), my_side = smem_u32(side) + warp * (S * Space::SIDE);
     const uint32_t my_bar = smem_u32(bars + warp * S);
     const bool zeros1 = a.w1.zeros != nullptr, zeros2 = a.w2.zeros != nullptr;
     if (lane == 0) {
@@ -301,7 +320,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     unsigned old = grid_arrive(a.sync);
 
     // what does not depend on the choice, while the others arrive
-    const int G1 = (int)gridDim.x, nb = (a.I + 7) >> 3;            // units per entry
+    const int G1 = (int)gridDim.x, nb = (a.I + 7) >> 3, nbp = (nb + W - 1) / W;      // units and pieces per entry
     const int ns1 = (a.H + Q4_SLAB - 1) / Q4_SLAB, ns2 = (a.I + Q4_SLAB - 1) / Q4_SLAB;
     int wk_n = MO_WARPS, wr_n = 1, wr = 0, wk = warp;              // stage 1: warps along hidden, groups along the units
     if (ns1 < MO_WARPS) {
@@ -313,11 +332,10 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     const bool active = wr < wr_n;
     const int per = !active ? 0 : ns1 <= MO_WARPS ? 1 : (ns1 - wk + MO_WARPS - 1) / MO_WARPS;
     // stage 2: this CTA's rows of hidden, in whole 8s
-    const int rows8 = (int)(((unsigned)(a.H + 7) / 8u + (unsigned)G1 - 1u) / (unsigned)G1);
-    const int r_lo = (int)min((long long)a.H, (long long)blockIdx.x * rows8 * 8);
-    const int r_hi = (int)min((long long)a.H, (long long)r_lo + rows8 * 8);
+    const int r_lo = (int)min((long long)a.H, (long long)blockIdx.x * a.rows8 * 8);
+    const int r_hi = (int)min((long long)a.H, (long long)r_lo + a.rows8 * 8);
     // bytes between the two 8-row parts' scales and zero points in stage 1
-    const int s_part = maps.s1_3d ? GP * MOE_SCALE_BOX * 2 : 256, z_part = maps.z1_3d ? GP * Q4_ZERO_BOX : 256;
+    const int s_part = maps.s1_3d ? GP * MOE_SCALE_BOX * 2 : Space::S_PART, z_part = maps.z1_3d ? GP * Q4_ZERO_BOX : Space::Z_PART;
 
     grid_wait(a.sync, old, a.status, a.timeout_ns);
     if (a.E <= 32)
@@ -339,62 +357,59 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         if (a.p) a.p[threadIdx.x] = L.p[threadIdx.x];
     }
 
-    // stage 1: an equal share of the units for every CTA
-    const unsigned units = (unsigned)entries * (unsigned)nb, share = units / (unsigned)G1, extra = units - share * G1;
+    // stage 1: an equal share of the pieces for every CTA
+    const unsigned units = (unsigned)entries * (unsigned)nbp, share = units / (unsigned)G1, extra = units - share * G1;
     const unsigned u0 = blockIdx.x * share + min(blockIdx.x, extra), u1 = u0 + share + (blockIdx.x < extra ? 1u : 0u);
     const int slabs2 = entries * ns2;                   // stage 2's (entry, slab) pieces, dealt out to the warps
     const unsigned u_first = active ? u0 + wr : u1;
-    const int ent_first = (int)(u_first / (unsigned)nb), b_first = (int)(u_first - (unsigned)ent_first * nb);
+    const int ent_first = (int)(u_first / (unsigned)nbp), b_first = (int)(u_first - (unsigned)ent_first * nbp);
 
     // fetching the warp's pieces: stage 1's, then stage 2's
     unsigned f_u = u_first;
-    int f_s = 0, f_ent = ent_first, f_b = b_first, f_panel = r_lo, f_i = warp, f_row = r_lo, f_stage = 0, fetched = 0;
-    constexpr uint32_t CS1 = 2048 + 2 * GP * MOE_SCALE_BOX * 2, Z1 = 2 * GP * Q4_ZERO_BOX;
-    constexpr uint32_t CS2 = 2048 + GP * Q4_SCALE_BOX * 2, Z2 = GP * Q4_ZERO_BOX;
+    int f_s = 0, f_ent = ent_first, f_b = b_first, f_panel = r_lo, f_i = warp, f_row = 0, f_stage = 0, fetched = 0;
+    const uint32_t bytes1 = W * 2048 + 2 * GP * MOE_SCALE_BOX * 2 + (zeros1 ? 2 * GP * Q4_ZERO_BOX : 0);
+    const uint32_t bytes2 = min(a.panel, Space::ROWS) * 128 + GP * Space::SCALE2_BOX * 2 + (zeros2 ? GP * Space::ZERO2_BOX : 0);
     const uint32_t leader = elect_one();
     auto fetch = [&]() {                                // the whole warp
-        const uint32_t st = my_ring + f_stage * MO_STAGE_BYTES, bar = my_bar + 8 * f_stage;
+        const uint32_t st = my_ring + f_stage * Space::CODES, sd = my_side + f_stage * Space::SIDE, bar = my_bar + 8 * f_stage;
         if (f_u < u1) {
-            const int half = L.ent_e[f_ent] * 2, slab = wk + f_s * MO_WARPS, x = f_b * 8;
-            arrive_expect_by(bar, CS1 + (zeros1 ? Z1 : 0u), leader);
+            const int half = L.ent_e[f_ent] * 2, slab = wk + f_s * MO_WARPS, x = f_b * W * 8;
+            arrive_expect_by(bar, bytes1, leader);
             tma_load_3d_by(st, &maps.c1, bar, slab * (Q4_SLAB / 2), x, half, leader);
+            if (W == 2) tma_load_3d_by(st + 2048, &maps.c1, bar, slab * (Q4_SLAB / 2), x + 8, half, leader);
             const int ra = half * a.I + x, rb = ra + a.I;
             if (maps.s1_3d) {
-                tma_load_3d_by(st + MO_SCALE_AT, &maps.s1, bar, x, slab * GP, half, leader);
+                tma_load_3d_by(sd, &maps.s1, bar, x, slab * GP, half, leader);
             } else {
-                tma_load_2d_by(st + MO_SCALE_AT, &maps.s1, bar, ra & ~7, slab * GP, leader);
-                tma_load_2d_by(st + MO_SCALE_AT + 256, &maps.s1, bar, rb & ~7, slab * GP, leader);
+                tma_load_2d_by(sd, &maps.s1, bar, ra & ~7, slab * GP, leader);
+                tma_load_2d_by(sd + Space::S_PART, &maps.s1, bar, rb & ~7, slab * GP, leader);
             }
             if (zeros1) {
                 if (maps.z1_3d) {
-                    tma_load_3d_by(st + MO_ZERO_AT, &maps.z1, bar, x & ~15, slab * GP, half, leader);
+                    tma_load_3d_by(sd + Space::ZERO_AT, &maps.z1, bar, x & ~15, slab * GP, half, leader);
                 } else {
-                    tma_load_2d_by(st + MO_ZERO_AT, &maps.z1, bar, ra & ~15, slab * GP, leader);
-                    tma_load_2d_by(st + MO_ZERO_AT + 256, &maps.z1, bar, rb & ~15, slab * GP, leader);
+                    tma_load_2d_by(sd + Space::ZERO_AT, &maps.z1, bar, ra & ~15, slab * GP, leader);
+                    tma_load_2d_by(sd + Space::ZERO_AT + Space::Z_PART, &maps.z1, bar, rb & ~15, slab * GP, leader);
                 }
             }
             if (++f_s == per) {
                 f_s = 0;
                 f_u += wr_n;
                 f_b += wr_n;
-                while (f_b >= nb) f_b -= nb, ++f_ent;
+                while (f_b >= nbp) f_b -= nbp, ++f_ent;
             }
         } else if (f_panel < r_hi && f_i < slabs2) {
             const int ent = ns2 == 1 ? f_i : (int)((unsigned)f_i / (unsigned)ns2), slab = f_i - ent * ns2;
-            const int row = L.ent_e[ent] * a.H + f_row;
-            arrive_expect_by(bar, CS2 + (zeros2 ? Z2 : 0u), leader);
+            const int row = L.ent_e[ent] * a.H + f_panel + f_row;
+            arrive_expect_by(bar, bytes2, leader);
             tma_load_2d_by(st, &maps.c2, bar, slab * (Q4_SLAB / 2), row, leader);
-            tma_load_2d_by(st + MO_SCALE_AT, &maps.s2, bar, row & ~7, slab * GP, leader);
-            if (zeros2) tma_load_2d_by(st + MO_ZERO_AT, &maps.z2, bar, row & ~15, slab * GP, leader);
-            f_row += 16;
-            if (f_row >= min(r_hi, f_panel + MO_PANEL)) {
-                f_row = f_panel;
+            tma_load_2d_by(sd, &maps.s2, bar, row & ~7, slab * GP, leader);
+            if (zeros2) tma_load_2d_by(sd + Space::ZERO_AT, &maps.z2, bar, row & ~15, slab * GP, leader);
+            f_row += Space::ROWS;
+            if (f_row >= min(r_hi - f_panel, a.panel)) {
+                f_row = 0;
                 f_i += MO_WARPS;
-                if (f_i >= slabs2) {
-                    f_i = warp;
-                    f_panel += MO_PANEL;
-                    f_row = f_panel;
-                }
+                if (f_i >= slabs2) f_i = warp, f_panel += a.panel;
             }
         } else {
             return;
@@ -412,8 +427,9 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     auto arrive = [&]() {                                // the next piece, when it is there
         ok = ok && q4_wait(my_bar + 8 * stage, parity, watch);
         __syncwarp();
-        return ring + (warp * S + stage) * MO_STAGE_BYTES;
     };
+    auto codes_at = [&]() { return ring + (warp * S + stage) * Space::CODES; };
+    auto side_at = [&]() { return side + (warp * S + stage) * Space::SIDE; };
     auto release = [&]() {
         __syncwarp();
         if (__all_sync(0xffffffffu, ok)) fetch();
@@ -427,14 +443,15 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         uint32_t xf[1][8][4];
         int have_ent = -1, have_slab = -1;
         int ent = ent_first, b8 = b_first;
-        for (unsigned first = u_first; first < u1; first += MO_HOLD * wr_n) {
+        constexpr int hold = HOLD / W;                           // pieces
+        for (unsigned first = u_first; first < u1; first += hold * wr_n) {
             int held = 0;
-            for (unsigned u = first; u < u1 && held < MO_HOLD; u += wr_n, ++held) {
-                float acc[1][4] = {};
-                const int ra = L.ent_e[ent] * 2 * a.I + b8 * 8, rb = ra + a.I;
+            for (unsigned u = first; u < u1 && held < hold; u += wr_n, ++held) {
+                float acc[W][1][4] = {};
+                const int i8 = b8 * W * 8, ra = L.ent_e[ent] * 2 * a.I + i8, rb = ra + a.I;
                 // where the parts' first rows lie in their copies
                 const int sa = maps.s1_3d ? 0 : ra & 7, sb = maps.s1_3d ? 0 : rb & 7;
-                const int za = maps.z1_3d ? b8 * 8 & 15 : ra & 15, zb = maps.z1_3d ? b8 * 8 & 15 : rb & 15;
+                const int za = maps.z1_3d ? i8 & 15 : ra & 15, zb = maps.z1_3d ? i8 & 15 : rb & 15;
                 for (int s = 0; s < per; ++s) {
                     const int slab = wk + s * MO_WARPS;
                     if (ent != have_ent || slab != have_slab) {
@@ -446,33 +463,43 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                             q4_load_slab<false>(xf[0], row, (long long)slab * Q4_SLAB + 8 * t, a.H, x_vec && slab < a.H / Q4_SLAB);
                         }
                     }
-                    const uint8_t *st = arrive();
+                    arrive();
+                    const uint8_t *sd = side_at();
                     Q4Slab b;
-                    b.base = st;
+                    b.base = codes_at();
                     b.codes = word;
-                    b.s0 = reinterpret_cast<const uint16_t *>(st + MO_SCALE_AT) + sa + g;
-                    b.s1 = reinterpret_cast<const uint16_t *>(st + MO_SCALE_AT + s_part) + sb + g;
-                    b.z0 = zeros1 ? st + MO_ZERO_AT + za + g : nullptr;
-                    b.z1 = st + MO_ZERO_AT + z_part + zb + g;
-                    q4_slab<BF16, SBF16, 1, G, MOE_SCALE_BOX>(acc, b, xf);
+                    b.s0 = reinterpret_cast<const uint16_t *>(sd) + sa + g;
+                    b.s1 = reinterpret_cast<const uint16_t *>(sd + s_part) + sb + g;
+                    b.z0 = zeros1 ? sd + Space::ZERO_AT + za + g : nullptr;
+                    b.z1 = sd + Space::ZERO_AT + z_part + zb + g;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) {
+                        q4_slab<BF16, SBF16, 1, G, MOE_SCALE_BOX>(acc[i], b, xf);
+                        b.base += 2048, b.s0 += 8, b.s1 += 8, b.z1 += 8;
+                        if (zeros1) b.z0 += 8;
+                    }
                     release();
                 }
-                float *tile = space + (held * MO_WARPS + warp) * MO_TILE + 2 * t * MO_TILE_LD + g;
+                float *tile = space + (held * W * MO_WARPS + warp) * MO_TILE + 2 * t * MO_TILE_LD + g;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) tile[(e & 1) * MO_TILE_LD + 8 * (e >> 1)] = acc[0][e];
+                for (int i = 0; i < W; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        tile[i * MO_WARPS * MO_TILE + (e & 1) * MO_TILE_LD + 8 * (e >> 1)] = acc[i][0][e];
                 b8 += wr_n;
-                while (b8 >= nb) b8 -= nb, ++ent;
+                while (b8 >= nbp) b8 -= nbp, ++ent;
             }
             __syncwarp();
             q4_group_sync(wr, wk_n);
             // two threads per token and four rows: each adds every other
             // warp's tile, in warp order, then the two join
             const int half = lane & 1;
-            for (int e = (wk * 32 + lane) >> 1; e < MO_HOLD * 16; e += wk_n * 16) {
-                const int hu = e >> 4, c = (e >> 1) & 7, r = (e & 1) * 4;
-                const unsigned u = first + (unsigned)(hu * wr_n);
-                const int ue = hu < held ? (int)(u / (unsigned)nb) : 0;
-                const bool in = hu < held && c < L.ent_n[ue];
+            for (int e = (wk * 32 + lane) >> 1; e < HOLD * 16; e += wk_n * 16) {
+                const int hu = e >> 4, hp = hu / W, c = (e >> 1) & 7, r = (e & 1) * 4;
+                const unsigned u = first + (unsigned)(hp * wr_n);
+                const int ue = hp < held ? (int)(u / (unsigned)nbp) : 0;
+                const int ub = (int)(u - (unsigned)ue * nbp) * W + (hu - hp * W);       // the unit within the entry
+                const bool in = hp < held && ub < nb && c < L.ent_n[ue];
                 const float *p = space + (hu * MO_WARPS + warp - wk) * MO_TILE + c * MO_TILE_LD + r;
                 float v[8] = {};
 #pragma unroll
@@ -486,7 +513,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1);
                 if (!in) continue;
-                const int i0 = (int)(u - (unsigned)ue * nb) * 8 + r + 2 * half;
+                const int i0 = ub * 8 + r + 2 * half;
                 uint16_t *h = a.h + L.pair[L.ent_at[ue] + c] * a.ldh + i0;
                 uint32_t part[PARTS] = {};
 #pragma unroll
@@ -511,13 +538,14 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     }
     old = grid_arrive(a.sync);
     // this warp's sums start at zero while the others arrive
-    float *sums = space + warp * a.T * MO_PANEL;
-    for (int i = lane; i < a.T * MO_PANEL; i += 32) sums[i] = 0.0f;
+    const int pld = TALL && a.T > moe_panel_tokens(G) ? 16 : MO_PANEL;      // a token's sums of a panel
+    float *sums = space + warp * a.T * pld;
+    for (int i = lane; i < a.T * pld; i += 32) sums[i] = 0.0f;
     grid_wait(a.sync, old, a.status, a.timeout_ns);
 
     // ------------------------------------------------ stage 2: down
-    for (int panel = r_lo; panel < r_hi; panel += MO_PANEL) {
-        const int p_hi = min(r_hi, panel + MO_PANEL);
+    for (int panel = r_lo; panel < r_hi; panel += a.panel) {
+        const int p_hi = min(r_hi, panel + a.panel);
         for (int i = warp; i < slabs2; i += MO_WARPS) {
             const int ent = (int)((unsigned)i / (unsigned)ns2), slab = i - ent * ns2, n = L.ent_n[ent], at = L.ent_at[ent];
             uint32_t xf[PARTS][8][4];
@@ -542,37 +570,47 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                 tok[c] = 2 * t + c < n ? L.tok[at + 2 * t + c] : -1;
                 pw[c] = 2 * t + c < n ? L.p[L.pair[at + 2 * t + c]] : 0.0f;
             }
-            for (int row = panel; row < p_hi; row += 16) {
-                float acc[1][4] = {};
-                const int ra = L.ent_e[ent] * a.H + row;
-                const uint8_t *st = arrive();
+            for (int row0 = 0; row0 < p_hi - panel; row0 += Space::ROWS) {
+                constexpr int HALVES = Space::ROWS / 16;
+                float acc[HALVES][1][4] = {};
+                const int ra = L.ent_e[ent] * a.H + panel + row0;
+                arrive();
+                const uint8_t *sd = side_at();
                 Q4Slab b;
-                b.base = st;
+                b.base = codes_at();
                 b.codes = word;
-                b.s0 = reinterpret_cast<const uint16_t *>(st + MO_SCALE_AT) + (ra & 7) + g;
-                b.s1 = b.s0 + 8;
-                b.z0 = zeros2 ? st + MO_ZERO_AT + (ra & 15) + g : nullptr;
-                b.z1 = b.z0 + 8;
-                q4_slab<true, SBF16, PARTS, G, Q4_SCALE_BOX, true>(acc, b, xf);
+                b.s0 = reinterpret_cast<const uint16_t *>(sd) + (ra & 7) + g;
+                b.z0 = zeros2 ? sd + Space::ZERO_AT + (ra & 15) + g : nullptr;
+#pragma unroll
+                for (int i = 0; i < HALVES; ++i) {
+                    if (i > 0 && p_hi - panel <= 16) break;
+                    b.s1 = b.s0 + 8;
+                    b.z1 = b.z0 + 8;
+                    q4_slab<true, SBF16, PARTS, G, Space::SCALE2_BOX, true, Space::ZERO2_BOX>(acc[i], b, xf);
+                    b.base += 2048, b.s0 += 16;
+                    if (zeros2) b.z0 += 16;
+                }
                 release();
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    if (tok[c] >= 0) {
-                        float *y = sums + tok[c] * MO_PANEL + (row - panel) + g;
-                        y[0] = fmaf(pw[c], acc[0][c], y[0]);
-                        y[8] = fmaf(pw[c], acc[0][2 + c], y[8]);
-                    }
+                for (int i = 0; i < HALVES; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (tok[c] >= 0 && (i == 0 || p_hi - panel > 16)) {
+                            float *y = sums + tok[c] * pld + row0 + 16 * i + g;
+                            y[0] = fmaf(pw[c], acc[i][0][c], y[0]);
+                            y[8] = fmaf(pw[c], acc[i][0][2 + c], y[8]);
+                        }
                 __syncwarp();
             }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < a.T * MO_PANEL; i += MO_THREADS) {
-            const int tk = i / MO_PANEL, r = i - tk * MO_PANEL;
+        for (int i = threadIdx.x; i < a.T * pld; i += MO_THREADS) {
+            const int tk = pld == 16 ? i / 16 : i / MO_PANEL, r = i - tk * pld;
             float y = 0.0f;
 #pragma unroll
             for (int w = 0; w < MO_WARPS; ++w) {
-                y += space[w * a.T * MO_PANEL + i];
-                space[w * a.T * MO_PANEL + i] = 0.0f;
+                y += space[w * a.T * pld + i];
+                space[w * a.T * pld + i] = 0.0f;
             }
             if (panel + r < p_hi) store_c1(a.Y, tk * a.ldy + panel + r, y, a.y_dtype);
         }
@@ -587,23 +625,23 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         }
 }
 
-template <bool BF16, bool SBF16, int G, int PARTS>
+template <bool BF16, bool SBF16, int G, int PARTS, bool TALL>
 cudaError_t launch_one(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_t st)
 {
-    constexpr auto kern = moe_kernel<BF16, SBF16, G, PARTS>;
+    constexpr auto kern = moe_kernel<BF16, SBF16, G, PARTS, TALL>;
     static std::atomic<bool> configured[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MO_SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (MO_SMEM<G, TALL>));
         if (e != cudaSuccess) return e;
         configured[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(MO_THREADS);
-    cfg.dynamicSmemBytes = MO_SMEM;
+    cfg.dynamicSmemBytes = MO_SMEM<G, TALL>;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;
@@ -616,8 +654,8 @@ cudaError_t launch_one(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_
 template <bool BF16, bool SBF16, int G>
 cudaError_t launch_parts(const MoeArgs &a, const MoeMaps &m, int grid, cudaStream_t st)
 {
-    return a.parts == 3 ? launch_one<BF16, SBF16, G, 3>(a, m, grid, st)
-                                     : launch_one<BF16, SBF16, G, 2>(a, m, grid, st);
+    if (a.parts == 3) return launch_one<BF16, SBF16, G, 3, false>(a, m, grid, st);
+    return a.tall ? launch_one<BF16, SBF16, G, 2, true>(a, m, grid, st) : launch_one<BF16, SBF16, G, 2, false>(a, m, grid, st);
 }
 
 template <bool BF16, bool SBF16>

@@ -82,6 +82,21 @@ def test_long_axes(ctx, shape):
     check(*out, X, R, w1, w2, I, k, "f32", True, f"{shape}")
 
 
+@pytest.mark.parametrize("shape", [(1, 256, 128, 8, 2), (3, 520, 264, 9, 3), (16, 384, 200, 12, 4), (32, 256, 64, 6, 2),
+                                   (32, 5000, 40, 3, 2), (20, 4000, 72, 5, 2), (9, 9100, 24, 3, 1), (2, 72, 5000, 3, 2)])
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, True), (128, False)])
+def test_tall_pieces(ctx, monkeypatch, shape, x, group, zeros):
+    """Pieces of two units and 32 rows: odd numbers of units, panels of 8 to 32
+    rows, several panels, several slabs to a warp."""
+    monkeypatch.setenv("TC_FORCE_VARIANT", "tail=1")
+    T, H, I, E, k = shape
+    X, R, w1, w2 = problem(T, H, I, E, k, x, "f32", group, zeros)
+    out = layer(ctx, X.cuda(), R.cuda(), w1, w2, I, E, k, x)
+    assert ctx.last_kernel.endswith("_tall")
+    check(*out, X, R, w1, w2, I, k, x, True, f"{shape}")
+
+
 @pytest.mark.parametrize("x", ["bf16", "f16"])
 def test_fp32_outputs_keep_24_bits(ctx, x):
     """One expert, one column of inter, one element of x per token: nothing is
