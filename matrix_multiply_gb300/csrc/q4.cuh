@@ -16,11 +16,12 @@ namespace tc {
 // 128-byte swizzle (16-byte unit u of row r sits at u ^ (r % 8)), so that a
 // warp reading one 32-bit word per lane -- word t of unit u of row g, lane =
 // 4 g + t -- touches all 32 banks.  Beside the codes lie, per group, the
-// scales of 24 rows and the zero points of 32, from the last row at or
+// scales of 24 rows and the zero points of 32 (of 16 more for two pieces
+// copied at once), from the last row at or
 // before the piece's first that is a multiple of 8 (16): TMA copies start at
 // multiples of 16 bytes.
 constexpr int Q4_SLAB = 256;
-constexpr int Q4_SCALE_PITCH = 2 * Q4_SCALE_BOX, Q4_ZERO_PITCH = Q4_ZERO_BOX;
+constexpr int Q4_ZERO_PITCH = Q4_ZERO_BOX;
 
 // D(16x8, f32) = A(16x16) * B(16x8) + C, A row-major, B column-major
 template <bool BF16>
