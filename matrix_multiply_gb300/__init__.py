@@ -310,6 +310,14 @@ class Stream:
             pass
 
 
+def _check_pitch(what: str, t, rows: int, row_len: int, per: int = 1):
+    """Rows that lie apart, at a pitch (``per`` units an element of t) that the
+    C structures hold.  Rows that share memory, as expand gives them, have none:
+    a stride of 0 would mean the default pitch there, past the end of t."""
+    if rows > 1 and not row_len <= t.stride(0) <= (2 ** 31 - 1) // per:
+        raise ValueError(f"{what} has a row stride of {t.stride(0)}, its rows are {row_len} long")
+
+
 class Q4Weight:
     """A 4-bit weight W[N, K] with group scales in caller-owned CUDA tensors:
     codes uint8 [N, >= K/2], scales f16/bf16 [ceil(K/group), >= N], zeros
@@ -331,6 +339,7 @@ class Q4Weight:
                 raise ValueError(f"{name} must be 2-D with unit column stride")
             if t.shape[0] < rows or t.shape[1] < need:
                 raise ValueError(f"{name} is {tuple(t.shape)}, the weight needs at least ({rows}, {need})")
+            _check_pitch(name, t, rows, need, 2 if name == "codes" else 1)
         for name, t in (("codes", codes), ("zeros", zeros)):
             if t is not None and t.dtype != torch.uint8:
                 raise ValueError(f"{name} must be uint8")
@@ -563,6 +572,7 @@ def _matrix_2d(t, N: int, K: int, what: str) -> tuple[int, int]:
         raise ValueError(f"{what} must be a CUDA tensor")
     if t.dim() != 2 or tuple(t.shape) != (N, K) or (K > 1 and t.stride(1) != 1):
         raise ValueError(f"{what} must be [{N}, {K}] with unit column stride")
+    _check_pitch(what, t, N, K)
     return _torch_dtype_code(t), t.stride(0) if N > 1 else 0
 
 
