@@ -610,6 +610,12 @@ def _check_q4_capacity(d: tc_gemm_desc, X, C):
         return   # the library reports the precise error
     _require(X, _extent(d.M, d.K, d.lda or d.K), "X")
     _require(C, _extent(d.M, d.N, d.ldc or d.N), "C")
+    # _require counts elements: of a narrower type they would be too few bytes
+    import torch
+    types = {TC_F16: torch.float16, TC_BF16: torch.bfloat16, TC_F32: torch.float32}
+    for name, t, code in (("X", X, d.a_dtype), ("C", C, d.c_dtype)):
+        if t is not None and not isinstance(t, int) and t.dtype != types.get(code, t.dtype):
+            raise ValueError(f"{name} must have the descriptor's dtype")
 
 
 def tc_gemm_q4_weight(ctx: Context, d: tc_gemm_desc, X, q: Q4Weight, C):

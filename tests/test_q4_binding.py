@@ -87,3 +87,25 @@ def test_matrices_of_rows_apart_reach_the_library():
         with pytest.raises(tg.TcError) as err:
             tg.tc_quantize_q4(NO_CTX, W, q)
         assert err.value.status == tg.TC_ERR_NULL
+
+
+@pytest.mark.parametrize("x,c", [(torch.float32, torch.float16), (torch.bfloat16, torch.float16), (torch.uint8, torch.float16),
+                                 (torch.float16, torch.bfloat16), (torch.float16, torch.float32), (torch.float16, torch.uint8)])
+def test_product_of_other_types_is_refused(x, c):
+    """Elements are counted, so a tensor of a narrower type than the
+    descriptor's would be too short."""
+    q = tg.Q4Weight(64, 96, 32, *parts())
+    d = tg.make_desc(4, 64, 96, "f16", "f16", b_dtype="i4", transpose_b=True)
+    stream = types.SimpleNamespace(ptr=None)
+    X, C = t(4, 96, dtype=x), t(4, 64, dtype=c)
+    for call in (lambda: tg.tc_gemm_q4_weight(NO_CTX, d, X, q, C),
+                 lambda: tg.tc_gemm_q4_weight_async(NO_CTX, d, X, q, C, stream),
+                 lambda: tg.PreparedGemm(NO_CTX, d, X, q, C, stream)):
+        with pytest.raises(ValueError):
+            call()
+    # addresses are the caller's word, and a type the library refuses is its to report
+    with pytest.raises(tg.TcError):
+        tg.tc_gemm_q4_weight(NO_CTX, d, 1 << 20, q, 1 << 30)
+    with pytest.raises(tg.TcError):
+        tg.tc_gemm_q4_weight(NO_CTX, tg.make_desc(4, 64, 96, "i8", "f32", b_dtype="i4", transpose_b=True), X, q,
+                             t(4, 64, dtype=F32))
