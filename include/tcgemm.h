@@ -282,7 +282,8 @@ typedef struct {
  * A group whose scale is 0 (all zeros, or too small for scale_dtype) gets
  * code = zero = 8.  A group that holds a NaN or an infinity, or is too large
  * for scale_dtype, gets a scale that is not finite, so its values read back
- * as NaN or infinity.  Codes from K to K rounded up to 32 stand for 0. */
+ * as NaN or infinity.  Codes from K to K rounded up to 32 stand for 0.  K is
+ * at most 65535 * 1024 (TC_ERR_DIM beyond), also for reading back. */
 tc_status_t tc_quantize_q4(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W, const tc_q4_weight *q);
 tc_status_t tc_quantize_q4_async(tc_ctx *ctx, tc_dtype_t w_dtype, int32_t ld, const void *W,
                                  const tc_q4_weight *q, tc_stream *s);

@@ -1428,6 +1428,7 @@ tc_status_t check_q4_matrix(const tc_q4_weight *q, tc_dtype_t dtype, int32_t ld,
     if (!W) return TC_ERR_NULL;
     tc_status_t st = check_q4(q, n);
     if (st != TC_OK) return st;
+    if (q->K > Q4_MATRIX_MAX_K) return TC_ERR_DIM;
     if (dtype != TC_F16 && dtype != TC_BF16 && dtype != TC_F32) return TC_ERR_DTYPE;
     *ldn = ld ? ld : q->K;
     if (*ldn < q->K) return TC_ERR_LD;

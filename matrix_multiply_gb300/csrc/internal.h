@@ -337,6 +337,8 @@ struct Q4View {
     int group, scale_bf16;
 };
 
+// Quantising and reading back: chunks of at least 1024 k, one per grid row.
+constexpr int Q4_MATRIX_MAX_K = 65535 * 1024;
 struct Q4QuantArgs {
     const void *W;
     long long ld;

@@ -373,8 +373,8 @@ __global__ void __launch_bounds__(QZ_THREADS, 4) q4_dequantize_kernel(const Q4De
     }
 }
 
-// CTAs of 16 rows x `cols` k; grid.y is limited to 65535 (K below 2^26: beyond,
-// a row alone would be 33 MB of codes)
+// CTAs of 16 rows x `cols` k; grid.y is limited to 65535, which
+// Q4_MATRIX_MAX_K keeps to
 bool qz_grid(const Q4View &q, int cols, dim3 *grid)
 {
     const long long bx = (q.N + QZ_ROWS - 1) / QZ_ROWS, by = (q.K + cols - 1) / cols;

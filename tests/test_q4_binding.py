@@ -109,3 +109,12 @@ def test_product_of_other_types_is_refused(x, c):
     with pytest.raises(tg.TcError):
         tg.tc_gemm_q4_weight(NO_CTX, tg.make_desc(4, 64, 96, "i8", "f32", b_dtype="i4", transpose_b=True), X, q,
                              t(4, 64, dtype=F32))
+
+
+def test_longest_rows():
+    """Quantising and reading back take K up to 65535 * 1024; a longer row is
+    refused as a size, not as a failed launch."""
+    K = 65535 * 1024
+    for k, want in ((K, tg.TC_OK), (K + 1, tg.TC_ERR_DIM)):
+        q = tg.tc_q4_weight(2, k, 32, tg.TC_F16, 0, 0, 1 << 32, 1 << 40, None)
+        assert tg.tc_q4_validate(q, W=1 << 50) == want
