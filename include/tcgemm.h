@@ -306,9 +306,13 @@ tc_status_t tc_q4_validate(const tc_q4_weight *q, tc_dtype_t dtype, int32_t ld, 
  * with the whole numbers code - zero are exact and summed in fp32 within a
  * group, the groups' sums times their scales are summed in fp32: no weight
  * is rounded to 16 bits on the way.  Deterministic run to run.  Calls of more
- * than 16 rows may take workspace from the stream, enlarged when a call needs
- * more than any before it: make the largest call once before a stream
- * capture. */
+ * than 16 rows take workspace from the stream: of one size for all of them, and
+ * a copy of X (M rows of K rounded up to 64) where its base or rows are off 16
+ * bytes.  Before a stream capture make one such call, the largest of those
+ * whose X is off 16 bytes if there are any; a captured call that would have to
+ * allocate returns TC_ERR_CUDA and captures nothing.  A stream's workspace moves
+ * when a later call, of whichever kind, needs more than any before it: graphs
+ * captured before that must not be launched after it. */
 tc_status_t tc_gemm_q4_weight(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X, void *C);
 tc_status_t tc_gemm_q4_weight_async(tc_ctx *ctx, const tc_gemm_desc *d, const tc_q4_weight *q, const void *X,
                                     void *C, tc_stream *s);
@@ -337,7 +341,9 @@ tc_status_t tc_gemm_q4_weight_validate(const tc_gemm_desc *d, const tc_q4_weight
  * TC_MOE_MAX_EXPERTS (TC_ERR_DIM otherwise, and when the weights' N and K do
  * not fit); Y, ids and weights overlap no input and one another
  * (TC_ERR_OVERLAP).  Deterministic run to run.  Takes workspace from the
- * stream: make one call before a stream capture. */
+ * stream, about 4 tokens (experts + 1.5 top_k inter) bytes: before a stream
+ * capture make the call that needs most; a captured call that would have to
+ * allocate returns TC_ERR_CUDA and captures nothing. */
 #define TC_MOE_MAX_TOKENS 32
 #define TC_MOE_MAX_EXPERTS 512
 #define TC_MOE_MAX_TOPK 16

@@ -35,7 +35,7 @@ struct tc_stream {
     void *rx = nullptr;              // relaxed fp32: the bf16 split operands
     size_t rx_cap = 0;
     unsigned *sync = nullptr;        // the grid barrier's words of kernels that cross one
-    bool sync_clear = false;         // they are as such a kernel expects and leaves them
+    std::atomic<bool> sync_clear{false};   // they are as such a kernel expects and leaves them
     unsigned *status_host = nullptr; // mapped, pinned: kernels report timeouts here
     unsigned *status_dev = nullptr;
 };
@@ -1580,8 +1580,18 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
 // The stream's words that kernels leave at 0: those of the grid barriers,
 // then the counts of the cut tiles of the 4-bit product.
 constexpr size_t SYNC_WORDS = 64;
-tc_status_t ensure_sync(tc_ctx *ctx, tc_stream *s)
+
+// Memory of a 4-bit call that needs `ws` and `rx` bytes and the words above:
+// taken before anything of the call is launched.  A call under stream capture
+// must find all of it there: what it allocated would be the graph's, and the
+// clearing a node of the graph, while later calls outside relied on both.
+tc_status_t reserve_q4(tc_ctx *ctx, tc_stream *s, size_t ws, size_t rx)
 {
+    if (ws <= s->ws_cap && rx <= s->rx_cap && s->sync && s->sync_clear) return TC_OK;
+    cudaStreamCaptureStatus capture;
+    if (cudaStreamIsCapturing(s->st, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return TC_ERR_CUDA;
+    tc_status_t st;
+    if ((st = ensure_ws(s, ws)) != TC_OK || (st = ensure_rx(s, rx)) != TC_OK) return st;
     const size_t bytes = (SYNC_WORDS + (size_t)2 * ctx->num_sms * Q4_MMA_COUNTS) * sizeof(unsigned);
     if (!s->sync && cudaMallocAsync(reinterpret_cast<void **>(&s->sync), bytes, s->st) != cudaSuccess) {
         s->sync = nullptr;
@@ -1653,11 +1663,14 @@ tc_status_t enqueue_q4_mma(tc_ctx *ctx, tc_stream *s, Q4GemmArgs a, const Force 
     plan_q4_mma(ctx->num_sms, a, f, &p);
     if ((int64_t)p.tiles_n * p.tiles_m * p.split > INT32_MAX / 2) return TC_ERR_OVERFLOW;
     int launches = 1;
-    if (!aligned16(a.X) || a.ldx % 8 != 0) {
-        // rows TMA cannot address: a copy with padded rows in the stream's buffer
-        const int64_t ld = cdiv(a.q.K, 64) * 64;
-        const tc_status_t st = ensure_rx(s, (size_t)(a.M * ld * 2));
-        if (st != TC_OK) return st;
+    // rows TMA cannot address: a copy with padded rows in the stream's buffer
+    const bool pack = !aligned16(a.X) || a.ldx % 8 != 0;
+    const int64_t ld = cdiv(a.q.K, 64) * 64;
+    // every call keeps what a cut of the last tiles needs (two tiles for each
+    // SM), so that a larger call, which may need no cut, stands for a smaller
+    const tc_status_t st = reserve_q4(ctx, s, (size_t)2 * ctx->num_sms * 128 * Q4_MMA_ROWS * 4, pack ? (size_t)(a.M * ld * 2) : 0);
+    if (st != TC_OK) return st;
+    if (pack) {
         PackBatch pb;
         pb.count = 1;
         pb.seg[0] = PackArgs{static_cast<const uint16_t *>(a.X), static_cast<uint16_t *>(s->rx), a.M, a.q.K, a.ldx, ld, 0, 0, 1};
@@ -1674,8 +1687,6 @@ tc_status_t enqueue_q4_mma(tc_ctx *ctx, tc_stream *s, Q4GemmArgs a, const Force 
     p.partial = nullptr;
     p.counts = nullptr;
     if (p.whole < p.tiles_n * p.tiles_m) {
-        tc_status_t st = ensure_ws(s, (size_t)p.grid * 2 * p.bn * Q4_MMA_ROWS * 4);
-        if (st != TC_OK || (st = ensure_sync(ctx, s)) != TC_OK) return st;
         p.partial = static_cast<float *>(s->ws);
         p.counts = s->sync + SYNC_WORDS;
     }
@@ -1823,8 +1834,7 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
                               : encode_q4(ctx, &m.z1, u8, a.w1.zeros, a.w1.N, g1, a.w1.lds, Q4_ZERO_BOX, gp, plain));
     if (a.w2.zeros) enc = enc && encode_q4(ctx, &m.z2, u8, a.w2.zeros, a.w2.N, g2, a.w2.lds, 16 + rows2, gp, plain);
     if (!enc) return TC_ERR_CUDA;
-    if ((st = ensure_ws(s, lb + hb)) != TC_OK) return st;
-    if ((st = ensure_sync(ctx, s)) != TC_OK) return st;
+    if ((st = reserve_q4(ctx, s, lb + hb, 0)) != TC_OK) return st;
     a.logits = static_cast<float *>(s->ws);
     a.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(s->ws) + lb);
     a.sync = s->sync;
