@@ -523,6 +523,9 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                 }
                 last = before == c1 - c0;
                 if (last) {
+                    // lane 0 alone has acquired the others' sums; the shuffle
+                    // that passed its count on orders no memory
+                    __syncwarp();
                     if (lane == 0) *count = 0u;                // as the next launch expects it
                     if (c1 > c0 + 1)
 #pragma unroll
