@@ -205,8 +205,11 @@ bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 // whole 16-row blocks) gemv_grid=<G> (the row-range form on G CTAs)
 // hband=<rows> (tc_gemm_host moves A and C in bands of this many rows).
 // Test hooks: debug_drop=1 (the MMA warp withholds the first tile's
-// "accumulator ready" signal, so the epilogue's wait expires) and
-// debug_timeout_ms=<ms> (the bound on every device wait).
+// "accumulator ready" signal, so the epilogue's wait expires; the first CTA of
+// a 4-bit product waits for 16 bytes that no copy brings, in the experts
+// layer's likewise with debug_drop=2, while with 1 its second CTA keeps its
+// arrival at the first grid barrier) and debug_timeout_ms=<ms> (the bound on
+// every device wait).
 struct Force {
     int bn = 0, split = 0, grid = 0, group_m = 0, ffma = -1, pack = 0, tail = -1, sms = 0, cg = 0;
     bool direct_store = false;
@@ -262,6 +265,12 @@ Force read_force()
         else if (k == "gemv_grid") f.gemv_grid = std::atoi(v.c_str());
     }
     return f;
+}
+
+// The bound on a kernel's waits: its own, or the forced one.
+unsigned long long wait_limit(const Force &f, unsigned long long ns)
+{
+    return f.debug_timeout_ms > 0 ? (unsigned long long)f.debug_timeout_ms * 1000000ull : ns;
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1559,7 +1568,8 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
     p->nblk = (int)cdiv(p->rows, p->block_rows);
     p->tail_rows = p->tall > 1 ? p->rows - (p->nblk - 1) * p->block_rows : p->block_rows;
     p->status = s->status_dev;
-    p->timeout_ns = 4000000000ull;
+    p->timeout_ns = wait_limit(f, 4000000000ull);
+    p->debug_drop = f.debug_drop;
     const int64_t groups = cdiv(a.q.K, a.q.group);
     const uint32_t gp = 256 / a.q.group;
     if (!encode_q4(ctx, &p->codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.q.codes, cdiv(a.q.K, 8) * 4, a.q.N, a.q.ldw / 2, 128,
@@ -1691,7 +1701,8 @@ tc_status_t enqueue_q4_mma(tc_ctx *ctx, tc_stream *s, Q4GemmArgs a, const Force 
         p.counts = s->sync + SYNC_WORDS;
     }
     p.status = s->status_dev;
-    p.timeout_ns = 4000000000ull + (unsigned long long)cdiv(a.q.K, 64) * 20000ull;
+    p.timeout_ns = wait_limit(f, 4000000000ull + (unsigned long long)cdiv(a.q.K, 64) * 20000ull);
+    p.debug_drop = f.debug_drop;
     if (launch_q4_mma(a, p, s->st) != cudaSuccess) return TC_ERR_CUDA;
     ctx->launches += launches;
     char buf[64];
@@ -1815,8 +1826,8 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     const double met = a.E * (1.0 - std::pow(1.0 - (double)a.k / a.E, a.T));
     const int64_t groups1 = std::max<int64_t>(1, 16 / cdiv(a.H, 256));
     const bool many = met * cdiv(a.I, 8) >= 8.0 * (double)(ctx->num_sms * groups1);
-    const int force = read_force().tail;
-    a.tall = a.parts == 2 && m.s1_3d && (force < 0 ? many : force > 0);
+    const Force f = read_force();
+    a.tall = a.parts == 2 && m.s1_3d && (f.tail < 0 ? many : f.tail > 0);
     const int rows2 = a.tall ? 32 : 16;
     // stage 2: a CTA's rows of hidden in whole 8s, in equal panels
     a.rows8 = (int)cdiv(cdiv(a.H, 8), ctx->num_sms);
@@ -1839,7 +1850,8 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     a.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(s->ws) + lb);
     a.sync = s->sync;
     a.status = s->status_dev;
-    a.timeout_ns = 4000000000ull;
+    a.timeout_ns = wait_limit(f, 4000000000ull);
+    a.debug_drop = f.debug_drop;
     if (launch_moe(a, m, ctx->num_sms, s->st) != cudaSuccess) return TC_ERR_CUDA;
     ctx->launches += 1;
     char buf[64];

@@ -376,6 +376,7 @@ struct Q4GemvPlan {
     CUtensorMap codes, tail, scales, zeros;
     unsigned *status;
     unsigned long long timeout_ns;
+    int debug_drop;            // test hook: the first CTA's copies never complete
 };
 // boxes of the maps: {128 bytes, block_rows (tail_rows)} with the 128-byte
 // swizzle, {8 + 16 tall scales, 256 / group}, {16 + 16 tall zeros, 256 / group}
@@ -399,6 +400,7 @@ struct Q4MmaPlan {
     CUtensorMap codes, x;      // boxes {128 bytes, 128 rows} and {64 elements, bn rows}, 128-byte swizzle
     unsigned *status;
     unsigned long long timeout_ns;
+    int debug_drop;            // test hook: the first CTA's third copy of X never completes
 };
 cudaError_t launch_q4_mma(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st);
 
@@ -422,6 +424,7 @@ struct MoeArgs {
     unsigned *sync;        // the grid barrier's word, 0 before the first launch of this grid size that uses it
     unsigned *status;
     unsigned long long timeout_ns;
+    int debug_drop;        // test hook: 1 the second CTA misses the first grid barrier, 2 the first CTA's copies never complete
 };
 // gate_up is seen as [2 experts][inter rows][..]: one copy brings 8 rows of
 // gate and the same 8 of up.  Boxes: codes {128 bytes, 8 rows, 2} with the

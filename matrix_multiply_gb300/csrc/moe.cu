@@ -90,11 +90,11 @@ __device__ __forceinline__ float warp_sum(float v)
 // flips when the last has arrived, and it needs no reset.  The wait is
 // bounded: past the limit the kernel reports and goes on, its outputs
 // undefined.
-__device__ __forceinline__ unsigned grid_arrive(unsigned *sync)
+__device__ __forceinline__ unsigned grid_arrive(unsigned *sync, bool drop = false)
 {
     unsigned old = 0;
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && !drop) {
         const unsigned add = blockIdx.x == 0 ? 0x80000000u - (gridDim.x - 1) : 1u;
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(sync), "r"(add) : "memory");
     }
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
         moe_router<BF16, 2>(a, L);
     else
         moe_router<BF16, 8>(a, L);
-    unsigned old = grid_arrive(a.sync);
+    unsigned old = grid_arrive(a.sync, a.debug_drop == 1 && blockIdx.x == 1);
 
     // what does not depend on the choice, while the others arrive
     const int G1 = (int)gridDim.x, nb = (a.I + 7) >> 3, nbp = (nb + W - 1) / W;      // units and pieces per entry
@@ -367,7 +367,8 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
     // fetching the warp's pieces: stage 1's, then stage 2's
     unsigned f_u = u_first;
     int f_s = 0, f_ent = ent_first, f_b = b_first, f_panel = r_lo, f_i = warp, f_row = 0, f_stage = 0, fetched = 0;
-    const uint32_t bytes1 = W * 2048 + 2 * GP * MOE_SCALE_BOX * 2 + (zeros1 ? 2 * GP * Q4_ZERO_BOX : 0);
+    uint32_t bytes1 = W * 2048 + 2 * GP * MOE_SCALE_BOX * 2 + (zeros1 ? 2 * GP * Q4_ZERO_BOX : 0);
+    if (a.debug_drop == 2 && blockIdx.x == 0) bytes1 += 16;
     const uint32_t bytes2 = min(a.panel, Space::ROWS) * 128 + GP * Space::SCALE2_BOX * 2 + (zeros2 ? GP * Space::ZERO2_BOX : 0);
     const uint32_t leader = elect_one();
     auto fetch = [&]() {                                // the whole warp

@@ -73,7 +73,7 @@ template <bool BF16, bool SBF16, int NT, int G, int MT>
 __global__ void __launch_bounds__(GV_WARPS * 32, 1)
     q4_gemv_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmT,
                    const __grid_constant__ CUtensorMap tmS, const __grid_constant__ CUtensorMap tmZ, int ksplit, int rows,
-                   int nblk, int block_rows, int tail_rows, unsigned *status, unsigned long long timeout_ns)
+                   int nblk, int block_rows, int tail_rows, unsigned *status, unsigned long long timeout_ns, int debug_drop)
 {
     constexpr int GP = Q4_SLAB / G;                // groups per slab
     constexpr int TILE = gv_tile<NT>();
@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
 
     // the warp's pieces, fetched in order
     const uint32_t leader = elect_one();
-    const uint32_t beside = GP * (2 * Stage::SCALE_BOX + (zeros ? Stage::ZERO_BOX : 0));
+    uint32_t beside = GP * (2 * Stage::SCALE_BOX + (zeros ? Stage::ZERO_BOX : 0));
+    if (debug_drop && blockIdx.x == 0) beside += 16;
     // blocks with rows in them
     const int have = nrows == rows ? nblk : (int)((unsigned)(nrows - 1) / (unsigned)block_rows) + 1;
     int f_first = wr, f_h = 0, f_s = 0, fetched = 0;
@@ -317,7 +318,7 @@ cudaError_t launch_one(const Q4GemmArgs &a, const Q4GemvPlan &p, cudaStream_t st
     }
     return launch_dependent(kern, dim3((unsigned)(p.clusters * p.ksplit)), dim3(GV_WARPS * 32), smem, st,
                             (unsigned)p.ksplit, a, p.codes, p.tail, p.scales, p.zeros, p.ksplit, p.rows, p.nblk,
-                            p.block_rows, p.tail_rows, p.status, p.timeout_ns);
+                            p.block_rows, p.tail_rows, p.status, p.timeout_ns, p.debug_drop);
 }
 
 template <bool BF16, bool SBF16, int NT, int G>

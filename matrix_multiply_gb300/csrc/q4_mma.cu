@@ -204,7 +204,7 @@ template <bool BF16, int BN, int G, bool CUT>
 __global__ void __launch_bounds__(QM_THREADS, 1)
     q4_mma_kernel(const Q4GemmArgs a, const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmX,
                   int split, int tiles_m, int units, int whole, float *partial, unsigned *counts, unsigned *status,
-                  unsigned long long timeout_ns)
+                  unsigned long long timeout_ns, int debug_drop)
 {
     constexpr int X_BYTES = BN * 256;              // a block of X: two halves of BN rows x 128 bytes
     constexpr int NG = QM_BK / G;                  // groups per block
@@ -279,7 +279,8 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                     }
                     const int st = xi % QM_XS;
                     if (!(ok = q4_wait(empty + 8 * st, ((xi / QM_XS) & 1) ^ 1, watch))) break;
-                    mbar_arrive_expect_tx(full + 8 * st, X_BYTES);
+                    const bool drop = debug_drop && blockIdx.x == 0 && xi == 2;
+                    mbar_arrive_expect_tx(full + 8 * st, X_BYTES + (drop ? 16 : 0));
                     tma_load_2d(smem_u32(smem) + st * X_BYTES, &tmX, full + 8 * st, kb * QM_BK, w.m0);
                     tma_load_2d(smem_u32(smem) + st * X_BYTES + X_BYTES / 2, &tmX, full + 8 * st, kb * QM_BK + 64, w.m0);
                     ++xi;
@@ -604,7 +605,7 @@ cudaError_t launch_one(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st)
     }
     return launch_dependent(kern, dim3((unsigned)p.grid), dim3(QM_THREADS), smem, st, (unsigned)p.split, a, p.codes, p.x,
                             p.split, p.tiles_m, p.tiles_n * p.tiles_m * p.split, p.whole, p.partial, p.counts, p.status,
-                            p.timeout_ns);
+                            p.timeout_ns, p.debug_drop);
 }
 
 template <bool BF16, int BN>
