@@ -305,7 +305,9 @@ tc_status_t tc_q4_validate(const tc_q4_weight *q, tc_dtype_t dtype, int32_t ld, 
  * and leading dimension; C overlaps none of the inputs.  The products of X
  * with the whole numbers code - zero are exact and summed in fp32 within a
  * group, the groups' sums times their scales are summed in fp32: no weight
- * is rounded to 16 bits on the way.  Deterministic run to run.  Calls of more
+ * is rounded to 16 bits on the way, and no group's sum overflows where its
+ * product with the scale would not.  (For bf16 X these sums are held at 2^-11
+ * of their value: results are kept to 2^-137 per group at best.)  Deterministic run to run.  Calls of more
  * than 16 rows take workspace from the stream: of one size for all of them, and
  * a copy of X (M rows of K rounded up to 64) where its base or rows are off 16
  * bytes.  Before a stream capture make one such call, the largest of those
@@ -335,8 +337,9 @@ tc_status_t tc_gemm_q4_weight_validate(const tc_gemm_desc *d, const tc_q4_weight
  * otherwise) and scale_dtype (TC_ERR_DTYPE).  ids (int32 [tokens, top_k]) and weights
  * (float [tokens, top_k]) receive the chosen experts and their p_j, in
  * descending order of l; either may be NULL.  silu(x) = x / (1 + exp(-x)).
- * h keeps 16 bits of its significand, all 24 where y_dtype is TC_F32, with
- * fp32's exponents; sums are fp32, Y is rounded once.  1 <= tokens <=
+ * h keeps 16 bits of its significand, all 24 where y_dtype is TC_F32 (which is
+ * how a caller gets the layer to fp32 accuracy), with fp32's exponents; sums are
+ * fp32, held as tc_gemm_q4_weight's, Y is rounded once.  1 <= tokens <=
  * TC_MOE_MAX_TOKENS, 1 <= top_k <= min(experts, TC_MOE_MAX_TOPK), experts <=
  * TC_MOE_MAX_EXPERTS (TC_ERR_DIM otherwise, and when the weights' N and K do
  * not fit); Y, ids and weights overlap no input and one another

@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
                 uint32_t part[PARTS] = {};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float gt = half ? v[2 + i] : v[i], up = half ? v[6 + i] : v[4 + i];
+                    const float gt = q4_whole<BF16>(half ? v[2 + i] : v[i]), up = q4_whole<BF16>(half ? v[6 + i] : v[4 + i]);
                     float x = i0 + i < a.I ? gt / (1.0f + expf(-gt)) * up : 0.0f;
 #pragma unroll
                     for (int q = 0; q < PARTS; ++q) {
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(MO_THREADS, 1) moe_kernel(const MoeArgs a, con
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 tok[c] = 2 * t + c < n ? L.tok[at + 2 * t + c] : -1;
-                pw[c] = 2 * t + c < n ? L.p[L.pair[at + 2 * t + c]] : 0.0f;
+                pw[c] = 2 * t + c < n ? q4_whole<true>(L.p[L.pair[at + 2 * t + c]]) : 0.0f;   // (h is bf16)
             }
             for (int row0 = 0; row0 < p_hi - panel; row0 += Space::ROWS) {
                 constexpr int HALVES = Space::ROWS / 16;

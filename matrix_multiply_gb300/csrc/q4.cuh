@@ -43,8 +43,19 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], const uint32_t (&a)[4], ui
     }
 }
 
-// What turns a row's codes into whole numbers code - zero: the zero point in
-// the biased form that q4_widen subtracts.
+// Widened codes are code - zero for f16 and (code - zero) / 2^11 for bf16: bf16
+// activations go up to fp32's largest, and a group's 128 products of up to 15
+// times that must not overflow before the scale brings them down (fp16's largest
+// leaves room).  Exact either way; sums of bf16 products are 2^-11 of what they
+// stand for until q4_whole.
+template <bool BF16>
+__device__ __forceinline__ float q4_whole(float sum)
+{
+    return BF16 ? sum * 2048.0f : sum;
+}
+
+// What turns a row's codes into widened ones: the zero point in the biased
+// form that q4_widen subtracts.
 struct Q4Zero {
     uint32_t a, b;
 };
@@ -52,15 +63,15 @@ template <bool BF16>
 __device__ __forceinline__ Q4Zero q4_zero_form(uint32_t z)
 {
     const uint32_t zz = z * 0x00010001u;
-    if constexpr (BF16) return Q4Zero{0x43004300u | zz, 0u};             // 128 + z
+    if constexpr (BF16) return Q4Zero{0x3D803D80u | zz, 0u};             // (128 + z) / 2^11
     return Q4Zero{0x64006400u | zz, 0xD400D400u | (zz << 4)};            // 1024 + z and -(64 + z)
 }
 
-// The word's eight codes minus the zero point as four pairs of exact 16-bit
-// floats (elements 0 1 | 2 3 | 4 5 | 6 7).  A masked nibble put under the
-// exponent of 2^10 (f16) is 1024 + code, or 1024 + 16 code for the nibble
-// above it, which one multiply-add brings back; bf16 has 7 fraction bits, so
-// there every nibble is shifted to the bottom under 2^7.
+// The word's eight codes, widened, as four pairs of exact 16-bit floats
+// (elements 0 1 | 2 3 | 4 5 | 6 7).  A masked nibble put under the exponent of
+// 2^10 (f16) is 1024 + code, or 1024 + 16 code for the nibble above it, which
+// one multiply-add brings back; bf16 has 7 fraction bits, so there every nibble
+// is shifted to the bottom, under 2^-4: (128 + code) / 2^11.
 template <bool BF16>
 __device__ __forceinline__ void q4_widen(uint32_t w, const Q4Zero &z, uint32_t (&p)[4])
 {
@@ -69,7 +80,7 @@ __device__ __forceinline__ void q4_widen(uint32_t w, const Q4Zero &z, uint32_t (
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t v;
-            asm("lop3.b32 %0, %1, 0x000f000f, 0x43004300, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)));
+            asm("lop3.b32 %0, %1, 0x000f000f, 0x3D803D80, 0xEA;" : "=r"(v) : "r"(w >> (4 * i)));
             const __nv_bfloat162 h = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), zz);
             p[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
@@ -110,9 +121,9 @@ __device__ __forceinline__ uint32_t q4_first_word(int g, int t) { return g * 128
 
 // acc[nt] (rows g, g + 8 x X rows 8 nt + 2 t, + 1) += the slab's product with
 // xf: step j's register q holds X row 8 nt + g, k = 32 j + 8 t + 2 q and + 1.
-// Each group's products are summed from zero by the tensor core -- whole
-// numbers times 16-bit floats, exact, added in fp32 -- and join the
-// accumulator times the row's scale.  JOIN: the NT operands are the parts of
+// Each group's products are summed from zero by the tensor core -- widened
+// codes times 16-bit floats, exact, added in fp32 -- and join the
+// accumulator times the row's scale (q4_whole is the caller's).  JOIN: the NT operands are the parts of
 // one (x = part 0 + part 1), their sums join acc[0].  SP, ZP: elements between
 // two groups' scales and zero points.  Every lane of the warp calls it.
 template <bool BF16, bool SBF16, int NT, int G, int SP, bool JOIN = false, int ZP = Q4_ZERO_PITCH>

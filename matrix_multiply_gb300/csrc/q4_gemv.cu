@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
         const int left = min(block_rows, nrows - blk * block_rows) - r;
         if (left <= 0 || col >= a.M) return;
         const long long off = col * a.ldc + r_lo + blk * block_rows + r;
-        v0 *= a.alpha, v1 *= a.alpha;
+        v0 = q4_whole<BF16>(v0) * a.alpha, v1 = q4_whole<BF16>(v1) * a.alpha;
         if (a.beta != 0.0f) {
             v0 = fmaf(a.beta, load_c(a.C, off, a.c_dtype), v0);
             if (left > 1) v1 = fmaf(a.beta, load_c(a.C, off + 1, a.c_dtype), v1);

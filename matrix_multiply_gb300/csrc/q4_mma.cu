@@ -3,8 +3,8 @@
 // columns.
 //
 // W stays 4 bits up to the SM: converter warps (thread = row of W) read the
-// codes that TMA brought to shared memory, turn them into the whole numbers
-// code - zero, exact in X's 16-bit type, and write them to TMEM, from where
+// codes that TMA brought to shared memory, widen them (q4_widen: code - zero,
+// exact in X's 16-bit type) and write them to TMEM, from where
 // the tensor core takes its 128-row operand; X's tiles come through shared
 // memory by TMA.  Each group of k is summed from zero in one of two TMEM
 // accumulators; promoting warps (thread = row of W, so a group's scale is
@@ -128,13 +128,13 @@ __device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi)
 
 // alpha * sum + beta * C_old of one row of W: C[off + c ldc], c < cols; the
 // lanes of a warp hold neighbouring rows
-template <int DT, int HB>
+template <int DT, int HB, bool BF16>
 __device__ __forceinline__ void store_columns(const Q4GemmArgs &a, long long off, int cols, const uint64_t (&acc)[HB / 2])
 {
     const bool whole = cols >= HB && a.beta == 0.0f;
 #pragma unroll
     for (int c = 0; c < HB; ++c) {
-        float v = a.alpha * __uint_as_float(c & 1 ? (uint32_t)(acc[c / 2] >> 32) : (uint32_t)acc[c / 2]);
+        float v = a.alpha * q4_whole<BF16>(__uint_as_float(c & 1 ? (uint32_t)(acc[c / 2] >> 32) : (uint32_t)acc[c / 2]));
         if (!whole) {
             if (c >= cols) break;
             if (a.beta != 0.0f) v = fmaf(a.beta, load_c(a.C, off, DT), v);
@@ -549,9 +549,9 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
                 const int cols = min(HB, a.M - w.m0 - half * HB);
                 const long long off = (long long)(w.m0 + half * HB) * a.ldc + n;
                 if (a.c_dtype == TC_F32)
-                    store_columns<TC_F32, HB>(a, off, cols, acc);
+                    store_columns<TC_F32, HB, BF16>(a, off, cols, acc);
                 else
-                    store_columns<BF16 ? TC_BF16 : TC_F16, HB>(a, off, cols, acc);
+                    store_columns<BF16 ? TC_BF16 : TC_F16, HB, BF16>(a, off, cols, acc);
             }
         }
     }
@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(QM_THREADS, 1)
 #pragma unroll
             for (int q = 1; q < 8; ++q)
                 if (q < split) v += p[q];
-            v *= a.alpha;
+            v = q4_whole<BF16>(v) * a.alpha;
             const long long off = (long long)(w.m0 + c) * a.ldc + n;
             if (a.beta != 0.0f) v = fmaf(a.beta, load_c(a.C, off, a.c_dtype), v);
             store_c1(a.C, off, v, a.c_dtype);
