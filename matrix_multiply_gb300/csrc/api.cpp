@@ -55,6 +55,7 @@ struct tc_ctx {
     int max_pairs[3] = {-1, -1, -1};               // resident CTA pairs (BN 128, 192, 256), queried once
     int csplit_clusters[2][17];                    // resident cluster splits (BN 64, 128; S), -1 = not queried
     int q4_clusters[9] = {-1, -1, -1, -1, -1, -1, -1, -1, -1};   // resident clusters of the 4-bit streaming kernel
+    int q4_mma_clusters[9] = {-1, -1, -1, -1, -1, -1, -1, -1, -1};   // and of its tensor-core kernel
     std::mutex mu;
     tc_ctx()
     {
@@ -1622,13 +1623,22 @@ tc_status_t reserve_q4(tc_ctx *ctx, tc_stream *s, size_t ws, size_t rx)
 // a tile takes 1 besides.  Shared out
 //   whole          in turn: 4096 x 11008 x 4096 330, cut 359
 //   in a cluster   K slices of each tile, where the tiles leave SMs idle: the
-//                  sums on chip take 2 to 7 (100 x 4096 x 4096: 13.3, whole 22)
+//                  sums on chip take 2 to 7 (100 x 4096 x 4096: 13.3, whole 22).
+//                  As many slices as leave all clusters resident at once: 15 of
+//                  7 or 8 CTAs are (32 x 2048 x 4096, 16 tiles: 8 slices 14.0, 7
+//                  15.3, 6 7.9; 32 x 1920 x 4096, 15 tiles: 7.5, 8.1, 7.9)
 //   cut            the last tiles in equal ranges, where the last wave of whole
 //                  ones is short: the sums in memory take 9, and this kernel is
 //                  7% slower per k (200 x 11008 x 4096: 31.3, whole 37.6;
 //                  384 rows: 42.4, whole 40.5)
-void plan_q4_mma(int num_sms, const Q4GemmArgs &a, const Force &f, Q4MmaPlan *p)
+void plan_q4_mma(tc_ctx *ctx, const Q4GemmArgs &a, const Force &f, Q4MmaPlan *p)
 {
+    const int num_sms = ctx->num_sms;
+    const auto resident = [&](int split) {
+        int &n = ctx->q4_mma_clusters[split];
+        if (n < 0) n = q4_mma_max_clusters(split);
+        return n;
+    };
     const int64_t pairs = cdiv(a.q.K, 256), tn = cdiv(a.q.N, Q4_MMA_ROWS);
     double best = 0.0;
     p->bn = 0;
@@ -1655,6 +1665,7 @@ void plan_q4_mma(int num_sms, const Q4GemmArgs &a, const Force &f, Q4MmaPlan *p)
         }
         int split = f.split > 0 ? std::min(f.split, 8) : (int)std::min<int64_t>(8, num_sms / tiles);
         split = (int)std::min<int64_t>(split, f.split > 0 ? pairs : pairs / 2);
+        while (split > 1 && resident(split) < (f.split > 0 ? 1 : tiles)) --split;
         if (split > 1)
             take((double)cdiv(pairs, split) * pair + 1.0 + bn * (0.03 + 0.05 / split), split, tiles, tiles * split);
         else
@@ -1663,14 +1674,14 @@ void plan_q4_mma(int num_sms, const Q4GemmArgs &a, const Force &f, Q4MmaPlan *p)
     if (p->bn == 0) {          // a forced width this kernel does not have
         Force g = f;
         g.bn = 0;
-        plan_q4_mma(num_sms, a, g, p);
+        plan_q4_mma(ctx, a, g, p);
     }
 }
 
 tc_status_t enqueue_q4_mma(tc_ctx *ctx, tc_stream *s, Q4GemmArgs a, const Force &f)
 {
     Q4MmaPlan p{};
-    plan_q4_mma(ctx->num_sms, a, f, &p);
+    plan_q4_mma(ctx, a, f, &p);
     if ((int64_t)p.tiles_n * p.tiles_m * p.split > INT32_MAX / 2) return TC_ERR_OVERFLOW;
     int launches = 1;
     // rows TMA cannot address: a copy with padded rows in the stream's buffer

@@ -403,6 +403,8 @@ struct Q4MmaPlan {
     int debug_drop;            // test hook: the first CTA's third copy of X never completes
 };
 cudaError_t launch_q4_mma(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st);
+// clusters of `split` CTAs of that kernel resident at once (0: none)
+int q4_mma_max_clusters(int split);
 
 // The mixture-of-experts layer (the public header states the formulas): one
 // cooperative launch of `grid` CTAs (moe.cu).

@@ -626,6 +626,28 @@ cudaError_t launch_group(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t s
 
 }  // namespace
 
+int q4_mma_max_clusters(int split)
+{
+    // (every instantiation fills an SM: one stands for all)
+    constexpr auto kern = q4_mma_kernel<true, 128, 128, false>;
+    constexpr int smem = qm_smem(128);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)split);
+    cfg.blockDim = dim3(QM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+    return n;
+}
+
 cudaError_t launch_q4_mma(const Q4GemmArgs &a, const Q4MmaPlan &p, cudaStream_t st)
 {
     if (p.split < 1 || p.split > 8 || p.grid < 1 || p.grid % p.split != 0 ||
