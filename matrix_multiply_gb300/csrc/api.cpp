@@ -1618,19 +1618,21 @@ tc_status_t reserve_q4(tc_ctx *ctx, tc_stream *s, size_t ws, size_t rx)
 // The tensor-core kernel's tile width and how its tiles are shared out: the
 // least estimated time, in us beyond a launch's own, from times measured over
 // 17 to 4096 rows of three weights (4096 x 4096 to 11008 x 4096, groups of
-// 128; smaller groups slow all of them alike).  256 k of a tile take 0.8 to
-// 1.07 by its width -- converting the 128 rows of W is the greater part -- and
-// a tile takes 1 besides.  Shared out
-//   whole          in turn: 4096 x 11008 x 4096 330, cut 359
+// 128).  256 k of a tile take 0.8 to 1.07 by its width -- converting the 128
+// rows of W is the greater part -- and a tile takes 1 besides.  Smaller groups
+// take the same plans: 512 x 11008 x 4096 in tiles of 96, 64 and 32 columns
+// takes 69, 79 and 140 with groups of 128, 93, 105 and 160 with 64, 156, 180
+// and 249 with 32, the same order.  Shared out
+//   whole          in turn: 4096 x 11008 x 4096 329, cut 356
 //   in a cluster   K slices of each tile, where the tiles leave SMs idle: the
-//                  sums on chip take 2 to 7 (100 x 4096 x 4096: 13.3, whole 22).
+//                  sums on chip take 2 to 7 (100 x 4096 x 4096: 13.7, whole 20.8).
 //                  As many slices as leave all clusters resident at once: 15 of
 //                  7 or 8 CTAs are (32 x 2048 x 4096, 16 tiles: 8 slices 14.0, 7
 //                  15.3, 6 7.9; 32 x 1920 x 4096, 15 tiles: 7.5, 8.1, 7.9)
 //   cut            the last tiles in equal ranges, where the last wave of whole
 //                  ones is short: the sums in memory take 9, and this kernel is
-//                  7% slower per k (200 x 11008 x 4096: 31.3, whole 37.6;
-//                  384 rows: 42.4, whole 40.5)
+//                  7% slower per k (200 x 11008 x 4096: 32.4, whole 38.6;
+//                  384 rows: 42.4, whole 39.0)
 void plan_q4_mma(tc_ctx *ctx, const Q4GemmArgs &a, const Force &f, Q4MmaPlan *p)
 {
     const int num_sms = ctx->num_sms;

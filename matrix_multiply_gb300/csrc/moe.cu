@@ -15,16 +15,17 @@
 // second barrier, since which weights stage 2 reads does not depend on h.  h
 // is kept as a sum of bf16 parts, multiplied one after the other: two of them
 // (16 bits of significand, any exponent) where y has 16 bits, 11 of them
-// significant at most; three (all 24 bits) where y is fp32.  Deterministic:
-// lists in index order, sums in fixed orders.
+// significant at most (of 2048 bf16 outputs of one token 9 are not the nearest to
+// their 64-bit values, of the same formulas in fp32 4); three (all 24 bits) where
+// y is fp32.  Deterministic: lists in index order, sums in fixed orders.
 //
 // Measured: 1 token, hidden 2048, inter 768, 8 of 64 experts, groups of 128:
-// 18.1 us for 19.7 MB, of which the launch takes 3.1, each stage's dependent
+// 18.4 us for 20.0 MB, of which the launch takes 3.1, each stage's dependent
 // loads, barriers and first passes through its code the rest.  16 tokens,
 // hidden 4096, inter 1408, 8 of 64, groups of 64 with zero points: 174 us for
-// about 530 MB, 45% of a plain copy's rate, bound by issue and the fixed
-// latencies of the widening chain (about 480 instructions per 16 rows x 256 k;
-// schedulers issue in 61% of the cycles), with pieces of 16 rows 186.  As separate launches the stages
+// about 535 MB, 46% of a plain copy's rate, bound by issue and the fixed
+// latencies of the widening chain (about 460 instructions per 16 rows x 256 k;
+// schedulers issue in 56% of the cycles), with pieces of 16 rows 186.  As separate launches the stages
 // would add two of them, with their drains, to every call.
 #include "q4.cuh"
 

@@ -9,9 +9,9 @@
 // memory and leave as 32-byte pieces.
 //
 // What bounds it: reading back, HBM; quantising, issue -- 154 instructions for
-// a warp's 256 weights, most of them the exact ties of the rounding.
+// a warp's 256 weights, 24 of them the test for exact ties of the rounding.
 // Measured, quantising and reading back together: 65536 x 4096 f16, groups of
-// 64 with zero points, 288 us for 1.37 GB, 70% of a plain copy's rate (162 and
+// 64 with zero points, 288 us for 1.37 GB, 71% of a plain copy's rate (162 and
 // 139 us, 4.1 and 4.9 TB/s, under the profiler); 4096 x 4096 bf16 24 us;
 // 1001 x 2999 fp32 with padded rows 15 us.
 #include "q4.cuh"

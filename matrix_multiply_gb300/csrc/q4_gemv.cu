@@ -21,13 +21,13 @@
 //
 // Measured (M x N x K, X and C in 16 bits but where said), with the share of
 // a plain copy's rate that the bytes come to:
-//   1 x 4096 x 4096, groups of 128              4.4 us   29%
-//   4 x 4096 x 11008, of 64 with zero points    8.9 us   41%
-//   16 x 11008 x 4096, of 32, C in fp32        12.7 us   30%
-// An empty launch takes 3.1; after it the kernel is bound by the issue of the
-// widening and its bookkeeping (about 230 instructions per 16 rows x 256 k in
-// q4_slab for groups of 128, and 130 for each piece of the ring; schedulers
-// issue in half of the cycles, 16 warps being what the registers hold), not by
+//   1 x 4096 x 4096, groups of 128              4.3 us   30%
+//   4 x 4096 x 11008, of 64 with zero points    8.8 us   42%
+//   16 x 11008 x 4096, of 32, C in fp32        12.4 us   32%
+// An empty launch takes 3.1; after it the kernel is bound by the issue and the
+// latencies of the widening and its bookkeeping (per 16 rows x 256 k 420
+// instructions in all at the second of these, 590 at the third; schedulers
+// issue in 45% of the cycles, 16 warps being what the registers hold), not by
 // HBM.  mma.sync
 // rather than tcgen05: with at most 16 columns the tensor cores are idle
 // either way, and W goes from the ring to the operand's registers without a
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(GV_WARPS * 32, 1)
         wk = warp - wr * mine;
     }
     const bool active = wr < wr_n;
-    // slabs of this warp in every block: one, unless K is above 4096 * 8
+    // slabs of this warp in every block: one, unless the CTA's part of K is above 4096
     const int per = !active ? 0 : mine <= GV_WARPS ? 1 : (mine - wk + GV_WARPS - 1) / GV_WARPS;
     const long long r_lo = (long long)cluster * rows;
     const int nrows = (int)min((long long)rows, a.q.N - r_lo);

@@ -26,11 +26,14 @@
 // What bounds it: the warps that convert.  256 k of a 128 x 128 tile take
 // 1.07 us, twice the tensor core's time for it; of the ~600
 // instructions per 128 k and scheduler two thirds widen codes, one warp's
-// chain of them with the stores to TMEM.  Wider tiles do not fit: the operand's
-// stages and two accumulators fill TMEM, the sums the registers.
-// Measured: 4096 x 11008 x 4096 (M x N x K, bf16, groups of 128 with zero
-// points) 329 us, 1.12 PFLOP/s, 60% of a bf16 product's measured rate;
-// 200 x 11008 x 4096 33 us; 17 x 4096 x 4096 9.3 us.  The plan's figures stand
+// chain of them with the stores to TMEM.  Wider tiles, which would convert
+// less often, have not been built: 160 columns fill TMEM with two accumulators
+// and three operand stages, and their sums would need registers moved from
+// other warps to the promoting ones.  The kernels of 128 and of 64 columns
+// spill 44 to 52 bytes a thread.
+// Measured: 4096 x 11008 x 4096 (M x N x K, bf16, groups of 128) 330 us, 1.12
+// PFLOP/s, 58% of a bf16 product's measured rate, groups of 64 449, of 32 800;
+// 200 x 11008 x 4096 33 us; 17 x 4096 x 4096 10 us.  The plan's figures stand
 // beside its cost model.
 #include "q4.cuh"
 
