@@ -49,8 +49,8 @@ extern "C" {
 
 /* TC_I8 / TC_I32: operands and accumulator of tc_gemm_i8_dequant; TC_I8
  * also the weight type of tc_gemm_q8_weight; TC_I4 the weight type of
- * tc_gemm_q4_weight. */
-typedef enum { TC_F16 = 1, TC_BF16 = 2, TC_F32 = 3, TC_I8 = 4, TC_I32 = 5, TC_I4 = 6 } tc_dtype_t;
+ * tc_gemm_q4_weight.  TC_I32 / TC_I64: the targets of tc_linear_xent. */
+typedef enum { TC_F16 = 1, TC_BF16 = 2, TC_F32 = 3, TC_I8 = 4, TC_I32 = 5, TC_I4 = 6, TC_I64 = 7 } tc_dtype_t;
 
 typedef enum {
     TC_OK = 0,
@@ -58,7 +58,7 @@ typedef enum {
     TC_ERR_DIM = 2,                /* M, N or K outside [1, 2^31-1]; batch < 1 */
     TC_ERR_LD = 3,                 /* a leading dimension below its minimum, or negative */
     TC_ERR_DTYPE = 4,              /* unsupported dtype combination */
-    TC_ERR_SCALAR = 5,             /* alpha or beta not finite */
+    TC_ERR_SCALAR = 5,             /* alpha or beta not finite; a scale or weight of tc_linear_xent out of its range */
     TC_ERR_OVERLAP = 6,            /* C's byte range overlaps A's or B's */
     TC_ERR_OVERFLOW = 7,           /* an element or byte count overflows int64 */
     TC_ERR_ALIGN_UNSUPPORTED = 8,  /* tc_gemm_splitk_noalloc: operands TMA cannot read in place; tc_q4_weight: a base off 16 bytes */
@@ -67,7 +67,7 @@ typedef enum {
     TC_ERR_STRIDE = 11,            /* batched: negative stride */
     TC_ERR_VARIANT = 12,           /* a forced variant cannot serve this problem */
     TC_ERR_SCRATCH = 13,           /* tc_gemm_splitk_noalloc: more scratch than its static buffer holds */
-    TC_ERR_EPILOGUE = 14,          /* fused epilogue: unknown activation, or f32 operands (see tc_gemm_epilogue) */
+    TC_ERR_EPILOGUE = 14,          /* fused epilogue: unknown activation or reduction, or f32 operands (see tc_gemm_epilogue) */
     TC_ERR_LAYOUT = 15             /* transpose flags the call does not support (tc_gemm_q8_weight) */
 } tc_status_t;
 
@@ -364,6 +364,68 @@ tc_status_t tc_moe_q4_async(tc_ctx *ctx, const tc_moe_desc *d, const void *X, co
 /* Host-only: the validation tc_moe_q4 runs first. */
 tc_status_t tc_moe_q4_validate(const tc_moe_desc *d, const void *X, const void *router, const tc_q4_weight *gate_up,
                                const tc_q4_weight *down, const void *Y, const int32_t *ids, const float *weights);
+
+/* ---- Training losses.
+ *
+ * Softmax cross entropy of hidden rows X [tokens, hidden] against a
+ * vocabulary's rows W [vocab, hidden], with targets y, without the logits ever
+ * being kept:
+ *   l[t, v] = scale * sum_h X[t, h] W[v, h]
+ *   lse[t]  = log sum_v exp(l[t, v])
+ *   loss[t] = lse[t] - l[t, y_t] + z_weight * lse[t]^2
+ * A row whose target is outside [0, vocab) (-100, say) does not count: its
+ * loss is 0, and it adds nothing to any gradient, whatever it holds.  loss
+ * receives the rows' losses (TC_REDUCE_NONE, tokens floats), their sum, or
+ * their mean over the rows that count, 0 if there are none (one float); lse
+ * (tokens floats, every row's) is what the backward call needs.
+ *
+ * The gradients, given grad, the gradient that arrives at loss (tokens floats
+ * or one, as loss):
+ *   g[t]    = grad[t], grad[0], or grad[0] / (rows that count)
+ *   G[t, v] = g[t] * ((1 + 2 z_weight lse[t]) exp(l[t, v] - lse[t]) - [v = y_t])
+ *   dX = scale * G W [tokens, hidden],  dW = scale * G^T X [vocab, hidden]
+ * Either of dX and dW may be NULL, for a frozen head or hidden rows that need
+ * none.  The logits are computed again, a piece of the vocabulary at a time.
+ *
+ * X and W have one dtype, TC_F16 or TC_BF16 (TC_ERR_DTYPE otherwise); dX and
+ * dW have grad_dtype, the same or TC_F32; target_dtype is TC_I32 or TC_I64.
+ * Logits, statistics and sums are fp32 (a reduced loss is summed in 64 bits).
+ * G is rounded to dtype for its products, for TC_F32 gradients it is held in
+ * two such parts, which doubles those products; with TC_F16 it is scaled by a
+ * power of two on the way, so that small gradients keep their bits.  scale is
+ * finite and above 0, z_weight finite and at least 0 (TC_ERR_SCALAR).  Leading
+ * dimensions as in tc_gemm, any alignment (a W that TMA cannot read in place,
+ * base or rows off 16 bytes, is copied piece by piece).  Outputs overlap no
+ * input and one another (TC_ERR_OVERLAP).  Deterministic run to run.
+ *
+ * Takes workspace from the stream: forward about tokens * vocab / 16 bytes
+ * (those statistics), backward up to 256 MiB for a piece of G and copies of
+ * X and, in fp32, dX.  Before a stream capture make the call that needs most; a
+ * captured call that would have to allocate returns TC_ERR_CUDA and captures
+ * nothing.  Graphs captured on one stream share its workspace: replays of them
+ * must not overlap. */
+typedef enum { TC_REDUCE_NONE = 0, TC_REDUCE_SUM = 1, TC_REDUCE_MEAN = 2 } tc_reduction_t;
+typedef struct {
+    int32_t tokens, hidden, vocab;
+    tc_dtype_t dtype, grad_dtype, target_dtype;
+    tc_reduction_t reduction;
+    float scale, z_weight;
+    int32_t ldx, ldw, lddx, lddw;
+} tc_xent_desc;
+tc_status_t tc_linear_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                           float *loss, float *lse);
+tc_status_t tc_linear_xent_async(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                                 float *loss, float *lse, tc_stream *s);
+tc_status_t tc_linear_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W,
+                                    const void *targets, const float *lse, const float *grad, void *dX, void *dW);
+tc_status_t tc_linear_xent_backward_async(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W,
+                                          const void *targets, const float *lse, const float *grad, void *dX, void *dW,
+                                          tc_stream *s);
+/* Host-only: the validation the calls run first. */
+tc_status_t tc_linear_xent_validate(const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                                    const float *loss, const float *lse);
+tc_status_t tc_linear_xent_backward_validate(const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                                             const float *lse, const float *grad, const void *dX, const void *dW);
 
 /* Same GEMM with HOST operands: copies A and B (and C when beta != 0) to the
  * device, runs, copies C back and waits.  Device buffers are cached in the

@@ -33,7 +33,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libtcgemm.so")
 
 # ------------------------------------------------------------------ enums
 
-TC_F16, TC_BF16, TC_F32, TC_I8, TC_I32, TC_I4 = 1, 2, 3, 4, 5, 6
+TC_F16, TC_BF16, TC_F32, TC_I8, TC_I32, TC_I4, TC_I64 = 1, 2, 3, 4, 5, 6, 7
 STATUS = {
     0: "TC_OK", 1: "TC_ERR_NULL", 2: "TC_ERR_DIM", 3: "TC_ERR_LD", 4: "TC_ERR_DTYPE",
     5: "TC_ERR_SCALAR", 6: "TC_ERR_OVERLAP", 7: "TC_ERR_OVERFLOW", 8: "TC_ERR_ALIGN_UNSUPPORTED",
@@ -89,6 +89,18 @@ class tc_moe_desc(ctypes.Structure):
                 ("ldx", ctypes.c_int32), ("ld_router", ctypes.c_int32), ("ldy", ctypes.c_int32)]
 
 
+TC_REDUCE_NONE, TC_REDUCE_SUM, TC_REDUCE_MEAN = 0, 1, 2
+_REDUCTIONS = {"none": TC_REDUCE_NONE, "sum": TC_REDUCE_SUM, "mean": TC_REDUCE_MEAN}
+
+
+class tc_xent_desc(ctypes.Structure):
+    """A softmax cross entropy against a vocabulary (see include/tcgemm.h)."""
+    _fields_ = [("tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("target_dtype", ctypes.c_int),
+                ("reduction", ctypes.c_int), ("scale", ctypes.c_float), ("z_weight", ctypes.c_float),
+                ("ldx", ctypes.c_int32), ("ldw", ctypes.c_int32), ("lddx", ctypes.c_int32), ("lddw", ctypes.c_int32)]
+
+
 class TcError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -109,6 +121,7 @@ def _load():
     E = ctypes.POINTER(tc_epilogue)
     Q = ctypes.POINTER(tc_q4_weight)
     MD = ctypes.POINTER(tc_moe_desc)
+    XD = ctypes.POINTER(tc_xent_desc)
     i32 = ctypes.c_int32
     sig = {
         "tc_ctx_create": (st, [ctypes.POINTER(vp), ctypes.c_int]),
@@ -145,6 +158,12 @@ def _load():
         "tc_moe_q4": (st, [vp, MD, vp, vp, Q, Q, vp, vp, vp]),
         "tc_moe_q4_async": (st, [vp, MD, vp, vp, Q, Q, vp, vp, vp, vp]),
         "tc_moe_q4_validate": (st, [MD, vp, vp, Q, Q, vp, vp, vp]),
+        "tc_linear_xent": (st, [vp, XD, vp, vp, vp, vp, vp]),
+        "tc_linear_xent_async": (st, [vp, XD, vp, vp, vp, vp, vp, vp]),
+        "tc_linear_xent_backward": (st, [vp, XD, vp, vp, vp, vp, vp, vp, vp]),
+        "tc_linear_xent_backward_async": (st, [vp, XD, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "tc_linear_xent_validate": (st, [XD, vp, vp, vp, vp, vp]),
+        "tc_linear_xent_backward_validate": (st, [XD, vp, vp, vp, vp, vp, vp, vp]),
         "tc_gemm_host": (st, [vp, D, vp, vp, vp]),
         "tc_gemm_splitk_noalloc": (st, [D, vp, vp, vp, ctypes.c_int, vp]),
         "tc_gemm_validate": (st, [D, vp, vp, vp]),
@@ -174,6 +193,8 @@ EXPORTED = (
     "tc_quantize_q4", "tc_quantize_q4_async", "tc_dequantize_q4", "tc_dequantize_q4_async", "tc_q4_validate",
     "tc_gemm_q4_weight", "tc_gemm_q4_weight_async", "tc_gemm_q4_weight_validate",
     "tc_moe_q4", "tc_moe_q4_async", "tc_moe_q4_validate",
+    "tc_linear_xent", "tc_linear_xent_async", "tc_linear_xent_backward", "tc_linear_xent_backward_async",
+    "tc_linear_xent_validate", "tc_linear_xent_backward_validate",
 )
 
 
@@ -189,7 +210,7 @@ def _check(status: int, what: str):
 
 # ------------------------------------------------------------------ helpers
 
-_DT_NAMES = {"f16": TC_F16, "bf16": TC_BF16, "f32": TC_F32, "i8": TC_I8, "i4": TC_I4}
+_DT_NAMES = {"f16": TC_F16, "bf16": TC_BF16, "f32": TC_F32, "i8": TC_I8, "i4": TC_I4, "i32": TC_I32, "i64": TC_I64}
 
 
 def _torch_dtype_code(t) -> int:
@@ -696,6 +717,126 @@ def tc_moe_q4_validate(d: tc_moe_desc, gate_up: tc_q4_weight, down: tc_q4_weight
     """Host-only validation status of a mixture-of-experts layer."""
     return int(_lib.tc_moe_q4_validate(ctypes.byref(d), _addr(X), _addr(router), ctypes.byref(gate_up),
                                        ctypes.byref(down), _addr(Y), _addr(ids) or None, _addr(weights) or None))
+
+
+def make_xent_desc(tokens, hidden, vocab, dtype, grad_dtype=None, *, reduction="mean", scale=1.0, z_weight=0.0,
+                   target_dtype="i64", ldx=0, ldw=0, lddx=0, lddw=0) -> tc_xent_desc:
+    """reduction: "none", "sum" or "mean" (or a TC_REDUCE_* code)."""
+    dt = _DT_NAMES.get(dtype, dtype)
+    return tc_xent_desc(tokens, hidden, vocab, dt, _DT_NAMES.get(grad_dtype, grad_dtype) if grad_dtype is not None else dt,
+                        _DT_NAMES.get(target_dtype, target_dtype), _REDUCTIONS.get(reduction, reduction), float(scale),
+                        float(z_weight), ldx, ldw, lddx, lddw)
+
+
+def _check_operand(name: str, t, n_elems: int, code: int):
+    """Capacity in elements, and the type they are counted in."""
+    import torch
+    _require(t, n_elems, name)
+    types = {TC_F16: torch.float16, TC_BF16: torch.bfloat16, TC_F32: torch.float32, TC_I32: torch.int32,
+             TC_I64: torch.int64}
+    if t is not None and not isinstance(t, int) and t.dtype != types.get(code, t.dtype):
+        raise ValueError(f"{name} is {t.dtype}, the call needs {types[code]}")
+
+
+def _check_vector(name: str, t, n_elems: int, code: int):
+    _check_operand(name, t, n_elems, code)
+    if t is not None and not isinstance(t, int) and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _check_rows(name: str, t, rows: int, cols: int, ld: int, code: int):
+    """A matrix at the descriptor's leading dimension, which a 2-D tensor must have."""
+    _check_operand(name, t, _extent(rows, cols, ld or cols), code)
+    if t is None or isinstance(t, int):
+        return
+    if t.dim() == 2 and ((cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or cols))):
+        raise ValueError(f"{name} has strides {tuple(t.stride())}, the descriptor rows of {cols} at {ld or cols}")
+
+
+class PreparedXent:
+    """A softmax cross entropy against a vocabulary (tc_linear_xent) with its
+    arguments checked and marshalled once: X [tokens, hidden], W [vocab,
+    hidden], targets [tokens], lse [tokens].  With ``loss`` (tokens floats, or
+    one where the descriptor reduces), enqueue() writes it and lse; with
+    ``grad`` (as loss) and ``dX`` and/or ``dW``, enqueue_backward() writes
+    those from lse.  One C call each; the tensors stay referenced as long as
+    this object."""
+
+    def __init__(self, ctx: Context, d: tc_xent_desc, X, W, targets, lse, stream: Stream | None = None, *, loss=None,
+                 grad=None, dX=None, dW=None):
+        vp = ctypes.c_void_p
+        if loss is None and grad is None:
+            raise ValueError("give loss, or grad with dX or dW")
+        if (grad is None) != (dX is None and dW is None):
+            raise ValueError("grad comes with dX or dW")
+        if min(d.tokens, d.hidden, d.vocab) >= 1:
+            n = d.tokens if d.reduction == TC_REDUCE_NONE else 1
+            _check_rows("X", X, d.tokens, d.hidden, d.ldx, d.dtype)
+            _check_rows("W", W, d.vocab, d.hidden, d.ldw, d.dtype)
+            _check_rows("dX", dX, d.tokens, d.hidden, d.lddx, d.grad_dtype)
+            _check_rows("dW", dW, d.vocab, d.hidden, d.lddw, d.grad_dtype)
+            _check_vector("targets", targets, d.tokens, d.target_dtype)
+            for name, t, count in (("lse", lse, d.tokens), ("loss", loss, n), ("grad", grad, n)):
+                _check_vector(name, t, count, TC_F32)
+        head = (vp(ctx.ptr), ctypes.byref(d), vp(_addr(X)), vp(_addr(W)), vp(_addr(targets)))
+        self._forward = head + (vp(_addr(loss)), vp(_addr(lse))) if loss is not None else None
+        self._backward = head + (vp(_addr(lse)), vp(_addr(grad)), vp(_addr(dX) or None), vp(_addr(dW) or None)) \
+            if grad is not None else None
+        self._stream = vp(stream.ptr) if stream is not None else None
+        self._keep = (ctx, d, X, W, targets, lse, stream, loss, grad, dX, dW)
+
+    def _call(self, name: str, args, wait: bool):
+        if args is None:
+            raise ValueError(f"{name} was not prepared: " + ("give loss" if "backward" not in name else "give grad"))
+        if wait:
+            return _check(getattr(_lib, name)(*args), name)
+        if self._stream is None:
+            raise ValueError("enqueueing needs the stream the call was prepared with")
+        _check(getattr(_lib, name + "_async")(*args, self._stream), name + "_async")
+
+    def enqueue(self):
+        self._call("tc_linear_xent", self._forward, False)
+
+    def run(self):
+        self._call("tc_linear_xent", self._forward, True)
+
+    def enqueue_backward(self):
+        self._call("tc_linear_xent_backward", self._backward, False)
+
+    def run_backward(self):
+        self._call("tc_linear_xent_backward", self._backward, True)
+
+
+def tc_linear_xent(ctx: Context, d: tc_xent_desc, X, W, targets, loss, lse):
+    """Softmax cross entropy of X's rows against W's (include/tcgemm.h),
+    synchronously."""
+    PreparedXent(ctx, d, X, W, targets, lse, loss=loss).run()
+
+
+def tc_linear_xent_async(ctx: Context, d: tc_xent_desc, X, W, targets, loss, lse, stream: Stream):
+    PreparedXent(ctx, d, X, W, targets, lse, stream, loss=loss).enqueue()
+
+
+def tc_linear_xent_backward(ctx: Context, d: tc_xent_desc, X, W, targets, lse, grad, dX=None, dW=None):
+    """Its gradients (either may be None) from the lse it wrote, synchronously."""
+    PreparedXent(ctx, d, X, W, targets, lse, grad=grad, dX=dX, dW=dW).run_backward()
+
+
+def tc_linear_xent_backward_async(ctx: Context, d: tc_xent_desc, X, W, targets, lse, grad, dX, dW, stream: Stream):
+    PreparedXent(ctx, d, X, W, targets, lse, stream, grad=grad, dX=dX, dW=dW).enqueue_backward()
+
+
+def tc_linear_xent_validate(d: tc_xent_desc, X=1 << 20, W=1 << 40, targets=2 << 40, loss=3 << 40, lse=4 << 40) -> int:
+    """Host-only validation status of a softmax cross entropy."""
+    return int(_lib.tc_linear_xent_validate(ctypes.byref(d) if d is not None else None, _addr(X), _addr(W),
+                                            _addr(targets), _addr(loss), _addr(lse)))
+
+
+def tc_linear_xent_backward_validate(d: tc_xent_desc, X=1 << 20, W=1 << 40, targets=2 << 40, lse=4 << 40,
+                                     grad=5 << 40, dX=6 << 40, dW=7 << 40) -> int:
+    return int(_lib.tc_linear_xent_backward_validate(ctypes.byref(d) if d is not None else None, _addr(X), _addr(W),
+                                                     _addr(targets), _addr(lse), _addr(grad), _addr(dX) or None,
+                                                     _addr(dW) or None))
 
 
 def tc_gemm_host(ctx: Context, d: tc_gemm_desc, A_host, B_host, C_host):

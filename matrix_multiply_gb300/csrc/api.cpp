@@ -655,11 +655,42 @@ tc_status_t enqueue_gemv(tc_ctx *ctx, tc_stream *s, GemvArgs &g, const Force &f,
     return TC_OK;
 }
 
+// Workspace of one planned problem: [packed A | packed B | split-K partials].
+struct WsLayout {
+    int64_t a_batch, b_batch, lda_p, ldb_p;
+    size_t a_pack_bytes, b_pack_bytes, part_bytes;
+    size_t bytes() const { return a_pack_bytes + b_pack_bytes + part_bytes + 256; }
+};
+
+WsLayout ws_layout(const Norm &n, const Plan &p)
+{
+    WsLayout w;
+    w.a_batch = (n.batch > 1 && n.sa != 0) ? n.batch : 1;
+    w.b_batch = (n.batch > 1 && n.sb != 0) ? n.batch : 1;
+    // repacked rows padded to 64 elements: 128-byte aligned rows for TMA
+    w.lda_p = p.pack_a ? (int64_t)round_up((size_t)n.a_cols, 64) : n.lda;
+    w.ldb_p = p.pack_b ? (int64_t)round_up((size_t)n.b_cols, 64) : n.ldb;
+    w.a_pack_bytes = p.pack_a ? round_up((size_t)(n.a_rows * w.lda_p * w.a_batch * 2), 256) : 0;
+    w.b_pack_bytes = p.pack_b ? round_up((size_t)(n.b_rows * w.ldb_p * w.b_batch * 2), 256) : 0;
+    // K slices summed through global memory
+    w.part_bytes =
+        p.split > 1 && !p.csplit ? (size_t)(p.units - p.split_base) * BM * p.cg * p.bn * sizeof(float) : 0;
+    return w;
+}
+
+// A product whose epilogue is the softmax cross entropy's (internal.h): mode is
+// XENT_LOSS (its C is not written) or XENT_GRAD (C, and `left` when epi.two).
+struct XentJob {
+    int mode;
+    XentEpi epi;
+    void *left;
+};
+
 // int_slices: the int8 path -- K slices hold exact integers and are added
 // as integers (through memory only, never a cluster split).
 tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Plan &plan, const void *A,
                     const void *B, void *C, tc_stream *s, const tc_epilogue *epi = nullptr,
-                    const float *col_scale = nullptr, bool int_slices = false)
+                    const float *col_scale = nullptr, bool int_slices = false, const XentJob *xent = nullptr)
 {
     cudaError_t e;
     Plan p = plan;
@@ -743,18 +774,11 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
         return TC_OK;
     }
 
-    // ---- workspace: [packed A | packed B | split-K partials]
-    const int64_t a_batch = (n.batch > 1 && n.sa != 0) ? n.batch : 1;
-    const int64_t b_batch = (n.batch > 1 && n.sb != 0) ? n.batch : 1;
-    // repacked rows padded to 64 elements: 128-byte aligned rows for TMA
-    const int64_t lda_p = p.pack_a ? (int64_t)round_up((size_t)n.a_cols, 64) : n.lda;
-    const int64_t ldb_p = p.pack_b ? (int64_t)round_up((size_t)n.b_cols, 64) : n.ldb;
-    const size_t a_pack_bytes = p.pack_a ? round_up((size_t)(n.a_rows * lda_p * a_batch * 2), 256) : 0;
-    const size_t b_pack_bytes = p.pack_b ? round_up((size_t)(n.b_rows * ldb_p * b_batch * 2), 256) : 0;
-    const bool partials = p.split > 1 && !p.csplit;     // K slices summed through global memory
-    const size_t part_bytes =
-        partials ? (size_t)(p.units - p.split_base) * BM * p.cg * p.bn * sizeof(float) : 0;
-    tc_status_t st = ensure_ws(s, a_pack_bytes + b_pack_bytes + part_bytes + 256);
+    const WsLayout w = ws_layout(n, p);
+    const int64_t a_batch = w.a_batch, b_batch = w.b_batch, lda_p = w.lda_p, ldb_p = w.ldb_p;
+    const size_t a_pack_bytes = w.a_pack_bytes, b_pack_bytes = w.b_pack_bytes;
+    const bool partials = w.part_bytes > 0;
+    tc_status_t st = ensure_ws(s, w.bytes());
     if (st != TC_OK) return st;
     uint8_t *ws = static_cast<uint8_t *>(s->ws);
     const void *Ause = A, *Buse = B;
@@ -829,6 +853,11 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     a.c_vec_ok = aligned16(C) && (n.ldc * ec) % 16 == 0 && (a.stride_c * ec) % 16 == 0;
     // C written through TMA stores of 32 x 32 chunks when its layout allows
     a.c_tma = a.c_vec_ok && p.tma_store;
+    if (xent) {
+        L.xent = xent->mode;
+        a.x = xent->epi;
+        a.c_tma = xent->mode == XENT_GRAD;
+    }
     a.c_3d = n.batch > 1;
     a.ws = partials ? reinterpret_cast<float *>(ws + a_pack_bytes + b_pack_bytes) : nullptr;
     a.status = s->status_dev;
@@ -886,6 +915,9 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     if (ok && a.ws)
         ok = encode_map(ctx, &L.tmW, TC_F32, a.ws, p.bn, (p.units - p.split_base) * rows_per_tile, p.bn, false, 1,
                         0, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (ok && xent && xent->epi.two)
+        ok = encode_map(ctx, &L.tmW, d->c_dtype, xent->left, d->N, d->M, n.ldc, false, 1, 0, 32, 32,
+                        CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return TC_ERR_CUDA;
     if ((e = launch_mma(L, s->st)) != cudaSuccess) return TC_ERR_CUDA;
     ++launches;
@@ -1873,6 +1905,378 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
     return TC_OK;
 }
 
+// ---------------------------------------------------- softmax cross entropy
+// The products run on the tensor-core kernel, their small companions are in
+// xent.cu; a call's memory is taken before anything of it is launched.
+
+// The stream's two buffers for a call that needs `ws` and `rx` bytes; under
+// stream capture both must be there (what a capture allocates is its graph's).
+tc_status_t reserve(tc_stream *s, size_t ws, size_t rx)
+{
+    if (ws <= s->ws_cap && rx <= s->rx_cap) return TC_OK;
+    cudaStreamCaptureStatus capture;
+    if (cudaStreamIsCapturing(s->st, &capture) != cudaSuccess || capture != cudaStreamCaptureStatusNone) return TC_ERR_CUDA;
+    const tc_status_t st = ensure_ws(s, ws);
+    return st != TC_OK ? st : ensure_rx(s, rx);
+}
+
+struct XentNorm {
+    int64_t ldx, ldw, lddx, lddw;
+    int64_t x_bytes, w_bytes, y_bytes, loss_bytes, lse_bytes;
+};
+
+tc_status_t check_xent(const tc_xent_desc *d, const void *X, const void *W, const void *targets, XentNorm *out)
+{
+    if (!d || !X || !W || !targets) return TC_ERR_NULL;
+    if (d->tokens < 1 || d->hidden < 1 || d->vocab < 1) return TC_ERR_DIM;
+    if ((d->dtype != TC_F16 && d->dtype != TC_BF16) || (d->grad_dtype != d->dtype && d->grad_dtype != TC_F32) ||
+        (d->target_dtype != TC_I32 && d->target_dtype != TC_I64))
+        return TC_ERR_DTYPE;
+    if (d->reduction != TC_REDUCE_NONE && d->reduction != TC_REDUCE_SUM && d->reduction != TC_REDUCE_MEAN)
+        return TC_ERR_EPILOGUE;
+    XentNorm n;
+    n.ldx = d->ldx ? d->ldx : d->hidden;
+    n.ldw = d->ldw ? d->ldw : d->hidden;
+    n.lddx = d->lddx ? d->lddx : d->hidden;
+    n.lddw = d->lddw ? d->lddw : d->hidden;
+    if (n.ldx < d->hidden || n.ldw < d->hidden || n.lddx < d->hidden || n.lddw < d->hidden) return TC_ERR_LD;
+    if (!std::isfinite(d->scale) || d->scale <= 0.0f || !std::isfinite(d->z_weight) || d->z_weight < 0.0f) return TC_ERR_SCALAR;
+    if (!extent(d->tokens, d->hidden, n.ldx, 1, 0, 2, &n.x_bytes) || !extent(d->vocab, d->hidden, n.ldw, 1, 0, 2, &n.w_bytes))
+        return TC_ERR_OVERFLOW;
+    // tiles are counted in 32 bits
+    if (cdiv(d->tokens, BM) * cdiv(d->vocab, BM) > INT32_MAX / 2) return TC_ERR_OVERFLOW;
+    n.y_bytes = (int64_t)d->tokens * (d->target_dtype == TC_I64 ? 8 : 4);
+    n.lse_bytes = (int64_t)d->tokens * 4;
+    n.loss_bytes = d->reduction == TC_REDUCE_NONE ? n.lse_bytes : 4;
+    *out = n;
+    return TC_OK;
+}
+
+struct Range {
+    const void *p;
+    int64_t bytes;
+};
+
+// Outputs (those that are given) against the inputs and one another.
+template <int O, int I>
+tc_status_t check_apart(const Range (&outs)[O], const Range (&ins)[I])
+{
+    for (int i = 0; i < O; ++i) {
+        if (!outs[i].p) continue;
+        for (const Range &r : ins)
+            if (r.p && ranges_overlap(outs[i].p, outs[i].bytes, r.p, r.bytes)) return TC_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].p && ranges_overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return TC_ERR_OVERLAP;
+    }
+    return TC_OK;
+}
+
+tc_status_t validate_xent(const tc_xent_desc *d, const void *X, const void *W, const void *targets, const float *loss,
+                          const float *lse, XentNorm *n)
+{
+    const tc_status_t st = check_xent(d, X, W, targets, n);
+    if (st != TC_OK) return st;
+    if (!loss || !lse) return TC_ERR_NULL;
+    const Range outs[] = {{loss, n->loss_bytes}, {lse, n->lse_bytes}};
+    const Range ins[] = {{X, n->x_bytes}, {W, n->w_bytes}, {targets, n->y_bytes}};
+    return check_apart(outs, ins);
+}
+
+tc_status_t validate_xent_backward(const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                                   const float *lse, const float *grad, const void *dX, const void *dW, XentNorm *n)
+{
+    const tc_status_t st = check_xent(d, X, W, targets, n);
+    if (st != TC_OK) return st;
+    if (!lse || !grad || (!dX && !dW)) return TC_ERR_NULL;
+    const int64_t es = (int64_t)elem_size(d->grad_dtype);
+    int64_t xb, wb;
+    if (!extent(d->tokens, d->hidden, n->lddx, 1, 0, es, &xb) || !extent(d->vocab, d->hidden, n->lddw, 1, 0, es, &wb))
+        return TC_ERR_OVERFLOW;
+    const Range outs[] = {{dX, xb}, {dW, wb}};
+    const Range ins[] = {{X, n->x_bytes}, {W, n->w_bytes}, {targets, n->y_bytes}, {lse, n->lse_bytes}, {grad, n->loss_bytes}};
+    return check_apart(outs, ins);
+}
+
+// Equal pieces of the vocabulary, whole tiles wide, whose memory at `bytes` a
+// column stays within XENT_PIECE_BYTES.
+constexpr int64_t XENT_PIECE_BYTES = 256ll << 20;
+int64_t xent_piece(int64_t vocab, int64_t bytes)
+{
+    const int64_t most = std::max<int64_t>(XENT_PIECE_BYTES / bytes / 256, 1) * 256;
+    return std::min<int64_t>(cdiv(cdiv(vocab, cdiv(vocab, most)), 256) * 256, vocab);
+}
+
+// The tensor-core kernel on whole tiles: the shape with the least modelled time.
+Plan plan_xent(int64_t M, int64_t N, int64_t K, int num_sms, const Force &f)
+{
+    static const int shapes[][2] = {{2, 256}, {1, 256}, {1, 128}};
+    Plan p;
+    double best = 1e300;
+    for (const auto &sh : shapes) {
+        const int c = sh[0], b = sh[1];
+        if ((f.cg && c != f.cg) || (f.bn && b != f.bn)) continue;
+        const int workers = c == 2 ? std::max(num_sms / 2, 1) : num_sms;
+        const int64_t tiles = cdiv(M, BM * c) * cdiv(N, b);
+        const double t = schedule(tiles, cdiv(K, BK), workers, c, b, 0).t;
+        if (t >= best - 1e-9) continue;
+        best = t;
+        p.cg = c;
+        p.bn = b;
+        p.tiles = p.seg0_tiles = p.split_base = p.units = tiles;
+        p.grid = (int)std::min<int64_t>(tiles, workers) * c;
+    }
+    if (best == 1e300) {               // a forced shape this product does not have
+        Force g = f;
+        g.cg = g.bn = 0;
+        return plan_xent(M, N, K, num_sms, g);
+    }
+    p.group_m = f.group_m > 0 ? f.group_m : 4;
+    char buf[48];
+    std::snprintf(buf, sizeof buf, "tcgen05_%dx%d%s", BM * p.cg, p.bn, p.cg == 2 ? "_pair" : "");
+    p.name = buf;
+    return p;
+}
+
+tc_gemm_desc xent_desc(int64_t M, int64_t N, int64_t K, tc_dtype_t dt, tc_dtype_t ct, bool ta, bool tb, float alpha,
+                       float beta, int64_t lda, int64_t ldb, int64_t ldc)
+{
+    return tc_gemm_desc{(int32_t)M, (int32_t)N, (int32_t)K, dt, dt, ct, TC_F32, ta, tb, alpha, beta, (int32_t)lda,
+                        (int32_t)ldb, (int32_t)ldc};
+}
+
+// Rows of a 16-bit matrix copied to rows TMA can read.
+tc_status_t pack_rows(tc_ctx *ctx, tc_stream *s, const void *src, int64_t ld, void *dst, int64_t ld_dst, int64_t rows,
+                      int64_t cols)
+{
+    PackBatch pb;
+    pb.count = 1;
+    pb.seg[0] = PackArgs{static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), rows, cols, ld, ld_dst, 0, 0, 1};
+    if (launch_pack(pb, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += 1;
+    return TC_OK;
+}
+
+// Offsets of a call's buffers in one workspace.
+struct Carve {
+    size_t at = 0;
+    size_t take(int64_t bytes)
+    {
+        const size_t r = at;
+        at += round_up((size_t)bytes, 256);
+        return r;
+    }
+};
+
+tc_status_t run_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W, const void *targets, float *loss,
+                     float *lse, tc_stream *s)
+{
+    if (!ctx || !s) return TC_ERR_NULL;
+    XentNorm n;
+    tc_status_t st = validate_xent(d, X, W, targets, loss, lse, &n);
+    if (st != TC_OK) return st;
+    const int64_t T = d->tokens, H = d->hidden, V = d->vocab, ldp = (int64_t)round_up((size_t)H, 64);
+    const bool pack_x = !aligned16(X) || n.ldx % 8 != 0, pack_w = !aligned16(W) || n.ldw % 8 != 0;
+    // one piece, unless W has to be copied
+    const int64_t cols = pack_w ? xent_piece(V, ldp * 2) : V;
+    const Force f = read_force();
+    std::lock_guard<std::mutex> g(ctx->mu);
+    if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    const Plan first = plan_xent(T, cols, H, ctx->num_sms, f);
+    Carve c;
+    const int64_t nparts = 2 * cdiv(V, first.bn);      // pieces are whole tiles, but for the last
+    const size_t o_part = c.take(nparts * T * (int64_t)sizeof(float2)), o_at = c.take(T * 4), o_rows = c.take(T * 4);
+    const size_t o_x = c.take(pack_x ? T * ldp * 2 : 0), o_w = c.take(pack_w ? cols * ldp * 2 : 0);
+    if ((st = reserve(s, 256, c.at)) != TC_OK) return st;
+    uint8_t *rx = static_cast<uint8_t *>(s->rx);
+    if (pack_x && (st = pack_rows(ctx, s, X, n.ldx, rx + o_x, ldp, T, H)) != TC_OK) return st;
+    for (int64_t v0 = 0; v0 < V; v0 += cols) {
+        const int64_t N = std::min(cols, V - v0);
+        const void *Wv = static_cast<const uint16_t *>(W) + v0 * n.ldw;
+        if (pack_w) {
+            if ((st = pack_rows(ctx, s, Wv, n.ldw, rx + o_w, ldp, N, H)) != TC_OK) return st;
+            Wv = rx + o_w;
+        }
+        // (the last piece keeps the tile width that the statistics are laid out by)
+        Force same = f;
+        same.bn = first.bn;
+        same.cg = first.cg;
+        const Plan p = plan_xent(T, N, H, ctx->num_sms, same);
+        const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, TC_F32, false, true, d->scale, 0.0f, pack_x ? ldp : n.ldx,
+                                          pack_w ? ldp : n.ldw, N);
+        const void *Xv = pack_x ? rx + o_x : X;
+        Norm gn{};
+        gn.lda = gd.lda;
+        gn.ldb = gd.ldb;
+        gn.ldc = gd.ldc;
+        gn.a_rows = T;
+        gn.b_rows = N;
+        gn.a_cols = gn.b_cols = H;
+        gn.batch = 1;
+        XentJob job{};
+        job.mode = XENT_LOSS;
+        job.epi.targets = targets;
+        job.epi.wide = d->target_dtype == TC_I64;
+        job.epi.first = (int)v0;
+        job.epi.vocab = d->vocab;
+        job.epi.k2 = d->scale * 1.4426950408889634f;
+        job.epi.part = reinterpret_cast<float2 *>(rx + o_part) + 2 * (v0 / first.bn) * T;
+        job.epi.at = reinterpret_cast<float *>(rx + o_at);
+        if ((st = enqueue(ctx, &gd, gn, p, Xv, Wv, rx + o_rows, s, nullptr, nullptr, false, &job)) != TC_OK) return st;
+    }
+    XentJoinArgs j{};
+    j.part = reinterpret_cast<const float2 *>(rx + o_part);
+    j.at = reinterpret_cast<const float *>(rx + o_at);
+    j.targets = targets;
+    j.wide = d->target_dtype == TC_I64;
+    j.vocab = d->vocab;
+    j.T = d->tokens;
+    j.nparts = (int)nparts;
+    j.reduction = d->reduction;
+    j.z = d->z_weight;
+    j.loss = loss;
+    j.lse = lse;
+    j.rows = reinterpret_cast<float *>(rx + o_rows);
+    int launches = 0;
+    if (launch_xent_join(j, s->st, &launches) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += launches;
+    ctx->last = "xent_loss_" + first.name + (pack_x ? "_packX" : "") + (pack_w ? "_packW" : "") + "_p" +
+                std::to_string(cdiv(V, cols));
+    return TC_OK;
+}
+
+tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                              const float *lse, const float *grad, void *dX, void *dW, tc_stream *s)
+{
+    if (!ctx || !s) return TC_ERR_NULL;
+    XentNorm n;
+    tc_status_t st = validate_xent_backward(d, X, W, targets, lse, grad, dX, dW, &n);
+    if (st != TC_OK) return st;
+    const int64_t T = d->tokens, H = d->hidden, V = d->vocab, ldp = (int64_t)round_up((size_t)H, 64);
+    const int64_t es = (int64_t)elem_size(d->grad_dtype);
+    const bool pack_w = !aligned16(W) || n.ldw % 8 != 0, f16 = d->dtype == TC_F16;
+    const int parts = d->grad_dtype == TC_F32 ? 2 : 1;
+    const int64_t cols = xent_piece(V, T * 2 * parts + (pack_w ? ldp * 2 : 0)), ldg = (int64_t)round_up((size_t)cols, 64);
+    // dX of several pieces is summed in fp32
+    const bool sum = dX && cols < V && d->grad_dtype != TC_F32;
+    const Force f = read_force();
+    std::lock_guard<std::mutex> lk(ctx->mu);
+    if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    Carve c;
+    const size_t o_cp = c.take(T * 4), o_cy = c.take(T * 4), o_un = c.take(f16 ? H * 4 : 0);
+    const size_t o_x = c.take(T * ldp * 2), o_w = c.take(pack_w ? cols * ldp * 2 : 0), o_sum = c.take(sum ? T * H * 4 : 0);
+    size_t o_g[2];
+    for (int i = 0; i < 2; ++i) o_g[i] = c.take(i < parts ? T * ldg * 2 : 0);
+    if ((st = reserve(s, 256, c.at)) != TC_OK) return st;
+    uint8_t *rx = static_cast<uint8_t *>(s->rx);
+    const float *unscale = f16 ? reinterpret_cast<const float *>(rx + o_un) : nullptr;
+
+    // the two products of the piece at v0 with part i of G
+    struct Product {
+        tc_gemm_desc d;
+        Norm n;
+        Plan p;
+        const void *A, *B;
+        void *C;
+    };
+    auto product = [&](bool rows, int64_t v0, int i, Product *q) {
+        const int64_t N = std::min(cols, V - v0);
+        const uint8_t *Gi = rx + o_g[i];
+        q->A = Gi;
+        if (rows) {
+            q->B = pack_w ? static_cast<const void *>(rx + o_w) : static_cast<const uint16_t *>(W) + v0 * n.ldw;
+            q->C = sum ? static_cast<void *>(rx + o_sum) : dX;
+            q->d = xent_desc(T, H, N, d->dtype, sum ? TC_F32 : d->grad_dtype, false, false, d->scale,
+                             v0 > 0 || i > 0 ? 1.0f : 0.0f, ldg, pack_w ? ldp : n.ldw, sum ? H : n.lddx);
+        } else {
+            q->B = rx + o_x;
+            q->C = static_cast<uint8_t *>(dW) + v0 * n.lddw * es;
+            q->d = xent_desc(N, H, T, d->dtype, d->grad_dtype, true, false, d->scale, i > 0 ? 1.0f : 0.0f, ldg, ldp, n.lddw);
+        }
+        const tc_status_t r = validate(&q->d, q->A, q->B, q->C, 1, 0, 0, 0, &q->n);
+        return r != TC_OK ? r : make_plan(&q->d, q->n, q->A, q->B, ctx->num_sms, &q->p, false);
+    };
+    // the largest workspace of them (a cluster split may have to go through memory)
+    size_t ws = 256;
+    for (const int64_t v0 : {(int64_t)0, (cdiv(V, cols) - 1) * cols}) {
+        for (int i = 0; i < 2; ++i) {
+            if (i == 0 ? !dX : !dW) continue;
+            Product q;
+            if ((st = product(i == 0, v0, 0, &q)) != TC_OK) return st;
+            q.p.csplit = false;
+            ws = std::max(ws, ws_layout(q.n, q.p).bytes());
+        }
+    }
+    if ((st = reserve(s, ws, c.at)) != TC_OK) return st;
+
+    XentPrepArgs a{};
+    a.targets = targets;
+    a.wide = d->target_dtype == TC_I64;
+    a.vocab = d->vocab;
+    a.T = d->tokens;
+    a.H = d->hidden;
+    a.reduction = d->reduction;
+    a.z = d->z_weight;
+    a.lse = lse;
+    a.grad = grad;
+    a.cp = reinterpret_cast<float *>(rx + o_cp);
+    a.cy = reinterpret_cast<float *>(rx + o_cy);
+    a.unscale = const_cast<float *>(unscale);
+    a.X = static_cast<const uint16_t *>(X);
+    a.ldx = n.ldx;
+    a.clean = reinterpret_cast<uint16_t *>(rx + o_x);
+    a.ld_clean = ldp;
+    if (launch_xent_prep(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += 1;
+    std::string name;
+    for (int64_t v0 = 0; v0 < V; v0 += cols) {
+        const int64_t N = std::min(cols, V - v0);
+        const void *Wv = static_cast<const uint16_t *>(W) + v0 * n.ldw;
+        if (pack_w) {
+            if ((st = pack_rows(ctx, s, Wv, n.ldw, rx + o_w, ldp, N, H)) != TC_OK) return st;
+            Wv = rx + o_w;
+        }
+        const Plan p = plan_xent(T, N, H, ctx->num_sms, f);
+        if (v0 == 0) name = p.name;
+        const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, d->dtype, false, true, 1.0f, 0.0f, ldp, pack_w ? ldp : n.ldw, ldg);
+        Norm gn{};
+        gn.lda = gd.lda;
+        gn.ldb = gd.ldb;
+        gn.ldc = gd.ldc;
+        gn.a_rows = T;
+        gn.b_rows = N;
+        gn.a_cols = gn.b_cols = H;
+        gn.batch = 1;
+        XentJob job{};
+        job.mode = XENT_GRAD;
+        job.epi.targets = targets;
+        job.epi.wide = a.wide;
+        job.epi.first = (int)v0;
+        job.epi.vocab = d->vocab;
+        job.epi.k2 = d->scale * 1.4426950408889634f;
+        job.epi.lse = lse;
+        job.epi.cp = a.cp;
+        job.epi.cy = a.cy;
+        job.epi.two = parts == 2;
+        job.left = rx + o_g[1];
+        if ((st = enqueue(ctx, &gd, gn, p, rx + o_x, Wv, rx + o_g[0], s, nullptr, nullptr, false, &job)) != TC_OK) return st;
+        for (int i = 0; i < parts; ++i) {
+            for (int k = 0; k < 2; ++k) {
+                if (k == 0 ? !dX : !dW) continue;
+                Product q;
+                if ((st = product(k == 0, v0, i, &q)) != TC_OK) return st;
+                if ((st = enqueue(ctx, &q.d, q.n, q.p, q.A, q.B, q.C, s, nullptr, unscale)) != TC_OK) return st;
+            }
+        }
+    }
+    if (sum) {
+        const XentRoundArgs r{reinterpret_cast<const float *>(rx + o_sum), dX, T, H, n.lddx, d->grad_dtype};
+        if (launch_xent_round(r, s->st) != cudaSuccess) return TC_ERR_CUDA;
+        ctx->launches += 1;
+    }
+    ctx->last = "xent_grad_" + name + (pack_w ? "_packW" : "") + "_p" + std::to_string(cdiv(V, cols));
+    return TC_OK;
+}
+
 // A C entry lets no C++ exception out (the name of the last kernel is a
 // std::string, the context's lock may throw).
 template <typename F>
@@ -1932,7 +2336,7 @@ const char *tc_status_string(tc_status_t st)
     case TC_ERR_STRIDE: return "invalid batch stride";
     case TC_ERR_VARIANT: return "forced variant cannot serve this problem";
     case TC_ERR_SCRATCH: return "problem needs more scratch than the static buffer of tc_gemm_splitk_noalloc holds";
-    case TC_ERR_EPILOGUE: return "fused epilogue refused: unknown activation, or f32 operands (exact-fp32 path)";
+    case TC_ERR_EPILOGUE: return "fused epilogue refused: unknown activation or reduction, or f32 operands (exact-fp32 path)";
     case TC_ERR_LAYOUT: return "transpose flags this call does not support";
     }
     return "unknown status";
@@ -2193,6 +2597,49 @@ tc_status_t tc_moe_q4_validate(const tc_moe_desc *d, const void *X, const void *
 {
     MoeArgs a;
     return validate_moe(d, X, router, gate_up, down, Y, ids, weights, &a);
+}
+
+tc_status_t tc_linear_xent_async(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                                 float *loss, float *lse, tc_stream *s)
+{
+    return guarded([&] { return run_xent(ctx, d, X, W, targets, loss, lse, s); });
+}
+
+tc_status_t tc_linear_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                           float *loss, float *lse)
+{
+    if (!ctx) return TC_ERR_NULL;
+    const tc_status_t st = guarded([&] { return run_xent(ctx, d, X, W, targets, loss, lse, ctx->def); });
+    return st == TC_OK ? tc_stream_sync(ctx->def) : st;
+}
+
+tc_status_t tc_linear_xent_backward_async(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W,
+                                          const void *targets, const float *lse, const float *grad, void *dX, void *dW,
+                                          tc_stream *s)
+{
+    return guarded([&] { return run_xent_backward(ctx, d, X, W, targets, lse, grad, dX, dW, s); });
+}
+
+tc_status_t tc_linear_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const void *W,
+                                    const void *targets, const float *lse, const float *grad, void *dX, void *dW)
+{
+    if (!ctx) return TC_ERR_NULL;
+    const tc_status_t st = guarded([&] { return run_xent_backward(ctx, d, X, W, targets, lse, grad, dX, dW, ctx->def); });
+    return st == TC_OK ? tc_stream_sync(ctx->def) : st;
+}
+
+tc_status_t tc_linear_xent_validate(const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                                    const float *loss, const float *lse)
+{
+    XentNorm n;
+    return validate_xent(d, X, W, targets, loss, lse, &n);
+}
+
+tc_status_t tc_linear_xent_backward_validate(const tc_xent_desc *d, const void *X, const void *W, const void *targets,
+                                             const float *lse, const float *grad, const void *dX, const void *dW)
+{
+    XentNorm n;
+    return validate_xent_backward(d, X, W, targets, lse, grad, dX, dW, &n);
 }
 
 tc_status_t tc_gemm_batched_async(tc_ctx *ctx, const tc_gemm_batched_desc *bd, const void *A, const void *B,

@@ -39,6 +39,15 @@ __device__ __forceinline__ void store_c1(void *C, long long off, float v, int c_
     }
 }
 
+// 2^x by the PTX approximate instruction: relative error 2^-22, results below
+// 2^-126 are 0.
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Fused epilogue (tessl architecture.md, "Fused Epilogue"): activation(y +
 // bias[col]) in fp32 on the value y = alpha * acc + beta * C_old.
 // GeluTanh: 0.5 x (1 + tanh(z)), z = sqrt(2/pi) (x + 0.044715 x^3),

@@ -103,6 +103,27 @@ __host__ __device__ constexpr int mma_smem_bytes(int bn, int cg, bool epi = fals
     return mma_stages(bn, cg, epi) * stage_bytes(bn, cg) + smem_reserve(bn, cg, epi);
 }
 
+// What the epilogue of a product of hidden rows with a vocabulary's rows needs
+// for a softmax cross entropy (the public header states the formulas); the
+// product's columns are the vocabulary's [first, first + N).
+struct XentEpi {
+    const void *targets;   // one for each row of the product: int32, or int64 when `wide`
+    int wide;
+    int first, vocab;
+    float k2;              // logits to base-2 exponents: their scale times log2(e)
+    // the loss: for row r and the half h of output tile column tn the largest
+    // exponent and the sum of 2^(exponent - largest) at part[(2 tn + h) * M + r],
+    // and the logit of the row's target, where it is in this range, at at[r]
+    float2 *part;
+    float *at;
+    // the gradient: lse[r], and the factors of the probabilities and of the
+    // target's one (both 0 for a row that is not counted); C receives the
+    // rounded values and, through the fourth descriptor when `two`, what the
+    // rounding left
+    const float *lse, *cp, *cy;
+    int two;
+};
+
 // Device-side arguments of the tensor-core kernel (the two TMA descriptors
 // travel as separate __grid_constant__ parameters).
 struct MmaArgs {
@@ -152,8 +173,10 @@ struct MmaArgs {
     // bytes; the tile's other rows hold stale data, which reaches only
     // output rows beyond M (never stored)
     int a_short_bytes;
+    XentEpi x;
 };
 
+enum XentMode { XENT_NONE = 0, XENT_LOSS = 1, XENT_GRAD = 2 };
 struct MmaLaunch {
     int bn;
     int cg;      // CTAs per tile: 1, or 2 for a CTA pair (cluster of two)
@@ -163,6 +186,10 @@ struct MmaLaunch {
     // memory (BN 64 or 128, one CTA per unit: grid == args.total_units)
     int csplit;
     int grid;    // CTAs (a multiple of cg)
+    // softmax cross entropy in place of the plain epilogue (args.x; whole-K
+    // tiles of 256 or 128 columns): XENT_LOSS writes no C, XENT_GRAD writes it
+    // (16-bit, by TMA stores)
+    int xent;
     CUtensorMap tmA, tmB, tmC, tmW;   // A, B, C and the split-K workspace
     MmaArgs args;
 };
@@ -324,6 +351,53 @@ struct PackBatch {
     PackArgs seg[PACK_MAX];
 };
 cudaError_t launch_pack(PackBatch &pb, cudaStream_t st);
+
+// --------------------------------------------- softmax cross entropy (xent.cu)
+// around the tensor-core kernel's XENT_LOSS and XENT_GRAD products.
+
+// Joins the partial statistics of T rows (nparts of them, as XentEpi lays them
+// out) into lse, and into each row's loss or the reduced one.
+struct XentJoinArgs {
+    const float2 *part;
+    const float *at;
+    const void *targets;
+    int wide, vocab;
+    int T, nparts;
+    int reduction;         // tc_reduction_t
+    float z;
+    float *loss, *lse;
+    float *rows;           // scratch: the rows' losses of a reduced one, T floats
+};
+// one launch, or two for the reduced loss of more rows than a block joins
+cudaError_t launch_xent_join(const XentJoinArgs &a, cudaStream_t st, int *launches);
+
+// What the gradient's products read besides W: each row's factors (XentEpi's cp
+// and cy), X in rows of ld_clean elements with the rows that do not count
+// zeroed, and for f16 the factors times a power of two that puts the largest
+// between 2^13 and 2^14, with its inverse H times for the products' columns.
+struct XentPrepArgs {
+    const void *targets;
+    int wide, vocab;
+    int T, H, reduction;
+    float z;
+    const float *lse, *grad;   // grad: T values, or one where reduced
+    float *cp, *cy;
+    float *unscale;            // H floats (f16), or null
+    const uint16_t *X;
+    long long ldx;
+    uint16_t *clean;
+    long long ld_clean;        // a multiple of 8; clean is 16-byte aligned
+};
+cudaError_t launch_xent_prep(const XentPrepArgs &a, cudaStream_t st);
+
+// dst [rows, cols] (f16 or bf16, leading dimension ld) = the contiguous fp32 src, rounded
+struct XentRoundArgs {
+    const float *src;
+    void *dst;
+    long long rows, cols, ld;
+    int dtype;
+};
+cudaError_t launch_xent_round(const XentRoundArgs &a, cudaStream_t st);
 
 // ------------------------------------------------------------- 4-bit weights
 // A tc_q4_weight after validation (the public header states the format):

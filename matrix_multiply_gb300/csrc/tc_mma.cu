@@ -258,6 +258,12 @@ __device__ __forceinline__ float bias_of(const MmaArgs &a, int lane, long long c
     return (a.bias && col < a.N) ? load_c(a.bias, col, a.c_dtype) : 0.0f;
 }
 
+// x rounded to a 16-bit type
+__device__ __forceinline__ float round16(float x, int dtype)
+{
+    return dtype == TC_BF16 ? __bfloat162float(__float2bfloat16_rn(x)) : __half2float(__float2half_rn(x));
+}
+
 // x[i] for a run-time i < N, from registers (the unrolled selects keep the
 // array out of local memory).
 template <int N>
@@ -549,6 +555,51 @@ __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *p
     }
 }
 
+// ---------------------------------------------------------------- softmax cross entropy
+
+// Row r's target as a column of this product (negative, or N and beyond, where
+// it is in another piece of the vocabulary or the row is not counted).
+__device__ __forceinline__ int xent_target(const XentEpi &x, long long row, int M)
+{
+    if (row >= M) return -1;
+    const long long y = x.wide ? static_cast<const long long *>(x.targets)[row]
+                               : (long long)static_cast<const int *>(x.targets)[row];
+    return y >= 0 && y < x.vocab ? (int)(y - x.first) : -1;
+}
+
+// One chunk of a row's statistics: m the largest exponent so far, s the sum of
+// 2^(exponent - m).  The lane owns the row, so nothing crosses lanes: 32
+// multiply-adds, exponentials and additions per chunk and one rescaling of s.
+// Sums are fp32: at most 2^15 terms of at most 1 meet in a half tile's partial
+// sum, and the partial sums of a row are joined pairwise.
+__device__ __forceinline__ void xent_statistics(const MmaArgs &a, long long col0, const float (&v)[32], float &m,
+                                                float &s)
+{
+    float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    const int n = (int)min((long long)32, a.N - col0);
+    if (n == 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], j < n ? v[j] : -INFINITY);
+    }
+    const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * a.x.k2;
+    const float next = fmaxf(m, top);
+    const float base = next == -INFINITY ? 0.0f : next;     // only -inf so far: 2^(-inf - 0) = 0
+    float sum[4] = {s * exp2_approx(m - base), 0.0f, 0.0f, 0.0f};
+    if (n == 32) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[j & 3] += exp2_approx(fmaf(v[j], a.x.k2, -base));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < n) sum[j & 3] += exp2_approx(fmaf(v[j], a.x.k2, -base));
+    }
+    s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    m = next;
+}
+
 // ---------------------------------------------------------------- kernel
 
 // CG = 1: one CTA computes a 128 x BN tile with tcgen05.mma.cta_group::1.
@@ -581,7 +632,17 @@ __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *p
 // slice's partial tile stays in its CTA's shared memory and csplit_reduce
 // adds them across the cluster, so no partial tile goes through global
 // memory and no second kernel runs.
-template <int BN, int CG, bool GROUPED, bool EPI, bool I8ACC = false, bool CSPLIT = false>
+//
+// XENT: the softmax cross entropy of the rows of A against those of B, in
+// place of the epilogue.  A row's logits are the row of one TMEM lane, so each
+// epilogue lane keeps its row's running maximum and sum in registers over its
+// chunks of the tile (XENT_LOSS: two floats leave the chip per row and half
+// tile), or turns them into the gradient of the logits from the row's known
+// lse (XENT_GRAD).  Eight epilogue warps: per element a multiply-add, an
+// exponential and two or three more operations, 1.5 us for the 128 x 256
+// outputs of an SM, which the next tile's MMAs hide from a hidden size of
+// about 512 on.
+template <int BN, int CG, bool GROUPED, bool EPI, bool I8ACC = false, bool CSPLIT = false, int XENT = XENT_NONE>
 __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmW,
@@ -603,6 +664,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     constexpr uint32_t RUN_COL = 2 * BN;           // I8ACC: the running int32 sums
     static_assert(!I8ACC || (EPI && !GROUPED && 3 * BN <= 512), "on-chip slices: two accumulators and the sums");
     static_assert(!CSPLIT || (CG == 1 && !GROUPED && !I8ACC), "cluster split-K: one CTA per slice");
+    static_assert(XENT == XENT_NONE || (EPI && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
     static_assert(!CSPLIT || BM * csplit_ld<BN>() * 4 <= S * STAGE, "the partial tile fits in the idle ring");
     constexpr int CHUNKS = BN / 32;
     static_assert(CG == 1 || CG == 2, "one CTA or a CTA pair");
@@ -655,7 +717,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             prefetch_tmap(&tmA);
             prefetch_tmap(&tmB);
             if (args.c_tma) prefetch_tmap(&tmC);
-            if (args.ws) prefetch_tmap(&tmW);
+            if (args.ws || (XENT == XENT_GRAD && args.x.two)) prefetch_tmap(&tmW);
         }
         // let the next kernel in the stream (the split-K reduction, or the
         // next GEMM) launch early; it waits for this grid to finish before
@@ -956,9 +1018,21 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             // wait for the accumulator so that its latency hides behind the MMAs
             constexpr int NCH = CHUNKS / CSTEP;
             float bpre[NCH];
+            // cross entropy: what the lane's row needs, loaded as early
+            int target = -1;
+            float rowlse = 0.0f, cp = 0.0f, cy = 0.0f;
+            if constexpr (XENT != XENT_NONE) {
+                const long long row = (long long)w.tm * (BM * CL) + row_in_tile;
+                target = xent_target(args.x, row, args.M);
+                if (XENT == XENT_GRAD && row < args.M) {
+                    cp = args.x.cp[row];
+                    cy = args.x.cy[row];
+                    rowlse = args.x.lse[row] * 1.4426950408889634f;
+                }
+            }
 #pragma unroll
             for (int i = 0; i < NCH; ++i)
-                bpre[i] = EPI ? bias_of(ea, lane, (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32) : 0.0f;
+                bpre[i] = EPI && XENT == XENT_NONE ? bias_of(ea, lane, (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32) : 0.0f;
             // segments of the unit (see the MMA warp): one, or the K slices
             // that I8ACC adds up in TMEM
             const int nseg = I8ACC ? (w.kb1 - w.kb0 + args.slice_kb - 1) / args.slice_kb : 1;
@@ -1018,6 +1092,52 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         }
                     }
                     if (!last) tmem_st_wait();
+                } else if constexpr (XENT != XENT_NONE) {
+                    float m = -INFINITY, s = 0.0f;
+#pragma unroll 1
+                    for (int c = chunk0; c < CHUNKS; c += CSTEP) {
+                        uint32_t r[32];
+                        __syncwarp();
+                        tmem_ld_32x32b_x32(taddr + c * 32, r);
+                        tmem_ld_wait();
+                        if (c == LAST_C0 + chunk0) release();
+                        const long long col0 = (long long)w.tn * BN + c * 32;
+                        if (col0 >= args.N) continue;         // (the whole warp; release() came with the last chunk)
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                        // the target's column of this chunk, in few warps' chunks
+                        const int hit = target - (int)col0;
+                        const bool any = __any_sync(0xffffffffu, hit >= 0 && hit < 32);
+                        if constexpr (XENT == XENT_LOSS) {
+                            if (any && hit >= 0 && hit < 32 && col0 + hit < args.N) args.x.at[row] = pick(v, hit) * args.alpha;
+                            xent_statistics(args, col0, v, m, s);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = cp * exp2_approx(fmaf(v[j], args.x.k2, -rowlse));
+                            if (any) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] -= j == hit ? cy : 0.0f;
+                            }
+                            if (cp == 0.0f && cy == 0.0f) {      // not counted: 0 whatever its logits are
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                            }
+                            const long long row0 = row - lane;
+                            if (row0 < args.M) {
+                                store_tma<EBUFS>(&tmC, false, args.c_dtype, staging(STG_TMA), lane, 0, row0, col0, v);
+                                if (args.x.two) {
+                                    // what the rounding left, rounded in turn
+#pragma unroll
+                                    for (int j = 0; j < 32; ++j) v[j] -= round16(v[j], args.c_dtype);
+                                    store_tma<EBUFS>(&tmW, false, args.c_dtype, staging(STG_TMA), lane, 0, row0, col0, v);
+                                }
+                            }
+                        }
+                    }
+                    if constexpr (XENT == XENT_LOSS) {
+                        if (row < args.M) args.x.part[(2LL * w.tn + chunk0) * args.M + row] = make_float2(m, s);
+                    }
                 } else if (w.S == 1) {
 #pragma unroll 1
                     for (int c = chunk0; c < CHUNKS; c += CSTEP) {
@@ -1097,10 +1217,11 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     }
 }
 
-template <int BN, int CG, bool GROUPED = false, bool EPI = false, bool I8ACC = false, bool CSPLIT = false>
+template <int BN, int CG, bool GROUPED = false, bool EPI = false, bool I8ACC = false, bool CSPLIT = false,
+          int XENT = XENT_NONE>
 cudaError_t launch_kernel(const MmaLaunch &L, cudaStream_t st, const TableOf<GROUPED> &gt = TableOf<GROUPED>{})
 {
-    constexpr auto kern = mma_kernel<BN, CG, GROUPED, EPI, I8ACC, CSPLIT>;
+    constexpr auto kern = mma_kernel<BN, CG, GROUPED, EPI, I8ACC, CSPLIT, XENT>;
     constexpr int smem = mma_smem_bytes(BN, CG, EPI || GROUPED);
     constexpr int threads = mma_threads(BN, CG, EPI || GROUPED);
     // per device: the kernel's shared-memory limit is raised once (callers
@@ -1323,8 +1444,20 @@ cudaError_t launch_reduce(const ReduceArgs &r, cudaStream_t st)
                      : launch_dependent(splitk_reduce_kernel<false, 8>, grid, block, 0, st, 1u, r);
 }
 
+template <int XENT>
+cudaError_t launch_xent(const MmaLaunch &L, cudaStream_t st)
+{
+    if (L.csplit || L.i8acc || L.args.seg0_tiles != L.args.total_units || L.args.seg0_split != 1) return cudaErrorInvalidValue;
+    if (L.cg == 2 && L.bn == 256) return launch_kernel<256, 2, false, true, false, false, XENT>(L, st);
+    if (L.cg == 1 && L.bn == 256) return launch_kernel<256, 1, false, true, false, false, XENT>(L, st);
+    if (L.cg == 1 && L.bn == 128) return launch_kernel<128, 1, false, true, false, false, XENT>(L, st);
+    return cudaErrorInvalidValue;
+}
+
 cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
 {
+    if (L.xent == XENT_LOSS) return launch_xent<XENT_LOSS>(L, st);
+    if (L.xent == XENT_GRAD) return L.args.c_tma ? launch_xent<XENT_GRAD>(L, st) : cudaErrorInvalidValue;
     const bool epi = L.args.bias != nullptr || L.args.act != TC_ACT_NONE || L.args.col_scale != nullptr;
     if (L.csplit) {
         if (L.cg != 1 || L.i8acc) return cudaErrorInvalidValue;

@@ -1,0 +1,263 @@
+// Softmax cross entropy of hidden rows X [T, H] against a vocabulary W [V, H]:
+// the small kernels around the products (tc_mma.cu, XENT_LOSS and XENT_GRAD).
+//
+//   loss       l = scale X W^T stays in TMEM: each half tile of a row leaves
+//              its largest exponent and its sum of exponentials, and the
+//              target's logit; `join` makes lse and the losses of them.
+//   gradients  G = the gradient of l, piece by piece of the vocabulary,
+//              rounded to X's type; dX += G W_piece and dW_piece = G^T X are
+//              plain products.  `prep` runs first, `round` last where dX was
+//              summed over pieces in fp32.
+//
+// All of it is some microseconds beside products of 2 T H V operations each.
+#include "elem.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "../../include/tcgemm.h"
+
+namespace tc {
+namespace {
+
+constexpr int JOIN_THREADS = 256;
+constexpr float LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ bool counts(const void *targets, int wide, int vocab, long long row, long long &y)
+{
+    y = wide ? static_cast<const long long *>(targets)[row] : (long long)static_cast<const int *>(targets)[row];
+    return y >= 0 && y < vocab;
+}
+
+// (m, s) <- the statistics of both: s 2^m + t 2^n = (..) 2^max(m, n)
+__device__ __forceinline__ void merge(float &m, float &s, float n, float t)
+{
+    const float top = fmaxf(m, n), base = top == -INFINITY ? 0.0f : top;
+    s = s * exp2_approx(m - base) + t * exp2_approx(n - base);
+    m = top;
+}
+
+// Block sum in a fixed order (a tree over lanes, then over warps); the result
+// in every thread.
+template <typename T>
+__device__ __forceinline__ T block_sum(T v, T *buf)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    T r = buf[0];
+    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) r += buf[w];
+    __syncthreads();
+    return r;
+}
+
+// the sum of a block's rows and how many count, the reduced loss of them
+__device__ __forceinline__ float reduced(double sum, int n, int reduction)
+{
+    return (float)(reduction == TC_REDUCE_MEAN && n > 0 ? sum / n : sum);
+}
+
+// A block joins `rows` neighbouring rows (a power of two up to 8: 64 bytes of
+// each part), its threads the parts in turns; two floats per row and 128
+// columns of the vocabulary are read once.
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const XentJoinArgs a, int rows)
+{
+    __shared__ float sm[JOIN_THREADS], ss[JOIN_THREADS];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int per = JOIN_THREADS / rows;
+    const int r = threadIdx.x % rows, q = threadIdx.x / rows;
+    const long long row = (long long)blockIdx.x * rows + r;
+    const bool in = row < a.T;
+    float m = -INFINITY, s = 0.0f;
+    if (in) {
+        int i = q;
+        for (; i + 3 * per < a.nparts; i += 4 * per) {
+            float2 p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = __ldcg(a.part + (long long)(i + j * per) * a.T + row);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) merge(m, s, p[j].x, p[j].y);
+        }
+        for (; i < a.nparts; i += per) {
+            const float2 p = __ldcg(a.part + (long long)i * a.T + row);
+            merge(m, s, p.x, p.y);
+        }
+    }
+    sm[threadIdx.x] = m;
+    ss[threadIdx.x] = s;
+    __syncthreads();
+    for (int step = per / 2; step > 0; step >>= 1) {
+        if (q < step) {
+            merge(m, s, sm[threadIdx.x + step * rows], ss[threadIdx.x + step * rows]);
+            sm[threadIdx.x] = m;
+            ss[threadIdx.x] = s;
+        }
+        __syncthreads();
+    }
+    float loss = 0.0f;
+    bool counted = false;
+    if (q == 0 && in) {
+        const float lse = (m + log2f(s)) * LN2;
+        long long y;
+        counted = counts(a.targets, a.wide, a.vocab, row, y);
+        loss = counted ? lse - a.at[row] + a.z * lse * lse : 0.0f;
+        a.lse[row] = lse;
+        if (a.reduction == TC_REDUCE_NONE)
+            a.loss[row] = loss;
+        else if (gridDim.x > 1)
+            a.rows[row] = loss;
+    }
+    if (a.reduction != TC_REDUCE_NONE && gridDim.x == 1) {
+        __shared__ double sums[JOIN_THREADS / 32];
+        __shared__ int ns[JOIN_THREADS / 32];
+        const double sum = block_sum((double)loss, sums);
+        const int n = block_sum(counted ? 1 : 0, ns);
+        if (threadIdx.x == 0) a.loss[0] = reduced(sum, n, a.reduction);
+    }
+}
+
+// The reduced loss of many rows: one block, in 64 bits and a fixed order.
+__global__ void __launch_bounds__(1024) total_kernel(const XentJoinArgs a)
+{
+    __shared__ double sums[32];
+    __shared__ int ns[32];
+    griddep_wait();
+    griddep_launch_dependents();
+    double sum = 0.0;
+    int n = 0;
+    for (int row = threadIdx.x; row < a.T; row += 1024) {
+        long long y;
+        sum += (double)a.rows[row];
+        n += counts(a.targets, a.wide, a.vocab, row, y) ? 1 : 0;
+    }
+    sum = block_sum(sum, sums);
+    n = block_sum(n, ns);
+    if (threadIdx.x == 0) a.loss[0] = reduced(sum, n, a.reduction);
+}
+
+constexpr int PREP_THREADS = 1024;
+
+// Block 0 makes the rows' factors, the others copy X (8 elements a thread and
+// turn), zeros for the rows that do not count: what such a row holds, a NaN
+// among it, must not reach dW, whose products run over the rows.
+__global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const XentPrepArgs a)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    if (blockIdx.x > 0) {
+        const long long per = a.ld_clean / 8, all = per * a.T;
+        const bool whole = (reinterpret_cast<uintptr_t>(a.X) & 15u) == 0 && a.ldx % 8 == 0;
+        for (long long i = (long long)(blockIdx.x - 1) * PREP_THREADS + threadIdx.x; i < all;
+             i += (long long)(gridDim.x - 1) * PREP_THREADS) {
+            const long long row = i / per, col = (i - row * per) * 8;
+            long long y;
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (counts(a.targets, a.wide, a.vocab, row, y)) {
+                const uint16_t *src = a.X + row * a.ldx + col;
+                if (whole && col + 8 <= a.H) {
+                    w = *reinterpret_cast<const uint4 *>(src);
+                } else {
+                    uint32_t h[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) h[j] = col + j < a.H ? src[j] : 0u;
+                    w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+                }
+            }
+            *reinterpret_cast<uint4 *>(a.clean + row * a.ld_clean + col) = w;
+        }
+        return;
+    }
+    __shared__ int ns[32];
+    __shared__ float tops[32];
+    long long y;
+    float scale = 1.0f;
+    if (a.reduction == TC_REDUCE_MEAN) {
+        int n = 0;
+        for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) n += counts(a.targets, a.wide, a.vocab, t, y) ? 1 : 0;
+        n = block_sum(n, ns);
+        scale = 1.0f / (float)max(n, 1);
+    }
+    auto factors = [&](int t, float &cp, float &cy) {
+        cp = cy = 0.0f;
+        if (!counts(a.targets, a.wide, a.vocab, t, y)) return;
+        cy = a.grad[a.reduction == TC_REDUCE_NONE ? t : 0] * scale;
+        cp = a.z != 0.0f ? cy * (1.0f + 2.0f * a.z * a.lse[t]) : cy;
+    };
+    float power = 1.0f;
+    if (a.unscale) {
+        // f16 spans 2^-24 to 2^16: probabilities far below one times a small
+        // gradient would be lost, so G is held as a multiple of it
+        float top = 0.0f;
+        for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) {
+            float cp, cy;
+            factors(t, cp, cy);
+            top = fmaxf(top, fmaxf(fabsf(cp), fabsf(cy)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+        __syncthreads();
+        for (int w = 0; w < 32; ++w) top = fmaxf(top, tops[w]);
+        // top = f 2^e with f in [1/2, 1); the inverse stays a normal number
+        int e;
+        if (top > 0.0f && top < INFINITY) {
+            frexpf(top, &e);
+            power = ldexpf(1.0f, min(14 - e, 126));
+        }
+        for (int h = threadIdx.x; h < a.H; h += PREP_THREADS) a.unscale[h] = 1.0f / power;
+    }
+    for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) {
+        float cp, cy;
+        factors(t, cp, cy);
+        a.cp[t] = cp * power;
+        a.cy[t] = cy * power;
+    }
+}
+
+__global__ void __launch_bounds__(256) round_kernel(const XentRoundArgs a)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const long long per = (a.cols + 7) / 8, all = per * a.rows;
+    const bool whole = a.cols % 8 == 0 && a.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dst) & 15u) == 0;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
+        const long long row = i / per, col = (i - row * per) * 8;
+        const float *src = a.src + row * a.cols + col;
+        if (whole) {
+            const float4 x = *reinterpret_cast<const float4 *>(src), y = *reinterpret_cast<const float4 *>(src + 4);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst) + row * a.ld + col) =
+                make_uint4(pack2(x.x, x.y, a.dtype), pack2(x.z, x.w, a.dtype), pack2(y.x, y.y, a.dtype), pack2(y.z, y.w, a.dtype));
+        } else {
+            for (int j = 0; j < 8 && col + j < a.cols; ++j) store_c1(a.dst, row * a.ld + col + j, src[j], a.dtype);
+        }
+    }
+}
+
+unsigned blocks_for(long long items, int threads) { return (unsigned)min((items + threads - 1) / threads, 8LL * 152); }
+
+}  // namespace
+
+cudaError_t launch_xent_join(const XentJoinArgs &a, cudaStream_t st, int *launches)
+{
+    int rows = 1;
+    while (rows < 8 && rows < a.T) rows *= 2;
+    const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
+    *launches = 1;
+    cudaError_t e = launch_dependent(join_kernel, dim3(grid), dim3(JOIN_THREADS), 0, st, 1u, a, rows);
+    if (e != cudaSuccess || a.reduction == TC_REDUCE_NONE || grid == 1) return e;
+    *launches = 2;
+    return launch_dependent(total_kernel, dim3(1), dim3(1024), 0, st, 1u, a);
+}
+
+cudaError_t launch_xent_prep(const XentPrepArgs &a, cudaStream_t st)
+{
+    const unsigned copy = blocks_for(a.ld_clean / 8 * a.T, PREP_THREADS);
+    return launch_dependent(prep_kernel, dim3(1 + copy), dim3(PREP_THREADS), 0, st, 1u, a);
+}
+
+cudaError_t launch_xent_round(const XentRoundArgs &a, cudaStream_t st)
+{
+    return launch_dependent(round_kernel, dim3(blocks_for((a.cols + 7) / 8 * a.rows, 256)), dim3(256), 0, st, 1u, a);
+}
+
+}  // namespace tc
