@@ -427,6 +427,65 @@ tc_status_t tc_linear_xent_validate(const tc_xent_desc *d, const void *X, const 
 tc_status_t tc_linear_xent_backward_validate(const tc_xent_desc *d, const void *X, const void *W, const void *targets,
                                              const float *lse, const float *grad, const void *dX, const void *dW);
 
+/* Routing of tokens to experts from the router's logits l [tokens, experts]
+ * (tc_gemm of hidden rows and router), for training: the choice and its weights
+ * as tc_moe_q4 makes them, what the choice adds to the training loss, and the
+ * gradient back to the logits.
+ *   p[t, e]    = softmax(l[t, :])
+ *   the top_k experts e_j of token t by l, ties to the lowest index (a NaN
+ *   counts as the largest); an expert whose logit is -inf is never chosen: ids
+ *   are -1 and weights 0 from where only such are left
+ *   weights w_j = p[t, e_j], with renormalize divided by their sum
+ * A token counts where valid (one byte each, NULL: all) is not 0 and any of its
+ * logits is above -inf; the others get ids -1 and weights 0.  With n the tokens
+ * that count, c[e] those that chose e, f[e] = c[e] / (n top_k) and P[e] the
+ * mean over them of p[t, e]:
+ *   losses[0] = experts * sum_e f[e] P[e]   (1 where all experts are used alike)
+ *   losses[1] = mean of lse(l[t, :])^2
+ * both 0 where no token counts.  ids is int32 [tokens, top_k], weights float
+ * [tokens, top_k], counts int32 [experts + 1]: c, and n last.
+ *
+ * The backward call, from logits, valid, ids and counts as above, given the
+ * gradients that arrive at weights (grad_weights, NULL: none) and at the two
+ * losses (grad_losses, NULL: none), with f a constant as usual:
+ *   dlogits[t, e] = gl[0] (experts / n) p[e] (f[e] - sum_j f[j] p[j])
+ *                   + gl[1] (2 / n) lse p[e]
+ *                   + p[e] ([e = e_j] gw_j - sum_i gw_i w_i), or, renormalised,
+ *                     w_j (gw_j - sum_i gw_i w_i) at e = e_j
+ * and 0 for tokens that do not count.  (ids outside [0, experts) are taken as
+ * -1.)
+ *
+ * logits_dtype is TC_F16, TC_BF16 or TC_F32; dlogits has grad_dtype, that type
+ * or TC_F32 (TC_ERR_DTYPE otherwise); everything is computed in fp32 from the
+ * logits as they are, the losses' sums over a block's tokens in fp32 and over
+ * the blocks in 64 bits.  1 <= top_k <= min(experts, TC_MOE_MAX_TOPK), experts
+ * <= TC_MOE_MAX_EXPERTS (TC_ERR_DIM).  ld_logits, ld_dlogits: 0 = experts.
+ * Outputs overlap no input and one another (TC_ERR_OVERLAP).  Deterministic run
+ * to run.  The forward call takes a little workspace from the stream (under
+ * 1 MiB): make one before a stream capture. */
+typedef struct {
+    int32_t tokens, experts, top_k;
+    tc_dtype_t logits_dtype, grad_dtype;
+    bool renormalize;
+    int32_t ld_logits, ld_dlogits;
+} tc_route_desc;
+tc_status_t tc_moe_route(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid, int32_t *ids,
+                         float *weights, int32_t *counts, float *losses);
+tc_status_t tc_moe_route_async(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                               int32_t *ids, float *weights, int32_t *counts, float *losses, tc_stream *s);
+tc_status_t tc_moe_route_backward(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                                  const int32_t *ids, const int32_t *counts, const float *grad_weights,
+                                  const float *grad_losses, void *dlogits);
+tc_status_t tc_moe_route_backward_async(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                                        const int32_t *ids, const int32_t *counts, const float *grad_weights,
+                                        const float *grad_losses, void *dlogits, tc_stream *s);
+/* Host-only: the validation the calls run first. */
+tc_status_t tc_moe_route_validate(const tc_route_desc *d, const void *logits, const uint8_t *valid, const int32_t *ids,
+                                  const float *weights, const int32_t *counts, const float *losses);
+tc_status_t tc_moe_route_backward_validate(const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                                           const int32_t *ids, const int32_t *counts, const float *grad_weights,
+                                           const float *grad_losses, const void *dlogits);
+
 /* Same GEMM with HOST operands: copies A and B (and C when beta != 0) to the
  * device, runs, copies C back and waits.  Device buffers are cached in the
  * context, so concurrent calls on one context run one after the other.

@@ -19,6 +19,10 @@ that is issued many times; each ``enqueue()`` is then one C call.
 one, ``tc_gemm_q4_weight`` (or ``PreparedGemm``) multiplies by it, and
 ``tc_moe_q4`` (or ``PreparedMoe``) runs a mixture-of-experts layer over two.
 
+``PreparedXent`` (``tc_linear_xent``) and ``PreparedRoute`` (``tc_moe_route``)
+are what such a model trains on: the softmax cross entropy against a vocabulary,
+and the choice of experts with its balance loss, each with its backward call.
+
 There is no fallback: if the library is missing, importing this package
 raises.  Build it with ``python -c "import __graft_entry__ as g; g.build()"``.
 """
@@ -101,6 +105,13 @@ class tc_xent_desc(ctypes.Structure):
                 ("ldx", ctypes.c_int32), ("ldw", ctypes.c_int32), ("lddx", ctypes.c_int32), ("lddw", ctypes.c_int32)]
 
 
+class tc_route_desc(ctypes.Structure):
+    """A routing of tokens to experts (see include/tcgemm.h)."""
+    _fields_ = [("tokens", ctypes.c_int32), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("logits_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int), ("renormalize", ctypes.c_bool),
+                ("ld_logits", ctypes.c_int32), ("ld_dlogits", ctypes.c_int32)]
+
+
 class TcError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -122,6 +133,7 @@ def _load():
     Q = ctypes.POINTER(tc_q4_weight)
     MD = ctypes.POINTER(tc_moe_desc)
     XD = ctypes.POINTER(tc_xent_desc)
+    RD = ctypes.POINTER(tc_route_desc)
     i32 = ctypes.c_int32
     sig = {
         "tc_ctx_create": (st, [ctypes.POINTER(vp), ctypes.c_int]),
@@ -164,6 +176,12 @@ def _load():
         "tc_linear_xent_backward_async": (st, [vp, XD, vp, vp, vp, vp, vp, vp, vp, vp]),
         "tc_linear_xent_validate": (st, [XD, vp, vp, vp, vp, vp]),
         "tc_linear_xent_backward_validate": (st, [XD, vp, vp, vp, vp, vp, vp, vp]),
+        "tc_moe_route": (st, [vp, RD, vp, vp, vp, vp, vp, vp]),
+        "tc_moe_route_async": (st, [vp, RD, vp, vp, vp, vp, vp, vp, vp]),
+        "tc_moe_route_backward": (st, [vp, RD, vp, vp, vp, vp, vp, vp, vp]),
+        "tc_moe_route_backward_async": (st, [vp, RD, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "tc_moe_route_validate": (st, [RD, vp, vp, vp, vp, vp, vp]),
+        "tc_moe_route_backward_validate": (st, [RD, vp, vp, vp, vp, vp, vp, vp]),
         "tc_gemm_host": (st, [vp, D, vp, vp, vp]),
         "tc_gemm_splitk_noalloc": (st, [D, vp, vp, vp, ctypes.c_int, vp]),
         "tc_gemm_validate": (st, [D, vp, vp, vp]),
@@ -195,6 +213,8 @@ EXPORTED = (
     "tc_moe_q4", "tc_moe_q4_async", "tc_moe_q4_validate",
     "tc_linear_xent", "tc_linear_xent_async", "tc_linear_xent_backward", "tc_linear_xent_backward_async",
     "tc_linear_xent_validate", "tc_linear_xent_backward_validate",
+    "tc_moe_route", "tc_moe_route_async", "tc_moe_route_backward", "tc_moe_route_backward_async",
+    "tc_moe_route_validate", "tc_moe_route_backward_validate",
 )
 
 
@@ -753,6 +773,17 @@ def _check_rows(name: str, t, rows: int, cols: int, ld: int, code: int):
         raise ValueError(f"{name} has strides {tuple(t.stride())}, the descriptor rows of {cols} at {ld or cols}")
 
 
+def _prepared_call(name: str, args, stream, wait: bool):
+    """A prepared half of a training loss: synchronously, or on its stream."""
+    if args is None:
+        raise ValueError(f"{name} was not prepared: its outputs are missing")
+    if wait:
+        return _check(getattr(_lib, name)(*args), name)
+    if stream is None:
+        raise ValueError("enqueueing needs the stream the call was prepared with")
+    _check(getattr(_lib, name + "_async")(*args, stream), name + "_async")
+
+
 class PreparedXent:
     """A softmax cross entropy against a vocabulary (tc_linear_xent) with its
     arguments checked and marshalled once: X [tokens, hidden], W [vocab,
@@ -785,26 +816,17 @@ class PreparedXent:
         self._stream = vp(stream.ptr) if stream is not None else None
         self._keep = (ctx, d, X, W, targets, lse, stream, loss, grad, dX, dW)
 
-    def _call(self, name: str, args, wait: bool):
-        if args is None:
-            raise ValueError(f"{name} was not prepared: " + ("give loss" if "backward" not in name else "give grad"))
-        if wait:
-            return _check(getattr(_lib, name)(*args), name)
-        if self._stream is None:
-            raise ValueError("enqueueing needs the stream the call was prepared with")
-        _check(getattr(_lib, name + "_async")(*args, self._stream), name + "_async")
-
     def enqueue(self):
-        self._call("tc_linear_xent", self._forward, False)
+        _prepared_call("tc_linear_xent", self._forward, self._stream, False)
 
     def run(self):
-        self._call("tc_linear_xent", self._forward, True)
+        _prepared_call("tc_linear_xent", self._forward, self._stream, True)
 
     def enqueue_backward(self):
-        self._call("tc_linear_xent_backward", self._backward, False)
+        _prepared_call("tc_linear_xent_backward", self._backward, self._stream, False)
 
     def run_backward(self):
-        self._call("tc_linear_xent_backward", self._backward, True)
+        _prepared_call("tc_linear_xent_backward", self._backward, self._stream, True)
 
 
 def tc_linear_xent(ctx: Context, d: tc_xent_desc, X, W, targets, loss, lse):
@@ -837,6 +859,104 @@ def tc_linear_xent_backward_validate(d: tc_xent_desc, X=1 << 20, W=1 << 40, targ
     return int(_lib.tc_linear_xent_backward_validate(ctypes.byref(d) if d is not None else None, _addr(X), _addr(W),
                                                      _addr(targets), _addr(lse), _addr(grad), _addr(dX) or None,
                                                      _addr(dW) or None))
+
+
+def make_route_desc(tokens, experts, top_k, logits_dtype="f32", grad_dtype=None, *, renormalize=True, ld_logits=0,
+                    ld_dlogits=0) -> tc_route_desc:
+    dt = _DT_NAMES.get(logits_dtype, logits_dtype)
+    return tc_route_desc(tokens, experts, top_k, dt,
+                         _DT_NAMES.get(grad_dtype, grad_dtype) if grad_dtype is not None else dt, bool(renormalize),
+                         ld_logits, ld_dlogits)
+
+
+class PreparedRoute:
+    """A routing of tokens to experts (tc_moe_route) with its arguments checked
+    and marshalled once: logits [tokens, experts], ids int32 [tokens, top_k],
+    counts int32 [experts + 1], and valid (uint8 or bool [tokens]) or None.
+    With ``weights`` (float32, as ids) and ``losses`` (two floats), enqueue()
+    writes ids, weights, counts and losses; with ``dlogits``, and
+    ``grad_weights`` and/or ``grad_losses``, enqueue_backward() writes the
+    logits' gradient.  One C call each; the tensors stay referenced as long as
+    this object."""
+
+    def __init__(self, ctx: Context, d: tc_route_desc, logits, ids, counts, stream: Stream | None = None, *, valid=None,
+                 weights=None, losses=None, grad_weights=None, grad_losses=None, dlogits=None):
+        import torch
+        vp = ctypes.c_void_p
+        if (weights is None) != (losses is None):
+            raise ValueError("weights come with losses")
+        if weights is None and dlogits is None:
+            raise ValueError("give weights and losses, or dlogits")
+        if dlogits is None and (grad_weights is not None or grad_losses is not None):
+            raise ValueError("gradients come with dlogits")
+        if min(d.tokens, d.experts, d.top_k) >= 1:
+            n = d.tokens * d.top_k
+            _check_rows("logits", logits, d.tokens, d.experts, d.ld_logits, d.logits_dtype)
+            _check_rows("dlogits", dlogits, d.tokens, d.experts, d.ld_dlogits, d.grad_dtype)
+            for name, t, count, code in (("ids", ids, n, TC_I32), ("counts", counts, d.experts + 1, TC_I32),
+                                         ("weights", weights, n, TC_F32), ("losses", losses, 2, TC_F32),
+                                         ("grad_weights", grad_weights, n, TC_F32),
+                                         ("grad_losses", grad_losses, 2, TC_F32)):
+                _check_vector(name, t, count, code)
+            if valid is not None and not isinstance(valid, int):
+                if valid.dtype not in (torch.uint8, torch.bool):
+                    raise ValueError("valid must be uint8 or bool")
+                _check_vector("valid", valid, d.tokens, TC_I8)
+        head = (vp(ctx.ptr), ctypes.byref(d), vp(_addr(logits)), vp(_addr(valid) or None), vp(_addr(ids)))
+        self._forward = head + (vp(_addr(weights)), vp(_addr(counts)), vp(_addr(losses))) if weights is not None else None
+        self._backward = head + (vp(_addr(counts)), vp(_addr(grad_weights) or None), vp(_addr(grad_losses) or None),
+                                 vp(_addr(dlogits))) if dlogits is not None else None
+        self._stream = vp(stream.ptr) if stream is not None else None
+        self._keep = (ctx, d, logits, ids, counts, stream, valid, weights, losses, grad_weights, grad_losses, dlogits)
+
+    def enqueue(self):
+        _prepared_call("tc_moe_route", self._forward, self._stream, False)
+
+    def run(self):
+        _prepared_call("tc_moe_route", self._forward, self._stream, True)
+
+    def enqueue_backward(self):
+        _prepared_call("tc_moe_route_backward", self._backward, self._stream, False)
+
+    def run_backward(self):
+        _prepared_call("tc_moe_route_backward", self._backward, self._stream, True)
+
+
+def tc_moe_route(ctx: Context, d: tc_route_desc, logits, ids, weights, counts, losses, valid=None):
+    """Choice of experts, its weights, counts and losses (include/tcgemm.h),
+    synchronously."""
+    PreparedRoute(ctx, d, logits, ids, counts, valid=valid, weights=weights, losses=losses).run()
+
+
+def tc_moe_route_async(ctx: Context, d: tc_route_desc, logits, ids, weights, counts, losses, stream: Stream, valid=None):
+    PreparedRoute(ctx, d, logits, ids, counts, stream, valid=valid, weights=weights, losses=losses).enqueue()
+
+
+def tc_moe_route_backward(ctx: Context, d: tc_route_desc, logits, ids, counts, dlogits, grad_weights=None,
+                          grad_losses=None, valid=None):
+    """The logits' gradient, synchronously."""
+    PreparedRoute(ctx, d, logits, ids, counts, valid=valid, grad_weights=grad_weights, grad_losses=grad_losses,
+                  dlogits=dlogits).run_backward()
+
+
+def tc_moe_route_backward_async(ctx: Context, d: tc_route_desc, logits, ids, counts, dlogits, stream: Stream,
+                                grad_weights=None, grad_losses=None, valid=None):
+    PreparedRoute(ctx, d, logits, ids, counts, stream, valid=valid, grad_weights=grad_weights, grad_losses=grad_losses,
+                  dlogits=dlogits).enqueue_backward()
+
+
+def tc_moe_route_validate(d: tc_route_desc, logits=1 << 40, valid=None, ids=2 << 40, weights=3 << 40, counts=4 << 40,
+                          losses=5 << 40) -> int:
+    """Host-only validation status of a routing."""
+    return int(_lib.tc_moe_route_validate(ctypes.byref(d) if d is not None else None, _addr(logits), _addr(valid) or None,
+                                          _addr(ids), _addr(weights), _addr(counts), _addr(losses)))
+
+
+def tc_moe_route_backward_validate(d: tc_route_desc, logits=1 << 40, valid=None, ids=2 << 40, counts=4 << 40,
+                                   grad_weights=6 << 40, grad_losses=7 << 40, dlogits=8 << 40) -> int:
+    return int(_lib.tc_moe_route_backward_validate(ctypes.byref(d) if d is not None else None, _addr(logits),
+                                                   _addr(valid) or None, _addr(ids), _addr(counts),
+                                                   _addr(grad_weights) or None, _addr(grad_losses) or None, _addr(dlogits)))
 
 
 def tc_gemm_host(ctx: Context, d: tc_gemm_desc, A_host, B_host, C_host):

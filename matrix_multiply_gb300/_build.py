@@ -25,7 +25,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", f"-I{INCLUDE}"]
 SOURCES = ["api.cpp", "tc_mma.cu", "ffma.cu", "pack.cu", "gemv.cu", "q4.cu", "q4_gemv.cu", "q4_mma.cu", "moe.cu",
-           "xent.cu"]
+           "xent.cu", "route.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "elem.cuh", "q4.cuh"]
 
 

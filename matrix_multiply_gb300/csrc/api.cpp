@@ -2277,6 +2277,126 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     return TC_OK;
 }
 
+// ------------------------------------------------------- routing to experts
+
+struct RouteNorm {
+    int64_t ld, ldd, logit_bytes, valid_bytes, pair_bytes, count_bytes;
+};
+
+tc_status_t check_route(const tc_route_desc *d, const void *logits, RouteNorm *out)
+{
+    if (!d || !logits) return TC_ERR_NULL;
+    if (d->tokens < 1 || d->experts < 1 || d->experts > TC_MOE_MAX_EXPERTS || d->top_k < 1 || d->top_k > TC_MOE_MAX_TOPK ||
+        d->top_k > d->experts)
+        return TC_ERR_DIM;
+    if ((d->logits_dtype != TC_F16 && d->logits_dtype != TC_BF16 && d->logits_dtype != TC_F32) ||
+        (d->grad_dtype != d->logits_dtype && d->grad_dtype != TC_F32))
+        return TC_ERR_DTYPE;
+    RouteNorm n;
+    n.ld = d->ld_logits ? d->ld_logits : d->experts;
+    n.ldd = d->ld_dlogits ? d->ld_dlogits : d->experts;
+    if (n.ld < d->experts || n.ldd < d->experts) return TC_ERR_LD;
+    if (!extent(d->tokens, d->experts, n.ld, 1, 0, (int64_t)elem_size(d->logits_dtype), &n.logit_bytes)) return TC_ERR_OVERFLOW;
+    n.valid_bytes = d->tokens;
+    n.pair_bytes = 4LL * d->tokens * d->top_k;
+    n.count_bytes = 4LL * (d->experts + 1);
+    *out = n;
+    return TC_OK;
+}
+
+tc_status_t validate_route(const tc_route_desc *d, const void *logits, const uint8_t *valid, const int32_t *ids,
+                           const float *weights, const int32_t *counts, const float *losses, RouteNorm *n)
+{
+    const tc_status_t st = check_route(d, logits, n);
+    if (st != TC_OK) return st;
+    if (!ids || !weights || !counts || !losses) return TC_ERR_NULL;
+    const Range outs[] = {{ids, n->pair_bytes}, {weights, n->pair_bytes}, {counts, n->count_bytes}, {losses, 8}};
+    const Range ins[] = {{logits, n->logit_bytes}, {valid, n->valid_bytes}};
+    return check_apart(outs, ins);
+}
+
+tc_status_t validate_route_backward(const tc_route_desc *d, const void *logits, const uint8_t *valid, const int32_t *ids,
+                                    const int32_t *counts, const float *grad_weights, const float *grad_losses,
+                                    const void *dlogits, RouteNorm *n)
+{
+    const tc_status_t st = check_route(d, logits, n);
+    if (st != TC_OK) return st;
+    if (!ids || !counts || !dlogits) return TC_ERR_NULL;
+    int64_t bytes;
+    if (!extent(d->tokens, d->experts, n->ldd, 1, 0, (int64_t)elem_size(d->grad_dtype), &bytes)) return TC_ERR_OVERFLOW;
+    const Range outs[] = {{dlogits, bytes}};
+    const Range ins[] = {{logits, n->logit_bytes}, {valid, n->valid_bytes}, {ids, n->pair_bytes},
+                         {counts, n->count_bytes}, {grad_weights, n->pair_bytes}, {grad_losses, 8}};
+    return check_apart(outs, ins);
+}
+
+tc_status_t run_route(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid, int32_t *ids,
+                      float *weights, int32_t *counts, float *losses, tc_stream *s)
+{
+    if (!ctx || !s) return TC_ERR_NULL;
+    RouteNorm n;
+    tc_status_t st = validate_route(d, logits, valid, ids, weights, counts, losses, &n);
+    if (st != TC_OK) return st;
+    std::lock_guard<std::mutex> lk(ctx->mu);
+    if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    const int blocks = route_blocks(d->tokens, d->experts, ctx->num_sms);
+    // (the same for every call, so that any stands for those of a capture)
+    const size_t row = round_up((size_t)(TC_MOE_MAX_EXPERTS + 1) * 4 * ctx->num_sms, 256);
+    if ((st = reserve(s, 256, 2 * row)) != TC_OK) return st;
+    RouteArgs a{};
+    a.T = d->tokens;
+    a.E = d->experts;
+    a.k = d->top_k;
+    a.dtype = d->logits_dtype;
+    a.renorm = d->renormalize;
+    a.logits = logits;
+    a.ld = n.ld;
+    a.valid = valid;
+    a.ids = ids;
+    a.weights = weights;
+    a.counts = counts;
+    a.losses = losses;
+    a.part = static_cast<float *>(s->rx);
+    a.part_n = reinterpret_cast<int *>(static_cast<uint8_t *>(s->rx) + row);
+    int launches = 0;
+    if (launch_route(a, blocks, s->st, &launches) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += launches;
+    ctx->last = "moe_route_e" + std::to_string(a.E) + "_k" + std::to_string(a.k) + "_b" + std::to_string(blocks);
+    return TC_OK;
+}
+
+tc_status_t run_route_backward(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                               const int32_t *ids, const int32_t *counts, const float *grad_weights,
+                               const float *grad_losses, void *dlogits, tc_stream *s)
+{
+    if (!ctx || !s) return TC_ERR_NULL;
+    RouteNorm n;
+    const tc_status_t st = validate_route_backward(d, logits, valid, ids, counts, grad_weights, grad_losses, dlogits, &n);
+    if (st != TC_OK) return st;
+    std::lock_guard<std::mutex> lk(ctx->mu);
+    if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
+    RouteGradArgs a{};
+    a.T = d->tokens;
+    a.E = d->experts;
+    a.k = d->top_k;
+    a.dtype = d->logits_dtype;
+    a.renorm = d->renormalize;
+    a.logits = logits;
+    a.ld = n.ld;
+    a.valid = valid;
+    a.ids = ids;
+    a.counts = counts;
+    a.grad_weights = grad_weights;
+    a.grad_losses = grad_losses;
+    a.dl = dlogits;
+    a.ld_dl = n.ldd;
+    a.dl_dtype = d->grad_dtype;
+    if (launch_route_grad(a, ctx->num_sms, s->st) != cudaSuccess) return TC_ERR_CUDA;
+    ctx->launches += 1;
+    ctx->last = "moe_route_grad_e" + std::to_string(a.E) + "_k" + std::to_string(a.k);
+    return TC_OK;
+}
+
 // A C entry lets no C++ exception out (the name of the last kernel is a
 // std::string, the context's lock may throw).
 template <typename F>
@@ -2640,6 +2760,55 @@ tc_status_t tc_linear_xent_backward_validate(const tc_xent_desc *d, const void *
 {
     XentNorm n;
     return validate_xent_backward(d, X, W, targets, lse, grad, dX, dW, &n);
+}
+
+tc_status_t tc_moe_route_async(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                               int32_t *ids, float *weights, int32_t *counts, float *losses, tc_stream *s)
+{
+    return guarded([&] { return run_route(ctx, d, logits, valid, ids, weights, counts, losses, s); });
+}
+
+tc_status_t tc_moe_route(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid, int32_t *ids,
+                         float *weights, int32_t *counts, float *losses)
+{
+    if (!ctx) return TC_ERR_NULL;
+    const tc_status_t st = guarded([&] { return run_route(ctx, d, logits, valid, ids, weights, counts, losses, ctx->def); });
+    return st == TC_OK ? tc_stream_sync(ctx->def) : st;
+}
+
+tc_status_t tc_moe_route_backward_async(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                                        const int32_t *ids, const int32_t *counts, const float *grad_weights,
+                                        const float *grad_losses, void *dlogits, tc_stream *s)
+{
+    return guarded([&] {
+        return run_route_backward(ctx, d, logits, valid, ids, counts, grad_weights, grad_losses, dlogits, s);
+    });
+}
+
+tc_status_t tc_moe_route_backward(tc_ctx *ctx, const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                                  const int32_t *ids, const int32_t *counts, const float *grad_weights,
+                                  const float *grad_losses, void *dlogits)
+{
+    if (!ctx) return TC_ERR_NULL;
+    const tc_status_t st = guarded([&] {
+        return run_route_backward(ctx, d, logits, valid, ids, counts, grad_weights, grad_losses, dlogits, ctx->def);
+    });
+    return st == TC_OK ? tc_stream_sync(ctx->def) : st;
+}
+
+tc_status_t tc_moe_route_validate(const tc_route_desc *d, const void *logits, const uint8_t *valid, const int32_t *ids,
+                                  const float *weights, const int32_t *counts, const float *losses)
+{
+    RouteNorm n;
+    return validate_route(d, logits, valid, ids, weights, counts, losses, &n);
+}
+
+tc_status_t tc_moe_route_backward_validate(const tc_route_desc *d, const void *logits, const uint8_t *valid,
+                                           const int32_t *ids, const int32_t *counts, const float *grad_weights,
+                                           const float *grad_losses, const void *dlogits)
+{
+    RouteNorm n;
+    return validate_route_backward(d, logits, valid, ids, counts, grad_weights, grad_losses, dlogits, &n);
 }
 
 tc_status_t tc_gemm_batched_async(tc_ctx *ctx, const tc_gemm_batched_desc *bd, const void *A, const void *B,

@@ -399,6 +399,35 @@ struct XentRoundArgs {
 };
 cudaError_t launch_xent_round(const XentRoundArgs &a, cudaStream_t st);
 
+// ------------------------------------------- routing to experts (route.cu)
+struct RouteArgs {
+    int T, E, k, dtype, renorm;
+    const void *logits;
+    long long ld;
+    const uint8_t *valid;      // T, or null
+    int *ids;                  // [T, k]
+    float *weights;            // [T, k]
+    int *counts;               // [E + 1], the tokens last
+    float *losses;             // [2]
+    float *part;               // scratch: [blocks][E + 1]
+    int *part_n;               // scratch: [blocks][E + 1]
+};
+// the blocks of a call (part and part_n have a row for each)
+int route_blocks(int T, int E, int num_sms);
+cudaError_t launch_route(const RouteArgs &a, int blocks, cudaStream_t st, int *launches);
+struct RouteGradArgs {
+    int T, E, k, dtype, renorm;
+    const void *logits;
+    long long ld;
+    const uint8_t *valid;
+    const int *ids, *counts;
+    const float *grad_weights, *grad_losses;   // either may be null
+    void *dl;
+    long long ld_dl;
+    int dl_dtype;
+};
+cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t st);
+
 // ------------------------------------------------------------- 4-bit weights
 // A tc_q4_weight after validation (the public header states the format):
 // row n's codes at codes + n * ldw / 2 bytes, the scale of (n, k) at

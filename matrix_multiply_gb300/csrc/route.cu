@@ -1,0 +1,436 @@
+// Routing of tokens to experts from their logits l [T, E], with the balance
+// loss, its counts and the gradient of it all (the public header states the
+// formulas).
+//
+// A warp takes a token, lane g its experts g C .. g C + C - 1 (C = E / 32
+// rounded up to a power of two), so that the lowest lane with the largest value
+// holds the lowest index.  One pass over the logits forward, one backward: the
+// softmax is computed again there from them, nothing of size T E is kept.  The
+// means of the probabilities stay in the lanes' registers over a warp's tokens
+// and are added up in a fixed order, over a block's warps and then over the
+// blocks, which a second launch does; counts are whole numbers.
+#include "elem.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "../../include/tcgemm.h"
+
+#include <algorithm>
+#include <climits>
+#include <type_traits>
+
+namespace tc {
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr unsigned FULL = 0xffffffffu;
+
+// Whole numbers in the order of the floats they stand for: -0 as 0, a NaN (which
+// the addition leaves with its sign clear and every other bit set) above all.
+__device__ __forceinline__ int key_of(float x)
+{
+    const int s = __float_as_int(__fadd_rn(x, 0.0f));
+    return s ^ ((s >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float of_key(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
+constexpr int KEY_NEG_INF = (int)0x807fffffu;      // key_of(-inf); INT_MIN, below it, is no value
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+
+template <int DT>
+__device__ __forceinline__ float load_one(const void *p, long long i)
+{
+    return load_c(p, i, DT);
+}
+
+// The lane's C values of a row (`vec`: the row starts on 16 bytes and has a
+// multiple of 16 bytes); -inf past the last expert.
+template <int DT, int C>
+__device__ __forceinline__ void load_row(const void *row, int E, int lane, bool vec, float (&v)[C])
+{
+    constexpr int PER = DT == TC_F32 ? 4 : 8;
+    if constexpr (C >= PER) {
+        if (vec) {
+#pragma unroll
+            for (int q = 0; q < C / PER; ++q) {
+                const int e = lane * C + q * PER;
+                if (e < E) {
+                    if constexpr (DT == TC_F32) {
+                        const float4 x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e));
+                        v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
+                    } else {
+                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + e));
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (DT == TC_BF16) {
+                                v[8 * q + 2 * j] = __uint_as_float(w[j] << 16);
+                                v[8 * q + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                            } else {
+                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+                                v[8 * q + 2 * j] = f.x;
+                                v[8 * q + 2 * j + 1] = f.y;
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) v[PER * q + j] = -INFINITY;
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int e = lane * C + i;
+        v[i] = e < E ? load_one<DT>(row, e) : -INFINITY;
+    }
+}
+
+template <int C>
+struct Shape {
+    // (16 values a lane, their running means and the two candidates: 128 registers)
+    static constexpr int THREADS = C == 16 ? 512 : 1024;
+    static constexpr int WARPS = THREADS / 32;
+};
+
+// The sums over all blocks' rows of `part` (E + 1 numbers each, the last one that
+// of lse^2, and E + 1 counts, the last one that of the tokens), in the order of
+// the blocks; then the counts and the losses.  A whole block; `sums` and `ns`
+// hold E + 1 numbers each.
+__device__ __forceinline__ void finish(const RouteArgs &a, const float *part, const int *counts, int blocks, double *sums,
+                                       int *ns)
+{
+    const int n1 = a.E + 1;
+    for (int i = threadIdx.x; i < n1; i += blockDim.x) {
+        double s = 0.0;
+        int n = 0;
+#pragma unroll 8
+        for (int b = 0; b < blocks; ++b) {
+            s += (double)part[(long long)b * n1 + i];
+            n += counts[(long long)b * n1 + i];
+        }
+        sums[i] = s;
+        ns[i] = n;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n1; i += blockDim.x) a.counts[i] = ns[i];
+    if (threadIdx.x < 32) {
+        const double n = ns[a.E] > 0 ? ns[a.E] : 1;
+        double b = 0.0;
+        for (int e = threadIdx.x; e < a.E; e += 32) b += (double)ns[e] * sums[e];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(FULL, b, o);
+        if (threadIdx.x == 0) {
+            a.losses[0] = (float)(b * a.E / (n * n * a.k));
+            a.losses[1] = (float)(sums[a.E] / n);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(1024) finish_kernel(const RouteArgs a, int blocks)
+{
+    __shared__ double sums[TC_MOE_MAX_EXPERTS + 1];
+    __shared__ int ns[TC_MOE_MAX_EXPERTS + 1];
+    griddep_wait();
+    griddep_launch_dependents();
+    finish(a, a.part, a.part_n, blocks, sums, ns);
+}
+
+template <int DT, int C>
+__global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const RouteArgs a)
+{
+    constexpr int W = Shape<C>::WARPS;
+    extern __shared__ float rows[];                   // [W][E]: the warps' means
+    __shared__ float zs[W];
+    __shared__ int tokens[W];
+    __shared__ int chosen[TC_MOE_MAX_EXPERTS + 1];
+    __shared__ int slot_id[W][TC_MOE_MAX_TOPK];
+    __shared__ float slot_e[W][TC_MOE_MAX_TOPK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int i = threadIdx.x; i <= a.E; i += Shape<C>::THREADS) chosen[i] = 0;
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const long long es = DT == TC_F32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && a.ld * es % 16 == 0 && a.E * es % 16 == 0;
+    float mean[C], z = 0.0f;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) mean[i] = 0.0f;
+    for (long long t = (long long)blockIdx.x * W + warp; t < a.T; t += (long long)gridDim.x * W) {
+        float v[C];
+        load_row<DT, C>(static_cast<const char *>(a.logits) + t * a.ld * es, a.E, lane, vec, v);
+        const bool valid = a.valid == nullptr || a.valid[t] != 0;
+        // the lane's two largest, the earlier of equal ones first
+        int k1 = INT_MIN, k2 = INT_MIN, i1 = 0, i2 = 0;
+        unsigned used = 0;
+        auto two = [&]() {
+            k1 = k2 = INT_MIN;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int e = lane * C + i;
+                const int k = (e < a.E && !(used >> i & 1u)) ? key_of(v[i]) : INT_MIN;
+                if (k > k1) {
+                    k2 = k1, i2 = i1;
+                    k1 = k, i1 = i;
+                } else if (k > k2) {
+                    k2 = k, i2 = i;
+                }
+            }
+        };
+        two();
+        int top = __reduce_max_sync(FULL, k1);
+        int got = 0;
+        if (valid && top > KEY_NEG_INF) {
+            const float big = of_key(top);
+            float s = 0.0f;
+            float e[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                e[i] = exp2_approx((v[i] - big) * LOG2E);
+                s += e[i];
+            }
+            s = warp_sum(s);
+            const float inv = 1.0f / s;
+#pragma unroll
+            for (int i = 0; i < C; ++i) mean[i] = fmaf(e[i], inv, mean[i]);
+            const float lse = big + logf(s);
+            z = fmaf(lse, lse, z);
+            ++n;
+            // one after the other the largest that is left; a lane whose two are
+            // taken looks for the next two (8 of 256: in one round of eight)
+            bool second = true;
+            for (; got < a.k && top > KEY_NEG_INF; ++got) {
+                const int src = __ffs(__ballot_sync(FULL, k1 == top)) - 1;
+                bool look = false;
+                if (lane == src) {
+                    const int id = lane * C + i1;
+                    slot_id[warp][got] = id;
+                    slot_e[warp][got] = exp2_approx((of_key(top) - big) * LOG2E) * inv;
+                    atomicAdd(&chosen[id], 1);
+                    used |= 1u << i1;
+                    k1 = k2, i1 = i2, k2 = INT_MIN;
+                    look = C > 2 && !second;
+                    second = false;
+                }
+                if (C > 2 && __any_sync(FULL, look)) {
+                    if (look) {
+                        two();
+                        second = true;
+                    }
+                }
+                top = __reduce_max_sync(FULL, k1);
+            }
+        }
+        __syncwarp();
+        const bool mine = lane < got;
+        float w = mine ? slot_e[warp][lane & (TC_MOE_MAX_TOPK - 1)] : 0.0f;
+        if (a.renorm) {
+            const float total = warp_sum(w);
+            if (mine) w /= total;
+        }
+        if (lane < a.k) {
+            a.ids[t * a.k + lane] = mine ? slot_id[warp][lane & (TC_MOE_MAX_TOPK - 1)] : -1;
+            a.weights[t * a.k + lane] = w;
+        }
+        __syncwarp();
+    }
+    // the block's sums, over its warps in their order
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        if (lane * C + i < a.E) rows[warp * a.E + lane * C + i] = mean[i];
+    if (lane == 0) zs[warp] = z, tokens[warp] = n;
+    __syncthreads();
+    float *part = a.part + (long long)blockIdx.x * (a.E + 1);
+    int *part_n = a.part_n + (long long)blockIdx.x * (a.E + 1);
+    for (int e = threadIdx.x; e <= a.E; e += Shape<C>::THREADS) {
+        float s = 0.0f;
+        int c = e < a.E ? chosen[e] : 0;
+#pragma unroll 8
+        for (int w = 0; w < W; ++w) {
+            s += e < a.E ? rows[w * a.E + e] : zs[w];
+            if (e == a.E) c += tokens[w];
+        }
+        part[e] = s;
+        part_n[e] = c;
+    }
+    if (gridDim.x > 1) return;
+    // the only block: what it wrote is all there is
+    __shared__ double sums[TC_MOE_MAX_EXPERTS + 1];
+    __syncthreads();
+    finish(a, part, part_n, 1, sums, chosen);
+}
+
+template <int DT, int C>
+__global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradArgs a)
+{
+    constexpr int W = 8;
+    // a token's probabilities, where the lanes of the chosen experts find theirs,
+    // and the gradients through the weights, where those lanes leave them
+    __shared__ __align__(16) float probs[W][32 * C];
+    __shared__ __align__(16) float through[W][32 * C];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < C; ++i) through[warp][lane * C + i] = 0.0f;
+    griddep_wait();
+    griddep_launch_dependents();
+
+    const long long es = DT == TC_F32 ? 4 : 2, ed = a.dl_dtype == TC_F32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0 && a.ld * es % 16 == 0 && a.E * es % 16 == 0;
+    const bool vec_out = (reinterpret_cast<uintptr_t>(a.dl) & 15u) == 0 && a.ld_dl * ed % 16 == 0 && a.E * ed % 16 == 0;
+    const float n = (float)max(a.counts[a.E], 1);
+    // the balance loss's and the other's factors; f times the first
+    const float gb = a.grad_losses ? a.grad_losses[0] * (float)a.E / n : 0.0f;
+    const float gz = a.grad_losses ? a.grad_losses[1] * 2.0f / n : 0.0f;
+    float f[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int e = lane * C + i;
+        f[i] = e < a.E ? gb * ((float)a.counts[e] / (n * (float)a.k)) : 0.0f;
+    }
+    for (long long t = (long long)blockIdx.x * W + warp; t < a.T; t += (long long)gridDim.x * W) {
+        float v[C];
+        load_row<DT, C>(static_cast<const char *>(a.logits) + t * a.ld * es, a.E, lane, vec, v);
+        const bool valid = a.valid == nullptr || a.valid[t] != 0;
+        int id = -1;
+        float gw = 0.0f;
+        if (a.grad_weights && lane < a.k) {
+            id = a.ids[t * a.k + lane];
+            gw = a.grad_weights[t * a.k + lane];
+        }
+        int key = INT_MIN;
+#pragma unroll
+        for (int i = 0; i < C; ++i) key = max(key, lane * C + i < a.E ? key_of(v[i]) : INT_MIN);
+        const int top = __reduce_max_sync(FULL, key);
+        if (!valid || top <= KEY_NEG_INF) {
+#pragma unroll
+            for (int i = 0; i < C; ++i) v[i] = 0.0f;
+        } else {
+            const float big = of_key(top);
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                v[i] = exp2_approx((v[i] - big) * LOG2E);
+                s += v[i];
+            }
+            s = warp_sum(s);
+            const float inv = 1.0f / s;
+            float fp = 0.0f;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                v[i] *= inv;
+                fp = fmaf(f[i], v[i], fp);
+            }
+            // dl = p (f - sum f p + gz lse + what comes through the weights)
+            float all = gz * (big + logf(s)) - warp_sum(fp);
+            if (a.grad_weights) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) probs[warp][lane * C + i] = v[i];
+                __syncwarp();
+                const bool on = id >= 0 && id < a.E;
+                const float p = on ? probs[warp][id] : 0.0f;
+                const float dot = warp_sum(on ? gw * p : 0.0f);
+                if (a.renorm) {
+                    const float r = 1.0f / warp_sum(p);
+                    if (on) atomicAdd(&through[warp][id], p * r * (gw - dot * r));
+                } else {
+                    if (on) atomicAdd(&through[warp][id], p * gw);
+                    all -= dot;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < C; ++i) v[i] = fmaf(v[i], f[i] + all, through[warp][lane * C + i]);
+                __syncwarp();
+                if (on) through[warp][id] = 0.0f;
+            } else {
+#pragma unroll
+                for (int i = 0; i < C; ++i) v[i] *= f[i] + all;
+            }
+        }
+        char *row = static_cast<char *>(a.dl) + t * a.ld_dl * ed;
+        bool stored = false;
+        if constexpr (C >= 4) {
+            if (vec_out && a.dl_dtype == TC_F32) {
+#pragma unroll
+                for (int q = 0; q < C / 4; ++q)
+                    if (lane * C + 4 * q < a.E)
+                        *reinterpret_cast<float4 *>(row + (lane * C + 4 * q) * 4) =
+                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                stored = true;
+            }
+        }
+        if constexpr (C >= 8) {
+            if (vec_out && a.dl_dtype != TC_F32) {
+#pragma unroll
+                for (int q = 0; q < C / 8; ++q)
+                    if (lane * C + 8 * q < a.E)
+                        *reinterpret_cast<uint4 *>(row + (lane * C + 8 * q) * 2) =
+                            make_uint4(pack2(v[8 * q], v[8 * q + 1], a.dl_dtype), pack2(v[8 * q + 2], v[8 * q + 3], a.dl_dtype),
+                                       pack2(v[8 * q + 4], v[8 * q + 5], a.dl_dtype), pack2(v[8 * q + 6], v[8 * q + 7], a.dl_dtype));
+                stored = true;
+            }
+        }
+        if (!stored) {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+                if (lane * C + i < a.E) store_c1(row, lane * C + i, v[i], a.dl_dtype);
+        }
+    }
+}
+
+// The call with the type and the values a lane as constants.
+template <typename F>
+cudaError_t by_shape(int dtype, int E, F f)
+{
+    const auto wide = [&](auto dt) {
+        if (E <= 32) return f(dt, std::integral_constant<int, 1>{});
+        if (E <= 64) return f(dt, std::integral_constant<int, 2>{});
+        if (E <= 128) return f(dt, std::integral_constant<int, 4>{});
+        if (E <= 256) return f(dt, std::integral_constant<int, 8>{});
+        return f(dt, std::integral_constant<int, 16>{});
+    };
+    if (dtype == TC_F32) return wide(std::integral_constant<int, TC_F32>{});
+    if (dtype == TC_BF16) return wide(std::integral_constant<int, TC_BF16>{});
+    return wide(std::integral_constant<int, TC_F16>{});
+}
+
+}  // namespace
+
+int route_blocks(int T, int E, int num_sms)
+{
+    const int warps = E <= 256 ? Shape<8>::WARPS : Shape<16>::WARPS;
+    // two rounds of one block cost less than a second launch
+    if (T <= 2 * warps) return 1;
+    return (int)std::min<long long>(((long long)T + warps - 1) / warps, num_sms);
+}
+
+cudaError_t launch_route(const RouteArgs &a, int blocks, cudaStream_t st, int *launches)
+{
+    *launches = blocks > 1 ? 2 : 1;
+    const cudaError_t e = by_shape(a.dtype, a.E, [&](auto dt, auto c) {
+        constexpr int C = decltype(c)::value;
+        const size_t smem = (size_t)Shape<C>::WARPS * a.E * sizeof(float);      // 32 KiB at most
+        return launch_dependent(route_kernel<decltype(dt)::value, C>, dim3((unsigned)blocks), dim3(Shape<C>::THREADS), smem, st,
+                                1u, a);
+    });
+    if (e != cudaSuccess || blocks == 1) return e;
+    return launch_dependent(finish_kernel, dim3(1), dim3(1024), 0, st, 1u, a, blocks);
+}
+
+cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t st)
+{
+    return by_shape(a.dtype, a.E, [&](auto dt, auto c) {
+        const unsigned grid = (unsigned)std::min<long long>(((long long)a.T + 7) / 8, 8LL * num_sms);
+        return launch_dependent(route_grad_kernel<decltype(dt)::value, decltype(c)::value>, dim3(grid), dim3(256), 0, st, 1u, a);
+    });
+}
+
+}  // namespace tc
