@@ -182,6 +182,7 @@ struct Plan {
     int seg0_split = 1, seg1_split = 1;
     bool tma_store = true;
     bool pack_a = false, pack_b = false;
+    int seg_kb = 0;            // sums cut along K, this many K blocks each (0: whole)
     int64_t tiles = 0, units = 0;
     std::string name;
 };
@@ -864,7 +865,8 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     a.bias = epi ? epi->bias : nullptr;
     a.act = epi ? (int)epi->activation : (int)TC_ACT_NONE;
     a.col_scale = col_scale;
-    a.slice_kb = p.i8acc ? I8_SLICE_KB : 0;
+    a.slice_kb = p.i8acc ? I8_SLICE_KB : p.seg_kb > 0 ? p.seg_kb : a.num_kb;
+    L.seg = p.seg_kb > 0 && !xent;
     const int64_t kb_per_unit = a.num_kb;
     a.timeout_ns = 4000000000ull + (unsigned long long)kb_per_unit * 20000ull;
     {
@@ -2006,6 +2008,15 @@ int64_t xent_piece(int64_t vocab, int64_t bytes)
     return std::min<int64_t>(cdiv(cdiv(vocab, cdiv(vocab, most)), 256) * 256, vocab);
 }
 
+// K blocks that are summed on the tensor core before the sum is added in fp32,
+// rounded to nearest, where results in fp32 depend on it: the tensor core
+// truncates (lse over a hidden size of 4096 1.4e-6 off in one sum).
+constexpr int XENT_SEG_KB = 16;
+// Rows up to which G is held in two parts for 16-bit gradients too: its products
+// then wait for W and dW, not for the tensor core, and the rounding of G would
+// be as large as that of the gradients.
+constexpr int64_t XENT_TWO_PART_ROWS = 128;
+
 // The tensor-core kernel on whole tiles: the shape with the least modelled time.
 Plan plan_xent(int64_t M, int64_t N, int64_t K, int num_sms, const Force &f)
 {
@@ -2030,7 +2041,9 @@ Plan plan_xent(int64_t M, int64_t N, int64_t K, int num_sms, const Force &f)
         g.cg = g.bn = 0;
         return plan_xent(M, N, K, num_sms, g);
     }
-    p.group_m = f.group_m > 0 ? f.group_m : 4;
+    // bands of A's rows that stay in L2 while B passes once: 4096 x 131072 x 4096
+    // warm 2.60 ms in bands of 16 tile rows (32 MiB), 2.64 of 8, 2.72 of 4
+    p.group_m = f.group_m > 0 ? f.group_m : (int)std::min<int64_t>(std::max<int64_t>((32 << 20) / (BM * p.cg * K * 2), 4), 64);
     char buf[48];
     std::snprintf(buf, sizeof buf, "tcgen05_%dx%d%s", BM * p.cg, p.bn, p.cg == 2 ? "_pair" : "");
     p.name = buf;
@@ -2100,7 +2113,8 @@ tc_status_t run_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const vo
         Force same = f;
         same.bn = first.bn;
         same.cg = first.cg;
-        const Plan p = plan_xent(T, N, H, ctx->num_sms, same);
+        Plan p = plan_xent(T, N, H, ctx->num_sms, same);
+        p.seg_kb = XENT_SEG_KB;
         const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, TC_F32, false, true, d->scale, 0.0f, pack_x ? ldp : n.ldx,
                                           pack_w ? ldp : n.ldw, N);
         const void *Xv = pack_x ? rx + o_x : X;
@@ -2154,23 +2168,26 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     const int64_t T = d->tokens, H = d->hidden, V = d->vocab, ldp = (int64_t)round_up((size_t)H, 64);
     const int64_t es = (int64_t)elem_size(d->grad_dtype);
     const bool pack_w = !aligned16(W) || n.ldw % 8 != 0, f16 = d->dtype == TC_F16;
-    const int parts = d->grad_dtype == TC_F32 ? 2 : 1;
-    const int64_t cols = xent_piece(V, T * 2 * parts + (pack_w ? ldp * 2 : 0)), ldg = (int64_t)round_up((size_t)cols, 64);
-    // dX of several pieces is summed in fp32
-    const bool sum = dX && cols < V && d->grad_dtype != TC_F32;
+    const bool f32 = d->grad_dtype == TC_F32;
+    // G in two parts, one below the other: dX is then a product of 2 T rows whose
+    // halves are added, dW one over 2 T rows of X, repeated
+    const int64_t parts = f32 || T <= XENT_TWO_PART_ROWS ? 2 : 1, TG = T * parts;
+    const int64_t cols = xent_piece(V, TG * 2 + (pack_w ? ldp * 2 : 0)), ldg = (int64_t)round_up((size_t)cols, 64);
+    // dX of several pieces or parts is summed in fp32
+    const bool sum = dX && (cols < V || parts == 2);
+    if (TG > INT32_MAX) return TC_ERR_OVERFLOW;
     const Force f = read_force();
     std::lock_guard<std::mutex> lk(ctx->mu);
     if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
     Carve c;
     const size_t o_cp = c.take(T * 4), o_cy = c.take(T * 4), o_un = c.take(f16 ? H * 4 : 0);
-    const size_t o_x = c.take(T * ldp * 2), o_w = c.take(pack_w ? cols * ldp * 2 : 0), o_sum = c.take(sum ? T * H * 4 : 0);
-    size_t o_g[2];
-    for (int i = 0; i < 2; ++i) o_g[i] = c.take(i < parts ? T * ldg * 2 : 0);
+    const size_t o_x = c.take(TG * ldp * 2), o_w = c.take(pack_w ? cols * ldp * 2 : 0), o_sum = c.take(sum ? TG * H * 4 : 0);
+    const size_t o_g = c.take(TG * ldg * 2);
     if ((st = reserve(s, 256, c.at)) != TC_OK) return st;
     uint8_t *rx = static_cast<uint8_t *>(s->rx);
     const float *unscale = f16 ? reinterpret_cast<const float *>(rx + o_un) : nullptr;
 
-    // the two products of the piece at v0 with part i of G
+    // the two products of the piece at v0 with G
     struct Product {
         tc_gemm_desc d;
         Norm n;
@@ -2178,30 +2195,41 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         const void *A, *B;
         void *C;
     };
-    auto product = [&](bool rows, int64_t v0, int i, Product *q) {
+    auto product = [&](bool rows, int64_t v0, Product *q) {
         const int64_t N = std::min(cols, V - v0);
-        const uint8_t *Gi = rx + o_g[i];
-        q->A = Gi;
+        q->A = rx + o_g;
         if (rows) {
             q->B = pack_w ? static_cast<const void *>(rx + o_w) : static_cast<const uint16_t *>(W) + v0 * n.ldw;
             q->C = sum ? static_cast<void *>(rx + o_sum) : dX;
-            q->d = xent_desc(T, H, N, d->dtype, sum ? TC_F32 : d->grad_dtype, false, false, d->scale,
-                             v0 > 0 || i > 0 ? 1.0f : 0.0f, ldg, pack_w ? ldp : n.ldw, sum ? H : n.lddx);
+            q->d = xent_desc(TG, H, N, d->dtype, sum ? TC_F32 : d->grad_dtype, false, false, d->scale, v0 > 0 ? 1.0f : 0.0f,
+                             ldg, pack_w ? ldp : n.ldw, sum ? H : n.lddx);
         } else {
             q->B = rx + o_x;
             q->C = static_cast<uint8_t *>(dW) + v0 * n.lddw * es;
-            q->d = xent_desc(N, H, T, d->dtype, d->grad_dtype, true, false, d->scale, i > 0 ? 1.0f : 0.0f, ldg, ldp, n.lddw);
+            q->d = xent_desc(N, H, TG, d->dtype, d->grad_dtype, true, false, d->scale, 0.0f, ldg, ldp, n.lddw);
         }
-        const tc_status_t r = validate(&q->d, q->A, q->B, q->C, 1, 0, 0, 0, &q->n);
-        return r != TC_OK ? r : make_plan(&q->d, q->n, q->A, q->B, ctx->num_sms, &q->p, false);
+        tc_status_t r = validate(&q->d, q->A, q->B, q->C, 1, 0, 0, 0, &q->n);
+        if (r == TC_OK) r = make_plan(&q->d, q->n, q->A, q->B, ctx->num_sms, &q->p, false);
+        // (8 tile rows by 9 columns in flight read least: the gradients of
+        // 4096 x 65536 x 4096 take 4.25 ms, with 4 rows 4.34)
+        if (f.group_m == 0) q->p.group_m = 8;
+        if (r != TC_OK || !f32) return r;
+        if (q->p.cg == 1 && q->p.bn == 192) {     // a shape that cannot cut its sums
+            const bool pa = q->p.pack_a, pb = q->p.pack_b;
+            q->p = plan_xent(q->d.M, q->d.N, q->d.K, ctx->num_sms, Force{});
+            q->p.pack_a = pa;
+            q->p.pack_b = pb;
+        }
+        q->p.seg_kb = XENT_SEG_KB;
+        return r;
     };
     // the largest workspace of them (a cluster split may have to go through memory)
     size_t ws = 256;
     for (const int64_t v0 : {(int64_t)0, (cdiv(V, cols) - 1) * cols}) {
-        for (int i = 0; i < 2; ++i) {
-            if (i == 0 ? !dX : !dW) continue;
+        for (const bool rows : {true, false}) {
+            if (rows ? !dX : !dW) continue;
             Product q;
-            if ((st = product(i == 0, v0, 0, &q)) != TC_OK) return st;
+            if ((st = product(rows, v0, &q)) != TC_OK) return st;
             q.p.csplit = false;
             ws = std::max(ws, ws_layout(q.n, q.p).bytes());
         }
@@ -2225,6 +2253,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     a.ldx = n.ldx;
     a.clean = reinterpret_cast<uint16_t *>(rx + o_x);
     a.ld_clean = ldp;
+    a.copies = (int)parts;
     if (launch_xent_prep(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
     ctx->launches += 1;
     std::string name;
@@ -2235,7 +2264,8 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             if ((st = pack_rows(ctx, s, Wv, n.ldw, rx + o_w, ldp, N, H)) != TC_OK) return st;
             Wv = rx + o_w;
         }
-        const Plan p = plan_xent(T, N, H, ctx->num_sms, f);
+        Plan p = plan_xent(T, N, H, ctx->num_sms, f);
+        p.seg_kb = f32 ? XENT_SEG_KB : 0;
         if (v0 == 0) name = p.name;
         const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, d->dtype, false, true, 1.0f, 0.0f, ldp, pack_w ? ldp : n.ldw, ldg);
         Norm gn{};
@@ -2257,23 +2287,22 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         job.epi.cp = a.cp;
         job.epi.cy = a.cy;
         job.epi.two = parts == 2;
-        job.left = rx + o_g[1];
-        if ((st = enqueue(ctx, &gd, gn, p, rx + o_x, Wv, rx + o_g[0], s, nullptr, nullptr, false, &job)) != TC_OK) return st;
-        for (int i = 0; i < parts; ++i) {
-            for (int k = 0; k < 2; ++k) {
-                if (k == 0 ? !dX : !dW) continue;
-                Product q;
-                if ((st = product(k == 0, v0, i, &q)) != TC_OK) return st;
-                if ((st = enqueue(ctx, &q.d, q.n, q.p, q.A, q.B, q.C, s, nullptr, unscale)) != TC_OK) return st;
-            }
+        job.left = rx + o_g + (size_t)(T * ldg * 2);
+        if ((st = enqueue(ctx, &gd, gn, p, rx + o_x, Wv, rx + o_g, s, nullptr, nullptr, false, &job)) != TC_OK) return st;
+        for (const bool rows : {true, false}) {
+            if (rows ? !dX : !dW) continue;
+            Product q;
+            if ((st = product(rows, v0, &q)) != TC_OK) return st;
+            if ((st = enqueue(ctx, &q.d, q.n, q.p, q.A, q.B, q.C, s, nullptr, unscale)) != TC_OK) return st;
         }
     }
     if (sum) {
-        const XentRoundArgs r{reinterpret_cast<const float *>(rx + o_sum), dX, T, H, n.lddx, d->grad_dtype};
+        const float *at = reinterpret_cast<const float *>(rx + o_sum);
+        const XentRoundArgs r{at, parts == 2 ? at + T * H : nullptr, dX, T, H, n.lddx, d->grad_dtype};
         if (launch_xent_round(r, s->st) != cudaSuccess) return TC_ERR_CUDA;
         ctx->launches += 1;
     }
-    ctx->last = "xent_grad_" + name + (pack_w ? "_packW" : "") + "_p" + std::to_string(cdiv(V, cols));
+    ctx->last = "xent_grad_" + name + (parts == 2 ? "_two" : "") + (pack_w ? "_packW" : "") + "_p" + std::to_string(cdiv(V, cols));
     return TC_OK;
 }
 

@@ -167,7 +167,7 @@ struct MmaArgs {
     const void *bias;
     int act;
     const float *col_scale;
-    int slice_kb;          // on-chip int8 accumulation: K blocks per exact slice
+    int slice_kb;          // K blocks per slice of an accumulator cut along K (int8, cross entropy, MmaLaunch::seg)
     // one-CTA tiles over fewer than BM rows of a K-major A: its copies carry
     // only the rows that exist (rounded up to 8) and a stage this many fewer
     // bytes; the tile's other rows hold stale data, which reaches only
@@ -186,6 +186,7 @@ struct MmaLaunch {
     // memory (BN 64 or 128, one CTA per unit: grid == args.total_units)
     int csplit;
     int grid;    // CTAs (a multiple of cg)
+    int seg;     // sums cut along K, args.slice_kb blocks each (not the one-CTA 192-wide tile)
     // softmax cross entropy in place of the plain epilogue (args.x; whole-K
     // tiles of 256 or 128 columns): XENT_LOSS writes no C, XENT_GRAD writes it
     // (16-bit, by TMA stores)
@@ -387,12 +388,13 @@ struct XentPrepArgs {
     long long ldx;
     uint16_t *clean;
     long long ld_clean;        // a multiple of 8; clean is 16-byte aligned
+    int copies;                // of the T rows, one below the other
 };
 cudaError_t launch_xent_prep(const XentPrepArgs &a, cudaStream_t st);
 
-// dst [rows, cols] (f16 or bf16, leading dimension ld) = the contiguous fp32 src, rounded
+// dst [rows, cols] (leading dimension ld) = the contiguous fp32 src (+ more, if not null), rounded to dtype
 struct XentRoundArgs {
-    const float *src;
+    const float *src, *more;
     void *dst;
     long long rows, cols, ld;
     int dtype;

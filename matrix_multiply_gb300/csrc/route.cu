@@ -100,27 +100,11 @@ struct Shape {
     static constexpr int WARPS = THREADS / 32;
 };
 
-// The sums over all blocks' rows of `part` (E + 1 numbers each, the last one that
-// of lse^2, and E + 1 counts, the last one that of the tokens), in the order of
-// the blocks; then the counts and the losses.  A whole block; `sums` and `ns`
-// hold E + 1 numbers each.
-__device__ __forceinline__ void finish(const RouteArgs &a, const float *part, const int *counts, int blocks, double *sums,
-                                       int *ns)
+// The counts and the losses from the sums over all tokens (E + 1 numbers each:
+// the last of `sums` is that of lse^2, of `ns` the tokens); a whole block.
+__device__ __forceinline__ void finish(const RouteArgs &a, const double *sums, const int *ns)
 {
-    const int n1 = a.E + 1;
-    for (int i = threadIdx.x; i < n1; i += blockDim.x) {
-        double s = 0.0;
-        int n = 0;
-#pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-            s += (double)part[(long long)b * n1 + i];
-            n += counts[(long long)b * n1 + i];
-        }
-        sums[i] = s;
-        ns[i] = n;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n1; i += blockDim.x) a.counts[i] = ns[i];
+    for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.counts[i] = ns[i];
     if (threadIdx.x < 32) {
         const double n = ns[a.E] > 0 ? ns[a.E] : 1;
         double b = 0.0;
@@ -134,13 +118,41 @@ __device__ __forceinline__ void finish(const RouteArgs &a, const float *part, co
     }
 }
 
+// Adds the blocks' rows up, in a fixed order: 16 groups of 64 threads take every
+// 16th row, up to 9 columns a thread, with 8 rows' loads in flight; the groups'
+// sums meet in shared memory, in 64 bits.  (One thread a column: 36 us for 152
+// rows of 257.)
+constexpr int JOIN_GROUPS = 16;
 __global__ void __launch_bounds__(1024) finish_kernel(const RouteArgs a, int blocks)
 {
+    __shared__ float gs[JOIN_GROUPS][TC_MOE_MAX_EXPERTS + 1];
     __shared__ double sums[TC_MOE_MAX_EXPERTS + 1];
     __shared__ int ns[TC_MOE_MAX_EXPERTS + 1];
+    for (int i = threadIdx.x; i <= a.E; i += 1024) ns[i] = 0;
+    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
-    finish(a, a.part, a.part_n, blocks, sums, ns);
+    const int n1 = a.E + 1, g = threadIdx.x >> 6;
+    for (int e = threadIdx.x & 63; e < n1; e += 64) {
+        float s = 0.0f;
+        int n = 0;
+#pragma unroll 8
+        for (int b = g; b < blocks; b += JOIN_GROUPS) {
+            s += __ldcg(a.part + (long long)b * n1 + e);
+            n += __ldcg(a.part_n + (long long)b * n1 + e);
+        }
+        gs[g][e] = s;
+        atomicAdd(&ns[e], n);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < n1; e += 1024) {
+        double s = 0.0;
+#pragma unroll
+        for (int i = 0; i < JOIN_GROUPS; ++i) s += (double)gs[i][e];
+        sums[e] = s;
+    }
+    __syncthreads();
+    finish(a, sums, ns);
 }
 
 template <int DT, int C>
@@ -151,8 +163,6 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
     __shared__ float zs[W];
     __shared__ int tokens[W];
     __shared__ int chosen[TC_MOE_MAX_EXPERTS + 1];
-    __shared__ int slot_id[W][TC_MOE_MAX_TOPK];
-    __shared__ float slot_e[W][TC_MOE_MAX_TOPK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i <= a.E; i += Shape<C>::THREADS) chosen[i] = 0;
     __syncthreads();
@@ -169,26 +179,29 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
         float v[C];
         load_row<DT, C>(static_cast<const char *>(a.logits) + t * a.ld * es, a.E, lane, vec, v);
         const bool valid = a.valid == nullptr || a.valid[t] != 0;
-        // the lane's two largest, the earlier of equal ones first
-        int k1 = INT_MIN, k2 = INT_MIN, i1 = 0, i2 = 0;
+        // the lane's two largest that are left, the earlier of equal ones first
+        // (branch-free: written with branches the kernel executes 2.5 times the
+        // instructions)
+        int k1, k2, i1, i2;
         unsigned used = 0;
-        auto two = [&]() {
+        auto two = [&](auto all) {
             k1 = k2 = INT_MIN;
+            i1 = i2 = 0;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                const int e = lane * C + i;
-                const int k = (e < a.E && !(used >> i & 1u)) ? key_of(v[i]) : INT_MIN;
-                if (k > k1) {
-                    k2 = k1, i2 = i1;
-                    k1 = k, i1 = i;
-                } else if (k > k2) {
-                    k2 = k, i2 = i;
-                }
+                int k = key_of(v[i]);
+                if (!decltype(all)::value) k = used >> i & 1u ? INT_MIN : k;
+                const bool a1 = k > k1, a2 = k > k2;
+                i2 = a1 ? i1 : a2 ? i : i2;
+                k2 = max(k2, min(k1, k));
+                i1 = a1 ? i : i1;
+                k1 = max(k1, k);
             }
         };
-        two();
+        two(std::true_type{});
         int top = __reduce_max_sync(FULL, k1);
-        int got = 0;
+        int got = 0, id = -1;
+        float w = 0.0f;
         if (valid && top > KEY_NEG_INF) {
             const float big = of_key(top);
             float s = 0.0f;
@@ -205,43 +218,38 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
             const float lse = big + logf(s);
             z = fmaf(lse, lse, z);
             ++n;
-            // one after the other the largest that is left; a lane whose two are
-            // taken looks for the next two (8 of 256: in one round of eight)
-            bool second = true;
+            // One after the other the largest that is left, the j-th for lane j;
+            // a lane whose two are taken looks for its next two (8 of 256: 1.2
+            // times a token)
+            int key = INT_MIN, have = 2;
             for (; got < a.k && top > KEY_NEG_INF; ++got) {
                 const int src = __ffs(__ballot_sync(FULL, k1 == top)) - 1;
-                bool look = false;
-                if (lane == src) {
-                    const int id = lane * C + i1;
-                    slot_id[warp][got] = id;
-                    slot_e[warp][got] = exp2_approx((of_key(top) - big) * LOG2E) * inv;
-                    atomicAdd(&chosen[id], 1);
-                    used |= 1u << i1;
-                    k1 = k2, i1 = i2, k2 = INT_MIN;
-                    look = C > 2 && !second;
-                    second = false;
-                }
-                if (C > 2 && __any_sync(FULL, look)) {
-                    if (look) {
-                        two();
-                        second = true;
+                const int at = __shfl_sync(FULL, lane * C + i1, src);
+                if (lane == got) id = at, key = top;
+                const bool mine = lane == src;
+                if (C > 2) used |= mine ? 1u << i1 : 0u;
+                k1 = mine ? k2 : k1;
+                i1 = mine ? i2 : i1;
+                k2 = mine ? INT_MIN : k2;
+                if (C > 2) {
+                    have -= mine ? 1 : 0;
+                    if (__any_sync(FULL, have == 0) && have == 0) {
+                        two(std::false_type{});
+                        have = 2;
                     }
                 }
                 top = __reduce_max_sync(FULL, k1);
             }
-        }
-        __syncwarp();
-        const bool mine = lane < got;
-        float w = mine ? slot_e[warp][lane & (TC_MOE_MAX_TOPK - 1)] : 0.0f;
-        if (a.renorm) {
-            const float total = warp_sum(w);
-            if (mine) w /= total;
+            if (id >= 0) {
+                w = exp2_approx((of_key(key) - big) * LOG2E) * inv;
+                atomicAdd(&chosen[id], 1);
+            }
+            if (a.renorm) w /= warp_sum(w);
         }
         if (lane < a.k) {
-            a.ids[t * a.k + lane] = mine ? slot_id[warp][lane & (TC_MOE_MAX_TOPK - 1)] : -1;
+            a.ids[t * a.k + lane] = id;
             a.weights[t * a.k + lane] = w;
         }
-        __syncwarp();
     }
     // the block's sums, over its warps in their order
 #pragma unroll
@@ -249,8 +257,7 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
         if (lane * C + i < a.E) rows[warp * a.E + lane * C + i] = mean[i];
     if (lane == 0) zs[warp] = z, tokens[warp] = n;
     __syncthreads();
-    float *part = a.part + (long long)blockIdx.x * (a.E + 1);
-    int *part_n = a.part_n + (long long)blockIdx.x * (a.E + 1);
+    __shared__ double sums[TC_MOE_MAX_EXPERTS + 1];
     for (int e = threadIdx.x; e <= a.E; e += Shape<C>::THREADS) {
         float s = 0.0f;
         int c = e < a.E ? chosen[e] : 0;
@@ -259,14 +266,18 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
             s += e < a.E ? rows[w * a.E + e] : zs[w];
             if (e == a.E) c += tokens[w];
         }
-        part[e] = s;
-        part_n[e] = c;
+        if (gridDim.x > 1) {
+            a.part[(long long)blockIdx.x * (a.E + 1) + e] = s;
+            a.part_n[(long long)blockIdx.x * (a.E + 1) + e] = c;
+        } else {
+            sums[e] = (double)s;
+            chosen[e] = c;
+        }
     }
     if (gridDim.x > 1) return;
-    // the only block: what it wrote is all there is
-    __shared__ double sums[TC_MOE_MAX_EXPERTS + 1];
+    // the only block: these are all
     __syncthreads();
-    finish(a, part, part_n, 1, sums, chosen);
+    finish(a, sums, chosen);
 }
 
 template <int DT, int C>

@@ -642,7 +642,15 @@ __device__ __forceinline__ void xent_statistics(const MmaArgs &a, long long col0
 // exponential and two or three more operations, 1.5 us for the 128 x 256
 // outputs of an SM, which the next tile's MMAs hide from a hidden size of
 // about 512 on.
-template <int BN, int CG, bool GROUPED, bool EPI, bool I8ACC = false, bool CSPLIT = false, int XENT = XENT_NONE>
+//
+// SEG (and XENT): the accumulator is cut along K.  The tensor core truncates
+// what it adds, so a sum of K products comes out up to (K / 16) 2^-24 of its
+// size too small (K = 4096: the mean of a loss 3.2e-6 off); here it sums
+// args.slice_kb blocks at a time, from zero, and the epilogue's threads add
+// those sums in registers, rounding to nearest, while the next ones are made in
+// the other TMEM buffer.
+template <int BN, int CG, bool GROUPED, bool EPI, bool I8ACC = false, bool CSPLIT = false, int XENT = XENT_NONE,
+          bool SEG = XENT != XENT_NONE>
 __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmW,
@@ -664,7 +672,8 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     constexpr uint32_t RUN_COL = 2 * BN;           // I8ACC: the running int32 sums
     static_assert(!I8ACC || (EPI && !GROUPED && 3 * BN <= 512), "on-chip slices: two accumulators and the sums");
     static_assert(!CSPLIT || (CG == 1 && !GROUPED && !I8ACC), "cluster split-K: one CTA per slice");
-    static_assert(XENT == XENT_NONE || (EPI && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
+    static_assert(!SEG || (EW == 8 && !GROUPED && !I8ACC), "segments: at most 128 sums in a thread's registers");
+    static_assert(XENT == XENT_NONE || (EPI && SEG && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
     static_assert(!CSPLIT || BM * csplit_ld<BN>() * 4 <= S * STAGE, "the partial tile fits in the idle ring");
     constexpr int CHUNKS = BN / 32;
     static_assert(CG == 1 || CG == 2, "one CTA or a CTA pair");
@@ -875,8 +884,9 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                 const uint64_t astep = a_kmajor ? 2u : 128u, bstep = b_kmajor ? 2u : B_SW64 ? 64u : 128u;
                 // Segments of the unit, each accumulated in its own TMEM buffer
                 // from zero: the whole K range, or (I8ACC) K slices of
-                // args.slice_kb blocks that the epilogue adds up on chip.
-                const int seg_kb = I8ACC ? args.slice_kb : w.nkb;
+                // args.slice_kb blocks that the epilogue adds up on chip (SEG
+                // likewise).
+                const int seg_kb = I8ACC || SEG ? args.slice_kb : w.nkb;
                 for (int k0 = 0; ok && k0 < w.nkb; k0 += seg_kb, ++local) {
                     const int k1 = min(k0 + seg_kb, w.nkb);
                     const uint32_t acc = local & 1u, aph = (local >> 1) & 1u;
@@ -1034,8 +1044,9 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             for (int i = 0; i < NCH; ++i)
                 bpre[i] = EPI && XENT == XENT_NONE ? bias_of(ea, lane, (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32) : 0.0f;
             // segments of the unit (see the MMA warp): one, or the K slices
-            // that I8ACC adds up in TMEM
-            const int nseg = I8ACC ? (w.kb1 - w.kb0 + args.slice_kb - 1) / args.slice_kb : 1;
+            // that I8ACC adds up in TMEM, SEG in registers
+            const int nseg = I8ACC || SEG ? (w.kb1 - w.kb0 + args.slice_kb - 1) / args.slice_kb : 1;
+            float sums[SEG ? NCH * 32 : 1];        // of the segments before the last
             bool ok = true;
             for (int sg = 0; sg < nseg; ++sg, ++local) {
                 const uint32_t acc = local & 1u, aph = (local >> 1) & 1u;
@@ -1061,6 +1072,45 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     }
                 };
 
+                if constexpr (SEG) {
+                    // 16 columns at a time: with 128 sums a thread has no
+                    // registers for more
+                    if (nseg > 1 || XENT == XENT_LOSS) {
+                        const bool first = sg == 0, last = sg + 1 == nseg;
+#pragma unroll
+                        for (int i = 0; i < 2 * NCH; ++i) {
+                            const uint32_t at = taddr + (chunk0 + (i >> 1) * CSTEP) * 32 + (i & 1) * 16;
+                            uint32_t r[16];
+                            __syncwarp();
+                            tmem_ld_32x32b_x16(at, r);
+                            tmem_ld_wait();
+                            if (last && XENT != XENT_LOSS) {
+                                // back to where the plain epilogue finds them
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(sums[16 * i + j] + __uint_as_float(r[j]));
+                                tmem_st_32x32b_x16(at, r);
+                            } else {
+                                if (i == 2 * NCH - 1) release();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    sums[16 * i + j] = first ? __uint_as_float(r[j]) : sums[16 * i + j] + __uint_as_float(r[j]);
+                            }
+                        }
+                        if (!last) continue;
+                        if (XENT != XENT_LOSS) tmem_st_wait();
+                    }
+                }
+                // the i-th of this warp's chunks of the accumulator, which goes
+                // back to the MMA warp with the last
+                auto fetch = [&](int i, float (&v)[32]) {
+                    uint32_t r[32];
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(taddr + (chunk0 + i * CSTEP) * 32, r);
+                    tmem_ld_wait();
+                    if (i == NCH - 1) release();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                };
                 if constexpr (I8ACC) {
                     // This segment's fp32 accumulator holds exact integers (a
                     // K slice of at most 1024 int8 products); they are added as
@@ -1092,64 +1142,59 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         }
                     }
                     if (!last) tmem_st_wait();
-                } else if constexpr (XENT != XENT_NONE) {
+                } else if constexpr (XENT == XENT_LOSS) {
+                    // from the registers: the accumulator is free already
                     float m = -INFINITY, s = 0.0f;
-#pragma unroll 1
-                    for (int c = chunk0; c < CHUNKS; c += CSTEP) {
-                        uint32_t r[32];
-                        __syncwarp();
-                        tmem_ld_32x32b_x32(taddr + c * 32, r);
-                        tmem_ld_wait();
-                        if (c == LAST_C0 + chunk0) release();
-                        const long long col0 = (long long)w.tn * BN + c * 32;
-                        if (col0 >= args.N) continue;         // (the whole warp; release() came with the last chunk)
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i) {
+                        const long long col0 = (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32;
+                        if (col0 >= args.N) continue;         // (the whole warp)
                         float v[32];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                        for (int j = 0; j < 32; ++j) v[j] = sums[32 * i + j];
                         // the target's column of this chunk, in few warps' chunks
                         const int hit = target - (int)col0;
+                        const bool here = hit >= 0 && hit < 32 && col0 + hit < args.N;
+                        if (__any_sync(0xffffffffu, here) && here) args.x.at[row] = pick(v, hit) * args.alpha;
+                        xent_statistics(args, col0, v, m, s);
+                    }
+                    if (row < args.M) args.x.part[(2LL * w.tn + chunk0) * args.M + row] = make_float2(m, s);
+                } else if constexpr (XENT == XENT_GRAD) {
+#pragma unroll 1
+                    for (int i = 0; i < NCH; ++i) {
+                        float v[32];
+                        fetch(i, v);
+                        const long long col0 = (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32;
+                        if (col0 >= args.N) continue;
+                        const int hit = target - (int)col0;
                         const bool any = __any_sync(0xffffffffu, hit >= 0 && hit < 32);
-                        if constexpr (XENT == XENT_LOSS) {
-                            if (any && hit >= 0 && hit < 32 && col0 + hit < args.N) args.x.at[row] = pick(v, hit) * args.alpha;
-                            xent_statistics(args, col0, v, m, s);
-                        } else {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = cp * exp2_approx(fmaf(v[j], args.x.k2, -rowlse));
-                            if (any) {
+                        for (int j = 0; j < 32; ++j) v[j] = cp * exp2_approx(fmaf(v[j], args.x.k2, -rowlse));
+                        if (any) {
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] -= j == hit ? cy : 0.0f;
-                            }
-                            if (cp == 0.0f && cy == 0.0f) {      // not counted: 0 whatever its logits are
+                            for (int j = 0; j < 32; ++j) v[j] -= j == hit ? cy : 0.0f;
+                        }
+                        if (cp == 0.0f && cy == 0.0f) {      // not counted: 0 whatever its logits are
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                            }
-                            const long long row0 = row - lane;
-                            if (row0 < args.M) {
-                                store_tma<EBUFS>(&tmC, false, args.c_dtype, staging(STG_TMA), lane, 0, row0, col0, v);
-                                if (args.x.two) {
-                                    // what the rounding left, rounded in turn
+                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                        }
+                        const long long row0 = row - lane;
+                        if (row0 < args.M) {
+                            store_tma<EBUFS>(&tmC, false, args.c_dtype, staging(STG_TMA), lane, 0, row0, col0, v);
+                            if (args.x.two) {
+                                // what the rounding left, rounded in turn
 #pragma unroll
-                                    for (int j = 0; j < 32; ++j) v[j] -= round16(v[j], args.c_dtype);
-                                    store_tma<EBUFS>(&tmW, false, args.c_dtype, staging(STG_TMA), lane, 0, row0, col0, v);
-                                }
+                                for (int j = 0; j < 32; ++j) v[j] -= round16(v[j], args.c_dtype);
+                                store_tma<EBUFS>(&tmW, false, args.c_dtype, staging(STG_TMA), lane, 0, row0, col0, v);
                             }
                         }
                     }
-                    if constexpr (XENT == XENT_LOSS) {
-                        if (row < args.M) args.x.part[(2LL * w.tn + chunk0) * args.M + row] = make_float2(m, s);
-                    }
                 } else if (w.S == 1) {
 #pragma unroll 1
-                    for (int c = chunk0; c < CHUNKS; c += CSTEP) {
-                        uint32_t r[32];
-                        __syncwarp();
-                        tmem_ld_32x32b_x32(taddr + c * 32, r);
-                        tmem_ld_wait();
-                        if (c == LAST_C0 + chunk0) release();
+                    for (int i = 0; i < NCH; ++i) {
                         float v[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                        emit(w.b, row, (long long)w.tn * BN + c * 32, v, pick(bpre, (c - chunk0) / CSTEP));
+                        fetch(i, v);
+                        emit(w.b, row, (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32, v, pick(bpre, i));
                     }
                 } else if constexpr (CSPLIT) {
                     // K slice of a cluster split: the partial tile goes to this
@@ -1158,17 +1203,12 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     // accumulator's commit).  csplit_reduce adds the slices.
                     float *red = reinterpret_cast<float *>(smem) + (quarter * 32 + lane) * csplit_ld<BN>();
 #pragma unroll 1
-                    for (int c = chunk0; c < CHUNKS; c += CSTEP) {
-                        uint32_t r[32];
-                        __syncwarp();
-                        tmem_ld_32x32b_x32(taddr + c * 32, r);
-                        tmem_ld_wait();
-                        if (c == LAST_C0 + chunk0) release();
-                        float4 *dst = reinterpret_cast<float4 *>(red + c * 32);
+                    for (int i = 0; i < NCH; ++i) {
+                        float v[32];
+                        fetch(i, v);
+                        float4 *dst = reinterpret_cast<float4 *>(red + (chunk0 + i * CSTEP) * 32);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            dst[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                                 __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+                        for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                     }
                 } else {
                     // K slice: the raw fp32 partial tile goes to its workspace
@@ -1177,16 +1217,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     const long long wrow0 =
                         (long long)(w.ufirst + w.s - args.split_base) * (BM * CG) + (int)rank * BM + quarter * 32;
 #pragma unroll 1
-                    for (int c = chunk0; c < CHUNKS; c += CSTEP) {
-                        uint32_t r[32];
-                        __syncwarp();
-                        tmem_ld_32x32b_x32(taddr + c * 32, r);
-                        tmem_ld_wait();
-                        if (c == LAST_C0 + chunk0) release();
+                    for (int i = 0; i < NCH; ++i) {
                         float v[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                        store_tma<EBUFS>(&tmW, false, TC_F32, staging(STG_TMA), lane, 0, wrow0, c * 32, v);
+                        fetch(i, v);
+                        store_tma<EBUFS>(&tmW, false, TC_F32, staging(STG_TMA), lane, 0, wrow0, (chunk0 + i * CSTEP) * 32, v);
                     }
                 }
             }
@@ -1218,10 +1252,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
 }
 
 template <int BN, int CG, bool GROUPED = false, bool EPI = false, bool I8ACC = false, bool CSPLIT = false,
-          int XENT = XENT_NONE>
+          int XENT = XENT_NONE, bool SEG = XENT != XENT_NONE>
 cudaError_t launch_kernel(const MmaLaunch &L, cudaStream_t st, const TableOf<GROUPED> &gt = TableOf<GROUPED>{})
 {
-    constexpr auto kern = mma_kernel<BN, CG, GROUPED, EPI, I8ACC, CSPLIT, XENT>;
+    constexpr auto kern = mma_kernel<BN, CG, GROUPED, EPI, I8ACC, CSPLIT, XENT, SEG>;
     constexpr int smem = mma_smem_bytes(BN, CG, EPI || GROUPED);
     constexpr int threads = mma_threads(BN, CG, EPI || GROUPED);
     // per device: the kernel's shared-memory limit is raised once (callers
@@ -1454,8 +1488,29 @@ cudaError_t launch_xent(const MmaLaunch &L, cudaStream_t st)
     return cudaErrorInvalidValue;
 }
 
+// Sums cut along K (args.slice_kb blocks), with the plain epilogue.
+template <int BN, int CG, bool CSPLIT = false>
+cudaError_t launch_seg(const MmaLaunch &L, cudaStream_t st)
+{
+    return launch_kernel<BN, CG, false, true, false, CSPLIT, XENT_NONE, true>(L, st);
+}
+
 cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
 {
+    if ((L.xent || L.seg) && L.args.slice_kb < 1) return cudaErrorInvalidValue;
+    if (L.seg) {
+        if (L.csplit) return L.cg == 1 && L.bn == 128 ? launch_seg<128, 1, true>(L, st)
+                             : L.cg == 1 && L.bn == 64 ? launch_seg<64, 1, true>(L, st)
+                                                       : cudaErrorInvalidValue;
+        if (L.cg == 2) return L.bn == 256   ? launch_seg<256, 2>(L, st)
+                              : L.bn == 192 ? launch_seg<192, 2>(L, st)
+                              : L.bn == 128 ? launch_seg<128, 2>(L, st)
+                                            : cudaErrorInvalidValue;
+        return L.bn == 256   ? launch_seg<256, 1>(L, st)
+               : L.bn == 128 ? launch_seg<128, 1>(L, st)
+               : L.bn == 64  ? launch_seg<64, 1>(L, st)
+                             : cudaErrorInvalidValue;
+    }
     if (L.xent == XENT_LOSS) return launch_xent<XENT_LOSS>(L, st);
     if (L.xent == XENT_GRAD) return L.args.c_tma ? launch_xent<XENT_GRAD>(L, st) : cudaErrorInvalidValue;
     const bool epi = L.args.bias != nullptr || L.args.act != TC_ACT_NONE || L.args.col_scale != nullptr;

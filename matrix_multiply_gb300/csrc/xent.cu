@@ -5,8 +5,8 @@
 //              its largest exponent and its sum of exponentials, and the
 //              target's logit; `join` makes lse and the losses of them.
 //   gradients  G = the gradient of l, piece by piece of the vocabulary,
-//              rounded to X's type; dX += G W_piece and dW_piece = G^T X are
-//              plain products.  `prep` runs first, `round` last where dX was
+//              rounded to X's type (in two parts where that is not enough);
+//              dX += G W_piece and dW_piece = G^T X are plain products.  `prep` runs first, `round` last where dX was
 //              summed over pieces in fp32.
 //
 // All of it is some microseconds beside products of 2 T H V operations each.
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const XentPrepArgs a
                     w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
                 }
             }
-            *reinterpret_cast<uint4 *>(a.clean + row * a.ld_clean + col) = w;
+            for (int k = 0; k < a.copies; ++k) *reinterpret_cast<uint4 *>(a.clean + (k * (long long)a.T + row) * a.ld_clean + col) = w;
         }
         return;
     }
@@ -221,14 +221,30 @@ __global__ void __launch_bounds__(256) round_kernel(const XentRoundArgs a)
     const long long per = (a.cols + 7) / 8, all = per * a.rows;
     const bool whole = a.cols % 8 == 0 && a.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dst) & 15u) == 0;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
-        const long long row = i / per, col = (i - row * per) * 8;
-        const float *src = a.src + row * a.cols + col;
+        const long long row = i / per, col = (i - row * per) * 8, at = row * a.cols + col;
+        float v[8];
         if (whole) {
-            const float4 x = *reinterpret_cast<const float4 *>(src), y = *reinterpret_cast<const float4 *>(src + 4);
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst) + row * a.ld + col) =
-                make_uint4(pack2(x.x, x.y, a.dtype), pack2(x.z, x.w, a.dtype), pack2(y.x, y.y, a.dtype), pack2(y.z, y.w, a.dtype));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float4 x = *reinterpret_cast<const float4 *>(a.src + at + 4 * q);
+                if (a.more) {
+                    const float4 y = *reinterpret_cast<const float4 *>(a.more + at + 4 * q);
+                    x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+                }
+                v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
+            }
+            if (a.dtype == TC_F32) {
+                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.dst) + row * a.ld + col);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dst) + row * a.ld + col) =
+                    make_uint4(pack2(v[0], v[1], a.dtype), pack2(v[2], v[3], a.dtype), pack2(v[4], v[5], a.dtype),
+                               pack2(v[6], v[7], a.dtype));
+            }
         } else {
-            for (int j = 0; j < 8 && col + j < a.cols; ++j) store_c1(a.dst, row * a.ld + col + j, src[j], a.dtype);
+            for (int j = 0; j < 8 && col + j < a.cols; ++j)
+                store_c1(a.dst, row * a.ld + col + j, a.src[at + j] + (a.more ? a.more[at + j] : 0.0f), a.dtype);
         }
     }
 }

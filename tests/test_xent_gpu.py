@@ -212,3 +212,24 @@ def test_every_tile_shape(ctx, monkeypatch, bn, cg):
     gx, gw = backward(ctx, c, lse32)
     within(gx, dX, ex)
     within(gw, dW, ew)
+
+
+def off(out, want):
+    return float((out.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("H", [512, 2000, 4096])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_fp32_results_are_fp32(ctx, H, dtype):
+    """Long sums do not lose what the tensor core truncates: a segment of 512
+    products loses at most (512 / 16) 2^-24 = 1.9e-6 of their sizes' sum, half of
+    it on average, and an exponential of a few tenths less errs by a few 1e-7."""
+    c = Case(200, H, 6000, dtype, grad="f32", seed=16)
+    loss, _, lse, _ = c.forward()
+    got = forward(ctx, c)
+    assert off(got[1], lse) < 1e-6 and off(got[0], loss) < 2e-6
+    dX, _, dW, _ = c.backward(c.lse32())
+    gx, gw = backward(ctx, c, c.lse32())
+    # G in two parts: half a step of bf16, squared, is 2^-16 at most, a third of it on average
+    limit = 1e-5 if dtype == "bf16" else 4e-6
+    assert off(gx, dX) < limit and off(gw, dW) < limit
