@@ -285,6 +285,13 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr)
     return v;
 }
 
+__device__ __forceinline__ double ld_shared_cluster_f64(uint32_t cluster_addr)
+{
+    double v;
+    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // arrive on an mbarrier given by its shared::cluster address (any CTA of the cluster)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
 {

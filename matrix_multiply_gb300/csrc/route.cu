@@ -100,59 +100,178 @@ struct Shape {
     static constexpr int WARPS = THREADS / 32;
 };
 
-// The counts and the losses from the sums over all tokens (E + 1 numbers each:
-// the last of `sums` is that of lse^2, of `ns` the tokens); a whole block.
-__device__ __forceinline__ void finish(const RouteArgs &a, const double *sums, const int *ns)
+// The choice of one token from its keys x (lane g's are those of experts g C ..),
+// one after the other the largest that is left, the j-th for lane j.  A lane
+// keeps its two largest at hand, the earlier of equal ones first, and looks for
+// its next two when both are taken.  (Branch-free: with branches the kernel
+// executes 2.5 times the instructions.)
+template <int C>
+__device__ __forceinline__ void choose(int k, int lane, const int (&x)[C], int top, int &got, int &id, int &key)
 {
-    for (int i = threadIdx.x; i <= a.E; i += blockDim.x) a.counts[i] = ns[i];
-    if (threadIdx.x < 32) {
-        const double n = ns[a.E] > 0 ? ns[a.E] : 1;
-        double b = 0.0;
-        for (int e = threadIdx.x; e < a.E; e += 32) b += (double)ns[e] * sums[e];
+    int k1, k2, i1, i2;
+    unsigned used = 0;
+    auto two = [&]() {
+        k1 = k2 = INT_MIN;
+        i1 = i2 = 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) b += __shfl_xor_sync(FULL, b, o);
-        if (threadIdx.x == 0) {
-            a.losses[0] = (float)(b * a.E / (n * n * a.k));
-            a.losses[1] = (float)(sums[a.E] / n);
+        for (int i = 0; i < C; ++i) {
+            const int y = used >> i & 1u ? INT_MIN : x[i];
+            const bool first = y > k1, second = y > k2;
+            i2 = first ? i1 : second ? i : i2;
+            k2 = max(k2, min(k1, y));
+            i1 = first ? i : i1;
+            k1 = max(k1, y);
         }
+    };
+    two();
+    int have = 2;
+    for (; got < k && top > KEY_NEG_INF; ++got) {
+        const int src = __ffs(__ballot_sync(FULL, k1 == top)) - 1;
+        const int at = __shfl_sync(FULL, lane * C + i1, src);
+        if (lane == got) id = at, key = top;
+        const bool mine = lane == src;
+        if (C > 2) used |= mine ? 1u << i1 : 0u;
+        k1 = mine ? k2 : k1;
+        i1 = mine ? i2 : i1;
+        k2 = mine ? INT_MIN : k2;
+        if (C > 2) {
+            have -= mine ? 1 : 0;
+            if (__any_sync(FULL, have == 0) && have == 0) {
+                two();
+                have = 2;
+            }
+        }
+        top = __reduce_max_sync(FULL, k1);
     }
 }
 
-// Adds the blocks' rows up, in a fixed order: 16 groups of 64 threads take every
-// 16th row, up to 9 columns a thread, with 8 rows' loads in flight; the groups'
-// sums meet in shared memory, in 64 bits.  (One thread a column: 36 us for 152
-// rows of 257.)
-constexpr int JOIN_GROUPS = 16;
+// The same where few values compete: the k-th largest of the lanes' maxima k1
+// bounds the k-th largest value from below, and what reaches it, 10 of 256 for
+// k = 8, goes to one lane each in the order of the indices (which is theirs) and
+// finds its rank by comparing with the others.  False, with nothing done, where
+// more than 32 reach it.  (65536 x 256, k = 8: all of the kernel 52 us with the
+// rounds above, 44 with these.)
+template <int C>
+__device__ __forceinline__ bool choose_few(int k, int lane, const int (&x)[C], int k1, int top, int2 *found, int &got,
+                                           int &id, int &key, int &slot)
+{
+    int bound = top, left = k1;
+#pragma unroll 4
+    for (int j = 1; j < k; ++j) {
+        left = left == bound ? INT_MIN : left;      // (equal ones at once: the bound is the lower)
+        bound = __reduce_max_sync(FULL, left);
+    }
+    bound = max(bound, KEY_NEG_INF + 1);
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) mine += x[i] >= bound ? 1 : 0;
+    int after = mine;                               // with those of the lanes before
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(FULL, after, o);
+        after += lane >= o ? y : 0;
+    }
+    const int all = __shfl_sync(FULL, after, 31);
+    if (all > 32) return false;
+    int2 *at = found + (after - mine);
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        if (x[i] >= bound) *at++ = make_int2(x[i], lane * C + i);
+    __syncwarp();
+    const int2 f = lane < all ? found[lane] : make_int2(INT_MIN, -1);
+    __syncwarp();
+    int rank = __popc(__match_any_sync(FULL, f.x) & ((1u << lane) - 1u));
+    for (int r = 0; r < all; r += 4) {              // (lanes from `all` on are below every key)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) rank += __shfl_sync(FULL, f.x, (r + q) & 31) > f.x ? 1 : 0;
+    }
+    got = min(all, k);
+    id = f.y;
+    key = f.x;
+    slot = rank;
+    return true;
+}
+
+// The losses from b = sum_e c[e] (sum of p over the tokens) and z, of n tokens.
+__device__ __forceinline__ void write_losses(const RouteArgs &a, double b, double z, int tokens)
+{
+    const double n = tokens > 0 ? tokens : 1;
+    a.losses[0] = (float)(b * a.E / (n * n * a.k));
+    a.losses[1] = (float)(z / n);
+}
+
+__device__ __forceinline__ double warp_sum(double v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+
+// Adds the blocks' rows up, in a fixed order.  A cluster of 8 blocks shares the
+// columns (and every block takes the last one, of lse^2 and the tokens); a
+// block's 32 warps take every 32nd row, so that 5 loads a thread, all in flight,
+// read the rows of 152 blocks once; the warps' sums meet in shared memory in 64
+// bits, the blocks' shares of the balance loss in the first one's.  (One block
+// for everything takes 19 us for 257 columns, one thread a column 36.)
+constexpr int FINISH_BLOCKS = 8;
+constexpr int FINISH_COLUMNS = TC_MOE_MAX_EXPERTS / FINISH_BLOCKS + 1;
 __global__ void __launch_bounds__(1024) finish_kernel(const RouteArgs a, int blocks)
 {
-    __shared__ float gs[JOIN_GROUPS][TC_MOE_MAX_EXPERTS + 1];
-    __shared__ double sums[TC_MOE_MAX_EXPERTS + 1];
-    __shared__ int ns[TC_MOE_MAX_EXPERTS + 1];
-    for (int i = threadIdx.x; i <= a.E; i += 1024) ns[i] = 0;
-    __syncthreads();
+    __shared__ float ps[32][FINISH_COLUMNS];
+    __shared__ int pn[32][FINISH_COLUMNS];
+    __shared__ double sums[FINISH_COLUMNS];
+    __shared__ int ns[FINISH_COLUMNS];
+    __shared__ double share;
     griddep_wait();
     griddep_launch_dependents();
-    const int n1 = a.E + 1, g = threadIdx.x >> 6;
-    for (int e = threadIdx.x & 63; e < n1; e += 64) {
+    const int n1 = a.E + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = (a.E + FINISH_BLOCKS - 1) / FINISH_BLOCKS, first = min((int)blockIdx.x * per, a.E);
+    const int own = min(per, a.E - first);
+    for (int c = lane; c <= own; c += 32) {
+        const int e = c < own ? first + c : a.E;
         float s = 0.0f;
         int n = 0;
-#pragma unroll 8
-        for (int b = g; b < blocks; b += JOIN_GROUPS) {
+#pragma unroll 5
+        for (int b = warp; b < blocks; b += 32) {
             s += __ldcg(a.part + (long long)b * n1 + e);
             n += __ldcg(a.part_n + (long long)b * n1 + e);
         }
-        gs[g][e] = s;
-        atomicAdd(&ns[e], n);
+        ps[warp][c] = s;
+        pn[warp][c] = n;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < n1; e += 1024) {
+    for (int c = threadIdx.x; c <= own; c += 1024) {
         double s = 0.0;
-#pragma unroll
-        for (int i = 0; i < JOIN_GROUPS; ++i) s += (double)gs[i][e];
-        sums[e] = s;
+        int n = 0;
+#pragma unroll 8
+        for (int w = 0; w < 32; ++w) {
+            s += (double)ps[w][c];
+            n += pn[w][c];
+        }
+        sums[c] = s;
+        ns[c] = n;
+        if (c < own)
+            a.counts[first + c] = n;
+        else if (blockIdx.x == 0)
+            a.counts[a.E] = n;
     }
     __syncthreads();
-    finish(a, sums, ns);
+    if (warp == 0) {
+        double b = 0.0;
+        for (int c = lane; c < own; c += 32) b += (double)ns[c] * sums[c];
+        b = warp_sum(b);
+        if (lane == 0) share = b;
+    }
+    __syncwarp();
+    cluster_sync();
+    if (blockIdx.x == 0 && warp == 0) {
+        double b = 0.0;
+        if (lane < FINISH_BLOCKS) b = ld_shared_cluster_f64(mapa_shared(smem_u32(&share), (uint32_t)lane));
+        b = warp_sum(b);
+        if (lane == 0) write_losses(a, b, sums[own], ns[own]);
+    }
+    __syncwarp();
+    cluster_sync();                 // no block leaves while the first may read its share
 }
 
 template <int DT, int C>
@@ -163,6 +282,7 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
     __shared__ float zs[W];
     __shared__ int tokens[W];
     __shared__ int chosen[TC_MOE_MAX_EXPERTS + 1];
+    __shared__ int2 found[C > 2 ? W : 1][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i <= a.E; i += Shape<C>::THREADS) chosen[i] = 0;
     __syncthreads();
@@ -179,76 +299,48 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
         float v[C];
         load_row<DT, C>(static_cast<const char *>(a.logits) + t * a.ld * es, a.E, lane, vec, v);
         const bool valid = a.valid == nullptr || a.valid[t] != 0;
-        // the lane's two largest that are left, the earlier of equal ones first
-        // (branch-free: written with branches the kernel executes 2.5 times the
-        // instructions)
-        int k1, k2, i1, i2;
-        unsigned used = 0;
-        auto two = [&](auto all) {
-            k1 = k2 = INT_MIN;
-            i1 = i2 = 0;
+        int x[C];
 #pragma unroll
-            for (int i = 0; i < C; ++i) {
-                int k = key_of(v[i]);
-                if (!decltype(all)::value) k = used >> i & 1u ? INT_MIN : k;
-                const bool a1 = k > k1, a2 = k > k2;
-                i2 = a1 ? i1 : a2 ? i : i2;
-                k2 = max(k2, min(k1, k));
-                i1 = a1 ? i : i1;
-                k1 = max(k1, k);
-            }
-        };
-        two(std::true_type{});
-        int top = __reduce_max_sync(FULL, k1);
-        int got = 0, id = -1;
+        for (int i = 0; i < C; ++i) x[i] = key_of(v[i]);
+        int k1 = x[0];
+#pragma unroll
+        for (int i = 1; i < C; ++i) k1 = max(k1, x[i]);
+        const int top = __reduce_max_sync(FULL, k1);
+        // this lane's choice, if any, and its place among the token's
+        int got = 0, id = -1, key = INT_MIN, slot = lane;
         float w = 0.0f;
         if (valid && top > KEY_NEG_INF) {
             const float big = of_key(top);
             float s = 0.0f;
-            float e[C];
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                e[i] = exp2_approx((v[i] - big) * LOG2E);
-                s += e[i];
+                v[i] = exp2_approx((v[i] - big) * LOG2E);
+                s += v[i];
             }
             s = warp_sum(s);
             const float inv = 1.0f / s;
 #pragma unroll
-            for (int i = 0; i < C; ++i) mean[i] = fmaf(e[i], inv, mean[i]);
-            const float lse = big + logf(s);
+            for (int i = 0; i < C; ++i) mean[i] = fmaf(v[i], inv, mean[i]);
+            const float lse = fmaf(__log2f(s), LN2, big);
             z = fmaf(lse, lse, z);
             ++n;
-            // One after the other the largest that is left, the j-th for lane j;
-            // a lane whose two are taken looks for its next two (8 of 256: 1.2
-            // times a token)
-            int key = INT_MIN, have = 2;
-            for (; got < a.k && top > KEY_NEG_INF; ++got) {
-                const int src = __ffs(__ballot_sync(FULL, k1 == top)) - 1;
-                const int at = __shfl_sync(FULL, lane * C + i1, src);
-                if (lane == got) id = at, key = top;
-                const bool mine = lane == src;
-                if (C > 2) used |= mine ? 1u << i1 : 0u;
-                k1 = mine ? k2 : k1;
-                i1 = mine ? i2 : i1;
-                k2 = mine ? INT_MIN : k2;
-                if (C > 2) {
-                    have -= mine ? 1 : 0;
-                    if (__any_sync(FULL, have == 0) && have == 0) {
-                        two(std::false_type{});
-                        have = 2;
-                    }
-                }
-                top = __reduce_max_sync(FULL, k1);
-            }
-            if (id >= 0) {
+            bool few = false;
+            if constexpr (C > 2) few = choose_few<C>(a.k, lane, x, k1, top, found[warp], got, id, key, slot);
+            if (!few) choose<C>(a.k, lane, x, top, got, id, key);
+            const bool mine = id >= 0 && slot < got;
+            if (mine) {
                 w = exp2_approx((of_key(key) - big) * LOG2E) * inv;
                 atomicAdd(&chosen[id], 1);
             }
-            if (a.renorm) w /= warp_sum(w);
+            if (a.renorm) w *= 1.0f / warp_sum(w);
+            if (mine) {
+                a.ids[t * a.k + slot] = id;
+                a.weights[t * a.k + slot] = w;
+            }
         }
-        if (lane < a.k) {
-            a.ids[t * a.k + lane] = id;
-            a.weights[t * a.k + lane] = w;
+        if (lane >= got && lane < a.k) {
+            a.ids[t * a.k + lane] = -1;
+            a.weights[t * a.k + lane] = 0.0f;
         }
     }
     // the block's sums, over its warps in their order
@@ -277,7 +369,13 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
     if (gridDim.x > 1) return;
     // the only block: these are all
     __syncthreads();
-    finish(a, sums, chosen);
+    for (int e = threadIdx.x; e <= a.E; e += Shape<C>::THREADS) a.counts[e] = chosen[e];
+    if (warp == 0) {
+        double b = 0.0;
+        for (int e = lane; e < a.E; e += 32) b += (double)chosen[e] * sums[e];
+        b = warp_sum(b);
+        if (lane == 0) write_losses(a, b, sums[a.E], chosen[a.E]);
+    }
 }
 
 template <int DT, int C>
@@ -433,7 +531,7 @@ cudaError_t launch_route(const RouteArgs &a, int blocks, cudaStream_t st, int *l
                                 1u, a);
     });
     if (e != cudaSuccess || blocks == 1) return e;
-    return launch_dependent(finish_kernel, dim3(1), dim3(1024), 0, st, 1u, a, blocks);
+    return launch_dependent(finish_kernel, dim3(FINISH_BLOCKS), dim3(1024), 0, st, (unsigned)FINISH_BLOCKS, a, blocks);
 }
 
 cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t st)
