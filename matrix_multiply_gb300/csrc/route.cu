@@ -35,6 +35,36 @@ __device__ __forceinline__ int key_of(float x)
 __device__ __forceinline__ float of_key(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 constexpr int KEY_NEG_INF = (int)0x807fffffu;      // key_of(-inf); INT_MIN, below it, is no value
 
+// The larger, a NaN if either is one.
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// 1 / x to an ulp (x here is a sum of probabilities, or of exponentials with a 1
+// among them: neither tiny nor huge)
+__device__ __forceinline__ float inverse(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int warp_scan(int v)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+        asm("{\n\t.reg .pred p;\n\t.reg .s32 r;\n\t"
+            "shfl.sync.up.b32 r|p, %0, %1, 0, 0xffffffff;\n\t"
+            "@p add.s32 %0, %0, r;\n\t}"
+            : "+r"(v)
+            : "r"(o));
+    return v;
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -48,39 +78,48 @@ __device__ __forceinline__ float load_one(const void *p, long long i)
     return load_c(p, i, DT);
 }
 
+// Which expert is the lane's i-th: V neighbours at a time, and those side by side
+// over the lanes (INTERLEAVED: wide accesses without bank conflicts or sectors
+// read twice) or the lane's all together (the order that ties need).
+template <int C, bool INTERLEAVED>
+__device__ __forceinline__ constexpr int expert(int lane, int i)
+{
+    constexpr int V = C < 4 ? C : 4;
+    return INTERLEAVED ? (i / V) * 32 * V + lane * V + i % V : lane * C + i;
+}
+
 // The lane's C values of a row (`vec`: the row starts on 16 bytes and has a
 // multiple of 16 bytes); -inf past the last expert.
-template <int DT, int C>
+template <int DT, int C, bool INTERLEAVED>
 __device__ __forceinline__ void load_row(const void *row, int E, int lane, bool vec, float (&v)[C])
 {
-    constexpr int PER = DT == TC_F32 ? 4 : 8;
+    // 16 bytes at a time where a lane has them together
+    constexpr int PER = DT == TC_F32 || INTERLEAVED ? 4 : 8;
     if constexpr (C >= PER) {
         if (vec) {
 #pragma unroll
             for (int q = 0; q < C / PER; ++q) {
-                const int e = lane * C + q * PER;
+                const int e = expert<C, INTERLEAVED>(lane, q * PER);
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
                 if (e < E) {
-                    if constexpr (DT == TC_F32) {
-                        const float4 x = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + e));
-                        v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
+                    if constexpr (DT == TC_F32 || PER == 8) {
+                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + e * (DT == TC_F32 ? 4 : 2)));
+                        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
                     } else {
-                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + e));
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (DT == TC_BF16) {
-                                v[8 * q + 2 * j] = __uint_as_float(w[j] << 16);
-                                v[8 * q + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-                            } else {
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-                                v[8 * q + 2 * j] = f.x;
-                                v[8 * q + 2 * j + 1] = f.y;
-                            }
-                        }
+                        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(static_cast<const char *>(row) + e * 2));
+                        w[0] = x.x, w[1] = x.y;
                     }
-                } else {
+                }
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) v[PER * q + j] = -INFINITY;
+                for (int j = 0; j < PER; ++j) {
+                    float x;
+                    if constexpr (DT == TC_F32)
+                        x = __uint_as_float(w[j]);
+                    else if constexpr (DT == TC_BF16)
+                        x = __uint_as_float(j % 2 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+                    else
+                        x = __half2float(__ushort_as_half((unsigned short)(w[j / 2] >> (j % 2 * 16))));
+                    v[PER * q + j] = e < E ? x : -INFINITY;
                 }
             }
             return;
@@ -88,9 +127,16 @@ __device__ __forceinline__ void load_row(const void *row, int E, int lane, bool 
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int e = lane * C + i;
+        const int e = expert<C, INTERLEAVED>(lane, i);
         v[i] = e < E ? load_one<DT>(row, e) : -INFINITY;
     }
+}
+
+// The row of the warp's next token on its way into L2: a line for each of the
+// first lanes.
+__device__ __forceinline__ void fetch_ahead(const void *row, long long bytes, int lane)
+{
+    if (lane * 128 < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(row) + lane * 128));
 }
 
 template <int C>
@@ -100,13 +146,13 @@ struct Shape {
     static constexpr int WARPS = THREADS / 32;
 };
 
-// The choice of one token from its keys x (lane g's are those of experts g C ..),
+// The choice of one token from its logits v (lane g's are those of experts g C ..),
 // one after the other the largest that is left, the j-th for lane j.  A lane
 // keeps its two largest at hand, the earlier of equal ones first, and looks for
 // its next two when both are taken.  (Branch-free: with branches the kernel
 // executes 2.5 times the instructions.)
 template <int C>
-__device__ __forceinline__ void choose(int k, int lane, const int (&x)[C], int top, int &got, int &id, int &key)
+__device__ __forceinline__ void choose(int k, int lane, const float (&v)[C], int top, int &got, int &id, int &key)
 {
     int k1, k2, i1, i2;
     unsigned used = 0;
@@ -115,7 +161,7 @@ __device__ __forceinline__ void choose(int k, int lane, const int (&x)[C], int t
         i1 = i2 = 0;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int y = used >> i & 1u ? INT_MIN : x[i];
+            const int y = used >> i & 1u ? INT_MIN : key_of(v[i]);
             const bool first = y > k1, second = y > k2;
             i2 = first ? i1 : second ? i : i2;
             k2 = max(k2, min(k1, y));
@@ -145,49 +191,44 @@ __device__ __forceinline__ void choose(int k, int lane, const int (&x)[C], int t
     }
 }
 
-// The same where few values compete: the k-th largest of the lanes' maxima k1
-// bounds the k-th largest value from below, and what reaches it, 10 of 256 for
-// k = 8, goes to one lane each in the order of the indices (which is theirs) and
-// finds its rank by comparing with the others.  False, with nothing done, where
-// more than 32 reach it.  (65536 x 256, k = 8: all of the kernel 52 us with the
-// rounds above, 44 with these.)
+// The same where few values compete: the k-th largest of the lanes' maxima (k1 in
+// keys) bounds the k-th largest value from below, and what reaches it, 10 of 256
+// for k = 8, goes to one lane each in the order of the indices (which is theirs)
+// and finds its rank by comparing with the others.  False, with nothing done,
+// where more than 32 reach it, or a NaN is among them.  (65536 x 256, k = 8: all
+// of the call 62 us with the rounds above.)
 template <int C>
-__device__ __forceinline__ bool choose_few(int k, int lane, const int (&x)[C], int k1, int top, int2 *found, int &got,
+__device__ __forceinline__ bool choose_few(int k, int lane, const float (&v)[C], int k1, int top, int2 *found, int &got,
                                            int &id, int &key, int &slot)
 {
+    if (top == INT_MAX) return false;
     int bound = top, left = k1;
 #pragma unroll 4
     for (int j = 1; j < k; ++j) {
         left = left == bound ? INT_MIN : left;      // (equal ones at once: the bound is the lower)
         bound = __reduce_max_sync(FULL, left);
     }
-    bound = max(bound, KEY_NEG_INF + 1);
+    const float least = of_key(max(bound, KEY_NEG_INF + 1));
     int mine = 0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) mine += x[i] >= bound ? 1 : 0;
-    int after = mine;                               // with those of the lanes before
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(FULL, after, o);
-        after += lane >= o ? y : 0;
-    }
-    const int all = __shfl_sync(FULL, after, 31);
+    for (int i = 0; i < C; ++i) mine += v[i] >= least ? 1 : 0;
+    const int after = warp_scan(mine), all = __shfl_sync(FULL, after, 31);
     if (all > 32) return false;
     int2 *at = found + (after - mine);
 #pragma unroll
     for (int i = 0; i < C; ++i)
-        if (x[i] >= bound) *at++ = make_int2(x[i], lane * C + i);
+        if (v[i] >= least) *at++ = make_int2(__float_as_int(v[i]), lane * C + i);
     __syncwarp();
-    const int2 f = lane < all ? found[lane] : make_int2(INT_MIN, -1);
+    const int2 f = lane < all ? found[lane] : make_int2(0, -1);
     __syncwarp();
-    int rank = __popc(__match_any_sync(FULL, f.x) & ((1u << lane) - 1u));
+    key = f.y >= 0 ? key_of(__int_as_float(f.x)) : INT_MIN;
+    int rank = __popc(__match_any_sync(FULL, key) & ((1u << lane) - 1u));
     for (int r = 0; r < all; r += 4) {              // (lanes from `all` on are below every key)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) rank += __shfl_sync(FULL, f.x, (r + q) & 31) > f.x ? 1 : 0;
+        for (int q = 0; q < 4; ++q) rank += __shfl_sync(FULL, key, r + q) > key ? 1 : 0;
     }
     got = min(all, k);
     id = f.y;
-    key = f.x;
     slot = rank;
     return true;
 }
@@ -295,21 +336,26 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
     int n = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) mean[i] = 0.0f;
-    for (long long t = (long long)blockIdx.x * W + warp; t < a.T; t += (long long)gridDim.x * W) {
+    const long long first = (long long)blockIdx.x * W + warp, step = (long long)gridDim.x * W;
+    const char *row = static_cast<const char *>(a.logits) + first * a.ld * es;
+    const long long row_step = step * a.ld * es;
+    int *ids = a.ids + first * a.k;
+    float *weights = a.weights + first * a.k;
+    for (long long t = first; t < a.T; t += step, row += row_step, ids += step * a.k, weights += step * a.k) {
         float v[C];
-        load_row<DT, C>(static_cast<const char *>(a.logits) + t * a.ld * es, a.E, lane, vec, v);
+        load_row<DT, C, false>(row, a.E, lane, vec, v);
+        if (t + step < a.T) fetch_ahead(row + row_step, a.E * es, lane);
         const bool valid = a.valid == nullptr || a.valid[t] != 0;
-        int x[C];
+        float most = v[0];
 #pragma unroll
-        for (int i = 0; i < C; ++i) x[i] = key_of(v[i]);
-        int k1 = x[0];
-#pragma unroll
-        for (int i = 1; i < C; ++i) k1 = max(k1, x[i]);
-        const int top = __reduce_max_sync(FULL, k1);
+        for (int i = 1; i < C; ++i) most = max_nan(most, v[i]);
+        const int k1 = key_of(most), top = __reduce_max_sync(FULL, k1);
         // this lane's choice, if any, and its place among the token's
         int got = 0, id = -1, key = INT_MIN, slot = lane;
-        float w = 0.0f;
         if (valid && top > KEY_NEG_INF) {
+            bool few = false;
+            if constexpr (C > 2) few = choose_few<C>(a.k, lane, v, k1, top, found[warp], got, id, key, slot);
+            if (!few) choose<C>(a.k, lane, v, top, got, id, key);
             const float big = of_key(top);
             float s = 0.0f;
 #pragma unroll
@@ -318,29 +364,24 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
                 s += v[i];
             }
             s = warp_sum(s);
-            const float inv = 1.0f / s;
+            const float inv = inverse(s);
 #pragma unroll
             for (int i = 0; i < C; ++i) mean[i] = fmaf(v[i], inv, mean[i]);
             const float lse = fmaf(__log2f(s), LN2, big);
             z = fmaf(lse, lse, z);
             ++n;
-            bool few = false;
-            if constexpr (C > 2) few = choose_few<C>(a.k, lane, x, k1, top, found[warp], got, id, key, slot);
-            if (!few) choose<C>(a.k, lane, x, top, got, id, key);
             const bool mine = id >= 0 && slot < got;
+            float w = mine ? exp2_approx((of_key(key) - big) * LOG2E) * inv : 0.0f;
+            if (a.renorm) w *= inverse(warp_sum(w));
             if (mine) {
-                w = exp2_approx((of_key(key) - big) * LOG2E) * inv;
                 atomicAdd(&chosen[id], 1);
-            }
-            if (a.renorm) w *= 1.0f / warp_sum(w);
-            if (mine) {
-                a.ids[t * a.k + slot] = id;
-                a.weights[t * a.k + slot] = w;
+                ids[slot] = id;
+                weights[slot] = w;
             }
         }
         if (lane >= got && lane < a.k) {
-            a.ids[t * a.k + lane] = -1;
-            a.weights[t * a.k + lane] = 0.0f;
+            ids[lane] = -1;
+            weights[lane] = 0.0f;
         }
     }
     // the block's sums, over its warps in their order
@@ -402,95 +443,101 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradArgs a)
     float f[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int e = lane * C + i;
+        const int e = expert<C, true>(lane, i);
         f[i] = e < a.E ? gb * ((float)a.counts[e] / (n * (float)a.k)) : 0.0f;
     }
-    for (long long t = (long long)blockIdx.x * W + warp; t < a.T; t += (long long)gridDim.x * W) {
+    const long long first = (long long)blockIdx.x * W + warp, step = (long long)gridDim.x * W;
+    const char *src = static_cast<const char *>(a.logits) + first * a.ld * es;
+    const long long src_step = step * a.ld * es, row_step = step * a.ld_dl * ed;
+    char *row = static_cast<char *>(a.dl) + first * a.ld_dl * ed;
+    long long pair = first * a.k + lane;
+    for (long long t = first; t < a.T; t += step, src += src_step, row += row_step, pair += step * a.k) {
         float v[C];
-        load_row<DT, C>(static_cast<const char *>(a.logits) + t * a.ld * es, a.E, lane, vec, v);
+        load_row<DT, C, true>(src, a.E, lane, vec, v);
+        if (t + step < a.T) fetch_ahead(src + src_step, a.E * es, lane);
         const bool valid = a.valid == nullptr || a.valid[t] != 0;
         int id = -1;
         float gw = 0.0f;
         if (a.grad_weights && lane < a.k) {
-            id = a.ids[t * a.k + lane];
-            gw = a.grad_weights[t * a.k + lane];
+            id = a.ids[pair];
+            gw = a.grad_weights[pair];
         }
-        int key = INT_MIN;
+        float most = v[0];
 #pragma unroll
-        for (int i = 0; i < C; ++i) key = max(key, lane * C + i < a.E ? key_of(v[i]) : INT_MIN);
-        const int top = __reduce_max_sync(FULL, key);
+        for (int i = 1; i < C; ++i) most = max_nan(most, v[i]);
+        const int top = __reduce_max_sync(FULL, key_of(most));
         if (!valid || top <= KEY_NEG_INF) {
 #pragma unroll
             for (int i = 0; i < C; ++i) v[i] = 0.0f;
         } else {
             const float big = of_key(top);
-            float s = 0.0f;
+            float s = 0.0f, fp = 0.0f;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
                 v[i] = exp2_approx((v[i] - big) * LOG2E);
                 s += v[i];
-            }
-            s = warp_sum(s);
-            const float inv = 1.0f / s;
-            float fp = 0.0f;
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-                v[i] *= inv;
                 fp = fmaf(f[i], v[i], fp);
             }
+            s = warp_sum(s);
+            const float inv = inverse(s);
             // dl = p (f - sum f p + gz lse + what comes through the weights)
-            float all = gz * (big + logf(s)) - warp_sum(fp);
+            float all = gz * fmaf(__log2f(s), LN2, big) - warp_sum(fp) * inv;
             if (a.grad_weights) {
 #pragma unroll
-                for (int i = 0; i < C; ++i) probs[warp][lane * C + i] = v[i];
+                for (int i = 0; i < C; ++i) probs[warp][expert<C, true>(lane, i)] = v[i];
                 __syncwarp();
                 const bool on = id >= 0 && id < a.E;
-                const float p = on ? probs[warp][id] : 0.0f;
+                const float p = on ? probs[warp][id] * inv : 0.0f;
                 const float dot = warp_sum(on ? gw * p : 0.0f);
+                float g = p * gw;
                 if (a.renorm) {
-                    const float r = 1.0f / warp_sum(p);
-                    if (on) atomicAdd(&through[warp][id], p * r * (gw - dot * r));
+                    const float r = inverse(warp_sum(p));
+                    g = p * r * (gw - dot * r);
                 } else {
-                    if (on) atomicAdd(&through[warp][id], p * gw);
                     all -= dot;
+                }
+                // an index met twice: its gradients are added, lane by lane
+                const unsigned same = __match_any_sync(FULL, on ? id : -1 - lane);
+                if (__any_sync(FULL, same != 1u << lane)) {
+                    for (int j = 0; j < a.k; ++j) {
+                        if (lane == j && on) through[warp][id] += g;
+                        __syncwarp();
+                    }
+                } else if (on) {
+                    through[warp][id] = g;
                 }
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < C; ++i) v[i] = fmaf(v[i], f[i] + all, through[warp][lane * C + i]);
+                for (int i = 0; i < C; ++i) v[i] = fmaf(v[i] * inv, f[i] + all, through[warp][expert<C, true>(lane, i)]);
                 __syncwarp();
                 if (on) through[warp][id] = 0.0f;
             } else {
 #pragma unroll
-                for (int i = 0; i < C; ++i) v[i] *= f[i] + all;
+                for (int i = 0; i < C; ++i) v[i] *= inv * (f[i] + all);
             }
         }
-        char *row = static_cast<char *>(a.dl) + t * a.ld_dl * ed;
         bool stored = false;
         if constexpr (C >= 4) {
-            if (vec_out && a.dl_dtype == TC_F32) {
+            if (vec_out) {
 #pragma unroll
-                for (int q = 0; q < C / 4; ++q)
-                    if (lane * C + 4 * q < a.E)
-                        *reinterpret_cast<float4 *>(row + (lane * C + 4 * q) * 4) =
-                            make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                stored = true;
-            }
-        }
-        if constexpr (C >= 8) {
-            if (vec_out && a.dl_dtype != TC_F32) {
-#pragma unroll
-                for (int q = 0; q < C / 8; ++q)
-                    if (lane * C + 8 * q < a.E)
-                        *reinterpret_cast<uint4 *>(row + (lane * C + 8 * q) * 2) =
-                            make_uint4(pack2(v[8 * q], v[8 * q + 1], a.dl_dtype), pack2(v[8 * q + 2], v[8 * q + 3], a.dl_dtype),
-                                       pack2(v[8 * q + 4], v[8 * q + 5], a.dl_dtype), pack2(v[8 * q + 6], v[8 * q + 7], a.dl_dtype));
+                for (int q = 0; q < C / 4; ++q) {
+                    const int e = expert<C, true>(lane, 4 * q);
+                    if (e >= a.E) continue;
+                    if (a.dl_dtype == TC_F32)
+                        *reinterpret_cast<float4 *>(row + e * 4) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                    else
+                        *reinterpret_cast<uint2 *>(row + e * 2) =
+                            make_uint2(pack2(v[4 * q], v[4 * q + 1], a.dl_dtype), pack2(v[4 * q + 2], v[4 * q + 3], a.dl_dtype));
+                }
                 stored = true;
             }
         }
         if (!stored) {
 #pragma unroll
-            for (int i = 0; i < C; ++i)
-                if (lane * C + i < a.E) store_c1(row, lane * C + i, v[i], a.dl_dtype);
+            for (int i = 0; i < C; ++i) {
+                const int e = expert<C, true>(lane, i);
+                if (e < a.E) store_c1(row, e, v[i], a.dl_dtype);
+            }
         }
     }
 }
