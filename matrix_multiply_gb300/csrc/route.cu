@@ -419,8 +419,15 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
     }
 }
 
+// Resident blocks of 8 warps per SM, which is what covers a token's chain of
+// loads, reductions and exchanges (65536 x 256: 4 blocks of 64 registers 35.1
+// us, 5 of 48
+// 33.0); 16 values a lane need 80.
+template <int C>
+constexpr int GRAD_BLOCKS = C <= 2 ? 6 : C <= 8 ? 5 : 3;
+
 template <int DT, int C>
-__global__ void __launch_bounds__(256) route_grad_kernel(const RouteGradArgs a)
+__global__ void __launch_bounds__(256, GRAD_BLOCKS<C>) route_grad_kernel(const RouteGradArgs a)
 {
     constexpr int W = 8;
     // a token's probabilities, where the lanes of the chosen experts find theirs,
@@ -584,8 +591,12 @@ cudaError_t launch_route(const RouteArgs &a, int blocks, cudaStream_t st, int *l
 cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t st)
 {
     return by_shape(a.dtype, a.E, [&](auto dt, auto c) {
-        const unsigned grid = (unsigned)std::min<long long>(((long long)a.T + 7) / 8, 8LL * num_sms);
-        return launch_dependent(route_grad_kernel<decltype(dt)::value, decltype(c)::value>, dim3(grid), dim3(256), 0, st, 1u, a);
+        constexpr int C = decltype(c)::value;
+        // a block for every 8 tokens up to two rounds of them, then a fixed grid
+        // (8192 x 60 on the resident blocks alone: 6.7 us for 4.7)
+        const long long blocks = ((long long)a.T + 7) / 8, resident = (long long)GRAD_BLOCKS<C> * num_sms;
+        const unsigned grid = (unsigned)(blocks <= 2 * resident ? blocks : resident);
+        return launch_dependent(route_grad_kernel<decltype(dt)::value, C>, dim3(grid), dim3(256), 0, st, 1u, a);
     });
 }
 
