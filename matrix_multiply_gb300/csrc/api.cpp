@@ -17,6 +17,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <algorithm>
 #include <atomic>
 #include <memory>
@@ -2057,13 +2058,22 @@ tc_gemm_desc xent_desc(int64_t M, int64_t N, int64_t K, tc_dtype_t dt, tc_dtype_
                         (int32_t)ldb, (int32_t)ldc};
 }
 
-// Rows of a 16-bit matrix copied to rows TMA can read.
-tc_status_t pack_rows(tc_ctx *ctx, tc_stream *s, const void *src, int64_t ld, void *dst, int64_t ld_dst, int64_t rows,
-                      int64_t cols)
+// Rows of 16-bit matrices copied to rows TMA can read, in one launch.
+struct Rows {
+    const void *src;
+    int64_t ld;
+    void *dst;
+    int64_t ld_dst, rows, cols;
+};
+tc_status_t pack_rows(tc_ctx *ctx, tc_stream *s, std::initializer_list<Rows> all)
 {
     PackBatch pb;
-    pb.count = 1;
-    pb.seg[0] = PackArgs{static_cast<const uint16_t *>(src), static_cast<uint16_t *>(dst), rows, cols, ld, ld_dst, 0, 0, 1};
+    pb.count = 0;
+    for (const Rows &r : all)
+        if (r.rows > 0)
+            pb.seg[pb.count++] = PackArgs{static_cast<const uint16_t *>(r.src), static_cast<uint16_t *>(r.dst), r.rows, r.cols,
+                                          r.ld, r.ld_dst, 0, 0, 1};
+    if (pb.count == 0) return TC_OK;
     if (launch_pack(pb, s->st) != cudaSuccess) return TC_ERR_CUDA;
     ctx->launches += 1;
     return TC_OK;
@@ -2101,14 +2111,13 @@ tc_status_t run_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const vo
     const size_t o_x = c.take(pack_x ? T * ldp * 2 : 0), o_w = c.take(pack_w ? cols * ldp * 2 : 0);
     if ((st = reserve(s, 256, c.at)) != TC_OK) return st;
     uint8_t *rx = static_cast<uint8_t *>(s->rx);
-    if (pack_x && (st = pack_rows(ctx, s, X, n.ldx, rx + o_x, ldp, T, H)) != TC_OK) return st;
     for (int64_t v0 = 0; v0 < V; v0 += cols) {
         const int64_t N = std::min(cols, V - v0);
         const void *Wv = static_cast<const uint16_t *>(W) + v0 * n.ldw;
-        if (pack_w) {
-            if ((st = pack_rows(ctx, s, Wv, n.ldw, rx + o_w, ldp, N, H)) != TC_OK) return st;
-            Wv = rx + o_w;
-        }
+        if ((st = pack_rows(ctx, s, {{X, n.ldx, rx + o_x, ldp, pack_x && v0 == 0 ? T : 0, H},
+                                     {Wv, n.ldw, rx + o_w, ldp, pack_w ? N : 0, H}})) != TC_OK)
+            return st;
+        if (pack_w) Wv = rx + o_w;
         // (the last piece keeps the tile width that the statistics are laid out by)
         Force same = f;
         same.bn = first.bn;
@@ -2181,7 +2190,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
     Carve c;
     const size_t o_cp = c.take(T * 4), o_cy = c.take(T * 4), o_un = c.take(f16 ? H * 4 : 0);
-    const size_t o_x = c.take(TG * ldp * 2), o_w = c.take(pack_w ? cols * ldp * 2 : 0), o_sum = c.take(sum ? TG * H * 4 : 0);
+    const size_t o_x = c.take(TG * ldp * 2), o_w = c.take(pack_w ? cols * ldp * 2 : 0), o_sum = c.take(sum ? TG * ldp * 4 : 0);
     const size_t o_g = c.take(TG * ldg * 2);
     if ((st = reserve(s, 256, c.at)) != TC_OK) return st;
     uint8_t *rx = static_cast<uint8_t *>(s->rx);
@@ -2202,7 +2211,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             q->B = pack_w ? static_cast<const void *>(rx + o_w) : static_cast<const uint16_t *>(W) + v0 * n.ldw;
             q->C = sum ? static_cast<void *>(rx + o_sum) : dX;
             q->d = xent_desc(TG, H, N, d->dtype, sum ? TC_F32 : d->grad_dtype, false, false, d->scale, v0 > 0 ? 1.0f : 0.0f,
-                             ldg, pack_w ? ldp : n.ldw, sum ? H : n.lddx);
+                             ldg, pack_w ? ldp : n.ldw, sum ? ldp : n.lddx);
         } else {
             q->B = rx + o_x;
             q->C = static_cast<uint8_t *>(dW) + v0 * n.lddw * es;
@@ -2260,10 +2269,8 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     for (int64_t v0 = 0; v0 < V; v0 += cols) {
         const int64_t N = std::min(cols, V - v0);
         const void *Wv = static_cast<const uint16_t *>(W) + v0 * n.ldw;
-        if (pack_w) {
-            if ((st = pack_rows(ctx, s, Wv, n.ldw, rx + o_w, ldp, N, H)) != TC_OK) return st;
-            Wv = rx + o_w;
-        }
+        if ((st = pack_rows(ctx, s, {{Wv, n.ldw, rx + o_w, ldp, pack_w ? N : 0, H}})) != TC_OK) return st;
+        if (pack_w) Wv = rx + o_w;
         Plan p = plan_xent(T, N, H, ctx->num_sms, f);
         p.seg_kb = f32 ? XENT_SEG_KB : 0;
         if (v0 == 0) name = p.name;
@@ -2298,7 +2305,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     }
     if (sum) {
         const float *at = reinterpret_cast<const float *>(rx + o_sum);
-        const XentRoundArgs r{at, parts == 2 ? at + T * H : nullptr, dX, T, H, n.lddx, d->grad_dtype};
+        const XentRoundArgs r{at, parts == 2 ? at + T * ldp : nullptr, dX, T, H, ldp, n.lddx, d->grad_dtype};
         if (launch_xent_round(r, s->st) != cudaSuccess) return TC_ERR_CUDA;
         ctx->launches += 1;
     }

@@ -392,11 +392,12 @@ struct XentPrepArgs {
 };
 cudaError_t launch_xent_prep(const XentPrepArgs &a, cudaStream_t st);
 
-// dst [rows, cols] (leading dimension ld) = the contiguous fp32 src (+ more, if not null), rounded to dtype
+// dst [rows, cols] (leading dimension ld) = the fp32 src (+ more, if not null; both of leading dimension
+// ld_src, a multiple of 4, from 16-byte boundaries), rounded to dtype
 struct XentRoundArgs {
     const float *src, *more;
     void *dst;
-    long long rows, cols, ld;
+    long long rows, cols, ld_src, ld;
     int dtype;
 };
 cudaError_t launch_xent_round(const XentRoundArgs &a, cudaStream_t st);

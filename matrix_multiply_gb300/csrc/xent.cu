@@ -35,19 +35,20 @@ __device__ __forceinline__ void merge(float &m, float &s, float n, float t)
     m = top;
 }
 
-// Block sum in a fixed order (a tree over lanes, then over warps); the result
-// in every thread.
+// Block sum in a fixed order (a tree over lanes, then one over the warps' sums);
+// the result in every thread.
 template <typename T>
 __device__ __forceinline__ T block_sum(T v, T *buf)
 {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) buf[warp] = v;
     __syncthreads();
-    T r = buf[0];
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) r += buf[w];
-    __syncthreads();
-    return r;
+    v = lane < (int)(blockDim.x >> 5) ? buf[lane] : T(0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
 }
 
 // the sum of a block's rows and how many count, the reduced loss of them
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(256) round_kernel(const XentRoundArgs a)
     const long long per = (a.cols + 7) / 8, all = per * a.rows;
     const bool whole = a.cols % 8 == 0 && a.ld % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dst) & 15u) == 0;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += (long long)gridDim.x * 256) {
-        const long long row = i / per, col = (i - row * per) * 8, at = row * a.cols + col;
+        const long long row = i / per, col = (i - row * per) * 8, at = row * a.ld_src + col;
         float v[8];
         if (whole) {
 #pragma unroll
