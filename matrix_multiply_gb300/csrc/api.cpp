@@ -183,6 +183,7 @@ struct Plan {
     int seg0_split = 1, seg1_split = 1;
     bool tma_store = true;
     bool pack_a = false, pack_b = false;
+    bool seg = false;          // the kernels of a cross entropy's gradients, with
     int seg_kb = 0;            // sums cut along K, this many K blocks each (0: whole)
     int64_t tiles = 0, units = 0;
     std::string name;
@@ -860,6 +861,7 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
         a.x = xent->epi;
         a.c_tma = xent->mode == XENT_GRAD;
     }
+    a.c_wide = a.c_tma && d->c_dtype != TC_F32 && (xent || (p.seg && !p.csplit && p.bn % 128 == 0));
     a.c_3d = n.batch > 1;
     a.ws = partials ? reinterpret_cast<float *>(ws + a_pack_bytes + b_pack_bytes) : nullptr;
     a.status = s->status_dev;
@@ -867,7 +869,7 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     a.act = epi ? (int)epi->activation : (int)TC_ACT_NONE;
     a.col_scale = col_scale;
     a.slice_kb = p.i8acc ? I8_SLICE_KB : p.seg_kb > 0 ? p.seg_kb : a.num_kb;
-    L.seg = p.seg_kb > 0 && !xent;
+    L.seg = p.seg;
     const int64_t kb_per_unit = a.num_kb;
     a.timeout_ns = 4000000000ull + (unsigned long long)kb_per_unit * 20000ull;
     {
@@ -911,16 +913,15 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
         }
     }
     if (ok && a.c_tma)
-        ok = encode_map(ctx, &L.tmC, d->c_dtype, C, d->N, d->M, n.ldc, a.c_3d, n.batch, a.stride_c, 32, 32,
-                        d->c_dtype == TC_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+        ok = encode_map(ctx, &L.tmC, d->c_dtype, C, d->N, d->M, n.ldc, a.c_3d, n.batch, a.stride_c, a.c_wide ? 64 : 32, 32,
+                        d->c_dtype == TC_F32 || a.c_wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
     // split-K workspace: one row-major fp32 (BM*cg) x BN tile per K-slice unit
     const int64_t rows_per_tile = (int64_t)BM * p.cg;
     if (ok && a.ws)
         ok = encode_map(ctx, &L.tmW, TC_F32, a.ws, p.bn, (p.units - p.split_base) * rows_per_tile, p.bn, false, 1,
                         0, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
     if (ok && xent && xent->epi.two)
-        ok = encode_map(ctx, &L.tmW, d->c_dtype, xent->left, d->N, d->M, n.ldc, false, 1, 0, 32, 32,
-                        CU_TENSOR_MAP_SWIZZLE_64B);
+        ok = encode_map(ctx, &L.tmW, d->c_dtype, xent->left, d->N, d->M, n.ldc, false, 1, 0, 64, 32);
     if (!ok) return TC_ERR_CUDA;
     if ((e = launch_mma(L, s->st)) != cudaSuccess) return TC_ERR_CUDA;
     ++launches;
@@ -2222,14 +2223,15 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         // (8 tile rows by 9 columns in flight read least: the gradients of
         // 4096 x 65536 x 4096 take 4.25 ms, with 4 rows 4.34)
         if (f.group_m == 0) q->p.group_m = 8;
-        if (r != TC_OK || !f32) return r;
-        if (q->p.cg == 1 && q->p.bn == 192) {     // a shape that cannot cut its sums
+        if (r != TC_OK) return r;
+        if (q->p.cg == 1 && q->p.bn == 192) {     // a shape that these kernels do not have
             const bool pa = q->p.pack_a, pb = q->p.pack_b;
             q->p = plan_xent(q->d.M, q->d.N, q->d.K, ctx->num_sms, Force{});
             q->p.pack_a = pa;
             q->p.pack_b = pb;
         }
-        q->p.seg_kb = XENT_SEG_KB;
+        q->p.seg = true;
+        q->p.seg_kb = f32 ? XENT_SEG_KB : 0;
         return r;
     };
     // the largest workspace of them (a cluster split may have to go through memory)

@@ -258,12 +258,6 @@ __device__ __forceinline__ float bias_of(const MmaArgs &a, int lane, long long c
     return (a.bias && col < a.N) ? load_c(a.bias, col, a.c_dtype) : 0.0f;
 }
 
-// x rounded to a 16-bit type
-__device__ __forceinline__ float round16(float x, int dtype)
-{
-    return dtype == TC_BF16 ? __bfloat162float(__float2bfloat16_rn(x)) : __half2float(__float2half_rn(x));
-}
-
 // x[i] for a run-time i < N, from registers (the unrolled selects keep the
 // array out of local memory).
 template <int N>
@@ -450,6 +444,56 @@ __device__ __forceinline__ void store_tma(const CUtensorMap *map, bool is3d, int
             tma_store_3d(map, smem_u32(buf), (int)col0, (int)row0, b);
         else
             tma_store_2d(map, smem_u32(buf), (int)col0, (int)row0);
+        bulk_commit();
+    }
+}
+
+// The same for 64 columns of a 16-bit C: rows of 128 bytes (128-byte swizzle),
+// the lane's values times `scale`, stored as one.  With the type decided once and
+// nothing else to look at per value this is what makes an epilogue that is all of
+// a short product's time short: 32000 x 2048 outputs over K = 64 take LEANOLD
+// through the general epilogue above, LEANNEW through this one.
+template <bool BF16>
+__device__ __forceinline__ void fill_wide_as(uint8_t *buf, int lane, float scale, const float (&v)[2][32])
+{
+    constexpr int DT = BF16 ? TC_BF16 : TC_F16;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const float *x = &v[q >> 2][8 * (q & 3)];
+        *reinterpret_cast<uint4 *>(buf + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+            make_uint4(pack2(x[0] * scale, x[1] * scale, DT), pack2(x[2] * scale, x[3] * scale, DT),
+                       pack2(x[4] * scale, x[5] * scale, DT), pack2(x[6] * scale, x[7] * scale, DT));
+    }
+}
+__device__ __forceinline__ void fill_wide(int dtype, uint8_t *buf, int lane, float scale, const float (&v)[2][32])
+{
+    if (dtype == TC_BF16)
+        fill_wide_as<true>(buf, lane, scale, v);
+    else
+        fill_wide_as<false>(buf, lane, scale, v);
+}
+// v - v rounded to a 16-bit type
+__device__ __forceinline__ void left_over(int dtype, float (&v)[2][32])
+{
+    if (dtype == TC_BF16) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] -= __bfloat162float(__float2bfloat16_rn(v[j >> 5][j & 31]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] -= __half2float(__float2half_rn(v[j >> 5][j & 31]));
+    }
+}
+__device__ __forceinline__ void free_wide(int lane)        // before the first half: the buffer's last store has read it
+{
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+}
+__device__ __forceinline__ void store_wide(const CUtensorMap *map, const uint8_t *buf, int lane, long long row0, long long col0)
+{
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(map, smem_u32(buf), (int)col0, (int)row0);
         bulk_commit();
     }
 }
@@ -676,6 +720,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     static_assert(XENT == XENT_NONE || (EPI && SEG && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
     static_assert(!CSPLIT || BM * csplit_ld<BN>() * 4 <= S * STAGE, "the partial tile fits in the idle ring");
     constexpr int CHUNKS = BN / 32;
+    // 16-bit C in stores of 64 columns: a warp's chunks then come in pairs of
+    // neighbours (with half as many pairs as warps a lane quarter has, not)
+    constexpr bool WIDE64 = SEG && !CSPLIT && BN % 128 == 0;
+    static_assert(XENT != XENT_GRAD || WIDE64, "G is stored 64 columns at a time");
     static_assert(CG == 1 || CG == 2, "one CTA or a CTA pair");
     constexpr int CL = CG;                        // CTAs per cluster
     static_assert(BNL % 32 == 0 && BN <= 256, "each CTA's B share must be whole 32-column boxes");
@@ -950,6 +998,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
         const int row_in_tile = (int)rank * BM + quarter * 32 + lane;
         constexpr int EBUFS = epi_bufs(BN, CG, WIDE);
         constexpr int LAST_C0 = CHUNKS - CSTEP;        // this warp's last chunk: LAST_C0 + chunk0
+        // the warp's i-th chunk
+        const auto chunk_of = [&](int i) {
+            return WIDE64 ? 2 * (chunk0 + (i >> 1) * CSTEP) + (i & 1) : chunk0 + i * CSTEP;
+        };
         static_assert(CHUNKS % CSTEP == 0, "chunks split evenly between the warps of a lane quarter");
         uint8_t *my_stage = cstage + warp * epi_warp_bytes(BN, CG, WIDE);
         // The warp's staging is either its TMA chunk buffers (two that
@@ -1042,7 +1094,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             }
 #pragma unroll
             for (int i = 0; i < NCH; ++i)
-                bpre[i] = EPI && XENT == XENT_NONE ? bias_of(ea, lane, (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32) : 0.0f;
+                bpre[i] = EPI && XENT == XENT_NONE ? bias_of(ea, lane, (long long)w.tn * BN + chunk_of(i) * 32) : 0.0f;
             // segments of the unit (see the MMA warp): one, or the K slices
             // that I8ACC adds up in TMEM, SEG in registers
             const int nseg = I8ACC || SEG ? (w.kb1 - w.kb0 + args.slice_kb - 1) / args.slice_kb : 1;
@@ -1079,7 +1131,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         const bool first = sg == 0, last = sg + 1 == nseg;
 #pragma unroll
                         for (int i = 0; i < 2 * NCH; ++i) {
-                            const uint32_t at = taddr + (chunk0 + (i >> 1) * CSTEP) * 32 + (i & 1) * 16;
+                            const uint32_t at = taddr + chunk_of(i >> 1) * 32 + (i & 1) * 16;
                             uint32_t r[16];
                             __syncwarp();
                             tmem_ld_32x32b_x16(at, r);
@@ -1105,11 +1157,22 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                 auto fetch = [&](int i, float (&v)[32]) {
                     uint32_t r[32];
                     __syncwarp();
-                    tmem_ld_32x32b_x32(taddr + (chunk0 + i * CSTEP) * 32, r);
+                    tmem_ld_32x32b_x32(taddr + chunk_of(i) * 32, r);
                     tmem_ld_wait();
                     if (i == NCH - 1) release();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                };
+                // the i-th and the next, 64 columns side by side
+                auto fetch2 = [&](int i, float (&v)[2][32]) {
+                    uint32_t r[2][32];
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(taddr + chunk_of(i) * 32, r[0]);
+                    tmem_ld_32x32b_x32(taddr + chunk_of(i) * 32 + 32, r[1]);
+                    tmem_ld_wait();
+                    if (i == NCH - 2) release();
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] = __uint_as_float(r[j >> 5][j & 31]);
                 };
                 if constexpr (I8ACC) {
                     // This segment's fp32 accumulator holds exact integers (a
@@ -1147,7 +1210,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     float m = -INFINITY, s = 0.0f;
 #pragma unroll
                     for (int i = 0; i < NCH; ++i) {
-                        const long long col0 = (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32;
+                        const long long col0 = (long long)w.tn * BN + chunk_of(i) * 32;
                         if (col0 >= args.N) continue;         // (the whole warp)
                         float v[32];
 #pragma unroll
@@ -1161,40 +1224,56 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     if (row < args.M) args.x.part[(2LL * w.tn + chunk0) * args.M + row] = make_float2(m, s);
                 } else if constexpr (XENT == XENT_GRAD) {
 #pragma unroll 1
-                    for (int i = 0; i < NCH; ++i) {
-                        float v[32];
-                        fetch(i, v);
-                        const long long col0 = (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32;
-                        if (col0 >= args.N) continue;
+                    for (int i = 0; i < NCH; i += 2) {
+                        float v[2][32];
+                        fetch2(i, v);
+                        const long long col0 = (long long)w.tn * BN + chunk_of(i) * 32, row0 = row - lane;
+                        if (col0 >= args.N || row0 >= args.M) continue;      // (the whole warp)
                         const int hit = target - (int)col0;
-                        const bool any = __any_sync(0xffffffffu, hit >= 0 && hit < 32);
+                        const bool any = __any_sync(0xffffffffu, hit >= 0 && hit < 64);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = cp * exp2_approx(fmaf(v[j], args.x.k2, -rowlse));
-                        if (any) {
+                        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] -= j == hit ? cy : 0.0f;
-                        }
-                        if (cp == 0.0f && cy == 0.0f) {      // not counted: 0 whatever its logits are
+                            for (int j = 0; j < 32; ++j) v[h][j] = cp * exp2_approx(fmaf(v[h][j], args.x.k2, -rowlse));
+                            if (any) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                        }
-                        const long long row0 = row - lane;
-                        if (row0 < args.M) {
-                            store_tma<EBUFS>(&tmC, false, args.c_dtype, staging(STG_TMA), lane, 0, row0, col0, v);
-                            if (args.x.two) {
-                                // what the rounding left, rounded in turn
+                                for (int j = 0; j < 32; ++j) v[h][j] -= 32 * h + j == hit ? cy : 0.0f;
+                            }
+                            if (cp == 0.0f && cy == 0.0f) {      // not counted: 0 whatever its logits are
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] -= round16(v[j], args.c_dtype);
-                                store_tma<EBUFS>(&tmW, false, args.c_dtype, staging(STG_TMA), lane, 0, row0, col0, v);
+                                for (int j = 0; j < 32; ++j) v[h][j] = 0.0f;
                             }
                         }
+                        free_wide(lane);
+                        fill_wide(args.c_dtype, my_stage, lane, 1.0f, v);
+                        store_wide(&tmC, my_stage, lane, row0, col0);
+                        if (args.x.two) {
+                            // what the rounding left, rounded in turn
+                            left_over(args.c_dtype, v);
+                            free_wide(lane);
+                            fill_wide(args.c_dtype, my_stage, lane, 1.0f, v);
+                            store_wide(&tmW, my_stage, lane, row0, col0);
+                        }
+                    }
+                } else if (WIDE64 && w.S == 1 && args.c_wide) {
+                    // (beta is 0, a column scale the same for all columns)
+                    const float scale = args.col_scale ? args.alpha * args.col_scale[0] : args.alpha;
+#pragma unroll 1
+                    for (int i = 0; i < NCH; i += 2) {
+                        float v[2][32];
+                        fetch2(i, v);
+                        const long long col0 = (long long)w.tn * BN + chunk_of(i) * 32, row0 = row - lane;
+                        if (col0 >= args.N || row0 >= args.M) continue;      // (the whole warp)
+                        free_wide(lane);
+                        fill_wide(args.c_dtype, my_stage, lane, scale, v);
+                        store_wide(&tmC, my_stage, lane, row0, col0);
                     }
                 } else if (w.S == 1) {
 #pragma unroll 1
                     for (int i = 0; i < NCH; ++i) {
                         float v[32];
                         fetch(i, v);
-                        emit(w.b, row, (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32, v, pick(bpre, i));
+                        emit(w.b, row, (long long)w.tn * BN + chunk_of(i) * 32, v, pick(bpre, i));
                     }
                 } else if constexpr (CSPLIT) {
                     // K slice of a cluster split: the partial tile goes to this
@@ -1206,7 +1285,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     for (int i = 0; i < NCH; ++i) {
                         float v[32];
                         fetch(i, v);
-                        float4 *dst = reinterpret_cast<float4 *>(red + (chunk0 + i * CSTEP) * 32);
+                        float4 *dst = reinterpret_cast<float4 *>(red + chunk_of(i) * 32);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                     }
@@ -1220,7 +1299,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     for (int i = 0; i < NCH; ++i) {
                         float v[32];
                         fetch(i, v);
-                        store_tma<EBUFS>(&tmW, false, TC_F32, staging(STG_TMA), lane, 0, wrow0, (chunk0 + i * CSTEP) * 32, v);
+                        store_tma<EBUFS>(&tmW, false, TC_F32, staging(STG_TMA), lane, 0, wrow0, chunk_of(i) * 32, v);
                     }
                 }
             }
