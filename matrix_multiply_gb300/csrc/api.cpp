@@ -183,7 +183,7 @@ struct Plan {
     int seg0_split = 1, seg1_split = 1;
     bool tma_store = true;
     bool pack_a = false, pack_b = false;
-    bool seg = false;          // the kernels of a cross entropy's gradients, with
+    bool product = false;      // one of the products of a cross entropy's gradients
     int seg_kb = 0;            // sums cut along K, this many K blocks each (0: whole)
     int64_t tiles = 0, units = 0;
     std::string name;
@@ -861,7 +861,7 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
         a.x = xent->epi;
         a.c_tma = xent->mode == XENT_GRAD;
     }
-    a.c_wide = a.c_tma && d->c_dtype != TC_F32 && (xent || (p.seg && !p.csplit && p.bn % 128 == 0));
+    a.c_wide = a.c_tma && d->c_dtype != TC_F32 && (xent || (p.product && !p.csplit && p.bn % 128 == 0 && d->beta == 0.0f));
     a.c_3d = n.batch > 1;
     a.ws = partials ? reinterpret_cast<float *>(ws + a_pack_bytes + b_pack_bytes) : nullptr;
     a.status = s->status_dev;
@@ -869,7 +869,8 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     a.act = epi ? (int)epi->activation : (int)TC_ACT_NONE;
     a.col_scale = col_scale;
     a.slice_kb = p.i8acc ? I8_SLICE_KB : p.seg_kb > 0 ? p.seg_kb : a.num_kb;
-    L.seg = p.seg;
+    L.seg = p.seg_kb > 0;
+    if (p.product) L.xent = XENT_PRODUCT;
     const int64_t kb_per_unit = a.num_kb;
     a.timeout_ns = 4000000000ull + (unsigned long long)kb_per_unit * 20000ull;
     {
@@ -2230,7 +2231,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             q->p.pack_a = pa;
             q->p.pack_b = pb;
         }
-        q->p.seg = true;
+        q->p.product = true;
         q->p.seg_kb = f32 ? XENT_SEG_KB : 0;
         return r;
     };

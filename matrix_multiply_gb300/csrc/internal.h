@@ -155,7 +155,7 @@ struct MmaArgs {
     int c_dtype;           // TC_F16 / TC_BF16 / TC_F32
     int c_vec_ok;          // 16-byte vector loads/stores allowed on C
     int c_tma;             // C is written by TMA stores through the third descriptor
-    int c_wide;            // those of 64 columns each (16-bit C, beta 0; MmaLaunch::seg or xent)
+    int c_wide;            // those of 64 columns each (16-bit C, beta 0; MmaLaunch::xent)
     int c_3d;              // that descriptor is 3-D (batch index third)
     float *ws;             // split-K partial tiles (written through the fourth descriptor)
     unsigned *status;      // device status word (0 = fine)
@@ -177,7 +177,11 @@ struct MmaArgs {
     XentEpi x;
 };
 
-enum XentMode { XENT_NONE = 0, XENT_LOSS = 1, XENT_GRAD = 2 };
+// XENT_LOSS writes no C, XENT_GRAD writes G (16-bit, wide stores, whole-K tiles
+// of 256 or 128 columns like XENT_LOSS); XENT_PRODUCT is one of the gradients'
+// products with G, its 16-bit C in wide stores too (tiles of 256 or 128 columns;
+// beta 0, a col_scale the same for all columns)
+enum XentMode { XENT_NONE = 0, XENT_LOSS = 1, XENT_GRAD = 2, XENT_PRODUCT = 3 };
 struct MmaLaunch {
     int bn;
     int cg;      // CTAs per tile: 1, or 2 for a CTA pair (cluster of two)
@@ -187,14 +191,7 @@ struct MmaLaunch {
     // memory (BN 64 or 128, one CTA per unit: grid == args.total_units)
     int csplit;
     int grid;    // CTAs (a multiple of cg)
-    // the products of a cross entropy's gradients: sums cut along K,
-    // args.slice_kb blocks each, a 16-bit C in wide stores (tiles of 256 or 128
-    // columns; cut sums also in 192-wide pairs, 64-wide tiles and cluster splits).
-    // A col_scale has the same value for all columns here.
-    int seg;
-    // softmax cross entropy in place of the plain epilogue (args.x; whole-K
-    // tiles of 256 or 128 columns): XENT_LOSS writes no C, XENT_GRAD writes it
-    // (16-bit, by TMA stores)
+    int seg;     // sums cut along K, args.slice_kb blocks each (cross entropy, not the one-CTA 192-wide tile)
     int xent;
     CUtensorMap tmA, tmB, tmC, tmW;   // A, B, C and the split-K workspace
     MmaArgs args;

@@ -678,7 +678,7 @@ __device__ __forceinline__ void xent_statistics(const MmaArgs &a, long long col0
 // memory and no second kernel runs.
 //
 // XENT: the softmax cross entropy of the rows of A against those of B, in
-// place of the epilogue.  A row's logits are the row of one TMEM lane, so each
+// place of the epilogue (or, XENT_PRODUCT, a shorter one).  A row's logits are the row of one TMEM lane, so each
 // epilogue lane keeps its row's running maximum and sum in registers over its
 // chunks of the tile (XENT_LOSS: two floats leave the chip per row and half
 // tile), or turns them into the gradient of the logits from the row's known
@@ -687,14 +687,14 @@ __device__ __forceinline__ void xent_statistics(const MmaArgs &a, long long col0
 // outputs of an SM, which the next tile's MMAs hide from a hidden size of
 // about 512 on.
 //
-// SEG (and XENT): the accumulator is cut along K.  The tensor core truncates
+// SEG: the accumulator is cut along K.  The tensor core truncates
 // what it adds, so a sum of K products comes out up to (K / 16) 2^-24 of its
 // size too small (K = 4096: the mean of a loss 3.2e-6 off); here it sums
 // args.slice_kb blocks at a time, from zero, and the epilogue's threads add
 // those sums in registers, rounding to nearest, while the next ones are made in
 // the other TMEM buffer.
 template <int BN, int CG, bool GROUPED, bool EPI, bool I8ACC = false, bool CSPLIT = false, int XENT = XENT_NONE,
-          bool SEG = XENT != XENT_NONE>
+          bool SEG = false>
 __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmW,
@@ -717,12 +717,13 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     static_assert(!I8ACC || (EPI && !GROUPED && 3 * BN <= 512), "on-chip slices: two accumulators and the sums");
     static_assert(!CSPLIT || (CG == 1 && !GROUPED && !I8ACC), "cluster split-K: one CTA per slice");
     static_assert(!SEG || (EW == 8 && !GROUPED && !I8ACC), "segments: at most 128 sums in a thread's registers");
-    static_assert(XENT == XENT_NONE || (EPI && SEG && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
+    static_assert(XENT != XENT_LOSS || SEG, "a row's statistics are taken from registers");
+    static_assert(XENT == XENT_NONE || XENT == XENT_PRODUCT || (EPI && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
     static_assert(!CSPLIT || BM * csplit_ld<BN>() * 4 <= S * STAGE, "the partial tile fits in the idle ring");
     constexpr int CHUNKS = BN / 32;
     // 16-bit C in stores of 64 columns: a warp's chunks then come in pairs of
     // neighbours (with half as many pairs as warps a lane quarter has, not)
-    constexpr bool WIDE64 = SEG && !CSPLIT && BN % 128 == 0;
+    constexpr bool WIDE64 = XENT != XENT_NONE && !CSPLIT && BN % 128 == 0;
     static_assert(XENT != XENT_GRAD || WIDE64, "G is stored 64 columns at a time");
     static_assert(CG == 1 || CG == 2, "one CTA or a CTA pair");
     constexpr int CL = CG;                        // CTAs per cluster
@@ -1083,7 +1084,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             // cross entropy: what the lane's row needs, loaded as early
             int target = -1;
             float rowlse = 0.0f, cp = 0.0f, cy = 0.0f;
-            if constexpr (XENT != XENT_NONE) {
+            if constexpr (XENT == XENT_LOSS || XENT == XENT_GRAD) {
                 const long long row = (long long)w.tm * (BM * CL) + row_in_tile;
                 target = xent_target(args.x, row, args.M);
                 if (XENT == XENT_GRAD && row < args.M) {
@@ -1094,7 +1095,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             }
 #pragma unroll
             for (int i = 0; i < NCH; ++i)
-                bpre[i] = EPI && XENT == XENT_NONE ? bias_of(ea, lane, (long long)w.tn * BN + chunk_of(i) * 32) : 0.0f;
+                bpre[i] = EPI && (XENT == XENT_NONE || XENT == XENT_PRODUCT) ? bias_of(ea, lane, (long long)w.tn * BN + chunk_of(i) * 32) : 0.0f;
             // segments of the unit (see the MMA warp): one, or the K slices
             // that I8ACC adds up in TMEM, SEG in registers
             const int nseg = I8ACC || SEG ? (w.kb1 - w.kb0 + args.slice_kb - 1) / args.slice_kb : 1;
@@ -1255,7 +1256,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                             store_wide(&tmW, my_stage, lane, row0, col0);
                         }
                     }
-                } else if (WIDE64 && w.S == 1 && args.c_wide) {
+                } else if (XENT == XENT_PRODUCT && WIDE64 && w.S == 1 && args.c_wide) {
                     // (beta is 0, a column scale the same for all columns)
                     const float scale = args.col_scale ? args.alpha * args.col_scale[0] : args.alpha;
 #pragma unroll 1
@@ -1331,7 +1332,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
 }
 
 template <int BN, int CG, bool GROUPED = false, bool EPI = false, bool I8ACC = false, bool CSPLIT = false,
-          int XENT = XENT_NONE, bool SEG = XENT != XENT_NONE>
+          int XENT = XENT_NONE, bool SEG = false>
 cudaError_t launch_kernel(const MmaLaunch &L, cudaStream_t st, const TableOf<GROUPED> &gt = TableOf<GROUPED>{})
 {
     constexpr auto kern = mma_kernel<BN, CG, GROUPED, EPI, I8ACC, CSPLIT, XENT, SEG>;
@@ -1557,41 +1558,54 @@ cudaError_t launch_reduce(const ReduceArgs &r, cudaStream_t st)
                      : launch_dependent(splitk_reduce_kernel<false, 8>, grid, block, 0, st, 1u, r);
 }
 
-template <int XENT>
+template <int XENT, bool SEG>
 cudaError_t launch_xent(const MmaLaunch &L, cudaStream_t st)
 {
     if (L.csplit || L.i8acc || L.args.seg0_tiles != L.args.total_units || L.args.seg0_split != 1) return cudaErrorInvalidValue;
-    if (L.cg == 2 && L.bn == 256) return launch_kernel<256, 2, false, true, false, false, XENT>(L, st);
-    if (L.cg == 1 && L.bn == 256) return launch_kernel<256, 1, false, true, false, false, XENT>(L, st);
-    if (L.cg == 1 && L.bn == 128) return launch_kernel<128, 1, false, true, false, false, XENT>(L, st);
+    if (L.cg == 2 && L.bn == 256) return launch_kernel<256, 2, false, true, false, false, XENT, SEG>(L, st);
+    if (L.cg == 1 && L.bn == 256) return launch_kernel<256, 1, false, true, false, false, XENT, SEG>(L, st);
+    if (L.cg == 1 && L.bn == 128) return launch_kernel<128, 1, false, true, false, false, XENT, SEG>(L, st);
     return cudaErrorInvalidValue;
 }
 
-// Sums cut along K (args.slice_kb blocks), with the plain epilogue.
-template <int BN, int CG, bool CSPLIT = false>
-cudaError_t launch_seg(const MmaLaunch &L, cudaStream_t st)
+// One of the gradients' products; SEG: sums cut along K.
+template <int BN, int CG, bool SEG, bool CSPLIT = false>
+cudaError_t launch_product(const MmaLaunch &L, cudaStream_t st)
 {
-    return launch_kernel<BN, CG, false, true, false, CSPLIT, XENT_NONE, true>(L, st);
+    return launch_kernel<BN, CG, false, true, false, CSPLIT, XENT_PRODUCT, SEG>(L, st);
 }
 
 cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
 {
-    if ((L.xent || L.seg) && L.args.slice_kb < 1) return cudaErrorInvalidValue;
-    if (L.seg) {
-        if (L.csplit) return L.cg == 1 && L.bn == 128 ? launch_seg<128, 1, true>(L, st)
-                             : L.cg == 1 && L.bn == 64 ? launch_seg<64, 1, true>(L, st)
+    if ((L.xent == XENT_LOSS || L.seg) && L.args.slice_kb < 1) return cudaErrorInvalidValue;
+    if (L.xent == XENT_LOSS) return launch_xent<XENT_LOSS, true>(L, st);
+    if (L.xent == XENT_GRAD) {
+        if (!L.args.c_wide) return cudaErrorInvalidValue;
+        return L.seg ? launch_xent<XENT_GRAD, true>(L, st) : launch_xent<XENT_GRAD, false>(L, st);
+    }
+    if (L.xent == XENT_PRODUCT && L.seg) {
+        if (L.csplit) return L.cg == 1 && L.bn == 128 ? launch_product<128, 1, true, true>(L, st)
+                             : L.cg == 1 && L.bn == 64 ? launch_product<64, 1, true, true>(L, st)
                                                        : cudaErrorInvalidValue;
-        if (L.cg == 2) return L.bn == 256   ? launch_seg<256, 2>(L, st)
-                              : L.bn == 192 ? launch_seg<192, 2>(L, st)
-                              : L.bn == 128 ? launch_seg<128, 2>(L, st)
+        if (L.cg == 2) return L.bn == 256   ? launch_product<256, 2, true>(L, st)
+                              : L.bn == 192 ? launch_product<192, 2, true>(L, st)
+                              : L.bn == 128 ? launch_product<128, 2, true>(L, st)
                                             : cudaErrorInvalidValue;
-        return L.bn == 256   ? launch_seg<256, 1>(L, st)
-               : L.bn == 128 ? launch_seg<128, 1>(L, st)
-               : L.bn == 64  ? launch_seg<64, 1>(L, st)
+        return L.bn == 256   ? launch_product<256, 1, true>(L, st)
+               : L.bn == 128 ? launch_product<128, 1, true>(L, st)
+               : L.bn == 64  ? launch_product<64, 1, true>(L, st)
                              : cudaErrorInvalidValue;
     }
-    if (L.xent == XENT_LOSS) return launch_xent<XENT_LOSS>(L, st);
-    if (L.xent == XENT_GRAD) return L.args.c_tma ? launch_xent<XENT_GRAD>(L, st) : cudaErrorInvalidValue;
+    if (L.xent == XENT_PRODUCT && L.args.c_wide) {
+        if (L.csplit) return cudaErrorInvalidValue;
+        if (L.cg == 2) return L.bn == 256   ? launch_product<256, 2, false>(L, st)
+                              : L.bn == 128 ? launch_product<128, 2, false>(L, st)
+                                            : cudaErrorInvalidValue;
+        return L.bn == 256   ? launch_product<256, 1, false>(L, st)
+               : L.bn == 128 ? launch_product<128, 1, false>(L, st)
+                             : cudaErrorInvalidValue;
+    }
+    // (a product in fp32 whole, or in tiles of other widths: the plain kernels)
     const bool epi = L.args.bias != nullptr || L.args.act != TC_ACT_NONE || L.args.col_scale != nullptr;
     if (L.csplit) {
         if (L.cg != 1 || L.i8acc) return cudaErrorInvalidValue;
