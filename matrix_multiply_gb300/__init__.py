@@ -765,12 +765,20 @@ def _check_vector(name: str, t, n_elems: int, code: int):
 
 
 def _check_rows(name: str, t, rows: int, cols: int, ld: int, code: int):
-    """A matrix at the descriptor's leading dimension, which a 2-D tensor must have."""
+    """A matrix at the descriptor's leading dimension: a 2-D tensor of that stride,
+    or a contiguous one of any shape where the rows follow one another."""
     _check_operand(name, t, _extent(rows, cols, ld or cols), code)
-    if t is None or isinstance(t, int):
+    if t is None or isinstance(t, int) or ((ld or cols) == cols and t.is_contiguous()):
         return
-    if t.dim() == 2 and ((cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or cols))):
+    if t.dim() != 2 or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) != (ld or cols)):
         raise ValueError(f"{name} has strides {tuple(t.stride())}, the descriptor rows of {cols} at {ld or cols}")
+
+
+def _check_device(ctx: Context, **tensors):
+    """The context's kernels run on its device."""
+    for name, t in tensors.items():
+        if t is not None and not isinstance(t, int) and t.is_cuda and t.device.index != ctx.device:
+            raise ValueError(f"{name} is on {t.device}, the context on device {ctx.device}")
 
 
 def _prepared_call(name: str, args, stream, wait: bool):
@@ -809,6 +817,7 @@ class PreparedXent:
             _check_vector("targets", targets, d.tokens, d.target_dtype)
             for name, t, count in (("lse", lse, d.tokens), ("loss", loss, n), ("grad", grad, n)):
                 _check_vector(name, t, count, TC_F32)
+        _check_device(ctx, X=X, W=W, targets=targets, lse=lse, loss=loss, grad=grad, dX=dX, dW=dW)
         head = (vp(ctx.ptr), ctypes.byref(d), vp(_addr(X)), vp(_addr(W)), vp(_addr(targets)))
         self._forward = head + (vp(_addr(loss)), vp(_addr(lse))) if loss is not None else None
         self._backward = head + (vp(_addr(lse)), vp(_addr(grad)), vp(_addr(dX) or None), vp(_addr(dW) or None)) \
@@ -902,6 +911,8 @@ class PreparedRoute:
                 if valid.dtype not in (torch.uint8, torch.bool):
                     raise ValueError("valid must be uint8 or bool")
                 _check_vector("valid", valid, d.tokens, TC_I8)
+        _check_device(ctx, logits=logits, ids=ids, counts=counts, valid=valid, weights=weights, losses=losses,
+                      grad_weights=grad_weights, grad_losses=grad_losses, dlogits=dlogits)
         head = (vp(ctx.ptr), ctypes.byref(d), vp(_addr(logits)), vp(_addr(valid) or None), vp(_addr(ids)))
         self._forward = head + (vp(_addr(weights)), vp(_addr(counts)), vp(_addr(losses))) if weights is not None else None
         self._backward = head + (vp(_addr(counts)), vp(_addr(grad_weights) or None), vp(_addr(grad_losses) or None),

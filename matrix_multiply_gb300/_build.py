@@ -26,7 +26,7 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "--expt-relaxed-constexpr", f"-I{INCLUDE}"]
 SOURCES = ["api.cpp", "tc_mma.cu", "ffma.cu", "pack.cu", "gemv.cu", "q4.cu", "q4_gemv.cu", "q4_mma.cu", "moe.cu",
            "xent.cu", "route.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "elem.cuh", "q4.cuh"]
+HEADERS = ["internal.h", "ptx.cuh", "elem.cuh", "q4.cuh", "xent.cuh"]
 
 
 def nvcc() -> str:

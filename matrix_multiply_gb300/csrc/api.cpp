@@ -184,6 +184,7 @@ struct Plan {
     bool tma_store = true;
     bool pack_a = false, pack_b = false;
     bool product = false;      // one of the products of a cross entropy's gradients
+    int fold = 0;              // its C has this many rows, sums of two of the product's each (cluster split)
     int seg_kb = 0;            // sums cut along K, this many K blocks each (0: whole)
     int64_t tiles = 0, units = 0;
     std::string name;
@@ -632,6 +633,14 @@ tc_status_t read_status(tc_stream *s)
     return TC_OK;
 }
 
+// Clusters of S CTAs of a cluster split's kernel resident at once, queried once.
+int csplit_clusters(tc_ctx *ctx, int bn, int S)
+{
+    int &n = ctx->csplit_clusters[bn == 64 ? 0 : 1][std::min(S, CSPLIT_MAX)];
+    if (n < 0) n = max_active_csplit_clusters(bn, S);
+    return n;
+}
+
 // Enqueue one validated, planned problem on stream s (epi: the fused
 // bias/activation epilogue, or null).
 // col_scale: the int8 path's per-column dequantisation (its K slices then
@@ -731,15 +740,12 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
         // 8 of 12).  Unless the split was forced, the slice count shrinks
         // until every tile's cluster is resident; with no schedulable
         // cluster at all the same slices go through global memory.
-        auto clusters = [&](int S) {
-            int &mc = ctx->csplit_clusters[p.bn == 64 ? 0 : 1][std::min(S, CSPLIT_MAX)];
-            if (mc < 0) mc = max_active_csplit_clusters(p.bn, S);
-            return mc;
-        };
+        auto clusters = [&](int S) { return csplit_clusters(ctx, p.bn, S); };
         int S = p.seg0_split;
         if (read_force().split == 0)
             while (S > 2 && clusters(S) < p.tiles) --S;
         if (clusters(S) < 1 || int_slices) {
+            if (p.fold > 0) return TC_ERR_VARIANT;
             p.csplit = false;
             p.grid = (int)std::min<int64_t>(p.units, ctx->num_sms);
             const std::string::size_type at = p.name.find("_csplit");
@@ -855,7 +861,8 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     const int64_t ec = (int64_t)elem_size(d->c_dtype);
     a.c_vec_ok = aligned16(C) && (n.ldc * ec) % 16 == 0 && (a.stride_c * ec) % 16 == 0;
     // C written through TMA stores of 32 x 32 chunks when its layout allows
-    a.c_tma = a.c_vec_ok && p.tma_store;
+    a.c_tma = a.c_vec_ok && p.tma_store && !p.csplit;
+    a.fold = p.fold;
     if (xent) {
         L.xent = xent->mode;
         a.x = xent->epi;
@@ -1946,6 +1953,7 @@ tc_status_t check_xent(const tc_xent_desc *d, const void *X, const void *W, cons
     n.lddw = d->lddw ? d->lddw : d->hidden;
     if (n.ldx < d->hidden || n.ldw < d->hidden || n.lddx < d->hidden || n.lddw < d->hidden) return TC_ERR_LD;
     if (!std::isfinite(d->scale) || d->scale <= 0.0f || !std::isfinite(d->z_weight) || d->z_weight < 0.0f) return TC_ERR_SCALAR;
+    if (d->hidden > INT32_MAX - 63) return TC_ERR_OVERFLOW;       // copies have rows of whole 64s
     if (!extent(d->tokens, d->hidden, n.ldx, 1, 0, 2, &n.x_bytes) || !extent(d->vocab, d->hidden, n.ldw, 1, 0, 2, &n.w_bytes))
         return TC_ERR_OVERFLOW;
     // tiles are counted in 32 bits
@@ -2206,6 +2214,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         const void *A, *B;
         void *C;
     };
+    bool folded = false;
     auto product = [&](bool rows, int64_t v0, Product *q) {
         const int64_t N = std::min(cols, V - v0);
         q->A = rx + o_g;
@@ -2233,6 +2242,15 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         }
         q->p.product = true;
         q->p.seg_kb = f32 ? XENT_SEG_KB : 0;
+        // halves of one tile row meet where the cluster's slices do
+        if (rows && parts == 2 && TG <= BM && cols == V && q->p.csplit && csplit_clusters(ctx, q->p.bn, 2) > 0) {
+            q->p.fold = (int)T;
+            q->C = dX;
+            q->d.c_dtype = d->grad_dtype;
+            q->d.ldc = (int32_t)n.lddx;
+            q->n.ldc = n.lddx;
+            folded = true;
+        }
         return r;
     };
     // the largest workspace of them (a cluster split may have to go through memory)
@@ -2266,8 +2284,12 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     a.clean = reinterpret_cast<uint16_t *>(rx + o_x);
     a.ld_clean = ldp;
     a.copies = (int)parts;
-    if (launch_xent_prep(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
-    ctx->launches += 1;
+    // few rows: no launch of its own
+    const bool own_prep = T <= XENT_OWN_PREP_ROWS && cols == V && aligned16(X) && n.ldx % 8 == 0;
+    if (!own_prep) {
+        if (launch_xent_prep(a, s->st) != cudaSuccess) return TC_ERR_CUDA;
+        ctx->launches += 1;
+    }
     std::string name;
     for (int64_t v0 = 0; v0 < V; v0 += cols) {
         const int64_t N = std::min(cols, V - v0);
@@ -2277,7 +2299,8 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         Plan p = plan_xent(T, N, H, ctx->num_sms, f);
         p.seg_kb = f32 ? XENT_SEG_KB : 0;
         if (v0 == 0) name = p.name;
-        const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, d->dtype, false, true, 1.0f, 0.0f, ldp, pack_w ? ldp : n.ldw, ldg);
+        const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, d->dtype, false, true, 1.0f, 0.0f, own_prep ? n.ldx : ldp,
+                                          pack_w ? ldp : n.ldw, ldg);
         Norm gn{};
         gn.lda = gd.lda;
         gn.ldb = gd.ldb;
@@ -2297,8 +2320,10 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         job.epi.cp = a.cp;
         job.epi.cy = a.cy;
         job.epi.two = parts == 2;
+        job.epi.own_prep = own_prep;
+        job.epi.prep = a;
         job.left = rx + o_g + (size_t)(T * ldg * 2);
-        if ((st = enqueue(ctx, &gd, gn, p, rx + o_x, Wv, rx + o_g, s, nullptr, nullptr, false, &job)) != TC_OK) return st;
+        if ((st = enqueue(ctx, &gd, gn, p, own_prep ? X : rx + o_x, Wv, rx + o_g, s, nullptr, nullptr, false, &job)) != TC_OK) return st;
         for (const bool rows : {true, false}) {
             if (rows ? !dX : !dW) continue;
             Product q;
@@ -2306,7 +2331,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             if ((st = enqueue(ctx, &q.d, q.n, q.p, q.A, q.B, q.C, s, nullptr, unscale)) != TC_OK) return st;
         }
     }
-    if (sum) {
+    if (sum && !folded) {
         const float *at = reinterpret_cast<const float *>(rx + o_sum);
         const XentRoundArgs r{at, parts == 2 ? at + T * ldp : nullptr, dX, T, H, ldp, n.lddx, d->grad_dtype};
         if (launch_xent_round(r, s->st) != cudaSuccess) return TC_ERR_CUDA;

@@ -103,6 +103,25 @@ __host__ __device__ constexpr int mma_smem_bytes(int bn, int cg, bool epi = fals
     return mma_stages(bn, cg, epi) * stage_bytes(bn, cg) + smem_reserve(bn, cg, epi);
 }
 
+// What the gradient's products read besides W: each row's factors (cp and
+// cy of XentEpi), X in rows of ld_clean elements with the rows that do not count
+// zeroed, and for f16 the factors times a power of two that puts the largest
+// between 2^13 and 2^14, with its inverse H times for the products' columns.
+struct XentPrepArgs {
+    const void *targets;
+    int wide, vocab;
+    int T, H, reduction;
+    float z;
+    const float *lse, *grad;   // grad: T values, or one where reduced
+    float *cp, *cy;
+    float *unscale;            // H floats (f16), or null
+    const uint16_t *X;
+    long long ldx;
+    uint16_t *clean;
+    long long ld_clean;        // a multiple of 8; clean is 16-byte aligned
+    int copies;                // of the T rows, one below the other
+};
+
 // What the epilogue of a product of hidden rows with a vocabulary's rows needs
 // for a softmax cross entropy (the public header states the formulas); the
 // product's columns are the vocabulary's [first, first + N).
@@ -122,7 +141,12 @@ struct XentEpi {
     // rounding left
     const float *lse, *cp, *cy;
     int two;
+    // few rows, X readable by TMA as it is: the kernel that makes G makes the
+    // factors too, and the copy of X (what launch_xent_prep does otherwise)
+    int own_prep;
+    XentPrepArgs prep;
 };
+constexpr int XENT_OWN_PREP_ROWS = 128;
 
 // Device-side arguments of the tensor-core kernel (the two TMA descriptors
 // travel as separate __grid_constant__ parameters).
@@ -168,6 +192,9 @@ struct MmaArgs {
     const void *bias;
     int act;
     const float *col_scale;
+    // XENT_PRODUCT in a cluster split of one tile row: C has `fold` rows, the sums
+    // of rows r and fold + r of the product (0: not)
+    int fold;
     int slice_kb;          // K blocks per slice of an accumulator cut along K (int8, cross entropy, MmaLaunch::seg)
     // one-CTA tiles over fewer than BM rows of a K-major A: its copies carry
     // only the rows that exist (rounded up to 8) and a stage this many fewer
@@ -374,24 +401,6 @@ struct XentJoinArgs {
 // one launch, or two for the reduced loss of more rows than a block joins
 cudaError_t launch_xent_join(const XentJoinArgs &a, cudaStream_t st, int *launches);
 
-// What the gradient's products read besides W: each row's factors (XentEpi's cp
-// and cy), X in rows of ld_clean elements with the rows that do not count
-// zeroed, and for f16 the factors times a power of two that puts the largest
-// between 2^13 and 2^14, with its inverse H times for the products' columns.
-struct XentPrepArgs {
-    const void *targets;
-    int wide, vocab;
-    int T, H, reduction;
-    float z;
-    const float *lse, *grad;   // grad: T values, or one where reduced
-    float *cp, *cy;
-    float *unscale;            // H floats (f16), or null
-    const uint16_t *X;
-    long long ldx;
-    uint16_t *clean;
-    long long ld_clean;        // a multiple of 8; clean is 16-byte aligned
-    int copies;                // of the T rows, one below the other
-};
 cudaError_t launch_xent_prep(const XentPrepArgs &a, cudaStream_t st);
 
 // dst [rows, cols] (leading dimension ld) = the fp32 src (+ more, if not null; both of leading dimension

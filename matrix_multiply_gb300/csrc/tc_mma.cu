@@ -34,6 +34,7 @@
 #include "elem.cuh"
 #include "internal.h"
 #include "ptx.cuh"
+#include "xent.cuh"
 #include "../../include/tcgemm.h"
 
 #include <cuda_bf16.h>
@@ -564,7 +565,8 @@ __device__ __forceinline__ void finish4(const MmaArgs &a, int b, long long grow,
 // CTA of rank r sums rows [r * ceil(BM/S), ...) of all S partial tiles,
 // reading its peers' shared memory in slice order (deterministic), and
 // writes those rows of C.  Every thread of the CTA takes part.
-template <int BN, bool EPI>
+// FOLD: with a.fold set, its rows are sums of two rows of the product.
+template <int BN, bool EPI, bool FOLD>
 __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *partial)
 {
     constexpr int LD = csplit_ld<BN>();
@@ -572,8 +574,9 @@ __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *p
     constexpr int SMAX = 16;
     const int S = a.seg0_split;
     const uint32_t rank = cluster_ctarank();
-    const int rows = (BM + S - 1) / S;
-    const int r0 = min(BM, (int)rank * rows), r1 = min(BM, r0 + rows);
+    const bool fold = FOLD && a.fold > 0;
+    const int all = fold ? a.fold : BM, rows = (all + S - 1) / S;
+    const int r0 = min(all, (int)rank * rows), r1 = min(all, r0 + rows);
     const Unit w = decode_unit(a, (int)blockIdx.x);
     const uint32_t base = smem_u32(partial);
     for (int g = threadIdx.x; g < (r1 - r0) * G; g += blockDim.x) {
@@ -595,6 +598,21 @@ __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *p
                 v[3] += p[q].w;
             }
         }
+        if (fold) {
+            const uint32_t more = off + (uint32_t)(a.fold * LD * 4);
+#pragma unroll
+            for (int q = 0; q < SMAX; ++q)
+                if (q < S) p[q] = ld_shared_cluster_f4(mapa_shared(more, (uint32_t)q));
+#pragma unroll
+            for (int q = 0; q < SMAX; ++q) {
+                if (q < S) {
+                    v[0] += p[q].x;
+                    v[1] += p[q].y;
+                    v[2] += p[q].z;
+                    v[3] += p[q].w;
+                }
+            }
+        }
         finish4<EPI>(a, w.b, grow, gcol, v);
     }
 }
@@ -605,10 +623,8 @@ __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *p
 // it is in another piece of the vocabulary or the row is not counted).
 __device__ __forceinline__ int xent_target(const XentEpi &x, long long row, int M)
 {
-    if (row >= M) return -1;
-    const long long y = x.wide ? static_cast<const long long *>(x.targets)[row]
-                               : (long long)static_cast<const int *>(x.targets)[row];
-    return y >= 0 && y < x.vocab ? (int)(y - x.first) : -1;
+    long long y;
+    return row < M && xent_counts(x.targets, x.wide, x.vocab, row, y) ? (int)(y - x.first) : -1;
 }
 
 // One chunk of a row's statistics: m the largest exponent so far, s the sum of
@@ -1055,6 +1071,33 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                 store_direct(ea, b, row, col0, v);
             }
         };
+        // few rows: their factors' common parts, by every warp for itself
+        float mean = 1.0f, power = 1.0f;
+        const bool own_prep = XENT == XENT_GRAD && args.x.own_prep;
+        if constexpr (XENT == XENT_GRAD) {
+            if (own_prep) {
+                const XentPrepArgs &q = args.x.prep;
+                if (q.reduction == TC_REDUCE_MEAN) {
+                    int n = 0;
+                    for (int t = lane; t < q.T; t += 32) n += xent_counts(q, t) ? 1 : 0;
+                    mean = 1.0f / (float)max(__reduce_add_sync(0xffffffffu, n), 1);
+                }
+                if (q.unscale) {
+                    float top = 0.0f;
+                    for (int t = lane; t < q.T; t += 32) {
+                        float p, y;
+                        xent_factors(q, t, mean, p, y);
+                        top = fmaxf(top, fmaxf(fabsf(p), fabsf(y)));
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    power = xent_power(top);
+                    for (int h = blockIdx.x * (EW * 32) + threadIdx.x; h < q.H; h += gridDim.x * (EW * 32))
+                        q.unscale[h] = 1.0f / power;
+                }
+                xent_copy(q, (long long)blockIdx.x * (EW * 32) + threadIdx.x, (long long)gridDim.x * (EW * 32));
+            }
+        }
         const uint32_t tempty_leader0 = CG == 2 ? mapa_shared(smem_u32(&tempty_bar[0]), 0) : 0u;
         const uint32_t tempty_leader1 = CG == 2 ? mapa_shared(smem_u32(&tempty_bar[1]), 0) : 0u;
         for (int u = cluster; u < args.total_units; u += nclusters) {
@@ -1088,8 +1131,14 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                 const long long row = (long long)w.tm * (BM * CL) + row_in_tile;
                 target = xent_target(args.x, row, args.M);
                 if (XENT == XENT_GRAD && row < args.M) {
-                    cp = args.x.cp[row];
-                    cy = args.x.cy[row];
+                    if (own_prep) {
+                        xent_factors(args.x.prep, (int)row, mean, cp, cy);
+                        cp *= power;
+                        cy *= power;
+                    } else {
+                        cp = args.x.cp[row];
+                        cy = args.x.cy[row];
+                    }
                     rowlse = args.x.lse[row] * 1.4426950408889634f;
                 }
             }
@@ -1269,6 +1318,18 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         fill_wide(args.c_dtype, my_stage, lane, scale, v);
                         store_wide(&tmC, my_stage, lane, row0, col0);
                     }
+                } else if (XENT == XENT_PRODUCT && w.S == 1 && args.c_tma && args.c_dtype == TC_F32 && args.beta == 0.0f) {
+                    const float scale = args.col_scale ? args.alpha * args.col_scale[0] : args.alpha;
+#pragma unroll 1
+                    for (int i = 0; i < NCH; ++i) {
+                        float v[32];
+                        fetch(i, v);
+                        const long long col0 = (long long)w.tn * BN + chunk_of(i) * 32, row0 = row - lane;
+                        if (col0 >= args.N || row0 >= args.M) continue;      // (the whole warp)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] *= scale;
+                        store_tma<EBUFS>(&tmC, false, TC_F32, staging(STG_TMA), lane, 0, row0, col0, v);
+                    }
                 } else if (w.S == 1) {
 #pragma unroll 1
                     for (int i = 0; i < NCH; ++i) {
@@ -1317,7 +1378,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     __syncthreads();
     if constexpr (CSPLIT) {
         cluster_sync();              // every slice's partial tile is in its CTA's shared memory
-        csplit_reduce<BN, EPI>(args, smem);
+        csplit_reduce<BN, EPI, XENT == XENT_PRODUCT>(args, smem);
         cluster_sync();              // no CTA releases its shared memory while a peer may read it
     } else if (CL == 2) {
         cluster_sync();              // no CTA leaves while its peer may still signal it or copy into it
@@ -1583,6 +1644,10 @@ cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
         if (!L.args.c_wide) return cudaErrorInvalidValue;
         return L.seg ? launch_xent<XENT_GRAD, true>(L, st) : launch_xent<XENT_GRAD, false>(L, st);
     }
+    if (L.xent == XENT_PRODUCT && L.csplit && L.args.fold > 0 && !L.seg)
+        return L.cg == 1 && L.bn == 128 ? launch_product<128, 1, false, true>(L, st)
+               : L.cg == 1 && L.bn == 64 ? launch_product<64, 1, false, true>(L, st)
+                                         : cudaErrorInvalidValue;
     if (L.xent == XENT_PRODUCT && L.seg) {
         if (L.csplit) return L.cg == 1 && L.bn == 128 ? launch_product<128, 1, true, true>(L, st)
                              : L.cg == 1 && L.bn == 64 ? launch_product<64, 1, true, true>(L, st)

@@ -13,6 +13,7 @@
 #include "elem.cuh"
 #include "internal.h"
 #include "ptx.cuh"
+#include "xent.cuh"
 #include "../../include/tcgemm.h"
 
 namespace tc {
@@ -20,12 +21,6 @@ namespace {
 
 constexpr int JOIN_THREADS = 256;
 constexpr float LN2 = 0.6931471805599453f;
-
-__device__ __forceinline__ bool counts(const void *targets, int wide, int vocab, long long row, long long &y)
-{
-    y = wide ? static_cast<const long long *>(targets)[row] : (long long)static_cast<const int *>(targets)[row];
-    return y >= 0 && y < vocab;
-}
 
 // (m, s) <- the statistics of both: s 2^m + t 2^n = (..) 2^max(m, n)
 __device__ __forceinline__ void merge(float &m, float &s, float n, float t)
@@ -100,7 +95,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const XentJoinArgs a
     if (q == 0 && in) {
         const float lse = (m + log2f(s)) * LN2;
         long long y;
-        counted = counts(a.targets, a.wide, a.vocab, row, y);
+        counted = xent_counts(a.targets, a.wide, a.vocab, row, y);
         loss = counted ? lse - a.at[row] + a.z * lse * lse : 0.0f;
         a.lse[row] = lse;
         if (a.reduction == TC_REDUCE_NONE)
@@ -129,7 +124,7 @@ __global__ void __launch_bounds__(1024) total_kernel(const XentJoinArgs a)
     for (int row = threadIdx.x; row < a.T; row += 1024) {
         long long y;
         sum += (double)a.rows[row];
-        n += counts(a.targets, a.wide, a.vocab, row, y) ? 1 : 0;
+        n += xent_counts(a.targets, a.wide, a.vocab, row, y) ? 1 : 0;
     }
     sum = block_sum(sum, sums);
     n = block_sum(n, ns);
@@ -138,60 +133,30 @@ __global__ void __launch_bounds__(1024) total_kernel(const XentJoinArgs a)
 
 constexpr int PREP_THREADS = 1024;
 
-// Block 0 makes the rows' factors, the others copy X (8 elements a thread and
-// turn), zeros for the rows that do not count: what such a row holds, a NaN
-// among it, must not reach dW, whose products run over the rows.
+// Block 0 makes the rows' factors, the others copy X.
 __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const XentPrepArgs a)
 {
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x > 0) {
-        const long long per = a.ld_clean / 8, all = per * a.T;
-        const bool whole = (reinterpret_cast<uintptr_t>(a.X) & 15u) == 0 && a.ldx % 8 == 0;
-        for (long long i = (long long)(blockIdx.x - 1) * PREP_THREADS + threadIdx.x; i < all;
-             i += (long long)(gridDim.x - 1) * PREP_THREADS) {
-            const long long row = i / per, col = (i - row * per) * 8;
-            long long y;
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (counts(a.targets, a.wide, a.vocab, row, y)) {
-                const uint16_t *src = a.X + row * a.ldx + col;
-                if (whole && col + 8 <= a.H) {
-                    w = *reinterpret_cast<const uint4 *>(src);
-                } else {
-                    uint32_t h[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) h[j] = col + j < a.H ? src[j] : 0u;
-                    w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-                }
-            }
-            for (int k = 0; k < a.copies; ++k) *reinterpret_cast<uint4 *>(a.clean + (k * (long long)a.T + row) * a.ld_clean + col) = w;
-        }
+        xent_copy(a, (long long)(blockIdx.x - 1) * PREP_THREADS + threadIdx.x, (long long)(gridDim.x - 1) * PREP_THREADS);
         return;
     }
     __shared__ int ns[32];
     __shared__ float tops[32];
-    long long y;
-    float scale = 1.0f;
+    float mean = 1.0f;
     if (a.reduction == TC_REDUCE_MEAN) {
         int n = 0;
-        for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) n += counts(a.targets, a.wide, a.vocab, t, y) ? 1 : 0;
+        for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) n += xent_counts(a, t) ? 1 : 0;
         n = block_sum(n, ns);
-        scale = 1.0f / (float)max(n, 1);
+        mean = 1.0f / (float)max(n, 1);
     }
-    auto factors = [&](int t, float &cp, float &cy) {
-        cp = cy = 0.0f;
-        if (!counts(a.targets, a.wide, a.vocab, t, y)) return;
-        cy = a.grad[a.reduction == TC_REDUCE_NONE ? t : 0] * scale;
-        cp = a.z != 0.0f ? cy * (1.0f + 2.0f * a.z * a.lse[t]) : cy;
-    };
     float power = 1.0f;
     if (a.unscale) {
-        // f16 spans 2^-24 to 2^16: probabilities far below one times a small
-        // gradient would be lost, so G is held as a multiple of it
         float top = 0.0f;
         for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) {
             float cp, cy;
-            factors(t, cp, cy);
+            xent_factors(a, t, mean, cp, cy);
             top = fmaxf(top, fmaxf(fabsf(cp), fabsf(cy)));
         }
 #pragma unroll
@@ -199,17 +164,12 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const XentPrepArgs a
         if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
         __syncthreads();
         for (int w = 0; w < 32; ++w) top = fmaxf(top, tops[w]);
-        // top = f 2^e with f in [1/2, 1); the inverse stays a normal number
-        int e;
-        if (top > 0.0f && top < INFINITY) {
-            frexpf(top, &e);
-            power = ldexpf(1.0f, min(14 - e, 126));
-        }
+        power = xent_power(top);
         for (int h = threadIdx.x; h < a.H; h += PREP_THREADS) a.unscale[h] = 1.0f / power;
     }
     for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) {
         float cp, cy;
-        factors(t, cp, cy);
+        xent_factors(a, t, mean, cp, cy);
         a.cp[t] = cp * power;
         a.cy[t] = cy * power;
     }

@@ -1,0 +1,69 @@
+// What the kernels of the softmax cross entropy share: which rows count, the
+// factors of a row's gradient, and the copy of X that the gradient of W is made
+// with.
+#pragma once
+#include "elem.cuh"
+#include "internal.h"
+
+namespace tc {
+
+// Row's target y, and whether the row counts.
+__device__ __forceinline__ bool xent_counts(const void *targets, int wide, int vocab, long long row, long long &y)
+{
+    y = wide ? static_cast<const long long *>(targets)[row] : (long long)static_cast<const int *>(targets)[row];
+    return y >= 0 && y < vocab;
+}
+__device__ __forceinline__ bool xent_counts(const XentPrepArgs &a, long long row)
+{
+    long long y;
+    return xent_counts(a.targets, a.wide, a.vocab, row, y);
+}
+
+// The gradient of row t's logits is cp p - cy [target]; mean: 1 / (rows that
+// count) for a mean, else 1.
+__device__ __forceinline__ void xent_factors(const XentPrepArgs &a, int t, float mean, float &cp, float &cy)
+{
+    cp = cy = 0.0f;
+    if (!xent_counts(a, t)) return;
+    cy = a.grad[a.reduction == TC_REDUCE_NONE ? t : 0] * mean;
+    cp = a.z != 0.0f ? cy * (1.0f + 2.0f * a.z * a.lse[t]) : cy;
+}
+
+// The power of two that puts the largest factor between 2^13 and 2^14.  f16 spans
+// 2^-24 to 2^16: probabilities far below one times a small gradient would be
+// lost, so G is held as a multiple of it.  The inverse stays a normal number.
+__device__ __forceinline__ float xent_power(float top)
+{
+    int e;
+    if (!(top > 0.0f && top < INFINITY)) return 1.0f;
+    frexpf(top, &e);
+    return ldexpf(1.0f, min(14 - e, 126));
+}
+
+// Thread `i` of `n`: X to a.clean, 8 elements a turn, zeros for the rows that do
+// not count: what such a row holds, a NaN among it, must not reach dW, whose
+// products run over the rows.
+__device__ __forceinline__ void xent_copy(const XentPrepArgs &a, long long i, long long n)
+{
+    const long long per = a.ld_clean / 8, all = per * a.T;
+    const bool whole = (reinterpret_cast<uintptr_t>(a.X) & 15u) == 0 && a.ldx % 8 == 0;
+    for (; i < all; i += n) {
+        const long long row = i / per, col = (i - row * per) * 8;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (xent_counts(a, row)) {
+            const uint16_t *src = a.X + row * a.ldx + col;
+            if (whole && col + 8 <= a.H) {
+                w = *reinterpret_cast<const uint4 *>(src);
+            } else {
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) h[j] = col + j < a.H ? src[j] : 0u;
+                w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+            }
+        }
+        for (int k = 0; k < a.copies; ++k)
+            *reinterpret_cast<uint4 *>(a.clean + (k * (long long)a.T + row) * a.ld_clean + col) = w;
+    }
+}
+
+}  // namespace tc
