@@ -1632,15 +1632,16 @@ bool plan_q4_gemv(tc_ctx *ctx, tc_stream *s, const Q4GemmArgs &a, const Force &f
                                    16 + 16 * p->tall, gp, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-// The stream's words that kernels leave at 0: those of the grid barriers,
-// then the counts of the cut tiles of the 4-bit product.
+// The stream's words that kernels leave at 0: those of the grid barriers (the
+// first) and the cross entropy's count of blocks (the last), then the counts of
+// the cut tiles of the 4-bit product.
 constexpr size_t SYNC_WORDS = 64;
 
-// Memory of a 4-bit call that needs `ws` and `rx` bytes and the words above:
+// Memory of a call that needs `ws` and `rx` bytes and the words above:
 // taken before anything of the call is launched.  A call under stream capture
 // must find all of it there: what it allocated would be the graph's, and the
 // clearing a node of the graph, while later calls outside relied on both.
-tc_status_t reserve_q4(tc_ctx *ctx, tc_stream *s, size_t ws, size_t rx)
+tc_status_t reserve_words(tc_ctx *ctx, tc_stream *s, size_t ws, size_t rx)
 {
     if (ws <= s->ws_cap && rx <= s->rx_cap && s->sync && s->sync_clear) return TC_OK;
     cudaStreamCaptureStatus capture;
@@ -1735,7 +1736,7 @@ tc_status_t enqueue_q4_mma(tc_ctx *ctx, tc_stream *s, Q4GemmArgs a, const Force 
     const int64_t ld = cdiv(a.q.K, 64) * 64;
     // every call keeps what a cut of the last tiles needs (two tiles for each
     // SM), so that a larger call, which may need no cut, stands for a smaller
-    const tc_status_t st = reserve_q4(ctx, s, (size_t)2 * ctx->num_sms * 128 * Q4_MMA_ROWS * 4, pack ? (size_t)(a.M * ld * 2) : 0);
+    const tc_status_t st = reserve_words(ctx, s, (size_t)2 * ctx->num_sms * 128 * Q4_MMA_ROWS * 4, pack ? (size_t)(a.M * ld * 2) : 0);
     if (st != TC_OK) return st;
     if (pack) {
         PackBatch pb;
@@ -1902,7 +1903,7 @@ tc_status_t run_moe(tc_ctx *ctx, const tc_moe_desc *d, const void *X, const void
                               : encode_q4(ctx, &m.z1, u8, a.w1.zeros, a.w1.N, g1, a.w1.lds, Q4_ZERO_BOX, gp, plain));
     if (a.w2.zeros) enc = enc && encode_q4(ctx, &m.z2, u8, a.w2.zeros, a.w2.N, g2, a.w2.lds, 16 + rows2, gp, plain);
     if (!enc) return TC_ERR_CUDA;
-    if ((st = reserve_q4(ctx, s, lb + hb, 0)) != TC_OK) return st;
+    if ((st = reserve_words(ctx, s, lb + hb, 0)) != TC_OK) return st;
     a.logits = static_cast<float *>(s->ws);
     a.h = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(s->ws) + lb);
     a.sync = s->sync;
@@ -2119,8 +2120,24 @@ tc_status_t run_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const vo
     const int64_t nparts = 2 * cdiv(V, first.bn);      // pieces are whole tiles, but for the last
     const size_t o_part = c.take(nparts * T * (int64_t)sizeof(float2)), o_at = c.take(T * 4), o_rows = c.take(T * 4);
     const size_t o_x = c.take(pack_x ? T * ldp * 2 : 0), o_w = c.take(pack_w ? cols * ldp * 2 : 0);
-    if ((st = reserve(s, 256, c.at)) != TC_OK) return st;
+    if ((st = reserve_words(ctx, s, 256, c.at)) != TC_OK) return st;
     uint8_t *rx = static_cast<uint8_t *>(s->rx);
+    XentJoinArgs j{};
+    j.part = reinterpret_cast<const float2 *>(rx + o_part);
+    j.at = reinterpret_cast<const float *>(rx + o_at);
+    j.targets = targets;
+    j.wide = d->target_dtype == TC_I64;
+    j.vocab = d->vocab;
+    j.T = d->tokens;
+    j.nparts = (int)nparts;
+    j.reduction = d->reduction;
+    j.z = d->z_weight;
+    j.loss = loss;
+    j.lse = lse;
+    j.rows = reinterpret_cast<float *>(rx + o_rows);
+    j.ticket = s->sync + SYNC_WORDS - 1;
+    const std::string name = "xent_loss_" + first.name + (pack_x ? "_packX" : "") + (pack_w ? "_packW" : "") + "_p" +
+                             std::to_string(cdiv(V, cols));
     for (int64_t v0 = 0; v0 < V; v0 += cols) {
         const int64_t N = std::min(cols, V - v0);
         const void *Wv = static_cast<const uint16_t *>(W) + v0 * n.ldw;
@@ -2156,24 +2173,10 @@ tc_status_t run_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const vo
         job.epi.at = reinterpret_cast<float *>(rx + o_at);
         if ((st = enqueue(ctx, &gd, gn, p, Xv, Wv, rx + o_rows, s, nullptr, nullptr, false, &job)) != TC_OK) return st;
     }
-    XentJoinArgs j{};
-    j.part = reinterpret_cast<const float2 *>(rx + o_part);
-    j.at = reinterpret_cast<const float *>(rx + o_at);
-    j.targets = targets;
-    j.wide = d->target_dtype == TC_I64;
-    j.vocab = d->vocab;
-    j.T = d->tokens;
-    j.nparts = (int)nparts;
-    j.reduction = d->reduction;
-    j.z = d->z_weight;
-    j.loss = loss;
-    j.lse = lse;
-    j.rows = reinterpret_cast<float *>(rx + o_rows);
     int launches = 0;
     if (launch_xent_join(j, s->st, &launches) != cudaSuccess) return TC_ERR_CUDA;
     ctx->launches += launches;
-    ctx->last = "xent_loss_" + first.name + (pack_x ? "_packX" : "") + (pack_w ? "_packW" : "") + "_p" +
-                std::to_string(cdiv(V, cols));
+    ctx->last = name;
     return TC_OK;
 }
 

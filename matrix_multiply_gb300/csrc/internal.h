@@ -397,8 +397,9 @@ struct XentJoinArgs {
     float z;
     float *loss, *lse;
     float *rows;           // scratch: the rows' losses of a reduced one, T floats
+    unsigned *ticket;      // counts blocks, 0 before and after a launch
 };
-// one launch, or two for the reduced loss of more rows than a block joins
+// one launch, or two for the reduced loss of very many rows
 cudaError_t launch_xent_join(const XentJoinArgs &a, cudaStream_t st, int *launches);
 
 cudaError_t launch_xent_prep(const XentPrepArgs &a, cudaStream_t st);

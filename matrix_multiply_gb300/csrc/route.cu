@@ -248,8 +248,8 @@ __device__ __forceinline__ double warp_sum(double v)
     return v;
 }
 
-// Adds the blocks' rows up, in a fixed order.  A cluster of 8 blocks shares the
-// columns (and every block takes the last one, of lse^2 and the tokens); a
+// Adds the blocks' rows up, in a fixed order.  A cluster of 8 blocks (one for up
+// to 64 experts) shares the columns (and every block takes the last one, of lse^2 and the tokens); a
 // block's 32 warps take every 32nd row, so that 5 loads a thread, all in flight,
 // read the rows of 152 blocks once; the warps' sums meet in shared memory in 64
 // bits, the blocks' shares of the balance loss in the first one's.  (One block
@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(1024) finish_kernel(const RouteArgs a, int blo
     __shared__ double share;
     griddep_wait();
     griddep_launch_dependents();
-    const int n1 = a.E + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per = (a.E + FINISH_BLOCKS - 1) / FINISH_BLOCKS, first = min((int)blockIdx.x * per, a.E);
+    const int n1 = a.E + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grid = (int)gridDim.x;
+    const int per = (a.E + grid - 1) / grid, first = min((int)blockIdx.x * per, a.E);
     const int own = min(per, a.E - first);
     for (int c = lane; c <= own; c += 32) {
         const int e = c < own ? first + c : a.E;
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(1024) finish_kernel(const RouteArgs a, int blo
     cluster_sync();
     if (blockIdx.x == 0 && warp == 0) {
         double b = 0.0;
-        if (lane < FINISH_BLOCKS) b = ld_shared_cluster_f64(mapa_shared(smem_u32(&share), (uint32_t)lane));
+        if (lane < grid) b = ld_shared_cluster_f64(mapa_shared(smem_u32(&share), (uint32_t)lane));
         b = warp_sum(b);
         if (lane == 0) write_losses(a, b, sums[own], ns[own]);
     }
@@ -585,7 +585,8 @@ cudaError_t launch_route(const RouteArgs &a, int blocks, cudaStream_t st, int *l
                                 1u, a);
     });
     if (e != cudaSuccess || blocks == 1) return e;
-    return launch_dependent(finish_kernel, dim3(FINISH_BLOCKS), dim3(1024), 0, st, (unsigned)FINISH_BLOCKS, a, blocks);
+    const unsigned n = a.E < FINISH_COLUMNS ? 1u : (unsigned)FINISH_BLOCKS;
+    return launch_dependent(finish_kernel, dim3(n), dim3(1024), 0, st, n, a, blocks);
 }
 
 cudaError_t launch_route_grad(const RouteGradArgs &a, int num_sms, cudaStream_t st)
