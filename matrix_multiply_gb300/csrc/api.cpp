@@ -865,7 +865,7 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     a.fold = p.fold;
     if (xent) {
         L.xent = xent->mode;
-        a.x = xent->epi;
+        L.x = xent->epi;
         a.c_tma = xent->mode == XENT_GRAD;
     }
     a.c_wide = a.c_tma && d->c_dtype != TC_F32 && (xent || (p.product && !p.csplit && p.bn % 128 == 0 && d->beta == 0.0f));

@@ -201,7 +201,6 @@ struct MmaArgs {
     // bytes; the tile's other rows hold stale data, which reaches only
     // output rows beyond M (never stored)
     int a_short_bytes;
-    XentEpi x;
 };
 
 // XENT_LOSS writes no C, XENT_GRAD writes G (16-bit, wide stores, whole-K tiles
@@ -222,6 +221,7 @@ struct MmaLaunch {
     int xent;
     CUtensorMap tmA, tmB, tmC, tmW;   // A, B, C and the split-K workspace
     MmaArgs args;
+    XentEpi x;   // XENT_LOSS and XENT_GRAD
 };
 
 cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st);

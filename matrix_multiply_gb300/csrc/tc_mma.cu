@@ -108,6 +108,12 @@ struct NoTable {
 };
 template <bool GROUPED>
 using TableOf = std::conditional_t<GROUPED, GroupTable, NoTable>;
+// The same of a cross entropy's epilogue.
+struct NoXent {
+    int none;
+};
+template <int XENT>
+using XentOf = std::conditional_t<XENT == XENT_LOSS || XENT == XENT_GRAD, XentEpi, NoXent>;
 
 // Linear tile id -> (batch entry, tile row, tile column): bands of group_m
 // tile rows, column-major inside a band.
@@ -632,8 +638,8 @@ __device__ __forceinline__ int xent_target(const XentEpi &x, long long row, int 
 // multiply-adds, exponentials and additions per chunk and one rescaling of s.
 // Sums are fp32: at most 2^15 terms of at most 1 meet in a half tile's partial
 // sum, and the partial sums of a row are joined pairwise.
-__device__ __forceinline__ void xent_statistics(const MmaArgs &a, long long col0, const float (&v)[32], float &m,
-                                                float &s)
+__device__ __forceinline__ void xent_statistics(const MmaArgs &a, float k2, long long col0, const float (&v)[32],
+                                                float &m, float &s)
 {
     float big[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     const int n = (int)min((long long)32, a.N - col0);
@@ -644,17 +650,17 @@ __device__ __forceinline__ void xent_statistics(const MmaArgs &a, long long col0
 #pragma unroll
         for (int j = 0; j < 32; ++j) big[j & 3] = fmaxf(big[j & 3], j < n ? v[j] : -INFINITY);
     }
-    const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * a.x.k2;
+    const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * k2;
     const float next = fmaxf(m, top);
     const float base = next == -INFINITY ? 0.0f : next;     // only -inf so far: 2^(-inf - 0) = 0
     float sum[4] = {s * exp2_approx(m - base), 0.0f, 0.0f, 0.0f};
     if (n == 32) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sum[j & 3] += exp2_approx(fmaf(v[j], a.x.k2, -base));
+        for (int j = 0; j < 32; ++j) sum[j & 3] += exp2_approx(fmaf(v[j], k2, -base));
     } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            if (j < n) sum[j & 3] += exp2_approx(fmaf(v[j], a.x.k2, -base));
+            if (j < n) sum[j & 3] += exp2_approx(fmaf(v[j], k2, -base));
     }
     s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
     m = next;
@@ -714,7 +720,7 @@ template <int BN, int CG, bool GROUPED, bool EPI, bool I8ACC = false, bool CSPLI
 __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     mma_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmW,
-               const MmaArgs args, const __grid_constant__ TableOf<GROUPED> gt)
+               const MmaArgs args, const __grid_constant__ TableOf<GROUPED> gt, const __grid_constant__ XentOf<XENT> xa)
 {
     constexpr int BNL = BN / CG;                   // B columns loaded by this CTA
     constexpr int STAGE = stage_bytes(BN, CG);
@@ -791,7 +797,9 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             prefetch_tmap(&tmA);
             prefetch_tmap(&tmB);
             if (args.c_tma) prefetch_tmap(&tmC);
-            if (args.ws || (XENT == XENT_GRAD && args.x.two)) prefetch_tmap(&tmW);
+            if (args.ws) prefetch_tmap(&tmW);
+            if constexpr (XENT == XENT_GRAD)
+                if (xa.two) prefetch_tmap(&tmW);
         }
         // let the next kernel in the stream (the split-K reduction, or the
         // next GEMM) launch early; it waits for this grid to finish before
@@ -1015,10 +1023,13 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
         const int row_in_tile = (int)rank * BM + quarter * 32 + lane;
         constexpr int EBUFS = epi_bufs(BN, CG, WIDE);
         constexpr int LAST_C0 = CHUNKS - CSTEP;        // this warp's last chunk: LAST_C0 + chunk0
-        // the warp's i-th chunk
+        // the warp's i-th chunk, and its chunks one after the other
         const auto chunk_of = [&](int i) {
             return WIDE64 ? 2 * (chunk0 + (i >> 1) * CSTEP) + (i & 1) : chunk0 + i * CSTEP;
         };
+        const int first_c = WIDE64 ? 2 * chunk0 : chunk0;
+        const int last_c = WIDE64 ? CHUNKS - 2 * CSTEP + 2 * chunk0 + 1 : LAST_C0 + chunk0;
+        const auto next_c = [](int c) { return WIDE64 ? (c & 1 ? c + 2 * CSTEP - 1 : c + 1) : c + CSTEP; };
         static_assert(CHUNKS % CSTEP == 0, "chunks split evenly between the warps of a lane quarter");
         uint8_t *my_stage = cstage + warp * epi_warp_bytes(BN, CG, WIDE);
         // The warp's staging is either its TMA chunk buffers (two that
@@ -1073,10 +1084,9 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
         };
         // few rows: their factors' common parts, by every warp for itself
         float mean = 1.0f, power = 1.0f;
-        const bool own_prep = XENT == XENT_GRAD && args.x.own_prep;
         if constexpr (XENT == XENT_GRAD) {
-            if (own_prep) {
-                const XentPrepArgs &q = args.x.prep;
+            if (xa.own_prep) {
+                const XentPrepArgs &q = xa.prep;
                 if (q.reduction == TC_REDUCE_MEAN) {
                     int n = 0;
                     for (int t = lane; t < q.T; t += 32) n += xent_counts(q, t) ? 1 : 0;
@@ -1129,22 +1139,25 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             float rowlse = 0.0f, cp = 0.0f, cy = 0.0f;
             if constexpr (XENT == XENT_LOSS || XENT == XENT_GRAD) {
                 const long long row = (long long)w.tm * (BM * CL) + row_in_tile;
-                target = xent_target(args.x, row, args.M);
-                if (XENT == XENT_GRAD && row < args.M) {
-                    if (own_prep) {
-                        xent_factors(args.x.prep, (int)row, mean, cp, cy);
+                target = xent_target(xa, row, args.M);
+            }
+            if constexpr (XENT == XENT_GRAD) {
+                const long long row = (long long)w.tm * (BM * CL) + row_in_tile;
+                if (row < args.M) {
+                    if (xa.own_prep) {
+                        xent_factors(xa.prep, (int)row, mean, cp, cy);
                         cp *= power;
                         cy *= power;
                     } else {
-                        cp = args.x.cp[row];
-                        cy = args.x.cy[row];
+                        cp = xa.cp[row];
+                        cy = xa.cy[row];
                     }
-                    rowlse = args.x.lse[row] * 1.4426950408889634f;
+                    rowlse = xa.lse[row] * 1.4426950408889634f;
                 }
             }
 #pragma unroll
             for (int i = 0; i < NCH; ++i)
-                bpre[i] = EPI && (XENT == XENT_NONE || XENT == XENT_PRODUCT) ? bias_of(ea, lane, (long long)w.tn * BN + chunk_of(i) * 32) : 0.0f;
+                bpre[i] = EPI && XENT == XENT_NONE ? bias_of(ea, lane, (long long)w.tn * BN + (chunk0 + i * CSTEP) * 32) : 0.0f;
             // segments of the unit (see the MMA warp): one, or the K slices
             // that I8ACC adds up in TMEM, SEG in registers
             const int nseg = I8ACC || SEG ? (w.kb1 - w.kb0 + args.slice_kb - 1) / args.slice_kb : 1;
@@ -1202,18 +1215,18 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         if (XENT != XENT_LOSS) tmem_st_wait();
                     }
                 }
-                // the i-th of this warp's chunks of the accumulator, which goes
-                // back to the MMA warp with the last
-                auto fetch = [&](int i, float (&v)[32]) {
+                // chunk c of the accumulator, which goes back to the MMA warp with
+                // this warp's last
+                auto fetch = [&](int c, float (&v)[32]) {
                     uint32_t r[32];
                     __syncwarp();
-                    tmem_ld_32x32b_x32(taddr + chunk_of(i) * 32, r);
+                    tmem_ld_32x32b_x32(taddr + c * 32, r);
                     tmem_ld_wait();
-                    if (i == NCH - 1) release();
+                    if (c == last_c) release();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
                 };
-                // the i-th and the next, 64 columns side by side
+                // this warp's i-th chunk and the next, 64 columns side by side
                 auto fetch2 = [&](int i, float (&v)[2][32]) {
                     uint32_t r[2][32];
                     __syncwarp();
@@ -1268,10 +1281,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         // the target's column of this chunk, in few warps' chunks
                         const int hit = target - (int)col0;
                         const bool here = hit >= 0 && hit < 32 && col0 + hit < args.N;
-                        if (__any_sync(0xffffffffu, here) && here) args.x.at[row] = pick(v, hit) * args.alpha;
-                        xent_statistics(args, col0, v, m, s);
+                        if (__any_sync(0xffffffffu, here) && here) xa.at[row] = pick(v, hit) * args.alpha;
+                        xent_statistics(args, xa.k2, col0, v, m, s);
                     }
-                    if (row < args.M) args.x.part[(2LL * w.tn + chunk0) * args.M + row] = make_float2(m, s);
+                    if (row < args.M) xa.part[(2LL * w.tn + chunk0) * args.M + row] = make_float2(m, s);
                 } else if constexpr (XENT == XENT_GRAD) {
 #pragma unroll 1
                     for (int i = 0; i < NCH; i += 2) {
@@ -1284,7 +1297,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[h][j] = cp * exp2_approx(fmaf(v[h][j], args.x.k2, -rowlse));
+                            for (int j = 0; j < 32; ++j) v[h][j] = cp * exp2_approx(fmaf(v[h][j], xa.k2, -rowlse));
                             if (any) {
 #pragma unroll
                                 for (int j = 0; j < 32; ++j) v[h][j] -= 32 * h + j == hit ? cy : 0.0f;
@@ -1297,7 +1310,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         free_wide(lane);
                         fill_wide(args.c_dtype, my_stage, lane, 1.0f, v);
                         store_wide(&tmC, my_stage, lane, row0, col0);
-                        if (args.x.two) {
+                        if (xa.two) {
                             // what the rounding left, rounded in turn
                             left_over(args.c_dtype, v);
                             free_wide(lane);
@@ -1321,10 +1334,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                 } else if (XENT == XENT_PRODUCT && w.S == 1 && args.c_tma && args.c_dtype == TC_F32 && args.beta == 0.0f) {
                     const float scale = args.col_scale ? args.alpha * args.col_scale[0] : args.alpha;
 #pragma unroll 1
-                    for (int i = 0; i < NCH; ++i) {
+                    for (int c = first_c; c < CHUNKS; c = next_c(c)) {
                         float v[32];
-                        fetch(i, v);
-                        const long long col0 = (long long)w.tn * BN + chunk_of(i) * 32, row0 = row - lane;
+                        fetch(c, v);
+                        const long long col0 = (long long)w.tn * BN + c * 32, row0 = row - lane;
                         if (col0 >= args.N || row0 >= args.M) continue;      // (the whole warp)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] *= scale;
@@ -1332,10 +1345,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     }
                 } else if (w.S == 1) {
 #pragma unroll 1
-                    for (int i = 0; i < NCH; ++i) {
+                    for (int c = first_c; c < CHUNKS; c = next_c(c)) {
                         float v[32];
-                        fetch(i, v);
-                        emit(w.b, row, (long long)w.tn * BN + chunk_of(i) * 32, v, pick(bpre, i));
+                        fetch(c, v);
+                        emit(w.b, row, (long long)w.tn * BN + c * 32, v, WIDE64 ? 0.0f : pick(bpre, (c - chunk0) / CSTEP));
                     }
                 } else if constexpr (CSPLIT) {
                     // K slice of a cluster split: the partial tile goes to this
@@ -1344,10 +1357,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     // accumulator's commit).  csplit_reduce adds the slices.
                     float *red = reinterpret_cast<float *>(smem) + (quarter * 32 + lane) * csplit_ld<BN>();
 #pragma unroll 1
-                    for (int i = 0; i < NCH; ++i) {
+                    for (int c = first_c; c < CHUNKS; c = next_c(c)) {
                         float v[32];
-                        fetch(i, v);
-                        float4 *dst = reinterpret_cast<float4 *>(red + chunk_of(i) * 32);
+                        fetch(c, v);
+                        float4 *dst = reinterpret_cast<float4 *>(red + c * 32);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) dst[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
                     }
@@ -1358,10 +1371,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     const long long wrow0 =
                         (long long)(w.ufirst + w.s - args.split_base) * (BM * CG) + (int)rank * BM + quarter * 32;
 #pragma unroll 1
-                    for (int i = 0; i < NCH; ++i) {
+                    for (int c = first_c; c < CHUNKS; c = next_c(c)) {
                         float v[32];
-                        fetch(i, v);
-                        store_tma<EBUFS>(&tmW, false, TC_F32, staging(STG_TMA), lane, 0, wrow0, chunk_of(i) * 32, v);
+                        fetch(c, v);
+                        store_tma<EBUFS>(&tmW, false, TC_F32, staging(STG_TMA), lane, 0, wrow0, c * 32, v);
                     }
                 }
             }
@@ -1392,6 +1405,15 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     }
 }
 
+template <int XENT>
+XentOf<XENT> xent_of(const MmaLaunch &L)
+{
+    if constexpr (XENT == XENT_LOSS || XENT == XENT_GRAD)
+        return L.x;
+    else
+        return NoXent{0};
+}
+
 template <int BN, int CG, bool GROUPED = false, bool EPI = false, bool I8ACC = false, bool CSPLIT = false,
           int XENT = XENT_NONE, bool SEG = false>
 cudaError_t launch_kernel(const MmaLaunch &L, cudaStream_t st, const TableOf<GROUPED> &gt = TableOf<GROUPED>{})
@@ -1420,7 +1442,7 @@ cudaError_t launch_kernel(const MmaLaunch &L, cudaStream_t st, const TableOf<GRO
     if (CSPLIT && (cluster < 2 || cluster > 16 || L.grid != L.args.total_units || L.grid % cluster != 0))
         return cudaErrorInvalidValue;
     return launch_dependent(kern, dim3(L.grid), dim3(threads), smem, st, (unsigned)cluster, L.tmA, L.tmB, L.tmC,
-                            L.tmW, L.args, gt);
+                            L.tmW, L.args, gt, xent_of<XENT>(L));
 }
 
 // Clusters of S CTAs of the BN-wide cluster-split kernel that can be
