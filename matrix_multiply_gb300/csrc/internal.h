@@ -192,8 +192,8 @@ struct MmaArgs {
     const void *bias;
     int act;
     const float *col_scale;
-    // XENT_PRODUCT in a cluster split of one tile row: C has `fold` rows, the sums
-    // of rows r and fold + r of the product (0: not)
+    // XENT_FOLD, one tile row: C has `fold` rows, the sums of rows r and fold + r of
+    // the product
     int fold;
     int slice_kb;          // K blocks per slice of an accumulator cut along K (int8, cross entropy, MmaLaunch::seg)
     // one-CTA tiles over fewer than BM rows of a K-major A: its copies carry
@@ -206,8 +206,9 @@ struct MmaArgs {
 // XENT_LOSS writes no C, XENT_GRAD writes G (16-bit, wide stores, whole-K tiles
 // of 256 or 128 columns like XENT_LOSS); XENT_PRODUCT is one of the gradients'
 // products with G, its 16-bit C in wide stores too (tiles of 256 or 128 columns;
-// beta 0, a col_scale the same for all columns)
-enum XentMode { XENT_NONE = 0, XENT_LOSS = 1, XENT_GRAD = 2, XENT_PRODUCT = 3 };
+// beta 0, a col_scale the same for all columns); XENT_FOLD the same as a cluster
+// split that adds pairs of rows (MmaArgs::fold)
+enum XentMode { XENT_NONE = 0, XENT_LOSS = 1, XENT_GRAD = 2, XENT_PRODUCT = 3, XENT_FOLD = 4 };
 struct MmaLaunch {
     int bn;
     int cg;      // CTAs per tile: 1, or 2 for a CTA pair (cluster of two)

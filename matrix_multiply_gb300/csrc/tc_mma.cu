@@ -571,7 +571,7 @@ __device__ __forceinline__ void finish4(const MmaArgs &a, int b, long long grow,
 // CTA of rank r sums rows [r * ceil(BM/S), ...) of all S partial tiles,
 // reading its peers' shared memory in slice order (deterministic), and
 // writes those rows of C.  Every thread of the CTA takes part.
-// FOLD: with a.fold set, its rows are sums of two rows of the product.
+// FOLD: its a.fold rows are sums of two rows of the product.
 template <int BN, bool EPI, bool FOLD>
 __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *partial)
 {
@@ -580,8 +580,7 @@ __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *p
     constexpr int SMAX = 16;
     const int S = a.seg0_split;
     const uint32_t rank = cluster_ctarank();
-    const bool fold = FOLD && a.fold > 0;
-    const int all = fold ? a.fold : BM, rows = (all + S - 1) / S;
+    const int all = FOLD ? a.fold : BM, rows = (all + S - 1) / S;
     const int r0 = min(all, (int)rank * rows), r1 = min(all, r0 + rows);
     const Unit w = decode_unit(a, (int)blockIdx.x);
     const uint32_t base = smem_u32(partial);
@@ -604,7 +603,7 @@ __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *p
                 v[3] += p[q].w;
             }
         }
-        if (fold) {
+        if constexpr (FOLD) {
             const uint32_t more = off + (uint32_t)(a.fold * LD * 4);
 #pragma unroll
             for (int q = 0; q < SMAX; ++q)
@@ -740,7 +739,8 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     static_assert(!CSPLIT || (CG == 1 && !GROUPED && !I8ACC), "cluster split-K: one CTA per slice");
     static_assert(!SEG || (EW == 8 && !GROUPED && !I8ACC), "segments: at most 128 sums in a thread's registers");
     static_assert(XENT != XENT_LOSS || SEG, "a row's statistics are taken from registers");
-    static_assert(XENT == XENT_NONE || XENT == XENT_PRODUCT || (EPI && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
+    static_assert(XENT != XENT_FOLD || CSPLIT, "rows are added where the slices are");
+    static_assert(XENT == XENT_NONE || XENT >= XENT_PRODUCT || (EPI && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
     static_assert(!CSPLIT || BM * csplit_ld<BN>() * 4 <= S * STAGE, "the partial tile fits in the idle ring");
     constexpr int CHUNKS = BN / 32;
     // 16-bit C in stores of 64 columns: a warp's chunks then come in pairs of
@@ -1391,7 +1391,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     __syncthreads();
     if constexpr (CSPLIT) {
         cluster_sync();              // every slice's partial tile is in its CTA's shared memory
-        csplit_reduce<BN, EPI, XENT == XENT_PRODUCT>(args, smem);
+        csplit_reduce<BN, EPI, XENT == XENT_FOLD>(args, smem);
         cluster_sync();              // no CTA releases its shared memory while a peer may read it
     } else if (CL == 2) {
         cluster_sync();              // no CTA leaves while its peer may still signal it or copy into it
@@ -1652,10 +1652,17 @@ cudaError_t launch_xent(const MmaLaunch &L, cudaStream_t st)
 }
 
 // One of the gradients' products; SEG: sums cut along K.
-template <int BN, int CG, bool SEG, bool CSPLIT = false>
+template <int BN, int CG, bool SEG>
 cudaError_t launch_product(const MmaLaunch &L, cudaStream_t st)
 {
-    return launch_kernel<BN, CG, false, true, false, CSPLIT, XENT_PRODUCT, SEG>(L, st);
+    return launch_kernel<BN, CG, false, true, false, false, XENT_PRODUCT, SEG>(L, st);
+}
+template <int XENT, bool SEG>
+cudaError_t launch_product_split(const MmaLaunch &L, cudaStream_t st)
+{
+    if (L.cg == 1 && L.bn == 128) return launch_kernel<128, 1, false, true, false, true, XENT, SEG>(L, st);
+    if (L.cg == 1 && L.bn == 64) return launch_kernel<64, 1, false, true, false, true, XENT, SEG>(L, st);
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
@@ -1666,14 +1673,12 @@ cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
         if (!L.args.c_wide) return cudaErrorInvalidValue;
         return L.seg ? launch_xent<XENT_GRAD, true>(L, st) : launch_xent<XENT_GRAD, false>(L, st);
     }
-    if (L.xent == XENT_PRODUCT && L.csplit && L.args.fold > 0 && !L.seg)
-        return L.cg == 1 && L.bn == 128 ? launch_product<128, 1, false, true>(L, st)
-               : L.cg == 1 && L.bn == 64 ? launch_product<64, 1, false, true>(L, st)
-                                         : cudaErrorInvalidValue;
+    if (L.xent == XENT_FOLD) {
+        if (!L.csplit || L.args.fold < 1 || L.args.fold > BM) return cudaErrorInvalidValue;
+        return L.seg ? launch_product_split<XENT_FOLD, true>(L, st) : launch_product_split<XENT_FOLD, false>(L, st);
+    }
     if (L.xent == XENT_PRODUCT && L.seg) {
-        if (L.csplit) return L.cg == 1 && L.bn == 128 ? launch_product<128, 1, true, true>(L, st)
-                             : L.cg == 1 && L.bn == 64 ? launch_product<64, 1, true, true>(L, st)
-                                                       : cudaErrorInvalidValue;
+        if (L.csplit) return launch_product_split<XENT_PRODUCT, true>(L, st);
         if (L.cg == 2) return L.bn == 256   ? launch_product<256, 2, true>(L, st)
                               : L.bn == 192 ? launch_product<192, 2, true>(L, st)
                               : L.bn == 128 ? launch_product<128, 2, true>(L, st)
