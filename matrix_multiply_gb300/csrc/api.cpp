@@ -876,7 +876,7 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     a.act = epi ? (int)epi->activation : (int)TC_ACT_NONE;
     a.col_scale = col_scale;
     a.slice_kb = p.i8acc ? I8_SLICE_KB : p.seg_kb > 0 ? p.seg_kb : a.num_kb;
-    L.seg = p.seg_kb > 0;
+    L.seg = p.seg_kb > 0 && p.seg_kb < a.num_kb;
     if (p.product) L.xent = p.fold > 0 ? XENT_FOLD : XENT_PRODUCT;
     const int64_t kb_per_unit = a.num_kb;
     a.timeout_ns = 4000000000ull + (unsigned long long)kb_per_unit * 20000ull;

@@ -1343,6 +1343,19 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         for (int j = 0; j < 32; ++j) v[j] *= scale;
                         store_tma<EBUFS>(&tmC, false, TC_F32, staging(STG_TMA), lane, 0, row0, col0, v);
                     }
+                } else if (XENT == XENT_PRODUCT && w.S == 1 && !args.c_tma && args.beta == 0.0f) {
+                    const float scale = args.col_scale ? args.alpha * args.col_scale[0] : args.alpha;
+                    float *xbuf = reinterpret_cast<float *>(my_stage);
+#pragma unroll 1
+                    for (int c = first_c; c < CHUNKS; c = next_c(c)) {
+                        float v[32];
+                        fetch(c, v);
+                        const long long col0 = (long long)w.tn * BN + c * 32, row0 = row - lane;
+                        if (col0 >= args.N || row0 >= args.M) continue;      // (the whole warp)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] *= scale;
+                        store_staged(args, xbuf, lane, 0, row0, col0, v);
+                    }
                 } else if (w.S == 1) {
 #pragma unroll 1
                     for (int c = first_c; c < CHUNKS; c = next_c(c)) {
@@ -1688,8 +1701,8 @@ cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
                : L.bn == 64  ? launch_product<64, 1, true>(L, st)
                              : cudaErrorInvalidValue;
     }
-    if (L.xent == XENT_PRODUCT && L.args.c_wide) {
-        if (L.csplit) return cudaErrorInvalidValue;
+    // (beta 0 in tiles that these kernels have; else the plain ones)
+    if (L.xent == XENT_PRODUCT && !L.csplit && L.args.beta == 0.0f && L.bn % 128 == 0) {
         if (L.cg == 2) return L.bn == 256   ? launch_product<256, 2, false>(L, st)
                               : L.bn == 128 ? launch_product<128, 2, false>(L, st)
                                             : cudaErrorInvalidValue;
@@ -1697,7 +1710,6 @@ cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
                : L.bn == 128 ? launch_product<128, 1, false>(L, st)
                              : cudaErrorInvalidValue;
     }
-    // (a product in fp32 whole, or in tiles of other widths: the plain kernels)
     const bool epi = L.args.bias != nullptr || L.args.act != TC_ACT_NONE || L.args.col_scale != nullptr;
     if (L.csplit) {
         if (L.cg != 1 || L.i8acc) return cudaErrorInvalidValue;
