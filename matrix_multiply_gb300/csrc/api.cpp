@@ -2062,6 +2062,61 @@ Plan plan_xent(int64_t M, int64_t N, int64_t K, int num_sms, const Force &f)
     return p;
 }
 
+// The plan of one of the gradients' products, M rows of N columns over K with
+// outputs of `es` bytes.  make_plan's, but where this is measured to be better
+// (backward calls with one of the gradients, us):
+//   dW (M the piece of the vocabulary): a tile's stores take as long as some
+//     hundred of K, so short products want one-CTA tiles (300 rows in two parts x
+//     1024 x 10007, fp32: 39.7, pairs 44.6; 128 x 2048 x 32000: 74.2 for 78.6),
+//     and the last wave's tiles cut into slices cost a reduction, 6 us, more than
+//     it saves up to K = 2048 or so (1000 x 1024 x 10007: 51.2 whole, 55.9 cut)
+//   dX: slices of 256-wide tiles through memory instead of 128-wide ones in
+//     clusters where the rows fill them (1000 x 1024 x 10007: 51.8 for 59.7; for
+//     600 rows 47.4 for 45.9)
+tc_status_t plan_product(const tc_gemm_desc *d, const Norm &n, const void *A, const void *B, const void *C, int num_sms,
+                         const Force &f, bool dw, Plan *p)
+{
+    const tc_status_t st = make_plan(d, n, A, B, num_sms, p, false);
+    if (st != TC_OK || f.cg || f.bn || f.split || f.tail >= 0) return st;
+    const int64_t M = d->M, N = d->N, kb = cdiv(d->K, BK);
+    const auto whole = [&](int cg, int bn) {
+        Force g = f;
+        g.cg = cg;
+        g.bn = bn;
+        const Plan q = plan_xent(M, N, d->K, num_sms, g);
+        const bool pa = p->pack_a, pb = p->pack_b;
+        *p = q;
+        p->pack_a = pa;
+        p->pack_b = pb;
+    };
+    if (dw) {
+        // us of a 128 x 256 tile: 0.33 a K block at the tensor core's rate, and its
+        // stores at a 152nd of 3.7 TB/s
+        const double store = 128.0 * 256.0 * (double)elem_size(d->c_dtype) / 24.3e3;
+        if (cdiv(M, BM) * cdiv(N, 64) <= num_sms || p->csplit) return TC_OK;
+        const int64_t t128 = cdiv(M, BM) * cdiv(N, 128), t256 = cdiv(M, BM) * cdiv(N, 256);
+        // (rows off 16 bytes take several times that: the even share decides)
+        const bool rows16 = aligned16(C) && n.ldc * (int64_t)elem_size(d->c_dtype) % 16 == 0;
+        if (0.33 * (double)kb < store)
+            whole(1, t128 <= num_sms || (!rows16 && cdiv(t128, num_sms) < 2 * cdiv(t256, num_sms)) ? 128 : 256);
+        else if (kb < 48)
+            whole(0, 0);
+        return TC_OK;
+    }
+    const int64_t tiles = cdiv(M, BM) * cdiv(N, 256);
+    if (!p->csplit || M < 768 || tiles * 2 > num_sms) return TC_OK;
+    const int S = (int)std::min<int64_t>(num_sms / tiles, kb / 4);
+    const double cluster = (double)cdiv(kb, p->seg0_split) * p->bn / tile_rate(1, p->bn) + CSPLIT_FIXED;
+    if (S < 2 || (double)cdiv(kb, S) * 256.0 / tile_rate(1, 256) + SPLIT_FIXED >= cluster) return TC_OK;
+    whole(1, 256);
+    p->seg0_split = S;
+    p->split_base = 0;
+    p->units = tiles * S;
+    p->split = 2;
+    p->grid = (int)std::min<int64_t>(p->units, num_sms);
+    return TC_OK;
+}
+
 tc_gemm_desc xent_desc(int64_t M, int64_t N, int64_t K, tc_dtype_t dt, tc_dtype_t ct, bool ta, bool tb, float alpha,
                        float beta, int64_t lda, int64_t ldb, int64_t ldc)
 {
@@ -2232,7 +2287,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             q->d = xent_desc(N, H, TG, d->dtype, d->grad_dtype, true, false, d->scale, 0.0f, ldg, ldp, n.lddw);
         }
         tc_status_t r = validate(&q->d, q->A, q->B, q->C, 1, 0, 0, 0, &q->n);
-        if (r == TC_OK) r = make_plan(&q->d, q->n, q->A, q->B, ctx->num_sms, &q->p, false);
+        if (r == TC_OK) r = plan_product(&q->d, q->n, q->A, q->B, q->C, ctx->num_sms, f, !rows, &q->p);
         // (8 tile rows by 9 columns in flight read least: the gradients of
         // 4096 x 65536 x 4096 take 4.25 ms, with 4 rows 4.34)
         if (f.group_m == 0) q->p.group_m = 8;
