@@ -390,9 +390,11 @@ tc_status_t tc_moe_q4_validate(const tc_moe_desc *d, const void *X, const void *
  * X and W have one dtype, TC_F16 or TC_BF16 (TC_ERR_DTYPE otherwise); dX and
  * dW have grad_dtype, the same or TC_F32; target_dtype is TC_I32 or TC_I64.
  * Logits, statistics and sums are fp32 (a reduced loss is summed in 64 bits).
- * G is rounded to dtype for its products, for TC_F32 gradients it is held in
- * two such parts, which doubles those products; with TC_F16 it is scaled by a
- * power of two on the way, so that small gradients keep their bits.  scale is
+ * G, over the gradient that all rows share (the largest of grad where they do
+ * not), is rounded to dtype for its products; for TC_F32 gradients, and for up to
+ * 128 rows, it is held in two such parts (three for both with TC_BF16), which
+ * doubles those products.  lse is
+ * what the forward call wrote for these X and W.  scale is
  * finite and above 0, z_weight finite and at least 0 (TC_ERR_SCALAR).  Leading
  * dimensions as in tc_gemm, any alignment (a W that TMA cannot read in place,
  * base or rows off 16 bytes, is copied piece by piece).  Outputs overlap no

@@ -184,7 +184,8 @@ struct Plan {
     bool tma_store = true;
     bool pack_a = false, pack_b = false;
     bool product = false;      // one of the products of a cross entropy's gradients
-    int fold = 0;              // its C has this many rows, sums of two of the product's each (cluster split)
+    // its C has `fold` rows, sums of the product's (MmaArgs::fold)
+    int fold = 0, fold_parts = 0, fold_step = 0;
     int seg_kb = 0;            // sums cut along K, this many K blocks each (0: whole)
     int64_t tiles = 0, units = 0;
     std::string name;
@@ -691,11 +692,10 @@ WsLayout ws_layout(const Norm &n, const Plan &p)
 }
 
 // A product whose epilogue is the softmax cross entropy's (internal.h): mode is
-// XENT_LOSS (its C is not written) or XENT_GRAD (C, and `left` when epi.two).
+// XENT_LOSS (its C is not written) or XENT_GRAD (C has epi.parts * epi.part_rows rows).
 struct XentJob {
     int mode;
     XentEpi epi;
-    void *left;
 };
 
 // int_slices: the int8 path -- K slices hold exact integers and are added
@@ -863,6 +863,8 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
     // C written through TMA stores of 32 x 32 chunks when its layout allows
     a.c_tma = a.c_vec_ok && p.tma_store && !p.csplit;
     a.fold = p.fold;
+    a.fold_parts = p.fold_parts;
+    a.fold_step = p.fold_step;
     if (xent) {
         L.xent = xent->mode;
         L.x = xent->epi;
@@ -921,15 +923,13 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
         }
     }
     if (ok && a.c_tma)
-        ok = encode_map(ctx, &L.tmC, d->c_dtype, C, d->N, d->M, n.ldc, a.c_3d, n.batch, a.stride_c, a.c_wide ? 64 : 32, 32,
+        ok = encode_map(ctx, &L.tmC, d->c_dtype, C, d->N, xent ? xent->epi.parts * (int64_t)xent->epi.part_rows : d->M, n.ldc, a.c_3d, n.batch, a.stride_c, a.c_wide ? 64 : 32, 32,
                         d->c_dtype == TC_F32 || a.c_wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
     // split-K workspace: one row-major fp32 (BM*cg) x BN tile per K-slice unit
     const int64_t rows_per_tile = (int64_t)BM * p.cg;
     if (ok && a.ws)
         ok = encode_map(ctx, &L.tmW, TC_F32, a.ws, p.bn, (p.units - p.split_base) * rows_per_tile, p.bn, false, 1,
                         0, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (ok && xent && xent->epi.two)
-        ok = encode_map(ctx, &L.tmW, d->c_dtype, xent->left, d->N, d->M, n.ldc, false, 1, 0, 64, 32);
     if (!ok) return TC_ERR_CUDA;
     if ((e = launch_mma(L, s->st)) != cudaSuccess) return TC_ERR_CUDA;
     ++launches;
@@ -2022,12 +2022,14 @@ int64_t xent_piece(int64_t vocab, int64_t bytes)
 
 // K blocks that are summed on the tensor core before the sum is added in fp32,
 // rounded to nearest, where results in fp32 depend on it: the tensor core
-// truncates (lse over a hidden size of 4096 1.4e-6 off in one sum).
-constexpr int XENT_SEG_KB = 16;
-// Rows up to which G is held in two parts for 16-bit gradients too: its products
-// then wait for W and dW, not for the tensor core, and the rounding of G would
-// be as large as that of the gradients.
-constexpr int64_t XENT_TWO_PART_ROWS = 128;
+// truncates (f16, hidden size 1001 in one sum: lse 1.1e-6 off, in two 0.5e-6; of
+// bf16 products, whose significands are shorter, less is lost: 4096 in 4 sums
+// 1.8e-7 off, in one 1.4e-6).  Twice as many sums cost 4096 x 131072 x 4096 5%.
+int xent_seg_kb(tc_dtype_t dt) { return dt == TC_F16 ? 8 : 16; }
+// Rows up to which G is held in more parts than the gradients' type needs beyond
+// (two for 16 bits, where its rounding would be as large as theirs; of bf16 three
+// for fp32): its products then wait for W and dW, not for the tensor core.
+constexpr int64_t XENT_MORE_PARTS_ROWS = 128;
 
 // The tensor-core kernel on whole tiles: the shape with the least modelled time.
 Plan plan_xent(int64_t M, int64_t N, int64_t K, int num_sms, const Force &f)
@@ -2205,7 +2207,7 @@ tc_status_t run_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const vo
         same.bn = first.bn;
         same.cg = first.cg;
         Plan p = plan_xent(T, N, H, ctx->num_sms, same);
-        p.seg_kb = XENT_SEG_KB;
+        p.seg_kb = xent_seg_kb(d->dtype);
         const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, TC_F32, false, true, d->scale, 0.0f, pack_x ? ldp : n.ldx,
                                           pack_w ? ldp : n.ldw, N);
         const void *Xv = pack_x ? rx + o_x : X;
@@ -2244,25 +2246,27 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     if (st != TC_OK) return st;
     const int64_t T = d->tokens, H = d->hidden, V = d->vocab, ldp = (int64_t)round_up((size_t)H, 64);
     const int64_t es = (int64_t)elem_size(d->grad_dtype);
-    const bool pack_w = !aligned16(W) || n.ldw % 8 != 0, f16 = d->dtype == TC_F16;
+    const bool pack_w = !aligned16(W) || n.ldw % 8 != 0;
     const bool f32 = d->grad_dtype == TC_F32;
-    // G in two parts, one below the other: dX is then a product of 2 T rows whose
-    // halves are added, dW one over 2 T rows of X, repeated
-    const int64_t parts = f32 || T <= XENT_TWO_PART_ROWS ? 2 : 1, TG = T * parts;
+    const bool is_f16 = d->dtype == TC_F16;
+    // G in parts, whole warps' rows below each other: dX is then a product of all
+    // their rows, whose parts are added, dW one over as many rows of X, repeated
+    const int64_t parts = T <= XENT_MORE_PARTS_ROWS ? (!f32 ? 2 : is_f16 ? 2 : 3) : f32 ? 2 : 1;
+    const int64_t TP = parts > 1 ? (int64_t)round_up((size_t)T, 32) : T, TG = parts * TP;
     const int64_t cols = xent_piece(V, TG * 2 + (pack_w ? ldp * 2 : 0)), ldg = (int64_t)round_up((size_t)cols, 64);
     // dX of several pieces or parts is summed in fp32
-    const bool sum = dX && (cols < V || parts == 2);
+    const bool sum = dX && (cols < V || parts > 1);
     if (TG > INT32_MAX) return TC_ERR_OVERFLOW;
     const Force f = read_force();
     std::lock_guard<std::mutex> lk(ctx->mu);
     if (cudaSetDevice(ctx->device) != cudaSuccess) return TC_ERR_CUDA;
     Carve c;
-    const size_t o_cp = c.take(T * 4), o_cy = c.take(T * 4), o_un = c.take(f16 ? H * 4 : 0);
+    const size_t o_cp = c.take(T * 4), o_cy = c.take(T * 4), o_un = c.take(H * 4);
     const size_t o_x = c.take(TG * ldp * 2), o_w = c.take(pack_w ? cols * ldp * 2 : 0), o_sum = c.take(sum ? TG * ldp * 4 : 0);
     const size_t o_g = c.take(TG * ldg * 2);
     if ((st = reserve(s, 256, c.at)) != TC_OK) return st;
     uint8_t *rx = static_cast<uint8_t *>(s->rx);
-    const float *unscale = f16 ? reinterpret_cast<const float *>(rx + o_un) : nullptr;
+    float *unscale = reinterpret_cast<float *>(rx + o_un);
 
     // the two products of the piece at v0 with G
     struct Product {
@@ -2299,10 +2303,12 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             q->p.pack_b = pb;
         }
         q->p.product = true;
-        q->p.seg_kb = f32 ? XENT_SEG_KB : 0;
-        // halves of one tile row meet where the cluster's slices do
-        if (rows && parts == 2 && TG <= BM && cols == V && q->p.csplit && csplit_clusters(ctx, q->p.bn, 2) > 0) {
+        q->p.seg_kb = f32 ? xent_seg_kb(d->dtype) : 0;
+        // the parts of one tile row meet where the cluster's slices do
+        if (rows && parts > 1 && TG <= BM && cols == V && q->p.csplit && csplit_clusters(ctx, q->p.bn, 2) > 0) {
             q->p.fold = (int)T;
+            q->p.fold_parts = (int)parts;
+            q->p.fold_step = (int)TP;
             q->C = dX;
             q->d.c_dtype = d->grad_dtype;
             q->d.ldc = (int32_t)n.lddx;
@@ -2336,12 +2342,14 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     a.grad = grad;
     a.cp = reinterpret_cast<float *>(rx + o_cp);
     a.cy = reinterpret_cast<float *>(rx + o_cy);
-    a.unscale = const_cast<float *>(unscale);
+    a.unscale = unscale;
+    a.f16 = is_f16;
     a.X = static_cast<const uint16_t *>(X);
     a.ldx = n.ldx;
     a.clean = reinterpret_cast<uint16_t *>(rx + o_x);
     a.ld_clean = ldp;
     a.copies = (int)parts;
+    a.copy_rows = (int)TP;
     // few rows: no launch of its own
     const bool own_prep = T <= XENT_OWN_PREP_ROWS && cols == V && aligned16(X) && n.ldx % 8 == 0;
     if (!own_prep) {
@@ -2355,7 +2363,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         if ((st = pack_rows(ctx, s, {{Wv, n.ldw, rx + o_w, ldp, pack_w ? N : 0, H}})) != TC_OK) return st;
         if (pack_w) Wv = rx + o_w;
         Plan p = plan_xent(T, N, H, ctx->num_sms, f);
-        p.seg_kb = f32 ? XENT_SEG_KB : 0;
+        p.seg_kb = f32 ? xent_seg_kb(d->dtype) / 2 : 0;         // (an error of a logit is one of its exponential's size)
         if (v0 == 0) name = p.name;
         const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, d->dtype, false, true, 1.0f, 0.0f, own_prep ? n.ldx : ldp,
                                           pack_w ? ldp : n.ldw, ldg);
@@ -2377,10 +2385,10 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         job.epi.lse = lse;
         job.epi.cp = a.cp;
         job.epi.cy = a.cy;
-        job.epi.two = parts == 2;
+        job.epi.parts = (int)parts;
+        job.epi.part_rows = (int)TP;
         job.epi.own_prep = own_prep;
         job.epi.prep = a;
-        job.left = rx + o_g + (size_t)(T * ldg * 2);
         if ((st = enqueue(ctx, &gd, gn, p, own_prep ? X : rx + o_x, Wv, rx + o_g, s, nullptr, nullptr, false, &job)) != TC_OK) return st;
         for (const bool rows : {true, false}) {
             if (rows ? !dX : !dW) continue;
@@ -2391,11 +2399,11 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
     }
     if (sum && !folded) {
         const float *at = reinterpret_cast<const float *>(rx + o_sum);
-        const XentRoundArgs r{at, parts == 2 ? at + T * ldp : nullptr, dX, T, H, ldp, n.lddx, d->grad_dtype};
+        const XentRoundArgs r{at, (int)parts, TP * ldp, dX, T, H, ldp, n.lddx, d->grad_dtype};
         if (launch_xent_round(r, s->st) != cudaSuccess) return TC_ERR_CUDA;
         ctx->launches += 1;
     }
-    ctx->last = "xent_grad_" + name + (parts == 2 ? "_two" : "") + (pack_w ? "_packW" : "") + "_p" + std::to_string(cdiv(V, cols));
+    ctx->last = "xent_grad_" + name + (parts > 1 ? "_x" + std::to_string(parts) : "") + (pack_w ? "_packW" : "") + "_p" + std::to_string(cdiv(V, cols));
     return TC_OK;
 }
 

@@ -103,10 +103,10 @@ __host__ __device__ constexpr int mma_smem_bytes(int bn, int cg, bool epi = fals
     return mma_stages(bn, cg, epi) * stage_bytes(bn, cg) + smem_reserve(bn, cg, epi);
 }
 
-// What the gradient's products read besides W: each row's factors (cp and
-// cy of XentEpi), X in rows of ld_clean elements with the rows that do not count
-// zeroed, and for f16 the factors times a power of two that puts the largest
-// between 2^13 and 2^14, with its inverse H times for the products' columns.
+// What the gradient's products read besides W: each row's factors (cp and cy of
+// XentEpi) as multiples of what all rows share, that unit H times for the
+// products' columns, and X in rows of ld_clean elements with the rows that do not
+// count zeroed.
 struct XentPrepArgs {
     const void *targets;
     int wide, vocab;
@@ -114,12 +114,13 @@ struct XentPrepArgs {
     float z;
     const float *lse, *grad;   // grad: T values, or one where reduced
     float *cp, *cy;
-    float *unscale;            // H floats (f16), or null
+    float *unscale;            // H floats
+    int f16;                   // the factors besides times a power of two (xent.cuh)
     const uint16_t *X;
     long long ldx;
     uint16_t *clean;
     long long ld_clean;        // a multiple of 8; clean is 16-byte aligned
-    int copies;                // of the T rows, one below the other
+    int copies, copy_rows;     // of the T rows, copy_rows below each other, zeros between
 };
 
 // What the epilogue of a product of hidden rows with a vocabulary's rows needs
@@ -136,11 +137,11 @@ struct XentEpi {
     float2 *part;
     float *at;
     // the gradient: lse[r], and the factors of the probabilities and of the
-    // target's one (both 0 for a row that is not counted); C receives the
-    // rounded values and, through the fourth descriptor when `two`, what the
-    // rounding left
+    // target's one (both 0 for a row that is not counted); C receives the rounded
+    // values, and part_rows below each other what every rounding left, rounded in
+    // turn, in `parts` parts
     const float *lse, *cp, *cy;
-    int two;
+    int parts, part_rows;
     // few rows, X readable by TMA as it is: the kernel that makes G makes the
     // factors too, and the copy of X (what launch_xent_prep does otherwise)
     int own_prep;
@@ -192,9 +193,9 @@ struct MmaArgs {
     const void *bias;
     int act;
     const float *col_scale;
-    // XENT_FOLD, one tile row: C has `fold` rows, the sums of rows r and fold + r of
-    // the product
-    int fold;
+    // XENT_FOLD, one tile row: C has `fold` rows, row r the sum of the fold_parts
+    // rows r, fold_step + r, .. of the product
+    int fold, fold_parts, fold_step;
     int slice_kb;          // K blocks per slice of an accumulator cut along K (int8, cross entropy, MmaLaunch::seg)
     // one-CTA tiles over fewer than BM rows of a K-major A: its copies carry
     // only the rows that exist (rounded up to 8) and a stage this many fewer
@@ -405,10 +406,13 @@ cudaError_t launch_xent_join(const XentJoinArgs &a, cudaStream_t st, int *launch
 
 cudaError_t launch_xent_prep(const XentPrepArgs &a, cudaStream_t st);
 
-// dst [rows, cols] (leading dimension ld) = the fp32 src (+ more, if not null; both of leading dimension
-// ld_src, a multiple of 4, from 16-byte boundaries), rounded to dtype
+// dst [rows, cols] (leading dimension ld) = the sum of `parts` fp32 matrices, the
+// first at src, `step` floats apart, of leading dimension ld_src (a multiple of 4,
+// from 16-byte boundaries), rounded to dtype
 struct XentRoundArgs {
-    const float *src, *more;
+    const float *src;
+    int parts;
+    long long step;
     void *dst;
     long long rows, cols, ld_src, ld;
     int dtype;

@@ -571,7 +571,7 @@ __device__ __forceinline__ void finish4(const MmaArgs &a, int b, long long grow,
 // CTA of rank r sums rows [r * ceil(BM/S), ...) of all S partial tiles,
 // reading its peers' shared memory in slice order (deterministic), and
 // writes those rows of C.  Every thread of the CTA takes part.
-// FOLD: its a.fold rows are sums of two rows of the product.
+// FOLD: its a.fold rows are sums of a.fold_parts rows of the product each.
 template <int BN, bool EPI, bool FOLD>
 __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *partial)
 {
@@ -604,17 +604,19 @@ __device__ __forceinline__ void csplit_reduce(const MmaArgs &a, const uint8_t *p
             }
         }
         if constexpr (FOLD) {
-            const uint32_t more = off + (uint32_t)(a.fold * LD * 4);
+            for (int k = 1; k < a.fold_parts; ++k) {
+                const uint32_t more = off + (uint32_t)(k * a.fold_step * LD * 4);
 #pragma unroll
-            for (int q = 0; q < SMAX; ++q)
-                if (q < S) p[q] = ld_shared_cluster_f4(mapa_shared(more, (uint32_t)q));
+                for (int q = 0; q < SMAX; ++q)
+                    if (q < S) p[q] = ld_shared_cluster_f4(mapa_shared(more, (uint32_t)q));
 #pragma unroll
-            for (int q = 0; q < SMAX; ++q) {
-                if (q < S) {
-                    v[0] += p[q].x;
-                    v[1] += p[q].y;
-                    v[2] += p[q].z;
-                    v[3] += p[q].w;
+                for (int q = 0; q < SMAX; ++q) {
+                    if (q < S) {
+                        v[0] += p[q].x;
+                        v[1] += p[q].y;
+                        v[2] += p[q].z;
+                        v[3] += p[q].w;
+                    }
                 }
             }
         }
@@ -798,8 +800,6 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             prefetch_tmap(&tmB);
             if (args.c_tma) prefetch_tmap(&tmC);
             if (args.ws) prefetch_tmap(&tmW);
-            if constexpr (XENT == XENT_GRAD)
-                if (xa.two) prefetch_tmap(&tmW);
         }
         // let the next kernel in the stream (the split-K reduction, or the
         // next GEMM) launch early; it waits for this grid to finish before
@@ -1083,28 +1083,34 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             }
         };
         // few rows: their factors' common parts, by every warp for itself
-        float mean = 1.0f, power = 1.0f;
+        float unit = 1.0f, power = 1.0f;
         if constexpr (XENT == XENT_GRAD) {
             if (xa.own_prep) {
                 const XentPrepArgs &q = xa.prep;
-                if (q.reduction == TC_REDUCE_MEAN) {
-                    int n = 0;
-                    for (int t = lane; t < q.T; t += 32) n += xent_counts(q, t) ? 1 : 0;
-                    mean = 1.0f / (float)max(__reduce_add_sync(0xffffffffu, n), 1);
+                const auto warp_max = [](float v) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                    return v;
+                };
+                int n = 0;
+                float top = 0.0f;
+                for (int t = lane; t < q.T; t += 32) {
+                    if (!xent_counts(q, t)) continue;
+                    ++n;
+                    if (q.reduction == TC_REDUCE_NONE) top = fmaxf(top, fabsf(q.grad[t]));
                 }
-                if (q.unscale) {
-                    float top = 0.0f;
+                unit = xent_unit(q, warp_max(top), __reduce_add_sync(0xffffffffu, n));
+                if (q.f16) {
+                    float most = 0.0f;
                     for (int t = lane; t < q.T; t += 32) {
                         float p, y;
-                        xent_factors(q, t, mean, p, y);
-                        top = fmaxf(top, fmaxf(fabsf(p), fabsf(y)));
+                        xent_factors(q, t, unit, p, y);
+                        most = fmaxf(most, fmaxf(fabsf(p), fabsf(y)));
                     }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    power = xent_power(top);
-                    for (int h = blockIdx.x * (EW * 32) + threadIdx.x; h < q.H; h += gridDim.x * (EW * 32))
-                        q.unscale[h] = 1.0f / power;
+                    power = xent_power(warp_max(most));
                 }
+                for (int h = blockIdx.x * (EW * 32) + threadIdx.x; h < q.H; h += gridDim.x * (EW * 32))
+                    q.unscale[h] = unit / power;
                 xent_copy(q, (long long)blockIdx.x * (EW * 32) + threadIdx.x, (long long)gridDim.x * (EW * 32));
             }
         }
@@ -1145,7 +1151,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                 const long long row = (long long)w.tm * (BM * CL) + row_in_tile;
                 if (row < args.M) {
                     if (xa.own_prep) {
-                        xent_factors(xa.prep, (int)row, mean, cp, cy);
+                        xent_factors(xa.prep, (int)row, unit, cp, cy);
                         cp *= power;
                         cy *= power;
                     } else {
@@ -1307,15 +1313,12 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                                 for (int j = 0; j < 32; ++j) v[h][j] = 0.0f;
                             }
                         }
-                        free_wide(lane);
-                        fill_wide(args.c_dtype, my_stage, lane, 1.0f, v);
-                        store_wide(&tmC, my_stage, lane, row0, col0);
-                        if (xa.two) {
-                            // what the rounding left, rounded in turn
-                            left_over(args.c_dtype, v);
+                        for (int k = 0;;) {
                             free_wide(lane);
                             fill_wide(args.c_dtype, my_stage, lane, 1.0f, v);
-                            store_wide(&tmW, my_stage, lane, row0, col0);
+                            store_wide(&tmC, my_stage, lane, row0 + (long long)k * xa.part_rows, col0);
+                            if (++k == xa.parts) break;
+                            left_over(args.c_dtype, v);      // what the rounding left
                         }
                     }
                 } else if (XENT == XENT_PRODUCT && WIDE64 && w.S == 1 && args.c_wide) {
@@ -1687,7 +1690,8 @@ cudaError_t launch_mma(const MmaLaunch &L, cudaStream_t st)
         return L.seg ? launch_xent<XENT_GRAD, true>(L, st) : launch_xent<XENT_GRAD, false>(L, st);
     }
     if (L.xent == XENT_FOLD) {
-        if (!L.csplit || L.args.fold < 1 || L.args.fold > BM) return cudaErrorInvalidValue;
+        if (!L.csplit || L.args.fold < 1 || L.args.fold > L.args.fold_step || L.args.fold_parts * L.args.fold_step > BM)
+            return cudaErrorInvalidValue;
         return L.seg ? launch_product_split<XENT_FOLD, true>(L, st) : launch_product_split<XENT_FOLD, false>(L, st);
     }
     if (L.xent == XENT_PRODUCT && L.seg) {

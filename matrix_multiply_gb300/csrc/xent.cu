@@ -43,6 +43,16 @@ __device__ __forceinline__ T block_sum(T v, T *buf)
     return v;
 }
 
+__device__ __forceinline__ float block_max(float v, float *buf)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) v = fmaxf(v, buf[w]);
+    return v;
+}
+
 constexpr int JOIN_THREADS = 256;
 // rows a block of the join takes at once: 64 bytes of each part
 constexpr int JOIN_ROWS = 8;
@@ -178,33 +188,33 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const XentPrepArgs a
         return;
     }
     __shared__ int ns[32];
-    __shared__ float tops[32];
-    float mean = 1.0f;
-    if (a.reduction == TC_REDUCE_MEAN) {
-        int n = 0;
-        for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) n += xent_counts(a, t) ? 1 : 0;
+    __shared__ float tops[32], powers[32];
+    int n = 0;
+    float top = 0.0f;
+    if (a.reduction != TC_REDUCE_SUM) {
+        for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) {
+            if (!xent_counts(a, t)) continue;
+            ++n;
+            if (a.reduction == TC_REDUCE_NONE) top = fmaxf(top, fabsf(a.grad[t]));
+        }
         n = block_sum(n, ns);
-        mean = 1.0f / (float)max(n, 1);
+        top = block_max(top, tops);
     }
+    const float unit = xent_unit(a, top, n);
     float power = 1.0f;
-    if (a.unscale) {
-        float top = 0.0f;
+    if (a.f16) {
+        float most = 0.0f;
         for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) {
             float cp, cy;
-            xent_factors(a, t, mean, cp, cy);
-            top = fmaxf(top, fmaxf(fabsf(cp), fabsf(cy)));
+            xent_factors(a, t, unit, cp, cy);
+            most = fmaxf(most, fmaxf(fabsf(cp), fabsf(cy)));
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-        __syncthreads();
-        for (int w = 0; w < 32; ++w) top = fmaxf(top, tops[w]);
-        power = xent_power(top);
-        for (int h = threadIdx.x; h < a.H; h += PREP_THREADS) a.unscale[h] = 1.0f / power;
+        power = xent_power(block_max(most, powers));
     }
+    for (int h = threadIdx.x; h < a.H; h += PREP_THREADS) a.unscale[h] = unit / power;
     for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) {
         float cp, cy;
-        xent_factors(a, t, mean, cp, cy);
+        xent_factors(a, t, unit, cp, cy);
         a.cp[t] = cp * power;
         a.cy[t] = cy * power;
     }
@@ -223,8 +233,8 @@ __global__ void __launch_bounds__(256) round_kernel(const XentRoundArgs a)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 float4 x = *reinterpret_cast<const float4 *>(a.src + at + 4 * q);
-                if (a.more) {
-                    const float4 y = *reinterpret_cast<const float4 *>(a.more + at + 4 * q);
+                for (int k = 1; k < a.parts; ++k) {
+                    const float4 y = *reinterpret_cast<const float4 *>(a.src + k * a.step + at + 4 * q);
                     x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
                 }
                 v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
@@ -239,8 +249,11 @@ __global__ void __launch_bounds__(256) round_kernel(const XentRoundArgs a)
                                pack2(v[6], v[7], a.dtype));
             }
         } else {
-            for (int j = 0; j < 8 && col + j < a.cols; ++j)
-                store_c1(a.dst, row * a.ld + col + j, a.src[at + j] + (a.more ? a.more[at + j] : 0.0f), a.dtype);
+            for (int j = 0; j < 8 && col + j < a.cols; ++j) {
+                float x = a.src[at + j];
+                for (int k = 1; k < a.parts; ++k) x += a.src[k * a.step + at + j];
+                store_c1(a.dst, row * a.ld + col + j, x, a.dtype);
+            }
         }
     }
 }
@@ -263,7 +276,7 @@ cudaError_t launch_xent_join(const XentJoinArgs &a, cudaStream_t st, int *launch
 
 cudaError_t launch_xent_prep(const XentPrepArgs &a, cudaStream_t st)
 {
-    const unsigned copy = blocks_for(a.ld_clean / 8 * a.T, PREP_THREADS);
+    const unsigned copy = blocks_for(a.ld_clean / 8 * a.copy_rows, PREP_THREADS);
     return launch_dependent(prep_kernel, dim3(1 + copy), dim3(PREP_THREADS), 0, st, 1u, a);
 }
 

@@ -19,19 +19,30 @@ __device__ __forceinline__ bool xent_counts(const XentPrepArgs &a, long long row
     return xent_counts(a.targets, a.wide, a.vocab, row, y);
 }
 
-// The gradient of row t's logits is cp p - cy [target]; mean: 1 / (rows that
-// count) for a mean, else 1.
-__device__ __forceinline__ void xent_factors(const XentPrepArgs &a, int t, float mean, float &cp, float &cy)
+// The gradient of row t's logits is unit (cp p - cy [target]).  unit is what all
+// rows share: the gradient of a reduced loss, or the largest of the rows', so that
+// cy is 1 where they are alike and the target's cy (p - 1), the largest value of
+// the row by far where p is small, is rounded to 16 bits without an error.  (With
+// the gradients themselves in cy that rounding is the same for all rows of a mean
+// and adds up: 2048 x 32000 x 2048 in bf16 0.0029 off, with the unit UNITOFF.)
+__device__ __forceinline__ void xent_factors(const XentPrepArgs &a, int t, float unit, float &cp, float &cy)
 {
     cp = cy = 0.0f;
     if (!xent_counts(a, t)) return;
-    cy = a.grad[a.reduction == TC_REDUCE_NONE ? t : 0] * mean;
+    cy = a.reduction == TC_REDUCE_NONE ? a.grad[t] / unit : 1.0f;
     cp = a.z != 0.0f ? cy * (1.0f + 2.0f * a.z * a.lse[t]) : cy;
 }
 
-// The power of two that puts the largest factor between 2^13 and 2^14.  f16 spans
-// 2^-24 to 2^16: probabilities far below one times a small gradient would be
-// lost, so G is held as a multiple of it.  The inverse stays a normal number.
+// The unit, from the largest of the counted rows' gradients or their number.
+__device__ __forceinline__ float xent_unit(const XentPrepArgs &a, float top, int n)
+{
+    if (a.reduction == TC_REDUCE_NONE) return top > 0.0f && top < INFINITY ? top : 1.0f;
+    return a.reduction == TC_REDUCE_MEAN ? a.grad[0] / (float)max(n, 1) : a.grad[0];
+}
+
+// f16: the power of two that puts the largest factor between 2^13 and 2^14.  The
+// type spans 2^-24 to 2^16: probabilities far below one would be lost, so G is
+// held as a multiple of it.  The inverse stays a normal number.
 __device__ __forceinline__ float xent_power(float top)
 {
     int e;
@@ -45,12 +56,12 @@ __device__ __forceinline__ float xent_power(float top)
 // products run over the rows.
 __device__ __forceinline__ void xent_copy(const XentPrepArgs &a, long long i, long long n)
 {
-    const long long per = a.ld_clean / 8, all = per * a.T;
+    const long long per = a.ld_clean / 8, all = per * a.copy_rows;
     const bool whole = (reinterpret_cast<uintptr_t>(a.X) & 15u) == 0 && a.ldx % 8 == 0;
     for (; i < all; i += n) {
         const long long row = i / per, col = (i - row * per) * 8;
         uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (xent_counts(a, row)) {
+        if (row < a.T && xent_counts(a, row)) {
             const uint16_t *src = a.X + row * a.ldx + col;
             if (whole && col + 8 <= a.H) {
                 w = *reinterpret_cast<const uint4 *>(src);
@@ -62,7 +73,7 @@ __device__ __forceinline__ void xent_copy(const XentPrepArgs &a, long long i, lo
             }
         }
         for (int k = 0; k < a.copies; ++k)
-            *reinterpret_cast<uint4 *>(a.clean + (k * (long long)a.T + row) * a.ld_clean + col) = w;
+            *reinterpret_cast<uint4 *>(a.clean + ((long long)k * a.copy_rows + row) * a.ld_clean + col) = w;
     }
 }
 
