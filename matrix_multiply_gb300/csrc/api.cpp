@@ -2024,8 +2024,9 @@ int64_t xent_piece(int64_t vocab, int64_t bytes)
 // rounded to nearest, where results in fp32 depend on it: the tensor core
 // truncates (f16, hidden size 1001 in one sum: lse 1.1e-6 off, in two 0.5e-6; of
 // bf16 products, whose significands are shorter, less is lost: 4096 in 4 sums
-// 1.8e-7 off, in one 1.4e-6).  Twice as many sums cost 4096 x 131072 x 4096 5%.
-int xent_seg_kb(tc_dtype_t dt) { return dt == TC_F16 ? 8 : 16; }
+// 1.8e-7 off, in one 1.4e-6).  Twice as many sums cost 4096 x 131072 x 4096 5%,
+// and fewer rows, which wait for W, nothing.
+int xent_seg_kb(tc_dtype_t dt, int64_t rows) { return dt == TC_F16 || rows < 1024 ? 8 : 16; }
 // Rows up to which G is held in more parts than the gradients' type needs beyond
 // (two for 16 bits, where its rounding would be as large as theirs; of bf16 three
 // for fp32): its products then wait for W and dW, not for the tensor core.
@@ -2207,7 +2208,7 @@ tc_status_t run_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const vo
         same.bn = first.bn;
         same.cg = first.cg;
         Plan p = plan_xent(T, N, H, ctx->num_sms, same);
-        p.seg_kb = xent_seg_kb(d->dtype);
+        p.seg_kb = xent_seg_kb(d->dtype, T);
         const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, TC_F32, false, true, d->scale, 0.0f, pack_x ? ldp : n.ldx,
                                           pack_w ? ldp : n.ldw, N);
         const void *Xv = pack_x ? rx + o_x : X;
@@ -2303,7 +2304,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             q->p.pack_b = pb;
         }
         q->p.product = true;
-        q->p.seg_kb = f32 ? xent_seg_kb(d->dtype) : 0;
+        q->p.seg_kb = f32 ? xent_seg_kb(d->dtype, T) : 0;
         // the parts of one tile row meet where the cluster's slices do
         if (rows && parts > 1 && TG <= BM && cols == V && q->p.csplit && csplit_clusters(ctx, q->p.bn, 2) > 0) {
             q->p.fold = (int)T;
@@ -2363,7 +2364,16 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         if ((st = pack_rows(ctx, s, {{Wv, n.ldw, rx + o_w, ldp, pack_w ? N : 0, H}})) != TC_OK) return st;
         if (pack_w) Wv = rx + o_w;
         Plan p = plan_xent(T, N, H, ctx->num_sms, f);
-        p.seg_kb = f32 ? xent_seg_kb(d->dtype) / 2 : 0;         // (an error of a logit is one of its exponential's size)
+        if (f32 && !f.cg && !f.bn && p.units * p.cg > p.grid) {
+            // cut sums and several parts make wide tiles wait for their epilogues,
+            // which the registers do not suffice for (1000 x 1024 x 10007: G in
+            // 128 x 128 tiles 43 us, in wider ones 58; in one wave wider ones win)
+            Force g = f;
+            g.cg = 1;
+            g.bn = 128;
+            p = plan_xent(T, N, H, ctx->num_sms, g);
+        }
+        p.seg_kb = f32 ? xent_seg_kb(d->dtype, T) / 2 : 0;         // (an error of a logit is one of its exponential's size)
         if (v0 == 0) name = p.name;
         const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, d->dtype, false, true, 1.0f, 0.0f, own_prep ? n.ldx : ldp,
                                           pack_w ? ldp : n.ldw, ldg);

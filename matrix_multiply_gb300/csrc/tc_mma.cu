@@ -1168,6 +1168,12 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
             // that I8ACC adds up in TMEM, SEG in registers
             const int nseg = I8ACC || SEG ? (w.kb1 - w.kb0 + args.slice_kb - 1) / args.slice_kb : 1;
             float sums[SEG ? NCH * 32 : 1];        // of the segments before the last
+            if constexpr (SEG) {
+                // (a start of their own in every unit: taken from the first segment
+                // instead they count as live all through the epilogue, and spill)
+#pragma unroll
+                for (int j = 0; j < NCH * 32; ++j) sums[j] = 0.0f;
+            }
             bool ok = true;
             for (int sg = 0; sg < nseg; ++sg, ++local) {
                 const uint32_t acc = local & 1u, aph = (local >> 1) & 1u;
@@ -1196,8 +1202,11 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                 if constexpr (SEG) {
                     // 16 columns at a time: with 128 sums a thread has no
                     // registers for more
-                    if (nseg > 1 || XENT == XENT_LOSS) {
-                        const bool first = sg == 0, last = sg + 1 == nseg;
+                    // (a loss and G are made from the registers; else a whole sum
+                    // stays where it is)
+                    constexpr bool FROM_REGISTERS = XENT == XENT_LOSS || XENT == XENT_GRAD;
+                    if (nseg > 1 || FROM_REGISTERS) {
+                        const bool last = sg + 1 == nseg;
 #pragma unroll
                         for (int i = 0; i < 2 * NCH; ++i) {
                             const uint32_t at = taddr + chunk_of(i >> 1) * 32 + (i & 1) * 16;
@@ -1205,7 +1214,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                             __syncwarp();
                             tmem_ld_32x32b_x16(at, r);
                             tmem_ld_wait();
-                            if (last && XENT != XENT_LOSS) {
+                            if (last && !FROM_REGISTERS) {
                                 // back to where the plain epilogue finds them
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(sums[16 * i + j] + __uint_as_float(r[j]));
@@ -1214,11 +1223,11 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                                 if (i == 2 * NCH - 1) release();
 #pragma unroll
                                 for (int j = 0; j < 16; ++j)
-                                    sums[16 * i + j] = first ? __uint_as_float(r[j]) : sums[16 * i + j] + __uint_as_float(r[j]);
+                                    sums[16 * i + j] += __uint_as_float(r[j]);
                             }
                         }
                         if (!last) continue;
-                        if (XENT != XENT_LOSS) tmem_st_wait();
+                        if (!FROM_REGISTERS) tmem_st_wait();
                     }
                 }
                 // chunk c of the accumulator, which goes back to the MMA warp with
@@ -1292,12 +1301,10 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     }
                     if (row < args.M) xa.part[(2LL * w.tn + chunk0) * args.M + row] = make_float2(m, s);
                 } else if constexpr (XENT == XENT_GRAD) {
-#pragma unroll 1
-                    for (int i = 0; i < NCH; i += 2) {
-                        float v[2][32];
-                        fetch2(i, v);
+                    // the warp's i-th chunk and the next from their logits
+                    const auto store_g = [&](int i, float (&v)[2][32]) {
                         const long long col0 = (long long)w.tn * BN + chunk_of(i) * 32, row0 = row - lane;
-                        if (col0 >= args.N || row0 >= args.M) continue;      // (the whole warp)
+                        if (col0 >= args.N || row0 >= args.M) return;        // (the whole warp)
                         const int hit = target - (int)col0;
                         const bool any = __any_sync(0xffffffffu, hit >= 0 && hit < 64);
 #pragma unroll
@@ -1319,6 +1326,22 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                             store_wide(&tmC, my_stage, lane, row0 + (long long)k * xa.part_rows, col0);
                             if (++k == xa.parts) break;
                             left_over(args.c_dtype, v);      // what the rounding left
+                        }
+                    };
+                    if constexpr (SEG) {
+#pragma unroll
+                        for (int i = 0; i < NCH; i += 2) {
+                            float v[2][32];
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) v[j >> 5][j & 31] = sums[32 * i + j];
+                            store_g(i, v);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < NCH; i += 2) {
+                            float v[2][32];
+                            fetch2(i, v);
+                            store_g(i, v);
                         }
                     }
                 } else if (XENT == XENT_PRODUCT && WIDE64 && w.S == 1 && args.c_wide) {
@@ -1392,6 +1415,12 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                         fetch(c, v);
                         store_tma<EBUFS>(&tmW, false, TC_F32, staging(STG_TMA), lane, 0, wrow0, c * 32, v);
                     }
+                }
+                if constexpr (SEG) {
+                    // (the last segment: the sums are dead, which the compiler
+                    // does not see in a loop that could go on)
+                    ++local;
+                    break;
                 }
             }
             if (!ok) break;
