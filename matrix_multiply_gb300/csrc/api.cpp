@@ -2026,7 +2026,7 @@ int64_t xent_piece(int64_t vocab, int64_t bytes)
 // bf16 products, whose significands are shorter, less is lost: 4096 in 4 sums
 // 1.8e-7 off, in one 1.4e-6).  Twice as many sums cost 4096 x 131072 x 4096 5%,
 // and fewer rows, which wait for W, nothing.
-int xent_seg_kb(tc_dtype_t dt, int64_t rows) { return dt == TC_F16 || rows < 1024 ? 8 : 16; }
+int xent_seg_kb(tc_dtype_t dt, int64_t rows) { return rows <= BM ? 2 : dt == TC_F16 || rows < 1024 ? 8 : 16; }
 // Rows up to which G is held in more parts than the gradients' type needs beyond
 // (two for 16 bits, where its rounding would be as large as theirs; of bf16 three
 // for fp32): its products then wait for W and dW, not for the tensor core.
@@ -2226,7 +2226,7 @@ tc_status_t run_xent(tc_ctx *ctx, const tc_xent_desc *d, const void *X, const vo
         job.epi.wide = d->target_dtype == TC_I64;
         job.epi.first = (int)v0;
         job.epi.vocab = d->vocab;
-        job.epi.k2 = d->scale * 1.4426950408889634f;
+        job.epi.scale = d->scale;
         job.epi.part = reinterpret_cast<float2 *>(rx + o_part) + 2 * (v0 / first.bn) * T;
         job.epi.at = reinterpret_cast<float *>(rx + o_at);
         if ((st = enqueue(ctx, &gd, gn, p, Xv, Wv, rx + o_rows, s, nullptr, nullptr, false, &job)) != TC_OK) return st;
@@ -2373,7 +2373,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             g.bn = 128;
             p = plan_xent(T, N, H, ctx->num_sms, g);
         }
-        p.seg_kb = f32 ? xent_seg_kb(d->dtype, T) / 2 : 0;         // (an error of a logit is one of its exponential's size)
+        p.seg_kb = f32 ? std::max(xent_seg_kb(d->dtype, T) / 2, 2) : 0;         // (an error of a logit is one of its exponential's size)
         if (v0 == 0) name = p.name;
         const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, d->dtype, false, true, 1.0f, 0.0f, own_prep ? n.ldx : ldp,
                                           pack_w ? ldp : n.ldw, ldg);
@@ -2391,7 +2391,7 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         job.epi.wide = a.wide;
         job.epi.first = (int)v0;
         job.epi.vocab = d->vocab;
-        job.epi.k2 = d->scale * 1.4426950408889634f;
+        job.epi.scale = d->scale;
         job.epi.lse = lse;
         job.epi.cp = a.cp;
         job.epi.cy = a.cy;

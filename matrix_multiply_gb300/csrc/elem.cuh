@@ -48,6 +48,9 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+// e^x for x <= 0 the same way: off by |x| 2^-24 of its value besides.
+__device__ __forceinline__ float exp_approx(float x) { return exp2_approx(x * 1.4426950408889634f); }
+
 // Fused epilogue (tessl architecture.md, "Fused Epilogue"): activation(y +
 // bias[col]) in fp32 on the value y = alpha * acc + beta * C_old.
 // GeluTanh: 0.5 x (1 + tanh(z)), z = sqrt(2/pi) (x + 0.044715 x^3),

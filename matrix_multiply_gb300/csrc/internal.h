@@ -130,9 +130,9 @@ struct XentEpi {
     const void *targets;   // one for each row of the product: int32, or int64 when `wide`
     int wide;
     int first, vocab;
-    float k2;              // logits to base-2 exponents: their scale times log2(e)
+    float scale;           // of the logits
     // the loss: for row r and the half h of output tile column tn the largest
-    // exponent and the sum of 2^(exponent - largest) at part[(2 tn + h) * M + r],
+    // logit and the sum of e^(logit - largest) at part[(2 tn + h) * M + r],
     // and the logit of the row's target, where it is in this range, at at[r]
     float2 *part;
     float *at;

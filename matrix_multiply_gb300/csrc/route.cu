@@ -21,7 +21,6 @@
 namespace tc {
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                v[i] = exp2_approx((v[i] - big) * LOG2E);
+                v[i] = exp_approx(v[i] - big);
                 s += v[i];
             }
             s = warp_sum(s);
@@ -371,7 +370,7 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
             z = fmaf(lse, lse, z);
             ++n;
             const bool mine = id >= 0 && slot < got;
-            float w = mine ? exp2_approx((of_key(key) - big) * LOG2E) * inv : 0.0f;
+            float w = mine ? exp_approx(of_key(key) - big) * inv : 0.0f;
             if (a.renorm) w *= inverse(warp_sum(w));
             if (mine) {
                 atomicAdd(&chosen[id], 1);
@@ -481,7 +480,7 @@ __global__ void __launch_bounds__(256, GRAD_BLOCKS<C>) route_grad_kernel(const R
             float s = 0.0f, fp = 0.0f;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                v[i] = exp2_approx((v[i] - big) * LOG2E);
+                v[i] = expf(v[i] - big);       // (f - sum f p cancels: to an ulp)
                 s += v[i];
                 fp = fmaf(f[i], v[i], fp);
             }
@@ -495,14 +494,11 @@ __global__ void __launch_bounds__(256, GRAD_BLOCKS<C>) route_grad_kernel(const R
                 __syncwarp();
                 const bool on = id >= 0 && id < a.E;
                 const float p = on ? probs[warp][id] * inv : 0.0f;
-                const float dot = warp_sum(on ? gw * p : 0.0f);
-                float g = p * gw;
-                if (a.renorm) {
-                    const float r = inverse(warp_sum(p));
-                    g = p * r * (gw - dot * r);
-                } else {
-                    all -= dot;
-                }
+                // (divided, so that a token's only weight is 1 and its gradient 0)
+                const float w = a.renorm ? p / warp_sum(p) : p;
+                const float dot = warp_sum(on ? gw * w : 0.0f);
+                const float g = a.renorm ? w * (gw - dot) : w * gw;
+                if (!a.renorm) all -= dot;
                 // an index met twice: its gradients are added, lane by lane
                 const unsigned same = __match_any_sync(FULL, on ? id : -1 - lane);
                 if (__any_sync(FULL, same != 1u << lane)) {

@@ -2,7 +2,7 @@
 // the small kernels around the products (tc_mma.cu, XENT_LOSS and XENT_GRAD).
 //
 //   loss       l = scale X W^T stays in TMEM: each half tile of a row leaves
-//              its largest exponent and its sum of exponentials, and the
+//              its largest logit and its sum of exponentials, and the
 //              target's logit; `join` makes lse and the losses of them.
 //   gradients  G = the gradient of l, piece by piece of the vocabulary,
 //              rounded to X's type (in two parts where that is not enough);
@@ -19,11 +19,11 @@
 namespace tc {
 namespace {
 
-// (m, s) <- the statistics of both: s 2^m + t 2^n = (..) 2^max(m, n)
+// (m, s) <- the statistics of both: s e^m + t e^n = (..) e^max(m, n)
 __device__ __forceinline__ void merge(float &m, float &s, float n, float t)
 {
     const float top = fmaxf(m, n), base = top == -INFINITY ? 0.0f : top;
-    s = s * exp2_approx(m - base) + t * exp2_approx(n - base);
+    s = s * exp_approx(m - base) + t * exp_approx(n - base);
     m = top;
 }
 
@@ -107,7 +107,7 @@ __device__ __forceinline__ void join_rows(const XentJoinArgs &a, long long row0,
     float loss = 0.0f;
     bool counted = false;
     if (in && q == 0) {
-        const float lse = (m + log2f(s)) * 0.6931471805599453f;
+        const float lse = m + logf(s);
         long long y;
         counted = xent_counts(a.targets, a.wide, a.vocab, row, y);
         loss = counted ? lse - __ldcg(a.at + row) + a.z * lse * lse : 0.0f;

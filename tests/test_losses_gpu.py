@@ -2,6 +2,7 @@
 on several streams, after expired waits, past 32-bit offsets."""
 from __future__ import annotations
 
+import gc
 import time
 
 import pytest
@@ -97,6 +98,7 @@ class Route:
 
 
 def capture(place, *calls):
+    gc.collect()                                           # a graph freed during a capture would end it
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=place[1]):
         for c in calls:
@@ -135,6 +137,7 @@ def test_capture_and_replay(place, make):
 def test_first_call_under_capture_is_refused(place, make):
     call = make(place)
     before = place[0].launch_count
+    gc.collect()
     graph = torch.cuda.CUDAGraph()
     mark = torch.zeros(4, device="cuda")
     with torch.cuda.graph(graph, stream=place[1]):
@@ -310,6 +313,7 @@ def test_whole_step(place):
         step()
     torch.cuda.synchronize()
     first = [t.clone() for t in (loss, losses, dX, dW, dR)]
+    gc.collect()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=side):
         step()
