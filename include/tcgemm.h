@@ -392,17 +392,17 @@ tc_status_t tc_moe_q4_validate(const tc_moe_desc *d, const void *X, const void *
  * Logits, statistics and sums are fp32 (a reduced loss is summed in 64 bits).
  * G, over the gradient that all rows share (the largest of grad where they do
  * not), is rounded to dtype for its products; for TC_F32 gradients, and for up to
- * 128 rows, it is held in two such parts (three for both with TC_BF16), which
- * doubles those products.  lse is
- * what the forward call wrote for these X and W.  scale is
- * finite and above 0, z_weight finite and at least 0 (TC_ERR_SCALAR).  Leading
+ * 128 rows, it is held in two such parts (three for both with TC_BF16), each one
+ * more of those products.  lse is what the forward call wrote for these X and W.
+ * scale is finite and above 0, z_weight finite and at least 0 (TC_ERR_SCALAR).
+ * tokens, hidden and vocab are at most 2^31 - 4097 (TC_ERR_OVERFLOW).  Leading
  * dimensions as in tc_gemm, any alignment (a W that TMA cannot read in place,
  * base or rows off 16 bytes, is copied piece by piece).  Outputs overlap no
  * input and one another (TC_ERR_OVERLAP).  Deterministic run to run.
  *
  * Takes workspace from the stream: forward about tokens * vocab / 16 bytes
- * (those statistics), backward up to 256 MiB for a piece of G and copies of
- * X and, in fp32, dX.  Before a stream capture make the call that needs most; a
+ * (those statistics), backward about 256 MiB for a piece of G, and copies of X
+ * and, in fp32, dX; a copied W counts as part of its piece.  Before a stream capture make the call that needs most; a
  * captured call that would have to allocate returns TC_ERR_CUDA and captures
  * nothing.  Graphs captured on one stream share its workspace: replays of them
  * must not overlap. */

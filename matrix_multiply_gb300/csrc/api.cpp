@@ -923,7 +923,9 @@ tc_status_t enqueue(tc_ctx *ctx, const tc_gemm_desc *d, const Norm &n, const Pla
         }
     }
     if (ok && a.c_tma)
-        ok = encode_map(ctx, &L.tmC, d->c_dtype, C, d->N, xent ? xent->epi.parts * (int64_t)xent->epi.part_rows : d->M, n.ldc, a.c_3d, n.batch, a.stride_c, a.c_wide ? 64 : 32, 32,
+        ok = encode_map(ctx, &L.tmC, d->c_dtype, C, d->N,
+                        xent ? xent->epi.parts * (int64_t)xent->epi.part_rows : d->M, n.ldc, a.c_3d, n.batch,
+                        a.stride_c, a.c_wide ? 64 : 32, 32,
                         d->c_dtype == TC_F32 || a.c_wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
     // split-K workspace: one row-major fp32 (BM*cg) x BN tile per K-slice unit
     const int64_t rows_per_tile = (int64_t)BM * p.cg;
@@ -1933,6 +1935,7 @@ tc_status_t reserve(tc_stream *s, size_t ws, size_t rx)
     return st != TC_OK ? st : ensure_rx(s, rx);
 }
 
+constexpr int32_t XENT_MAX_DIM = INT32_MAX - 4096;
 struct XentNorm {
     int64_t ldx, ldw, lddx, lddw;
     int64_t x_bytes, w_bytes, y_bytes, loss_bytes, lse_bytes;
@@ -1954,7 +1957,9 @@ tc_status_t check_xent(const tc_xent_desc *d, const void *X, const void *W, cons
     n.lddw = d->lddw ? d->lddw : d->hidden;
     if (n.ldx < d->hidden || n.ldw < d->hidden || n.lddx < d->hidden || n.lddw < d->hidden) return TC_ERR_LD;
     if (!std::isfinite(d->scale) || d->scale <= 0.0f || !std::isfinite(d->z_weight) || d->z_weight < 0.0f) return TC_ERR_SCALAR;
-    if (d->hidden > INT32_MAX - 63) return TC_ERR_OVERFLOW;       // copies have rows of whole 64s
+    // kernels count rows and columns, those of a last partial tile or round among
+    // them, in 32 bits, and copies have rows of whole 64s
+    if (std::max({d->tokens, d->hidden, d->vocab}) > XENT_MAX_DIM) return TC_ERR_OVERFLOW;
     if (!extent(d->tokens, d->hidden, n.ldx, 1, 0, 2, &n.x_bytes) || !extent(d->vocab, d->hidden, n.ldw, 1, 0, 2, &n.w_bytes))
         return TC_ERR_OVERFLOW;
     // tiles are counted in 32 bits
@@ -2065,14 +2070,13 @@ Plan plan_xent(int64_t M, int64_t N, int64_t K, int num_sms, const Force &f)
     return p;
 }
 
-// The plan of one of the gradients' products, M rows of N columns over K with
-// outputs of `es` bytes.  make_plan's, but where this is measured to be better
-// (backward calls with one of the gradients, us):
+// The plan of one of the gradients' products.  make_plan's, but where this is
+// measured to be better (backward calls with one of the gradients, us):
 //   dW (M the piece of the vocabulary): a tile's stores take as long as some
 //     hundred of K, so short products want one-CTA tiles (300 rows in two parts x
 //     1024 x 10007, fp32: 39.7, pairs 44.6; 128 x 2048 x 32000: 74.2 for 78.6),
 //     and the last wave's tiles cut into slices cost a reduction, 6 us, more than
-//     it saves up to K = 2048 or so (1000 x 1024 x 10007: 51.2 whole, 55.9 cut)
+//     it saves up to 48 blocks of K (1000 x 1024 x 10007: 51.2 whole, 55.9 cut)
 //   dX: slices of 256-wide tiles through memory instead of 128-wide ones in
 //     clusters where the rows fill them (1000 x 1024 x 10007: 51.8 for 59.7; for
 //     600 rows 47.4 for 45.9)
@@ -2373,7 +2377,8 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
             g.bn = 128;
             p = plan_xent(T, N, H, ctx->num_sms, g);
         }
-        p.seg_kb = f32 ? std::max(xent_seg_kb(d->dtype, T) / 2, 2) : 0;         // (an error of a logit is one of its exponential's size)
+        // (an error of a logit is one of its exponential's size)
+        p.seg_kb = f32 ? std::max(xent_seg_kb(d->dtype, T) / 2, 2) : 0;
         if (v0 == 0) name = p.name;
         const tc_gemm_desc gd = xent_desc(T, N, H, d->dtype, d->dtype, false, true, 1.0f, 0.0f, own_prep ? n.ldx : ldp,
                                           pack_w ? ldp : n.ldw, ldg);
@@ -2413,7 +2418,8 @@ tc_status_t run_xent_backward(tc_ctx *ctx, const tc_xent_desc *d, const void *X,
         if (launch_xent_round(r, s->st) != cudaSuccess) return TC_ERR_CUDA;
         ctx->launches += 1;
     }
-    ctx->last = "xent_grad_" + name + (parts > 1 ? "_x" + std::to_string(parts) : "") + (pack_w ? "_packW" : "") + "_p" + std::to_string(cdiv(V, cols));
+    ctx->last = "xent_grad_" + name + (parts > 1 ? "_x" + std::to_string(parts) : "") + (pack_w ? "_packW" : "") + "_p" +
+                std::to_string(cdiv(V, cols));
     return TC_OK;
 }
 

@@ -248,8 +248,8 @@ __device__ __forceinline__ double warp_sum(double v)
 }
 
 // Adds the blocks' rows up, in a fixed order.  A cluster of 8 blocks (one for up
-// to 64 experts) shares the columns (and every block takes the last one, of lse^2 and the tokens); a
-// block's 32 warps take every 32nd row, so that 5 loads a thread, all in flight,
+// to 64 experts) shares the columns (and every block takes the last one, of lse^2
+// and the tokens); a block's 32 warps take every 32nd row, so that 5 loads a thread, all in flight,
 // read the rows of 152 blocks once; the warps' sums meet in shared memory in 64
 // bits, the blocks' shares of the balance loss in the first one's.  (One block
 // for everything takes 19 us for 257 columns, one thread a column 36.)
@@ -420,8 +420,7 @@ __global__ void __launch_bounds__(Shape<C>::THREADS, 1) route_kernel(const Route
 
 // Resident blocks of 8 warps per SM, which is what covers a token's chain of
 // loads, reductions and exchanges (65536 x 256: 4 blocks of 64 registers 35.1
-// us, 5 of 48
-// 33.0); 16 values a lane need 80.
+// us, 5 of 48 33.0); 16 values a lane need 80.
 template <int C>
 constexpr int GRAD_BLOCKS = C <= 2 ? 6 : C <= 8 ? 5 : 3;
 

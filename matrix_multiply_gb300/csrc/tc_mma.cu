@@ -656,7 +656,7 @@ __device__ __forceinline__ void xent_statistics(const MmaArgs &a, float scale, l
     }
     const float top = fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * scale;
     const float next = fmaxf(m, top);
-    const float base = next == -INFINITY ? 0.0f : next;     // only -inf so far: 2^(-inf - 0) = 0
+    const float base = next == -INFINITY ? 0.0f : next;     // only -inf so far: e^(-inf - 0) = 0
     float sum[4] = {s * exp_approx(m - base), 0.0f, 0.0f, 0.0f};
     if (n == 32) {
 #pragma unroll
@@ -704,11 +704,12 @@ __device__ __forceinline__ void xent_statistics(const MmaArgs &a, float scale, l
 // memory and no second kernel runs.
 //
 // XENT: the softmax cross entropy of the rows of A against those of B, in
-// place of the epilogue (or, XENT_PRODUCT, a shorter one).  A row's logits are the row of one TMEM lane, so each
-// epilogue lane keeps its row's running maximum and sum in registers over its
-// chunks of the tile (XENT_LOSS: two floats leave the chip per row and half
-// tile), or turns them into the gradient of the logits from the row's known
-// lse (XENT_GRAD).  Eight epilogue warps: per element a multiply-add, an
+// place of the epilogue (or, XENT_PRODUCT, a shorter one).  A row's logits are
+// the row of one TMEM lane, so each epilogue lane keeps its row's running maximum
+// and sum in registers over its chunks of the tile (XENT_LOSS: two floats leave
+// the chip per row and half tile), or turns them into the gradient of the logits
+// from the row's known lse (XENT_GRAD).  XENT_FOLD: a cluster split whose sums
+// also add the parts of the rows.  Eight epilogue warps: per element a multiply-add, an
 // exponential and two or three more operations, 1.5 us for the 128 x 256
 // outputs of an SM, which the next tile's MMAs hide from a hidden size of
 // about 512 on.
@@ -745,7 +746,8 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
     static_assert(!SEG || (EW == 8 && !GROUPED && !I8ACC), "segments: at most 128 sums in a thread's registers");
     static_assert(XENT != XENT_LOSS || SEG, "a row's statistics are taken from registers");
     static_assert(XENT != XENT_FOLD || CSPLIT, "rows are added where the slices are");
-    static_assert(XENT == XENT_NONE || XENT >= XENT_PRODUCT || (EPI && !GROUPED && !I8ACC && !CSPLIT), "cross entropy: eight epilogue warps, whole tiles");
+    static_assert(XENT == XENT_NONE || XENT >= XENT_PRODUCT || (EPI && !GROUPED && !I8ACC && !CSPLIT),
+                  "cross entropy: eight epilogue warps, whole tiles");
     static_assert(!CSPLIT || BM * csplit_ld<BN>() * 4 <= S * STAGE, "the partial tile fits in the idle ring");
     constexpr int CHUNKS = BN / 32;
     // 16-bit C in stores of 64 columns: a warp's chunks then come in pairs of

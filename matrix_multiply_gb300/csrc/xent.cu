@@ -5,9 +5,9 @@
 //              its largest logit and its sum of exponentials, and the
 //              target's logit; `join` makes lse and the losses of them.
 //   gradients  G = the gradient of l, piece by piece of the vocabulary,
-//              rounded to X's type (in two parts where that is not enough);
-//              dX += G W_piece and dW_piece = G^T X are plain products.  `prep` runs first, `round` last where dX was
-//              summed over pieces in fp32.
+//              rounded to X's type (in two or three parts where that is not enough);
+//              dX += G W_piece and dW_piece = G^T X are plain products.  `prep`
+//              runs first, `round` last where dX was summed over pieces in fp32.
 //
 // All of it is some microseconds beside products of 2 T H V operations each.
 #include "elem.cuh"

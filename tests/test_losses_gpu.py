@@ -163,6 +163,20 @@ def test_larger_call_then_captured_smaller_ones(place):
         c.check()
 
 
+def test_capture_of_kernels_that_have_not_run(place):
+    """What a capture needs of the stream is memory: a larger call of another kind has taken it."""
+    large = Xent(place, 900, 320, 30000, "bf16", reduction="mean")
+    large.enqueue()
+    large.check()
+    calls = [Xent(place, 20, 130, 1500, "f16", reduction="mean", ignored=0.2, grad="f32"),
+             Xent(place, 150, 1040, 2003, "bf16", reduction="sum", grad="f32"), Route(place, 70, 200, 6, "f16")]
+    graph = capture(place, *calls)
+    for _ in range(2):
+        graph.replay()
+        for c in calls:
+            c.check()
+
+
 def test_two_streams(place):
     ctx = place[0]
     sides = [torch.cuda.Stream() for _ in range(3)]

@@ -42,6 +42,17 @@ def test_descriptor(call, kw, want):
     assert call(**kw) == want
 
 
+@pytest.mark.parametrize("call", [forward, backward])
+@pytest.mark.parametrize("dim", ["tokens", "hidden", "vocab"])
+def test_largest(call, dim):
+    """32 bits hold a dimension, its last partial tile included."""
+    sizes = {"tokens": 1, "hidden": 1, "vocab": 1}
+    at = {k: i << 50 for i, k in enumerate(AT, 1)}
+    assert call(at, **{**sizes, dim: 2 ** 31 - 4097}) == tg.TC_OK
+    for n in (2 ** 31 - 4096, 2 ** 31 - 1):
+        assert call(at, **{**sizes, dim: n}) == tg.TC_ERR_OVERFLOW
+
+
 def test_null():
     assert tg.tc_linear_xent_validate(None) == tg.TC_ERR_NULL
     assert tg.tc_linear_xent_backward_validate(None) == tg.TC_ERR_NULL

@@ -110,6 +110,42 @@ def test_pieces(ctx, dtype, grad, pad):
     assert ctx.last_kernel.endswith("_p2")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("H", [64, 129])
+def test_bases_off_16_bytes(ctx, dtype, H):
+    """Every operand begins one element behind an aligned address."""
+    c = Case(70, H, 600, dtype, reduction="mean", ignored=0.2, seed=17)
+
+    def behind(t):
+        full = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+        out = full[1:].view(t.shape)
+        out.copy_(t)
+        return out
+
+    c.X, c.W, c.y, c.g = behind(c.X), behind(c.W), behind(c.y), behind(c.g)
+    loss, eloss, lse, elf = c.forward()
+    out = [behind(torch.zeros(n, device="cuda")) for n in (1, c.T)]
+    torch.cuda.synchronize()
+    tg.tc_linear_xent(ctx, c.desc(tg), c.X, c.W, c.y, *out)
+    within(out[0], loss, eloss)
+    within(out[1], lse, elf)
+    lse32 = behind(c.lse32())
+    dX, ex, dW, ew = c.backward(lse32)
+    gx, gw = behind(torch.zeros_like(c.X)), behind(torch.zeros_like(c.W))
+    torch.cuda.synchronize()
+    tg.tc_linear_xent_backward(ctx, c.desc(tg), c.X, c.W, c.y, lse32, c.g, gx, gw)
+    within(gx, dX, ex)
+    within(gw, dW, ew)
+
+
+@pytest.mark.parametrize("T", [1, 31, 32, 33, 64, 65, 128, 129])
+@pytest.mark.parametrize("dtype,grad", [("bf16", None), ("f16", None), ("bf16", "f32"), ("f16", "f32")])
+def test_parts_of_g(ctx, T, dtype, grad):
+    """The parts of G around whole warps and tiles, with a vocabulary long enough
+    for the cluster split that adds them up, and a hidden size of several segments."""
+    check(ctx, Case(T, 1100, 2100, dtype, reduction="none", z=0.001, ignored=0.1, grad=grad, seed=18))
+
+
 def test_frozen(ctx):
     c = Case(40, 64, 500, seed=6)
     lse = c.lse32()
