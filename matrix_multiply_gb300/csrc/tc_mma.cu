@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(mma_threads(BN, CG, EPI || GROUPED), 1)
                     power = xent_power(warp_max(most));
                 }
                 for (int h = blockIdx.x * (EW * 32) + threadIdx.x; h < q.H; h += gridDim.x * (EW * 32))
-                    q.unscale[h] = unit / power;
+                    q.unscale[h] = xent_unscale(unit, power);
                 xent_copy(q, (long long)blockIdx.x * (EW * 32) + threadIdx.x, (long long)gridDim.x * (EW * 32));
             }
         }

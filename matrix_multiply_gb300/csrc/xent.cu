@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(PREP_THREADS) prep_kernel(const XentPrepArgs a
         }
         power = xent_power(block_max(most, powers));
     }
-    for (int h = threadIdx.x; h < a.H; h += PREP_THREADS) a.unscale[h] = unit / power;
+    for (int h = threadIdx.x; h < a.H; h += PREP_THREADS) a.unscale[h] = xent_unscale(unit, power);
     for (int t = threadIdx.x; t < a.T; t += PREP_THREADS) {
         float cp, cy;
         xent_factors(a, t, unit, cp, cy);

@@ -30,7 +30,7 @@ __device__ __forceinline__ void xent_factors(const XentPrepArgs &a, int t, float
 {
     cp = cy = 0.0f;
     if (!xent_counts(a, t)) return;
-    cy = a.reduction == TC_REDUCE_NONE ? a.grad[t] / unit : 1.0f;
+    cy = a.reduction == TC_REDUCE_NONE ? a.grad[t] / unit : isfinite(unit) ? 1.0f : unit;
     cp = a.z != 0.0f ? cy * (1.0f + 2.0f * a.z * a.lse[t]) : cy;
 }
 
@@ -40,6 +40,10 @@ __device__ __forceinline__ float xent_unit(const XentPrepArgs &a, float top, int
     if (a.reduction == TC_REDUCE_NONE) return top > 0.0f && top < INFINITY ? top : 1.0f;
     return a.reduction == TC_REDUCE_MEAN ? a.grad[0] / (float)max(n, 1) : a.grad[0];
 }
+
+// What the products with G are multiplied by.  (A unit that is no number stays in
+// the rows that count, xent_factors: 0 times it would put it into the others' dX.)
+__device__ __forceinline__ float xent_unscale(float unit, float power) { return (isfinite(unit) ? unit : 1.0f) / power; }
 
 // f16: the power of two that puts the largest factor between 2^13 and 2^14.  The
 // type spans 2^-24 to 2^16: probabilities far below one would be lost, so G is

@@ -146,6 +146,30 @@ def test_parts_of_g(ctx, T, dtype, grad):
     check(ctx, Case(T, 1100, 2100, dtype, reduction="none", z=0.001, ignored=0.1, grad=grad, seed=18))
 
 
+@pytest.mark.parametrize("T", [20, 200])
+@pytest.mark.parametrize("dtype,grad", [("bf16", None), ("f16", None), ("bf16", "f32")])
+@pytest.mark.parametrize("reduction", ["sum", "mean"])
+@pytest.mark.parametrize("g", [float("inf"), float("nan")])
+def test_gradient_that_is_no_number(ctx, T, dtype, grad, reduction, g):
+    """It reaches the rows that count and no other; where none counts, nothing."""
+    c = Case(T, 130, 600, dtype, reduction=reduction, ignored=0.3, grad=grad, seed=19)
+    c.g.fill_(g)
+    lse32 = c.lse32()
+    out = {"bf16": torch.bfloat16, "f16": torch.float16}[dtype] if grad is None else torch.float32
+    counted = (c.y >= 0) & (c.y < 600)
+    assert 0 < int(counted.sum()) < T
+    for none in (False, True):
+        if none:
+            c.y.fill_(-100)
+            counted = counted & False
+        dX, dW = torch.ones(c.X.shape, dtype=out, device="cuda"), torch.ones(c.W.shape, dtype=out, device="cuda")
+        torch.cuda.synchronize()
+        tg.tc_linear_xent_backward(ctx, c.desc(tg), c.X, c.W, c.y, lse32, c.g, dX, dW)
+        assert bool((dX[~counted] == 0).all())
+        assert not bool(torch.isfinite(dX[counted]).any())
+        assert bool((dW == 0).all()) if none else not bool(torch.isfinite(dW).all())
+
+
 def test_frozen(ctx):
     c = Case(40, 64, 500, seed=6)
     lse = c.lse32()
